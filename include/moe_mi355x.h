@@ -312,6 +312,93 @@ int moe_read_probe(const void* buf, size_t bytes, uint32_t* sink, void* stream);
 int moe_forward_noalloc(const moe_desc* desc, const void* x, const moe_weights* w, float* y,
                         float* aux, moe_routing* routing, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Scored routing: the router of layers with many experts.
+ *
+ * Beside moe_route's softmax router it offers sigmoid scores, selection limited
+ * to the best groups of experts, a scale on the weights, up to 256 experts, the
+ * balance loss over every choice, and the gradients of all of that.  For a
+ * token x with logits l = W_r x (+ b_router):
+ *   scores      s_e = 1 / (1 + exp(-l_e)) or softmax(l)_e
+ *   selection   v_e = s_e (+ b_select_e): ranks only, carries no gradient.  A
+ *               b_select of -inf takes an expert out of the ranking as long as
+ *               others are left.
+ *   groups      the E experts form n_groups runs of E / n_groups; a group's value
+ *               is the sum of its group_top (1 or 2) best v; the top_groups best
+ *               groups stay, the others' experts cannot be chosen
+ *   top-k       the top_k best v of the groups that stay, in descending order
+ *   weights     w_j = scale * s_j / (sum of the k chosen s + 1e-20), or scale * s_j
+ *               without renormalisation
+ * Equal values rank by the lower index; a NaN ranks below every number (so the
+ * indices are always k different experts in [0, E)).
+ * Over the T tokens of a call:
+ *   load_e      assignments of expert e (before any capacity)
+ *   prob_mean_e mean of q_e, q = s / sum(s) for sigmoid scores, s for softmax
+ *   aux         E * sum_e load_e / (T k) * prob_mean_e
+ *   z_loss      mean of (log sum_e exp l_e)^2
+ * topk_idx and topk_w feed moe_permute, moe_combine (up to 64 experts),
+ * moe_mx_dispatch and moe_mx_forward.  d_model is a multiple of 128. */
+enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
+
+typedef struct moe_score_desc {
+  int32_t tokens;          /* T >= 1; T * max(n_experts, top_k) fits int32 */
+  int32_t d_model;         /* d, a multiple of 128 */
+  int32_t n_experts;       /* 1 .. 256 */
+  int32_t top_k;           /* 1 .. 8, at most the experts of top_groups groups */
+  int32_t dtype;           /* MOE_DTYPE_*: x, w_router and d_x */
+  int32_t score;           /* MOE_SCORE_* */
+  int32_t n_groups;        /* divides n_experts, at most 64; 1 = no groups */
+  int32_t top_groups;      /* 1 .. n_groups */
+  int32_t group_top;       /* 1 or 2, at most n_experts / n_groups */
+  int32_t renormalize;     /* 0 or 1 */
+  float scale;             /* finite */
+} moe_score_desc;
+
+/* Results of the scored router (device pointers). */
+typedef struct moe_score_out {
+  int32_t* topk_idx;       /* [T][k] */
+  float* topk_w;           /* [T][k] */
+  float* logits;           /* [T][E] b_router included, or NULL; the backward reads them */
+  int32_t* load;           /* [E] or NULL; the backward's d_aux needs it */
+  float* prob_mean;        /* [E] or NULL */
+  float* aux;              /* [1] or NULL */
+  float* z_loss;           /* [1] or NULL */
+} moe_score_out;
+
+/* Gradients the scored router's backward writes (device pointers, each may be
+ * NULL, not all). */
+typedef struct moe_score_grads {
+  void* d_x;               /* [T][d] dtype */
+  float* d_w_router;       /* [E][d] fp32 */
+  float* d_b_router;       /* [E] fp32 */
+  float* d_logits;         /* [T][E] fp32 */
+} moe_score_grads;
+
+/* Bytes of workspace either call below needs (host output). */
+int moe_score_workspace_size(const moe_score_desc* desc, size_t* bytes);
+
+/* The scored router.  x [T][d] dtype, w_router [E][d] dtype, b_router [E] fp32 or
+ * NULL, b_select [E] fp32 or NULL.  Writes out->topk_idx and out->topk_w (both
+ * required) and every other field that is not NULL. */
+int moe_score_route(const moe_score_desc* desc, const void* x, const void* w_router,
+                    const float* b_router, const float* b_select, moe_score_out* out,
+                    void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradients of the scored router: of
+ *   L = sum_tj d_topk_w_tj w_tj + d_aux * aux + d_z_loss * z_loss
+ * with respect to the logits, and through them x, W_r and b_router.  The choice
+ * of experts and load are constants.  Reads from `fwd` topk_idx, logits and, with
+ * d_aux, load, as the forward wrote them; an index outside [0, E) is a dropped
+ * slot and contributes nothing.  d_topk_w [T][k] fp32 or NULL (zero), d_aux and
+ * d_z_loss [1] fp32 device scalars or NULL (zero).  x is read for d_w_router only,
+ * w_router for d_x only (either may be NULL otherwise).  Sums are fp32 or wider in
+ * a fixed order; for bf16 layers the logit gradients enter the matrix products as
+ * two (d_x) or three (d_w_router) bf16 terms. */
+int moe_score_backward(const moe_score_desc* desc, const void* x, const void* w_router,
+                       const moe_score_out* fwd, const float* d_topk_w, const float* d_aux,
+                       const float* d_z_loss, moe_score_grads* grads, void* workspace,
+                       size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -19,12 +19,16 @@ MOE_OK, MOE_ERR_INVALID, MOE_ERR_UNSUPPORTED, MOE_ERR_WORKSPACE, MOE_ERR_HIP = 0
 MOE_FFN_AUTO, MOE_FFN_TILED, MOE_FFN_STREAM = 0, 1, 2
 MOE_H_AUTO, MOE_H_BF16, MOE_H_SPLIT = 0, 1, 2
 MOE_CAPACITY_DROP, MOE_CAPACITY_REROUTE = 0, 1
+MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
+_SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+_DTYPES = {"bf16": MOE_DTYPE_BF16, "f32": MOE_DTYPE_F32}
 _POLICIES = {"drop": MOE_CAPACITY_DROP, "reroute": MOE_CAPACITY_REROUTE}
 
 ENTRY_POINTS = ("moe_status_string", "moe_last_error", "moe_workspace_size", "moe_query_plan",
                 "moe_route", "moe_permute", "moe_ffn_up", "moe_ffn_up_gather", "moe_ffn_down", "moe_grouped_ffn",
                 "moe_shared_ffn", "moe_combine", "moe_forward", "moe_forward_noalloc",
-                "moe_read_probe")
+                "moe_read_probe", "moe_score_workspace_size", "moe_score_route",
+                "moe_score_backward")
 
 
 class MoeError(RuntimeError):
@@ -57,6 +61,21 @@ class CRouting(ctypes.Structure):
                  "prob_mean", "z_loss", "reroute_rounds")]
 
 
+class CScoreDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("tokens", "d_model", "n_experts", "top_k", "dtype", "score", "n_groups",
+                 "top_groups", "group_top", "renormalize")] + [("scale", ctypes.c_float)]
+
+
+class CScoreOut(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("topk_idx", "topk_w", "logits", "load", "prob_mean", "aux", "z_loss")]
+
+
+class CScoreGrads(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("d_x", "d_w_router", "d_b_router", "d_logits")]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -87,6 +106,9 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_forward": (I, [pd, P, pw, P, P, pr, P, S, P]),
         "moe_forward_noalloc": (I, [pd, P, pw, P, P, pr, P]),
         "moe_read_probe": (I, [P, S, P, P]),
+        "moe_score_workspace_size": (I, [P, ctypes.POINTER(S)]),
+        "moe_score_route": (I, [P, P, P, P, P, P, P, S, P]),
+        "moe_score_backward": (I, [P, P, P, P, P, P, P, P, P, S, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -408,3 +430,161 @@ def forward(x: torch.Tensor, weights: Weights, desc: Desc, workspace=None, strea
     aux = torch.empty((), dtype=torch.float32, device=x.device)
     moe_forward(desc, x, weights, y, aux, None, workspace, stream)
     return y, aux
+
+
+# ---- scored routing --------------------------------------------------------------------
+
+@dataclasses.dataclass
+class ScoreDesc:
+    """Options of the scored router (moe_score_desc)."""
+    tokens: int
+    d_model: int
+    n_experts: int
+    top_k: int
+    dtype: str = "bf16"          # "bf16" or "f32"
+    score: str = "softmax"       # "softmax" or "sigmoid"
+    n_groups: int = 1
+    top_groups: int = 1
+    group_top: int = 1           # experts a group is valued by: its best, or its best two
+    renormalize: bool = True
+    scale: float = 1.0
+
+    def to_c(self) -> CScoreDesc:
+        return CScoreDesc(self.tokens, self.d_model, self.n_experts, self.top_k,
+                          _DTYPES.get(self.dtype, -1), _SCORES.get(self.score, -1), self.n_groups,
+                          self.top_groups, self.group_top, int(bool(self.renormalize)), self.scale)
+
+    @property
+    def torch_dtype(self):
+        return torch.bfloat16 if self.dtype == "bf16" else torch.float32
+
+
+@dataclasses.dataclass
+class ScoreRouting:
+    """Results of moe_score_route; the backward reads topk_idx, logits and load."""
+    topk_idx: Optional[torch.Tensor] = None
+    topk_w: Optional[torch.Tensor] = None
+    logits: Optional[torch.Tensor] = None
+    load: Optional[torch.Tensor] = None
+    prob_mean: Optional[torch.Tensor] = None
+    aux: Optional[torch.Tensor] = None
+    z_loss: Optional[torch.Tensor] = None
+
+    @classmethod
+    def allocate(cls, desc: ScoreDesc, device, train: bool = False) -> "ScoreRouting":
+        """The indices and weights; with `train` also what the losses and the backward need."""
+        T, k, E = desc.tokens, desc.top_k, desc.n_experts
+        i32, f32 = dict(dtype=torch.int32, device=device), dict(dtype=torch.float32, device=device)
+        r = cls(topk_idx=torch.empty(T, k, **i32), topk_w=torch.empty(T, k, **f32))
+        if train:
+            r.logits, r.load = torch.empty(T, E, **f32), torch.empty(E, **i32)
+            r.prob_mean, r.aux, r.z_loss = (torch.empty(E, **f32), torch.empty((), **f32),
+                                            torch.empty((), **f32))
+        return r
+
+
+@dataclasses.dataclass
+class ScoreGrads:
+    """What moe_score_backward writes; leave out (None) what is not wanted."""
+    d_x: Optional[torch.Tensor] = None
+    d_w_router: Optional[torch.Tensor] = None
+    d_b_router: Optional[torch.Tensor] = None
+    d_logits: Optional[torch.Tensor] = None
+
+    @classmethod
+    def allocate(cls, desc: ScoreDesc, device) -> "ScoreGrads":
+        f32 = dict(dtype=torch.float32, device=device)
+        return cls(d_x=torch.empty(desc.tokens, desc.d_model, dtype=desc.torch_dtype, device=device),
+                   d_w_router=torch.empty(desc.n_experts, desc.d_model, **f32),
+                   d_b_router=torch.empty(desc.n_experts, **f32))
+
+
+class _Call:
+    """One call of the operators below: checks its tensors, all on one GPU, and runs it
+    there on the given stream, or on the current stream of that GPU."""
+
+    def __init__(self, anchor, name):
+        if not isinstance(anchor, torch.Tensor):
+            raise MoeError(MOE_ERR_INVALID, f"{name} must be a torch tensor")
+        self.device = anchor.device
+        if self.device.type != "cuda":
+            raise MoeError(MOE_ERR_INVALID, f"{name} is on {self.device}, expected a GPU")
+
+    def t(self, t, name, dtype, numel):
+        """Pointer of a contiguous tensor with at least numel elements, or None."""
+        if t is None:
+            return None
+        if not isinstance(t, torch.Tensor):
+            raise MoeError(MOE_ERR_INVALID, f"{name} must be a torch tensor or None")
+        if t.device != self.device or t.dtype != dtype or t.numel() < numel or not t.is_contiguous():
+            check_tensor(t, name, dtype, numel, self.device)
+        return t.data_ptr()
+
+    def ws(self, t, size_of):
+        """(pointer, bytes) of the workspace; None allocates one."""
+        if t is None:
+            t = self._keep = torch.empty(size_of(), dtype=torch.uint8, device=self.device)
+        else:
+            check_tensor(t, "workspace", None, 0, self.device)
+        return t.data_ptr(), t.numel() * t.element_size()
+
+    def run(self, fn, *args, stream=None):
+        if stream is None:
+            stream = torch.cuda.current_stream(self.device)
+        stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+        if torch.cuda.current_device() != self.device.index:
+            with torch.cuda.device(self.device):
+                status = fn(*args, stream)
+        else:
+            status = fn(*args, stream)
+        _check(status)
+
+
+def moe_score_workspace_size(desc: ScoreDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_score_workspace_size(ctypes.byref(desc.to_c()), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_score_workspace(desc: ScoreDesc, device) -> torch.Tensor:
+    return torch.empty(moe_score_workspace_size(desc), dtype=torch.uint8, device=device)
+
+
+def _score_out(c: _Call, d: ScoreDesc, r: ScoreRouting) -> CScoreOut:
+    T, k, E = d.tokens, d.top_k, d.n_experts
+    i32, f32 = torch.int32, torch.float32
+    return CScoreOut(c.t(r.topk_idx, "routing.topk_idx", i32, T * k),
+                     c.t(r.topk_w, "routing.topk_w", f32, T * k),
+                     c.t(r.logits, "routing.logits", f32, T * E), c.t(r.load, "routing.load", i32, E),
+                     c.t(r.prob_mean, "routing.prob_mean", f32, E),
+                     c.t(r.aux, "routing.aux", f32, 1), c.t(r.z_loss, "routing.z_loss", f32, 1))
+
+
+def moe_score_route(desc: ScoreDesc, x, w_router, routing: ScoreRouting, b_router=None, b_select=None,
+                    workspace=None, stream=None):
+    """Scored routing: writes every field of `routing` that is not None (topk_idx and
+    topk_w have to be there)."""
+    c = _Call(x, "x")
+    T, d, E, dt = desc.tokens, desc.d_model, desc.n_experts, desc.torch_dtype
+    ws, nb = c.ws(workspace, lambda: moe_score_workspace_size(desc))
+    c.run(load_library().moe_score_route, ctypes.byref(desc.to_c()), c.t(x, "x", dt, T * d),
+          c.t(w_router, "w_router", dt, E * d), c.t(b_router, "b_router", torch.float32, E),
+          c.t(b_select, "b_select", torch.float32, E), ctypes.byref(_score_out(c, desc, routing)), ws, nb,
+          stream=stream)
+
+
+def moe_score_backward(desc: ScoreDesc, x, w_router, routing: ScoreRouting, d_topk_w, grads: ScoreGrads,
+                       d_aux=None, d_z_loss=None, workspace=None, stream=None):
+    """Gradients of the scored router into the fields of `grads` that are not None; x may
+    be None without d_w_router, w_router without d_x."""
+    c = _Call(routing.logits, "routing.logits")
+    T, d, E, k, dt = desc.tokens, desc.d_model, desc.n_experts, desc.top_k, desc.torch_dtype
+    f32 = torch.float32
+    ws, nb = c.ws(workspace, lambda: moe_score_workspace_size(desc))
+    g = CScoreGrads(c.t(grads.d_x, "grads.d_x", dt, T * d), c.t(grads.d_w_router, "grads.d_w_router", f32, E * d),
+                    c.t(grads.d_b_router, "grads.d_b_router", f32, E),
+                    c.t(grads.d_logits, "grads.d_logits", f32, T * E))
+    c.run(load_library().moe_score_backward, ctypes.byref(desc.to_c()), c.t(x, "x", dt, T * d),
+          c.t(w_router, "w_router", dt, E * d), ctypes.byref(_score_out(c, desc, routing)),
+          c.t(d_topk_w, "d_topk_w", f32, T * k), c.t(d_aux, "d_aux", f32, 1),
+          c.t(d_z_loss, "d_z_loss", f32, 1), ctypes.byref(g), ws, nb, stream=stream)

@@ -4,43 +4,17 @@
 #include <cmath>
 #include <hip/hip_runtime.h>
 
-#include <cstdarg>
 #include <cstdint>
-#include <cstdio>
 #include <limits>
 #include <mutex>
 
 #include "../../include/moe_mi355x.h"
+#include "api_util.h"
 #include "kernels.h"
 
+using namespace moe::api;
+
 namespace {
-
-thread_local char g_err[512] = "";
-
-int fail(int status, const char* fmt, ...) {
-  va_list ap;
-  va_start(ap, fmt);
-  vsnprintf(g_err, sizeof(g_err), fmt, ap);
-  va_end(ap);
-  return status;
-}
-
-int ok() {
-  g_err[0] = '\0';
-  return MOE_OK;
-}
-
-bool aligned16(const void* p) { return (reinterpret_cast<uintptr_t>(p) & 15u) == 0; }
-
-#define MOE_REQUIRE_PTR(p, name)                                                       \
-  do {                                                                                 \
-    if (!(p)) return fail(MOE_ERR_INVALID, "%s must not be NULL", name);               \
-    if (!aligned16(p)) return fail(MOE_ERR_INVALID, "%s must be 16-byte aligned", name); \
-  } while (0)
-#define MOE_OPTIONAL_PTR(p, name)                                                      \
-  do {                                                                                 \
-    if ((p) && !aligned16(p)) return fail(MOE_ERR_INVALID, "%s must be 16-byte aligned", name); \
-  } while (0)
 
 // Whether y averages over several experts or carries weight 1: top-k > 1 or a
 // renormalised top-1.  A top-1 layer without renormalisation weights each
@@ -236,8 +210,6 @@ struct Layout {
   size_t total;
 };
 
-size_t up256(size_t v) { return (v + 255) & ~size_t(255); }
-
 Layout layout_of(const moe_desc* d) {
   Layout L{};
   const size_t T = d->tokens, E = d->n_experts, k = d->top_k, A = T * k;
@@ -295,11 +267,6 @@ Layout layout_of(const moe_desc* d) {
   return L;
 }
 
-template <typename T>
-T* at(void* ws, size_t off) {
-  return reinterpret_cast<T*>(static_cast<uint8_t*>(ws) + off);
-}
-
 int check_ws(const moe_desc* d, void* ws, size_t bytes, Layout& L) {
   L = layout_of(d);
   if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace must not be NULL");
@@ -307,41 +274,6 @@ int check_ws(const moe_desc* d, void* ws, size_t bytes, Layout& L) {
     return fail(MOE_ERR_WORKSPACE, "workspace must be 256-byte aligned");
   if (bytes < L.total)
     return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", bytes, L.total);
-  return MOE_OK;
-}
-
-// ---- aliasing -------------------------------------------------------------
-// Outputs (the workspace included) must be disjoint from each other and from
-// every input; a call that would write over its own operands is refused.
-
-struct Span {
-  const void* p;
-  size_t n;
-  const char* name;
-};
-
-struct Spans {
-  Span s[24];
-  int n = 0;
-  void add(const void* p, size_t bytes, const char* name) {
-    if (p && bytes && n < 24) s[n++] = Span{p, bytes, name};
-  }
-};
-
-bool overlaps(const Span& a, const Span& b) {
-  const uintptr_t a0 = reinterpret_cast<uintptr_t>(a.p), b0 = reinterpret_cast<uintptr_t>(b.p);
-  return a0 < b0 + b.n && b0 < a0 + a.n;
-}
-
-int check_alias(const Spans& outs, const Spans& ins) {
-  for (int i = 0; i < outs.n; ++i) {
-    for (int j = i + 1; j < outs.n; ++j)
-      if (overlaps(outs.s[i], outs.s[j]))
-        return fail(MOE_ERR_INVALID, "%s overlaps %s", outs.s[i].name, outs.s[j].name);
-    for (int j = 0; j < ins.n; ++j)
-      if (overlaps(outs.s[i], ins.s[j]))
-        return fail(MOE_ERR_INVALID, "%s overlaps %s", outs.s[i].name, ins.s[j].name);
-  }
   return MOE_OK;
 }
 
@@ -409,11 +341,6 @@ void add_routing_outputs(Spans& out, const moe_desc* d, const moe_routing& r) {
   out.add(r.prob_mean, b.e, "prob_mean");
   out.add(r.z_loss, 4, "z_loss");
   out.add(r.reroute_rounds, 4, "reroute_rounds");
-}
-
-int hip_status(hipError_t e, const char* what) {
-  if (e != hipSuccess) return fail(MOE_ERR_HIP, "%s: %s", what, hipGetErrorString(e));
-  return ok();
 }
 
 // Dispatch layout outputs that the router's aux reduction fills for small

@@ -1,0 +1,71 @@
+// Launchers of the scored router (score.hip) and its gradients (score_grad.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace moe {
+
+constexpr int kScoreMaxExperts = 256;
+
+struct ScoreShape {
+  bool bf16;
+  int T, d, E, k;
+};
+
+// Parts the d-long dot products are cut into (partial logits [parts][T][E]).
+int score_parts(const ScoreShape& s);
+// Blocks of the finishing kernel, each with a partial row of the sums over tokens.
+int score_finish_blocks(int T);
+
+struct ScoreArgs {
+  ScoreShape sh;
+  const void* x;
+  const void* w;
+  const float* b_router;   // or null
+  const float* b_select;   // or null
+  bool sigmoid;
+  int groups, top_groups, group_top;
+  bool renorm;
+  float scale;
+  int32_t* topk_idx;
+  float* topk_w;
+  float* logits;           // or null
+  int32_t* load;           // the rest or null
+  float* prob_mean;
+  float* aux;
+  float* z_loss;
+  float* part;             // workspace [parts][T][E]
+  double* psum;            // workspace [blocks][E]
+  int32_t* pload;          // workspace [blocks][E]
+  double* pz;              // workspace [blocks]
+};
+hipError_t launch_score(const ScoreArgs& a, hipStream_t s);
+
+// Slices of the token range that d_w_router is summed in.
+int score_grad_slices(const ScoreShape& s);
+
+struct ScoreGradArgs {
+  ScoreShape sh;
+  bool sigmoid, renorm;
+  float scale;
+  const void* x;
+  const void* w;
+  const int32_t* topk_idx;
+  const float* logits;
+  const int32_t* load;     // with d_aux
+  const float* d_topk_w;   // or null, as the next two
+  const float* d_aux;
+  const float* d_z;
+  void* d_x;               // or null, as the next three
+  float* d_w;
+  float* d_b;
+  float* d_logits;
+  float* dl;               // workspace [T][E]
+  double* pb;              // workspace [blocks][E]
+  float* pw;               // workspace [slices][E][d]
+};
+hipError_t launch_score_grad(const ScoreGradArgs& a, hipStream_t s);
+
+}  // namespace moe
