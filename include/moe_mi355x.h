@@ -399,6 +399,93 @@ int moe_score_backward(const moe_score_desc* desc, const void* x, const void* w_
                        const float* d_z_loss, moe_score_grads* grads, void* workspace,
                        size_t workspace_bytes, void* stream);
 
+/* ---------------------------------------------------------------------------
+ * Experts in microscaled 4-bit floating point (MXFP4).
+ *
+ * A row of K values is K / 32 blocks of 32.  Block b has one scale byte s (e8m0:
+ * 2^(s - 127), 255 = NaN) and 32 codes of four bits (e2m1: sign, then 0, 0.5, 1,
+ * 1.5, 2, 3, 4, 6); it stands for code * 2^(s - 127).  Codes are packed two to a
+ * byte, the even index in the low half: codes [rows][K/2], scales [rows][K/32].
+ *
+ * The expert products read W1 and W2 in this form (3.76 times fewer bytes than
+ * bf16).  moe_mx_desc.act says what the activations are:
+ *   MOE_MX_ACT_BF16   bf16; the weights are widened exactly to bf16 on the way into
+ *                     the matrix instruction
+ *   MOE_MX_ACT_MXFP4  quantised by the call as moe_mx_quantize does, both operands of
+ *                     the matrix instruction in 4 bits
+ * Products accumulate in fp32.  Limits: 1 <= n_experts <= 256, 1 <= top_k <= min(8,
+ * n_experts), d_model and d_ff multiples of 128, tokens * top_k * max(d_model, d_ff)
+ * and one expert's d_model * d_ff under 2^31.  Rows of an expert are the segment
+ * [offsets[e], offsets[e+1]) as moe_permute and moe_mx_dispatch lay them out; a
+ * segment outside [0, T*k) is cut to it.  The codes are frozen weights: there is no
+ * backward. */
+enum { MOE_MX_ACT_BF16 = 0, MOE_MX_ACT_MXFP4 = 1 };
+
+typedef struct moe_mx_desc {
+  int32_t tokens;          /* T */
+  int32_t d_model;         /* d */
+  int32_t d_ff;            /* F */
+  int32_t n_experts;       /* E */
+  int32_t top_k;           /* k */
+  int32_t act;             /* MOE_MX_ACT_* */
+  int32_t has_expert_bias; /* 1: b1 and b2 are given; 0: both absent */
+} moe_mx_desc;
+
+/* Expert weights (device pointers); a call needs only those of the products it runs. */
+typedef struct moe_mx_weights {
+  const uint8_t* w1;       /* [E][F][d/2] codes */
+  const uint8_t* s1;       /* [E][F][d/32] scales */
+  const void* b1;          /* [E][F] bf16, NULL iff !has_expert_bias */
+  const uint8_t* w2;       /* [E][d][F/2] */
+  const uint8_t* s2;       /* [E][d][F/32] */
+  const void* b2;          /* [E][d] bf16, NULL iff !has_expert_bias */
+} moe_mx_weights;
+
+/* Rows to MXFP4.  x: rows of cols values of `dtype`, row_stride elements apart; cols a
+ * multiple of 32, row_stride >= cols and a multiple of 16 bytes.  Per block, with
+ * a = max |x|: scale 2^(floor(log2 a) - 2), at least 2^-127 (and exactly that for a
+ * block of zeros); codes rounded to nearest, ties to even, values past 6 to 6.  A block
+ * with a NaN or an infinity gets scale 255.  rows = 0 does nothing. */
+int moe_mx_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_t row_stride,
+                    uint8_t* codes, uint8_t* scales, void* stream);
+
+/* MXFP4 to rows of `dtype`, row_stride elements apart (exact; the smallest scales
+ * reach bf16's and fp32's subnormals, the largest overflow to infinity). */
+int moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
+                      int dtype, void* out, int64_t row_stride, void* stream);
+
+/* Bytes of workspace any call below needs for this descriptor (host output);
+ * moe_mx_forward needs moe_score_workspace_size of its router on top. */
+int moe_mx_workspace_size(const moe_mx_desc* desc, size_t* bytes);
+
+/* The dispatch layout for up to 256 experts: reads r->topk_idx [T][k] (ids outside
+ * [0, E) are dropped assignments), writes r->counts [E], r->offsets [E+1],
+ * r->dest [T][k] and r->src [T*k] as moe_permute does without a capacity. */
+int moe_mx_dispatch(const moe_mx_desc* desc, moe_routing* r, void* workspace,
+                    size_t workspace_bytes, void* stream);
+
+/* h[r] = GELU_erf(a[r] W1_e^T + b1_e), bf16 [T*k][F], for every row r of expert e's
+ * segment; rows past the last segment are not written.  With src (the dispatch's
+ * [T*k]) a[r] is x[src[r] / k], x [T][d] bf16; src NULL: x is [T*k][d], a[r] = x[r]. */
+int moe_mx_ffn_up(const moe_mx_desc* desc, const void* x, const int32_t* src,
+                  const int32_t* offsets, const moe_mx_weights* w, void* h, void* workspace,
+                  size_t workspace_bytes, void* stream);
+
+/* o[r] = h[r] W2_e^T + b2_e, h [T*k][F] bf16, o [T*k][d] fp32. */
+int moe_mx_ffn_down(const moe_mx_desc* desc, const void* h, const int32_t* offsets,
+                    const moe_mx_weights* w, float* o, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/* The whole layer: moe_score_route, moe_mx_dispatch, moe_mx_ffn_up, moe_mx_ffn_down and
+ * the combine of moe_combine, bit for bit as the calls one by one.  route and desc agree
+ * in tokens, d_model, n_experts and top_k; route->dtype is BF16.  y [T][d] fp32; `out`
+ * may be NULL or any of its fields.  The workspace holds moe_mx_workspace_size(desc) +
+ * moe_score_workspace_size(route) bytes. */
+int moe_mx_forward(const moe_score_desc* route, const moe_mx_desc* desc, const void* x,
+                   const void* w_router, const float* b_router, const float* b_select,
+                   const moe_mx_weights* w, float* y, moe_score_out* out, void* workspace,
+                   size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -21,6 +21,8 @@ MOE_H_AUTO, MOE_H_BF16, MOE_H_SPLIT = 0, 1, 2
 MOE_CAPACITY_DROP, MOE_CAPACITY_REROUTE = 0, 1
 MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 _SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
+MOE_MX_ACT_BF16, MOE_MX_ACT_MXFP4 = 0, 1
+_MX_ACTS = {"bf16": MOE_MX_ACT_BF16, "mxfp4": MOE_MX_ACT_MXFP4}
 _DTYPES = {"bf16": MOE_DTYPE_BF16, "f32": MOE_DTYPE_F32}
 _POLICIES = {"drop": MOE_CAPACITY_DROP, "reroute": MOE_CAPACITY_REROUTE}
 
@@ -28,7 +30,8 @@ ENTRY_POINTS = ("moe_status_string", "moe_last_error", "moe_workspace_size", "mo
                 "moe_route", "moe_permute", "moe_ffn_up", "moe_ffn_up_gather", "moe_ffn_down", "moe_grouped_ffn",
                 "moe_shared_ffn", "moe_combine", "moe_forward", "moe_forward_noalloc",
                 "moe_read_probe", "moe_score_workspace_size", "moe_score_route",
-                "moe_score_backward")
+                "moe_score_backward", "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_workspace_size",
+                "moe_mx_dispatch", "moe_mx_ffn_up", "moe_mx_ffn_down", "moe_mx_forward")
 
 
 class MoeError(RuntimeError):
@@ -76,6 +79,15 @@ class CScoreGrads(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("d_x", "d_w_router", "d_b_router", "d_logits")]
 
 
+class CMxDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("tokens", "d_model", "d_ff", "n_experts", "top_k", "act", "has_expert_bias")]
+
+
+class CMxWeights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w1", "s1", "b1", "w2", "s2", "b2")]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -88,7 +100,7 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         raise RuntimeError(f"{path} is missing: build it with "
                            "`python -m sparse_mixture_experts_49_amd.build`")
     lib = ctypes.CDLL(path)
-    P, I, S = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t
+    P, I, S, L = ctypes.c_void_p, ctypes.c_int, ctypes.c_size_t, ctypes.c_int64
     pd, pw, pr = ctypes.POINTER(CDesc), ctypes.POINTER(CWeights), ctypes.POINTER(CRouting)
     sig = {
         "moe_status_string": (ctypes.c_char_p, [I]),
@@ -109,6 +121,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_score_workspace_size": (I, [P, ctypes.POINTER(S)]),
         "moe_score_route": (I, [P, P, P, P, P, P, P, S, P]),
         "moe_score_backward": (I, [P, P, P, P, P, P, P, P, P, S, P]),
+        "moe_mx_quantize": (I, [P, I, L, L, L, P, P, P]),
+        "moe_mx_dequantize": (I, [P, P, L, L, I, P, L, P]),
+        "moe_mx_workspace_size": (I, [P, ctypes.POINTER(S)]),
+        "moe_mx_dispatch": (I, [P, pr, P, S, P]),
+        "moe_mx_ffn_up": (I, [P, P, P, P, P, P, P, S, P]),
+        "moe_mx_ffn_down": (I, [P, P, P, P, P, P, S, P]),
+        "moe_mx_forward": (I, [P, P, P, P, P, P, P, P, P, P, S, P]),
     }
     for name, (res, args) in sig.items():
         fn = getattr(lib, name)
@@ -588,3 +607,150 @@ def moe_score_backward(desc: ScoreDesc, x, w_router, routing: ScoreRouting, d_to
           c.t(w_router, "w_router", dt, E * d), ctypes.byref(_score_out(c, desc, routing)),
           c.t(d_topk_w, "d_topk_w", f32, T * k), c.t(d_aux, "d_aux", f32, 1),
           c.t(d_z_loss, "d_z_loss", f32, 1), ctypes.byref(g), ws, nb, stream=stream)
+
+
+# ---- experts in microscaled 4-bit floating point ------------------------------------------
+
+@dataclasses.dataclass
+class MxDesc:
+    """Options of a layer with MXFP4 expert weights (moe_mx_desc)."""
+    tokens: int
+    d_model: int
+    d_ff: int
+    n_experts: int
+    top_k: int
+    act: str = "bf16"             # activations: "bf16", or "mxfp4" (quantised by the call)
+    has_expert_bias: bool = True
+
+    def to_c(self) -> CMxDesc:
+        return CMxDesc(self.tokens, self.d_model, self.d_ff, self.n_experts, self.top_k,
+                       _MX_ACTS.get(self.act, -1), int(bool(self.has_expert_bias)))
+
+
+@dataclasses.dataclass
+class MxWeights:
+    """Codes [E, N, K/2] and scales [E, N, K/32] (uint8) of the expert matrices, biases bf16;
+    a call needs only those of the products it runs."""
+    w1: Optional[torch.Tensor] = None
+    s1: Optional[torch.Tensor] = None
+    b1: Optional[torch.Tensor] = None
+    w2: Optional[torch.Tensor] = None
+    s2: Optional[torch.Tensor] = None
+    b2: Optional[torch.Tensor] = None
+
+    @classmethod
+    def quantize(cls, w1, w2, b1=None, b2=None) -> "MxWeights":
+        """From bf16 or fp32 expert matrices w1 [E, F, d] and w2 [E, d, F]."""
+        out = cls(b1=b1, b2=b2)
+        for n, w in (("1", w1), ("2", w2)):
+            codes, scales = alloc_mx(w.shape[0] * w.shape[1], w.shape[2], w.device)
+            moe_mx_quantize(w.reshape(-1, w.shape[2]), codes, scales)
+            setattr(out, "w" + n, codes.view(*w.shape[:2], -1))
+            setattr(out, "s" + n, scales.view(*w.shape[:2], -1))
+        return out
+
+
+def alloc_mx(rows: int, cols: int, device):
+    """(codes, scales) buffers of rows x cols values."""
+    return (torch.empty(rows, cols // 2, dtype=torch.uint8, device=device),
+            torch.empty(rows, cols // 32, dtype=torch.uint8, device=device))
+
+
+def _mx_rows(c: _Call, t, name):
+    """(pointer, dtype id, rows, cols, row stride) of a 2-D tensor whose rows are contiguous."""
+    if t.device != c.device or t.dtype not in (torch.bfloat16, torch.float32) or t.dim() != 2 or \
+            (t.shape[1] > 1 and t.stride(1) != 1):
+        raise MoeError(MOE_ERR_INVALID, f"{name} must be a bf16 or fp32 matrix with contiguous rows on {c.device}")
+    stride = t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
+    return (t.data_ptr(), MOE_DTYPE_BF16 if t.dtype == torch.bfloat16 else MOE_DTYPE_F32,
+            t.shape[0], t.shape[1], stride)
+
+
+def moe_mx_quantize(x, codes, scales, stream=None):
+    """Rows of x (bf16 or fp32 [rows, cols], any row stride) to MXFP4 codes and scales."""
+    c = _Call(x, "x")
+    p, dt, rows, cols, stride = _mx_rows(c, x, "x")
+    c.run(load_library().moe_mx_quantize, p, dt, rows, cols, stride,
+          c.t(codes, "codes", torch.uint8, rows * cols // 2),
+          c.t(scales, "scales", torch.uint8, rows * cols // 32), stream=stream)
+
+
+def moe_mx_dequantize(codes, scales, out, stream=None):
+    """MXFP4 codes and scales to the rows of out (bf16 or fp32 [rows, cols])."""
+    c = _Call(out, "out")
+    p, dt, rows, cols, stride = _mx_rows(c, out, "out")
+    c.run(load_library().moe_mx_dequantize, c.t(codes, "codes", torch.uint8, rows * cols // 2),
+          c.t(scales, "scales", torch.uint8, rows * cols // 32), rows, cols, dt, p, stride, stream=stream)
+
+
+def moe_mx_workspace_size(desc: MxDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_mx_workspace_size(ctypes.byref(desc.to_c()), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_mx_workspace(desc: MxDesc, device, route: Optional[ScoreDesc] = None) -> torch.Tensor:
+    """The workspace of the calls below; with `route`, of moe_mx_forward."""
+    n = moe_mx_workspace_size(desc) + (moe_score_workspace_size(route) if route is not None else 0)
+    return torch.empty(n, dtype=torch.uint8, device=device)
+
+
+def _mx_weights(c: _Call, d: MxDesc, w: MxWeights, up: bool, down: bool) -> CMxWeights:
+    E, D, F, u8, bf = d.n_experts, d.d_model, d.d_ff, torch.uint8, torch.bfloat16
+    n = E * D * F
+    return CMxWeights(c.t(w.w1, "weights.w1", u8, n // 2) if up else None,
+                      c.t(w.s1, "weights.s1", u8, n // 32) if up else None,
+                      c.t(w.b1, "weights.b1", bf, E * F) if up else None,
+                      c.t(w.w2, "weights.w2", u8, n // 2) if down else None,
+                      c.t(w.s2, "weights.s2", u8, n // 32) if down else None,
+                      c.t(w.b2, "weights.b2", bf, E * D) if down else None)
+
+
+def moe_mx_dispatch(desc: MxDesc, routing: Routing, workspace=None, stream=None):
+    """counts, offsets, dest and src of `routing` from its topk_idx, for up to 256 experts."""
+    c = _Call(routing.topk_idx, "routing.topk_idx")
+    A, E, i32 = desc.tokens * desc.top_k, desc.n_experts, torch.int32
+    r = CRouting(topk_idx=c.t(routing.topk_idx, "routing.topk_idx", i32, A),
+                 counts=c.t(routing.counts, "routing.counts", i32, E),
+                 offsets=c.t(routing.offsets, "routing.offsets", i32, E + 1),
+                 dest=c.t(routing.dest, "routing.dest", i32, A), src=c.t(routing.src, "routing.src", i32, A))
+    ws, nb = c.ws(workspace, lambda: moe_mx_workspace_size(desc))
+    c.run(load_library().moe_mx_dispatch, ctypes.byref(desc.to_c()), ctypes.byref(r), ws, nb, stream=stream)
+
+
+def moe_mx_ffn_up(desc: MxDesc, x, offsets, weights: MxWeights, h, src=None, workspace=None, stream=None):
+    """First expert product with GELU; with src, x holds the tokens and row r reads token
+    src[r] / top_k, else x holds the dispatched rows."""
+    c = _Call(x, "x")
+    R, bf = desc.tokens * desc.top_k, torch.bfloat16
+    ws, nb = c.ws(workspace, lambda: moe_mx_workspace_size(desc))
+    c.run(load_library().moe_mx_ffn_up, ctypes.byref(desc.to_c()),
+          c.t(x, "x", bf, (desc.tokens if src is not None else R) * desc.d_model), c.t(src, "src", torch.int32, R),
+          c.t(offsets, "offsets", torch.int32, desc.n_experts + 1),
+          ctypes.byref(_mx_weights(c, desc, weights, True, False)), c.t(h, "h", bf, R * desc.d_ff), ws, nb,
+          stream=stream)
+
+
+def moe_mx_ffn_down(desc: MxDesc, h, offsets, weights: MxWeights, o, workspace=None, stream=None):
+    """Second expert product, o fp32."""
+    c = _Call(h, "h")
+    R = desc.tokens * desc.top_k
+    ws, nb = c.ws(workspace, lambda: moe_mx_workspace_size(desc))
+    c.run(load_library().moe_mx_ffn_down, ctypes.byref(desc.to_c()), c.t(h, "h", torch.bfloat16, R * desc.d_ff),
+          c.t(offsets, "offsets", torch.int32, desc.n_experts + 1),
+          ctypes.byref(_mx_weights(c, desc, weights, False, True)),
+          c.t(o, "o", torch.float32, R * desc.d_model), ws, nb, stream=stream)
+
+
+def moe_mx_forward(route: ScoreDesc, desc: MxDesc, x, w_router, weights: MxWeights, y, routing=None,
+                   b_router=None, b_select=None, workspace=None, stream=None):
+    """The whole layer: scored routing, dispatch, both MXFP4 products, combine.  y fp32
+    [T, d]; `routing` (a ScoreRouting, or None) receives the fields it has."""
+    c = _Call(x, "x")
+    T, D, E, bf, f32 = desc.tokens, desc.d_model, desc.n_experts, torch.bfloat16, torch.float32
+    ws, nb = c.ws(workspace, lambda: moe_mx_workspace_size(desc) + moe_score_workspace_size(route))
+    out = ctypes.byref(_score_out(c, route, routing)) if routing is not None else None
+    c.run(load_library().moe_mx_forward, ctypes.byref(route.to_c()), ctypes.byref(desc.to_c()),
+          c.t(x, "x", bf, T * D), c.t(w_router, "w_router", bf, E * D), c.t(b_router, "b_router", f32, E),
+          c.t(b_select, "b_select", f32, E), ctypes.byref(_mx_weights(c, desc, weights, True, True)),
+          c.t(y, "y", f32, T * D), out, ws, nb, stream=stream)
