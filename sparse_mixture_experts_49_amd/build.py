@@ -15,7 +15,7 @@ CSRC = os.path.join(PKG, "csrc")
 BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_mi355x.so")
 SOURCES = ["api.cpp", "api_score.cpp", "score.hip", "score_grad.hip", "api_mx.cpp", "mx_quant.hip",
-           "mx_dispatch.hip", "mx_ffn.hip", "router.hip", "reroute.hip", "permute.hip", "ffn.hip", "combine.hip",
+           "mx_dispatch.hip", "mx_ffn.hip", "mx_tile.hip", "router.hip", "reroute.hip", "permute.hip", "ffn.hip", "combine.hip",
            "probe.hip"]
 ARCH = "gfx950"
 

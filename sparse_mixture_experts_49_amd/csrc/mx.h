@@ -1,5 +1,6 @@
 // Launchers of the MXFP4 kernels: quantisation (mx_quant.hip), the dispatch for up to
-// 256 experts (mx_dispatch.hip) and the expert products (mx_ffn.hip).
+// 256 experts (mx_dispatch.hip) and the expert products (mx_ffn.hip,
+// mx_tile.hip).
 #pragma once
 
 #include <hip/hip_runtime.h>
@@ -44,5 +45,6 @@ struct MxFfnArgs {
 size_t mx_act_bytes(int T, int k, int E, int K, bool fp4);
 size_t mx_partial_bytes(int T, int k, int E, int N, int K);
 hipError_t launch_mx_ffn(const MxFfnArgs& a, hipStream_t s);
+hipError_t launch_mx_tile(const MxFfnArgs& a, hipStream_t s);   // mx_tile.hip
 
 }  // namespace moe
