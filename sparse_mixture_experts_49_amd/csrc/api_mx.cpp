@@ -49,7 +49,7 @@ MxLayout layout_of(const moe_mx_desc* d) {
   size_t p = 0;
   auto take = [&](size_t bytes) { size_t at = p; p += up256(bytes); return at; };
   auto larger = [](size_t a, size_t b) { return a > b ? a : b; };
-  L.act = take(larger(moe::mx_act_bytes(T, k, E, D, fp4), moe::mx_act_bytes(T, k, E, F, fp4)));
+  L.act = take(larger(moe::mx_act_bytes(T, k, E, F, D, fp4), moe::mx_act_bytes(T, k, E, D, F, fp4)));
   L.partial = take(larger(moe::mx_partial_bytes(T, k, E, F, D), moe::mx_partial_bytes(T, k, E, D, F)));
   L.blk_hist = take(nb * E * 4);
   L.blk_base = take(nb * E * 4);

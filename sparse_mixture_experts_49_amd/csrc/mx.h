@@ -42,9 +42,11 @@ struct MxFfnArgs {
   uint8_t* act;            // workspace of mx_act_bytes
   float* partial;          // workspace of mx_partial_bytes
 };
-size_t mx_act_bytes(int T, int k, int E, int K, bool fp4);
+size_t mx_act_bytes(int T, int k, int E, int N, int K, bool fp4);
 size_t mx_partial_bytes(int T, int k, int E, int N, int K);
 hipError_t launch_mx_ffn(const MxFfnArgs& a, hipStream_t s);
-hipError_t launch_mx_tile(const MxFfnArgs& a, hipStream_t s);   // mx_tile.hip
+// mx_tile.hip: the LDS-tiled products (K >= 512).
+hipError_t launch_mx_tile(const MxFfnArgs& a, hipStream_t s);
+size_t mx_tile_bytes(long rows, int E, int N, int K, bool fp4);
 
 }  // namespace moe

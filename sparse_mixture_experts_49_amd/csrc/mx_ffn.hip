@@ -248,12 +248,13 @@ size_t mx_partial_bytes(int T, int k, int E, int N, int K) {
   return s > 1 ? (size_t)s * T * k * N * 4 : 0;
 }
 
-// Experts averaging at least 48 rows run the LDS-tiled kernel, the rest stream.
-static bool tiled(int T, int k, int E) { return (long)T * k >= 48L * E; }
+// Experts averaging at least 48 rows run the LDS-tiled kernel, the rest stream.  The tiled
+// kernel's loads run up to two steps of 256 k ahead, so it starts at k = 512.
+static bool tiled(int T, int k, int E, int K) { return (long)T * k >= 48L * E && K >= 512; }
 
-size_t mx_act_bytes(int T, int k, int E, int K, bool fp4) {
-  const size_t n = (size_t)T * k * K;
-  return !fp4 ? 0 : tiled(T, k, E) ? n / 2 + n / 32 : n * 2;
+size_t mx_act_bytes(int T, int k, int E, int N, int K, bool fp4) {
+  const long rows = (long)T * k;
+  return tiled(T, k, E, K) ? mx_tile_bytes(rows, E, N, K, fp4) : fp4 ? (size_t)rows * K * 2 : 0;
 }
 
 template <bool UP, int NMT>
@@ -272,7 +273,7 @@ static void launch_stream(const MxFfnArgs& a, const void* act, int splits, hipSt
 }
 
 hipError_t launch_mx_ffn(const MxFfnArgs& a, hipStream_t s) {
-  if (tiled(a.T, a.k, a.E)) return launch_mx_tile(a, s);
+  if (tiled(a.T, a.k, a.E, a.K)) return launch_mx_tile(a, s);
   const void* act = a.a;
   if (a.fp4) {
     // The values the 4-bit activations stand for, as bf16: exact in the products.

@@ -3,23 +3,28 @@
 // Block tile BM rows of one expert x 256 output columns, 4 waves as 2 x 2, one wave per
 // SIMD, each with BM/2 x 128 outputs as 32x32 MFMA tiles in fp32 accumulators.  The MFMA
 // takes W rows as its first operand, so a lane holds four consecutive columns of a row.
-//   FP4 activations:  steps of 128 k, v_mfma_scale_f32_32x32x64_f8f6f4 with both
+//   fp4 activations:  steps of 256 k, v_mfma_scale_f32_32x32x64_f8f6f4 with both
 //                     operands e2m1 and a scale byte per lane (its 32 values of k);
 //   bf16 activations: steps of 64 k, codes widened in registers to bf16 (exact, scale
 //                     included) one slice ahead of v_mfma_f32_32x32x16_bf16.  The k of a
 //                     slice is free as long as both operands agree: lane half h takes
 //                     k = 32 h + 8 s .. + 7 for slice s, so one 16-byte read of a code row
 //                     serves the lane's whole step and has one scale.
-// Operands go from memory straight into a ring of S LDS stages, scales among them
-// (one dword per row and 128 k).  One barrier per step, in its middle: the first half
-// multiplies what is in registers and reads the second half's fragments; then step t+1
-// has landed and everyone is done with stage t, so the second half reads step t+1's
-// first fragments and refills stage t with step t+S.  No fragment read waits on the
-// barrier it follows, and loads have S - 1/2 steps to arrive.
+//
+// What bounds the loads is cache lines, not bytes: measured on MI355X, LDS loads from L2
+// move about one line per ns and CU, whole or in part (rows of 128 B 127 B/ns, of 64 B
+// 65 B/ns, single dwords 4 B/ns).  So rows are read 128 B at a time where LDS allows it,
+// and the scales, which the caller has by rows (a line per row for 8 useful bytes), are
+// first copied to [k / 256][row][8 bytes], which a tile reads in whole lines.
+//
+// Persistent blocks, one per CU: the loads run S - 1/2 steps ahead of the products and go
+// on into the block's next tile, so its first steps arrive while this tile's results are
+// finished and stored.  One barrier per step, before its last part: by then the next step
+// has landed, everyone has read the last of this one, and its stage is refilled.
 //
 // LDS banks: 16-byte chunks of a row sit at chunk ^ f(row) such that 16 consecutive rows'
-// reads of one chunk touch every bank once (64 B rows: (row >> 2) & 3; 128 B rows:
-// (row >> 1) & 7; 32 B rows: (row >> 3) & 1).
+// reads of one chunk touch every bank once (128 B rows: (row >> 1) & 7; 32 B rows:
+// (row >> 3) & 1).
 #include <algorithm>
 #include <type_traits>
 
@@ -30,6 +35,7 @@ namespace moe {
 
 constexpr int kXcd = 8, kBand = 4;
 constexpr int kTileN = 256;
+constexpr int kCus = 256;           // one block per CU
 
 typedef int i32x8 __attribute__((ext_vector_type(8)));
 
@@ -41,38 +47,36 @@ __device__ __forceinline__ f32x16 mfma_fp4(u32x4 w, int ws, u32x4 a, int as, f32
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, BYTE, ws, BYTE, as);
 }
 
-// global -> LDS from a uniform base and a 32-bit lane offset; the compiler sees no LDS
-// write, the kernel waits for vmcnt itself.  dma16: 16 B per lane, dma4: 4 B per lane.
+// global -> LDS, 16 B per lane, from a uniform base and a 32-bit lane offset; the compiler
+// sees no LDS write, the kernel waits for vmcnt itself.
 __device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds_addr) {
   asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-               :: "v"(off), "s"(base), "s"(lds_addr) : "memory", "m0");
-}
-__device__ __forceinline__ void dma4(const void* base, uint32_t off, uint32_t lds_addr) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dword %0, %1"
                :: "v"(off), "s"(base), "s"(lds_addr) : "memory", "m0");
 }
 constexpr int wait_vm(int vm) { return (vm & 0xF) | ((vm >> 4) << 14) | (0x7 << 4) | (0xF << 8); }
 constexpr int wait_vm_lgkm0(int vm) { return (vm & 0xF) | ((vm >> 4) << 14) | (0x7 << 4); }
 
-// The experts' rows cut into m-tiles of BM laid end to end; lane l holds experts 4l .. 4l+3.
-struct Tiles {
-  int lo[4], hi[4], first[4];
-  int total;
+// The experts' rows cut into m-tiles of BM laid end to end, as a table in LDS: lane l
+// holds experts 4l .. 4l+3, entry [i][l] = {first row, end, first m-tile} of 4l + i.
+struct TileTable {
+  int lo[4][64], hi[4][64], first[4][64];
 };
 
+// Every wave writes the same table (no barrier needed); returns the number of m-tiles.
 template <int BM>
-__device__ __forceinline__ Tiles tiles_of(const int32_t* __restrict__ offsets, int E, int rows) {
+__device__ __forceinline__ int fill_tiles(const int32_t* __restrict__ offsets, int E, int rows,
+                                          TileTable& t) {
   const int lane = __lane_id();
-  Tiles t;
-  int n[4], sum = 0;
+  int first[4], sum = 0;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
     const int e = lane * 4 + i;
-    t.lo[i] = e < E ? min(max(offsets[e], 0), rows) : 0;
-    t.hi[i] = e < E ? min(max(offsets[e + 1], t.lo[i]), rows) : 0;
-    n[i] = (t.hi[i] - t.lo[i] + BM - 1) / BM;
-    t.first[i] = sum;
-    sum += n[i];
+    const int lo = e < E ? min(max(offsets[e], 0), rows) : 0;
+    const int hi = e < E ? min(max(offsets[e + 1], lo), rows) : 0;
+    t.lo[i][lane] = lo;
+    t.hi[i][lane] = hi;
+    first[i] = sum;
+    sum += (hi - lo + BM - 1) / BM;
   }
   int incl = sum;
 #pragma unroll
@@ -81,23 +85,26 @@ __device__ __forceinline__ Tiles tiles_of(const int32_t* __restrict__ offsets, i
     if (lane >= o) incl += v;
   }
 #pragma unroll
-  for (int i = 0; i < 4; ++i) t.first[i] += incl - sum;
-  t.total = __builtin_amdgcn_readfirstlane(__shfl(incl, 63));
-  return t;
+  for (int i = 0; i < 4; ++i) t.first[i][lane] = first[i] + incl - sum;
+  __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+  __builtin_amdgcn_wave_barrier();
+  return __builtin_amdgcn_readfirstlane(__shfl(incl, 63));
 }
 
 template <int BM>
-__device__ __forceinline__ bool find_tile(const Tiles& t, int mt, int& e, int& r0, int& r1) {
+__device__ __forceinline__ bool find_tile(const TileTable& t, int mt, int& e, int& r0, int& r1) {
+  const int lane = __lane_id();
   bool found = false;
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
-    const int n = (t.hi[i] - t.lo[i] + BM - 1) / BM;
-    const uint64_t own = __ballot(mt >= t.first[i] && mt < t.first[i] + n);
+    const int lo = t.lo[i][lane], hi = t.hi[i][lane], first = t.first[i][lane];
+    const int n = (hi - lo + BM - 1) / BM;
+    const uint64_t own = __ballot(mt >= first && mt < first + n);
     if (own) {
       const int l = __builtin_amdgcn_readfirstlane(__ffsll((unsigned long long)own) - 1);
       e = l * 4 + i;
-      r0 = __builtin_amdgcn_readfirstlane(__shfl(t.lo[i] + (mt - t.first[i]) * BM, l));
-      r1 = min(__builtin_amdgcn_readfirstlane(__shfl(t.hi[i], l)), r0 + BM);
+      r0 = __builtin_amdgcn_readlane(lo + (mt - first) * BM, l);
+      r1 = min(__builtin_amdgcn_readlane(hi, l), r0 + BM);
       found = true;
     }
   }
@@ -131,164 +138,331 @@ static long tile_blocks(long total, long ntn) {
 
 struct TileArgs {
   const uint8_t* a;        // codes [rows][K/2], or bf16 [rows][K]
-  const uint8_t* as;       // scales [rows][K/32] (FP4)
+  const uint8_t* as;       // scales of the dispatched rows [K/256][rows][8] (FP4)
   const int32_t* src;      // or null
   int k_top, tokens;
   const int32_t* offsets;
   int E, rows, N, K;
   const uint8_t* w;
-  const uint8_t* ws;
+  const uint8_t* ws;       // scales [E][K/256][N][8]
   const uint16_t* bias;
   void* out;
 };
 
+// Scales by rows ([row][K/32]) to groups of 256 k: [K/256 rounded up][row][8], dword h the
+// bytes of blocks h, h + 2, h + 4, h + 6 (the ones lane half h of the four slices of 64 k
+// needs); blocks past K are 0 (2^-127).  The first `w_units` threads take the weights, the
+// rest the dispatched rows of the activations.
+__global__ __launch_bounds__(256) void mx_scale_groups_kernel(
+    const uint8_t* __restrict__ ws, uint8_t* __restrict__ w_out, int64_t w_units, int N,
+    const uint8_t* __restrict__ as, uint8_t* __restrict__ a_out, int rows,
+    const int32_t* __restrict__ src, int k_top, int tokens, int K) {
+  int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
+  const int groups = (K + 255) / 256, pitch = K / 32;
+  const uint8_t* row;
+  uint8_t* out;
+  int g;
+  if (i < w_units) {
+    const int n = (int)(i % N);
+    const int64_t eg = i / N;
+    g = (int)(eg % groups);
+    row = ws + (eg / groups * N + n) * pitch;
+    out = w_out + i * 8;
+  } else {
+    i -= w_units;
+    if (!as || i >= (int64_t)rows * groups) return;
+    const int r = (int)(i % rows);
+    g = (int)(i / rows);
+    const int from = src ? (int)min((uint32_t)src[r] / (uint32_t)k_top, (uint32_t)tokens - 1u) : r;
+    row = as + (size_t)from * pitch;
+    out = a_out + i * 8;
+  }
+  const uint32_t lo = *reinterpret_cast<const uint32_t*>(row + g * 8);
+  const uint32_t hi = g * 8 + 4 < pitch ? *reinterpret_cast<const uint32_t*>(row + g * 8 + 4) : 0u;
+  *reinterpret_cast<uint2*>(out) = make_uint2(__builtin_amdgcn_perm(hi, lo, 0x06040200),
+                                              __builtin_amdgcn_perm(hi, lo, 0x07050301));
+}
+
 template <bool FP4, bool UP, int BM>
 __global__ __launch_bounds__(256, 1) void mx_tile_kernel(TileArgs p) {
-  constexpr int S = FP4 ? 4 : 3;
-  constexpr int BK = FP4 ? 128 : 64;
-  constexpr int kARow = FP4 ? 64 : 128, kWRow = FP4 ? 64 : 32;   // bytes per row per step
-  constexpr int kA = BM * kARow, kW = kTileN * kWRow;
-  constexpr int kSA = FP4 ? BM * 4 : 0, kSW = kTileN * 4;
-  constexpr int kStage = kA + kW + (FP4 ? 1024 : 0) + kSW;
-  constexpr int oW = kA, oSA = kA + kW, oSW = oSA + (FP4 ? 1024 : 0);
+  constexpr int S = FP4 ? 2 : 3;
+  constexpr int KS = FP4 ? 256 : 64;                             // k per step
+  constexpr int kWRow = FP4 ? 128 : 32;                          // bytes of a W row per step
+  constexpr int kA = BM * 128, kW = kTileN * kWRow;
+  constexpr int kSA = FP4 ? BM * 8 : 0, kSW = kTileN * 8;
+  constexpr int kStage = kA + kW + kSA + kSW;
+  constexpr int oW = kA, oSA = kA + kW, oSW = oSA + kSA;
   constexpr int kAI = kA / 4096, kWI = kW / 4096;                // 1 KB loads per wave
-  constexpr int L = kAI + kWI + (FP4 ? 2 : 1);
+  constexpr int L = kAI + kWI + 1;
   constexpr int kMT = BM / 64, kNT = 4;                          // 32x32 tiles per wave
-  static_assert(S * kStage <= 160 * 1024 && kAI >= 1 && kSA <= 1024, "LDS plan");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[S * kStage];
+  constexpr int kM = kMT * kNT;                                  // MFMAs per slice
+  constexpr int kOutStage = 4096;                                // epilogue bytes per wave
+  static_assert(S * kStage + 4 * kOutStage + sizeof(TileTable) <= 160 * 1024 && kAI >= 1, "LDS plan");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S * kStage + 4 * kOutStage];
+  __shared__ TileTable table;
 
-  const int ntn = (p.N + kTileN - 1) / kTileN;
-  const Tiles tiles = tiles_of<BM>(p.offsets, p.E, p.rows);
-  int mt, nt, e, r0, r1;
-  if (!tile_of(tiles.total, ntn, blockIdx.x, mt, nt)) return;
-  if (!find_tile<BM>(tiles, mt, e, r0, r1)) return;
-  const int n0 = nt * kTileN, N = p.N, K = p.K;
-
+  const int N = p.N, K = p.K, ntn = (N + kTileN - 1) / kTileN;
+  const int nk = (K + KS - 1) / KS;
   const int tid = threadIdx.x, lane = tid & 63;
   const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
   const int wm = wave >> 1, wn = wave & 1, fr = lane & 31, fc = lane >> 5;
-
-  // ---- load plan: 32-bit lane offsets from uniform bases that advance with k ----
-  auto arow = [&](int r) {
-    const int g = min(r0 + r, r1 - 1);
-    if constexpr (UP) {
-      if (p.src) return (int)min((uint32_t)p.src[g] / (uint32_t)p.k_top, (uint32_t)p.tokens - 1u);
-    }
-    return g;
-  };
-  const uint32_t a_pitch = FP4 ? K / 2 : K * 2, w_pitch = K / 2, s_pitch = K / 32;
-  uint32_t a_off[kAI], w_off[kWI], sa_off = 0, sw_off;
-#pragma unroll
-  for (int i = 0; i < kAI; ++i) {
-    constexpr int kLanes = kARow / 16, kPer = 64 / kLanes;       // lanes per row, rows per load
-    const int row = (i * 4 + wave) * kPer + lane / kLanes;
-    const int c = (lane % kLanes) ^ (FP4 ? (row >> 2) & 3 : (row >> 1) & 7);
-    a_off[i] = (uint32_t)arow(row) * a_pitch + c * 16;
-  }
-#pragma unroll
-  for (int i = 0; i < kWI; ++i) {
-    constexpr int kLanes = kWRow / 16, kPer = 64 / kLanes;
-    const int row = (i * 4 + wave) * kPer + lane / kLanes;
-    const int c = (lane % kLanes) ^ (FP4 ? (row >> 2) & 3 : (row >> 3) & 1);
-    w_off[i] = (uint32_t)min(n0 + row, N - 1) * w_pitch + c * 16;
-  }
-  // Scales: wave w takes rows (64 w + lane) of each operand (BM < 256: some rows twice,
-  // with the same value).
-  if constexpr (FP4) sa_off = (uint32_t)arow((wave * 64) % BM + lane) * s_pitch;
-  sw_off = (uint32_t)min(n0 + wave * 64 + lane, N - 1) * s_pitch;
-  const uint8_t* w_base = p.w + (size_t)e * N * (K / 2);
-  const uint8_t* ws_base = p.ws + (size_t)e * N * (K / 32);
-  const int nk = K / BK;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+  const uint32_t a_pitch = FP4 ? K / 2 : K * 2, w_pitch = K / 2;
 
-  // Load i (0 <= i < L) of step `t` into its stage; steps past the last repeat it (those
-  // loads land in a free stage and are never read).
-  auto load = [&](int i, int t, int stage) {
-    const int s = min(t, nk - 1);
+  // ---- the tile being loaded: 32-bit lane offsets from uniform bases that advance ----
+  const int total = fill_tiles<BM>(p.offsets, p.E, p.rows, table);
+  struct Where {
+    int e, r0, r1, n0;
+  };
+  int b = blockIdx.x;
+  auto locate = [&](Where& w) {
+    int mt, nt;
+    if (!tile_of(total, ntn, b, mt, nt)) return false;
+    if (!find_tile<BM>(table, mt, w.e, w.r0, w.r1)) return false;
+    w.n0 = nt * kTileN;
+    return true;
+  };
+  // W rows of load i: 4 kPer i + those of load 0, one lane offset; where the tile's second
+  // 128 columns are past N its first 128 are read again.
+  constexpr int kWLanes = kWRow / 16, kWPer = 64 / kWLanes;
+  uint32_t a_off[kAI];
+  const int w_row0 = wave * kWPer + lane / kWLanes;
+  const uint32_t w_off = (uint32_t)w_row0 * w_pitch +
+                         (((lane % kWLanes) ^ (FP4 ? (w_row0 >> 1) & 7 : (w_row0 >> 3) & 1)) << 4);
+  uint32_t w_wrap;                                               // bytes to go back
+  const uint8_t *w_base, *s_base;                                // s_base: this wave's scales
+  size_t s_step;                                                 // bytes per group of 256 k
+  auto aim = [&](const Where& w) {
+    int g[kAI];
+#pragma unroll
+    for (int i = 0; i < kAI; ++i) g[i] = min(w.r0 + (i * 4 + wave) * 8 + (lane >> 3), w.r1 - 1);
+    if (UP && p.src) {
+#pragma unroll
+      for (int i = 0; i < kAI; ++i) g[i] = p.src[g[i]];
+#pragma unroll
+      for (int i = 0; i < kAI; ++i)
+        g[i] = (int)min((uint32_t)g[i] / (uint32_t)p.k_top, (uint32_t)p.tokens - 1u);
+    }
+#pragma unroll
+    for (int i = 0; i < kAI; ++i) {
+      const int row = (i * 4 + wave) * 8 + (lane >> 3);
+      a_off[i] = (uint32_t)g[i] * a_pitch + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
+    }
+    w_base = p.w + ((size_t)w.e * N + w.n0) * w_pitch;
+    w_wrap = N - w.n0 < kTileN ? 128u * w_pitch : 0u;
+    // One 1 KB load of scales (128 rows) per wave and step: the first two waves the
+    // activations' (FP4; BM = 128: both the same), the others the weights'.
+    if (FP4 && wave < 2) {
+      s_base = p.as + ((size_t)w.r0 + (wave * 128) % BM) * 8;
+      s_step = (size_t)p.rows * 8;
+    } else {
+      s_base = p.ws + (((size_t)w.e * ((K + 255) / 256)) * N + w.n0 + (wave & 1) * 128) * 8;
+      s_step = (size_t)N * 8;
+    }
+  };
+  const uint32_t s_lds = (FP4 && wave < 2) ? oSA + (wave * 1024) % (kSA ? kSA : 1) : oSW + (wave & 1) * 1024;
+  // FP4 and K an odd multiple of 128: the last step's chunks past the row's end read the
+  // row's first half of that step instead; their scales are 0.
+  const uint32_t past_end = (FP4 && ((lane & 7) ^ ((wave * 4 + (lane >> 4)) & 7)) >= 4) ? 64u : 0u;
+
+  Where cur, next;
+  if (!locate(cur)) return;
+  next = cur;
+  bool more = true;                                              // the loads have a tile
+  aim(cur);
+  int ls = 0;                                                    // its step
+  auto load = [&](int i, int stage, uint32_t back) {
     const uint32_t base = lds0 + stage * kStage;
     if (i < kAI) {
-      dma16(p.a + (size_t)s * kARow, a_off[i < kAI ? i : 0], base + (i * 4 + wave) * 1024);
+      dma16(p.a + (size_t)ls * 128, a_off[i < kAI ? i : 0] - back, base + (i * 4 + wave) * 1024);
     } else if (i < kAI + kWI) {
       const int j = i - kAI;
-      dma16(w_base + (size_t)s * kWRow, w_off[j < 0 || j >= kWI ? 0 : j], base + oW + (j * 4 + wave) * 1024);
-    } else if (i == kAI + kWI) {
-      dma4(ws_base + (FP4 ? s : s >> 1) * 4, sw_off, base + oSW + wave * 256);
+      const uint32_t row = (uint32_t)(j * 4 * kWPer) * w_pitch - (j * 4 * kWPer >= 128 ? w_wrap : 0u);
+      dma16(w_base + row + (size_t)ls * kWRow, w_off - back, base + oW + (j * 4 + wave) * 1024);
     } else {
-      dma4(p.as + s * 4, sa_off, base + oSA + ((wave * 64) % BM) * 4);
+      dma16(s_base + (FP4 ? ls : ls >> 2) * s_step, (uint32_t)lane * 16, base + s_lds);
     }
+  };
+  auto back_of = [&]() -> uint32_t { return (FP4 && (K & 128) && ls == nk - 1) ? past_end : 0u; };
+  // After a step's loads: on to the next step, or tile; past the last tile the last step
+  // is loaded again (those loads land in a free stage and are never read).
+  auto advance = [&]() {
+    if (++ls < nk) return;
+    if (more) {
+      b += gridDim.x;
+      Where w;
+      more = locate(w);
+      if (more) {
+        next = w;
+        aim(w);
+        ls = 0;
+        return;
+      }
+    }
+    ls = nk - 1;
   };
 
   f32x16 acc[kNT][kMT];
-#pragma unroll
-  for (int j = 0; j < kNT; ++j)
-#pragma unroll
-    for (int m = 0; m < kMT; ++m)
-#pragma unroll
-      for (int q = 0; q < 16; ++q) acc[j][m][q] = 0.f;
-
+  // Fragment addresses: rows 32 apart share their swizzle, so a slice has one lane offset.
+  const uint32_t f_swz = (fr >> 1) & 7;
+  const uint32_t a_lane = (uint32_t)(wm * (BM / 2) + fr) * 128, w_lane = (uint32_t)(wn * 128 + fr) * kWRow;
   auto read_a = [&](int stage, int m, int chunk) {
-    const int row = wm * (BM / 2) + m * 32 + fr;
-    return ld16(lds + stage * kStage + row * kARow + ((chunk ^ (FP4 ? (row >> 2) & 3 : (row >> 1) & 7)) << 4));
+    return ld16(lds + (stage * kStage + a_lane + ((chunk ^ f_swz) << 4)) + m * 4096);
   };
   auto read_w = [&](int stage, int j, int chunk) {
-    const int row = wn * 128 + j * 32 + fr;
-    return ld16(lds + stage * kStage + oW + row * kWRow + ((chunk ^ (FP4 ? (row >> 2) & 3 : (row >> 3) & 1)) << 4));
+    const uint32_t c = (chunk ^ (FP4 ? f_swz : (uint32_t)(fr >> 3) & 1u)) << 4;
+    return ld16(lds + (stage * kStage + w_lane + c) + oW + j * 32 * kWRow);
   };
   auto read_sa = [&](int stage, int m) {
-    const uint32_t v = *reinterpret_cast<const uint32_t*>(lds + stage * kStage + oSA + (wm * (BM / 2) + m * 32 + fr) * 4);
-    return (int)(v >> (8 * fc));
+    return *reinterpret_cast<const int*>(lds + (stage * kStage + (wm * (BM / 2) + fr) * 8 + fc * 4) + oSA + m * 256);
   };
   auto read_sw = [&](int stage, int j) {
-    return *reinterpret_cast<const uint32_t*>(lds + stage * kStage + oSW + (wn * 128 + j * 32 + fr) * 4);
+    return *reinterpret_cast<const int*>(lds + (stage * kStage + (wn * 128 + fr) * 8 + fc * 4) + oSW + j * 256);
   };
 
-  // ---- prologue ----
+  // Epilogue of the tile at `w`: bias, GELU, then through the wave's own 4 KB of LDS (32 rows
+  // of 128 B, chunks at chunk ^ ((row >> 1) & 7)) to whole 128 B row segments.
+  uint8_t* my = lds + S * kStage + wave * kOutStage;
+  auto finish = [&](const Where& w) {
+    constexpr int kOut = UP ? 2 : 4, kCols = 128 / kOut;           // columns per 128 B
+    constexpr int kJ = kCols / 32;                                 // 32-column tiles per pass
+    uint2 braw[kNT][4];
 #pragma unroll
-  for (int s = 0; s < S; ++s)
+    for (int j = 0; j < kNT; ++j)
 #pragma unroll
-    for (int i = 0; i < L; ++i) load(i, s, s);
-  __builtin_amdgcn_s_waitcnt(wait_vm((S - 1) * L));
+      for (int g = 0; g < 4; ++g) {
+        const int col = w.n0 + wn * 128 + j * 32 + 8 * g + 4 * fc;
+        braw[j][g] = (p.bias && col < N) ? *reinterpret_cast<const uint2*>(p.bias + (size_t)w.e * N + col)
+                                         : make_uint2(0u, 0u);
+      }
+#pragma unroll
+    for (int m = 0; m < kMT; ++m) {
+#pragma unroll
+      for (int jp = 0; jp < kNT; jp += kJ) {
+#pragma unroll
+        for (int jj = 0; jj < kJ; ++jj)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int j = jp + jj;
+            float v[4];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = acc[j][m][4 * g + q];
+            v[0] += __uint_as_float(braw[j][g].x << 16);
+            v[1] += __uint_as_float(braw[j][g].x & 0xffff0000u);
+            v[2] += __uint_as_float(braw[j][g].y << 16);
+            v[3] += __uint_as_float(braw[j][g].y & 0xffff0000u);
+            if constexpr (UP) {
+              const int c = (jj * 4 + g) ^ ((fr >> 1) & 7);
+              *reinterpret_cast<uint2*>(my + fr * 128 + (c << 4) + fc * 8) =
+                  make_uint2(pack_bf16x2(gelu_erf(v[0]), gelu_erf(v[1])), pack_bf16x2(gelu_erf(v[2]), gelu_erf(v[3])));
+            } else {
+              const int c = (2 * g + fc) ^ ((fr >> 1) & 7);
+              *reinterpret_cast<f32x4*>(my + fr * 128 + (c << 4)) = f32x4{v[0], v[1], v[2], v[3]};
+            }
+          }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int row = i * 8 + (lane >> 3), c = lane & 7;
+          const u32x4 v = ld16(my + row * 128 + ((c ^ ((row >> 1) & 7)) << 4));
+          const int r = w.r0 + wm * (BM / 2) + m * 32 + row;
+          const int col = w.n0 + wn * 128 + jp * 32 + c * (16 / kOut);
+          if (r < w.r1 && col < N) st16(static_cast<uint8_t*>(p.out) + ((size_t)r * N + col) * kOut, v);
+        }
+        __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
+        __builtin_amdgcn_wave_barrier();
+      }
+    }
+  };
+
+  // ---- prologue: every stage but the last in full, of the last its first LA loads ----
+  constexpr int LA = FP4 ? (L + 1) / 2 : L;   // FP4: the rest goes with the next step's start
+#pragma unroll
+  for (int s = 0; s < S; ++s) {
+    const uint32_t back = back_of();
+#pragma unroll
+    for (int i = 0; i < L; ++i)
+      if (s < S - 1 || i < LA) load(i, s, back);
+    if (s < S - 1 || LA == L) advance();
+  }
+  __builtin_amdgcn_s_waitcnt(wait_vm((S - 2) * L + LA));
   __syncthreads();
 
-  int st = 0;                                          // stage of step t
+  int st = 0;                                          // stage of the step being multiplied
   if constexpr (FP4) {
     u32x4 xa[kMT], xw[kNT], ya[kMT], yw[kNT];
     int sa[kMT], sw[kNT];
 #pragma unroll
     for (int m = 0; m < kMT; ++m) xa[m] = read_a(0, m, fc), sa[m] = read_sa(0, m);
 #pragma unroll
-    for (int j = 0; j < kNT; ++j) xw[j] = read_w(0, j, fc), sw[j] = (int)(read_sw(0, j) >> (8 * fc));
-    constexpr int kM = kMT * kNT;
-    for (int t = 0; t < nk; ++t) {
-      const int st1 = st == S - 1 ? 0 : st + 1;
-      // Slice 0: its MFMAs, reads of slice 1.
+    for (int j = 0; j < kNT; ++j) xw[j] = read_w(0, j, fc), sw[j] = read_sw(0, j);
+    for (;;) {
 #pragma unroll
-      for (int q = 0; q < kM; ++q) {
-        const int j = q / kMT, m = q % kMT;
-        acc[j][m] = mfma_fp4<0>(xw[j], sw[j], xa[m], sa[m], acc[j][m]);
-        if (q < kMT) ya[q] = read_a(st, q, 2 + fc);
-        if (q < kNT) yw[q] = read_w(st, q, 2 + fc);
-        __builtin_amdgcn_sched_barrier(0);
+      for (int j = 0; j < kNT; ++j)
+#pragma unroll
+        for (int m = 0; m < kMT; ++m)
+#pragma unroll
+          for (int q = 0; q < 16; ++q) acc[j][m][q] = 0.f;
+      const Where done = cur;
+      bool go_on = false;
+      for (int t = 0; t < nk; ++t) {
+        // Slice 0: the rest of the pending step's loads (into the other stage).
+        {
+          const uint32_t back = back_of();
+#pragma unroll
+          for (int q = 0; q < kM; ++q) {
+            const int j = q / kMT, m = q % kMT;
+            acc[j][m] = mfma_fp4<0>(xw[j], sw[j], xa[m], sa[m], acc[j][m]);
+            if (q < kMT) ya[q] = read_a(st, q, 2 + fc);
+            if (q < kNT) yw[q] = read_w(st, q, 2 + fc);
+#pragma unroll
+            for (int i = LA + q * (L - LA) / kM; i < LA + (q + 1) * (L - LA) / kM; ++i) load(i, st ^ 1, back);
+            __builtin_amdgcn_sched_barrier(0);
+          }
+        }
+#pragma unroll
+        for (int q = 0; q < kM; ++q) {
+          const int j = q / kMT, m = q % kMT;
+          acc[j][m] = mfma_fp4<1>(yw[j], sw[j], ya[m], sa[m], acc[j][m]);
+          if (q < kMT) xa[q] = read_a(st, q, 4 + fc);
+          if (q < kNT) xw[q] = read_w(st, q, 4 + fc);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        advance();
+        if (t == nk - 1) go_on = more;
+#pragma unroll
+        for (int q = 0; q < kM; ++q) {
+          const int j = q / kMT, m = q % kMT;
+          acc[j][m] = mfma_fp4<2>(xw[j], sw[j], xa[m], sa[m], acc[j][m]);
+          if (q < kMT) ya[q] = read_a(st, q, 6 + fc);
+          if (q < kNT) yw[q] = read_w(st, q, 6 + fc);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+        __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));
+        __syncthreads();
+        // Slice 3: the next step's first fragments and scales, loads into this stage.
+        int na[kMT], nw[kNT];
+        const uint32_t back = back_of();
+#pragma unroll
+        for (int q = 0; q < kM; ++q) {
+          const int j = q / kMT, m = q % kMT;
+          acc[j][m] = mfma_fp4<3>(yw[j], sw[j], ya[m], sa[m], acc[j][m]);
+          if (q < kMT) xa[q] = read_a(st ^ 1, q, fc), na[q] = read_sa(st ^ 1, q);
+          if (q < kNT) xw[q] = read_w(st ^ 1, q, fc), nw[q] = read_sw(st ^ 1, q);
+#pragma unroll
+          for (int i = q * LA / kM; i < (q + 1) * LA / kM; ++i) load(i, st, back);
+          __builtin_amdgcn_sched_barrier(0);
+        }
+#pragma unroll
+        for (int m = 0; m < kMT; ++m) sa[m] = na[m];
+#pragma unroll
+        for (int j = 0; j < kNT; ++j) sw[j] = nw[j];
+        st ^= 1;
       }
-      __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0((S - 2) * L));
-      __syncthreads();
-      // Slice 1: its MFMAs, reads of the next step's slice 0, loads of step t + S.
-      int na[kMT], nw[kNT];
-#pragma unroll
-      for (int q = 0; q < kM; ++q) {
-        const int j = q / kMT, m = q % kMT;
-        acc[j][m] = mfma_fp4<2>(yw[j], sw[j], ya[m], sa[m], acc[j][m]);
-        if (q < kMT) xa[q] = read_a(st1, q, fc), na[q] = read_sa(st1, q);
-        if (q < kNT) xw[q] = read_w(st1, q, fc), nw[q] = (int)(read_sw(st1, q) >> (8 * fc));
-#pragma unroll
-        for (int i = q * L / kM; i < (q + 1) * L / kM; ++i) load(i, t + S, st);
-        __builtin_amdgcn_sched_barrier(0);
-      }
-#pragma unroll
-      for (int m = 0; m < kMT; ++m) sa[m] = na[m];
-#pragma unroll
-      for (int j = 0; j < kNT; ++j) sw[j] = nw[j];
-      st = st1;
+      finish(done);
+      if (!go_on) break;
+      cur = next;
     }
   } else {
     u32x4 xa[2][kMT], ya[2][kMT], raw[kNT], wf[2][kNT];
@@ -303,122 +477,81 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(TileArgs p) {
       else v = __builtin_bit_cast(uint32_t, __builtin_amdgcn_cvt_scalef32_pk_bf16_fp4(c, s[j], 3));
       to[j][q] = v;
     };
-    auto scale_of = [&](uint32_t v, int t) {
-      return __uint_as_float(((v >> (8 * (2 * (t & 1) + fc))) & 0xffu) << 23);
-    };
+    // The scale of step t: byte t % 4 of its group's dword.
+    auto scale_of = [&](int v, int t) { return __uint_as_float((((uint32_t)v >> (8 * (t & 3))) & 0xffu) << 23); };
 #pragma unroll
     for (int m = 0; m < kMT; ++m) xa[0][m] = read_a(0, m, 4 * fc), xa[1][m] = read_a(0, m, 4 * fc + 1);
 #pragma unroll
     for (int j = 0; j < kNT; ++j) raw[j] = read_w(0, j, fc), sc[j] = scale_of(read_sw(0, j), 0);
 #pragma unroll
     for (int i = 0; i < 4 * kNT; ++i) widen(raw, sc, wf[0], 0, i);
-    constexpr int kM = kMT * kNT;                      // MFMAs per slice
     constexpr int kCv = 4 * kNT;                       // conversions per slice
-    for (int t = 0; t < nk; ++t) {
-      const int st1 = st == S - 1 ? 0 : st + 1;
-      // Slices 0 and 1; reads of slices 2 and 3; conversions of slices 1 and 2.
+    for (;;) {
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+      for (int j = 0; j < kNT; ++j)
 #pragma unroll
-        for (int q = 0; q < kM; ++q) {
-          const int j = q / kMT, m = q % kMT;
-          acc[j][m] = mfma32_bf16(wf[s][j], xa[s][m], acc[j][m]);
+        for (int m = 0; m < kMT; ++m)
 #pragma unroll
-          for (int i = q * kCv / kM; i < (q + 1) * kCv / kM; ++i) widen(raw, sc, wf[s ^ 1], s + 1, i);
-          if (s == 0 && q < kMT) ya[0][q] = read_a(st, q, 4 * fc + 2), ya[1][q] = read_a(st, q, 4 * fc + 3);
-          __builtin_amdgcn_sched_barrier(0);
-        }
-      __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0((S - 2) * L));
-      __syncthreads();
-      // Slices 2 and 3; the next step's codes, scales and first fragments; loads.
-      u32x4 nraw[kNT];
-      float nsc[kNT];
+          for (int q = 0; q < 16; ++q) acc[j][m][q] = 0.f;
+      const Where done = cur;
+      bool go_on = false;
+      for (int t = 0; t < nk; ++t) {
+        const int st1 = st == S - 1 ? 0 : st + 1;
+        // Slices 0 and 1; reads of slices 2 and 3; conversions of slices 1 and 2.
 #pragma unroll
-      for (int s = 0; s < 2; ++s)
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-        for (int q = 0; q < kM; ++q) {
-          const int j = q / kMT, m = q % kMT;
-          acc[j][m] = mfma32_bf16(wf[s][j], ya[s][m], acc[j][m]);
+          for (int q = 0; q < kM; ++q) {
+            const int j = q / kMT, m = q % kMT;
+            acc[j][m] = mfma32_bf16(wf[s][j], xa[s][m], acc[j][m]);
 #pragma unroll
-          for (int i = q * kCv / kM; i < (q + 1) * kCv / kM; ++i) {
-            if (s == 0) widen(raw, sc, wf[1], 3, i);
-            else widen(nraw, nsc, wf[0], 0, i);
+            for (int i = q * kCv / kM; i < (q + 1) * kCv / kM; ++i) widen(raw, sc, wf[s ^ 1], s + 1, i);
+            if (s == 0 && q < kMT) ya[0][q] = read_a(st, q, 4 * fc + 2), ya[1][q] = read_a(st, q, 4 * fc + 3);
+            __builtin_amdgcn_sched_barrier(0);
           }
-          if (s == 0 && q < kNT) nraw[q] = read_w(st1, q, fc), nsc[q] = scale_of(read_sw(st1, q), t + 1);
-          if (s == 0 && q < kMT) xa[0][q] = read_a(st1, q, 4 * fc), xa[1][q] = read_a(st1, q, 4 * fc + 1);
-          const int at = s * kM + q;
+        __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0((S - 2) * L));
+        __syncthreads();
+        // Slices 2 and 3; the next step's codes, scales and first fragments; loads.
+        u32x4 nraw[kNT];
+        float nsc[kNT];
+        const int tn = t + 1 < nk ? t + 1 : 0;
 #pragma unroll
-          for (int i = at * L / (2 * kM); i < (at + 1) * L / (2 * kM); ++i) load(i, t + S, st);
-          __builtin_amdgcn_sched_barrier(0);
-        }
+        for (int s = 0; s < 2; ++s)
 #pragma unroll
-      for (int j = 0; j < kNT; ++j) raw[j] = nraw[j], sc[j] = nsc[j];
-      st = st1;
-    }
-  }
-  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");
-  __syncthreads();                                     // LDS free for the epilogue
-
-  // ---- epilogue: each wave turns its sub-tile in LDS and stores whole row segments ----
-  constexpr int kOut = UP ? 2 : 4;
-  constexpr int kRowB = 128 * kOut, kChunks = kRowB / 16;
-  constexpr int kRoom = S * kStage / 4 / kRowB / 32 * 32;         // rows a wave can stage
-  constexpr int kPass = kMT * 32 <= kRoom ? kMT * 32 : 32 * (kRoom / 32 >= 2 && kMT % 2 == 0 ? 2 : 1);
-  static_assert(kRoom >= 32 && (kMT * 32) % kPass == 0, "epilogue");
-  uint8_t* my = lds + wave * kPass * kRowB;
-  uint2 braw[kNT][4];
+          for (int q = 0; q < kM; ++q) {
+            const int j = q / kMT, m = q % kMT;
+            acc[j][m] = mfma32_bf16(wf[s][j], ya[s][m], acc[j][m]);
 #pragma unroll
-  for (int j = 0; j < kNT; ++j)
+            for (int i = q * kCv / kM; i < (q + 1) * kCv / kM; ++i) {
+              if (s == 0) widen(raw, sc, wf[1], 3, i);
+              else widen(nraw, nsc, wf[0], 0, i);
+            }
+            if (s == 0 && q < kNT) nraw[q] = read_w(st1, q, fc), nsc[q] = scale_of(read_sw(st1, q), tn);
+            if (s == 0 && q < kMT) xa[0][q] = read_a(st1, q, 4 * fc), xa[1][q] = read_a(st1, q, 4 * fc + 1);
+            const int at = s * kM + q;
 #pragma unroll
-    for (int g = 0; g < 4; ++g) {
-      const int col = n0 + wn * 128 + j * 32 + 8 * g + 4 * fc;
-      braw[j][g] = (p.bias && col < N) ? *reinterpret_cast<const uint2*>(p.bias + (size_t)e * N + col)
-                                       : make_uint2(0u, 0u);
-    }
-#pragma unroll
-  for (int pass = 0; pass < kMT * 32 / kPass; ++pass) {
-#pragma unroll
-    for (int j = 0; j < kNT; ++j)
-#pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const float bv[4] = {__uint_as_float(braw[j][g].x << 16), __uint_as_float(braw[j][g].x & 0xffff0000u),
-                             __uint_as_float(braw[j][g].y << 16), __uint_as_float(braw[j][g].y & 0xffff0000u)};
-#pragma unroll
-        for (int i = 0; i < kPass / 32; ++i) {
-          const int m = pass * (kPass / 32) + i, row = i * 32 + fr;
-          f32x4 v;
-#pragma unroll
-          for (int q = 0; q < 4; ++q) v[q] = acc[j][m][4 * g + q] + bv[q];
-          if constexpr (UP) {
-            const int chunk = (j * 4 + g) ^ (row & (kChunks - 1));
-            *reinterpret_cast<uint2*>(my + row * kRowB + (chunk << 4) + fc * 8) =
-                make_uint2(pack_bf16x2(gelu_erf(v[0]), gelu_erf(v[1])), pack_bf16x2(gelu_erf(v[2]), gelu_erf(v[3])));
-          } else {
-            const int chunk = (j * 8 + 2 * g + fc) ^ (row & (kChunks - 1));
-            *reinterpret_cast<f32x4*>(my + row * kRowB + (chunk << 4)) = v;
+            for (int i = at * L / (2 * kM); i < (at + 1) * L / (2 * kM); ++i) load(i, st, 0u);
+            __builtin_amdgcn_sched_barrier(0);
           }
-        }
+#pragma unroll
+        for (int j = 0; j < kNT; ++j) raw[j] = nraw[j], sc[j] = nsc[j];
+        st = st1;
+        advance();
+        if (t == nk - 1) go_on = more;
       }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_wave_barrier();
-    constexpr int kPerInst = 64 / kChunks;
-#pragma unroll 4
-    for (int rb = 0; rb < kPass; rb += kPerInst) {
-      const int row = rb + lane / kChunks, c = lane % kChunks;
-      const u32x4 v = ld16(my + row * kRowB + ((c ^ (row & (kChunks - 1))) << 4));
-      const int r = r0 + wm * (BM / 2) + pass * kPass + row;
-      const int col = n0 + wn * 128 + c * (16 / kOut);
-      if (r < r1 && col < N) st16(static_cast<uint8_t*>(p.out) + ((size_t)r * N + col) * kOut, v);
+      finish(done);
+      if (!go_on) break;
+      cur = next;
     }
-    asm volatile("s_waitcnt lgkmcnt(0)" ::: "memory");
-    __builtin_amdgcn_wave_barrier();
   }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");     // no load outlives its LDS
 }
 
 template <bool FP4, bool UP, int BM>
 static void launch_tile(const TileArgs& p, hipStream_t s) {
   const long most = p.rows / BM + std::min(p.E, p.rows);           // bound on the m-tiles
-  mx_tile_kernel<FP4, UP, BM><<<(unsigned)tile_blocks(most, (p.N + kTileN - 1) / kTileN), 256, 0, s>>>(p);
+  const long blocks = tile_blocks(most, (p.N + kTileN - 1) / kTileN);
+  mx_tile_kernel<FP4, UP, BM><<<(unsigned)std::min(blocks, (long)kCus), 256, 0, s>>>(p);
 }
 
 template <bool FP4, bool UP>
@@ -429,6 +562,26 @@ static void launch_tile_rows(const TileArgs& p, int bm, hipStream_t s) {
 
 // Rows per tile: 256 from 192 rows per expert on average, else 128.
 static int tile_height(long rows, int E) { return rows >= 192L * E ? 256 : 128; }
+
+// Activation codes and scales (FP4), then the regrouped scales, each padded by one tile's
+// worth of rows that the last tile may read past the end.
+struct TileSpace {
+  size_t scales, a_groups, w_groups, total;
+};
+static TileSpace tile_space(long rows, int E, int N, int K, bool fp4) {
+  auto up256 = [](size_t v) { return (v + 255) & ~size_t(255); };
+  const size_t groups = (K + 255) / 256, pad = 256 * 8;
+  TileSpace t{};
+  t.scales = fp4 ? up256((size_t)rows * K / 2) : 0;
+  t.a_groups = t.scales + (fp4 ? up256((size_t)rows * K / 32) : 0);
+  t.w_groups = t.a_groups + (fp4 ? up256(groups * rows * 8 + pad) : 0);
+  t.total = t.w_groups + up256((size_t)E * groups * N * 8 + pad);
+  return t;
+}
+
+size_t mx_tile_bytes(long rows, int E, int N, int K, bool fp4) {
+  return tile_space(rows, E, N, K, fp4).total;
+}
 
 hipError_t launch_mx_tile(const MxFfnArgs& a, hipStream_t s) {
   TileArgs p{};
@@ -441,20 +594,28 @@ hipError_t launch_mx_tile(const MxFfnArgs& a, hipStream_t s) {
   p.N = a.N;
   p.K = a.K;
   p.w = a.w;
-  p.ws = a.ws;
   p.bias = static_cast<const uint16_t*>(a.bias);
   p.out = a.out;
-  const int bm = tile_height(p.rows, a.E);
+  const TileSpace t = tile_space(p.rows, a.E, a.N, a.K, a.fp4);
+  uint8_t* scales = a.act + t.scales;
+  uint8_t* a_groups = a.act + t.a_groups;
+  uint8_t* w_groups = a.act + t.w_groups;
+  p.a = static_cast<const uint8_t*>(a.a);
   if (a.fp4) {
-    uint8_t* scales = a.act + (size_t)a.a_rows * a.K / 2;
     if (hipError_t e = launch_mx_quantize(a.a, true, a.a_rows, a.K, a.K, a.act, scales, s)) return e;
     p.a = a.act;
-    p.as = scales;
-    a.up ? launch_tile_rows<true, true>(p, bm, s) : launch_tile_rows<true, false>(p, bm, s);
-  } else {
-    p.a = static_cast<const uint8_t*>(a.a);
-    a.up ? launch_tile_rows<false, true>(p, bm, s) : launch_tile_rows<false, false>(p, bm, s);
+    p.as = a_groups;
   }
+  p.ws = w_groups;
+  const int groups = (a.K + 255) / 256;
+  const int64_t w_units = (int64_t)a.E * groups * a.N, units = w_units + (a.fp4 ? (int64_t)p.rows * groups : 0);
+  mx_scale_groups_kernel<<<(unsigned)((units + 255) / 256), 256, 0, s>>>(
+      a.ws, w_groups, w_units, a.N, a.fp4 ? scales : nullptr, a_groups, p.rows, p.src, a.k, a.T, a.K);
+  const int bm = tile_height(p.rows, a.E);
+  if (a.fp4)
+    a.up ? launch_tile_rows<true, true>(p, bm, s) : launch_tile_rows<true, false>(p, bm, s);
+  else
+    a.up ? launch_tile_rows<false, true>(p, bm, s) : launch_tile_rows<false, false>(p, bm, s);
   return hipGetLastError();
 }
 
