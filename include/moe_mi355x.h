@@ -341,8 +341,8 @@ int moe_forward_noalloc(const moe_desc* desc, const void* x, const moe_weights* 
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 
 typedef struct moe_score_desc {
-  int32_t tokens;          /* T >= 1; T * max(n_experts, top_k) fits int32 */
-  int32_t d_model;         /* d, a multiple of 128 */
+  int32_t tokens;          /* T, 1 .. 2^22 */
+  int32_t d_model;         /* d, a multiple of 128, at most 2^20 */
   int32_t n_experts;       /* 1 .. 256 */
   int32_t top_k;           /* 1 .. 8, at most the experts of top_groups groups */
   int32_t dtype;           /* MOE_DTYPE_*: x, w_router and d_x */

@@ -518,6 +518,13 @@ class ScoreGrads:
                    d_b_router=torch.empty(desc.n_experts, **f32))
 
 
+try:                                   # the handle alone, without a Stream object around it
+    _raw_stream = torch._C._cuda_getCurrentRawStream
+except AttributeError:
+    def _raw_stream(index):
+        return torch.cuda.current_stream(index).cuda_stream
+
+
 class _Call:
     """One call of the operators below: checks its tensors, all on one GPU, and runs it
     there on the given stream, or on the current stream of that GPU."""
@@ -549,8 +556,9 @@ class _Call:
 
     def run(self, fn, *args, stream=None):
         if stream is None:
-            stream = torch.cuda.current_stream(self.device)
-        stream = stream.cuda_stream if hasattr(stream, "cuda_stream") else stream
+            stream = _raw_stream(self.device.index)
+        elif hasattr(stream, "cuda_stream"):
+            stream = stream.cuda_stream
         if torch.cuda.current_device() != self.device.index:
             with torch.cuda.device(self.device):
                 status = fn(*args, stream)

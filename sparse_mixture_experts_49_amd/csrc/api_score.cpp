@@ -1,6 +1,5 @@
 // C ABI of the scored router: argument validation, workspace carving, launches.
 #include <cmath>
-#include <limits>
 
 #include "api_util.h"
 #include "score.h"
@@ -12,6 +11,8 @@ namespace {
 int validate_score(const moe_score_desc* d) {
   if (!d) return fail(MOE_ERR_INVALID, "desc must not be NULL");
   if (d->tokens < 1) return fail(MOE_ERR_INVALID, "tokens must be >= 1 (got %d)", d->tokens);
+  if (d->tokens > 1 << 22)
+    return fail(MOE_ERR_UNSUPPORTED, "tokens must be <= 2^22 (got %d)", d->tokens);
   if (d->d_model < 1) return fail(MOE_ERR_INVALID, "d_model must be >= 1 (got %d)", d->d_model);
   if (d->d_model % 128)
     return fail(MOE_ERR_UNSUPPORTED, "d_model (%d) must be a multiple of 128", d->d_model);
@@ -40,9 +41,8 @@ int validate_score(const moe_score_desc* d) {
   if (d->renormalize != 0 && d->renormalize != 1)
     return fail(MOE_ERR_INVALID, "renormalize must be 0 or 1");
   if (!std::isfinite(d->scale)) return fail(MOE_ERR_INVALID, "scale must be finite");
-  const long long widest = d->n_experts > d->top_k ? d->n_experts : d->top_k;
-  if (d->tokens * widest > std::numeric_limits<int32_t>::max())
-    return fail(MOE_ERR_UNSUPPORTED, "tokens * max(n_experts, top_k) exceeds int32");
+  if (d->d_model > 1 << 20)
+    return fail(MOE_ERR_UNSUPPORTED, "d_model must be <= 2^20 (got %d)", d->d_model);
   return MOE_OK;
 }
 
@@ -60,17 +60,18 @@ struct ScoreLayout {
 ScoreLayout layout_of(const moe_score_desc* d) {
   ScoreLayout L{};
   const moe::ScoreShape s = shape_of(d);
-  const size_t T = s.T, E = s.E, nb = moe::score_finish_blocks(s.T);
+  const size_t T = s.T, E = s.E;
   size_t p = 0;
   auto take = [&](size_t bytes) { size_t at = p; p += up256(bytes); return at; };
   L.part = take((size_t)moe::score_parts(s) * T * E * 4);
-  L.psum = take(nb * E * 8);
-  L.pload = take(nb * E * 4);
-  L.pz = take(nb * 8);
+  const size_t sums = T < 256 ? T : 256;              // blocks with partial sums, at most
+  L.psum = take(sums * E * 8);
+  L.pload = take(sums * E * 4);
+  L.pz = take(sums * 8);
   L.total = p;
   p = 0;
-  L.dl = take(T * E * 4);
-  L.pb = take(nb * E * 8);
+  L.dl = take(moe::score_dl_bytes(s));
+  L.pb = take((size_t)moe::score_grad_sum_blocks(s.T) * E * 8);
   L.pw = take((size_t)moe::score_grad_slices(s) * E * s.d * 4);
   if (p > L.total) L.total = p;
   return L;
@@ -218,7 +219,7 @@ int moe_score_backward(const moe_score_desc* desc, const void* x, const void* w_
   a.d_w = grads->d_w_router;
   a.d_b = grads->d_b_router;
   a.d_logits = grads->d_logits;
-  a.dl = at<float>(ws, L.dl);
+  a.dl = at<void>(ws, L.dl);
   a.pb = at<double>(ws, L.pb);
   a.pw = at<float>(ws, L.pw);
   return hip_status(moe::launch_score_grad(a, static_cast<hipStream_t>(stream)),

@@ -124,6 +124,43 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
   return __builtin_bit_cast(uint32_t, __builtin_convertvector((f32x2){lo, hi}, bf16x2));
 }
 
+// global -> LDS, 16 B per lane to lds_addr + lane * 16, from a uniform base and a 32-bit
+// lane offset.  The compiler sees no LDS write: the kernel waits for vmcnt itself
+// (wait_vm: at most vm vector-memory operations outstanding).
+__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds_addr) {
+  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
+               :: "v"(off), "s"(base), "s"(lds_addr) : "memory", "m0");
+}
+constexpr int wait_vm(int vm) { return (vm & 0xF) | ((vm >> 4) << 14) | (0x7 << 4) | (0xF << 8); }
+constexpr int wait_vm_lgkm0(int vm) { return (vm & 0xF) | ((vm >> 4) << 14) | (0x7 << 4); }
+
+// Reductions over the 64 lanes with DPP moves (a few cycles each, where a shuffle goes
+// through LDS): pairs, quads, eights and rows of 16 by permutation, then rows 0 -> 1 and
+// 2 -> 3, then the lower half into the upper; lane 63 holds the result, returned to all.
+template <typename F>
+__device__ __forceinline__ uint32_t wave_reduce(uint32_t v, uint32_t unit, F f) {
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)unit, (int)v, 0xB1, 0xF, 0xF, false));   // quad [1,0,3,2]
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)unit, (int)v, 0x4E, 0xF, 0xF, false));   // quad [2,3,0,1]
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)unit, (int)v, 0x141, 0xF, 0xF, false));  // half-row mirror
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)unit, (int)v, 0x140, 0xF, 0xF, false));  // row mirror
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)unit, (int)v, 0x142, 0xA, 0xF, false));  // row_bcast15
+  v = f(v, (uint32_t)__builtin_amdgcn_update_dpp((int)unit, (int)v, 0x143, 0xC, 0xF, false));  // row_bcast31
+  return (uint32_t)__builtin_amdgcn_readlane((int)v, 63);
+}
+__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
+  return wave_reduce(v, 0u, [](uint32_t a, uint32_t b) { return a > b ? a : b; });
+}
+__device__ __forceinline__ float wave_max_f(float v) {
+  return __uint_as_float(wave_reduce(__float_as_uint(v), 0xff800000u, [](uint32_t a, uint32_t b) {
+    return __float_as_uint(fmaxf(__uint_as_float(a), __uint_as_float(b)));
+  }));
+}
+__device__ __forceinline__ float wave_sum_f(float v) {
+  return __uint_as_float(wave_reduce(__float_as_uint(v), 0u, [](uint32_t a, uint32_t b) {
+    return __float_as_uint(__uint_as_float(a) + __uint_as_float(b));
+  }));
+}
+
 __device__ __forceinline__ int lane_id() { return __lane_id(); }
 
 }  // namespace moe

@@ -47,15 +47,6 @@ __device__ __forceinline__ f32x16 mfma_fp4(u32x4 w, int ws, u32x4 a, int as, f32
   return __builtin_amdgcn_mfma_scale_f32_32x32x64_f8f6f4(x, y, c, 4, 4, BYTE, ws, BYTE, as);
 }
 
-// global -> LDS, 16 B per lane, from a uniform base and a 32-bit lane offset; the compiler
-// sees no LDS write, the kernel waits for vmcnt itself.
-__device__ __forceinline__ void dma16(const void* base, uint32_t off, uint32_t lds_addr) {
-  asm volatile("s_mov_b32 m0, %2\n\ts_nop 0\n\tglobal_load_lds_dwordx4 %0, %1"
-               :: "v"(off), "s"(base), "s"(lds_addr) : "memory", "m0");
-}
-constexpr int wait_vm(int vm) { return (vm & 0xF) | ((vm >> 4) << 14) | (0x7 << 4) | (0xF << 8); }
-constexpr int wait_vm_lgkm0(int vm) { return (vm & 0xF) | ((vm >> 4) << 14) | (0x7 << 4); }
-
 // The experts' rows cut into m-tiles of BM laid end to end, as a table in LDS: lane l
 // holds experts 4l .. 4l+3, entry [i][l] = {first row, end, first m-tile} of 4l + i.
 struct TileTable {

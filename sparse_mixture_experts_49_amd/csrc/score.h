@@ -16,7 +16,7 @@ struct ScoreShape {
 
 // Parts the d-long dot products are cut into (partial logits [parts][T][E]).
 int score_parts(const ScoreShape& s);
-// Blocks of the finishing kernel, each with a partial row of the sums over tokens.
+// Blocks of the finishing kernel (at most 256), each with a column of the partial sums.
 int score_finish_blocks(int T);
 
 struct ScoreArgs {
@@ -37,14 +37,17 @@ struct ScoreArgs {
   float* aux;
   float* z_loss;
   float* part;             // workspace [parts][T][E]
-  double* psum;            // workspace [blocks][E]
-  int32_t* pload;          // workspace [blocks][E]
+  double* psum;            // workspace [E][blocks], blocks <= 256
+  int32_t* pload;          // workspace [E][blocks]
   double* pz;              // workspace [blocks]
 };
 hipError_t launch_score(const ScoreArgs& a, hipStream_t s);
 
 // Slices of the token range that d_w_router is summed in.
 int score_grad_slices(const ScoreShape& s);
+// Bytes of the logit gradients in the workspace, and blocks that sum them for d_b.
+size_t score_dl_bytes(const ScoreShape& s);
+int score_grad_sum_blocks(int T);
 
 struct ScoreGradArgs {
   ScoreShape sh;
@@ -62,8 +65,8 @@ struct ScoreGradArgs {
   float* d_w;
   float* d_b;
   float* d_logits;
-  float* dl;               // workspace [T][E]
-  double* pb;              // workspace [blocks][E]
+  void* dl;                // workspace of score_dl_bytes
+  double* pb;              // workspace [E][score_grad_sum_blocks]
   float* pw;               // workspace [slices][E][d]
 };
 hipError_t launch_score_grad(const ScoreGradArgs& a, hipStream_t s);

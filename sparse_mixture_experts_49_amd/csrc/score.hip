@@ -6,6 +6,7 @@
 // problem: load balancing" (balance loss, z-loss, selection-only bias), with
 // sigmoid scores and group-limited selection added.
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.h"
 #include "score.h"
@@ -14,7 +15,16 @@ namespace moe {
 
 constexpr int kPartWaves = 4;       // waves of a logits block, 16 experts each
 
+// From 512 tokens the LDS-tiled kernel, below it the direct one.
+static bool score_tiled(const ScoreShape& s) { return s.T >= 512; }
+
 int score_parts(const ScoreShape& s) {
+  if (score_tiled(s)) {
+    // One part from 256 tiles' worth of half the chip; else enough to fill it, 128 of d
+    // or more in each.
+    const long tiles = (s.T + 63) / 64;
+    return tiles > 128 ? 1 : (int)std::max(1L, std::min(256 / tiles, s.d / 128L));
+  }
   // Enough waves to cover the chip twice (512 blocks), no part under 128 of d.
   const long blocks = (long)((s.T + 15) / 16) * ((s.E + 63) / 64);
   const long most = std::min(32L, s.d / 128L);
@@ -80,64 +90,44 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
-__device__ __forceinline__ uint32_t wave_max_u32(uint32_t v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = max(v, (uint32_t)__shfl_xor((int)v, o));
-  return v;
-}
-__device__ __forceinline__ float wave_max_f(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
-}
-__device__ __forceinline__ float wave_sum_f(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
-}
-
-// One wave per token; lane l holds experts l, l + 64, ... (PER of them).
-// TRAIN: also the partial sums over this block's tokens.
+// What a wave needs to finish tokens: lane l holds experts l, l + 64, ... (PER of them).
 template <int PER, bool TRAIN>
-__global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a, int parts) {
-  __shared__ float sel_lds[4][64 * PER];
-  __shared__ double sum_p[4][64 * PER];
-  __shared__ int sum_l[4][64 * PER];
-  __shared__ double sum_z[4];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int E = a.sh.E, T = a.sh.T, k = a.sh.k, G = a.groups;
-  const int gs = E / G;
-  int shift = 0;                                   // lanes per group: 2^shift
-  while ((G << (shift + 1)) <= 64) ++shift;
-  const int P = 1 << shift;
-  int gbit[PER];                                   // lane that knows whether j's group stays
+struct Finisher {
+  int shift, gs;                 // lanes per group 2^shift, experts per group
+  int gbit[PER];                 // lane that knows whether the group of expert j * 64 + l stays
   float bias[PER], bsel[PER];
-#pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    const int e = j * 64 + lane;
-    gbit[j] = e < E ? (e / gs) << shift : 0;
-    bias[j] = (a.b_router && e < E) ? a.b_router[e] : 0.f;
-    bsel[j] = (a.b_select && e < E) ? a.b_select[e] : 0.f;
-  }
-  double pq[PER], pz = 0.0;
+  double pq[PER], pz;            // TRAIN: this wave's sums over its tokens
   int pl[PER];
-#pragma unroll
-  for (int j = 0; j < PER; ++j) pq[j] = 0.0, pl[j] = 0;
 
-  for (int t = blockIdx.x * 4 + wave; t < T; t += gridDim.x * 4) {
-    float l[PER], s[PER];
+  __device__ __forceinline__ void init(const ScoreArgs& a) {
+    const int lane = __lane_id(), E = a.sh.E, G = a.groups;
+    gs = E / G;
+    shift = 0;
+    while ((G << (shift + 1)) <= 64) ++shift;
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const int e = j * 64 + lane;
-      l[j] = 0.f;
-      if (e < E)
-        for (int p = 0; p < parts; ++p) l[j] += a.part[((size_t)p * T + t) * E + e];
+      gbit[j] = e < E ? (e / gs) << shift : 0;
+      bias[j] = (a.b_router && e < E) ? a.b_router[e] : 0.f;
+      bsel[j] = (a.b_select && e < E) ? a.b_select[e] : 0.f;
+      pq[j] = 0.0;
+      pl[j] = 0;
+    }
+    pz = 0.0;
+  }
+
+  // One token from its raw logits l (no bias yet); sel: 64 * PER floats of LDS of this wave.
+  __device__ __forceinline__ void token(const ScoreArgs& a, int t, float (&l)[PER], float* sel) {
+    const int lane = __lane_id(), E = a.sh.E, k = a.sh.k, G = a.groups, P = 1 << shift;
+    float s[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int e = j * 64 + lane;
       l[j] = e < E ? l[j] + bias[j] : -INFINITY;
       if (a.logits && e < E) a.logits[(size_t)t * E + e] = l[j];
     }
     float m = l[0], tot = 0.f;
-    if (TRAIN || !a.sigmoid) {
+    if (a.z_loss || !a.sigmoid) {
 #pragma unroll
       for (int j = 1; j < PER; ++j) m = fmaxf(m, l[j]);
       m = wave_max_f(m);
@@ -157,19 +147,20 @@ __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a, int part
 #pragma unroll
       for (int j = 0; j < PER; ++j) s[j] = j * 64 + lane < E ? 1.f / (1.f + expf(-l[j])) : 0.f;
     } else {
+      const float r = 1.f / (tot > 0.f ? tot : 1.f);
 #pragma unroll
-      for (int j = 0; j < PER; ++j) s[j] /= tot > 0.f ? tot : 1.f;
+      for (int j = 0; j < PER; ++j) s[j] *= r;
     }
     if (TRAIN) {
-      float q = 1.f;
+      float r = 1.f;
       if (a.sigmoid) {
-        q = 0.f;
+        float q = 0.f;
 #pragma unroll
         for (int j = 0; j < PER; ++j) q += s[j];
-        q = fmaxf(wave_sum_f(q), 1e-20f);          // every score underflowed: q = 0
+        r = 1.f / fmaxf(wave_sum_f(q), 1e-20f);    // every score underflowed: q = 0
       }
 #pragma unroll
-      for (int j = 0; j < PER; ++j) pq[j] += (double)(s[j] / q);
+      for (int j = 0; j < PER; ++j) pq[j] += (double)(s[j] * r);
     }
 
     uint32_t key[PER];
@@ -177,7 +168,7 @@ __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a, int part
     for (int j = 0; j < PER; ++j) {
       const float v = s[j] + bsel[j];
       key[j] = j * 64 + lane < E ? order_key(v) : 0u;
-      if (G > 1) sel_lds[wave][j * 64 + lane] = v == v ? v : -INFINITY;
+      if (G > 1) sel[j * 64 + lane] = v == v ? v : -INFINITY;
     }
     if (G > 1) {
       // Lanes [g P, (g + 1) P) find the best two of group g.
@@ -187,7 +178,7 @@ __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a, int part
       const int g = lane >> shift;
       if (g < G)
         for (int i = lane & (P - 1); i < gs; i += P) {
-          const float v = sel_lds[wave][g * gs + i];
+          const float v = sel[g * gs + i];
           b1 = fmaxf(b1, fminf(b0, v));
           b0 = fmaxf(b0, v);
         }
@@ -200,7 +191,7 @@ __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a, int part
       const uint32_t gk = g < G ? order_key(a.group_top == 2 ? b0 + b1 : b0) : 0u;
       int rank = 0;
       for (int h = 0; h < G; ++h) {
-        const uint32_t hk = (uint32_t)__shfl((int)gk, h << shift);
+        const uint32_t hk = (uint32_t)__builtin_amdgcn_readlane((int)gk, h << shift);
         rank += hk > gk || (hk == gk && h < g);
       }
       const uint64_t stay = __ballot(g < G && rank < a.top_groups);
@@ -226,7 +217,7 @@ __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a, int part
           if (hit) {
             const int at = __ffsll((unsigned long long)hit) - 1;
             e = j * 64 + at;
-            r = __shfl(s[j], at);
+            r = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(s[j]), at));
             if (lane == at) {
               key[j] = 0u;
               if (TRAIN) ++pl[j];
@@ -242,89 +233,305 @@ __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a, int part
       a.topk_w[(size_t)t * k + lane] = a.renorm ? a.scale * (my_r / (total + 1e-20f)) : a.scale * my_r;
     }
   }
+};
 
-  if constexpr (TRAIN) {
+// LDS for the sums over a block's waves.
+template <int PER, int WAVES>
+struct FinishSums {
+  double p[WAVES][64 * PER], z[WAVES];
+  int l[WAVES][64 * PER];
+};
+
+// This block's column of the partial sums [E][blocks], waves added in order.
+template <int PER, int WAVES>
+__device__ __forceinline__ void store_sums(const ScoreArgs& a, const Finisher<PER, true>& f,
+                                           FinishSums<PER, WAVES>& sm, int wave) {
+  const int lane = __lane_id();
+  __syncthreads();
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      sum_p[wave][j * 64 + lane] = pq[j];
-      sum_l[wave][j * 64 + lane] = pl[j];
-    }
-    if (lane == 0) sum_z[wave] = pz;
-    __syncthreads();
-    for (int e = threadIdx.x; e < E; e += 256) {
-      a.psum[(size_t)blockIdx.x * E + e] = sum_p[0][e] + sum_p[1][e] + sum_p[2][e] + sum_p[3][e];
-      a.pload[(size_t)blockIdx.x * E + e] = sum_l[0][e] + sum_l[1][e] + sum_l[2][e] + sum_l[3][e];
-    }
-    if (threadIdx.x == 0) a.pz[blockIdx.x] = sum_z[0] + sum_z[1] + sum_z[2] + sum_z[3];
+  for (int j = 0; j < PER; ++j) {
+    sm.p[wave][j * 64 + lane] = f.pq[j];
+    sm.l[wave][j * 64 + lane] = f.pl[j];
+  }
+  if (lane == 0) sm.z[wave] = f.pz;
+  __syncthreads();
+  for (int e = threadIdx.x; e < a.sh.E; e += WAVES * 64) {
+    double p = sm.p[0][e];
+    int n = sm.l[0][e];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) p += sm.p[w][e], n += sm.l[w][e];
+    a.psum[(size_t)e * gridDim.x + blockIdx.x] = p;
+    a.pload[(size_t)e * gridDim.x + blockIdx.x] = n;
+  }
+  if (threadIdx.x == 0) {
+    double z = sm.z[0];
+#pragma unroll
+    for (int w = 1; w < WAVES; ++w) z += sm.z[w];
+    a.pz[blockIdx.x] = z;
   }
 }
 
-// The sums over blocks, in a fixed order, and what follows from them.  1024
-// threads: expert tid % 256, quarter tid / 256 of the blocks.
-__global__ __launch_bounds__(1024) void score_reduce_kernel(ScoreArgs a, int blocks) {
-  __shared__ double sp[4][kScoreMaxExperts];
-  __shared__ int sl[4][kScoreMaxExperts];
-  __shared__ double sx[kScoreMaxExperts], sz[kScoreMaxExperts];
-  const int e = threadIdx.x & 255, q = threadIdx.x >> 8, E = a.sh.E;
-  double p = 0.0;
-  int n = 0;
-  if (e < E)
-    for (int b = q; b < blocks; b += 4) {
-      p += a.psum[(size_t)b * E + e];
-      n += a.pload[(size_t)b * E + e];
+// Tokens whose logits are in `parts` parts in the workspace; one wave per token.
+template <int PER, bool TRAIN>
+__global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a, int parts) {
+  __shared__ float sel[4][64 * PER];
+  __shared__ FinishSums<PER, 4> sums;
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int E = a.sh.E, T = a.sh.T;
+  Finisher<PER, TRAIN> f;
+  f.init(a);
+  for (int t = blockIdx.x * 4 + wave; t < T; t += gridDim.x * 4) {
+    float l[PER];
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      const int e = j * 64 + lane;
+      l[j] = 0.f;
+      if (e < E)
+        for (int p = 0; p < parts; ++p) l[j] += a.part[((size_t)p * T + t) * E + e];
     }
-  sp[q][e] = p;
-  sl[q][e] = n;
-  if (q == 0) sz[e] = e < blocks ? a.pz[e] : 0.0;   // at most 256 blocks
-  __syncthreads();
-  if (q == 0) {
-    double v = 0.0;
-    if (e < E) {
-      const double mean = (sp[0][e] + sp[1][e] + sp[2][e] + sp[3][e]) / a.sh.T;
-      const int load = sl[0][e] + sl[1][e] + sl[2][e] + sl[3][e];
-      if (a.prob_mean) a.prob_mean[e] = (float)mean;
-      if (a.load) a.load[e] = load;
-      v = mean * load;
-    }
-    sx[e] = v;
+    f.token(a, t, l, sel[wave]);
   }
-  for (int o = 128; o > 0; o >>= 1) {
+  if constexpr (TRAIN) store_sums<PER, 4>(a, f, sums, wave);
+}
+
+// ---------------------------------------------------------------------------
+// Many tokens: 64 tokens x all experts (NE = 64, 128 or 256 columns) per block, both
+// operands through LDS in steps of 128 bytes of d, three stages, the loads two steps
+// ahead; rows of 128 B with 16 B chunks at chunk ^ ((row >> 1) & 7) (16 rows' reads of a
+// chunk touch every bank once).  W_r goes by the MFMA's first operand, so a lane holds
+// four neighbouring experts of a token.  bf16: MFMA 32x32x16; fp32: 32x32x2, lane half
+// h taking chunk 2s + h of a row for slice s (both operands agree on the k of a slot).
+//
+// One part (d not split): the tile's logits stay in LDS and the block finishes its own
+// tokens, so x is read once and the logits are written only if asked for; blocks are
+// persistent and carry the sums over their tokens in registers.  More parts (too few
+// tokens to fill the chip): partial logits to the workspace for score_finish_kernel.
+// ---------------------------------------------------------------------------
+constexpr int kRowsM = 64, kScoreStages = 3;
+
+template <typename T, int NE, bool FUSED, bool TRAIN>
+__global__ __launch_bounds__(256, 1) void score_tile_kernel(ScoreArgs a, int parts) {
+  constexpr int PER = NE / 64;
+  constexpr int kKs = 128 / sizeof(T);                 // d per step
+  constexpr int WN = NE == 256 ? 4 : 2, WM = 4 / WN;   // waves over experts, tokens
+  constexpr int MT = kRowsM / WM / 32, NT = NE / WN / 32;
+  constexpr int kA = kRowsM * 128, kStage = kA + NE * 128;
+  constexpr int kAI = kA / 4096, kWI = NE * 128 / 4096, L = kAI + kWI;
+  constexpr int kPitch = NE + 4;                       // floats per token's logits in LDS
+  constexpr int kLogits = kRowsM * kPitch * 4;
+  constexpr int kLds = kScoreStages * kStage > kLogits ? kScoreStages * kStage : kLogits;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
+  __shared__ float sel[FUSED ? 4 : 1][64 * PER];
+  __shared__ FinishSums<PER, FUSED && TRAIN ? 4 : 1> sums;
+
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave / WN, wn = wave % WN, fr = lane & 31, fc = lane >> 5;
+  const int E = a.sh.E, tokens = a.sh.T, d = a.sh.d;
+  const int part = FUSED ? 0 : blockIdx.y;
+  const int steps = d / kKs;
+  const int s0 = (int)((long)part * steps / parts), nk = (int)((long)(part + 1) * steps / parts) - s0;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+  const size_t pitch = (size_t)d * sizeof(T);
+  Finisher<PER, TRAIN> f;
+  if constexpr (FUSED) f.init(a);
+
+  // Loads: instruction i of wave w fills rows (4i + w) * 8 + lane / 8, chunk lane % 8.
+  const int lr = lane >> 3;
+  uint32_t w_off[kWI];
+#pragma unroll
+  for (int i = 0; i < kWI; ++i) {
+    const int row = (i * 4 + wave) * 8 + lr;
+    w_off[i] = (uint32_t)(min(row, E - 1) * pitch) + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
+  }
+  const uint32_t swz = (fr >> 1) & 7;
+  const int tiles = (tokens + kRowsM - 1) / kRowsM;
+
+  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
+    const int t0 = tile * kRowsM;
+    const uint8_t* x_base = static_cast<const uint8_t*>(a.x) + (size_t)t0 * pitch + (size_t)s0 * 128;
+    const uint8_t* w_base = static_cast<const uint8_t*>(a.w) + (size_t)s0 * 128;
+    uint32_t a_off[kAI];
+#pragma unroll
+    for (int i = 0; i < kAI; ++i) {
+      const int row = (i * 4 + wave) * 8 + lr;
+      a_off[i] = (uint32_t)(min(row, tokens - 1 - t0) * pitch) + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
+    }
+    auto load = [&](int i, int step, int stage) {      // steps past the last repeat it
+      const size_t k = (size_t)min(step, nk - 1) * 128;
+      const uint32_t base = lds0 + stage * kStage;
+      if (i < kAI) dma16(x_base + k, a_off[i < kAI ? i : 0], base + (i * 4 + wave) * 1024);
+      else dma16(w_base + k, w_off[i < kAI ? 0 : i - kAI], base + kA + ((i - kAI) * 4 + wave) * 1024);
+    };
+    f32x16 acc[NT][MT];
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[n][m][q] = 0.f;
+
+    __syncthreads();                                   // the last tile's logits are read
+#pragma unroll
+    for (int s = 0; s < kScoreStages - 1; ++s)
+#pragma unroll
+      for (int i = 0; i < L; ++i) load(i, s, s);
+    int st = 0;
+    for (int t = 0; t < nk; ++t) {
+      __builtin_amdgcn_s_waitcnt(wait_vm((kScoreStages - 2) * L));   // step t landed
+      __syncthreads();                                 // for all; step t - 1 is read
+      const int into = st == 0 ? kScoreStages - 1 : st - 1;
+#pragma unroll
+      for (int i = 0; i < L; ++i) load(i, t + kScoreStages - 1, into);
+      const uint8_t* base = lds + st * kStage;
+#pragma unroll
+      for (int s = 0; s < 4; ++s) {
+        u32x4 xa[MT], wb[NT];
+        const uint32_t c = ((2 * s + fc) ^ swz) << 4;
+#pragma unroll
+        for (int m = 0; m < MT; ++m) xa[m] = ld16(base + ((wm * MT * 32 + fr) * 128 + c) + m * 4096);
+#pragma unroll
+        for (int n = 0; n < NT; ++n) wb[n] = ld16(base + ((wn * NT * 32 + fr) * 128 + c) + kA + n * 4096);
+#pragma unroll
+        for (int n = 0; n < NT; ++n)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) {
+            if constexpr (sizeof(T) == 2) {
+              acc[n][m] = mfma32_bf16(wb[n], xa[m], acc[n][m]);
+            } else {
+#pragma unroll
+              for (int q = 0; q < 4; ++q)
+                acc[n][m] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(wb[n][q]), __uint_as_float(xa[m][q]),
+                                                                 acc[n][m], 0, 0, 0);
+            }
+          }
+      }
+      st = st == kScoreStages - 1 ? 0 : st + 1;
+    }
+    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");      // the repeated loads too
+    __syncthreads();                                   // LDS free
+
+    // Lane: token m * 32 + fr, experts n * 32 + 8 g + 4 fc .. + 3.
+    float* lg = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int n = 0; n < NT; ++n)
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int e = (wn * NT + n) * 32 + 8 * g + 4 * fc, r = (wm * MT + m) * 32 + fr;
+          *reinterpret_cast<f32x4*>(lg + r * kPitch + e) =
+              f32x4{acc[n][m][4 * g], acc[n][m][4 * g + 1], acc[n][m][4 * g + 2], acc[n][m][4 * g + 3]};
+        }
     __syncthreads();
-    if ((int)threadIdx.x < o) {
-      sx[threadIdx.x] += sx[threadIdx.x + o];
-      sz[threadIdx.x] += sz[threadIdx.x + o];
+    for (int i = 0; i < kRowsM / 4; ++i) {
+      const int r = i * 4 + wave, t = t0 + r;
+      if (t >= tokens) break;
+      float l[PER];
+#pragma unroll
+      for (int j = 0; j < PER; ++j) l[j] = lg[r * kPitch + j * 64 + lane];
+      if constexpr (FUSED) {
+        f.token(a, t, l, sel[wave]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+          if (j * 64 + lane < E) a.part[((size_t)part * tokens + t) * E + j * 64 + lane] = l[j];
+      }
     }
   }
-  if (threadIdx.x == 0) {
-    if (a.aux) *a.aux = (float)(sx[0] * E / ((double)a.sh.T * a.sh.k));
-    if (a.z_loss) *a.z_loss = (float)(sz[0] / a.sh.T);
+  if constexpr (FUSED && TRAIN) store_sums<PER, 4>(a, f, sums, wave);
+}
+
+// The sums over blocks (at most 256), in a fixed order, and what follows from them: one
+// block, a wave per expert at a time, its column of partial sums read at once.
+__global__ __launch_bounds__(1024) void score_reduce_kernel(ScoreArgs a, int blocks) {
+  __shared__ double share[kScoreMaxExperts];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, E = a.sh.E;
+  auto total = [&](double v) {
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
+    return v;
+  };
+#pragma unroll 4
+  for (int e = wave; e < E; e += 16) {
+    double p = 0.0;
+    int n = 0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int b = i * 64 + lane;
+      if (b < blocks) {
+        p += a.psum[(size_t)e * blocks + b];
+        n += a.pload[(size_t)e * blocks + b];
+      }
+    }
+    p = total(p) / a.sh.T;
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
+    if (lane == 0) {
+      if (a.prob_mean) a.prob_mean[e] = (float)p;
+      if (a.load) a.load[e] = n;
+      share[e] = p * n;
+    }
   }
+  __syncthreads();
+  if (wave == 0) {
+    double x = 0.0, z = 0.0;
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int j = i * 64 + lane;
+      if (j < E) x += share[j];
+      if (j < blocks) z += a.pz[j];
+    }
+    x = total(x);
+    z = total(z);
+    if (lane == 0) {
+      if (a.aux) *a.aux = (float)(x * E / ((double)a.sh.T * a.sh.k));
+      if (a.z_loss) *a.z_loss = (float)(z / a.sh.T);
+    }
+  }
+}
+
+template <typename T>
+static void launch_typed(const ScoreArgs& a, bool train, hipStream_t s) {
+  const ScoreShape& h = a.sh;
+  const int parts = score_parts(h);
+  int nb;                                              // blocks that hold partial sums
+  if (score_tiled(h)) {
+    const int tiles = (h.T + kRowsM - 1) / kRowsM;
+    nb = std::min(tiles, 256);
+    auto tile = [&](auto ne) {
+      constexpr int NE = decltype(ne)::value;
+      if (parts > 1) score_tile_kernel<T, NE, false, false><<<dim3(tiles, parts), 256, 0, s>>>(a, parts);
+      else if (train) score_tile_kernel<T, NE, true, true><<<nb, 256, 0, s>>>(a, 1);
+      else score_tile_kernel<T, NE, true, false><<<nb, 256, 0, s>>>(a, 1);
+    };
+    if (h.E <= 64) tile(std::integral_constant<int, 64>{});
+    else if (h.E <= 128) tile(std::integral_constant<int, 128>{});
+    else tile(std::integral_constant<int, 256>{});
+  } else {
+    const dim3 grid((h.T + 15) / 16, (h.E + 63) / 64, parts);
+    score_logits_kernel<T><<<grid, 256, 0, s>>>(static_cast<const T*>(a.x), static_cast<const T*>(a.w), h.T,
+                                               h.d, h.E, parts, a.part);
+  }
+  if (!score_tiled(h) || parts > 1) {
+    nb = score_finish_blocks(h.T);
+    auto finish = [&](auto per) {
+      constexpr int PER = decltype(per)::value;
+      if (train) score_finish_kernel<PER, true><<<nb, 256, 0, s>>>(a, parts);
+      else score_finish_kernel<PER, false><<<nb, 256, 0, s>>>(a, parts);
+    };
+    if (h.E <= 64) finish(std::integral_constant<int, 1>{});
+    else if (h.E <= 128) finish(std::integral_constant<int, 2>{});
+    else finish(std::integral_constant<int, 4>{});
+  }
+  if (train) score_reduce_kernel<<<1, 1024, 0, s>>>(a, nb);
 }
 
 hipError_t launch_score(const ScoreArgs& a, hipStream_t s) {
-  const ScoreShape& h = a.sh;
-  const int parts = score_parts(h), nb = score_finish_blocks(h.T);
-  const dim3 grid((h.T + 15) / 16, (h.E + 63) / 64, parts);
-  if (h.bf16)
-    score_logits_kernel<uint16_t><<<grid, 256, 0, s>>>(static_cast<const uint16_t*>(a.x),
-                                                      static_cast<const uint16_t*>(a.w), h.T, h.d,
-                                                      h.E, parts, a.part);
-  else
-    score_logits_kernel<float><<<grid, 256, 0, s>>>(static_cast<const float*>(a.x),
-                                                   static_cast<const float*>(a.w), h.T, h.d, h.E,
-                                                   parts, a.part);
   const bool train = a.load || a.prob_mean || a.aux || a.z_loss;
-  auto finish = [&](auto per) {
-    constexpr int PER = decltype(per)::value;
-    if (train)
-      score_finish_kernel<PER, true><<<nb, 256, 0, s>>>(a, parts);
-    else
-      score_finish_kernel<PER, false><<<nb, 256, 0, s>>>(a, parts);
-  };
-  if (h.E <= 64) finish(std::integral_constant<int, 1>{});
-  else if (h.E <= 128) finish(std::integral_constant<int, 2>{});
-  else finish(std::integral_constant<int, 4>{});
-  if (train) score_reduce_kernel<<<1, 1024, 0, s>>>(a, nb);
+  if (a.sh.bf16) launch_typed<uint16_t>(a, train, s);
+  else launch_typed<float>(a, train, s);
   return hipGetLastError();
 }
 

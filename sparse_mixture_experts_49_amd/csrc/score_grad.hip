@@ -7,29 +7,71 @@
 //   sigmoid: ds = dr + (dq - sum dq q) / sum s;  dl = ds s (1 - s)
 //   dl += d_z (2 / T) lse softmax(l)
 // and d_b = sum_t dl, d_x = dl W_r, d_W = dl^T x.
+//
+// bf16 layers: x and W_r go to the bf16 MFMA as they are and dl as a sum of bf16 terms,
+// dl = hi + mid (+ lo): two keep 17 bits, enough under d_x's rounding to bf16, three keep
+// all of fp32's for the fp32 d_W.  The terms are written once, by token for d_x and by
+// expert for d_W, so both products read them along their k.
 #include <algorithm>
+#include <type_traits>
 
 #include "device_common.h"
 #include "score.h"
 
 namespace moe {
 
+static int up_to(int v, int m) { return (v + m - 1) / m * m; }
+
+// Column blocks of the products: 256 columns of d each.
+constexpr int kGradCols = 256, kGradRows = 128, kGradK = 32;
+
 int score_grad_slices(const ScoreShape& s) {
-  // d_w_router tiles of 16 experts x 64 columns per wave; slices of at least 64
-  // tokens until 1024 waves run.
+  if (s.bf16) {
+    // Blocks of kGradRows experts x 256 columns; slices of at least 128 tokens until every
+    // CU has two.
+    const long tiles = (long)((s.E + kGradRows - 1) / kGradRows) * ((s.d + kGradCols - 1) / kGradCols);
+    return (int)std::max(1L, std::min({32L, (long)(s.T + 127) / 128, 512 / tiles}));
+  }
+  // fp32: tiles of 16 experts x 64 columns per wave; slices of at least 64 tokens until
+  // 2048 waves run.
   const long tiles = (long)((s.E + 15) / 16) * (s.d / 64);
   return (int)std::max(1L, std::min({16L, (long)(s.T + 63) / 64, 2048 / tiles}));
 }
 
-__device__ __forceinline__ float wsum(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
-  return v;
+// Tokens per tile of the logit-gradient kernel.
+static int grad_tile(int T) { return T >= 4096 ? 64 : 16; }
+static int grad_blocks(int T) {
+  const int tile = grad_tile(T);
+  return std::min(256, (T + tile - 1) / tile);
 }
 
-// One wave per token; lane l holds experts l, l + 64, ...
-template <int PER>
-__global__ __launch_bounds__(256) void score_dlogits_kernel(ScoreGradArgs a) {
+// Workspace of the logit gradients: fp32 [T][E], or bf16 terms [2][T'][E'] and [3][E''][T''].
+struct TermSpace {
+  size_t by_token, by_expert, total;   // elements of 2 bytes
+  int Ek, Tk;                          // row lengths: E and T rounded up to the k step
+};
+static TermSpace term_space(const ScoreShape& s) {
+  TermSpace t{};
+  t.Ek = up_to(s.E, kGradK);
+  t.Tk = up_to(s.T, 64);
+  t.by_token = (size_t)up_to(s.T, kGradRows) * t.Ek;
+  t.by_expert = (size_t)up_to(s.E, kGradRows) * t.Tk;
+  t.total = 2 * t.by_token + 3 * t.by_expert;
+  return t;
+}
+
+size_t score_dl_bytes(const ScoreShape& s) {
+  return s.bf16 ? term_space(s).total * 2 : (size_t)s.T * s.E * 4;
+}
+int score_grad_sum_blocks(int T) { return grad_blocks(T); }
+
+// dl of tiles of TT tokens: one wave per token, lane l the experts l, l + 64, ...; bf16
+// layers put the tile through LDS to write its terms along both axes.
+template <int PER, int TT, bool BF16>
+__global__ __launch_bounds__(256) void score_dlogits_kernel(ScoreGradArgs a, int Ek, int Tk, size_t by_token,
+                                                            size_t by_expert) {
+  constexpr int kPitch = 64 * PER + 1;
+  __shared__ float tile[BF16 ? TT * kPitch : 1];
   __shared__ double sum_b[4][64 * PER];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -40,88 +82,141 @@ __global__ __launch_bounds__(256) void score_dlogits_kernel(ScoreGradArgs a) {
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int e = j * 64 + lane;
-    dq[j] = (a.d_aux && e < E)
-                ? (float)((double)aux * E * a.load[e] / ((double)T * k) / T)
-                : 0.f;
+    dq[j] = (a.d_aux && e < E) ? (float)((double)aux * E * a.load[e] / ((double)T * k) / T) : 0.f;
     pb[j] = 0.0;
   }
-  for (int t = blockIdx.x * 4 + wave; t < T; t += gridDim.x * 4) {
-    float l[PER], p[PER], s[PER];
-    float m = -INFINITY;
+  for (int t0 = blockIdx.x * TT; t0 < T; t0 += gridDim.x * TT) {
+    for (int i = wave; i < TT; i += 4) {
+      const int t = t0 + i;
+      float dl[PER];
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int e = j * 64 + lane;
-      l[j] = e < E ? a.logits[(size_t)t * E + e] : -INFINITY;
-      m = fmaxf(m, l[j]);
-    }
+      for (int j = 0; j < PER; ++j) dl[j] = 0.f;
+      if (t < T) {
+        float l[PER], p[PER], s[PER];
+        float m = -INFINITY;
 #pragma unroll
-    for (int o = 32; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor(m, o));
-    if (m == -INFINITY) m = 0.f;
-    float tot = 0.f;
+        for (int j = 0; j < PER; ++j) {
+          const int e = j * 64 + lane;
+          l[j] = e < E ? a.logits[(size_t)t * E + e] : -INFINITY;
+          m = fmaxf(m, l[j]);
+        }
+        m = wave_max_f(m);
+        if (m == -INFINITY) m = 0.f;
+        float tot = 0.f;
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      p[j] = j * 64 + lane < E ? expf(l[j] - m) : 0.f;
-      tot += p[j];
-    }
-    tot = wsum(tot);
+        for (int j = 0; j < PER; ++j) {
+          p[j] = j * 64 + lane < E ? expf(l[j] - m) : 0.f;
+          tot += p[j];
+        }
+        tot = wave_sum_f(tot);
+        const float r_tot = 1.f / (tot > 0.f ? tot : 1.f);
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      p[j] /= tot > 0.f ? tot : 1.f;
-      s[j] = !a.sigmoid ? p[j] : j * 64 + lane < E ? 1.f / (1.f + expf(-l[j])) : 0.f;
-    }
-    // Chosen scores and the gradients of the raw weights.
-    int idx[8];
-    float g[8], S = 1e-20f, gw = 0.f;
+        for (int j = 0; j < PER; ++j) {
+          p[j] *= r_tot;
+          s[j] = !a.sigmoid ? p[j] : j * 64 + lane < E ? 1.f / (1.f + expf(-l[j])) : 0.f;
+        }
+        // Chosen scores and the gradients of the raw weights.
+        int idx[8];
+        float g[8], S = 1e-20f, gw = 0.f;
+        const int my_idx = lane < k ? a.topk_idx[(size_t)t * k + lane] : -1;
+        const float my_g = (lane < k && a.d_topk_w) ? a.d_topk_w[(size_t)t * k + lane] : 0.f;
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      idx[i] = i < k ? a.topk_idx[(size_t)t * k + i] : -1;
-      if (idx[i] >= E) idx[i] = -1;
-      g[i] = (idx[i] >= 0 && a.d_topk_w) ? a.d_topk_w[(size_t)t * k + i] : 0.f;
-      float r = 0.f;
+        for (int q = 0; q < 8; ++q) {
+          idx[q] = __builtin_amdgcn_readlane(my_idx, q);
+          if (idx[q] >= E || idx[q] < 0) idx[q] = -1;
+          g[q] = idx[q] >= 0 ? __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(my_g), q)) : 0.f;
+          float r = 0.f;
 #pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        const float v = __shfl(s[j], idx[i] & 63);
-        if (idx[i] >= 0 && (idx[i] >> 6) == j) r = v;
+          for (int j = 0; j < PER; ++j) {
+            const float v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(s[j]), idx[q] & 63));
+            if (idx[q] >= 0 && (idx[q] >> 6) == j) r = v;
+          }
+          S += r;
+          gw = fmaf(g[q], r, gw);
+        }
+        float ds[PER];
+        float cs = 0.f, cq = 0.f, ss = 0.f;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+          float dr = 0.f;
+#pragma unroll
+          for (int q = 0; q < 8; ++q)
+            if (idx[q] == j * 64 + lane) dr += a.renorm ? a.scale * (g[q] - gw / S) / S : a.scale * g[q];
+          ds[j] = dr;
+          ss += s[j];
+          cq = fmaf(dq[j], s[j], cq);
+        }
+        if (a.sigmoid && a.d_aux) {
+          ss = fmaxf(wave_sum_f(ss), 1e-20f);
+          cq = wave_sum_f(cq);
+#pragma unroll
+          for (int j = 0; j < PER; ++j) ds[j] += (dq[j] - cq / ss) / ss;
+        } else if (!a.sigmoid) {
+#pragma unroll
+          for (int j = 0; j < PER; ++j) {
+            ds[j] += dq[j];
+            cs = fmaf(ds[j], s[j], cs);
+          }
+          cs = wave_sum_f(cs);
+        }
+        const float zl = a.d_z ? z * 2.f / T * (m + logf(tot)) : 0.f;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+          const int e = j * 64 + lane;
+          const float v = a.sigmoid ? ds[j] * s[j] * (1.f - s[j]) : s[j] * (ds[j] - cs);
+          if (e < E) {
+            dl[j] = a.d_z ? fmaf(zl, p[j], v) : v;
+            if (a.d_logits) a.d_logits[(size_t)t * E + e] = dl[j];
+            if (!BF16) static_cast<float*>(a.dl)[(size_t)t * E + e] = dl[j];
+            pb[j] += (double)dl[j];
+          }
+        }
       }
-      S += r;
-      gw = fmaf(g[i], r, gw);
+      if constexpr (BF16)
+#pragma unroll
+        for (int j = 0; j < PER; ++j) tile[i * kPitch + j * 64 + lane] = dl[j];
     }
-    float ds[PER];
-    float cs = 0.f, cq = 0.f, ss = 0.f;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      float dr = 0.f;
-#pragma unroll
-      for (int i = 0; i < 8; ++i)
-        if (idx[i] == j * 64 + lane) dr += a.renorm ? a.scale * (g[i] - gw / S) / S : a.scale * g[i];
-      ds[j] = dr;
-      ss += s[j];
-      cq = fmaf(dq[j], s[j], cq);
-    }
-    if (a.sigmoid && a.d_aux) {
-      ss = fmaxf(wsum(ss), 1e-20f);
-      cq = wsum(cq);
-#pragma unroll
-      for (int j = 0; j < PER; ++j) ds[j] += (dq[j] - cq / ss) / ss;
-    } else if (!a.sigmoid) {
-#pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        ds[j] += dq[j];
-        cs = fmaf(ds[j], s[j], cs);
+    if constexpr (BF16) {
+      // Two neighbouring values at a time: hi, mid (and lo) terms, packed.
+      auto terms = [](float u, float v, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
+        hi = pack_bf16x2(u, v);
+        u -= __uint_as_float(hi << 16);
+        v -= __uint_as_float(hi & 0xffff0000u);
+        mid = pack_bf16x2(u, v);
+        u -= __uint_as_float(mid << 16);
+        v -= __uint_as_float(mid & 0xffff0000u);
+        lo = pack_bf16x2(u, v);
+      };
+      uint32_t* out = static_cast<uint32_t*>(a.dl);
+      __syncthreads();
+      if (a.d_x) {
+        const int half = Ek / 2;
+        for (int i = threadIdx.x; i < TT * half; i += 256) {
+          const int r = i / half, c = i - r * half;
+          uint32_t hi, mid, lo;
+          terms(tile[r * kPitch + 2 * c], tile[r * kPitch + 2 * c + 1], hi, mid, lo);
+          const size_t at = ((size_t)(t0 + r) * Ek) / 2 + c;
+          if (t0 + r < T) out[at] = hi, out[by_token / 2 + at] = mid;
+        }
       }
-      cs = wsum(cs);
-    }
-    const float zl = a.d_z ? z * 2.f / T * (m + logf(tot)) : 0.f;
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int e = j * 64 + lane;
-      float v = a.sigmoid ? ds[j] * s[j] * (1.f - s[j]) : s[j] * (ds[j] - cs);
-      v = fmaf(zl, p[j], v);
-      if (e < E) {
-        a.dl[(size_t)t * E + e] = v;
-        if (a.d_logits) a.d_logits[(size_t)t * E + e] = v;
-        pb[j] += (double)v;
+      if (a.d_w) {
+        uint32_t* tw = out + by_token;                 // after the two by-token terms
+        for (int i = threadIdx.x; i < E * (TT / 2); i += 256) {
+          const int e = i / (TT / 2), c = i % (TT / 2);
+          uint32_t hi, mid, lo;
+          terms(tile[(2 * c) * kPitch + e], tile[(2 * c + 1) * kPitch + e], hi, mid, lo);
+          const size_t at = ((size_t)e * Tk + t0) / 2 + c;
+          tw[at] = hi, tw[by_expert / 2 + at] = mid, tw[by_expert + at] = lo;
+        }
+        // The last tile also clears its rows' tail up to Tk (a k step past T).
+        if (t0 + TT >= T)
+          for (int i = threadIdx.x; i < E * ((Tk - t0 - TT) / 2); i += 256) {
+            const int n = (Tk - t0 - TT) / 2, e = i / n, c = i - e * n;
+            const size_t at = ((size_t)e * Tk + t0 + TT) / 2 + c;
+            tw[at] = 0u, tw[by_expert / 2 + at] = 0u, tw[by_expert + at] = 0u;
+          }
       }
+      __syncthreads();
     }
   }
   if (a.d_b) {
@@ -129,30 +224,170 @@ __global__ __launch_bounds__(256) void score_dlogits_kernel(ScoreGradArgs a) {
     for (int j = 0; j < PER; ++j) sum_b[wave][j * 64 + lane] = pb[j];
     __syncthreads();
     for (int e = threadIdx.x; e < E; e += 256)
-      a.pb[(size_t)blockIdx.x * E + e] = sum_b[0][e] + sum_b[1][e] + sum_b[2][e] + sum_b[3][e];
+      a.pb[(size_t)e * gridDim.x + blockIdx.x] = sum_b[0][e] + sum_b[1][e] + sum_b[2][e] + sum_b[3][e];
   }
 }
 
-__global__ __launch_bounds__(1024) void score_db_kernel(const double* __restrict__ pb, int blocks,
-                                                        int E, float* __restrict__ d_b) {
-  __shared__ double s[4][kScoreMaxExperts];
-  const int e = threadIdx.x & 255, q = threadIdx.x >> 8;
+// d_b: a wave per expert, its column of block sums (at most 256) read at once.
+__global__ __launch_bounds__(256) void score_db_kernel(const double* __restrict__ pb, int blocks,
+                                                       int E, float* __restrict__ d_b) {
+  const int lane = threadIdx.x & 63, e = blockIdx.x * 4 + (threadIdx.x >> 6);
+  if (e >= E) return;
   double p = 0.0;
-  if (e < E)
-    for (int b = q; b < blocks; b += 4) p += pb[(size_t)b * E + e];
-  s[q][e] = p;
-  __syncthreads();
-  if (q == 0 && e < E) d_b[e] = (float)(s[0][e] + s[1][e] + s[2][e] + s[3][e]);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int b = i * 64 + lane;
+    if (b < blocks) p += pb[(size_t)e * blocks + b];
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) p += __shfl_xor(p, o);
+  if (lane == 0) d_b[e] = (float)p;
 }
 
-template <typename T>
-__device__ __forceinline__ float as_f32(T v) { return Elem<T>::to_f32(v); }
+// ---------------------------------------------------------------------------
+// out[m][n] = sum_k A[m][k] B[k][n], A in PLANES bf16 terms along k, B bf16 with its rows
+// along n (d_x: A = dl by token, B = W_r; d_W: A = dl by expert, B = x, one slice of the
+// tokens per blockIdx.z).  Block 32 MT x 2 rows x 256 columns, 4 waves as 2 x 2, k in steps
+// of 32 through three LDS stages.
+//
+// The MFMA wants 8 values along k per lane from both operands.  A has them in a row; of B a
+// lane reads the pair of neighbouring columns 2l, 2l + 1 from 8 rows (4 bytes each, a row's
+// 32 pairs are 128 contiguous bytes) and splits the words into two fragments, even and odd
+// columns.  As the first operand they make a lane's accumulators, even and odd together, 8
+// neighbouring columns of one row: stores of 16 bytes (bf16) or 32 (fp32).
+//
+// LDS: A rows of 64 B, 16 B chunks at chunk ^ ((row >> 2) & 3); B rows of 512 B, their 128 B
+// quarters at quarter ^ ((row >> 3) & 1) so that the two lane halves (rows 8 apart) read
+// different banks.
+// ---------------------------------------------------------------------------
+template <int PLANES, int MT, bool OUT_BF16>
+__global__ __launch_bounds__(256, 1) void score_grad_gemm_kernel(
+    const uint16_t* __restrict__ A, size_t plane, int a_pitch, const uint16_t* __restrict__ B, int b_rows,
+    int d, int M, int K, int slices, void* __restrict__ out) {
+  constexpr int S = 3, kRows = 64 * MT;
+  constexpr int kA = kRows * 64, kStage = PLANES * kA + kGradK * 512;
+  constexpr int kAI = PLANES * kA / 4096, kBI = kGradK * 512 / 4096, L = kAI + kBI;
+  static_assert(kA % 4096 == 0 && S * kStage <= 160 * 1024, "load plan");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S * kStage];
+  const int lane = threadIdx.x & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1, fr = lane & 31, fc = lane >> 5;
+  const int m0 = blockIdx.y * kRows, n0 = blockIdx.x * kGradCols, sl = blockIdx.z;
+  const int steps = (K + kGradK - 1) / kGradK;
+  const int s0 = (int)((long)sl * steps / slices), nk = (int)((long)(sl + 1) * steps / slices) - s0;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
 
-// d_x tile of 16 tokens x 64 columns per wave: k-slot q of MFMA i is expert e0 + 4 i + q.
-template <typename T>
+  const uint16_t* a_base[PLANES];
+#pragma unroll
+  for (int q = 0; q < PLANES; ++q) a_base[q] = A + q * plane + (size_t)m0 * a_pitch + (size_t)s0 * kGradK;
+  // A: load i of wave w fills rows (4 i + w) * 16 + lane / 4 of the planes laid end to end.
+  uint32_t a_off[kA / 4096];
+#pragma unroll
+  for (int i = 0; i < kA / 4096; ++i) {
+    const int row = (i * 4 + wave) * 16 + (lane >> 2);
+    a_off[i] = (uint32_t)row * (uint32_t)a_pitch * 2u + (((lane & 3) ^ ((row >> 2) & 3)) << 4);
+  }
+  // B: load i of wave w fills rows 2 (4 i + w) + lane / 32; columns past d wrap to the tile's
+  // first half (not stored).
+  const uint8_t* b_tile = reinterpret_cast<const uint8_t*>(B + (size_t)s0 * kGradK * d + n0);
+  auto load = [&](int i, int step, int stage) {
+    const uint32_t base = lds0 + stage * kStage;
+    const int s = min(step, nk - 1);
+    if (i < kAI) {
+      const int q = i / (kA / 4096), j = i % (kA / 4096);
+      dma16(a_base[q] + s * kGradK, a_off[j], base + q * kA + (j * 4 + wave) * 1024);
+    } else {
+      const int j = i - kAI, r = 2 * (j * 4 + wave) + (lane >> 5);
+      int c = (lane & 31) ^ (((r >> 3) & 1) << 3);
+      if (n0 + c * 8 >= d) c -= 16;
+      const int row = min(r, b_rows - 1 - (s0 + s) * kGradK);
+      dma16(b_tile + (size_t)s * kGradK * d * 2, (uint32_t)(row * d + c * 8) * 2u, base + PLANES * kA + (j * 4 + wave) * 1024);
+    }
+  };
+
+  f32x16 acc[4][MT];                                   // [column group: 2 * (64 columns) + odd][m]
+#pragma unroll
+  for (int n = 0; n < 4; ++n)
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[n][m][q] = 0.f;
+#pragma unroll
+  for (int s = 0; s < S - 1; ++s)
+#pragma unroll
+    for (int i = 0; i < L; ++i) load(i, s, s);
+  int st = 0;
+  const uint32_t swz = (fr >> 2) & 3;
+  for (int t = 0; t < nk; ++t) {
+    __builtin_amdgcn_s_waitcnt(wait_vm((S - 2) * L));
+    __syncthreads();
+    const int into = st == 0 ? S - 1 : st - 1;
+#pragma unroll
+    for (int i = 0; i < L; ++i) load(i, t + S - 1, into);
+    const uint8_t* base = lds + st * kStage;
+#pragma unroll
+    for (int s = 0; s < kGradK / 16; ++s) {
+      u32x4 xa[PLANES][MT], b[4];
+#pragma unroll
+      for (int q = 0; q < PLANES; ++q)
+#pragma unroll
+        for (int m = 0; m < MT; ++m)
+          xa[q][m] = ld16(base + ((wm * MT * 32 + fr) * 64 + (((2 * s + fc) ^ swz) << 4)) + q * kA + m * 2048);
+#pragma unroll
+      for (int n = 0; n < 2; ++n) {
+        uint32_t w[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          const int quarter = (wn * 2 + n) ^ ((2 * s + fc) & 1);       // row 16 s + 8 fc + j
+          w[j] = *reinterpret_cast<const uint32_t*>(base + PLANES * kA + (16 * s + 8 * fc + j) * 512 + quarter * 128 + fr * 4);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          b[2 * n][j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], 0x05040100);
+          b[2 * n + 1][j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], 0x07060302);
+        }
+      }
+#pragma unroll
+      for (int q = PLANES - 1; q >= 0; --q)            // small terms first
+#pragma unroll
+        for (int n = 0; n < 4; ++n)
+#pragma unroll
+          for (int m = 0; m < MT; ++m) acc[n][m] = mfma32_bf16(b[n], xa[q][m], acc[n][m]);
+    }
+    st = st == S - 1 ? 0 : st + 1;
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");     // no load outlives its LDS
+  // Lane: row m * 32 + fr; accumulator 4 g + q of group 2 n (+ 1) is column
+  // n * 64 + 2 (8 g + 4 fc + q) (+ 1).
+#pragma unroll
+  for (int m = 0; m < MT; ++m) {
+    const int r = m0 + (wm * MT + m) * 32 + fr;
+    if (r >= M) continue;
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int col = n0 + wn * 128 + n * 64 + 16 * g + 8 * fc;
+        if (col >= d) continue;
+        const f32x16 &u = acc[2 * n][m], &v = acc[2 * n + 1][m];
+        if constexpr (OUT_BF16) {
+          u32x4 h;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) h[q] = pack_bf16x2(u[4 * g + q], v[4 * g + q]);
+          st16(static_cast<uint16_t*>(out) + (size_t)r * d + col, h);
+        } else {
+          float* o = static_cast<float*>(out) + ((size_t)sl * M + r) * d + col;
+          *reinterpret_cast<f32x4*>(o) = f32x4{u[4 * g], v[4 * g], u[4 * g + 1], v[4 * g + 1]};
+          *reinterpret_cast<f32x4*>(o + 4) = f32x4{u[4 * g + 2], v[4 * g + 2], u[4 * g + 3], v[4 * g + 3]};
+        }
+      }
+  }
+}
+
+// fp32 layers: d_x tile of 16 tokens x 64 columns per wave: k-slot q of MFMA i is expert e0 + 4 i + q.
 __global__ __launch_bounds__(256) void score_dx_kernel(const float* __restrict__ dl,
-                                                       const T* __restrict__ w, int tokens, int d,
-                                                       int E, T* __restrict__ d_x) {
+                                                       const float* __restrict__ w, int tokens, int d,
+                                                       int E, float* __restrict__ d_x) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, fr = lane & 15, fc = lane >> 4;
   const int t0 = blockIdx.x * 16, c0 = (blockIdx.y * 4 + wave) * 64;
   if (c0 >= d) return;
@@ -163,7 +398,7 @@ __global__ __launch_bounds__(256) void score_dx_kernel(const float* __restrict__
     const float a = e < E ? dl[(size_t)t * E + e] : 0.f;
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-      const float b = e < E ? as_f32<T>(w[(size_t)e * d + c0 + n * 16 + fr]) : 0.f;
+      const float b = e < E ? w[(size_t)e * d + c0 + n * 16 + fr] : 0.f;
       acc[n] = mfma_f32(a, b, acc[n]);
     }
   }
@@ -173,16 +408,13 @@ __global__ __launch_bounds__(256) void score_dx_kernel(const float* __restrict__
     for (int i = 0; i < 4; ++i) {
       const int row = t0 + 4 * fc + i;
       if (row >= tokens) continue;
-      T* out = d_x + (size_t)row * d + c0 + n * 16 + fr;
-      if constexpr (sizeof(T) == 2) *out = f32_to_bf16(acc[n][i]);
-      else *out = acc[n][i];
+      d_x[(size_t)row * d + c0 + n * 16 + fr] = acc[n][i];
     }
 }
 
 // d_w_router tile of 16 experts x 64 columns per wave over one slice of the tokens.
-template <typename T>
 __global__ __launch_bounds__(256) void score_dw_kernel(const float* __restrict__ dl,
-                                                       const T* __restrict__ x, int tokens, int d,
+                                                       const float* __restrict__ x, int tokens, int d,
                                                        int E, int slices, float* __restrict__ out) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, fr = lane & 15, fc = lane >> 4;
   const int e0 = blockIdx.x * 16, c0 = (blockIdx.y * 4 + wave) * 64, sl = blockIdx.z;
@@ -195,7 +427,7 @@ __global__ __launch_bounds__(256) void score_dw_kernel(const float* __restrict__
     const float a = t < tb ? dl[(size_t)t * E + e] : 0.f;
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
-      const float b = t < tb ? as_f32<T>(x[(size_t)t * d + c0 + n * 16 + fr]) : 0.f;
+      const float b = t < tb ? x[(size_t)t * d + c0 + n * 16 + fr] : 0.f;
       acc[n] = mfma_f32(a, b, acc[n]);
     }
   }
@@ -217,32 +449,71 @@ __global__ __launch_bounds__(256) void score_dw_sum_kernel(const float* __restri
   *reinterpret_cast<f32x4*>(d_w + i) = v;
 }
 
-template <typename T>
-static void launch_products(const ScoreGradArgs& a, hipStream_t s) {
+static void sum_slices(const ScoreGradArgs& a, int slices, hipStream_t s) {
+  const size_t n = (size_t)a.sh.E * a.sh.d;
+  score_dw_sum_kernel<<<(unsigned)((n / 4 + 255) / 256), 256, 0, s>>>(a.pw, n, slices, a.d_w);
+}
+
+static void products_f32(const ScoreGradArgs& a, hipStream_t s) {
   const ScoreShape& h = a.sh;
+  const float* dl = static_cast<const float*>(a.dl);
   if (a.d_x)
-    score_dx_kernel<T><<<dim3((h.T + 15) / 16, (h.d + 255) / 256), 256, 0, s>>>(
-        a.dl, static_cast<const T*>(a.w), h.T, h.d, h.E, static_cast<T*>(a.d_x));
+    score_dx_kernel<<<dim3((h.T + 15) / 16, (h.d + 255) / 256), 256, 0, s>>>(
+        dl, static_cast<const float*>(a.w), h.T, h.d, h.E, static_cast<float*>(a.d_x));
   if (a.d_w) {
     const int slices = score_grad_slices(h);
-    score_dw_kernel<T><<<dim3((h.E + 15) / 16, (h.d + 255) / 256, slices), 256, 0, s>>>(
-        a.dl, static_cast<const T*>(a.x), h.T, h.d, h.E, slices, slices > 1 ? a.pw : a.d_w);
-    if (slices > 1) {
-      const size_t n = (size_t)h.E * h.d;
-      score_dw_sum_kernel<<<(unsigned)((n / 4 + 255) / 256), 256, 0, s>>>(a.pw, n, slices, a.d_w);
-    }
+    score_dw_kernel<<<dim3((h.E + 15) / 16, (h.d + 255) / 256, slices), 256, 0, s>>>(
+        dl, static_cast<const float*>(a.x), h.T, h.d, h.E, slices, slices > 1 ? a.pw : a.d_w);
+    if (slices > 1) sum_slices(a, slices, s);
   }
+}
+
+static void products_bf16(const ScoreGradArgs& a, hipStream_t s) {
+  const ScoreShape& h = a.sh;
+  const TermSpace t = term_space(h);
+  const uint16_t* dl = static_cast<const uint16_t*>(a.dl);
+  const int cols = (h.d + kGradCols - 1) / kGradCols;
+  if (a.d_x)
+    score_grad_gemm_kernel<2, 2, true><<<dim3(cols, (h.T + 127) / 128, 1), 256, 0, s>>>(
+        dl, t.by_token, t.Ek, static_cast<const uint16_t*>(a.w), h.E, h.d, h.T, h.E, 1, a.d_x);
+  if (a.d_w) {
+    const int slices = score_grad_slices(h);
+    float* out = slices > 1 ? a.pw : a.d_w;
+    const uint16_t* by_expert = dl + 2 * t.by_token;
+    const uint16_t* x = static_cast<const uint16_t*>(a.x);
+    if (h.E <= 64)
+      score_grad_gemm_kernel<3, 1, false><<<dim3(cols, 1, slices), 256, 0, s>>>(
+          by_expert, t.by_expert, t.Tk, x, h.T, h.d, h.E, h.T, slices, out);
+    else
+      score_grad_gemm_kernel<3, 2, false><<<dim3(cols, (h.E + 127) / 128, slices), 256, 0, s>>>(
+          by_expert, t.by_expert, t.Tk, x, h.T, h.d, h.E, h.T, slices, out);
+    if (slices > 1) sum_slices(a, slices, s);
+  }
+}
+
+template <int PER>
+static void launch_dlogits(const ScoreGradArgs& a, int blocks, hipStream_t s) {
+  const TermSpace t = term_space(a.sh);
+  const bool big = grad_tile(a.sh.T) == 64;
+  if (a.sh.bf16 && big)
+    score_dlogits_kernel<PER, 64, true><<<blocks, 256, 0, s>>>(a, t.Ek, t.Tk, t.by_token, t.by_expert);
+  else if (a.sh.bf16)
+    score_dlogits_kernel<PER, 16, true><<<blocks, 256, 0, s>>>(a, t.Ek, t.Tk, t.by_token, t.by_expert);
+  else if (big)
+    score_dlogits_kernel<PER, 64, false><<<blocks, 256, 0, s>>>(a, 0, 0, 0, 0);
+  else
+    score_dlogits_kernel<PER, 16, false><<<blocks, 256, 0, s>>>(a, 0, 0, 0, 0);
 }
 
 hipError_t launch_score_grad(const ScoreGradArgs& a, hipStream_t s) {
   const ScoreShape& h = a.sh;
-  const int nb = score_finish_blocks(h.T);
-  if (h.E <= 64) score_dlogits_kernel<1><<<nb, 256, 0, s>>>(a);
-  else if (h.E <= 128) score_dlogits_kernel<2><<<nb, 256, 0, s>>>(a);
-  else score_dlogits_kernel<4><<<nb, 256, 0, s>>>(a);
-  if (a.d_b) score_db_kernel<<<1, 1024, 0, s>>>(a.pb, nb, h.E, a.d_b);
-  if (h.bf16) launch_products<uint16_t>(a, s);
-  else launch_products<float>(a, s);
+  const int nb = grad_blocks(h.T);
+  if (h.E <= 64) launch_dlogits<1>(a, nb, s);
+  else if (h.E <= 128) launch_dlogits<2>(a, nb, s);
+  else launch_dlogits<4>(a, nb, s);
+  if (a.d_b) score_db_kernel<<<(h.E + 3) / 4, 256, 0, s>>>(a.pb, nb, h.E, a.d_b);
+  if (h.bf16) products_bf16(a, s);
+  else products_f32(a, s);
   return hipGetLastError();
 }
 
