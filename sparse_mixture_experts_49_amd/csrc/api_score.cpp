@@ -52,7 +52,7 @@ moe::ScoreShape shape_of(const moe_score_desc* d) {
 
 // The forward and the backward use the same bytes, one call at a time.
 struct ScoreLayout {
-  size_t part, psum, pload, pz;   // forward
+  size_t part, psum, pload, pz, share, done;   // forward
   size_t dl, pb, pw;              // backward
   size_t total;
 };
@@ -68,6 +68,8 @@ ScoreLayout layout_of(const moe_score_desc* d) {
   L.psum = take(sums * E * 8);
   L.pload = take(sums * E * 4);
   L.pz = take(sums * 8);
+  L.share = take(E * 8);
+  L.done = take(4);
   L.total = p;
   p = 0;
   L.dl = take(moe::score_dl_bytes(s));
@@ -158,6 +160,8 @@ int moe_score_route(const moe_score_desc* desc, const void* x, const void* w_rou
   a.psum = at<double>(ws, L.psum);
   a.pload = at<int32_t>(ws, L.pload);
   a.pz = at<double>(ws, L.pz);
+  a.share = at<double>(ws, L.share);
+  a.done = at<uint32_t>(ws, L.done);
   return hip_status(moe::launch_score(a, static_cast<hipStream_t>(stream)), "scored router launch");
 }
 

@@ -161,6 +161,18 @@ __device__ __forceinline__ float wave_sum_f(float v) {
   }));
 }
 
+// e^x within ~2 ulp for every x: 2^(x log2 e) with the rounding error of the product put
+// back to first order (not for |x| >= 88, where the result leaves fp32's normal range;
+// infinities and NaN come out as they should).
+__device__ __forceinline__ float exp_f32(float x) {
+  constexpr float kL = 1.44269504088896340736f, kLo = 1.92596299112661746887e-8f, kLn2 = 0.69314718055994530942f;
+  const float t = x * kL;
+  const float e = fmaf(x, kLo, fmaf(x, kL, -t));
+  const float r = __builtin_amdgcn_exp2f(t);
+  return fabsf(x) < 88.f ? fmaf(r, e * kLn2, r) : r;
+}
+__device__ __forceinline__ float sigmoid_f32(float x) { return __builtin_amdgcn_rcpf(1.f + exp_f32(-x)); }
+
 __device__ __forceinline__ int lane_id() { return __lane_id(); }
 
 }  // namespace moe

@@ -16,8 +16,6 @@ struct ScoreShape {
 
 // Parts the d-long dot products are cut into (partial logits [parts][T][E]).
 int score_parts(const ScoreShape& s);
-// Blocks of the finishing kernel (at most 256), each with a column of the partial sums.
-int score_finish_blocks(int T);
 
 struct ScoreArgs {
   ScoreShape sh;
@@ -40,6 +38,8 @@ struct ScoreArgs {
   double* psum;            // workspace [E][blocks], blocks <= 256
   int32_t* pload;          // workspace [E][blocks]
   double* pz;              // workspace [blocks]
+  double* share;           // workspace [E]
+  uint32_t* done;          // workspace [1]
 };
 hipError_t launch_score(const ScoreArgs& a, hipStream_t s);
 

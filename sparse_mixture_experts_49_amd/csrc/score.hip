@@ -20,7 +20,7 @@ static bool score_tiled(const ScoreShape& s) { return s.T >= 512; }
 
 int score_parts(const ScoreShape& s) {
   if (score_tiled(s)) {
-    // One part from 256 tiles' worth of half the chip; else enough to fill it, 128 of d
+    // One part where the tiles fill more than half the chip; else enough to fill it, 128 of d
     // or more in each.
     const long tiles = (s.T + 63) / 64;
     return tiles > 128 ? 1 : (int)std::max(1L, std::min(256 / tiles, s.d / 128L));
@@ -31,19 +31,18 @@ int score_parts(const ScoreShape& s) {
   return (int)std::max(1L, std::min(most, 512 / blocks));
 }
 
-// Few tokens per block keep every CU busy; many blocks would cost the reduction.
-int score_finish_blocks(int T) { return std::max(1, std::min(256, (T + 3) / 4)); }
-
 // Partial logits: wave w of block (t-tile, e-tile, part) multiplies 16 tokens by
 // 16 experts over its part of d, operands straight from memory to registers.
 template <typename T>
 __global__ __launch_bounds__(256) void score_logits_kernel(const T* __restrict__ x,
                                                            const T* __restrict__ w, int tokens,
                                                            int d, int E, int parts,
-                                                           float* __restrict__ part) {
+                                                           float* __restrict__ part,
+                                                           uint32_t* __restrict__ done) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int fr = lane & 15, fc = lane >> 4;
   const int t0 = blockIdx.x * 16, e0 = blockIdx.y * 64 + wave * 16, p = blockIdx.z;
+  if (t0 == 0 && e0 == 0 && p == 0 && lane == 0) *done = 0u;   // score_reduce_kernel's counter
   if (e0 >= E) return;
   const int chunks = d / 128;
   const int c0 = (int)((long)p * chunks / parts), c1 = (int)((long)(p + 1) * chunks / parts);
@@ -90,12 +89,28 @@ __device__ __forceinline__ uint32_t order_key(float v) {
   return (b & 0x80000000u) ? ~b : (b | 0x80000000u);
 }
 
+// One value per lane's pair step of a reduction over 2^shift neighbouring lanes, o = 1, 2, 4,
+// ...: permutations of quads, eights and rows of 16 (equal within the smaller groups by
+// then, so a mirror pairs as an exchange would), beyond that a shuffle.
+template <int STEP>
+__device__ __forceinline__ float pair_of(float v) {
+  const int i = (int)__float_as_uint(v);
+  if constexpr (STEP == 0) return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, i, 0xB1, 0xF, 0xF, false));
+  if constexpr (STEP == 1) return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, i, 0x4E, 0xF, 0xF, false));
+  if constexpr (STEP == 2) return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, i, 0x141, 0xF, 0xF, false));
+  if constexpr (STEP == 3) return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, i, 0x140, 0xF, 0xF, false));
+  return __shfl_xor(v, 1 << STEP);
+}
+
 // What a wave needs to finish tokens: lane l holds experts l, l + 64, ... (PER of them).
+// Straight-line code: lanes past E carry logit -inf and key 0 (one token per wave is bound by
+// instruction issue and latency, branches cost most of both).
 template <int PER, bool TRAIN>
 struct Finisher {
   int shift, gs;                 // lanes per group 2^shift, experts per group
   int gbit[PER];                 // lane that knows whether the group of expert j * 64 + l stays
-  float bias[PER], bsel[PER];
+  bool live[PER];                // j * 64 + l < E
+  float bsel[PER];
   double pq[PER], pz;            // TRAIN: this wave's sums over its tokens
   int pl[PER];
 
@@ -107,49 +122,39 @@ struct Finisher {
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const int e = j * 64 + lane;
-      gbit[j] = e < E ? (e / gs) << shift : 0;
-      bias[j] = (a.b_router && e < E) ? a.b_router[e] : 0.f;
-      bsel[j] = (a.b_select && e < E) ? a.b_select[e] : 0.f;
+      live[j] = e < E;
+      gbit[j] = live[j] ? (e / gs) << shift : 0;
+      bsel[j] = (a.b_select && live[j]) ? a.b_select[e] : 0.f;
       pq[j] = 0.0;
       pl[j] = 0;
     }
     pz = 0.0;
   }
 
-  // One token from its raw logits l (no bias yet); sel: 64 * PER floats of LDS of this wave.
-  __device__ __forceinline__ void token(const ScoreArgs& a, int t, float (&l)[PER], float* sel) {
-    const int lane = __lane_id(), E = a.sh.E, k = a.sh.k, G = a.groups, P = 1 << shift;
+  // One token from its logits (lanes past E: -inf); sel: 64 * PER floats of LDS of this wave.
+  __device__ __forceinline__ void token(const ScoreArgs& a, int t, const float (&l)[PER], float* sel) {
+    const int lane = __lane_id(), k = a.sh.k, G = a.groups;
     float s[PER];
-#pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int e = j * 64 + lane;
-      l[j] = e < E ? l[j] + bias[j] : -INFINITY;
-      if (a.logits && e < E) a.logits[(size_t)t * E + e] = l[j];
-    }
-    float m = l[0], tot = 0.f;
-    if (a.z_loss || !a.sigmoid) {
+    if ((TRAIN && a.z_loss) || !a.sigmoid) {
+      float m = l[0], tot = 0.f;
 #pragma unroll
       for (int j = 1; j < PER; ++j) m = fmaxf(m, l[j]);
       m = wave_max_f(m);
-      if (m == -INFINITY) m = 0.f;                 // every logit -inf: all scores 0
+      m = m == -INFINITY ? 0.f : m;                // every logit -inf: all scores 0
 #pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        s[j] = j * 64 + lane < E ? expf(l[j] - m) : 0.f;
-        tot += s[j];
-      }
+      for (int j = 0; j < PER; ++j) tot += s[j] = exp_f32(l[j] - m);
       tot = wave_sum_f(tot);
-    }
-    if (TRAIN && a.z_loss) {
-      const double lse = (double)m + (double)logf(tot);
-      pz += lse * lse;
+      if (TRAIN && a.z_loss) {
+        const double lse = (double)m + (double)__builtin_amdgcn_logf(tot) * 0.69314718055994530942;
+        pz += lse * lse;
+      }
+      const float r = tot > 0.f ? 1.f / tot : tot != tot ? tot : 0.f;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) s[j] *= r;
     }
     if (a.sigmoid) {
 #pragma unroll
-      for (int j = 0; j < PER; ++j) s[j] = j * 64 + lane < E ? 1.f / (1.f + expf(-l[j])) : 0.f;
-    } else {
-      const float r = 1.f / (tot > 0.f ? tot : 1.f);
-#pragma unroll
-      for (int j = 0; j < PER; ++j) s[j] *= r;
+      for (int j = 0; j < PER; ++j) s[j] = sigmoid_f32(l[j]);
     }
     if (TRAIN) {
       float r = 1.f;
@@ -157,7 +162,8 @@ struct Finisher {
         float q = 0.f;
 #pragma unroll
         for (int j = 0; j < PER; ++j) q += s[j];
-        r = 1.f / fmaxf(wave_sum_f(q), 1e-20f);    // every score underflowed: q = 0
+        q = wave_sum_f(q);
+        r = 1.f / (q < 1e-20f ? 1e-20f : q);       // every score underflowed: q = 0
       }
 #pragma unroll
       for (int j = 0; j < PER; ++j) pq[j] += (double)(s[j] * r);
@@ -167,37 +173,50 @@ struct Finisher {
 #pragma unroll
     for (int j = 0; j < PER; ++j) {
       const float v = s[j] + bsel[j];
-      key[j] = j * 64 + lane < E ? order_key(v) : 0u;
+      key[j] = live[j] ? order_key(v) : 0u;
       if (G > 1) sel[j * 64 + lane] = v == v ? v : -INFINITY;
     }
     if (G > 1) {
-      // Lanes [g P, (g + 1) P) find the best two of group g.
+      // Lanes [g P, (g + 1) P), P = 2^shift, find the best two of group g.
       __builtin_amdgcn_fence(__ATOMIC_RELEASE, "wavefront");
       __builtin_amdgcn_wave_barrier();
+      const int g = lane >> shift, P = 1 << shift, p = lane & (P - 1);
+      const float* mine = sel + min(g, G - 1) * gs;
       float b0 = -INFINITY, b1 = -INFINITY;
-      const int g = lane >> shift;
-      if (g < G)
-        for (int i = lane & (P - 1); i < gs; i += P) {
-          const float v = sel[g * gs + i];
-          b1 = fmaxf(b1, fminf(b0, v));
-          b0 = fmaxf(b0, v);
+      for (int i = 0; i < gs; i += 4 * P) {
+        float v[4];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) v[q] = mine[min(i + q * P + p, gs - 1)];
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+          v[q] = i + q * P + p < gs ? v[q] : -INFINITY;
+          b1 = fmaxf(b1, fminf(b0, v[q]));
+          b0 = fmaxf(b0, v[q]);
         }
-      __builtin_amdgcn_wave_barrier();
-      for (int o = 1; o < P; o <<= 1) {
-        const float c0 = __shfl_xor(b0, o), c1 = __shfl_xor(b1, o);
-        b1 = fmaxf(fmaxf(b1, c1), fminf(b0, c0));
-        b0 = fmaxf(b0, c0);
       }
+      __builtin_amdgcn_wave_barrier();
+      auto merge = [&](auto step) {
+        constexpr int ST = decltype(step)::value;
+        if (shift > ST) {
+          const float c0 = pair_of<ST>(b0), c1 = pair_of<ST>(b1);
+          b1 = fmaxf(fmaxf(b1, c1), fminf(b0, c0));
+          b0 = fmaxf(b0, c0);
+        }
+      };
+      merge(std::integral_constant<int, 0>{});
+      merge(std::integral_constant<int, 1>{});
+      merge(std::integral_constant<int, 2>{});
+      merge(std::integral_constant<int, 3>{});
+      merge(std::integral_constant<int, 4>{});
       const uint32_t gk = g < G ? order_key(a.group_top == 2 ? b0 + b1 : b0) : 0u;
       int rank = 0;
       for (int h = 0; h < G; ++h) {
         const uint32_t hk = (uint32_t)__builtin_amdgcn_readlane((int)gk, h << shift);
-        rank += hk > gk || (hk == gk && h < g);
+        rank += (hk > gk) | ((hk == gk) & (h < g));
       }
-      const uint64_t stay = __ballot(g < G && rank < a.top_groups);
+      const uint64_t stay = __ballot((g < G) & (rank < a.top_groups));
 #pragma unroll
-      for (int j = 0; j < PER; ++j)
-        if (!((stay >> gbit[j]) & 1)) key[j] = 0u;
+      for (int j = 0; j < PER; ++j) key[j] = ((stay >> gbit[j]) & 1) ? key[j] : 0u;
     }
 
     // Top-k: the wave's best value, then the lowest expert that has it.
@@ -208,25 +227,25 @@ struct Finisher {
 #pragma unroll
       for (int j = 1; j < PER; ++j) best = max(best, key[j]);
       best = wave_max_u32(best);
-      int e = -1;
+      int e = 0;
+#pragma unroll
+      for (int j = PER - 1; j >= 0; --j) {
+        const uint64_t hit = __ballot(key[j] == best);
+        e = hit ? j * 64 + __ffsll((unsigned long long)hit) - 1 : e;
+      }
+      e = __builtin_amdgcn_readfirstlane(e);
       float r = 0.f;
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
-        if (e < 0) {
-          const uint64_t hit = __ballot(key[j] == best);
-          if (hit) {
-            const int at = __ffsll((unsigned long long)hit) - 1;
-            e = j * 64 + at;
-            r = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(s[j]), at));
-            if (lane == at) {
-              key[j] = 0u;
-              if (TRAIN) ++pl[j];
-            }
-          }
-        }
+        const bool it = j * 64 + lane == e;
+        r = it ? s[j] : r;
+        key[j] = it ? 0u : key[j];
+        if (TRAIN) pl[j] += it;
       }
+      r = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(r), e & 63));
       total += r;
-      if (lane == i) my_r = r, my_e = e;
+      my_r = lane == i ? r : my_r;
+      my_e = lane == i ? e : my_e;
     }
     if (lane < k) {
       a.topk_idx[(size_t)t * k + lane] = my_e;
@@ -235,64 +254,73 @@ struct Finisher {
   }
 };
 
-// LDS for the sums over a block's waves.
-template <int PER, int WAVES>
-struct FinishSums {
-  double p[WAVES][64 * PER], z[WAVES];
-  int l[WAVES][64 * PER];
-};
-
-// This block's column of the partial sums [E][blocks], waves added in order.
-template <int PER, int WAVES>
-__device__ __forceinline__ void store_sums(const ScoreArgs& a, const Finisher<PER, true>& f,
-                                           FinishSums<PER, WAVES>& sm, int wave) {
-  const int lane = __lane_id();
-  __syncthreads();
-#pragma unroll
-  for (int j = 0; j < PER; ++j) {
-    sm.p[wave][j * 64 + lane] = f.pq[j];
-    sm.l[wave][j * 64 + lane] = f.pl[j];
-  }
-  if (lane == 0) sm.z[wave] = f.pz;
-  __syncthreads();
-  for (int e = threadIdx.x; e < a.sh.E; e += WAVES * 64) {
-    double p = sm.p[0][e];
-    int n = sm.l[0][e];
-#pragma unroll
-    for (int w = 1; w < WAVES; ++w) p += sm.p[w][e], n += sm.l[w][e];
-    a.psum[(size_t)e * gridDim.x + blockIdx.x] = p;
-    a.pload[(size_t)e * gridDim.x + blockIdx.x] = n;
-  }
-  if (threadIdx.x == 0) {
-    double z = sm.z[0];
-#pragma unroll
-    for (int w = 1; w < WAVES; ++w) z += sm.z[w];
-    a.pz[blockIdx.x] = z;
-  }
-}
-
-// Tokens whose logits are in `parts` parts in the workspace; one wave per token.
-template <int PER, bool TRAIN>
-__global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a, int parts) {
-  __shared__ float sel[4][64 * PER];
-  __shared__ FinishSums<PER, 4> sums;
+// Tokens whose logits lie in `parts` parts at `in` [parts][T][E] (no bias yet), or, FINAL, as
+// they are in a.logits; one wave per token.  TRAIN: this block's column of the sums over
+// tokens, [E][blocks], waves added in order.
+template <int PER, bool TRAIN, int WAVES>
+__global__ __launch_bounds__(WAVES * 64) void score_finish_kernel(ScoreArgs a, int parts, bool final) {
+  __shared__ float sel[WAVES][64 * PER];
+  __shared__ double sum_p[TRAIN ? WAVES : 1][64 * PER];
+  __shared__ int sum_l[TRAIN ? WAVES : 1][64 * PER];
+  __shared__ double sum_z[WAVES];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int E = a.sh.E, T = a.sh.T;
+  const size_t step = (size_t)T * E;
   Finisher<PER, TRAIN> f;
   f.init(a);
-  for (int t = blockIdx.x * 4 + wave; t < T; t += gridDim.x * 4) {
-    float l[PER];
+  float bias[PER];
 #pragma unroll
-    for (int j = 0; j < PER; ++j) {
-      const int e = j * 64 + lane;
-      l[j] = 0.f;
-      if (e < E)
-        for (int p = 0; p < parts; ++p) l[j] += a.part[((size_t)p * T + t) * E + e];
+  for (int j = 0; j < PER; ++j) bias[j] = (!final && a.b_router && f.live[j]) ? a.b_router[j * 64 + lane] : 0.f;
+  const float* in = final ? a.logits : a.part;
+  for (int t = blockIdx.x * WAVES + wave; t < T; t += gridDim.x * WAVES) {
+    float l[PER];
+    const float* row = in + (size_t)t * E;
+#pragma unroll
+    for (int j = 0; j < PER; ++j) l[j] = row[min(j * 64 + lane, E - 1)];
+    for (int p = 1; p < parts; p += 4) {               // parts added in order, four loads at once
+      float v[4][PER];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int j = 0; j < PER; ++j) v[q][j] = row[min(p + q, parts - 1) * step + min(j * 64 + lane, E - 1)];
+#pragma unroll
+      for (int q = 0; q < 4; ++q)
+#pragma unroll
+        for (int j = 0; j < PER; ++j) l[j] += p + q < parts ? v[q][j] : 0.f;
+    }
+#pragma unroll
+    for (int j = 0; j < PER; ++j) l[j] = f.live[j] ? l[j] + bias[j] : -INFINITY;
+    if (!final && a.logits) {
+#pragma unroll
+      for (int j = 0; j < PER; ++j)
+        if (f.live[j]) a.logits[(size_t)t * E + j * 64 + lane] = l[j];
     }
     f.token(a, t, l, sel[wave]);
   }
-  if constexpr (TRAIN) store_sums<PER, 4>(a, f, sums, wave);
+  if constexpr (TRAIN) {
+#pragma unroll
+    for (int j = 0; j < PER; ++j) {
+      sum_p[wave][j * 64 + lane] = f.pq[j];
+      sum_l[wave][j * 64 + lane] = f.pl[j];
+    }
+    if (lane == 0) sum_z[wave] = f.pz;
+    __syncthreads();
+    for (int e = threadIdx.x; e < E; e += WAVES * 64) {
+      double p = sum_p[0][e];
+      int n = sum_l[0][e];
+#pragma unroll
+      for (int w = 1; w < WAVES; ++w) p += sum_p[w][e], n += sum_l[w][e];
+      a.psum[(size_t)e * gridDim.x + blockIdx.x] = p;
+      a.pload[(size_t)e * gridDim.x + blockIdx.x] = n;
+    }
+    if (threadIdx.x == 0) {
+      double z = sum_z[0];
+#pragma unroll
+      for (int w = 1; w < WAVES; ++w) z += sum_z[w];
+      a.pz[blockIdx.x] = z;
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -302,17 +330,14 @@ __global__ __launch_bounds__(256) void score_finish_kernel(ScoreArgs a, int part
 // chunk touch every bank once).  W_r goes by the MFMA's first operand, so a lane holds
 // four neighbouring experts of a token.  bf16: MFMA 32x32x16; fp32: 32x32x2, lane half
 // h taking chunk 2s + h of a row for slice s (both operands agree on the k of a slot).
-//
-// One part (d not split): the tile's logits stay in LDS and the block finishes its own
-// tokens, so x is read once and the logits are written only if asked for; blocks are
-// persistent and carry the sums over their tokens in registers.  More parts (too few
-// tokens to fill the chip): partial logits to the workspace for score_finish_kernel.
+// One part (d not split) and the logits wanted: they are written there, bias included;
+// else to the workspace.  Finishing the tokens in this kernel measured slower: with one
+// wave per SIMD a token took 5 us, the separate kernel has the waves to hide that.
 // ---------------------------------------------------------------------------
 constexpr int kRowsM = 64, kScoreStages = 3;
 
-template <typename T, int NE, bool FUSED, bool TRAIN>
+template <typename T, int NE>
 __global__ __launch_bounds__(256, 1) void score_tile_kernel(ScoreArgs a, int parts) {
-  constexpr int PER = NE / 64;
   constexpr int kKs = 128 / sizeof(T);                 // d per step
   constexpr int WN = NE == 256 ? 4 : 2, WM = 4 / WN;   // waves over experts, tokens
   constexpr int MT = kRowsM / WM / 32, NT = NE / WN / 32;
@@ -322,139 +347,128 @@ __global__ __launch_bounds__(256, 1) void score_tile_kernel(ScoreArgs a, int par
   constexpr int kLogits = kRowsM * kPitch * 4;
   constexpr int kLds = kScoreStages * kStage > kLogits ? kScoreStages * kStage : kLogits;
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
-  __shared__ float sel[FUSED ? 4 : 1][64 * PER];
-  __shared__ FinishSums<PER, FUSED && TRAIN ? 4 : 1> sums;
 
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int wm = wave / WN, wn = wave % WN, fr = lane & 31, fc = lane >> 5;
   const int E = a.sh.E, tokens = a.sh.T, d = a.sh.d;
-  const int part = FUSED ? 0 : blockIdx.y;
+  const int part = blockIdx.y, t0 = blockIdx.x * kRowsM;
   const int steps = d / kKs;
   const int s0 = (int)((long)part * steps / parts), nk = (int)((long)(part + 1) * steps / parts) - s0;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
   const size_t pitch = (size_t)d * sizeof(T);
-  Finisher<PER, TRAIN> f;
-  if constexpr (FUSED) f.init(a);
+  if (part == 0 && blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0u;
 
   // Loads: instruction i of wave w fills rows (4i + w) * 8 + lane / 8, chunk lane % 8.
   const int lr = lane >> 3;
-  uint32_t w_off[kWI];
+  uint32_t a_off[kAI], w_off[kWI];
 #pragma unroll
   for (int i = 0; i < kWI; ++i) {
     const int row = (i * 4 + wave) * 8 + lr;
     w_off[i] = (uint32_t)(min(row, E - 1) * pitch) + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
   }
-  const uint32_t swz = (fr >> 1) & 7;
-  const int tiles = (tokens + kRowsM - 1) / kRowsM;
-
-  for (int tile = blockIdx.x; tile < tiles; tile += gridDim.x) {
-    const int t0 = tile * kRowsM;
-    const uint8_t* x_base = static_cast<const uint8_t*>(a.x) + (size_t)t0 * pitch + (size_t)s0 * 128;
-    const uint8_t* w_base = static_cast<const uint8_t*>(a.w) + (size_t)s0 * 128;
-    uint32_t a_off[kAI];
 #pragma unroll
-    for (int i = 0; i < kAI; ++i) {
-      const int row = (i * 4 + wave) * 8 + lr;
-      a_off[i] = (uint32_t)(min(row, tokens - 1 - t0) * pitch) + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
-    }
-    auto load = [&](int i, int step, int stage) {      // steps past the last repeat it
-      const size_t k = (size_t)min(step, nk - 1) * 128;
-      const uint32_t base = lds0 + stage * kStage;
-      if (i < kAI) dma16(x_base + k, a_off[i < kAI ? i : 0], base + (i * 4 + wave) * 1024);
-      else dma16(w_base + k, w_off[i < kAI ? 0 : i - kAI], base + kA + ((i - kAI) * 4 + wave) * 1024);
-    };
-    f32x16 acc[NT][MT];
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int q = 0; q < 16; ++q) acc[n][m][q] = 0.f;
-
-    __syncthreads();                                   // the last tile's logits are read
-#pragma unroll
-    for (int s = 0; s < kScoreStages - 1; ++s)
-#pragma unroll
-      for (int i = 0; i < L; ++i) load(i, s, s);
-    int st = 0;
-    for (int t = 0; t < nk; ++t) {
-      __builtin_amdgcn_s_waitcnt(wait_vm((kScoreStages - 2) * L));   // step t landed
-      __syncthreads();                                 // for all; step t - 1 is read
-      const int into = st == 0 ? kScoreStages - 1 : st - 1;
-#pragma unroll
-      for (int i = 0; i < L; ++i) load(i, t + kScoreStages - 1, into);
-      const uint8_t* base = lds + st * kStage;
-#pragma unroll
-      for (int s = 0; s < 4; ++s) {
-        u32x4 xa[MT], wb[NT];
-        const uint32_t c = ((2 * s + fc) ^ swz) << 4;
-#pragma unroll
-        for (int m = 0; m < MT; ++m) xa[m] = ld16(base + ((wm * MT * 32 + fr) * 128 + c) + m * 4096);
-#pragma unroll
-        for (int n = 0; n < NT; ++n) wb[n] = ld16(base + ((wn * NT * 32 + fr) * 128 + c) + kA + n * 4096);
-#pragma unroll
-        for (int n = 0; n < NT; ++n)
-#pragma unroll
-          for (int m = 0; m < MT; ++m) {
-            if constexpr (sizeof(T) == 2) {
-              acc[n][m] = mfma32_bf16(wb[n], xa[m], acc[n][m]);
-            } else {
-#pragma unroll
-              for (int q = 0; q < 4; ++q)
-                acc[n][m] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(wb[n][q]), __uint_as_float(xa[m][q]),
-                                                                 acc[n][m], 0, 0, 0);
-            }
-          }
-      }
-      st = st == kScoreStages - 1 ? 0 : st + 1;
-    }
-    asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");      // the repeated loads too
-    __syncthreads();                                   // LDS free
-
-    // Lane: token m * 32 + fr, experts n * 32 + 8 g + 4 fc .. + 3.
-    float* lg = reinterpret_cast<float*>(lds);
-#pragma unroll
-    for (int n = 0; n < NT; ++n)
-#pragma unroll
-      for (int m = 0; m < MT; ++m)
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int e = (wn * NT + n) * 32 + 8 * g + 4 * fc, r = (wm * MT + m) * 32 + fr;
-          *reinterpret_cast<f32x4*>(lg + r * kPitch + e) =
-              f32x4{acc[n][m][4 * g], acc[n][m][4 * g + 1], acc[n][m][4 * g + 2], acc[n][m][4 * g + 3]};
-        }
-    __syncthreads();
-    for (int i = 0; i < kRowsM / 4; ++i) {
-      const int r = i * 4 + wave, t = t0 + r;
-      if (t >= tokens) break;
-      float l[PER];
-#pragma unroll
-      for (int j = 0; j < PER; ++j) l[j] = lg[r * kPitch + j * 64 + lane];
-      if constexpr (FUSED) {
-        f.token(a, t, l, sel[wave]);
-      } else {
-#pragma unroll
-        for (int j = 0; j < PER; ++j)
-          if (j * 64 + lane < E) a.part[((size_t)part * tokens + t) * E + j * 64 + lane] = l[j];
-      }
-    }
+  for (int i = 0; i < kAI; ++i) {
+    const int row = (i * 4 + wave) * 8 + lr;
+    a_off[i] = (uint32_t)(min(row, tokens - 1 - t0) * pitch) + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
   }
-  if constexpr (FUSED && TRAIN) store_sums<PER, 4>(a, f, sums, wave);
+  const uint32_t swz = (fr >> 1) & 7;
+  const uint8_t* x_base = static_cast<const uint8_t*>(a.x) + (size_t)t0 * pitch + (size_t)s0 * 128;
+  const uint8_t* w_base = static_cast<const uint8_t*>(a.w) + (size_t)s0 * 128;
+  auto load = [&](int i, int step, int stage) {        // steps past the last repeat it
+    const size_t k = (size_t)min(step, nk - 1) * 128;
+    const uint32_t base = lds0 + stage * kStage;
+    if (i < kAI) dma16(x_base + k, a_off[i < kAI ? i : 0], base + (i * 4 + wave) * 1024);
+    else dma16(w_base + k, w_off[i < kAI ? 0 : i - kAI], base + kA + ((i - kAI) * 4 + wave) * 1024);
+  };
+  f32x16 acc[NT][MT];
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[n][m][q] = 0.f;
+
+#pragma unroll
+  for (int s = 0; s < kScoreStages - 1; ++s)
+#pragma unroll
+    for (int i = 0; i < L; ++i) load(i, s, s);
+  int st = 0;
+  for (int t = 0; t < nk; ++t) {
+    __builtin_amdgcn_s_waitcnt(wait_vm((kScoreStages - 2) * L));     // step t landed
+    __syncthreads();                                   // for all; step t - 1 is read
+    const int into = st == 0 ? kScoreStages - 1 : st - 1;
+#pragma unroll
+    for (int i = 0; i < L; ++i) load(i, t + kScoreStages - 1, into);
+    const uint8_t* base = lds + st * kStage;
+#pragma unroll
+    for (int s = 0; s < 4; ++s) {
+      u32x4 xa[MT], wb[NT];
+      const uint32_t c = ((2 * s + fc) ^ swz) << 4;
+#pragma unroll
+      for (int m = 0; m < MT; ++m) xa[m] = ld16(base + ((wm * MT * 32 + fr) * 128 + c) + m * 4096);
+#pragma unroll
+      for (int n = 0; n < NT; ++n) wb[n] = ld16(base + ((wn * NT * 32 + fr) * 128 + c) + kA + n * 4096);
+#pragma unroll
+      for (int n = 0; n < NT; ++n)
+#pragma unroll
+        for (int m = 0; m < MT; ++m) {
+          if constexpr (sizeof(T) == 2) {
+            acc[n][m] = mfma32_bf16(wb[n], xa[m], acc[n][m]);
+          } else {
+#pragma unroll
+            for (int q = 0; q < 4; ++q)
+              acc[n][m] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(wb[n][q]), __uint_as_float(xa[m][q]),
+                                                               acc[n][m], 0, 0, 0);
+          }
+        }
+    }
+    st = st == kScoreStages - 1 ? 0 : st + 1;
+  }
+  asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");        // the repeated loads too
+  __syncthreads();                                     // LDS free
+
+  // Lane: token m * 32 + fr, experts n * 32 + 8 g + 4 fc .. + 3.
+  float* lg = reinterpret_cast<float*>(lds);
+#pragma unroll
+  for (int n = 0; n < NT; ++n)
+#pragma unroll
+    for (int m = 0; m < MT; ++m)
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        const int e = (wn * NT + n) * 32 + 8 * g + 4 * fc, r = (wm * MT + m) * 32 + fr;
+        *reinterpret_cast<f32x4*>(lg + r * kPitch + e) =
+            f32x4{acc[n][m][4 * g], acc[n][m][4 * g + 1], acc[n][m][4 * g + 2], acc[n][m][4 * g + 3]};
+      }
+  __syncthreads();
+  const bool final = parts == 1 && a.logits;
+  float* out = final ? a.logits : a.part + (size_t)part * tokens * E;
+  float bias[NE / 64];
+#pragma unroll
+  for (int j = 0; j < NE / 64; ++j)
+    bias[j] = (final && a.b_router && j * 64 + lane < E) ? a.b_router[j * 64 + lane] : 0.f;
+#pragma unroll 4
+  for (int i = 0; i < kRowsM / 4; ++i) {
+    const int r = i * 4 + wave, t = t0 + r;
+#pragma unroll
+    for (int j = 0; j < NE / 64; ++j)
+      if (t < tokens && j * 64 + lane < E) out[(size_t)t * E + j * 64 + lane] = lg[r * kPitch + j * 64 + lane] + bias[j];
+  }
 }
 
-// The sums over blocks (at most 256), in a fixed order, and what follows from them: one
-// block, a wave per expert at a time, its column of partial sums read at once.
+// The sums over blocks (at most 256) in a fixed order: a wave per expert, its column read at
+// once.  The block that finishes last (a counter that the logits kernel cleared; agent-wide
+// release and acquire around it) has all of them and writes the losses.
 __global__ __launch_bounds__(1024) void score_reduce_kernel(ScoreArgs a, int blocks) {
-  __shared__ double share[kScoreMaxExperts];
+  __shared__ bool last;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, E = a.sh.E;
+  const int e = blockIdx.x * 16 + wave;
   auto total = [&](double v) {
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) v += __shfl_xor(v, o);
     return v;
   };
-#pragma unroll 4
-  for (int e = wave; e < E; e += 16) {
+  if (e < E) {
     double p = 0.0;
     int n = 0;
 #pragma unroll
@@ -471,24 +485,27 @@ __global__ __launch_bounds__(1024) void score_reduce_kernel(ScoreArgs a, int blo
     if (lane == 0) {
       if (a.prob_mean) a.prob_mean[e] = (float)p;
       if (a.load) a.load[e] = n;
-      share[e] = p * n;
+      a.share[e] = p * n;
     }
   }
+  if (!a.aux && !a.z_loss) return;
   __syncthreads();
-  if (wave == 0) {
-    double x = 0.0, z = 0.0;
+  if (threadIdx.x == 0)
+    last = __hip_atomic_fetch_add(a.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;
+  __syncthreads();
+  if (!last || wave != 0) return;
+  double x = 0.0, z = 0.0;
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int j = i * 64 + lane;
-      if (j < E) x += share[j];
-      if (j < blocks) z += a.pz[j];
-    }
-    x = total(x);
-    z = total(z);
-    if (lane == 0) {
-      if (a.aux) *a.aux = (float)(x * E / ((double)a.sh.T * a.sh.k));
-      if (a.z_loss) *a.z_loss = (float)(z / a.sh.T);
-    }
+  for (int i = 0; i < 4; ++i) {
+    const int j = i * 64 + lane;
+    if (j < E) x += __hip_atomic_load(a.share + j, __ATOMIC_RELAXED, __HIP_MEMORY_SCOPE_AGENT);
+    if (j < blocks) z += a.pz[j];
+  }
+  x = total(x);
+  z = total(z);
+  if (lane == 0) {
+    if (a.aux) *a.aux = (float)(x * E / ((double)a.sh.T * a.sh.k));
+    if (a.z_loss) *a.z_loss = (float)(z / a.sh.T);
   }
 }
 
@@ -496,36 +513,31 @@ template <typename T>
 static void launch_typed(const ScoreArgs& a, bool train, hipStream_t s) {
   const ScoreShape& h = a.sh;
   const int parts = score_parts(h);
-  int nb;                                              // blocks that hold partial sums
-  if (score_tiled(h)) {
-    const int tiles = (h.T + kRowsM - 1) / kRowsM;
-    nb = std::min(tiles, 256);
-    auto tile = [&](auto ne) {
-      constexpr int NE = decltype(ne)::value;
-      if (parts > 1) score_tile_kernel<T, NE, false, false><<<dim3(tiles, parts), 256, 0, s>>>(a, parts);
-      else if (train) score_tile_kernel<T, NE, true, true><<<nb, 256, 0, s>>>(a, 1);
-      else score_tile_kernel<T, NE, true, false><<<nb, 256, 0, s>>>(a, 1);
-    };
-    if (h.E <= 64) tile(std::integral_constant<int, 64>{});
-    else if (h.E <= 128) tile(std::integral_constant<int, 128>{});
-    else tile(std::integral_constant<int, 256>{});
+  const bool tiled = score_tiled(h);
+  if (tiled) {
+    const dim3 grid((h.T + kRowsM - 1) / kRowsM, parts);
+    if (h.E <= 64) score_tile_kernel<T, 64><<<grid, 256, 0, s>>>(a, parts);
+    else if (h.E <= 128) score_tile_kernel<T, 128><<<grid, 256, 0, s>>>(a, parts);
+    else score_tile_kernel<T, 256><<<grid, 256, 0, s>>>(a, parts);
   } else {
     const dim3 grid((h.T + 15) / 16, (h.E + 63) / 64, parts);
     score_logits_kernel<T><<<grid, 256, 0, s>>>(static_cast<const T*>(a.x), static_cast<const T*>(a.w), h.T,
-                                               h.d, h.E, parts, a.part);
+                                               h.d, h.E, parts, a.part, a.done);
   }
-  if (!score_tiled(h) || parts > 1) {
-    nb = score_finish_blocks(h.T);
-    auto finish = [&](auto per) {
-      constexpr int PER = decltype(per)::value;
-      if (train) score_finish_kernel<PER, true><<<nb, 256, 0, s>>>(a, parts);
-      else score_finish_kernel<PER, false><<<nb, 256, 0, s>>>(a, parts);
-    };
-    if (h.E <= 64) finish(std::integral_constant<int, 1>{});
-    else if (h.E <= 128) finish(std::integral_constant<int, 2>{});
-    else finish(std::integral_constant<int, 4>{});
-  }
-  if (train) score_reduce_kernel<<<1, 1024, 0, s>>>(a, nb);
+  // Blocks of 4 waves while they spread over the chip, of 16 where tokens abound.
+  const bool big = h.T >= 4096, final = tiled && parts == 1 && a.logits;
+  const int nb = std::min(256, (h.T + (big ? 15 : 3)) / (big ? 16 : 4));
+  auto finish = [&](auto per) {
+    constexpr int PER = decltype(per)::value;
+    if (train && big) score_finish_kernel<PER, true, 16><<<nb, 1024, 0, s>>>(a, parts, final);
+    else if (train) score_finish_kernel<PER, true, 4><<<nb, 256, 0, s>>>(a, parts, final);
+    else if (big) score_finish_kernel<PER, false, 16><<<nb, 1024, 0, s>>>(a, parts, final);
+    else score_finish_kernel<PER, false, 4><<<nb, 256, 0, s>>>(a, parts, final);
+  };
+  if (h.E <= 64) finish(std::integral_constant<int, 1>{});
+  else if (h.E <= 128) finish(std::integral_constant<int, 2>{});
+  else finish(std::integral_constant<int, 4>{});
+  if (train) score_reduce_kernel<<<(h.E + 15) / 16, 1024, 0, s>>>(a, nb);
 }
 
 hipError_t launch_score(const ScoreArgs& a, hipStream_t s) {

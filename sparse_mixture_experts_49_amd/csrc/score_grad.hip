@@ -65,18 +65,19 @@ size_t score_dl_bytes(const ScoreShape& s) {
 }
 int score_grad_sum_blocks(int T) { return grad_blocks(T); }
 
-// dl of tiles of TT tokens: one wave per token, lane l the experts l, l + 64, ...; bf16
+// dl of tiles of TT tokens, a wave four of them, lane l the experts l, l + 64, ...; bf16
 // layers put the tile through LDS to write its terms along both axes.
 template <int PER, int TT, bool BF16>
-__global__ __launch_bounds__(256) void score_dlogits_kernel(ScoreGradArgs a, int Ek, int Tk, size_t by_token,
+__global__ __launch_bounds__(TT * 16) void score_dlogits_kernel(ScoreGradArgs a, int Ek, int Tk, size_t by_token,
                                                             size_t by_expert) {
-  constexpr int kPitch = 64 * PER + 1;
+  constexpr int kPitch = 64 * PER + 1, WAVES = TT / 4, kThreads = TT * 16;   // four tokens a wave
   __shared__ float tile[BF16 ? TT * kPitch : 1];
-  __shared__ double sum_b[4][64 * PER];
+  __shared__ double sum_b[WAVES][64 * PER];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int E = a.sh.E, T = a.sh.T, k = a.sh.k;
   float dq[PER];
+  const bool soft = !a.sigmoid || a.d_z;               // softmax(l) is needed
   const float aux = a.d_aux ? *a.d_aux : 0.f, z = a.d_z ? *a.d_z : 0.f;
   double pb[PER];
 #pragma unroll
@@ -86,54 +87,55 @@ __global__ __launch_bounds__(256) void score_dlogits_kernel(ScoreGradArgs a, int
     pb[j] = 0.0;
   }
   for (int t0 = blockIdx.x * TT; t0 < T; t0 += gridDim.x * TT) {
-    for (int i = wave; i < TT; i += 4) {
+    for (int i = wave; i < TT; i += WAVES) {
       const int t = t0 + i;
       float dl[PER];
 #pragma unroll
       for (int j = 0; j < PER; ++j) dl[j] = 0.f;
       if (t < T) {
         float l[PER], p[PER], s[PER];
-        float m = -INFINITY;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) l[j] = a.logits[(size_t)t * E + min(j * 64 + lane, E - 1)];
+        const int my_idx = a.topk_idx[(size_t)t * k + min(lane, k - 1)];
+        const float my_g = a.d_topk_w ? a.d_topk_w[(size_t)t * k + min(lane, k - 1)] : 0.f;
+        float m = -INFINITY, tot = 0.f;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
-          const int e = j * 64 + lane;
-          l[j] = e < E ? a.logits[(size_t)t * E + e] : -INFINITY;
+          l[j] = j * 64 + lane < E ? l[j] : -INFINITY;
           m = fmaxf(m, l[j]);
         }
-        m = wave_max_f(m);
-        if (m == -INFINITY) m = 0.f;
-        float tot = 0.f;
+        if (soft) {
+          m = wave_max_f(m);
+          m = m == -INFINITY ? 0.f : m;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          p[j] = j * 64 + lane < E ? expf(l[j] - m) : 0.f;
-          tot += p[j];
-        }
-        tot = wave_sum_f(tot);
-        const float r_tot = 1.f / (tot > 0.f ? tot : 1.f);
+          for (int j = 0; j < PER; ++j) tot += p[j] = exp_f32(l[j] - m);
+          tot = wave_sum_f(tot);
+          const float r_tot = tot > 0.f ? 1.f / tot : tot != tot ? tot : 0.f;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          p[j] *= r_tot;
-          s[j] = !a.sigmoid ? p[j] : j * 64 + lane < E ? 1.f / (1.f + expf(-l[j])) : 0.f;
+          for (int j = 0; j < PER; ++j) p[j] *= r_tot;
         }
+#pragma unroll
+        for (int j = 0; j < PER; ++j) s[j] = a.sigmoid ? sigmoid_f32(l[j]) : p[j];
         // Chosen scores and the gradients of the raw weights.
         int idx[8];
         float g[8], S = 1e-20f, gw = 0.f;
-        const int my_idx = lane < k ? a.topk_idx[(size_t)t * k + lane] : -1;
-        const float my_g = (lane < k && a.d_topk_w) ? a.d_topk_w[(size_t)t * k + lane] : 0.f;
 #pragma unroll
         for (int q = 0; q < 8; ++q) {
-          idx[q] = __builtin_amdgcn_readlane(my_idx, q);
-          if (idx[q] >= E || idx[q] < 0) idx[q] = -1;
+          idx[q] = q < k ? __builtin_amdgcn_readlane(my_idx, q) : -1;
+          idx[q] = (uint32_t)idx[q] < (uint32_t)E ? idx[q] : -1;
           g[q] = idx[q] >= 0 ? __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(my_g), q)) : 0.f;
           float r = 0.f;
 #pragma unroll
           for (int j = 0; j < PER; ++j) {
             const float v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(s[j]), idx[q] & 63));
-            if (idx[q] >= 0 && (idx[q] >> 6) == j) r = v;
+            r = idx[q] >> 6 == j ? v : r;              // idx -1: none
           }
           S += r;
           gw = fmaf(g[q], r, gw);
         }
+        const float rS = 1.f / S;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) g[q] = a.renorm ? a.scale * (g[q] - gw * rS) * rS : a.scale * g[q];
         float ds[PER];
         float cs = 0.f, cq = 0.f, ss = 0.f;
 #pragma unroll
@@ -141,16 +143,17 @@ __global__ __launch_bounds__(256) void score_dlogits_kernel(ScoreGradArgs a, int
           float dr = 0.f;
 #pragma unroll
           for (int q = 0; q < 8; ++q)
-            if (idx[q] == j * 64 + lane) dr += a.renorm ? a.scale * (g[q] - gw / S) / S : a.scale * g[q];
+            dr += idx[q] == j * 64 + lane ? g[q] : 0.f;
           ds[j] = dr;
           ss += s[j];
           cq = fmaf(dq[j], s[j], cq);
         }
         if (a.sigmoid && a.d_aux) {
-          ss = fmaxf(wave_sum_f(ss), 1e-20f);
-          cq = wave_sum_f(cq);
+          ss = wave_sum_f(ss);
+          const float rs = 1.f / (ss < 1e-20f ? 1e-20f : ss);
+          cq = wave_sum_f(cq) * rs;
 #pragma unroll
-          for (int j = 0; j < PER; ++j) ds[j] += (dq[j] - cq / ss) / ss;
+          for (int j = 0; j < PER; ++j) ds[j] += (dq[j] - cq) * rs;
         } else if (!a.sigmoid) {
 #pragma unroll
           for (int j = 0; j < PER; ++j) {
@@ -159,7 +162,7 @@ __global__ __launch_bounds__(256) void score_dlogits_kernel(ScoreGradArgs a, int
           }
           cs = wave_sum_f(cs);
         }
-        const float zl = a.d_z ? z * 2.f / T * (m + logf(tot)) : 0.f;
+        const float zl = a.d_z ? z * 2.f / T * fmaf(__builtin_amdgcn_logf(tot), 0.69314718055994530942f, m) : 0.f;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
           const int e = j * 64 + lane;
@@ -190,18 +193,20 @@ __global__ __launch_bounds__(256) void score_dlogits_kernel(ScoreGradArgs a, int
       uint32_t* out = static_cast<uint32_t*>(a.dl);
       __syncthreads();
       if (a.d_x) {
-        const int half = Ek / 2;
-        for (int i = threadIdx.x; i < TT * half; i += 256) {
-          const int r = i / half, c = i - r * half;
+        constexpr int kPer = 32 * PER;                 // pairs per row, at most
+#pragma unroll 4
+        for (int i = threadIdx.x; i < TT * kPer; i += kThreads) {
+          const int r = i / kPer, c = i % kPer;
           uint32_t hi, mid, lo;
           terms(tile[r * kPitch + 2 * c], tile[r * kPitch + 2 * c + 1], hi, mid, lo);
           const size_t at = ((size_t)(t0 + r) * Ek) / 2 + c;
-          if (t0 + r < T) out[at] = hi, out[by_token / 2 + at] = mid;
+          if (t0 + r < T && 2 * c < Ek) out[at] = hi, out[by_token / 2 + at] = mid;
         }
       }
       if (a.d_w) {
         uint32_t* tw = out + by_token;                 // after the two by-token terms
-        for (int i = threadIdx.x; i < E * (TT / 2); i += 256) {
+#pragma unroll 4
+        for (int i = threadIdx.x; i < E * (TT / 2); i += kThreads) {
           const int e = i / (TT / 2), c = i % (TT / 2);
           uint32_t hi, mid, lo;
           terms(tile[(2 * c) * kPitch + e], tile[(2 * c + 1) * kPitch + e], hi, mid, lo);
@@ -210,7 +215,7 @@ __global__ __launch_bounds__(256) void score_dlogits_kernel(ScoreGradArgs a, int
         }
         // The last tile also clears its rows' tail up to Tk (a k step past T).
         if (t0 + TT >= T)
-          for (int i = threadIdx.x; i < E * ((Tk - t0 - TT) / 2); i += 256) {
+          for (int i = threadIdx.x; i < E * ((Tk - t0 - TT) / 2); i += kThreads) {
             const int n = (Tk - t0 - TT) / 2, e = i / n, c = i - e * n;
             const size_t at = ((size_t)e * Tk + t0 + TT) / 2 + c;
             tw[at] = 0u, tw[by_expert / 2 + at] = 0u, tw[by_expert + at] = 0u;
@@ -223,8 +228,12 @@ __global__ __launch_bounds__(256) void score_dlogits_kernel(ScoreGradArgs a, int
 #pragma unroll
     for (int j = 0; j < PER; ++j) sum_b[wave][j * 64 + lane] = pb[j];
     __syncthreads();
-    for (int e = threadIdx.x; e < E; e += 256)
-      a.pb[(size_t)e * gridDim.x + blockIdx.x] = sum_b[0][e] + sum_b[1][e] + sum_b[2][e] + sum_b[3][e];
+    for (int e = threadIdx.x; e < E; e += kThreads) {
+      double p = sum_b[0][e];
+#pragma unroll
+      for (int w = 1; w < WAVES; ++w) p += sum_b[w][e];
+      a.pb[(size_t)e * gridDim.x + blockIdx.x] = p;
+    }
   }
 }
 
@@ -496,11 +505,11 @@ static void launch_dlogits(const ScoreGradArgs& a, int blocks, hipStream_t s) {
   const TermSpace t = term_space(a.sh);
   const bool big = grad_tile(a.sh.T) == 64;
   if (a.sh.bf16 && big)
-    score_dlogits_kernel<PER, 64, true><<<blocks, 256, 0, s>>>(a, t.Ek, t.Tk, t.by_token, t.by_expert);
+    score_dlogits_kernel<PER, 64, true><<<blocks, 1024, 0, s>>>(a, t.Ek, t.Tk, t.by_token, t.by_expert);
   else if (a.sh.bf16)
     score_dlogits_kernel<PER, 16, true><<<blocks, 256, 0, s>>>(a, t.Ek, t.Tk, t.by_token, t.by_expert);
   else if (big)
-    score_dlogits_kernel<PER, 64, false><<<blocks, 256, 0, s>>>(a, 0, 0, 0, 0);
+    score_dlogits_kernel<PER, 64, false><<<blocks, 1024, 0, s>>>(a, 0, 0, 0, 0);
   else
     score_dlogits_kernel<PER, 16, false><<<blocks, 256, 0, s>>>(a, 0, 0, 0, 0);
 }
