@@ -223,7 +223,7 @@ int moe_score_backward(const moe_score_desc* desc, const void* x, const void* w_
   a.d_w = grads->d_w_router;
   a.d_b = grads->d_b_router;
   a.d_logits = grads->d_logits;
-  a.dl = at<void>(ws, L.dl);
+  a.dl = at<float>(ws, L.dl);
   a.pb = at<double>(ws, L.pb);
   a.pw = at<float>(ws, L.pw);
   return hip_status(moe::launch_score_grad(a, static_cast<hipStream_t>(stream)),

@@ -65,7 +65,7 @@ struct ScoreGradArgs {
   float* d_w;
   float* d_b;
   float* d_logits;
-  void* dl;                // workspace of score_dl_bytes
+  float* dl;               // workspace of score_dl_bytes
   double* pb;              // workspace [E][score_grad_sum_blocks]
   float* pw;               // workspace [slices][E][d]
 };

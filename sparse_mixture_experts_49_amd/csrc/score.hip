@@ -20,10 +20,10 @@ static bool score_tiled(const ScoreShape& s) { return s.T >= 512; }
 
 int score_parts(const ScoreShape& s) {
   if (score_tiled(s)) {
-    // One part where the tiles fill more than half the chip; else enough to fill it, 128 of d
-    // or more in each.
-    const long tiles = (s.T + 63) / 64;
-    return tiles > 128 ? 1 : (int)std::max(1L, std::min(256 / tiles, s.d / 128L));
+    // One part where the tiles fill more than half the chip; else enough to fill it, two
+    // steps or more in each.
+    const long tiles = (s.T + 63) / 64, steps = s.d / (s.bf16 ? 64 : 32);
+    return tiles > 128 ? 1 : (int)std::max(1L, std::min(256 / tiles, steps / 2));
   }
   // Enough waves to cover the chip twice (512 blocks), no part under 128 of d.
   const long blocks = (long)((s.T + 15) / 16) * ((s.E + 63) / 64);
@@ -324,33 +324,40 @@ __global__ __launch_bounds__(WAVES * 64) void score_finish_kernel(ScoreArgs a, i
 }
 
 // ---------------------------------------------------------------------------
-// Many tokens: 64 tokens x all experts (NE = 64, 128 or 256 columns) per block, both
-// operands through LDS in steps of 128 bytes of d, three stages, the loads two steps
-// ahead; rows of 128 B with 16 B chunks at chunk ^ ((row >> 1) & 7) (16 rows' reads of a
-// chunk touch every bank once).  W_r goes by the MFMA's first operand, so a lane holds
-// four neighbouring experts of a token.  bf16: MFMA 32x32x16; fp32: 32x32x2, lane half
-// h taking chunk 2s + h of a row for slice s (both operands agree on the k of a slot).
-// One part (d not split) and the logits wanted: they are written there, bias included;
-// else to the workspace.  Finishing the tokens in this kernel measured slower: with one
-// wave per SIMD a token took 5 us, the separate kernel has the waves to hide that.
+// Many tokens: 64 tokens x all experts (NE columns) per block, both operands through LDS in
+// steps of 128 bytes of d; rows of 128 B with 16 B chunks at chunk ^ ((row >> 1) & 7) (16
+// rows' reads of a chunk touch every bank once).  W_r goes by the MFMA's first operand, so a
+// lane holds four neighbouring experts of a token.  bf16: MFMA 32x32x16; fp32: 32x32x2,
+// lane half h taking chunk 2s + h of a row for slice s (both operands agree on the k of a
+// slot).
+// W_r comes from L2, two steps ahead; x from memory, five: 256 CUs need about
+// 8 MB in flight to read at full rate, two steps of x were 4 MB.
+// Eight waves, two per SIMD: waves 0-3 multiply the first half of each step, 4-7 the
+// second, each over the whole tile, so LDS is read no more often than by four waves while
+// one wave's reads run under the other's MFMAs; the halves add up at the end through LDS.
+// One part (d not split) and the logits wanted: they are written there, bias included; else
+// to the workspace.  Finishing the tokens in this kernel measured slower: with so few
+// waves a token took 5 us, the separate kernel has the waves to hide that.
 // ---------------------------------------------------------------------------
-constexpr int kRowsM = 64, kScoreStages = 3;
+constexpr int kRowsM = 64, kXStages = 6, kWStages = 3;
 
 template <typename T, int NE>
-__global__ __launch_bounds__(256, 1) void score_tile_kernel(ScoreArgs a, int parts) {
+__global__ __launch_bounds__(512, 1) void score_tile_kernel(ScoreArgs a, int parts) {
   constexpr int kKs = 128 / sizeof(T);                 // d per step
-  constexpr int WN = NE == 256 ? 4 : 2, WM = 4 / WN;   // waves over experts, tokens
+  constexpr int WN = NE == 256 ? 4 : 2, WM = 4 / WN;   // waves of a half over experts, tokens
   constexpr int MT = kRowsM / WM / 32, NT = NE / WN / 32;
-  constexpr int kA = kRowsM * 128, kStage = kA + NE * 128;
-  constexpr int kAI = kA / 4096, kWI = NE * 128 / 4096, L = kAI + kWI;
+  constexpr int kX = kRowsM * 128, kW = NE * 128, kWBase = kXStages * kX;
+  constexpr int kWI = kW / 8192, L = 1 + kWI;          // 1 KB loads per wave and step
   constexpr int kPitch = NE + 4;                       // floats per token's logits in LDS
   constexpr int kLogits = kRowsM * kPitch * 4;
-  constexpr int kLds = kScoreStages * kStage > kLogits ? kScoreStages * kStage : kLogits;
+  constexpr int kStages = kWBase + kWStages * kW;
+  constexpr int kLds = kStages > kLogits ? kStages : kLogits;
+  static_assert(kX == 8192 && kW % 8192 == 0 && kLds <= 160 * 1024, "load plan");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
 
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave / WN, wn = wave % WN, fr = lane & 31, fc = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = wave >> 2;
+  const int wm = (wave & 3) / WN, wn = (wave & 3) % WN, fr = lane & 31, fc = lane >> 5;
   const int E = a.sh.E, tokens = a.sh.T, d = a.sh.d;
   const int part = blockIdx.y, t0 = blockIdx.x * kRowsM;
   const int steps = d / kKs;
@@ -359,27 +366,22 @@ __global__ __launch_bounds__(256, 1) void score_tile_kernel(ScoreArgs a, int par
   const size_t pitch = (size_t)d * sizeof(T);
   if (part == 0 && blockIdx.x == 0 && threadIdx.x == 0) *a.done = 0u;
 
-  // Loads: instruction i of wave w fills rows (4i + w) * 8 + lane / 8, chunk lane % 8.
-  const int lr = lane >> 3;
-  uint32_t a_off[kAI], w_off[kWI];
+  // Loads: instruction i of wave w fills rows (8i + w) * 8 + lane / 8, chunk lane % 8.
+  const int row0 = wave * 8 + (lane >> 3);
+  const uint32_t chunk = ((lane & 7) ^ ((row0 >> 1) & 7)) << 4;
+  const uint32_t x_off = (uint32_t)(min(row0, tokens - 1 - t0) * pitch) + chunk;
+  uint32_t w_off[kWI];
 #pragma unroll
-  for (int i = 0; i < kWI; ++i) {
-    const int row = (i * 4 + wave) * 8 + lr;
-    w_off[i] = (uint32_t)(min(row, E - 1) * pitch) + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
-  }
-#pragma unroll
-  for (int i = 0; i < kAI; ++i) {
-    const int row = (i * 4 + wave) * 8 + lr;
-    a_off[i] = (uint32_t)(min(row, tokens - 1 - t0) * pitch) + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
-  }
+  for (int i = 0; i < kWI; ++i) w_off[i] = (uint32_t)(min(i * 64 + row0, E - 1) * pitch) + chunk;
   const uint32_t swz = (fr >> 1) & 7;
   const uint8_t* x_base = static_cast<const uint8_t*>(a.x) + (size_t)t0 * pitch + (size_t)s0 * 128;
   const uint8_t* w_base = static_cast<const uint8_t*>(a.w) + (size_t)s0 * 128;
-  auto load = [&](int i, int step, int stage) {        // steps past the last repeat it
-    const size_t k = (size_t)min(step, nk - 1) * 128;
-    const uint32_t base = lds0 + stage * kStage;
-    if (i < kAI) dma16(x_base + k, a_off[i < kAI ? i : 0], base + (i * 4 + wave) * 1024);
-    else dma16(w_base + k, w_off[i < kAI ? 0 : i - kAI], base + kA + ((i - kAI) * 4 + wave) * 1024);
+  // Steps past the last repeat it (into free stages).
+  auto load_x = [&](int step, int stage) {
+    dma16(x_base + (size_t)min(step, nk - 1) * 128, x_off, lds0 + stage * kX + wave * 1024);
+  };
+  auto load_w = [&](int i, int step, int stage) {
+    dma16(w_base + (size_t)min(step, nk - 1) * 128, w_off[i], lds0 + kWBase + stage * kW + (i * 8 + wave) * 1024);
   };
   f32x16 acc[NT][MT];
 #pragma unroll
@@ -389,67 +391,99 @@ __global__ __launch_bounds__(256, 1) void score_tile_kernel(ScoreArgs a, int par
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[n][m][q] = 0.f;
 
+  u32x4 xa[2][MT], wb[2][NT];
+  auto read = [&](int i, int stage_x, int stage_w) {   // slice i of this half of a step
+    const uint32_t c = ((4 * half + 2 * i + fc) ^ swz) << 4;
 #pragma unroll
-  for (int s = 0; s < kScoreStages - 1; ++s)
+    for (int m = 0; m < MT; ++m) xa[i][m] = ld16(lds + stage_x * kX + ((wm * MT * 32 + fr) * 128 + c) + m * 4096);
 #pragma unroll
-    for (int i = 0; i < L; ++i) load(i, s, s);
-  int st = 0;
-  for (int t = 0; t < nk; ++t) {
-    __builtin_amdgcn_s_waitcnt(wait_vm((kScoreStages - 2) * L));     // step t landed
-    __syncthreads();                                   // for all; step t - 1 is read
-    const int into = st == 0 ? kScoreStages - 1 : st - 1;
+    for (int n = 0; n < NT; ++n)
+      wb[i][n] = ld16(lds + kWBase + stage_w * kW + ((wn * NT * 32 + fr) * 128 + c) + n * 4096);
+  };
+  // Slice 0 of step t is in registers when it starts; slice 1 is read under slice 0's MFMAs
+  // and the next step's slice 0 under slice 1's, with the loads between the MFMAs (all at
+  // once they hold the waves up).  The barrier sits in the middle: the next step has landed,
+  // everyone has read the last of this one.
 #pragma unroll
-    for (int i = 0; i < L; ++i) load(i, t + kScoreStages - 1, into);
-    const uint8_t* base = lds + st * kStage;
+  for (int s = 0; s < kXStages; ++s) load_x(s, s);
 #pragma unroll
-    for (int s = 0; s < 4; ++s) {
-      u32x4 xa[MT], wb[NT];
-      const uint32_t c = ((2 * s + fc) ^ swz) << 4;
+  for (int s = 0; s < kWStages; ++s)
 #pragma unroll
-      for (int m = 0; m < MT; ++m) xa[m] = ld16(base + ((wm * MT * 32 + fr) * 128 + c) + m * 4096);
+    for (int i = 0; i < kWI; ++i) load_w(i, s, s);
+  __builtin_amdgcn_s_waitcnt(wait_vm((kWStages - 1) * kWI));
+  __syncthreads();
+  read(0, 0, 0);
+  int sx = 0, sw = 0;                                  // stages of step t
+  constexpr int kM = NT * MT;
+  auto mfma = [&](int i, int q) {
+    const int n = q / MT, m = q % MT;
+    if constexpr (sizeof(T) == 2) {
+      acc[n][m] = mfma32_bf16(wb[i][n], xa[i][m], acc[n][m]);
+    } else {
 #pragma unroll
-      for (int n = 0; n < NT; ++n) wb[n] = ld16(base + ((wn * NT * 32 + fr) * 128 + c) + kA + n * 4096);
-#pragma unroll
-      for (int n = 0; n < NT; ++n)
-#pragma unroll
-        for (int m = 0; m < MT; ++m) {
-          if constexpr (sizeof(T) == 2) {
-            acc[n][m] = mfma32_bf16(wb[n], xa[m], acc[n][m]);
-          } else {
-#pragma unroll
-            for (int q = 0; q < 4; ++q)
-              acc[n][m] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(wb[n][q]), __uint_as_float(xa[m][q]),
-                                                               acc[n][m], 0, 0, 0);
-          }
-        }
+      for (int j = 0; j < 4; ++j)
+        acc[n][m] = __builtin_amdgcn_mfma_f32_32x32x2f32(__uint_as_float(wb[i][n][j]), __uint_as_float(xa[i][m][j]),
+                                                         acc[n][m], 0, 0, 0);
     }
-    st = st == kScoreStages - 1 ? 0 : st + 1;
+  };
+  for (int t = 0; t < nk; ++t) {
+    const int sx1 = sx == kXStages - 1 ? 0 : sx + 1, sw1 = sw == kWStages - 1 ? 0 : sw + 1;
+    read(1, sx, sw);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int q = 0; q < kM; ++q) mfma(0, q);
+    __builtin_amdgcn_sched_barrier(0);
+    // Step t + 1 landed: in flight may be only what step t - 1 issued (at first W's step 2).
+    if (t == 0) __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(kWI));
+    else __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(L));
+    __syncthreads();
+    read(0, sx1, sw1);
+    __builtin_amdgcn_sched_barrier(0);
+#pragma unroll
+    for (int q = 0; q < kM; ++q) {
+      mfma(1, q);
+#pragma unroll
+      for (int j = q * L / kM; j < (q + 1) * L / kM; ++j) {
+        if (j == 0) load_x(t + kXStages, sx);
+        else load_w(j - 1, t + kWStages, sw);
+      }
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    sx = sx1;
+    sw = sw1;
   }
   asm volatile("s_waitcnt vmcnt(0) lgkmcnt(0)" ::: "memory");        // the repeated loads too
   __syncthreads();                                     // LDS free
 
-  // Lane: token m * 32 + fr, experts n * 32 + 8 g + 4 fc .. + 3.
+  // Lane: token m * 32 + fr, experts n * 32 + 8 g + 4 fc .. + 3.  First half + second half.
   float* lg = reinterpret_cast<float*>(lds);
 #pragma unroll
-  for (int n = 0; n < NT; ++n)
+  for (int h = 1; h >= 0; --h) {
+    if (half == h) {
 #pragma unroll
-    for (int m = 0; m < MT; ++m)
+      for (int n = 0; n < NT; ++n)
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int e = (wn * NT + n) * 32 + 8 * g + 4 * fc, r = (wm * MT + m) * 32 + fr;
-        *reinterpret_cast<f32x4*>(lg + r * kPitch + e) =
-            f32x4{acc[n][m][4 * g], acc[n][m][4 * g + 1], acc[n][m][4 * g + 2], acc[n][m][4 * g + 3]};
-      }
-  __syncthreads();
+        for (int m = 0; m < MT; ++m)
+#pragma unroll
+          for (int g = 0; g < 4; ++g) {
+            const int e = (wn * NT + n) * 32 + 8 * g + 4 * fc, r = (wm * MT + m) * 32 + fr;
+            f32x4* at = reinterpret_cast<f32x4*>(lg + r * kPitch + e);
+            f32x4 v = {acc[n][m][4 * g], acc[n][m][4 * g + 1], acc[n][m][4 * g + 2], acc[n][m][4 * g + 3]};
+            if (h == 0) v += *at;
+            *at = v;
+          }
+    }
+    __syncthreads();
+  }
   const bool final = parts == 1 && a.logits;
   float* out = final ? a.logits : a.part + (size_t)part * tokens * E;
   float bias[NE / 64];
 #pragma unroll
   for (int j = 0; j < NE / 64; ++j)
     bias[j] = (final && a.b_router && j * 64 + lane < E) ? a.b_router[j * 64 + lane] : 0.f;
-#pragma unroll 4
-  for (int i = 0; i < kRowsM / 4; ++i) {
-    const int r = i * 4 + wave, t = t0 + r;
+#pragma unroll
+  for (int i = 0; i < kRowsM / 8; ++i) {
+    const int r = i * 8 + wave, t = t0 + r;
 #pragma unroll
     for (int j = 0; j < NE / 64; ++j)
       if (t < tokens && j * 64 + lane < E) out[(size_t)t * E + j * 64 + lane] = lg[r * kPitch + j * 64 + lane] + bias[j];
@@ -516,9 +550,10 @@ static void launch_typed(const ScoreArgs& a, bool train, hipStream_t s) {
   const bool tiled = score_tiled(h);
   if (tiled) {
     const dim3 grid((h.T + kRowsM - 1) / kRowsM, parts);
-    if (h.E <= 64) score_tile_kernel<T, 64><<<grid, 256, 0, s>>>(a, parts);
-    else if (h.E <= 128) score_tile_kernel<T, 128><<<grid, 256, 0, s>>>(a, parts);
-    else score_tile_kernel<T, 256><<<grid, 256, 0, s>>>(a, parts);
+    if (h.E <= 64) score_tile_kernel<T, 64><<<grid, 512, 0, s>>>(a, parts);
+    else if (h.E <= 128) score_tile_kernel<T, 128><<<grid, 512, 0, s>>>(a, parts);
+    else if (h.E <= 192) score_tile_kernel<T, 192><<<grid, 512, 0, s>>>(a, parts);
+    else score_tile_kernel<T, 256><<<grid, 512, 0, s>>>(a, parts);
   } else {
     const dim3 grid((h.T + 15) / 16, (h.E + 63) / 64, parts);
     score_logits_kernel<T><<<grid, 256, 0, s>>>(static_cast<const T*>(a.x), static_cast<const T*>(a.w), h.T,

@@ -10,8 +10,9 @@
 //
 // bf16 layers: x and W_r go to the bf16 MFMA as they are and dl as a sum of bf16 terms,
 // dl = hi + mid (+ lo): two keep 17 bits, enough under d_x's rounding to bf16, three keep
-// all of fp32's for the fp32 d_W.  The terms are written once, by token for d_x and by
-// expert for d_W, so both products read them along their k.
+// all of fp32's for the fp32 d_W.  dl itself is kept in fp32, by token for d_x and by expert
+// for d_W, so both products read it along their k and split it in registers (written out as
+// terms it is half as many bytes again and, by 64-byte rows, three times the cache lines).
 #include <algorithm>
 #include <type_traits>
 
@@ -28,9 +29,9 @@ constexpr int kGradCols = 256, kGradRows = 128, kGradK = 32;
 int score_grad_slices(const ScoreShape& s) {
   if (s.bf16) {
     // Blocks of kGradRows experts x 256 columns; slices of at least 128 tokens until every
-    // CU has two.
+    // CU has a block (its LDS holds no second one).
     const long tiles = (long)((s.E + kGradRows - 1) / kGradRows) * ((s.d + kGradCols - 1) / kGradCols);
-    return (int)std::max(1L, std::min({32L, (long)(s.T + 127) / 128, 512 / tiles}));
+    return (int)std::max(1L, std::min({32L, (long)(s.T + 127) / 128, 256 / tiles}));
   }
   // fp32: tiles of 16 experts x 64 columns per wave; slices of at least 64 tokens until
   // 2048 waves run.
@@ -45,31 +46,30 @@ static int grad_blocks(int T) {
   return std::min(256, (T + tile - 1) / tile);
 }
 
-// Workspace of the logit gradients: fp32 [T][E], or bf16 terms [2][T'][E'] and [3][E''][T''].
-struct TermSpace {
-  size_t by_token, by_expert, total;   // elements of 2 bytes
-  int Ek, Tk;                          // row lengths: E and T rounded up to the k step
+// Workspace of the logit gradients: by token [T'][Ek] and, for bf16 layers, by expert
+// [E'][Tk], fp32; rows padded with zeros to whole k steps (T', E': up to whole tiles, not
+// written).
+struct DlSpace {
+  int Ek, Tk;
+  size_t by_expert, total;             // elements
 };
-static TermSpace term_space(const ScoreShape& s) {
-  TermSpace t{};
+static DlSpace dl_space(const ScoreShape& s) {
+  DlSpace t{};
   t.Ek = up_to(s.E, kGradK);
   t.Tk = up_to(s.T, 64);
-  t.by_token = (size_t)up_to(s.T, kGradRows) * t.Ek;
-  t.by_expert = (size_t)up_to(s.E, kGradRows) * t.Tk;
-  t.total = 2 * t.by_token + 3 * t.by_expert;
+  t.by_expert = (size_t)up_to(s.T, kGradRows) * t.Ek;
+  t.total = t.by_expert + (s.bf16 ? (size_t)up_to(s.E, kGradRows) * t.Tk : 0);
   return t;
 }
 
-size_t score_dl_bytes(const ScoreShape& s) {
-  return s.bf16 ? term_space(s).total * 2 : (size_t)s.T * s.E * 4;
-}
+size_t score_dl_bytes(const ScoreShape& s) { return dl_space(s).total * 4; }
 int score_grad_sum_blocks(int T) { return grad_blocks(T); }
 
 // dl of tiles of TT tokens, a wave four of them, lane l the experts l, l + 64, ...; bf16
-// layers put the tile through LDS to write its terms along both axes.
+// layers put the tile through LDS to write it along the other axis too.
 template <int PER, int TT, bool BF16>
-__global__ __launch_bounds__(TT * 16) void score_dlogits_kernel(ScoreGradArgs a, int Ek, int Tk, size_t by_token,
-                                                            size_t by_expert) {
+__global__ __launch_bounds__(TT * 16) void score_dlogits_kernel(ScoreGradArgs a, int Ek, int Tk,
+                                                                size_t by_expert) {
   constexpr int kPitch = 64 * PER + 1, WAVES = TT / 4, kThreads = TT * 16;   // four tokens a wave
   __shared__ float tile[BF16 ? TT * kPitch : 1];
   __shared__ double sum_b[WAVES][64 * PER];
@@ -170,9 +170,9 @@ __global__ __launch_bounds__(TT * 16) void score_dlogits_kernel(ScoreGradArgs a,
           if (e < E) {
             dl[j] = a.d_z ? fmaf(zl, p[j], v) : v;
             if (a.d_logits) a.d_logits[(size_t)t * E + e] = dl[j];
-            if (!BF16) static_cast<float*>(a.dl)[(size_t)t * E + e] = dl[j];
             pb[j] += (double)dl[j];
           }
+          if (e < Ek) a.dl[(size_t)t * Ek + e] = dl[j];
         }
       }
       if constexpr (BF16)
@@ -180,47 +180,19 @@ __global__ __launch_bounds__(TT * 16) void score_dlogits_kernel(ScoreGradArgs a,
         for (int j = 0; j < PER; ++j) tile[i * kPitch + j * 64 + lane] = dl[j];
     }
     if constexpr (BF16) {
-      // Two neighbouring values at a time: hi, mid (and lo) terms, packed.
-      auto terms = [](float u, float v, uint32_t& hi, uint32_t& mid, uint32_t& lo) {
-        hi = pack_bf16x2(u, v);
-        u -= __uint_as_float(hi << 16);
-        v -= __uint_as_float(hi & 0xffff0000u);
-        mid = pack_bf16x2(u, v);
-        u -= __uint_as_float(mid << 16);
-        v -= __uint_as_float(mid & 0xffff0000u);
-        lo = pack_bf16x2(u, v);
-      };
-      uint32_t* out = static_cast<uint32_t*>(a.dl);
       __syncthreads();
-      if (a.d_x) {
-        constexpr int kPer = 32 * PER;                 // pairs per row, at most
+      float* out = a.dl + by_expert + t0;
 #pragma unroll 4
-        for (int i = threadIdx.x; i < TT * kPer; i += kThreads) {
-          const int r = i / kPer, c = i % kPer;
-          uint32_t hi, mid, lo;
-          terms(tile[r * kPitch + 2 * c], tile[r * kPitch + 2 * c + 1], hi, mid, lo);
-          const size_t at = ((size_t)(t0 + r) * Ek) / 2 + c;
-          if (t0 + r < T && 2 * c < Ek) out[at] = hi, out[by_token / 2 + at] = mid;
-        }
+      for (int i = threadIdx.x; i < E * TT; i += kThreads) {
+        const int e = i / TT, c = i % TT;
+        out[(size_t)e * Tk + c] = tile[c * kPitch + e];
       }
-      if (a.d_w) {
-        uint32_t* tw = out + by_token;                 // after the two by-token terms
-#pragma unroll 4
-        for (int i = threadIdx.x; i < E * (TT / 2); i += kThreads) {
-          const int e = i / (TT / 2), c = i % (TT / 2);
-          uint32_t hi, mid, lo;
-          terms(tile[(2 * c) * kPitch + e], tile[(2 * c + 1) * kPitch + e], hi, mid, lo);
-          const size_t at = ((size_t)e * Tk + t0) / 2 + c;
-          tw[at] = hi, tw[by_expert / 2 + at] = mid, tw[by_expert + at] = lo;
+      // The last tile also clears its rows' tail up to Tk (a k step past T).
+      if (t0 + TT >= T)
+        for (int i = threadIdx.x; i < E * (Tk - t0 - TT); i += kThreads) {
+          const int n = Tk - t0 - TT, e = i / n, c = i - e * n;
+          out[(size_t)e * Tk + TT + c] = 0.f;
         }
-        // The last tile also clears its rows' tail up to Tk (a k step past T).
-        if (t0 + TT >= T)
-          for (int i = threadIdx.x; i < E * ((Tk - t0 - TT) / 2); i += kThreads) {
-            const int n = (Tk - t0 - TT) / 2, e = i / n, c = i - e * n;
-            const size_t at = ((size_t)e * Tk + t0 + TT) / 2 + c;
-            tw[at] = 0u, tw[by_expert / 2 + at] = 0u, tw[by_expert + at] = 0u;
-          }
-      }
       __syncthreads();
     }
   }
@@ -254,10 +226,12 @@ __global__ __launch_bounds__(256) void score_db_kernel(const double* __restrict_
 }
 
 // ---------------------------------------------------------------------------
-// out[m][n] = sum_k A[m][k] B[k][n], A in PLANES bf16 terms along k, B bf16 with its rows
-// along n (d_x: A = dl by token, B = W_r; d_W: A = dl by expert, B = x, one slice of the
-// tokens per blockIdx.z).  Block 32 MT x 2 rows x 256 columns, 4 waves as 2 x 2, k in steps
-// of 32 through three LDS stages.
+// out[m][n] = sum_k A[m][k] B[k][n], A fp32 along k and multiplied as a sum of TERMS bf16
+// terms, B bf16 with its rows along n (d_x: A = dl by token, B = W_r; d_W: A = dl by expert, B = x, one slice of the
+// tokens per blockIdx.z).  Block 64 MT rows x 256 columns, k in steps of 32 through four LDS
+// stages.  Eight waves, two per SIMD: waves 0-3 (2 x 2 over the tile) multiply the first 16 k
+// of each step, waves 4-7 the second, so one wave's LDS reads run under the other's MFMAs;
+// at the end each half finishes one half of the columns with the other's sums.
 //
 // The MFMA wants 8 values along k per lane from both operands.  A has them in a row; of B a
 // lane reads the pair of neighbouring columns 2l, 2l + 1 from 8 rows (4 bytes each, a row's
@@ -265,52 +239,68 @@ __global__ __launch_bounds__(256) void score_db_kernel(const double* __restrict_
 // columns.  As the first operand they make a lane's accumulators, even and odd together, 8
 // neighbouring columns of one row: stores of 16 bytes (bf16) or 32 (fp32).
 //
-// LDS: A rows of 64 B, 16 B chunks at chunk ^ ((row >> 2) & 3); B rows of 512 B, their 128 B
+// LDS: A rows of 128 B, 16 B chunks at chunk ^ ((row >> 1) & 7); B rows of 512 B, their 128 B
 // quarters at quarter ^ ((row >> 3) & 1) so that the two lane halves (rows 8 apart) read
 // different banks.
 // ---------------------------------------------------------------------------
-template <int PLANES, int MT, bool OUT_BF16>
-__global__ __launch_bounds__(256, 1) void score_grad_gemm_kernel(
-    const uint16_t* __restrict__ A, size_t plane, int a_pitch, const uint16_t* __restrict__ B, int b_rows,
+// Eight fp32 values (two registers' worth of 16 B) to TERMS bf16 fragments.
+template <int TERMS>
+__device__ __forceinline__ void split_terms(f32x4 lo, f32x4 hi, u32x4 (&out)[TERMS]) {
+#pragma unroll
+  for (int j = 0; j < 4; ++j) {
+    float u = j < 2 ? lo[2 * j] : hi[2 * j - 4], v = j < 2 ? lo[2 * j + 1] : hi[2 * j - 3];
+#pragma unroll
+    for (int q = 0; q < TERMS; ++q) {
+      const uint32_t w = pack_bf16x2(u, v);
+      out[q][j] = w;
+      u -= __uint_as_float(w << 16);
+      v -= __uint_as_float(w & 0xffff0000u);
+    }
+  }
+}
+
+template <int TERMS, int MT, bool OUT_BF16>
+__global__ __launch_bounds__(512, 1) void score_grad_gemm_kernel(
+    const float* __restrict__ A, int a_pitch, const uint16_t* __restrict__ B, int b_rows,
     int d, int M, int K, int slices, void* __restrict__ out) {
-  constexpr int S = 3, kRows = 64 * MT;
-  constexpr int kA = kRows * 64, kStage = PLANES * kA + kGradK * 512;
-  constexpr int kAI = PLANES * kA / 4096, kBI = kGradK * 512 / 4096, L = kAI + kBI;
-  static_assert(kA % 4096 == 0 && S * kStage <= 160 * 1024, "load plan");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[S * kStage];
+  constexpr int S = 4, kRows = 64 * MT;
+  constexpr int kA = kRows * 128, kStage = kA + kGradK * 512;
+  constexpr int kAI = kA / 8192, kBI = 2, L = kAI + kBI;   // 1 KB loads per wave and step
+  constexpr int kSwap = 8 * MT * 32 * 68 * 4;          // one wave's 32 MT rows x 64 columns, padded
+  constexpr int kLds = S * kStage > kSwap ? S * kStage : kSwap;
+  static_assert(kLds <= 160 * 1024, "load plan");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
   const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int wm = wave >> 1, wn = wave & 1, fr = lane & 31, fc = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = wave >> 2;
+  const int wm = (wave >> 1) & 1, wn = wave & 1, fr = lane & 31, fc = lane >> 5;
   const int m0 = blockIdx.y * kRows, n0 = blockIdx.x * kGradCols, sl = blockIdx.z;
   const int steps = (K + kGradK - 1) / kGradK;
   const int s0 = (int)((long)sl * steps / slices), nk = (int)((long)(sl + 1) * steps / slices) - s0;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
 
-  const uint16_t* a_base[PLANES];
+  // A: load i of wave w fills rows 8 (8 i + w) + lane / 8.
+  const float* a_base = A + (size_t)m0 * a_pitch + (size_t)s0 * kGradK;
+  uint32_t a_off[kAI];
 #pragma unroll
-  for (int q = 0; q < PLANES; ++q) a_base[q] = A + q * plane + (size_t)m0 * a_pitch + (size_t)s0 * kGradK;
-  // A: load i of wave w fills rows (4 i + w) * 16 + lane / 4 of the planes laid end to end.
-  uint32_t a_off[kA / 4096];
-#pragma unroll
-  for (int i = 0; i < kA / 4096; ++i) {
-    const int row = (i * 4 + wave) * 16 + (lane >> 2);
-    a_off[i] = (uint32_t)row * (uint32_t)a_pitch * 2u + (((lane & 3) ^ ((row >> 2) & 3)) << 4);
+  for (int i = 0; i < kAI; ++i) {
+    const int row = (i * 8 + wave) * 8 + (lane >> 3);
+    a_off[i] = (uint32_t)row * (uint32_t)a_pitch * 4u + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
   }
-  // B: load i of wave w fills rows 2 (4 i + w) + lane / 32; columns past d wrap to the tile's
-  // first half (not stored).
+  // B: load i of wave w fills rows 2 (8 i + w) + lane / 32; rows past the last repeat it (A is
+  // 0 there), columns past d wrap to the tile's first half (not stored).
   const uint8_t* b_tile = reinterpret_cast<const uint8_t*>(B + (size_t)s0 * kGradK * d + n0);
   auto load = [&](int i, int step, int stage) {
     const uint32_t base = lds0 + stage * kStage;
     const int s = min(step, nk - 1);
     if (i < kAI) {
-      const int q = i / (kA / 4096), j = i % (kA / 4096);
-      dma16(a_base[q] + s * kGradK, a_off[j], base + q * kA + (j * 4 + wave) * 1024);
+      dma16(a_base + (size_t)s * kGradK, a_off[i < kAI ? i : 0], base + (i * 8 + wave) * 1024);
     } else {
-      const int j = i - kAI, r = 2 * (j * 4 + wave) + (lane >> 5);
+      const int j = i - kAI, r = 2 * (j * 8 + wave) + (lane >> 5);
       int c = (lane & 31) ^ (((r >> 3) & 1) << 3);
       if (n0 + c * 8 >= d) c -= 16;
       const int row = min(r, b_rows - 1 - (s0 + s) * kGradK);
-      dma16(b_tile + (size_t)s * kGradK * d * 2, (uint32_t)(row * d + c * 8) * 2u, base + PLANES * kA + (j * 4 + wave) * 1024);
+      dma16(b_tile + (size_t)s * kGradK * d * 2, (uint32_t)(row * d + c * 8) * 2u,
+            base + kA + (j * 8 + wave) * 1024);
     }
   };
 
@@ -321,80 +311,125 @@ __global__ __launch_bounds__(256, 1) void score_grad_gemm_kernel(
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[n][m][q] = 0.f;
+  // k 16 half + 8 fc .. + 7: chunks 4 half + 2 fc and the next.
+  const uint32_t a_lane = (wm * MT * 32 + fr) * 128 + (((4 * half + 2 * fc) ^ ((fr >> 1) & 7)) << 4);
+  const uint32_t b_lane = kA + (16 * half + 8 * fc) * 512 + fr * 4;
+  f32x4 lo[MT], hi[MT];
+  uint32_t w[2][8];
+  u32x4 xa[MT][TERMS], b[4];
+  auto read = [&](int stage) {
+    const uint8_t* base = lds + stage * kStage;
 #pragma unroll
-  for (int s = 0; s < S - 1; ++s)
-#pragma unroll
-    for (int i = 0; i < L; ++i) load(i, s, s);
-  int st = 0;
-  const uint32_t swz = (fr >> 2) & 3;
-  for (int t = 0; t < nk; ++t) {
-    __builtin_amdgcn_s_waitcnt(wait_vm((S - 2) * L));
-    __syncthreads();
-    const int into = st == 0 ? S - 1 : st - 1;
-#pragma unroll
-    for (int i = 0; i < L; ++i) load(i, t + S - 1, into);
-    const uint8_t* base = lds + st * kStage;
-#pragma unroll
-    for (int s = 0; s < kGradK / 16; ++s) {
-      u32x4 xa[PLANES][MT], b[4];
-#pragma unroll
-      for (int q = 0; q < PLANES; ++q)
-#pragma unroll
-        for (int m = 0; m < MT; ++m)
-          xa[q][m] = ld16(base + ((wm * MT * 32 + fr) * 64 + (((2 * s + fc) ^ swz) << 4)) + q * kA + m * 2048);
-#pragma unroll
-      for (int n = 0; n < 2; ++n) {
-        uint32_t w[8];
-#pragma unroll
-        for (int j = 0; j < 8; ++j) {
-          const int quarter = (wn * 2 + n) ^ ((2 * s + fc) & 1);       // row 16 s + 8 fc + j
-          w[j] = *reinterpret_cast<const uint32_t*>(base + PLANES * kA + (16 * s + 8 * fc + j) * 512 + quarter * 128 + fr * 4);
-        }
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-          b[2 * n][j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], 0x05040100);
-          b[2 * n + 1][j] = __builtin_amdgcn_perm(w[2 * j + 1], w[2 * j], 0x07060302);
-        }
-      }
-#pragma unroll
-      for (int q = PLANES - 1; q >= 0; --q)            // small terms first
-#pragma unroll
-        for (int n = 0; n < 4; ++n)
-#pragma unroll
-          for (int m = 0; m < MT; ++m) acc[n][m] = mfma32_bf16(b[n], xa[q][m], acc[n][m]);
+    for (int m = 0; m < MT; ++m) {
+      lo[m] = __builtin_bit_cast(f32x4, ld16(base + a_lane + m * 4096));
+      hi[m] = __builtin_bit_cast(f32x4, ld16(base + (a_lane ^ 16) + m * 4096));
     }
-    st = st == S - 1 ? 0 : st + 1;
-  }
-  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");     // no load outlives its LDS
-  // Lane: row m * 32 + fr; accumulator 4 g + q of group 2 n (+ 1) is column
-  // n * 64 + 2 (8 g + 4 fc + q) (+ 1).
 #pragma unroll
-  for (int m = 0; m < MT; ++m) {
-    const int r = m0 + (wm * MT + m) * 32 + fr;
-    if (r >= M) continue;
+    for (int n = 0; n < 2; ++n) {
+      const uint32_t quarter = ((wn * 2 + n) ^ fc) * 128;    // row 16 half + 8 fc + j
+#pragma unroll
+      for (int j = 0; j < 8; ++j) w[n][j] = *reinterpret_cast<const uint32_t*>(base + b_lane + quarter + j * 512);
+    }
+  };
+  auto fragments = [&]() {
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
-      for (int g = 0; g < 4; ++g) {
-        const int col = n0 + wn * 128 + n * 64 + 16 * g + 8 * fc;
-        if (col >= d) continue;
-        const f32x16 &u = acc[2 * n][m], &v = acc[2 * n + 1][m];
-        if constexpr (OUT_BF16) {
-          u32x4 h;
+      for (int j = 0; j < 4; ++j) {
+        b[2 * n][j] = __builtin_amdgcn_perm(w[n][2 * j + 1], w[n][2 * j], 0x05040100);
+        b[2 * n + 1][j] = __builtin_amdgcn_perm(w[n][2 * j + 1], w[n][2 * j], 0x07060302);
+      }
 #pragma unroll
-          for (int q = 0; q < 4; ++q) h[q] = pack_bf16x2(u[4 * g + q], v[4 * g + q]);
-          st16(static_cast<uint16_t*>(out) + (size_t)r * d + col, h);
-        } else {
-          float* o = static_cast<float*>(out) + ((size_t)sl * M + r) * d + col;
-          *reinterpret_cast<f32x4*>(o) = f32x4{u[4 * g], v[4 * g], u[4 * g + 1], v[4 * g + 1]};
-          *reinterpret_cast<f32x4*>(o + 4) = f32x4{u[4 * g + 2], v[4 * g + 2], u[4 * g + 3], v[4 * g + 3]};
+    for (int m = 0; m < MT; ++m) split_terms<TERMS>(lo[m], hi[m], xa[m]);
+  };
+  // Step t's words are in registers when it starts; step t + 1's are read, and step t + S's
+  // loads issued, under its MFMAs.  The two waves of a SIMD make their fragments at
+  // different ends of the step, so one's VALU work runs under the other's MFMAs.
+#pragma unroll
+  for (int s = 0; s < S; ++s)
+#pragma unroll
+    for (int i = 0; i < L; ++i) load(i, s, s);
+  __builtin_amdgcn_s_waitcnt(wait_vm((S - 1) * L));
+  __syncthreads();
+  read(0);
+  if (half == 1) fragments();
+  int st = 0;
+  for (int t = 0; t < nk; ++t) {
+    const int st1 = st == S - 1 ? 0 : st + 1;
+    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0((S - 2) * L));    // step t + 1 landed, step t read
+    __syncthreads();
+    if (half == 0) fragments();
+    read(st1);
+    __builtin_amdgcn_sched_barrier(0);
+    constexpr int kM = TERMS * 4 * MT;                 // small terms first
+#pragma unroll
+    for (int i = 0; i < kM; ++i) {
+      const int q = TERMS - 1 - i / (4 * MT), n = i / MT % 4, m = i % MT;
+      acc[n][m] = mfma32_bf16(b[n], xa[m][q], acc[n][m]);
+#pragma unroll
+      for (int j = i * L / kM; j < (i + 1) * L / kM; ++j) load(j, t + S, st);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (half == 1) fragments();
+    st = st1;
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");     // no load outlives its LDS
+  __syncthreads();
+
+  // Lane: row m * 32 + fr; accumulator 4 g + q of group 2 n (+ 1) is column
+  // n * 64 + 2 (8 g + 4 fc + q) (+ 1).  Half h keeps n = h and hands over the other.
+  float* swap = reinterpret_cast<float*>(lds);
+  auto cols8 = [&](int n, int m, int g, f32x4& lo, f32x4& hi) {
+    const f32x16 &u = acc[2 * n][m], &v = acc[2 * n + 1][m];
+    lo = f32x4{u[4 * g], v[4 * g], u[4 * g + 1], v[4 * g + 1]};
+    hi = f32x4{u[4 * g + 2], v[4 * g + 2], u[4 * g + 3], v[4 * g + 3]};
+  };
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+    if (n != half) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          f32x4 lo, hi;
+          cols8(n, m, g, lo, hi);
+          float* at = swap + ((wave * MT + m) * 32 + fr) * 68 + 16 * g + 8 * fc;
+          *reinterpret_cast<f32x4*>(at) = lo;
+          *reinterpret_cast<f32x4*>(at + 4) = hi;
+        }
+    }
+  __syncthreads();
+#pragma unroll
+  for (int n = 0; n < 2; ++n)
+    if (n == half) {
+#pragma unroll
+      for (int m = 0; m < MT; ++m) {
+        const int r = m0 + (wm * MT + m) * 32 + fr;
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int col = n0 + wn * 128 + n * 64 + 16 * g + 8 * fc;
+          f32x4 lo, hi;
+          cols8(n, m, g, lo, hi);
+          const float* at = swap + (((wave ^ 4) * MT + m) * 32 + fr) * 68 + 16 * g + 8 * fc;
+          lo += *reinterpret_cast<const f32x4*>(at);
+          hi += *reinterpret_cast<const f32x4*>(at + 4);
+          if (r >= M || col >= d) continue;
+          if constexpr (OUT_BF16) {
+            st16(static_cast<uint16_t*>(out) + (size_t)r * d + col,
+                 u32x4{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]), pack_bf16x2(hi[0], hi[1]),
+                       pack_bf16x2(hi[2], hi[3])});
+          } else {
+            float* o = static_cast<float*>(out) + ((size_t)sl * M + r) * d + col;
+            *reinterpret_cast<f32x4*>(o) = lo;
+            *reinterpret_cast<f32x4*>(o + 4) = hi;
+          }
         }
       }
-  }
+    }
 }
 
 // fp32 layers: d_x tile of 16 tokens x 64 columns per wave: k-slot q of MFMA i is expert e0 + 4 i + q.
-__global__ __launch_bounds__(256) void score_dx_kernel(const float* __restrict__ dl,
+__global__ __launch_bounds__(256) void score_dx_kernel(const float* __restrict__ dl, int pitch,
                                                        const float* __restrict__ w, int tokens, int d,
                                                        int E, float* __restrict__ d_x) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, fr = lane & 15, fc = lane >> 4;
@@ -404,7 +439,7 @@ __global__ __launch_bounds__(256) void score_dx_kernel(const float* __restrict__
   f32x4 acc[4] = {};
   for (int e0 = 0; e0 < E; e0 += 4) {
     const int e = e0 + fc;
-    const float a = e < E ? dl[(size_t)t * E + e] : 0.f;
+    const float a = e < E ? dl[(size_t)t * pitch + e] : 0.f;
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       const float b = e < E ? w[(size_t)e * d + c0 + n * 16 + fr] : 0.f;
@@ -422,7 +457,7 @@ __global__ __launch_bounds__(256) void score_dx_kernel(const float* __restrict__
 }
 
 // d_w_router tile of 16 experts x 64 columns per wave over one slice of the tokens.
-__global__ __launch_bounds__(256) void score_dw_kernel(const float* __restrict__ dl,
+__global__ __launch_bounds__(256) void score_dw_kernel(const float* __restrict__ dl, int pitch,
                                                        const float* __restrict__ x, int tokens, int d,
                                                        int E, int slices, float* __restrict__ out) {
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, fr = lane & 15, fc = lane >> 4;
@@ -433,7 +468,7 @@ __global__ __launch_bounds__(256) void score_dw_kernel(const float* __restrict__
   f32x4 acc[4] = {};
   for (int t0 = ta; t0 < tb; t0 += 4) {
     const int t = t0 + fc;
-    const float a = t < tb ? dl[(size_t)t * E + e] : 0.f;
+    const float a = t < tb ? dl[(size_t)t * pitch + e] : 0.f;
 #pragma unroll
     for (int n = 0; n < 4; ++n) {
       const float b = t < tb ? x[(size_t)t * d + c0 + n * 16 + fr] : 0.f;
@@ -465,53 +500,52 @@ static void sum_slices(const ScoreGradArgs& a, int slices, hipStream_t s) {
 
 static void products_f32(const ScoreGradArgs& a, hipStream_t s) {
   const ScoreShape& h = a.sh;
-  const float* dl = static_cast<const float*>(a.dl);
+  const int pitch = dl_space(h).Ek;
   if (a.d_x)
     score_dx_kernel<<<dim3((h.T + 15) / 16, (h.d + 255) / 256), 256, 0, s>>>(
-        dl, static_cast<const float*>(a.w), h.T, h.d, h.E, static_cast<float*>(a.d_x));
+        a.dl, pitch, static_cast<const float*>(a.w), h.T, h.d, h.E, static_cast<float*>(a.d_x));
   if (a.d_w) {
     const int slices = score_grad_slices(h);
     score_dw_kernel<<<dim3((h.E + 15) / 16, (h.d + 255) / 256, slices), 256, 0, s>>>(
-        dl, static_cast<const float*>(a.x), h.T, h.d, h.E, slices, slices > 1 ? a.pw : a.d_w);
+        a.dl, pitch, static_cast<const float*>(a.x), h.T, h.d, h.E, slices, slices > 1 ? a.pw : a.d_w);
     if (slices > 1) sum_slices(a, slices, s);
   }
 }
 
 static void products_bf16(const ScoreGradArgs& a, hipStream_t s) {
   const ScoreShape& h = a.sh;
-  const TermSpace t = term_space(h);
-  const uint16_t* dl = static_cast<const uint16_t*>(a.dl);
+  const DlSpace t = dl_space(h);
   const int cols = (h.d + kGradCols - 1) / kGradCols;
   if (a.d_x)
-    score_grad_gemm_kernel<2, 2, true><<<dim3(cols, (h.T + 127) / 128, 1), 256, 0, s>>>(
-        dl, t.by_token, t.Ek, static_cast<const uint16_t*>(a.w), h.E, h.d, h.T, h.E, 1, a.d_x);
+    score_grad_gemm_kernel<2, 2, true><<<dim3(cols, (h.T + 127) / 128, 1), 512, 0, s>>>(
+        a.dl, t.Ek, static_cast<const uint16_t*>(a.w), h.E, h.d, h.T, h.E, 1, a.d_x);
   if (a.d_w) {
     const int slices = score_grad_slices(h);
     float* out = slices > 1 ? a.pw : a.d_w;
-    const uint16_t* by_expert = dl + 2 * t.by_token;
+    const float* by_expert = a.dl + t.by_expert;
     const uint16_t* x = static_cast<const uint16_t*>(a.x);
     if (h.E <= 64)
-      score_grad_gemm_kernel<3, 1, false><<<dim3(cols, 1, slices), 256, 0, s>>>(
-          by_expert, t.by_expert, t.Tk, x, h.T, h.d, h.E, h.T, slices, out);
+      score_grad_gemm_kernel<3, 1, false><<<dim3(cols, 1, slices), 512, 0, s>>>(
+          by_expert, t.Tk, x, h.T, h.d, h.E, h.T, slices, out);
     else
-      score_grad_gemm_kernel<3, 2, false><<<dim3(cols, (h.E + 127) / 128, slices), 256, 0, s>>>(
-          by_expert, t.by_expert, t.Tk, x, h.T, h.d, h.E, h.T, slices, out);
+      score_grad_gemm_kernel<3, 2, false><<<dim3(cols, (h.E + 127) / 128, slices), 512, 0, s>>>(
+          by_expert, t.Tk, x, h.T, h.d, h.E, h.T, slices, out);
     if (slices > 1) sum_slices(a, slices, s);
   }
 }
 
 template <int PER>
 static void launch_dlogits(const ScoreGradArgs& a, int blocks, hipStream_t s) {
-  const TermSpace t = term_space(a.sh);
+  const DlSpace t = dl_space(a.sh);
   const bool big = grad_tile(a.sh.T) == 64;
   if (a.sh.bf16 && big)
-    score_dlogits_kernel<PER, 64, true><<<blocks, 1024, 0, s>>>(a, t.Ek, t.Tk, t.by_token, t.by_expert);
+    score_dlogits_kernel<PER, 64, true><<<blocks, 1024, 0, s>>>(a, t.Ek, t.Tk, t.by_expert);
   else if (a.sh.bf16)
-    score_dlogits_kernel<PER, 16, true><<<blocks, 256, 0, s>>>(a, t.Ek, t.Tk, t.by_token, t.by_expert);
+    score_dlogits_kernel<PER, 16, true><<<blocks, 256, 0, s>>>(a, t.Ek, t.Tk, t.by_expert);
   else if (big)
-    score_dlogits_kernel<PER, 64, false><<<blocks, 1024, 0, s>>>(a, 0, 0, 0, 0);
+    score_dlogits_kernel<PER, 64, false><<<blocks, 1024, 0, s>>>(a, t.Ek, 0, 0);
   else
-    score_dlogits_kernel<PER, 16, false><<<blocks, 256, 0, s>>>(a, 0, 0, 0, 0);
+    score_dlogits_kernel<PER, 16, false><<<blocks, 256, 0, s>>>(a, t.Ek, 0, 0);
 }
 
 hipError_t launch_score_grad(const ScoreGradArgs& a, hipStream_t s) {
