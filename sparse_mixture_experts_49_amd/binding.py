@@ -453,8 +453,23 @@ def forward(x: torch.Tensor, weights: Weights, desc: Desc, workspace=None, strea
 
 # ---- scored routing --------------------------------------------------------------------
 
+class _CDescOnce:
+    """A descriptor whose C struct is made once and again after a field changes."""
+
+    def __setattr__(self, name, value):
+        object.__setattr__(self, name, value)
+        self.__dict__.pop("_ref", None)
+
+    def ref(self):
+        """The C struct by reference, as the calls take it."""
+        r = self.__dict__.get("_ref")
+        if r is None:
+            r = self.__dict__["_ref"] = ctypes.byref(self.to_c())
+        return r
+
+
 @dataclasses.dataclass
-class ScoreDesc:
+class ScoreDesc(_CDescOnce):
     """Options of the scored router (moe_score_desc)."""
     tokens: int
     d_model: int
@@ -518,9 +533,11 @@ class ScoreGrads:
                    d_b_router=torch.empty(desc.n_experts, **f32))
 
 
-try:                                   # the handle alone, without a Stream object around it
-    _raw_stream = torch._C._cuda_getCurrentRawStream
+try:                                   # the bare handle and index, without objects around them
+    _raw_stream, _current_device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
 except AttributeError:
+    _current_device = torch.cuda.current_device
+
     def _raw_stream(index):
         return torch.cuda.current_stream(index).cuda_stream
 
@@ -532,9 +549,14 @@ class _Call:
     def __init__(self, anchor, name):
         if not isinstance(anchor, torch.Tensor):
             raise MoeError(MOE_ERR_INVALID, f"{name} must be a torch tensor")
-        self.device = anchor.device
-        if self.device.type != "cuda":
-            raise MoeError(MOE_ERR_INVALID, f"{name} is on {self.device}, expected a GPU")
+        self.anchor = anchor
+        if not anchor.is_cuda:
+            raise MoeError(MOE_ERR_INVALID, f"{name} is on {anchor.device}, expected a GPU")
+        self.index = anchor.get_device()
+
+    @property
+    def device(self):
+        return self.anchor.device
 
     def t(self, t, name, dtype, numel):
         """Pointer of a contiguous tensor with at least numel elements, or None."""
@@ -542,7 +564,8 @@ class _Call:
             return None
         if not isinstance(t, torch.Tensor):
             raise MoeError(MOE_ERR_INVALID, f"{name} must be a torch tensor or None")
-        if t.device != self.device or t.dtype != dtype or t.numel() < numel or not t.is_contiguous():
+        if not (t.is_cuda and t.get_device() == self.index and t.dtype is dtype and t.numel() >= numel
+                and t.is_contiguous()):
             check_tensor(t, name, dtype, numel, self.device)
         return t.data_ptr()
 
@@ -550,26 +573,29 @@ class _Call:
         """(pointer, bytes) of the workspace; None allocates one."""
         if t is None:
             t = self._keep = torch.empty(size_of(), dtype=torch.uint8, device=self.device)
-        else:
+        elif not (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == self.index and t.is_contiguous()):
+            if not isinstance(t, torch.Tensor):
+                raise MoeError(MOE_ERR_INVALID, "workspace must be a torch tensor or None")
             check_tensor(t, "workspace", None, 0, self.device)
-        return t.data_ptr(), t.numel() * t.element_size()
+        return t.data_ptr(), t.nbytes
 
     def run(self, fn, *args, stream=None):
         if stream is None:
-            stream = _raw_stream(self.device.index)
+            stream = _raw_stream(self.index)
         elif hasattr(stream, "cuda_stream"):
             stream = stream.cuda_stream
-        if torch.cuda.current_device() != self.device.index:
-            with torch.cuda.device(self.device):
+        if _current_device() != self.index:
+            with torch.cuda.device(self.index):
                 status = fn(*args, stream)
         else:
             status = fn(*args, stream)
-        _check(status)
+        if status != MOE_OK:
+            _check(status)
 
 
 def moe_score_workspace_size(desc: ScoreDesc) -> int:
     n = ctypes.c_size_t(0)
-    _check(load_library().moe_score_workspace_size(ctypes.byref(desc.to_c()), ctypes.byref(n)))
+    _check(load_library().moe_score_workspace_size(desc.ref(), ctypes.byref(n)))
     return n.value
 
 
@@ -594,7 +620,7 @@ def moe_score_route(desc: ScoreDesc, x, w_router, routing: ScoreRouting, b_route
     c = _Call(x, "x")
     T, d, E, dt = desc.tokens, desc.d_model, desc.n_experts, desc.torch_dtype
     ws, nb = c.ws(workspace, lambda: moe_score_workspace_size(desc))
-    c.run(load_library().moe_score_route, ctypes.byref(desc.to_c()), c.t(x, "x", dt, T * d),
+    c.run(load_library().moe_score_route, desc.ref(), c.t(x, "x", dt, T * d),
           c.t(w_router, "w_router", dt, E * d), c.t(b_router, "b_router", torch.float32, E),
           c.t(b_select, "b_select", torch.float32, E), ctypes.byref(_score_out(c, desc, routing)), ws, nb,
           stream=stream)
@@ -611,7 +637,7 @@ def moe_score_backward(desc: ScoreDesc, x, w_router, routing: ScoreRouting, d_to
     g = CScoreGrads(c.t(grads.d_x, "grads.d_x", dt, T * d), c.t(grads.d_w_router, "grads.d_w_router", f32, E * d),
                     c.t(grads.d_b_router, "grads.d_b_router", f32, E),
                     c.t(grads.d_logits, "grads.d_logits", f32, T * E))
-    c.run(load_library().moe_score_backward, ctypes.byref(desc.to_c()), c.t(x, "x", dt, T * d),
+    c.run(load_library().moe_score_backward, desc.ref(), c.t(x, "x", dt, T * d),
           c.t(w_router, "w_router", dt, E * d), ctypes.byref(_score_out(c, desc, routing)),
           c.t(d_topk_w, "d_topk_w", f32, T * k), c.t(d_aux, "d_aux", f32, 1),
           c.t(d_z_loss, "d_z_loss", f32, 1), ctypes.byref(g), ws, nb, stream=stream)
@@ -620,7 +646,7 @@ def moe_score_backward(desc: ScoreDesc, x, w_router, routing: ScoreRouting, d_to
 # ---- experts in microscaled 4-bit floating point ------------------------------------------
 
 @dataclasses.dataclass
-class MxDesc:
+class MxDesc(_CDescOnce):
     """Options of a layer with MXFP4 expert weights (moe_mx_desc)."""
     tokens: int
     d_model: int
@@ -664,20 +690,20 @@ def alloc_mx(rows: int, cols: int, device):
             torch.empty(rows, cols // 32, dtype=torch.uint8, device=device))
 
 
-def _mx_rows(c: _Call, t, name):
+def _mx_rows(t, name):
     """(pointer, dtype id, rows, cols, row stride) of a 2-D tensor whose rows are contiguous."""
-    if t.device != c.device or t.dtype not in (torch.bfloat16, torch.float32) or t.dim() != 2 or \
-            (t.shape[1] > 1 and t.stride(1) != 1):
-        raise MoeError(MOE_ERR_INVALID, f"{name} must be a bf16 or fp32 matrix with contiguous rows on {c.device}")
-    stride = t.stride(0) if t.shape[0] > 1 else -(-t.shape[1] // 8) * 8
-    return (t.data_ptr(), MOE_DTYPE_BF16 if t.dtype == torch.bfloat16 else MOE_DTYPE_F32,
-            t.shape[0], t.shape[1], stride)
+    dt = MOE_DTYPE_BF16 if t.dtype is torch.bfloat16 else MOE_DTYPE_F32 if t.dtype is torch.float32 else -1
+    shape, strides = t.shape, t.stride()
+    if dt < 0 or len(shape) != 2 or (shape[1] > 1 and strides[1] != 1):
+        raise MoeError(MOE_ERR_INVALID, f"{name} must be a bf16 or fp32 matrix with contiguous rows")
+    rows, cols = shape
+    return t.data_ptr(), dt, rows, cols, strides[0] if rows > 1 else -(-cols // 8) * 8
 
 
 def moe_mx_quantize(x, codes, scales, stream=None):
     """Rows of x (bf16 or fp32 [rows, cols], any row stride) to MXFP4 codes and scales."""
     c = _Call(x, "x")
-    p, dt, rows, cols, stride = _mx_rows(c, x, "x")
+    p, dt, rows, cols, stride = _mx_rows(x, "x")
     c.run(load_library().moe_mx_quantize, p, dt, rows, cols, stride,
           c.t(codes, "codes", torch.uint8, rows * cols // 2),
           c.t(scales, "scales", torch.uint8, rows * cols // 32), stream=stream)
@@ -686,14 +712,14 @@ def moe_mx_quantize(x, codes, scales, stream=None):
 def moe_mx_dequantize(codes, scales, out, stream=None):
     """MXFP4 codes and scales to the rows of out (bf16 or fp32 [rows, cols])."""
     c = _Call(out, "out")
-    p, dt, rows, cols, stride = _mx_rows(c, out, "out")
+    p, dt, rows, cols, stride = _mx_rows(out, "out")
     c.run(load_library().moe_mx_dequantize, c.t(codes, "codes", torch.uint8, rows * cols // 2),
           c.t(scales, "scales", torch.uint8, rows * cols // 32), rows, cols, dt, p, stride, stream=stream)
 
 
 def moe_mx_workspace_size(desc: MxDesc) -> int:
     n = ctypes.c_size_t(0)
-    _check(load_library().moe_mx_workspace_size(ctypes.byref(desc.to_c()), ctypes.byref(n)))
+    _check(load_library().moe_mx_workspace_size(desc.ref(), ctypes.byref(n)))
     return n.value
 
 
@@ -723,7 +749,7 @@ def moe_mx_dispatch(desc: MxDesc, routing: Routing, workspace=None, stream=None)
                  offsets=c.t(routing.offsets, "routing.offsets", i32, E + 1),
                  dest=c.t(routing.dest, "routing.dest", i32, A), src=c.t(routing.src, "routing.src", i32, A))
     ws, nb = c.ws(workspace, lambda: moe_mx_workspace_size(desc))
-    c.run(load_library().moe_mx_dispatch, ctypes.byref(desc.to_c()), ctypes.byref(r), ws, nb, stream=stream)
+    c.run(load_library().moe_mx_dispatch, desc.ref(), ctypes.byref(r), ws, nb, stream=stream)
 
 
 def moe_mx_ffn_up(desc: MxDesc, x, offsets, weights: MxWeights, h, src=None, workspace=None, stream=None):
@@ -732,7 +758,7 @@ def moe_mx_ffn_up(desc: MxDesc, x, offsets, weights: MxWeights, h, src=None, wor
     c = _Call(x, "x")
     R, bf = desc.tokens * desc.top_k, torch.bfloat16
     ws, nb = c.ws(workspace, lambda: moe_mx_workspace_size(desc))
-    c.run(load_library().moe_mx_ffn_up, ctypes.byref(desc.to_c()),
+    c.run(load_library().moe_mx_ffn_up, desc.ref(),
           c.t(x, "x", bf, (desc.tokens if src is not None else R) * desc.d_model), c.t(src, "src", torch.int32, R),
           c.t(offsets, "offsets", torch.int32, desc.n_experts + 1),
           ctypes.byref(_mx_weights(c, desc, weights, True, False)), c.t(h, "h", bf, R * desc.d_ff), ws, nb,
@@ -744,7 +770,7 @@ def moe_mx_ffn_down(desc: MxDesc, h, offsets, weights: MxWeights, o, workspace=N
     c = _Call(h, "h")
     R = desc.tokens * desc.top_k
     ws, nb = c.ws(workspace, lambda: moe_mx_workspace_size(desc))
-    c.run(load_library().moe_mx_ffn_down, ctypes.byref(desc.to_c()), c.t(h, "h", torch.bfloat16, R * desc.d_ff),
+    c.run(load_library().moe_mx_ffn_down, desc.ref(), c.t(h, "h", torch.bfloat16, R * desc.d_ff),
           c.t(offsets, "offsets", torch.int32, desc.n_experts + 1),
           ctypes.byref(_mx_weights(c, desc, weights, False, True)),
           c.t(o, "o", torch.float32, R * desc.d_model), ws, nb, stream=stream)
@@ -758,7 +784,7 @@ def moe_mx_forward(route: ScoreDesc, desc: MxDesc, x, w_router, weights: MxWeigh
     T, D, E, bf, f32 = desc.tokens, desc.d_model, desc.n_experts, torch.bfloat16, torch.float32
     ws, nb = c.ws(workspace, lambda: moe_mx_workspace_size(desc) + moe_score_workspace_size(route))
     out = ctypes.byref(_score_out(c, route, routing)) if routing is not None else None
-    c.run(load_library().moe_mx_forward, ctypes.byref(route.to_c()), ctypes.byref(desc.to_c()),
+    c.run(load_library().moe_mx_forward, route.ref(), desc.ref(),
           c.t(x, "x", bf, T * D), c.t(w_router, "w_router", bf, E * D), c.t(b_router, "b_router", f32, E),
           c.t(b_select, "b_select", f32, E), ctypes.byref(_mx_weights(c, desc, weights, True, True)),
           c.t(y, "y", f32, T * D), out, ws, nb, stream=stream)
