@@ -225,82 +225,196 @@ __global__ __launch_bounds__(256) void score_db_kernel(const double* __restrict_
   if (lane == 0) d_b[e] = (float)p;
 }
 
+// Two neighbouring fp32 values to one word of each of TERMS bf16 fragments.
+template <int TERMS>
+__device__ __forceinline__ void split_pair(float u, float v, uint32_t (&out)[TERMS]) {
+#pragma unroll
+  for (int q = 0; q < TERMS; ++q) {
+    out[q] = pack_bf16x2(u, v);
+    u -= __uint_as_float(out[q] << 16);
+    v -= __uint_as_float(out[q] & 0xffff0000u);
+  }
+}
+
+// The MFMA wants 8 values along k per lane from both operands.  The products' B (W_r by
+// expert, x by token) has its rows along n, so a lane reads the pair of neighbouring columns
+// 2l, 2l + 1 from 8 rows (a row's 32 pairs are 128 contiguous bytes) and splits the words into
+// two fragments, even and odd columns.  As the first operand they make a lane's accumulators,
+// even and odd together, 8 neighbouring columns of one row: column 16 g + 8 fc of 64.
+__device__ __forceinline__ uint32_t even_pair(uint32_t w0, uint32_t w1) {
+  return __builtin_amdgcn_perm(w1, w0, 0x05040100);
+}
+__device__ __forceinline__ uint32_t odd_pair(uint32_t w0, uint32_t w1) {
+  return __builtin_amdgcn_perm(w1, w0, 0x07060302);
+}
+__device__ __forceinline__ void columns8(const f32x16& u, const f32x16& v, int g, f32x4& lo, f32x4& hi) {
+  lo = f32x4{u[4 * g], v[4 * g], u[4 * g + 1], v[4 * g + 1]};
+  hi = f32x4{u[4 * g + 2], v[4 * g + 2], u[4 * g + 3], v[4 * g + 3]};
+}
+
 // ---------------------------------------------------------------------------
-// out[m][n] = sum_k A[m][k] B[k][n], A fp32 along k and multiplied as a sum of TERMS bf16
-// terms, B bf16 with its rows along n (d_x: A = dl by token, B = W_r; d_W: A = dl by expert, B = x, one slice of the
-// tokens per blockIdx.z).  Block 64 MT rows x 256 columns, k in steps of 32 through four LDS
-// stages.  Eight waves, two per SIMD: waves 0-3 (2 x 2 over the tile) multiply the first 16 k
-// of each step, waves 4-7 the second, so one wave's LDS reads run under the other's MFMAs;
-// at the end each half finishes one half of the columns with the other's sums.
-//
-// The MFMA wants 8 values along k per lane from both operands.  A has them in a row; of B a
-// lane reads the pair of neighbouring columns 2l, 2l + 1 from 8 rows (4 bytes each, a row's
-// 32 pairs are 128 contiguous bytes) and splits the words into two fragments, even and odd
-// columns.  As the first operand they make a lane's accumulators, even and odd together, 8
-// neighbouring columns of one row: stores of 16 bytes (bf16) or 32 (fp32).
+// d_x[t] = dl[t] W_r.  k is the experts, at most 256, so W_r stays in registers: a wave has 64
+// columns of it for every expert (NE / 2 registers), a block of eight 512, and tiles of 32
+// tokens stream past.  The block splits a tile of dl into its two bf16 terms once, into LDS
+// (rows of 2 NE bytes per term, 16 B chunks at chunk ^ (row & 7)), two tiles in turn with one
+// barrier each; the next tile's dl is on its way meanwhile.
+// ---------------------------------------------------------------------------
+constexpr int kDxCols = 512, kDxRows = 32;
+
+template <int NE>
+__global__ __launch_bounds__(512, 2) void score_dx_bf16_kernel(const float* __restrict__ dl, int pitch,
+                                                               const uint16_t* __restrict__ w, int T, int d,
+                                                               int E, int groups, uint16_t* __restrict__ d_x) {
+  constexpr int kTerm = kDxRows * NE * 2, kChunks = NE / 8, kUnits = kDxRows * kChunks;
+  constexpr int kPer = (kUnits + 511) / 512;           // chunks of 8 values per thread
+  constexpr int kSlices = NE / 16;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * 2 * kTerm];
+  const int lane = threadIdx.x & 63, fr = lane & 31, fc = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int group = blockIdx.x % groups, c0 = (blockIdx.x / groups) * kDxCols + wave * 64;
+  const int tiles = (T + kDxRows - 1) / kDxRows;
+  const bool active = c0 < d;                          // d is a multiple of 128
+
+  u32x4 b[kSlices][2];
+  {
+    const uint16_t* col = w + (active ? c0 : 0) + 2 * fr;
+#pragma unroll
+    for (int s = 0; s < kSlices; ++s) {
+      uint32_t v[8];
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        const int e = s * 16 + fc * 8 + j;
+        v[j] = *reinterpret_cast<const uint32_t*>(col + (size_t)min(e, E - 1) * d);
+        v[j] = e < E ? v[j] : 0u;
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) b[s][0][j] = even_pair(v[2 * j], v[2 * j + 1]), b[s][1][j] = odd_pair(v[2 * j], v[2 * j + 1]);
+    }
+  }
+
+  f32x4 next[kPer][2];
+  auto fetch = [&](int tile) {                         // dl has whole tiles of rows
+    const float* row = dl + (size_t)min(tile, tiles - 1) * kDxRows * pitch;
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int u = i * 512 + (int)threadIdx.x, r = u / kChunks, c = u % kChunks;
+      next[i][0] = next[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
+      if (u < kUnits && c * 8 < pitch) {               // pitch: E up to 32, zeros behind E
+        next[i][0] = *reinterpret_cast<const f32x4*>(row + (size_t)r * pitch + c * 8);
+        next[i][1] = *reinterpret_cast<const f32x4*>(row + (size_t)r * pitch + c * 8 + 4);
+      }
+    }
+  };
+  auto put = [&](int buffer) {
+#pragma unroll
+    for (int i = 0; i < kPer; ++i) {
+      const int u = i * 512 + (int)threadIdx.x, r = u / kChunks, c = u % kChunks;
+      if (u >= kUnits) continue;
+      u32x4 q[2];
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        const f32x4 f = next[i][j >> 1];
+        uint32_t o[2];
+        split_pair<2>(f[2 * (j & 1)], f[2 * (j & 1) + 1], o);
+        q[0][j] = o[0], q[1][j] = o[1];
+      }
+      uint8_t* at = lds + buffer * 2 * kTerm + r * NE * 2 + ((c ^ (r & 7)) << 4);
+      *reinterpret_cast<u32x4*>(at) = q[0];
+      *reinterpret_cast<u32x4*>(at + kTerm) = q[1];
+    }
+  };
+  fetch(group);
+  put(0);
+  fetch(group + groups);
+  __syncthreads();
+  int buffer = 0;
+  for (int tile = group; tile < tiles; tile += groups, buffer ^= 1) {
+    put(buffer ^ 1);
+    fetch(tile + 2 * groups);
+    f32x16 acc[2];
+#pragma unroll
+    for (int n = 0; n < 2; ++n)
+#pragma unroll
+      for (int q = 0; q < 16; ++q) acc[n][q] = 0.f;
+    const uint8_t* base = lds + buffer * 2 * kTerm + fr * NE * 2;
+#pragma unroll
+    for (int s = 0; s < kSlices; ++s) {
+      const uint32_t at = ((2 * s + fc) ^ (fr & 7)) << 4;
+      const u32x4 hi = ld16(base + at), mid = ld16(base + kTerm + at);
+#pragma unroll
+      for (int n = 0; n < 2; ++n) acc[n] = mfma32_bf16(b[s][n], mid, acc[n]);
+#pragma unroll
+      for (int n = 0; n < 2; ++n) acc[n] = mfma32_bf16(b[s][n], hi, acc[n]);
+    }
+    const int t = tile * kDxRows + fr;
+    if (active && t < T) {
+      uint16_t* o = d_x + (size_t)t * d + c0 + 8 * fc;
+#pragma unroll
+      for (int g = 0; g < 4; ++g) {
+        f32x4 lo, hi;
+        columns8(acc[0], acc[1], g, lo, hi);
+        st16(o + 16 * g, u32x4{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]),
+                               pack_bf16x2(hi[0], hi[1]), pack_bf16x2(hi[2], hi[3])});
+      }
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// d_W[e][c] = sum_t dl[t][e] x[t][c]: A = dl by expert, fp32 along k and multiplied as three
+// bf16 terms, B = x, one slice of the tokens per block.  Block 64 MT experts x 256 columns, k in
+// steps of 32 through four LDS stages, four waves as 2 x 2, one per SIMD.  All work but the
+// MFMAs runs in their shadow: while a slice of 16 k is multiplied, the next one's fragments
+// are made from words in registers, the words of the one after are read from LDS, and the
+// loads of four steps ahead are issued.  One barrier per step.
 //
 // LDS: A rows of 128 B, 16 B chunks at chunk ^ ((row >> 1) & 7); B rows of 512 B, their 128 B
 // quarters at quarter ^ ((row >> 3) & 1) so that the two lane halves (rows 8 apart) read
 // different banks.
 // ---------------------------------------------------------------------------
-// Eight fp32 values (two registers' worth of 16 B) to TERMS bf16 fragments.
-template <int TERMS>
-__device__ __forceinline__ void split_terms(f32x4 lo, f32x4 hi, u32x4 (&out)[TERMS]) {
-#pragma unroll
-  for (int j = 0; j < 4; ++j) {
-    float u = j < 2 ? lo[2 * j] : hi[2 * j - 4], v = j < 2 ? lo[2 * j + 1] : hi[2 * j - 3];
-#pragma unroll
-    for (int q = 0; q < TERMS; ++q) {
-      const uint32_t w = pack_bf16x2(u, v);
-      out[q][j] = w;
-      u -= __uint_as_float(w << 16);
-      v -= __uint_as_float(w & 0xffff0000u);
-    }
-  }
-}
-
-template <int TERMS, int MT, bool OUT_BF16>
-__global__ __launch_bounds__(512, 1) void score_grad_gemm_kernel(
-    const float* __restrict__ A, int a_pitch, const uint16_t* __restrict__ B, int b_rows,
-    int d, int M, int K, int slices, void* __restrict__ out) {
-  constexpr int S = 4, kRows = 64 * MT;
+template <int MT>
+__global__ __launch_bounds__(256, 1) void score_dw_bf16_kernel(
+    const float* __restrict__ A, int a_pitch, const uint16_t* __restrict__ B, int T, int d, int E,
+    int slices, float* __restrict__ out) {
+  constexpr int S = 4, TERMS = 3, kRows = 64 * MT;
   constexpr int kA = kRows * 128, kStage = kA + kGradK * 512;
-  constexpr int kAI = kA / 8192, kBI = 2, L = kAI + kBI;   // 1 KB loads per wave and step
-  constexpr int kSwap = 8 * MT * 32 * 68 * 4;          // one wave's 32 MT rows x 64 columns, padded
-  constexpr int kLds = S * kStage > kSwap ? S * kStage : kSwap;
-  static_assert(kLds <= 160 * 1024, "load plan");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[kLds];
-  const int lane = threadIdx.x & 63;
-  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6), half = wave >> 2;
-  const int wm = (wave >> 1) & 1, wn = wave & 1, fr = lane & 31, fc = lane >> 5;
-  const int m0 = blockIdx.y * kRows, n0 = blockIdx.x * kGradCols, sl = blockIdx.z;
-  const int steps = (K + kGradK - 1) / kGradK;
+  constexpr int kAI = kA / 4096, kBI = 4, L = kAI + kBI;   // 1 KB loads per wave and step
+  constexpr int kM = TERMS * 4 * MT;                   // MFMAs per slice
+  static_assert(S * kStage <= 160 * 1024, "load plan");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[S * kStage];
+  const int lane = threadIdx.x & 63, fr = lane & 31, fc = lane >> 5;
+  const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int wm = wave >> 1, wn = wave & 1;
+  // Slices fastest: with 8 of them the blocks of an XCD share one's dl and x in its L2.
+  const int sl = blockIdx.x, n0 = blockIdx.y * kGradCols, m0 = blockIdx.z * kRows;
+  const int steps = (T + kGradK - 1) / kGradK;
   const int s0 = (int)((long)sl * steps / slices), nk = (int)((long)(sl + 1) * steps / slices) - s0;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
 
-  // A: load i of wave w fills rows 8 (8 i + w) + lane / 8.
+  // A: load i of wave w fills rows 8 (4 i + w) + lane / 8.
   const float* a_base = A + (size_t)m0 * a_pitch + (size_t)s0 * kGradK;
   uint32_t a_off[kAI];
 #pragma unroll
   for (int i = 0; i < kAI; ++i) {
-    const int row = (i * 8 + wave) * 8 + (lane >> 3);
+    const int row = (i * 4 + wave) * 8 + (lane >> 3);
     a_off[i] = (uint32_t)row * (uint32_t)a_pitch * 4u + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
   }
-  // B: load i of wave w fills rows 2 (8 i + w) + lane / 32; rows past the last repeat it (A is
+  // B: load i of wave w fills rows 2 (4 i + w) + lane / 32; rows past the last repeat it (A is
   // 0 there), columns past d wrap to the tile's first half (not stored).
   const uint8_t* b_tile = reinterpret_cast<const uint8_t*>(B + (size_t)s0 * kGradK * d + n0);
   auto load = [&](int i, int step, int stage) {
     const uint32_t base = lds0 + stage * kStage;
     const int s = min(step, nk - 1);
     if (i < kAI) {
-      dma16(a_base + (size_t)s * kGradK, a_off[i < kAI ? i : 0], base + (i * 8 + wave) * 1024);
+      dma16(a_base + (size_t)s * kGradK, a_off[i < kAI ? i : 0], base + (i * 4 + wave) * 1024);
     } else {
-      const int j = i - kAI, r = 2 * (j * 8 + wave) + (lane >> 5);
+      const int j = i - kAI, r = 2 * (j * 4 + wave) + (lane >> 5);
       int c = (lane & 31) ^ (((r >> 3) & 1) << 3);
       if (n0 + c * 8 >= d) c -= 16;
-      const int row = min(r, b_rows - 1 - (s0 + s) * kGradK);
+      const int row = min(r, T - 1 - (s0 + s) * kGradK);
       dma16(b_tile + (size_t)s * kGradK * d * 2, (uint32_t)(row * d + c * 8) * 2u,
-            base + kA + (j * 8 + wave) * 1024);
+            base + kA + (j * 4 + wave) * 1024);
     }
   };
 
@@ -311,119 +425,102 @@ __global__ __launch_bounds__(512, 1) void score_grad_gemm_kernel(
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[n][m][q] = 0.f;
-  // k 16 half + 8 fc .. + 7: chunks 4 half + 2 fc and the next.
-  const uint32_t a_lane = (wm * MT * 32 + fr) * 128 + (((4 * half + 2 * fc) ^ ((fr >> 1) & 7)) << 4);
-  const uint32_t b_lane = kA + (16 * half + 8 * fc) * 512 + fr * 4;
-  f32x4 lo[MT], hi[MT];
-  uint32_t w[2][8];
-  u32x4 xa[MT][TERMS], b[4];
-  auto read = [&](int stage) {
-    const uint8_t* base = lds + stage * kStage;
-#pragma unroll
-    for (int m = 0; m < MT; ++m) {
-      lo[m] = __builtin_bit_cast(f32x4, ld16(base + a_lane + m * 4096));
-      hi[m] = __builtin_bit_cast(f32x4, ld16(base + (a_lane ^ 16) + m * 4096));
-    }
-#pragma unroll
-    for (int n = 0; n < 2; ++n) {
-      const uint32_t quarter = ((wn * 2 + n) ^ fc) * 128;    // row 16 half + 8 fc + j
-#pragma unroll
-      for (int j = 0; j < 8; ++j) w[n][j] = *reinterpret_cast<const uint32_t*>(base + b_lane + quarter + j * 512);
-    }
+  const uint32_t a_lane = (wm * MT * 32 + fr) * 128, a_swz = (fr >> 1) & 7;
+  const uint32_t b_lane = kA + 8 * fc * 512 + fr * 4;
+  f32x4 raw[MT][2];                                    // dl, 8 values along k
+  uint32_t pairs[2][8];                                // x, 8 rows of a pair of columns
+  u32x4 xa[2][MT][TERMS], b[2][4];
+  // Slice h of a stage: k 16 h + 8 fc .. + 7.
+  auto read_a = [&](int stage, int h, int m) {
+    const uint8_t* row = lds + stage * kStage + a_lane + m * 4096;
+    raw[m][0] = __builtin_bit_cast(f32x4, ld16(row + (((4 * h + 2 * fc) ^ a_swz) << 4)));
+    raw[m][1] = __builtin_bit_cast(f32x4, ld16(row + (((4 * h + 2 * fc + 1) ^ a_swz) << 4)));
   };
-  auto fragments = [&]() {
-#pragma unroll
-    for (int n = 0; n < 2; ++n)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        b[2 * n][j] = __builtin_amdgcn_perm(w[n][2 * j + 1], w[n][2 * j], 0x05040100);
-        b[2 * n + 1][j] = __builtin_amdgcn_perm(w[n][2 * j + 1], w[n][2 * j], 0x07060302);
-      }
-#pragma unroll
-    for (int m = 0; m < MT; ++m) split_terms<TERMS>(lo[m], hi[m], xa[m]);
+  auto read_b = [&](int stage, int h, int i) {         // i: 8 rows of two column groups
+    const int n = i / 8, j = i % 8;
+    pairs[n][j] = *reinterpret_cast<const uint32_t*>(lds + stage * kStage + b_lane + (16 * h + j) * 512 +
+                                                     ((wn * 2 + n) ^ fc) * 128);
   };
-  // Step t's words are in registers when it starts; step t + 1's are read, and step t + S's
-  // loads issued, under its MFMAs.  The two waves of a SIMD make their fragments at
-  // different ends of the step, so one's VALU work runs under the other's MFMAs.
+  auto make_a = [&](u32x4 (&to)[MT][TERMS], int i) {
+    const int m = i / 4, j = i % 4;
+    uint32_t o[TERMS];
+    split_pair<TERMS>(raw[m][j >> 1][2 * (j & 1)], raw[m][j >> 1][2 * (j & 1) + 1], o);
+#pragma unroll
+    for (int q = 0; q < TERMS; ++q) to[m][q][j] = o[q];
+  };
+  auto make_b = [&](u32x4 (&to)[4], int i) {
+    const int n = i / 4, j = i % 4;
+    to[2 * n][j] = even_pair(pairs[n][2 * j], pairs[n][2 * j + 1]);
+    to[2 * n + 1][j] = odd_pair(pairs[n][2 * j], pairs[n][2 * j + 1]);
+  };
+
 #pragma unroll
   for (int s = 0; s < S; ++s)
 #pragma unroll
     for (int i = 0; i < L; ++i) load(i, s, s);
   __builtin_amdgcn_s_waitcnt(wait_vm((S - 1) * L));
   __syncthreads();
-  read(0);
-  if (half == 1) fragments();
+#pragma unroll
+  for (int h = 0; h < 2; ++h) {                        // slice 0 as fragments, slice 1 as words
+#pragma unroll
+    for (int m = 0; m < MT; ++m) read_a(0, h, m);
+#pragma unroll
+    for (int i = 0; i < 16; ++i) read_b(0, h, i);
+    if (h == 0) {
+#pragma unroll
+      for (int i = 0; i < 4 * MT; ++i) make_a(xa[0], i);
+#pragma unroll
+      for (int i = 0; i < 8; ++i) make_b(b[0], i);
+    }
+  }
   int st = 0;
   for (int t = 0; t < nk; ++t) {
     const int st1 = st == S - 1 ? 0 : st + 1;
     __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0((S - 2) * L));    // step t + 1 landed, step t read
     __syncthreads();
-    if (half == 0) fragments();
-    read(st1);
-    __builtin_amdgcn_sched_barrier(0);
-    constexpr int kM = TERMS * 4 * MT;                 // small terms first
 #pragma unroll
-    for (int i = 0; i < kM; ++i) {
-      const int q = TERMS - 1 - i / (4 * MT), n = i / MT % 4, m = i % MT;
-      acc[n][m] = mfma32_bf16(b[n], xa[m][q], acc[n][m]);
+    for (int h = 0; h < 2; ++h) {
+      // First third: the next slice's dl; second: its x, and the dl words of the one after;
+      // last: their x words.
 #pragma unroll
-      for (int j = i * L / kM; j < (i + 1) * L / kM; ++j) load(j, t + S, st);
-      __builtin_amdgcn_sched_barrier(0);
+      for (int i = 0; i < kM; ++i) {                   // small terms first
+        constexpr int kThird = kM / 3;
+        const int q = TERMS - 1 - i / (4 * MT), n = i / MT % 4, m = i % MT, j = i % kThird;
+        acc[n][m] = mfma32_bf16(b[h][n], xa[h][m][q], acc[n][m]);
+        if (i < kThird) {
+#pragma unroll
+          for (int u = j * 4 * MT / kThird; u < (j + 1) * 4 * MT / kThird; ++u) make_a(xa[h ^ 1], u);
+        } else if (i < 2 * kThird) {
+#pragma unroll
+          for (int u = j * 8 / kThird; u < (j + 1) * 8 / kThird; ++u) make_b(b[h ^ 1], u);
+          if (j < MT) read_a(st1, h, j);
+        } else {
+#pragma unroll
+          for (int u = j * 16 / kThird; u < (j + 1) * 16 / kThird; ++u) read_b(st1, h, u);
+        }
+        const int at = h * kM + i;
+#pragma unroll
+        for (int u = at * L / (2 * kM); u < (at + 1) * L / (2 * kM); ++u) load(u, t + S, st);
+        __builtin_amdgcn_sched_barrier(0);
+      }
     }
-    if (half == 1) fragments();
     st = st1;
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");     // no load outlives its LDS
-  __syncthreads();
-
-  // Lane: row m * 32 + fr; accumulator 4 g + q of group 2 n (+ 1) is column
-  // n * 64 + 2 (8 g + 4 fc + q) (+ 1).  Half h keeps n = h and hands over the other.
-  float* swap = reinterpret_cast<float*>(lds);
-  auto cols8 = [&](int n, int m, int g, f32x4& lo, f32x4& hi) {
-    const f32x16 &u = acc[2 * n][m], &v = acc[2 * n + 1][m];
-    lo = f32x4{u[4 * g], v[4 * g], u[4 * g + 1], v[4 * g + 1]};
-    hi = f32x4{u[4 * g + 2], v[4 * g + 2], u[4 * g + 3], v[4 * g + 3]};
-  };
 #pragma unroll
   for (int n = 0; n < 2; ++n)
-    if (n != half) {
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
+    for (int m = 0; m < MT; ++m) {
+      const int r = m0 + (wm * MT + m) * 32 + fr;
 #pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          f32x4 lo, hi;
-          cols8(n, m, g, lo, hi);
-          float* at = swap + ((wave * MT + m) * 32 + fr) * 68 + 16 * g + 8 * fc;
-          *reinterpret_cast<f32x4*>(at) = lo;
-          *reinterpret_cast<f32x4*>(at + 4) = hi;
-        }
-    }
-  __syncthreads();
-#pragma unroll
-  for (int n = 0; n < 2; ++n)
-    if (n == half) {
-#pragma unroll
-      for (int m = 0; m < MT; ++m) {
-        const int r = m0 + (wm * MT + m) * 32 + fr;
-#pragma unroll
-        for (int g = 0; g < 4; ++g) {
-          const int col = n0 + wn * 128 + n * 64 + 16 * g + 8 * fc;
-          f32x4 lo, hi;
-          cols8(n, m, g, lo, hi);
-          const float* at = swap + (((wave ^ 4) * MT + m) * 32 + fr) * 68 + 16 * g + 8 * fc;
-          lo += *reinterpret_cast<const f32x4*>(at);
-          hi += *reinterpret_cast<const f32x4*>(at + 4);
-          if (r >= M || col >= d) continue;
-          if constexpr (OUT_BF16) {
-            st16(static_cast<uint16_t*>(out) + (size_t)r * d + col,
-                 u32x4{pack_bf16x2(lo[0], lo[1]), pack_bf16x2(lo[2], lo[3]), pack_bf16x2(hi[0], hi[1]),
-                       pack_bf16x2(hi[2], hi[3])});
-          } else {
-            float* o = static_cast<float*>(out) + ((size_t)sl * M + r) * d + col;
-            *reinterpret_cast<f32x4*>(o) = lo;
-            *reinterpret_cast<f32x4*>(o + 4) = hi;
-          }
-        }
+      for (int g = 0; g < 4; ++g) {
+        const int col = n0 + wn * 128 + n * 64 + 16 * g + 8 * fc;
+        f32x4 lo, hi;
+        columns8(acc[2 * n][m], acc[2 * n + 1][m], g, lo, hi);
+        if (r >= E || col >= d) continue;
+        float* o = out + ((size_t)sl * E + r) * d + col;
+        *reinterpret_cast<f32x4*>(o) = lo;
+        *reinterpret_cast<f32x4*>(o + 4) = hi;
       }
     }
 }
@@ -512,24 +609,34 @@ static void products_f32(const ScoreGradArgs& a, hipStream_t s) {
   }
 }
 
+template <int NE>
+static void launch_dx(const ScoreGradArgs& a, hipStream_t s) {
+  const ScoreShape& h = a.sh;
+  const int cols = (h.d + kDxCols - 1) / kDxCols, tiles = (h.T + kDxRows - 1) / kDxRows;
+  const int groups = std::min(std::max(1, 256 / cols), tiles);   // one block per CU
+  score_dx_bf16_kernel<NE><<<cols * groups, 512, 0, s>>>(
+      a.dl, dl_space(h).Ek, static_cast<const uint16_t*>(a.w), h.T, h.d, h.E, groups, static_cast<uint16_t*>(a.d_x));
+}
+
 static void products_bf16(const ScoreGradArgs& a, hipStream_t s) {
   const ScoreShape& h = a.sh;
   const DlSpace t = dl_space(h);
-  const int cols = (h.d + kGradCols - 1) / kGradCols;
-  if (a.d_x)
-    score_grad_gemm_kernel<2, 2, true><<<dim3(cols, (h.T + 127) / 128, 1), 512, 0, s>>>(
-        a.dl, t.Ek, static_cast<const uint16_t*>(a.w), h.E, h.d, h.T, h.E, 1, a.d_x);
+  if (a.d_x) {
+    if (h.E <= 64) launch_dx<64>(a, s);
+    else if (h.E <= 128) launch_dx<128>(a, s);
+    else if (h.E <= 192) launch_dx<192>(a, s);
+    else launch_dx<256>(a, s);
+  }
   if (a.d_w) {
-    const int slices = score_grad_slices(h);
+    const int slices = score_grad_slices(h), cols = (h.d + kGradCols - 1) / kGradCols;
     float* out = slices > 1 ? a.pw : a.d_w;
     const float* by_expert = a.dl + t.by_expert;
     const uint16_t* x = static_cast<const uint16_t*>(a.x);
     if (h.E <= 64)
-      score_grad_gemm_kernel<3, 1, false><<<dim3(cols, 1, slices), 512, 0, s>>>(
-          by_expert, t.Tk, x, h.T, h.d, h.E, h.T, slices, out);
+      score_dw_bf16_kernel<1><<<dim3(slices, cols, 1), 256, 0, s>>>(by_expert, t.Tk, x, h.T, h.d, h.E, slices, out);
     else
-      score_grad_gemm_kernel<3, 2, false><<<dim3(cols, (h.E + 127) / 128, slices), 512, 0, s>>>(
-          by_expert, t.Tk, x, h.T, h.d, h.E, h.T, slices, out);
+      score_dw_bf16_kernel<2><<<dim3(slices, cols, (h.E + 127) / 128), 256, 0, s>>>(by_expert, t.Tk, x, h.T, h.d, h.E,
+                                                                                 slices, out);
     if (slices > 1) sum_slices(a, slices, s);
   }
 }
