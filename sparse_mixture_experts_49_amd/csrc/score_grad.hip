@@ -10,9 +10,8 @@
 //
 // bf16 layers: x and W_r go to the bf16 MFMA as they are and dl as a sum of bf16 terms,
 // dl = hi + mid (+ lo): two keep 17 bits, enough under d_x's rounding to bf16, three keep
-// all of fp32's for the fp32 d_W.  dl itself is kept in fp32, by token for d_x and by expert
-// for d_W, so both products read it along their k and split it in registers (written out as
-// terms it is half as many bytes again and, by 64-byte rows, three times the cache lines).
+// all of fp32's for the fp32 d_W.  dl itself is kept in fp32 and split where it is multiplied
+// (written out as terms it is half as many bytes again and more cache lines).
 #include <algorithm>
 #include <type_traits>
 
@@ -21,7 +20,7 @@
 
 namespace moe {
 
-static int up_to(int v, int m) { return (v + m - 1) / m * m; }
+__host__ __device__ static int up_to(int v, int m) { return (v + m - 1) / m * m; }
 
 // Column blocks of the products: 256 columns of d each.
 constexpr int kGradCols = 256, kGradRows = 128, kGradK = 32;
@@ -46,32 +45,17 @@ static int grad_blocks(int T) {
   return std::min(256, (T + tile - 1) / tile);
 }
 
-// Workspace of the logit gradients: by token [T'][Ek] and, for bf16 layers, by expert
-// [E'][Tk], fp32; rows padded with zeros to whole k steps (T', E': up to whole tiles, not
-// written).
-struct DlSpace {
-  int Ek, Tk;
-  size_t by_expert, total;             // elements
-};
-static DlSpace dl_space(const ScoreShape& s) {
-  DlSpace t{};
-  t.Ek = up_to(s.E, kGradK);
-  t.Tk = up_to(s.T, 64);
-  t.by_expert = (size_t)up_to(s.T, kGradRows) * t.Ek;
-  t.total = t.by_expert + (s.bf16 ? (size_t)up_to(s.E, kGradRows) * t.Tk : 0);
-  return t;
-}
+// Workspace of the logit gradients: fp32 [T up to 32][E up to whole tiles of the d_W product],
+// zeros behind T and E.
+static int dl_pitch(int E) { return E <= 64 ? 64 : up_to(E, kGradRows); }
 
-size_t score_dl_bytes(const ScoreShape& s) { return dl_space(s).total * 4; }
+size_t score_dl_bytes(const ScoreShape& s) { return (size_t)up_to(s.T, kGradK) * dl_pitch(s.E) * 4; }
 int score_grad_sum_blocks(int T) { return grad_blocks(T); }
 
-// dl of tiles of TT tokens, a wave four of them, lane l the experts l, l + 64, ...; bf16
-// layers put the tile through LDS to write it along the other axis too.
-template <int PER, int TT, bool BF16>
-__global__ __launch_bounds__(TT * 16) void score_dlogits_kernel(ScoreGradArgs a, int Ek, int Tk,
-                                                                size_t by_expert) {
-  constexpr int kPitch = 64 * PER + 1, WAVES = TT / 4, kThreads = TT * 16;   // four tokens a wave
-  __shared__ float tile[BF16 ? TT * kPitch : 1];
+// dl of tiles of TT tokens, a wave four of them, lane l the experts l, l + 64, ...
+template <int PER, int TT>
+__global__ __launch_bounds__(TT * 16) void score_dlogits_kernel(ScoreGradArgs a, int pitch) {
+  constexpr int WAVES = TT / 4, kThreads = TT * 16;    // four tokens a wave
   __shared__ double sum_b[WAVES][64 * PER];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -87,114 +71,93 @@ __global__ __launch_bounds__(TT * 16) void score_dlogits_kernel(ScoreGradArgs a,
     pb[j] = 0.0;
   }
   for (int t0 = blockIdx.x * TT; t0 < T; t0 += gridDim.x * TT) {
-    for (int i = wave; i < TT; i += WAVES) {
-      const int t = t0 + i;
-      float dl[PER];
+    for (int t = t0 + wave; t < min(t0 + TT, T); t += WAVES) {
+      float l[PER], p[PER], s[PER];
 #pragma unroll
-      for (int j = 0; j < PER; ++j) dl[j] = 0.f;
-      if (t < T) {
-        float l[PER], p[PER], s[PER];
+      for (int j = 0; j < PER; ++j) l[j] = a.logits[(size_t)t * E + min(j * 64 + lane, E - 1)];
+      const int my_idx = a.topk_idx[(size_t)t * k + min(lane, k - 1)];
+      const float my_g = a.d_topk_w ? a.d_topk_w[(size_t)t * k + min(lane, k - 1)] : 0.f;
+      float m = -INFINITY, tot = 0.f;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) l[j] = a.logits[(size_t)t * E + min(j * 64 + lane, E - 1)];
-        const int my_idx = a.topk_idx[(size_t)t * k + min(lane, k - 1)];
-        const float my_g = a.d_topk_w ? a.d_topk_w[(size_t)t * k + min(lane, k - 1)] : 0.f;
-        float m = -INFINITY, tot = 0.f;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          l[j] = j * 64 + lane < E ? l[j] : -INFINITY;
-          m = fmaxf(m, l[j]);
-        }
-        if (soft) {
-          m = wave_max_f(m);
-          m = m == -INFINITY ? 0.f : m;
-#pragma unroll
-          for (int j = 0; j < PER; ++j) tot += p[j] = exp_f32(l[j] - m);
-          tot = wave_sum_f(tot);
-          const float r_tot = tot > 0.f ? 1.f / tot : tot != tot ? tot : 0.f;
-#pragma unroll
-          for (int j = 0; j < PER; ++j) p[j] *= r_tot;
-        }
-#pragma unroll
-        for (int j = 0; j < PER; ++j) s[j] = a.sigmoid ? sigmoid_f32(l[j]) : p[j];
-        // Chosen scores and the gradients of the raw weights.
-        int idx[8];
-        float g[8], S = 1e-20f, gw = 0.f;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) {
-          idx[q] = q < k ? __builtin_amdgcn_readlane(my_idx, q) : -1;
-          idx[q] = (uint32_t)idx[q] < (uint32_t)E ? idx[q] : -1;
-          g[q] = idx[q] >= 0 ? __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(my_g), q)) : 0.f;
-          float r = 0.f;
-#pragma unroll
-          for (int j = 0; j < PER; ++j) {
-            const float v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(s[j]), idx[q] & 63));
-            r = idx[q] >> 6 == j ? v : r;              // idx -1: none
-          }
-          S += r;
-          gw = fmaf(g[q], r, gw);
-        }
-        const float rS = 1.f / S;
-#pragma unroll
-        for (int q = 0; q < 8; ++q) g[q] = a.renorm ? a.scale * (g[q] - gw * rS) * rS : a.scale * g[q];
-        float ds[PER];
-        float cs = 0.f, cq = 0.f, ss = 0.f;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          float dr = 0.f;
-#pragma unroll
-          for (int q = 0; q < 8; ++q)
-            dr += idx[q] == j * 64 + lane ? g[q] : 0.f;
-          ds[j] = dr;
-          ss += s[j];
-          cq = fmaf(dq[j], s[j], cq);
-        }
-        if (a.sigmoid && a.d_aux) {
-          ss = wave_sum_f(ss);
-          const float rs = 1.f / (ss < 1e-20f ? 1e-20f : ss);
-          cq = wave_sum_f(cq) * rs;
-#pragma unroll
-          for (int j = 0; j < PER; ++j) ds[j] += (dq[j] - cq) * rs;
-        } else if (!a.sigmoid) {
-#pragma unroll
-          for (int j = 0; j < PER; ++j) {
-            ds[j] += dq[j];
-            cs = fmaf(ds[j], s[j], cs);
-          }
-          cs = wave_sum_f(cs);
-        }
-        const float zl = a.d_z ? z * 2.f / T * fmaf(__builtin_amdgcn_logf(tot), 0.69314718055994530942f, m) : 0.f;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          const int e = j * 64 + lane;
-          const float v = a.sigmoid ? ds[j] * s[j] * (1.f - s[j]) : s[j] * (ds[j] - cs);
-          if (e < E) {
-            dl[j] = a.d_z ? fmaf(zl, p[j], v) : v;
-            if (a.d_logits) a.d_logits[(size_t)t * E + e] = dl[j];
-            pb[j] += (double)dl[j];
-          }
-          if (e < Ek) a.dl[(size_t)t * Ek + e] = dl[j];
-        }
+      for (int j = 0; j < PER; ++j) {
+        l[j] = j * 64 + lane < E ? l[j] : -INFINITY;
+        m = fmaxf(m, l[j]);
       }
-      if constexpr (BF16)
+      if (soft) {
+        m = wave_max_f(m);
+        m = m == -INFINITY ? 0.f : m;
 #pragma unroll
-        for (int j = 0; j < PER; ++j) tile[i * kPitch + j * 64 + lane] = dl[j];
-    }
-    if constexpr (BF16) {
-      __syncthreads();
-      float* out = a.dl + by_expert + t0;
-#pragma unroll 4
-      for (int i = threadIdx.x; i < E * TT; i += kThreads) {
-        const int e = i / TT, c = i % TT;
-        out[(size_t)e * Tk + c] = tile[c * kPitch + e];
+        for (int j = 0; j < PER; ++j) tot += p[j] = exp_f32(l[j] - m);
+        tot = wave_sum_f(tot);
+        const float r_tot = tot > 0.f ? 1.f / tot : tot != tot ? tot : 0.f;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) p[j] *= r_tot;
       }
-      // The last tile also clears its rows' tail up to Tk (a k step past T).
-      if (t0 + TT >= T)
-        for (int i = threadIdx.x; i < E * (Tk - t0 - TT); i += kThreads) {
-          const int n = Tk - t0 - TT, e = i / n, c = i - e * n;
-          out[(size_t)e * Tk + TT + c] = 0.f;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) s[j] = a.sigmoid ? sigmoid_f32(l[j]) : p[j];
+      // Chosen scores and the gradients of the raw weights.
+      int idx[8];
+      float g[8], S = 1e-20f, gw = 0.f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {
+        idx[q] = q < k ? __builtin_amdgcn_readlane(my_idx, q) : -1;
+        idx[q] = (uint32_t)idx[q] < (uint32_t)E ? idx[q] : -1;
+        g[q] = idx[q] >= 0 ? __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(my_g), q)) : 0.f;
+        float r = 0.f;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+          const float v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(s[j]), idx[q] & 63));
+          r = idx[q] >> 6 == j ? v : r;              // idx -1: none
         }
-      __syncthreads();
+        S += r;
+        gw = fmaf(g[q], r, gw);
+      }
+      const float rS = 1.f / S;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) g[q] = a.renorm ? a.scale * (g[q] - gw * rS) * rS : a.scale * g[q];
+      float ds[PER];
+      float cs = 0.f, cq = 0.f, ss = 0.f;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        float dr = 0.f;
+#pragma unroll
+        for (int q = 0; q < 8; ++q)
+          dr += idx[q] == j * 64 + lane ? g[q] : 0.f;
+        ds[j] = dr;
+        ss += s[j];
+        cq = fmaf(dq[j], s[j], cq);
+      }
+      if (a.sigmoid && a.d_aux) {
+        ss = wave_sum_f(ss);
+        const float rs = 1.f / (ss < 1e-20f ? 1e-20f : ss);
+        cq = wave_sum_f(cq) * rs;
+#pragma unroll
+        for (int j = 0; j < PER; ++j) ds[j] += (dq[j] - cq) * rs;
+      } else if (!a.sigmoid) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) {
+          ds[j] += dq[j];
+          cs = fmaf(ds[j], s[j], cs);
+        }
+        cs = wave_sum_f(cs);
+      }
+      const float zl = a.d_z ? z * 2.f / T * fmaf(__builtin_amdgcn_logf(tot), 0.69314718055994530942f, m) : 0.f;
+#pragma unroll
+      for (int j = 0; j < PER; ++j) {
+        const int e = j * 64 + lane;
+        const float v = a.sigmoid ? ds[j] * s[j] * (1.f - s[j]) : s[j] * (ds[j] - cs);
+        float dl = 0.f;
+        if (e < E) {
+          dl = a.d_z ? fmaf(zl, p[j], v) : v;
+          if (a.d_logits) a.d_logits[(size_t)t * E + e] = dl;
+          pb[j] += (double)dl;
+        }
+        if (e < pitch) a.dl[(size_t)t * pitch + e] = dl;
+      }
     }
+    // The last tile also clears the rows behind T (the end of d_W's last step).
+    if (t0 + TT >= T)
+      for (int i = threadIdx.x; i < (up_to(T, kGradK) - T) * pitch; i += kThreads) a.dl[(size_t)T * pitch + i] = 0.f;
   }
   if (a.d_b) {
 #pragma unroll
@@ -362,16 +325,16 @@ __global__ __launch_bounds__(512, 2) void score_dx_bf16_kernel(const float* __re
 }
 
 // ---------------------------------------------------------------------------
-// d_W[e][c] = sum_t dl[t][e] x[t][c]: A = dl by expert, fp32 along k and multiplied as three
-// bf16 terms, B = x, one slice of the tokens per block.  Block 64 MT experts x 256 columns, k in
+// d_W[e][c] = sum_t dl[t][e] x[t][c]: A = dl, fp32 and multiplied as three bf16 terms, B = x,
+// one slice of the tokens per block.  Block 64 MT experts x 256 columns, k in
 // steps of 32 through four LDS stages, four waves as 2 x 2, one per SIMD.  All work but the
 // MFMAs runs in their shadow: while a slice of 16 k is multiplied, the next one's fragments
 // are made from words in registers, the words of the one after are read from LDS, and the
 // loads of four steps ahead are issued.  One barrier per step.
 //
-// LDS: A rows of 128 B, 16 B chunks at chunk ^ ((row >> 1) & 7); B rows of 512 B, their 128 B
-// quarters at quarter ^ ((row >> 3) & 1) so that the two lane halves (rows 8 apart) read
-// different banks.
+// Both operands have their rows (tokens) along k, so a lane reads single words of 8 rows: of dl
+// its expert's, of x its pair of columns.  LDS: rows of 256 MT and 512 B, their 128 B parts at
+// part ^ ((row >> 3) & 1) so that the two lane halves (rows 8 apart) read different banks.
 // ---------------------------------------------------------------------------
 template <int MT>
 __global__ __launch_bounds__(256, 1) void score_dw_bf16_kernel(
@@ -392,13 +355,14 @@ __global__ __launch_bounds__(256, 1) void score_dw_bf16_kernel(
   const int s0 = (int)((long)sl * steps / slices), nk = (int)((long)(sl + 1) * steps / slices) - s0;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
 
-  // A: load i of wave w fills rows 8 (4 i + w) + lane / 8.
-  const float* a_base = A + (size_t)m0 * a_pitch + (size_t)s0 * kGradK;
+  // A: load i of wave w fills 1 KB of rows of 256 MT bytes.
+  constexpr int kALanes = 16 * MT;                     // lanes per row
+  const float* a_base = A + (size_t)s0 * kGradK * a_pitch + m0;
   uint32_t a_off[kAI];
 #pragma unroll
   for (int i = 0; i < kAI; ++i) {
-    const int row = (i * 4 + wave) * 8 + (lane >> 3);
-    a_off[i] = (uint32_t)row * (uint32_t)a_pitch * 4u + (((lane & 7) ^ ((row >> 1) & 7)) << 4);
+    const int row = (i * 4 + wave) * (64 / kALanes) + lane / kALanes;
+    a_off[i] = (uint32_t)row * (uint32_t)a_pitch * 4u + (((lane % kALanes) ^ (((row >> 3) & 1) << 3)) << 4);
   }
   // B: load i of wave w fills rows 2 (4 i + w) + lane / 32; rows past the last repeat it (A is
   // 0 there), columns past d wrap to the tile's first half (not stored).
@@ -407,7 +371,7 @@ __global__ __launch_bounds__(256, 1) void score_dw_bf16_kernel(
     const uint32_t base = lds0 + stage * kStage;
     const int s = min(step, nk - 1);
     if (i < kAI) {
-      dma16(a_base + (size_t)s * kGradK, a_off[i < kAI ? i : 0], base + (i * 4 + wave) * 1024);
+      dma16(a_base + (size_t)s * kGradK * a_pitch, a_off[i < kAI ? i : 0], base + (i * 4 + wave) * 1024);
     } else {
       const int j = i - kAI, r = 2 * (j * 4 + wave) + (lane >> 5);
       int c = (lane & 31) ^ (((r >> 3) & 1) << 3);
@@ -425,16 +389,15 @@ __global__ __launch_bounds__(256, 1) void score_dw_bf16_kernel(
     for (int m = 0; m < MT; ++m)
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[n][m][q] = 0.f;
-  const uint32_t a_lane = (wm * MT * 32 + fr) * 128, a_swz = (fr >> 1) & 7;
-  const uint32_t b_lane = kA + 8 * fc * 512 + fr * 4;
-  f32x4 raw[MT][2];                                    // dl, 8 values along k
+  const uint32_t a_lane = 8 * fc * kRows * 4 + fr * 4, b_lane = kA + 8 * fc * 512 + fr * 4;
+  float raw[MT][8];                                    // dl, 8 rows of an expert
   uint32_t pairs[2][8];                                // x, 8 rows of a pair of columns
   u32x4 xa[2][MT][TERMS], b[2][4];
   // Slice h of a stage: k 16 h + 8 fc .. + 7.
-  auto read_a = [&](int stage, int h, int m) {
-    const uint8_t* row = lds + stage * kStage + a_lane + m * 4096;
-    raw[m][0] = __builtin_bit_cast(f32x4, ld16(row + (((4 * h + 2 * fc) ^ a_swz) << 4)));
-    raw[m][1] = __builtin_bit_cast(f32x4, ld16(row + (((4 * h + 2 * fc + 1) ^ a_swz) << 4)));
+  auto read_a = [&](int stage, int h, int i) {
+    const int m = i / 8, j = i % 8;
+    raw[m][j] = *reinterpret_cast<const float*>(lds + stage * kStage + a_lane + (16 * h + j) * kRows * 4 +
+                                                ((wm * MT + m) ^ fc) * 128);
   };
   auto read_b = [&](int stage, int h, int i) {         // i: 8 rows of two column groups
     const int n = i / 8, j = i % 8;
@@ -444,7 +407,7 @@ __global__ __launch_bounds__(256, 1) void score_dw_bf16_kernel(
   auto make_a = [&](u32x4 (&to)[MT][TERMS], int i) {
     const int m = i / 4, j = i % 4;
     uint32_t o[TERMS];
-    split_pair<TERMS>(raw[m][j >> 1][2 * (j & 1)], raw[m][j >> 1][2 * (j & 1) + 1], o);
+    split_pair<TERMS>(raw[m][2 * j], raw[m][2 * j + 1], o);
 #pragma unroll
     for (int q = 0; q < TERMS; ++q) to[m][q][j] = o[q];
   };
@@ -463,7 +426,7 @@ __global__ __launch_bounds__(256, 1) void score_dw_bf16_kernel(
 #pragma unroll
   for (int h = 0; h < 2; ++h) {                        // slice 0 as fragments, slice 1 as words
 #pragma unroll
-    for (int m = 0; m < MT; ++m) read_a(0, h, m);
+    for (int i = 0; i < 8 * MT; ++i) read_a(0, h, i);
 #pragma unroll
     for (int i = 0; i < 16; ++i) read_b(0, h, i);
     if (h == 0) {
@@ -493,7 +456,8 @@ __global__ __launch_bounds__(256, 1) void score_dw_bf16_kernel(
         } else if (i < 2 * kThird) {
 #pragma unroll
           for (int u = j * 8 / kThird; u < (j + 1) * 8 / kThird; ++u) make_b(b[h ^ 1], u);
-          if (j < MT) read_a(st1, h, j);
+#pragma unroll
+          for (int u = j * 8 * MT / kThird; u < (j + 1) * 8 * MT / kThird; ++u) read_a(st1, h, u);
         } else {
 #pragma unroll
           for (int u = j * 16 / kThird; u < (j + 1) * 16 / kThird; ++u) read_b(st1, h, u);
@@ -597,7 +561,7 @@ static void sum_slices(const ScoreGradArgs& a, int slices, hipStream_t s) {
 
 static void products_f32(const ScoreGradArgs& a, hipStream_t s) {
   const ScoreShape& h = a.sh;
-  const int pitch = dl_space(h).Ek;
+  const int pitch = dl_pitch(h.E);
   if (a.d_x)
     score_dx_kernel<<<dim3((h.T + 15) / 16, (h.d + 255) / 256), 256, 0, s>>>(
         a.dl, pitch, static_cast<const float*>(a.w), h.T, h.d, h.E, static_cast<float*>(a.d_x));
@@ -615,12 +579,11 @@ static void launch_dx(const ScoreGradArgs& a, hipStream_t s) {
   const int cols = (h.d + kDxCols - 1) / kDxCols, tiles = (h.T + kDxRows - 1) / kDxRows;
   const int groups = std::min(std::max(1, 256 / cols), tiles);   // one block per CU
   score_dx_bf16_kernel<NE><<<cols * groups, 512, 0, s>>>(
-      a.dl, dl_space(h).Ek, static_cast<const uint16_t*>(a.w), h.T, h.d, h.E, groups, static_cast<uint16_t*>(a.d_x));
+      a.dl, dl_pitch(h.E), static_cast<const uint16_t*>(a.w), h.T, h.d, h.E, groups, static_cast<uint16_t*>(a.d_x));
 }
 
 static void products_bf16(const ScoreGradArgs& a, hipStream_t s) {
   const ScoreShape& h = a.sh;
-  const DlSpace t = dl_space(h);
   if (a.d_x) {
     if (h.E <= 64) launch_dx<64>(a, s);
     else if (h.E <= 128) launch_dx<128>(a, s);
@@ -630,12 +593,11 @@ static void products_bf16(const ScoreGradArgs& a, hipStream_t s) {
   if (a.d_w) {
     const int slices = score_grad_slices(h), cols = (h.d + kGradCols - 1) / kGradCols;
     float* out = slices > 1 ? a.pw : a.d_w;
-    const float* by_expert = a.dl + t.by_expert;
     const uint16_t* x = static_cast<const uint16_t*>(a.x);
     if (h.E <= 64)
-      score_dw_bf16_kernel<1><<<dim3(slices, cols, 1), 256, 0, s>>>(by_expert, t.Tk, x, h.T, h.d, h.E, slices, out);
+      score_dw_bf16_kernel<1><<<dim3(slices, cols, 1), 256, 0, s>>>(a.dl, dl_pitch(h.E), x, h.T, h.d, h.E, slices, out);
     else
-      score_dw_bf16_kernel<2><<<dim3(slices, cols, (h.E + 127) / 128), 256, 0, s>>>(by_expert, t.Tk, x, h.T, h.d, h.E,
+      score_dw_bf16_kernel<2><<<dim3(slices, cols, (h.E + 127) / 128), 256, 0, s>>>(a.dl, dl_pitch(h.E), x, h.T, h.d, h.E,
                                                                                  slices, out);
     if (slices > 1) sum_slices(a, slices, s);
   }
@@ -643,16 +605,11 @@ static void products_bf16(const ScoreGradArgs& a, hipStream_t s) {
 
 template <int PER>
 static void launch_dlogits(const ScoreGradArgs& a, int blocks, hipStream_t s) {
-  const DlSpace t = dl_space(a.sh);
-  const bool big = grad_tile(a.sh.T) == 64;
-  if (a.sh.bf16 && big)
-    score_dlogits_kernel<PER, 64, true><<<blocks, 1024, 0, s>>>(a, t.Ek, t.Tk, t.by_expert);
-  else if (a.sh.bf16)
-    score_dlogits_kernel<PER, 16, true><<<blocks, 256, 0, s>>>(a, t.Ek, t.Tk, t.by_expert);
-  else if (big)
-    score_dlogits_kernel<PER, 64, false><<<blocks, 1024, 0, s>>>(a, t.Ek, 0, 0);
+  const int pitch = dl_pitch(a.sh.E);
+  if (grad_tile(a.sh.T) == 64)
+    score_dlogits_kernel<PER, 64><<<blocks, 1024, 0, s>>>(a, pitch);
   else
-    score_dlogits_kernel<PER, 16, false><<<blocks, 256, 0, s>>>(a, t.Ek, 0, 0);
+    score_dlogits_kernel<PER, 16><<<blocks, 256, 0, s>>>(a, pitch);
 }
 
 hipError_t launch_score_grad(const ScoreGradArgs& a, hipStream_t s) {
