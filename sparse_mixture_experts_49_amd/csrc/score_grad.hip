@@ -52,22 +52,26 @@ static int dl_pitch(int E) { return E <= 64 ? 64 : up_to(E, kGradRows); }
 size_t score_dl_bytes(const ScoreShape& s) { return (size_t)up_to(s.T, kGradK) * dl_pitch(s.E) * 4; }
 int score_grad_sum_blocks(int T) { return grad_blocks(T); }
 
-// dl of tiles of TT tokens, a wave four of them, lane l the experts l, l + 64, ...
-template <int PER, int TT>
-__global__ __launch_bounds__(TT * 16) void score_dlogits_kernel(ScoreGradArgs a, int pitch) {
-  constexpr int WAVES = TT / 4, kThreads = TT * 16;    // four tokens a wave
+// dl of tiles of TT tokens, one at a time per wave, lane l the experts l, l + 64, ... and for
+// the chosen ones lane q < k the q-th.  Bound by instruction issue, so straight-line: experts
+// behind E and slots behind k carry zeros, what depends on an argument is computed with 0 where
+// it is absent.
+template <int PER, int TT, bool SIGMOID>
+__global__ __launch_bounds__(TT * 16) void score_dlogits_kernel(ScoreGradArgs a) {
+  constexpr int WAVES = TT / 4, kThreads = TT * 16, kPitch = 64 * PER;
   __shared__ double sum_b[WAVES][64 * PER];
   const int lane = threadIdx.x & 63;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int E = a.sh.E, T = a.sh.T, k = a.sh.k;
+  const float aux = a.d_aux ? *a.d_aux : 0.f, z = a.d_z ? *a.d_z * 2.f / T : 0.f;
   float dq[PER];
-  const bool soft = !a.sigmoid || a.d_z;               // softmax(l) is needed
-  const float aux = a.d_aux ? *a.d_aux : 0.f, z = a.d_z ? *a.d_z : 0.f;
+  bool live[PER];
   double pb[PER];
 #pragma unroll
   for (int j = 0; j < PER; ++j) {
     const int e = j * 64 + lane;
-    dq[j] = (a.d_aux && e < E) ? (float)((double)aux * E * a.load[e] / ((double)T * k) / T) : 0.f;
+    live[j] = e < E;
+    dq[j] = (a.d_aux && live[j]) ? (float)((double)aux * E * a.load[e] / ((double)T * k) / T) : 0.f;
     pb[j] = 0.0;
   }
   for (int t0 = blockIdx.x * TT; t0 < T; t0 += gridDim.x * TT) {
@@ -75,15 +79,17 @@ __global__ __launch_bounds__(TT * 16) void score_dlogits_kernel(ScoreGradArgs a,
       float l[PER], p[PER], s[PER];
 #pragma unroll
       for (int j = 0; j < PER; ++j) l[j] = a.logits[(size_t)t * E + min(j * 64 + lane, E - 1)];
-      const int my_idx = a.topk_idx[(size_t)t * k + min(lane, k - 1)];
-      const float my_g = a.d_topk_w ? a.d_topk_w[(size_t)t * k + min(lane, k - 1)] : 0.f;
-      float m = -INFINITY, tot = 0.f;
+      int idx = a.topk_idx[(size_t)t * k + min(lane, k - 1)];
+      float g = a.d_topk_w ? a.d_topk_w[(size_t)t * k + min(lane, k - 1)] : 0.f;
+      idx = (lane < k && (uint32_t)idx < (uint32_t)E) ? idx : -1;
+      g = idx >= 0 ? g : 0.f;
 #pragma unroll
-      for (int j = 0; j < PER; ++j) {
-        l[j] = j * 64 + lane < E ? l[j] : -INFINITY;
-        m = fmaxf(m, l[j]);
-      }
-      if (soft) {
+      for (int j = 0; j < PER; ++j) l[j] = live[j] ? l[j] : -INFINITY;
+      float zl = 0.f;                                  // d_z (2 / T) lse
+      if (!SIGMOID || a.d_z) {
+        float m = l[0], tot = 0.f;
+#pragma unroll
+        for (int j = 1; j < PER; ++j) m = fmaxf(m, l[j]);
         m = wave_max_f(m);
         m = m == -INFINITY ? 0.f : m;
 #pragma unroll
@@ -92,72 +98,80 @@ __global__ __launch_bounds__(TT * 16) void score_dlogits_kernel(ScoreGradArgs a,
         const float r_tot = tot > 0.f ? 1.f / tot : tot != tot ? tot : 0.f;
 #pragma unroll
         for (int j = 0; j < PER; ++j) p[j] *= r_tot;
+        if (a.d_z) zl = z * fmaf(__builtin_amdgcn_logf(tot), 0.69314718055994530942f, m);
+      } else {
+#pragma unroll
+        for (int j = 0; j < PER; ++j) p[j] = 0.f;
       }
 #pragma unroll
-      for (int j = 0; j < PER; ++j) s[j] = a.sigmoid ? sigmoid_f32(l[j]) : p[j];
-      // Chosen scores and the gradients of the raw weights.
-      int idx[8];
-      float g[8], S = 1e-20f, gw = 0.f;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) {
-        idx[q] = q < k ? __builtin_amdgcn_readlane(my_idx, q) : -1;
-        idx[q] = (uint32_t)idx[q] < (uint32_t)E ? idx[q] : -1;
-        g[q] = idx[q] >= 0 ? __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(my_g), q)) : 0.f;
-        float r = 0.f;
-#pragma unroll
-        for (int j = 0; j < PER; ++j) {
-          const float v = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(s[j]), idx[q] & 63));
-          r = idx[q] >> 6 == j ? v : r;              // idx -1: none
-        }
-        S += r;
-        gw = fmaf(g[q], r, gw);
-      }
-      const float rS = 1.f / S;
-#pragma unroll
-      for (int q = 0; q < 8; ++q) g[q] = a.renorm ? a.scale * (g[q] - gw * rS) * rS : a.scale * g[q];
-      float ds[PER];
-      float cs = 0.f, cq = 0.f, ss = 0.f;
+      for (int j = 0; j < PER; ++j) s[j] = SIGMOID ? sigmoid_f32(l[j]) : p[j];
+      // Chosen scores and the gradients of the raw weights, lane q those of choice q.
+      float r = 0.f;
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
-        float dr = 0.f;
-#pragma unroll
-        for (int q = 0; q < 8; ++q)
-          dr += idx[q] == j * 64 + lane ? g[q] : 0.f;
-        ds[j] = dr;
-        ss += s[j];
-        cq = fmaf(dq[j], s[j], cq);
+        const float v = __uint_as_float(
+            (uint32_t)__builtin_amdgcn_ds_bpermute((idx & 63) << 2, (int)__float_as_uint(s[j])));
+        r = idx >> 6 == j ? v : r;                     // idx -1: none
       }
-      if (a.sigmoid && a.d_aux) {
-        ss = wave_sum_f(ss);
-        const float rs = 1.f / (ss < 1e-20f ? 1e-20f : ss);
-        cq = wave_sum_f(cq) * rs;
+      if (a.renorm) {
+        const float rS = 1.f / (wave_sum_f(r) + 1e-20f), gw = wave_sum_f(g * r);
+        g = a.scale * (g - gw * rS) * rS;
+      } else {
+        g *= a.scale;
+      }
+      float ds[PER];
 #pragma unroll
-        for (int j = 0; j < PER; ++j) ds[j] += (dq[j] - cq) * rs;
-      } else if (!a.sigmoid) {
+      for (int j = 0; j < PER; ++j) ds[j] = 0.f;
+#pragma unroll
+      for (int q = 0; q < 8; ++q) {                    // k is at most 8
+        const int iq = __builtin_amdgcn_readlane(idx, q);
+        const float gq = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(g), q));
+#pragma unroll
+        for (int j = 0; j < PER; ++j) ds[j] += iq == j * 64 + lane ? gq : 0.f;
+      }
+      float dl[PER];
+      if constexpr (SIGMOID) {
+        if (a.d_aux) {
+          float cq = 0.f, ss = 0.f;
+#pragma unroll
+          for (int j = 0; j < PER; ++j) {
+            ss += s[j];
+            cq = fmaf(dq[j], s[j], cq);
+          }
+          ss = wave_sum_f(ss);
+          const float rs = 1.f / (ss < 1e-20f ? 1e-20f : ss);
+          cq = wave_sum_f(cq) * rs;
+#pragma unroll
+          for (int j = 0; j < PER; ++j) ds[j] = fmaf(dq[j] - cq, rs, ds[j]);
+        }
+#pragma unroll
+        for (int j = 0; j < PER; ++j) dl[j] = ds[j] * s[j] * (1.f - s[j]);
+      } else {
+        float cs = 0.f;
 #pragma unroll
         for (int j = 0; j < PER; ++j) {
           ds[j] += dq[j];
           cs = fmaf(ds[j], s[j], cs);
         }
         cs = wave_sum_f(cs);
+#pragma unroll
+        for (int j = 0; j < PER; ++j) dl[j] = s[j] * (ds[j] - cs);
       }
-      const float zl = a.d_z ? z * 2.f / T * fmaf(__builtin_amdgcn_logf(tot), 0.69314718055994530942f, m) : 0.f;
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
-        const int e = j * 64 + lane;
-        const float v = a.sigmoid ? ds[j] * s[j] * (1.f - s[j]) : s[j] * (ds[j] - cs);
-        float dl = 0.f;
-        if (e < E) {
-          dl = a.d_z ? fmaf(zl, p[j], v) : v;
-          if (a.d_logits) a.d_logits[(size_t)t * E + e] = dl;
-          pb[j] += (double)dl;
-        }
-        if (e < pitch) a.dl[(size_t)t * pitch + e] = dl;
+        dl[j] = live[j] ? fmaf(zl, p[j], dl[j]) : 0.f;
+        pb[j] += (double)dl[j];
+        a.dl[(size_t)t * kPitch + j * 64 + lane] = dl[j];
+      }
+      if (a.d_logits) {
+#pragma unroll
+        for (int j = 0; j < PER; ++j)
+          if (live[j]) a.d_logits[(size_t)t * E + j * 64 + lane] = dl[j];
       }
     }
     // The last tile also clears the rows behind T (the end of d_W's last step).
     if (t0 + TT >= T)
-      for (int i = threadIdx.x; i < (up_to(T, kGradK) - T) * pitch; i += kThreads) a.dl[(size_t)T * pitch + i] = 0.f;
+      for (int i = threadIdx.x; i < (up_to(T, kGradK) - T) * kPitch; i += kThreads) a.dl[(size_t)T * kPitch + i] = 0.f;
   }
   if (a.d_b) {
 #pragma unroll
@@ -603,13 +617,13 @@ static void products_bf16(const ScoreGradArgs& a, hipStream_t s) {
   }
 }
 
-template <int PER>
+template <int PER>                                     // 64 PER: dl_pitch(E)
 static void launch_dlogits(const ScoreGradArgs& a, int blocks, hipStream_t s) {
-  const int pitch = dl_pitch(a.sh.E);
-  if (grad_tile(a.sh.T) == 64)
-    score_dlogits_kernel<PER, 64><<<blocks, 1024, 0, s>>>(a, pitch);
-  else
-    score_dlogits_kernel<PER, 16><<<blocks, 256, 0, s>>>(a, pitch);
+  const bool big = grad_tile(a.sh.T) == 64;
+  if (a.sigmoid && big) score_dlogits_kernel<PER, 64, true><<<blocks, 1024, 0, s>>>(a);
+  else if (a.sigmoid) score_dlogits_kernel<PER, 16, true><<<blocks, 256, 0, s>>>(a);
+  else if (big) score_dlogits_kernel<PER, 64, false><<<blocks, 1024, 0, s>>>(a);
+  else score_dlogits_kernel<PER, 16, false><<<blocks, 256, 0, s>>>(a);
 }
 
 hipError_t launch_score_grad(const ScoreGradArgs& a, hipStream_t s) {
