@@ -116,6 +116,21 @@ __device__ __forceinline__ float gelu_erf(float z) {
   return fmaf(-fabsf(z), q * e, fmaxf(z, 0.f));
 }
 
+// The same for a result that is rounded to bf16 next: Phi(-|z|) = exp2(q(|z|)) with q of
+// degree 7 fitted to log2 Phi(-x) on [0, 7], so one transcendental instead of two.  Relative
+// error under 1e-5, 1/200 of the rounding's; past -7 the result stays above -1.2e-11 |z| / 7.
+__device__ __forceinline__ float gelu_for_bf16(float z) {
+  const float x = fminf(fabsf(z), 7.f);
+  float q = fmaf(-1.5882183106441516e-06f, x, 5.615340342046693e-05f);
+  q = fmaf(q, x, -0.0008832158055156469f);
+  q = fmaf(q, x, 0.008303220383822918f);
+  q = fmaf(q, x, -0.053501322865486145f);
+  q = fmaf(q, x, -0.4589643180370331f);
+  q = fmaf(q, x, -1.1510356664657593f);
+  q = fmaf(q, x, -1.0000139474868774f);
+  return fmaf(-fabsf(z), __builtin_amdgcn_exp2f(q), fmaxf(z, 0.f));
+}
+
 // Two fp32 values rounded to bf16 (nearest, ties to even) and packed, lo in
 // bits 0..15: one v_cvt_pk_bf16_f32 on gfx950.
 typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));

@@ -235,7 +235,7 @@ __global__ __launch_bounds__(512, 1) void mx_stream_kernel(StreamArgs p) {
       v[3] += __uint_as_float(b.y & 0xffff0000u);
       if constexpr (UP)
         *reinterpret_cast<uint2*>(static_cast<uint16_t*>(p.out) + (size_t)r * N + n) =
-            make_uint2(pack_bf16x2(gelu_erf(v[0]), gelu_erf(v[1])), pack_bf16x2(gelu_erf(v[2]), gelu_erf(v[3])));
+            make_uint2(pack_bf16x2(gelu_for_bf16(v[0]), gelu_for_bf16(v[1])), pack_bf16x2(gelu_for_bf16(v[2]), gelu_for_bf16(v[3])));
       else
         *reinterpret_cast<f32x4*>(static_cast<float*>(p.out) + (size_t)r * N + n) = v;
     }
@@ -274,7 +274,7 @@ __global__ __launch_bounds__(256) void mx_split_sum_kernel(
   }
   if constexpr (UP)
     *reinterpret_cast<uint2*>(static_cast<uint16_t*>(out) + (size_t)r * N + n) =
-        make_uint2(pack_bf16x2(gelu_erf(v[0]), gelu_erf(v[1])), pack_bf16x2(gelu_erf(v[2]), gelu_erf(v[3])));
+        make_uint2(pack_bf16x2(gelu_for_bf16(v[0]), gelu_for_bf16(v[1])), pack_bf16x2(gelu_for_bf16(v[2]), gelu_for_bf16(v[3])));
   else
     *reinterpret_cast<f32x4*>(static_cast<float*>(out) + (size_t)r * N + n) = v;
 }

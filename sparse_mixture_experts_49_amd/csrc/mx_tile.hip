@@ -89,36 +89,38 @@ struct TileArgs {
 
 // Scales by rows ([row][K/32]) to groups of 256 k: [K/256 rounded up][row][8], dword h the
 // bytes of blocks h, h + 2, h + 4, h + 6 (the ones lane half h of the four slices of 64 k
-// needs); blocks past K are 0 (2^-127).  The first `w_units` threads take the weights, the
-// rest the dispatched rows of the activations.
+// needs); blocks past K are 0 (2^-127).  A block turns 64 rows x 16 groups through LDS, so both
+// sides go by whole cache lines; the first `w_blocks` take the weights (N rows per expert, a
+// multiple of 64), the rest the dispatched rows of the activations.
 __global__ __launch_bounds__(256) void mx_scale_groups_kernel(
-    const uint8_t* __restrict__ ws, uint8_t* __restrict__ w_out, int64_t w_units, int N,
+    const uint8_t* __restrict__ ws, uint8_t* __restrict__ w_out, int w_blocks, int N,
     const uint8_t* __restrict__ as, uint8_t* __restrict__ a_out, int rows,
     const int32_t* __restrict__ src, int k_top, int tokens, int K) {
-  int64_t i = (int64_t)blockIdx.x * 256 + threadIdx.x;
-  const int groups = (K + 255) / 256, pitch = K / 32;
-  const uint8_t* row;
-  uint8_t* out;
-  int g;
-  if (i < w_units) {
-    const int n = (int)(i % N);
-    const int64_t eg = i / N;
-    g = (int)(eg % groups);
-    row = ws + (eg / groups * N + n) * pitch;
-    out = w_out + i * 8;
-  } else {
-    i -= w_units;
-    if (!as || i >= (int64_t)rows * groups) return;
-    const int r = (int)(i % rows);
-    g = (int)(i / rows);
-    const int from = src ? (int)min((uint32_t)src[r] / (uint32_t)k_top, (uint32_t)tokens - 1u) : r;
-    row = as + (size_t)from * pitch;
-    out = a_out + i * 8;
+  __shared__ uint2 turn[16][65];
+  const int tid = threadIdx.x, groups = (K + 255) / 256, pitch = K / 32;
+  const bool weights = (int)blockIdx.x < w_blocks;
+  const int all = weights ? N : rows;                  // rows of the output
+  const int per = N / 64, e = weights ? blockIdx.x / per : 0;
+  const int r0 = (weights ? blockIdx.x - e * per : blockIdx.x - w_blocks) * 64, g0 = blockIdx.y * 16;
+  const uint8_t* in = weights ? ws + (size_t)e * N * pitch : as;
+  uint8_t* out = weights ? w_out + (size_t)e * groups * N * 8 : a_out;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = i * 16 + (tid >> 4), g = g0 + (tid & 15);
+    if (r0 + r >= all || g >= groups) continue;
+    const int from = !weights && src ? (int)min((uint32_t)src[r0 + r] / (uint32_t)k_top, (uint32_t)tokens - 1u) : r0 + r;
+    const uint8_t* at = in + (size_t)from * pitch + g * 8;
+    const uint32_t lo = *reinterpret_cast<const uint32_t*>(at);
+    const uint32_t hi = g * 8 + 4 < pitch ? *reinterpret_cast<const uint32_t*>(at + 4) : 0u;
+    turn[tid & 15][r] = make_uint2(__builtin_amdgcn_perm(hi, lo, 0x06040200), __builtin_amdgcn_perm(hi, lo, 0x07050301));
   }
-  const uint32_t lo = *reinterpret_cast<const uint32_t*>(row + g * 8);
-  const uint32_t hi = g * 8 + 4 < pitch ? *reinterpret_cast<const uint32_t*>(row + g * 8 + 4) : 0u;
-  *reinterpret_cast<uint2*>(out) = make_uint2(__builtin_amdgcn_perm(hi, lo, 0x06040200),
-                                              __builtin_amdgcn_perm(hi, lo, 0x07050301));
+  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    const int r = tid & 63, g = i * 4 + (tid >> 6);
+    if (r0 + r < all && g0 + g < groups)
+      *reinterpret_cast<uint2*>(out + ((size_t)(g0 + g) * all + r0 + r) * 8) = turn[g][r];
+  }
 }
 
 template <bool FP4, bool UP, int BM>
@@ -294,8 +296,8 @@ __global__ __launch_bounds__(256, 1) void mx_tile_kernel(TileArgs p) {
             uint32_t h[2][2];
 #pragma unroll
             for (int i = 0; i < 2; ++i) {
-              h[i][0] = pack_bf16x2(gelu_erf(v[g + i][0]), gelu_erf(v[g + i][1]));
-              h[i][1] = pack_bf16x2(gelu_erf(v[g + i][2]), gelu_erf(v[g + i][3]));
+              h[i][0] = pack_bf16x2(gelu_for_bf16(v[g + i][0]), gelu_for_bf16(v[g + i][1]));
+              h[i][1] = pack_bf16x2(gelu_for_bf16(v[g + i][2]), gelu_for_bf16(v[g + i][3]));
             }
             const auto s0 = __builtin_amdgcn_permlane32_swap(h[0][0], h[1][0], false, false);
             const auto s1 = __builtin_amdgcn_permlane32_swap(h[0][1], h[1][1], false, false);
@@ -556,9 +558,9 @@ hipError_t launch_mx_tile(const MxFfnArgs& a, hipStream_t s) {
   }
   p.ws = w_groups;
   const int groups = (a.K + 255) / 256;
-  const int64_t w_units = (int64_t)a.E * groups * a.N, units = w_units + (a.fp4 ? (int64_t)p.rows * groups : 0);
-  mx_scale_groups_kernel<<<(unsigned)((units + 255) / 256), 256, 0, s>>>(
-      a.ws, w_groups, w_units, a.N, a.fp4 ? scales : nullptr, a_groups, p.rows, p.src, a.k, a.T, a.K);
+  const int w_blocks = a.E * (a.N / 64), a_blocks = a.fp4 ? (p.rows + 63) / 64 : 0;
+  mx_scale_groups_kernel<<<dim3(w_blocks + a_blocks, (groups + 15) / 16), 256, 0, s>>>(
+      a.ws, w_groups, w_blocks, a.N, scales, a_groups, p.rows, p.src, a.k, a.T, a.K);
   const int bm = tile_height(p.rows, a.E, a.N);
   if (a.fp4)
     a.up ? launch_tile_rows<true, true>(p, bm, s) : launch_tile_rows<true, false>(p, bm, s);
