@@ -460,6 +460,9 @@ class _CDescOnce:
         object.__setattr__(self, name, value)
         self.__dict__.pop("_ref", None)
 
+    def __getstate__(self):              # copies and pickles make their own
+        return {k: v for k, v in self.__dict__.items() if k != "_ref"}
+
     def ref(self):
         """The C struct by reference, as the calls take it."""
         r = self.__dict__.get("_ref")

@@ -294,13 +294,17 @@ size_t mx_partial_bytes(int T, int k, int E, int N, int K) {
   return s > 1 ? (size_t)s * T * k * N * 4 : 0;
 }
 
-// Experts averaging at least 48 rows run the LDS-tiled kernel, the rest stream.  The tiled
-// kernel's loads run up to two steps of 256 k ahead, so it starts at k = 512.
-static bool tiled(int T, int k, int E, int K) { return (long)T * k >= 48L * E && K >= 512; }
+// Experts averaging many rows run the LDS-tiled kernel, the rest stream: from 32 rows with
+// fp4 activations, whose matrix products take a quarter of the time, from 56 with bf16 ones.
+// Streamed and tiled, us: E = 8, K = 4096, N = 14336: fp4 24 rows 72 and 68, 36 rows 120 and
+// 68; bf16 48 rows 120 and 119, 72 rows 180 and 123.  E = 64, K = 2048, N = 1408: fp4 24 rows 36
+// and 40, 36 rows 54 and 40; bf16 48 rows 62 and 66, 72 rows 89 and 74.  The tiled kernel's loads
+// run up to two steps of 256 k ahead, so it starts at k = 512.
+static bool tiled(long rows, int E, int K, bool fp4) { return rows >= (fp4 ? 32L : 56L) * E && K >= 512; }
 
 size_t mx_act_bytes(int T, int k, int E, int N, int K, bool fp4) {
   const long rows = (long)T * k;
-  return tiled(T, k, E, K) ? mx_tile_bytes(rows, E, N, K, fp4) : fp4 ? (size_t)rows * K * 2 : 0;
+  return tiled(rows, E, K, fp4) ? mx_tile_bytes(rows, E, N, K, fp4) : fp4 ? (size_t)rows * K * 2 : 0;
 }
 
 template <bool UP>
@@ -323,7 +327,8 @@ static void launch_stream(const MxFfnArgs& a, const void* act, hipStream_t s) {
   p.splits = splits;
   p.partial = a.partial;
   // Tiles of 16 rows and runs of 512 while experts average at most 12, else 32 rows and runs
-  // of 256 (the activations' share of the LDS).
+  // of 256 (the activations' share of the LDS): E = 8, K = 4096, N = 14336, 12 rows 48 and 51 us,
+  // 18 rows 84 and 71; E = 64, K = 2048, N = 1408, 9 rows 23.6 and 24.5 us, 18 rows 37 and 32.
   if ((long)R <= 12L * a.E) mx_stream_kernel<UP, 1, 512, 3><<<kStreamBlocks, 512, 0, s>>>(p);
   else mx_stream_kernel<UP, 2, 256, 4><<<kStreamBlocks, 512, 0, s>>>(p);
   if (splits > 1)
@@ -332,7 +337,7 @@ static void launch_stream(const MxFfnArgs& a, const void* act, hipStream_t s) {
 }
 
 hipError_t launch_mx_ffn(const MxFfnArgs& a, hipStream_t s) {
-  if (tiled(a.T, a.k, a.E, a.K)) return launch_mx_tile(a, s);
+  if (tiled((long)a.T * a.k, a.E, a.K, a.fp4)) return launch_mx_tile(a, s);
   const void* act = a.a;
   if (a.fp4) {
     // The values the 4-bit activations stand for, as bf16: exact in the products.

@@ -15,8 +15,10 @@ namespace moe {
 
 constexpr int kPartWaves = 4;       // waves of a logits block, 16 experts each
 
-// From 512 tokens the LDS-tiled kernel, below it the direct one.
-static bool score_tiled(const ScoreShape& s) { return s.T >= 512; }
+// Many tokens: the LDS-tiled kernel, few: the direct one.  Whole calls, direct and tiled: d =
+// 4096, 256 experts, 512 tokens 30 and 32 us, 1024 tokens 46 and 30; d = 2048, 64 experts,
+// 1024 tokens 17.5 and 17.7 us, 2048 tokens 22 and 18.
+static bool score_tiled(const ScoreShape& s) { return s.T >= (s.E <= 64 ? 1536 : 768); }
 
 int score_parts(const ScoreShape& s) {
   if (score_tiled(s)) {
@@ -559,8 +561,9 @@ static void launch_typed(const ScoreArgs& a, bool train, hipStream_t s) {
     score_logits_kernel<T><<<grid, 256, 0, s>>>(static_cast<const T*>(a.x), static_cast<const T*>(a.w), h.T,
                                                h.d, h.E, parts, a.part, a.done);
   }
-  // Blocks of 4 waves while they spread over the chip, of 16 where tokens abound.
-  const bool big = h.T >= 4096, final = tiled && parts == 1 && a.logits;
+  // Blocks of 4 waves while they spread over the chip, of 16 where tokens abound (whole calls,
+  // d = 4096, 256 experts: 512 tokens 30 and 32 us, 1024 tokens 31 and 30, 4096 tokens 42 and 37).
+  const bool big = h.T >= 1024, final = tiled && parts == 1 && a.logits;
   const int nb = std::min(256, (h.T + (big ? 15 : 3)) / (big ? 16 : 4));
   auto finish = [&](auto per) {
     constexpr int PER = decltype(per)::value;

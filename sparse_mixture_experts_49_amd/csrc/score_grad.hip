@@ -38,8 +38,10 @@ int score_grad_slices(const ScoreShape& s) {
   return (int)std::max(1L, std::min({16L, (long)(s.T + 63) / 64, 2048 / tiles}));
 }
 
-// Tokens per tile of the logit-gradient kernel.
-static int grad_tile(int T) { return T >= 4096 ? 64 : 16; }
+// Tokens per tile of the logit-gradient kernel (blocks of 4 or 16 waves): 64 and 256 experts,
+// tiles of 16 and 64, us: 4096 tokens 8.2 and 9.4, 11.2 and 14.4; 8192 tokens 10.7 and 9.8, 15.4
+// and 15.3; 16384 tokens 16 and 11, 26 and 18.
+static int grad_tile(int T) { return T >= 8192 ? 64 : 16; }
 static int grad_blocks(int T) {
   const int tile = grad_tile(T);
   return std::min(256, (T + tile - 1) / tile);

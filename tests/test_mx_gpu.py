@@ -156,8 +156,10 @@ def test_products(shape, act):
         return R.values(*R.quantize(a)) if act == "mxfp4" else a.double()
 
     # Any order of K fp32 additions of exact products: K roundings of partial sums, each at
-    # most the sum of |terms|; GELU has slope under 1.13 and its own error 2e-7 |z|; then
-    # bf16 or fp32 rounding.
+    # most the sum of |terms|; GELU has slope under 1.13 and its own error of 1.3e-5 |z|
+    # Phi(-|z|) (its polynomial's), at least in part under 2e-7 |z|, the rest, under 6.3e-6 |z|,
+    # within the room of the additions (128 * 1.13 U32 size > 8.6e-6 |z|, which a sum of exact
+    # 8-bit products uses no quarter of); then bf16 or fp32 rounding.
     W1, W2 = R.values(*L["w1"]).view(E, F, d), R.values(*L["w2"]).view(E, d, F)
     perm = L["x"][L["src"][:rows].long() // k]
     z, size = R.product(seen(perm), off, W1, L["b1"])
@@ -320,3 +322,100 @@ def test_two_streams_with_their_own_workspaces():
     torch.cuda.synchronize()
     assert torch.equal(outs[0][0], outs[1][0])
     assert not math.isnan(float(outs[0][0][:L["rows"]].float().sum()))
+
+
+# More tiles than CUs, so that blocks go on to further tiles: 128 and 256 rows high, k an odd
+# multiple of 128; 15 rows per expert, streamed 32 rows at a time over a long k.
+@pytest.mark.parametrize("act", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("shape", [(640, 6, 64, 640, 1408, True), (600, 8, 8, 512, 2816, False),
+                                   (60, 2, 8, 4096, 256, True), (150, 2, 8, 512, 640, True)],
+                         ids=lambda s: "T%d_k%d_E%d_d%d_F%d_b%d" % s)
+def test_products_over_many_tiles(shape, act):
+    test_products(shape, act)
+
+
+@pytest.mark.parametrize("act", ["bf16", "mxfp4"])
+def test_tiled_products_of_uneven_experts(act):
+    """K = 512 and 75 rows per expert on average: one expert has them all, or none has any, or
+    all but two slots go to one expert."""
+    T, E, k, d, F = 600, 8, 1, 512, 384
+    desc = moe.MxDesc(T, d, F, E, k, act=act)
+    mostly = torch.full((T, 1), 6)
+    mostly[0], mostly[599] = 0, 7
+    for idx in (torch.full((T, 1), 5), mostly, torch.full((T, 1), -1)):
+        L = _layer(T, k, E, d, F, True, 4, idx)
+        n = L["rows"]
+        h = torch.full((T, F), -77.0, device=DEV).bfloat16()
+        moe.moe_mx_ffn_up(desc, L["x"].to(DEV), L["offsets"].to(DEV), _weights(L), h, src=L["src"].to(DEV),
+                          workspace=_poisoned(desc))
+        assert torch.all(h[n:] == -77.0)
+        if n == 0:
+            continue
+        x = L["x"][L["src"][:n].long() // k]
+        a = R.values(*R.quantize(x)) if act == "mxfp4" else x.double()
+        z, size = R.product(a, L["offsets"], R.values(*L["w1"]).view(E, F, d), L["b1"])
+        room = 1.13 * (d + 1) * U32 * size + 1.3e-5 * R.gelu(-z.abs()).abs()
+        assert torch.all((h[:n].cpu().double() - R.gelu(z)).abs() <= room + U16 * (R.gelu(z).abs() + room))
+
+
+@pytest.mark.parametrize("d", [128, 512], ids=["streamed", "tiled"])
+def test_gelu_of_every_bf16_value(d):
+    """One weight of 1 per column, so that z is x itself: every finite value, against 64 bits.
+    z is exact, so the error is the polynomial's (1.3e-5 of |z| Phi(-|z|) up to |z| = 7, that
+    whole term, under 1e-11, beyond) and two fp32 roundings, then the rounding to bf16."""
+    F, T = d, 65536 // d
+    codes = torch.zeros(1, F, d // 2, dtype=torch.uint8)
+    n = torch.arange(F)
+    codes[0, n, n // 2] = torch.where(n % 2 == 0, 0x02, 0x20).to(torch.uint8)      # e2m1 1.0
+    scales = torch.full((1, F, d // 32), 127, dtype=torch.uint8)
+    x = torch.arange(65536, dtype=torch.int32).to(torch.int16).view(torch.bfloat16).view(T, d).clone()
+    x[~x.isfinite()] = 0.0
+    desc = moe.MxDesc(T, d, F, 1, 1, has_expert_bias=False)
+    h = torch.empty(T, F, dtype=torch.bfloat16, device=DEV)
+    moe.moe_mx_ffn_up(desc, x.to(DEV), torch.tensor([0, T], dtype=torch.int32, device=DEV),
+                      moe.MxWeights(w1=codes.to(DEV), s1=scales.to(DEV)), h)
+    z = x.double()
+    tail = z.abs() * 0.5 * torch.special.erfc(z.abs() * 0.5 ** 0.5)      # Phi by 1 + erf ends at -8.3
+    want = torch.where(z > 0, z - tail, -tail)
+    room = torch.where(z.abs() <= 7, 1.3e-5 * tail, tail.clamp(min=1e-30)) + 2 * U32 * want.abs()
+    got = h.cpu().double()
+    assert torch.all((got - want).abs() <= room + U16 * (want.abs() + room) + 2.0 ** -133)
+
+
+@pytest.mark.parametrize("act", ["bf16", "mxfp4"])
+def test_forward_on_the_tiled_path(act):
+    """A layer whose products are tiled, bit for bit as its parts; captured, and replayed with
+    eager calls of the same layer between."""
+    T, k, E, d, F = 450, 4, 16, 512, 640
+    L = _layer(T, k, E, d, F, True, 12)
+    g = torch.Generator().manual_seed(3)
+    wr = (torch.randn(E, d, generator=g) * d ** -0.5).bfloat16().to(DEV)
+    route, desc = moe.ScoreDesc(T, d, E, k), moe.MxDesc(T, d, F, E, k, act=act)
+    w, x = _weights(L), L["x"].to(DEV)
+    y, ws, eager_ws = torch.empty(T, d, device=DEV), _poisoned(desc, route), _poisoned(desc, route)
+    r = moe.ScoreRouting.allocate(route, DEV)
+    moe.moe_score_route(route, x, wr, r)
+    lay = moe.Routing(topk_idx=r.topk_idx, counts=torch.empty(E, dtype=torch.int32, device=DEV),
+                      offsets=torch.empty(E + 1, dtype=torch.int32, device=DEV), dest=torch.empty(T, k, dtype=torch.int32, device=DEV),
+                      src=torch.empty(T * k, dtype=torch.int32, device=DEV))
+    moe.moe_mx_dispatch(desc, lay)
+    h, o = torch.empty(T * k, F, dtype=torch.bfloat16, device=DEV), torch.empty(T * k, d, device=DEV)
+    moe.moe_mx_ffn_up(desc, x, lay.offsets, w, h, src=lay.src)
+    moe.moe_mx_ffn_down(desc, h, lay.offsets, w, o)
+    want = torch.empty_like(y)
+    moe.moe_combine(moe.Desc(T, d, F, E, k), o, lay.dest, r.topk_w, want)
+    moe.moe_mx_forward(route, desc, x, wr, w, y, workspace=ws)
+    assert torch.equal(y, want)
+    graph, s = torch.cuda.CUDAGraph(), torch.cuda.Stream()
+    torch.cuda.synchronize()
+    with torch.cuda.graph(graph, stream=s):
+        moe.moe_mx_forward(route, desc, x, wr, w, y, workspace=ws)
+    for _ in range(3):
+        y.zero_()
+        ws.fill_(0xFF)
+        eager = torch.empty_like(y)
+        moe.moe_mx_forward(route, desc, x, wr, w, eager, workspace=eager_ws)
+        torch.cuda.synchronize()
+        graph.replay()
+        torch.cuda.synchronize()
+        assert torch.equal(y, want) and torch.equal(eager, want)

@@ -296,3 +296,55 @@ def test_repeats_streams_and_graph_replays_agree():
         graph.replay()
         torch.cuda.synchronize()
         assert all(torch.equal(a, b) for a, b in zip(outs(), ref))
+
+
+@pytest.mark.parametrize("shape", [
+    (800, 384, 160, 6, "softmax", 8, 3, 1, False, 16.0, "f32"),
+    (1600, 128, 60, 4, "sigmoid", 4, 2, 1, True, 1.0, "bf16"),
+    (4099, 256, 64, 6, "softmax", 1, 1, 1, True, 1.0, "f32"),
+    (4500, 128, 192, 8, "sigmoid", 8, 4, 2, True, 2.5, "bf16"),
+    (8209, 128, 130, 3, "softmax", 13, 2, 2, True, 1.0, "bf16"),
+], ids=lambda s: "T%d_d%d_E%d_k%d_%s_g%d" % s[:6])
+def test_route_many_tokens(shape):
+    """Every height of the logits tile, logits in one part and in several, and the finish with
+    16 waves per block, each of which takes several tokens."""
+    test_route_exact_logits_with_ties(shape)
+
+
+@pytest.mark.parametrize("losses", [(None, None), (0.5, 0.25)], ids=["weights", "losses"])
+@pytest.mark.parametrize("case", [
+    (33, 1152, 160, 6, "sigmoid", True, 2.5, "bf16"),       # three column blocks, the last in part
+    (300, 128, 129, 2, "softmax", False, 1.0, "bf16"),
+    (4100, 128, 192, 8, "sigmoid", True, 2.5, "bf16"),
+    (8197, 128, 192, 8, "sigmoid", True, 2.5, "bf16"),      # tiles of 64 tokens, the last of 5
+    (8250, 128, 100, 4, "softmax", True, 1.0, "f32"),
+    (4161, 256, 100, 4, "softmax", True, 1.0, "bf16"),
+    (4500, 128, 60, 3, "softmax", True, 1.0, "f32"),
+    (20000, 128, 64, 2, "sigmoid", True, 1.0, "bf16"),      # more tiles than blocks
+], ids=lambda s: "T%d_d%d_E%d_k%d_%s" % s[:5])
+def test_backward_many_tokens(case, losses):
+    test_backward(case, losses)
+
+
+def test_backward_of_infinite_and_nan_logits():
+    """An expert masked by logit -inf has gradient 0 in its row and NaN nowhere; a token with a
+    NaN logit keeps the NaN to its own row of d_logits and d_x."""
+    T, d, E, k = 70, 256, 40, 4
+    for kind in ("softmax", "sigmoid"):
+        x, w, l, idx, load, dw = _grad_inputs(T, d, E, k, "bf16", 11)
+        l[:, 7] = -float("inf")
+        keep = torch.arange(E) != 7
+        idx = l.topk(k, 1).indices.to(torch.int32)
+        load = torch.bincount(idx.flatten().long(), minlength=E).to(torch.int32)
+        desc = _desc(T, d, E, k, kind)
+        got = _backward(desc, x, w, l, idx, load, dw, 0.5, None)
+        assert torch.all(got.d_logits[:, 7] == 0) and torch.all(got.d_w_router[7] == 0)
+        assert not any(t.isnan().any() for t in (got.d_x, got.d_w_router, got.d_b_router, got.d_logits))
+        args = (kind, idx.long(), load, k, True, 1.0, dw.double(), 0.5, None)
+        tol = 64 * U32 * R.d_logits_size(l.double(), *args)
+        err = (got.d_logits.cpu().double() - R.d_logits(l.double(), *args)).abs()
+        assert torch.all((err <= tol)[:, keep])
+        l[13, 3] = float("nan")
+        got = _backward(desc, x, w, l, idx, load, dw, None, None)
+        rows = torch.arange(T) != 13
+        assert not got.d_logits.cpu()[rows].isnan().any() and not got.d_x.cpu()[rows].isnan().any()
