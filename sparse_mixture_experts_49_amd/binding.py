@@ -572,10 +572,16 @@ class _Call:
             check_tensor(t, name, dtype, numel, self.device)
         return t.data_ptr()
 
-    def ws(self, t, size_of):
-        """(pointer, bytes) of the workspace; None allocates one."""
+    def ws(self, t, size_of, stream):
+        """(pointer, bytes) of the workspace; None allocates one, on the call's stream, so that
+        its memory goes to nobody else before the call has run there."""
         if t is None:
-            t = self._keep = torch.empty(size_of(), dtype=torch.uint8, device=self.device)
+            if stream is not None and not isinstance(stream, torch.cuda.Stream):
+                handle = getattr(stream, "cuda_stream", stream)
+                stream = (torch.cuda.ExternalStream(handle, device=self.device) if handle
+                          else torch.cuda.default_stream(self.device))
+            with torch.cuda.stream(stream):
+                t = self._keep = torch.empty(size_of(), dtype=torch.uint8, device=self.device)
         elif not (isinstance(t, torch.Tensor) and t.is_cuda and t.get_device() == self.index and t.is_contiguous()):
             if not isinstance(t, torch.Tensor):
                 raise MoeError(MOE_ERR_INVALID, "workspace must be a torch tensor or None")
@@ -622,7 +628,7 @@ def moe_score_route(desc: ScoreDesc, x, w_router, routing: ScoreRouting, b_route
     topk_w have to be there)."""
     c = _Call(x, "x")
     T, d, E, dt = desc.tokens, desc.d_model, desc.n_experts, desc.torch_dtype
-    ws, nb = c.ws(workspace, lambda: moe_score_workspace_size(desc))
+    ws, nb = c.ws(workspace, lambda: moe_score_workspace_size(desc), stream)
     c.run(load_library().moe_score_route, desc.ref(), c.t(x, "x", dt, T * d),
           c.t(w_router, "w_router", dt, E * d), c.t(b_router, "b_router", torch.float32, E),
           c.t(b_select, "b_select", torch.float32, E), ctypes.byref(_score_out(c, desc, routing)), ws, nb,
@@ -636,7 +642,7 @@ def moe_score_backward(desc: ScoreDesc, x, w_router, routing: ScoreRouting, d_to
     c = _Call(routing.logits, "routing.logits")
     T, d, E, k, dt = desc.tokens, desc.d_model, desc.n_experts, desc.top_k, desc.torch_dtype
     f32 = torch.float32
-    ws, nb = c.ws(workspace, lambda: moe_score_workspace_size(desc))
+    ws, nb = c.ws(workspace, lambda: moe_score_workspace_size(desc), stream)
     g = CScoreGrads(c.t(grads.d_x, "grads.d_x", dt, T * d), c.t(grads.d_w_router, "grads.d_w_router", f32, E * d),
                     c.t(grads.d_b_router, "grads.d_b_router", f32, E),
                     c.t(grads.d_logits, "grads.d_logits", f32, T * E))
@@ -751,7 +757,7 @@ def moe_mx_dispatch(desc: MxDesc, routing: Routing, workspace=None, stream=None)
                  counts=c.t(routing.counts, "routing.counts", i32, E),
                  offsets=c.t(routing.offsets, "routing.offsets", i32, E + 1),
                  dest=c.t(routing.dest, "routing.dest", i32, A), src=c.t(routing.src, "routing.src", i32, A))
-    ws, nb = c.ws(workspace, lambda: moe_mx_workspace_size(desc))
+    ws, nb = c.ws(workspace, lambda: moe_mx_workspace_size(desc), stream)
     c.run(load_library().moe_mx_dispatch, desc.ref(), ctypes.byref(r), ws, nb, stream=stream)
 
 
@@ -760,7 +766,7 @@ def moe_mx_ffn_up(desc: MxDesc, x, offsets, weights: MxWeights, h, src=None, wor
     src[r] / top_k, else x holds the dispatched rows."""
     c = _Call(x, "x")
     R, bf = desc.tokens * desc.top_k, torch.bfloat16
-    ws, nb = c.ws(workspace, lambda: moe_mx_workspace_size(desc))
+    ws, nb = c.ws(workspace, lambda: moe_mx_workspace_size(desc), stream)
     c.run(load_library().moe_mx_ffn_up, desc.ref(),
           c.t(x, "x", bf, (desc.tokens if src is not None else R) * desc.d_model), c.t(src, "src", torch.int32, R),
           c.t(offsets, "offsets", torch.int32, desc.n_experts + 1),
@@ -772,7 +778,7 @@ def moe_mx_ffn_down(desc: MxDesc, h, offsets, weights: MxWeights, o, workspace=N
     """Second expert product, o fp32."""
     c = _Call(h, "h")
     R = desc.tokens * desc.top_k
-    ws, nb = c.ws(workspace, lambda: moe_mx_workspace_size(desc))
+    ws, nb = c.ws(workspace, lambda: moe_mx_workspace_size(desc), stream)
     c.run(load_library().moe_mx_ffn_down, desc.ref(), c.t(h, "h", torch.bfloat16, R * desc.d_ff),
           c.t(offsets, "offsets", torch.int32, desc.n_experts + 1),
           ctypes.byref(_mx_weights(c, desc, weights, False, True)),
@@ -785,7 +791,7 @@ def moe_mx_forward(route: ScoreDesc, desc: MxDesc, x, w_router, weights: MxWeigh
     [T, d]; `routing` (a ScoreRouting, or None) receives the fields it has."""
     c = _Call(x, "x")
     T, D, E, bf, f32 = desc.tokens, desc.d_model, desc.n_experts, torch.bfloat16, torch.float32
-    ws, nb = c.ws(workspace, lambda: moe_mx_workspace_size(desc) + moe_score_workspace_size(route))
+    ws, nb = c.ws(workspace, lambda: moe_mx_workspace_size(desc) + moe_score_workspace_size(route), stream)
     out = ctypes.byref(_score_out(c, route, routing)) if routing is not None else None
     c.run(load_library().moe_mx_forward, route.ref(), desc.ref(),
           c.t(x, "x", bf, T * D), c.t(w_router, "w_router", bf, E * D), c.t(b_router, "b_router", f32, E),
