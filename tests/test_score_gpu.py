@@ -350,22 +350,32 @@ def test_backward_of_infinite_and_nan_logits():
         assert not got.d_logits.cpu()[rows].isnan().any() and not got.d_x.cpu()[rows].isnan().any()
 
 
-def test_own_workspace_on_another_stream():
-    """No workspace given and a stream that is not the current one: what the call allocates is
-    not handed out again while the call still waits on its stream."""
+def test_own_workspace_on_another_stream(monkeypatch):
+    """No workspace given and a stream that is not the current one: the current one is not
+    handed what the call allocated, which may still wait to run."""
     T, d, E, k = 2000, 256, 64, 4
     desc = _desc(T, d, E, k, "sigmoid")
     x, w, _ = _grid_inputs(desc, 2)
     want = _run(desc, x, w)
     x, w, s = x.to(DEV), w.to(DEV), torch.cuda.Stream()
+    size, empty, got = moe.moe_score_workspace_size(desc), torch.empty, []
+
+    def watched(*args, **kw):
+        t = empty(*args, **kw)
+        if t.dtype == torch.uint8 and t.numel() == size:
+            got.append(t.data_ptr())
+        return t
+
     for stream in (s, s.cuda_stream):
         r = moe.ScoreRouting.allocate(desc, DEV, train=True)
         torch.cuda.synchronize()
         with torch.cuda.stream(s):
             torch.cuda._sleep(20_000_000)
-        moe.moe_score_route(desc, x, w, r, stream=stream)
-        junk = [moe.alloc_score_workspace(desc, DEV).fill_(0xFF) for _ in range(4)]
+        with monkeypatch.context() as m:
+            m.setattr(torch, "empty", watched)
+            moe.moe_score_route(desc, x, w, r, stream=stream)
+        others = [moe.alloc_score_workspace(desc, DEV).fill_(0xFF) for _ in range(4)]
+        assert len(got) == 1 and got.pop() not in [t.data_ptr() for t in others]
         torch.cuda.synchronize()
         for name in ("topk_idx", "topk_w", "logits", "load", "prob_mean", "aux", "z_loss"):
             assert torch.equal(getattr(r, name), getattr(want, name)), name
-        del junk
