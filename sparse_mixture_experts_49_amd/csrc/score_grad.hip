@@ -235,8 +235,9 @@ __device__ __forceinline__ void columns8(const f32x16& u, const f32x16& v, int g
 // d_x[t] = dl[t] W_r.  k is the experts, at most 256, so W_r stays in registers: a wave has 64
 // columns of it for every expert (NE / 2 registers), a block of eight 512, and tiles of 32
 // tokens stream past.  The block splits a tile of dl into its two bf16 terms once, into LDS
-// (rows of 2 NE bytes per term, 16 B chunks at chunk ^ (row & 7)), two tiles in turn with one
-// barrier each; the next tile's dl is on its way meanwhile.
+// (rows of 2 NE bytes per term, 16 B chunks at chunk ^ f(row) such that 16 rows' reads of one
+// touch every bank once), two tiles in turn with one barrier each; the next tile's dl is on its
+// way meanwhile.
 // ---------------------------------------------------------------------------
 constexpr int kDxCols = 512, kDxRows = 32;
 
@@ -247,6 +248,8 @@ __global__ __launch_bounds__(512, 2) void score_dx_bf16_kernel(const float* __re
   constexpr int kTerm = kDxRows * NE * 2, kChunks = NE / 8, kUnits = kDxRows * kChunks;
   constexpr int kPer = (kUnits + 511) / 512;           // chunks of 8 values per thread
   constexpr int kSlices = NE / 16;
+  // Rows of whole 256 B start at the same bank, of odd multiples of 128 B at two in turn.
+  auto swz = [](int r) { return NE % 128 == 0 ? r & 15 : (r >> 1) & 7; };
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * 2 * kTerm];
   const int lane = threadIdx.x & 63, fr = lane & 31, fc = lane >> 5;
   const int wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
@@ -297,7 +300,7 @@ __global__ __launch_bounds__(512, 2) void score_dx_bf16_kernel(const float* __re
         split_pair<2>(f[2 * (j & 1)], f[2 * (j & 1) + 1], o);
         q[0][j] = o[0], q[1][j] = o[1];
       }
-      uint8_t* at = lds + buffer * 2 * kTerm + r * NE * 2 + ((c ^ (r & 7)) << 4);
+      uint8_t* at = lds + buffer * 2 * kTerm + r * NE * 2 + ((c ^ swz(r)) << 4);
       *reinterpret_cast<u32x4*>(at) = q[0];
       *reinterpret_cast<u32x4*>(at + kTerm) = q[1];
     }
@@ -308,22 +311,37 @@ __global__ __launch_bounds__(512, 2) void score_dx_bf16_kernel(const float* __re
   __syncthreads();
   int buffer = 0;
   for (int tile = group; tile < tiles; tile += groups, buffer ^= 1) {
-    put(buffer ^ 1);
-    fetch(tile + 2 * groups);
+    // The two waves of a SIMD do this before and after their MFMAs: one's runs under the
+    // other's.
+    if (wave < 4) {
+      put(buffer ^ 1);
+      fetch(tile + 2 * groups);
+    }
     f32x16 acc[2];
 #pragma unroll
     for (int n = 0; n < 2; ++n)
 #pragma unroll
       for (int q = 0; q < 16; ++q) acc[n][q] = 0.f;
     const uint8_t* base = lds + buffer * 2 * kTerm + fr * NE * 2;
+    u32x4 f[2][2];                                     // [slice % 2][hi, mid]
+    auto read = [&](int s) {
+      const uint32_t at = ((2 * s + fc) ^ swz(fr)) << 4;
+      f[s % 2][0] = ld16(base + at);
+      f[s % 2][1] = ld16(base + kTerm + at);
+    };
+    read(0);
 #pragma unroll
     for (int s = 0; s < kSlices; ++s) {
-      const uint32_t at = ((2 * s + fc) ^ (fr & 7)) << 4;
-      const u32x4 hi = ld16(base + at), mid = ld16(base + kTerm + at);
+      if (s + 1 < kSlices) read(s + 1);
 #pragma unroll
-      for (int n = 0; n < 2; ++n) acc[n] = mfma32_bf16(b[s][n], mid, acc[n]);
+      for (int q = 1; q >= 0; --q)
 #pragma unroll
-      for (int n = 0; n < 2; ++n) acc[n] = mfma32_bf16(b[s][n], hi, acc[n]);
+        for (int n = 0; n < 2; ++n) acc[n] = mfma32_bf16(b[s][n], f[s % 2][q], acc[n]);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+    if (wave >= 4) {
+      put(buffer ^ 1);
+      fetch(tile + 2 * groups);
     }
     const int t = tile * kDxRows + fr;
     if (active && t < T) {
