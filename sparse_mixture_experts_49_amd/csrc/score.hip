@@ -34,7 +34,8 @@ int score_parts(const ScoreShape& s) {
 }
 
 // Partial logits: wave w of block (t-tile, e-tile, part) multiplies 16 tokens by
-// 16 experts over its part of d, operands straight from memory to registers.
+// 16 experts over its part of d, operands straight from memory to registers.  Few tokens:
+// bound by latency, so d is split until the chip has work (1 token, d = 2048, 64 experts 3.0 us).
 template <typename T>
 __global__ __launch_bounds__(256) void score_logits_kernel(const T* __restrict__ x,
                                                            const T* __restrict__ w, int tokens,
@@ -106,7 +107,8 @@ __device__ __forceinline__ float pair_of(float v) {
 
 // What a wave needs to finish tokens: lane l holds experts l, l + 64, ... (PER of them).
 // Straight-line code: lanes past E carry logit -inf and key 0 (one token per wave is bound by
-// instruction issue and latency, branches cost most of both).
+// instruction issue and latency, branches cost most of both).  16384 tokens, 256 experts in 8
+// groups, k = 8, with the sums: 28 us (17 MB of logits would take 4); one token 4.5 us.
 template <int PER, bool TRAIN>
 struct Finisher {
   int shift, gs;                 // lanes per group 2^shift, experts per group
@@ -337,6 +339,9 @@ __global__ __launch_bounds__(WAVES * 64) void score_finish_kernel(ScoreArgs a, i
 // Eight waves, two per SIMD: waves 0-3 multiply the first half of each step, 4-7 the
 // second, each over the whole tile, so LDS is read no more often than by four waves while
 // one wave's reads run under the other's MFMAs; the halves add up at the end through LDS.
+// 16384 tokens, d = 4096, 256 experts: 44 us, x read at 3.0 TB/s, 780 TFLOP/s.  Bound: each
+// block also takes all of W_r from L2, 20480 cache lines at about one per ns in all; more
+// tokens per block would halve that but leave CUs idle (256 blocks here).
 // One part (d not split) and the logits wanted: they are written there, bias included; else
 // to the workspace.  Finishing the tokens in this kernel measured slower: with so few
 // waves a token took 5 us, the separate kernel has the waves to hide that.
@@ -494,7 +499,8 @@ __global__ __launch_bounds__(512, 1) void score_tile_kernel(ScoreArgs a, int par
 
 // The sums over blocks (at most 256) in a fixed order: a wave per expert, its column read at
 // once.  The block that finishes last (a counter that the logits kernel cleared; agent-wide
-// release and acquire around it) has all of them and writes the losses.
+// release and acquire around it) has all of them and writes the losses.  8 us whatever the
+// sizes: three dependent trips to memory.
 __global__ __launch_bounds__(1024) void score_reduce_kernel(ScoreArgs a, int blocks) {
   __shared__ bool last;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, E = a.sh.E;

@@ -57,7 +57,7 @@ int score_grad_sum_blocks(int T) { return grad_blocks(T); }
 // dl of tiles of TT tokens, one at a time per wave, lane l the experts l, l + 64, ... and for
 // the chosen ones lane q < k the q-th.  Bound by instruction issue, so straight-line: experts
 // behind E and slots behind k carry zeros, what depends on an argument is computed with 0 where
-// it is absent.
+// it is absent.  16384 tokens, 256 experts, k = 8: 22 us for 34 MB.
 template <int PER, int TT, bool SIGMOID>
 __global__ __launch_bounds__(TT * 16) void score_dlogits_kernel(ScoreGradArgs a) {
   constexpr int WAVES = TT / 4, kThreads = TT * 16, kPitch = 64 * PER;
@@ -237,7 +237,8 @@ __device__ __forceinline__ void columns8(const f32x16& u, const f32x16& v, int g
 // tokens stream past.  The block splits a tile of dl into its two bf16 terms once, into LDS
 // (rows of 2 NE bytes per term, 16 B chunks at chunk ^ f(row) such that 16 rows' reads of one
 // touch every bank once), two tiles in turn with one barrier each; the next tile's dl is on its
-// way meanwhile.
+// way meanwhile.  16384 x 4096, 256 experts: 77 us, 0.89 PFLOP/s of the two terms; the MFMAs
+// take 59% of the waves' time, the rest is reading W_r (once per block, 8 us) and the stores.
 // ---------------------------------------------------------------------------
 constexpr int kDxCols = 512, kDxRows = 32;
 
@@ -364,7 +365,10 @@ __global__ __launch_bounds__(512, 2) void score_dx_bf16_kernel(const float* __re
 // steps of 32 through four LDS stages, four waves as 2 x 2, one per SIMD.  All work but the
 // MFMAs runs in their shadow: while a slice of 16 k is multiplied, the next one's fragments
 // are made from words in registers, the words of the one after are read from LDS, and the
-// loads of four steps ahead are issued.  One barrier per step.
+// loads of four steps ahead are issued.  One barrier per step.  16384 x 4096, 256 experts: 111 to
+// 118 us by the box, 0.9 PFLOP/s of the three terms.  Nothing waits long: without the splitting
+// 98 us, without the LDS reads 105; the chip's clock falls to 1.9 GHz under it, at which the
+// MFMAs alone are busy 45% of the time.
 //
 // Both operands have their rows (tokens) along k, so a lane reads single words of 8 rows: of dl
 // its expert's, of x its pair of columns.  LDS: rows of 256 MT and 512 B, their 128 B parts at
