@@ -337,7 +337,9 @@ int moe_forward_noalloc(const moe_desc* desc, const void* x, const moe_weights* 
  *   aux         E * sum_e load_e / (T k) * prob_mean_e
  *   z_loss      mean of (log sum_e exp l_e)^2
  * topk_idx and topk_w feed moe_permute, moe_combine (up to 64 experts),
- * moe_mx_dispatch and moe_mx_forward.  d_model is a multiple of 128. */
+ * moe_mx_dispatch and moe_mx_forward.  d_model is a multiple of 128.
+ * The calls use their workspace until they have run: calls, or replays of captured
+ * ones, that may overlap need one each. */
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };
 
 typedef struct moe_score_desc {
@@ -418,7 +420,7 @@ int moe_score_backward(const moe_score_desc* desc, const void* x, const void* w_
  * and one expert's d_model * d_ff under 2^31.  Rows of an expert are the segment
  * [offsets[e], offsets[e+1]) as moe_permute and moe_mx_dispatch lay them out; a
  * segment outside [0, T*k) is cut to it.  The codes are frozen weights: there is no
- * backward. */
+ * backward.  Calls, or replays of captured ones, that may overlap need a workspace each. */
 enum { MOE_MX_ACT_BF16 = 0, MOE_MX_ACT_MXFP4 = 1 };
 
 typedef struct moe_mx_desc {
@@ -442,7 +444,7 @@ typedef struct moe_mx_weights {
 } moe_mx_weights;
 
 /* Rows to MXFP4.  x: rows of cols values of `dtype`, row_stride elements apart; cols a
- * multiple of 32, row_stride >= cols and a multiple of 16 bytes.  Per block, with
+ * multiple of 32, rows * cols at most 2^34, row_stride >= cols and a multiple of 16 bytes.  Per block, with
  * a = max |x|: scale 2^(floor(log2 a) - 2), at least 2^-127 (and exactly that for a
  * block of zeros); codes rounded to nearest, ties to even, values past 6 to 6.  A block
  * with a NaN or an infinity gets scale 255.  rows = 0 does nothing. */

@@ -154,9 +154,9 @@ int validate_rows(int dtype, int64_t rows, int64_t cols, int64_t stride) {
   if (stride < cols) return fail(MOE_ERR_INVALID, "row_stride must be >= cols");
   if (stride % (dtype == MOE_DTYPE_BF16 ? 8 : 4))
     return fail(MOE_ERR_INVALID, "row_stride must be a multiple of 16 bytes");
-  // One thread per 8 values in a one-dimensional grid of 256-thread blocks.
-  if (cols > std::numeric_limits<int32_t>::max() || rows > (int64_t(1) << 42) / cols)
-    return fail(MOE_ERR_UNSUPPORTED, "rows * cols must be at most 2^42");
+  // One thread per 8 values, and a launch takes under 2^32 threads.
+  if (cols > std::numeric_limits<int32_t>::max() || rows > (int64_t(1) << 34) / cols)
+    return fail(MOE_ERR_UNSUPPORTED, "rows * cols must be at most 2^34");
   return MOE_OK;
 }
 

@@ -13,7 +13,6 @@
 
 namespace moe {
 
-
 // Many tokens: the LDS-tiled kernel, few: the direct one.  Whole calls, direct and tiled: d =
 // 4096, 256 experts, 512 tokens 30 and 32 us, 1024 tokens 46 and 30; d = 2048, 64 experts,
 // 1024 tokens 17.5 and 17.7 us, 2048 tokens 22 and 18.

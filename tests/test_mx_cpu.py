@@ -115,3 +115,11 @@ def test_reference_rounds_to_nearest_even():
     codes, scales = R.quantize(x)
     assert scales.tolist() == [[127]]
     assert R.values(codes, scales)[0, :8].tolist() == [0.0, 1.0, 1.0, 2.0, 2.0, 4.0, 4.0, 6.0]
+
+
+@pytest.mark.parametrize("rows,cols", [(2 ** 29, 64), (2 ** 28 + 1, 64), (1, 2 ** 35)])
+def test_more_values_than_a_launch_has_threads(rows, cols):
+    lib = moe.load_library()
+    for st in (lib.moe_mx_quantize(0x1000, 1, rows, cols, cols, 0x8000, 0x9000, None),
+               lib.moe_mx_dequantize(0x8000, 0x9000, rows, cols, 1, 0x1000, cols, None)):
+        assert st == B.MOE_ERR_UNSUPPORTED and "2^34" in lib.moe_last_error().decode()
