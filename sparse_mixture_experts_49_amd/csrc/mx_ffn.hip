@@ -48,6 +48,13 @@ struct StreamArgs {
   float* partial;
 };
 
+// Words at the same address for all lanes, through the scalar cache: a vector load would be
+// waited for behind every load to LDS in flight.
+typedef __attribute__((address_space(4))) const uint32_t scalar_u32;
+__device__ __forceinline__ scalar_u32* scalar_words(const void* p) {
+  return (scalar_u32*)reinterpret_cast<uintptr_t>(p);
+}
+
 template <bool UP, int NMT, int RUN, int S>
 __global__ __launch_bounds__(512, 1) void mx_stream_kernel(StreamArgs p) {
   constexpr int kRows = 16 * NMT, G = RUN / 128;               // granules per run
@@ -56,7 +63,7 @@ __global__ __launch_bounds__(512, 1) void mx_stream_kernel(StreamArgs p) {
   constexpr int kStage = kA + kW + kS, oW = kA, oS = kA + kW;
   constexpr int kAI = kA / 8192, kWI = kW / 8192, L = kAI + kWI;   // 1 KB loads per wave
   constexpr int kALanes = kARow / 16, kWLanes = kWRow / 16;    // lanes per row (A: at most 64)
-  static_assert(kA % 8192 == 0 && kW % 8192 == 0 && kALanes <= 64, "load plan");
+  static_assert(kA % 8192 == 0 && kW % 8192 == 0 && (kALanes == 64 || kALanes == 32), "load plan");
   static_assert(S * kStage + sizeof(TileTable) <= 160 * 1024, "LDS");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[S * kStage];
   __shared__ TileTable table;
@@ -94,10 +101,18 @@ __global__ __launch_bounds__(512, 1) void mx_stream_kernel(StreamArgs p) {
   auto aim = [&](const Unit& w) {
 #pragma unroll
     for (int i = 0; i < kAI; ++i) {
-      constexpr int kPer = 64 / kALanes;
+      constexpr int kPer = 64 / kALanes;           // rows per load: 1 or 2
       const int row = (i * 8 + wave) * kPer + lane / kALanes;
-      const int r = min(w.r0 + row, w.r1 - 1);
-      const uint32_t tok = p.src ? min((uint32_t)p.src[r] / (uint32_t)p.k_top, (uint32_t)p.tokens - 1u) : (uint32_t)r;
+      uint32_t tok = (uint32_t)min(w.r0 + row, w.r1 - 1);
+      if (p.src) {
+        const int r = min(w.r0 + (i * 8 + wave) * kPer, w.r1 - 1);
+        tok = scalar_words(p.src)[r];
+        if (kPer == 2) {
+          const uint32_t second = scalar_words(p.src)[min(r + 1, w.r1 - 1)];
+          tok = lane / kALanes ? second : tok;
+        }
+        tok = min(tok / (uint32_t)p.k_top, (uint32_t)p.tokens - 1u);
+      }
       a_off[i] = tok * (uint32_t)K * 2u + ((lane % kALanes) ^ (row & 15)) * 16u + (uint32_t)w.g0 * 256u;
       a_max[i] = tok * (uint32_t)K * 2u + (uint32_t)K * 2u - 16u;
     }
@@ -222,7 +237,12 @@ __global__ __launch_bounds__(512, 1) void mx_stream_kernel(StreamArgs p) {
     // Lane: row m*16 + fr, columns n0 + 16 wave + 4 fc .. + 3.
     const int n = cur.n0 + wave * 16 + 4 * fc;
     uint2 b = make_uint2(0u, 0u);
-    if (p.bias && p.splits == 1 && n < N) b = *reinterpret_cast<const uint2*>(p.bias + (size_t)cur.e * N + n);
+    if (p.bias && p.splits == 1) {                 // the wave's 16 columns
+      scalar_u32* w = scalar_words(p.bias + (size_t)cur.e * N + min(cur.n0 + wave * 16, N - 16));
+      const uint32_t q[8] = {w[0], w[1], w[2], w[3], w[4], w[5], w[6], w[7]};
+      b = fc < 2 ? (fc == 0 ? make_uint2(q[0], q[1]) : make_uint2(q[2], q[3]))
+                 : (fc == 2 ? make_uint2(q[4], q[5]) : make_uint2(q[6], q[7]));
+    }
 #pragma unroll
     for (int m = 0; m < NMT; ++m) {
       const int r = cur.r0 + m * 16 + fr;
