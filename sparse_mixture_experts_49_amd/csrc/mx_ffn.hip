@@ -28,8 +28,8 @@ namespace moe {
 // at piece ^ (row % 16) (256 B rows) or piece ^ ((row >> 1) & 7) (128 B rows): 16 rows' reads
 // of one piece touch every bank once.
 // With `splits` > 1 a tile is one part of k, summed into `partial`.
-// 32 tokens x 2 of 8 experts, d = 4096, F = 14336: up 51 to 55 us, down 41 us: 4.6 and 6.1 TB/s
-// of codes and scales.  (Up's last round has half the blocks; giving those tiles to all blocks
+// 32 tokens x 2 of 8 experts, d = 4096, F = 14336, weights from memory: up 53 us, down 48: 4.7
+// and 5.2 TB/s of codes and scales, a copy's 4.8 read and written.  (Up's last round has half the blocks; giving those tiles to all blocks
 // by halves measured the same: the bytes take their time either way.)
 // ---------------------------------------------------------------------------
 constexpr int kStreamWaves = 8, kStreamCols = kStreamWaves * 16, kStreamBlocks = 256;
@@ -319,9 +319,9 @@ size_t mx_partial_bytes(int T, int k, int E, int N, int K) {
 
 // Experts averaging many rows run the LDS-tiled kernel, the rest stream: from 32 rows with
 // fp4 activations, whose matrix products take a quarter of the time, from 56 with bf16 ones.
-// Streamed and tiled, us: E = 8, K = 4096, N = 14336: fp4 24 rows 72 and 68, 36 rows 120 and
-// 68; bf16 48 rows 120 and 119, 72 rows 180 and 123.  E = 64, K = 2048, N = 1408: fp4 24 rows 36
-// and 40, 36 rows 54 and 40; bf16 48 rows 62 and 66, 72 rows 89 and 74.  The tiled kernel's loads
+// Streamed and tiled, us: E = 8, K = 4096, N = 14336: fp4 24 rows 70 and 66, 36 rows 119 and
+// 67; bf16 48 rows 115 and 119, 72 rows 179 and 120.  E = 64, K = 2048, N = 1408: fp4 24 rows 36
+// and 39, 36 rows 54 and 40; bf16 48 rows 61 and 65, 72 rows 89 and 73.  The tiled kernel's loads
 // run up to two steps of 256 k ahead, so it starts at k = 512.
 static bool tiled(long rows, int E, int K, bool fp4) { return rows >= (fp4 ? 32L : 56L) * E && K >= 512; }
 
@@ -350,8 +350,8 @@ static void launch_stream(const MxFfnArgs& a, const void* act, hipStream_t s) {
   p.splits = splits;
   p.partial = a.partial;
   // Tiles of 16 rows and runs of 512 while experts average at most 12, else 32 rows and runs
-  // of 256 (the activations' share of the LDS): E = 8, K = 4096, N = 14336, 12 rows 48 and 51 us,
-  // 18 rows 84 and 71; E = 64, K = 2048, N = 1408, 9 rows 23.6 and 24.5 us, 18 rows 37 and 32.
+  // of 256 (the activations' share of the LDS): E = 8, K = 4096, N = 14336, 12 rows 45 and 50 us,
+  // 18 rows 75 and 69; E = 64, K = 2048, N = 1408, 9 rows 22 and 24 us, 18 rows 33 and 32.
   if ((long)R <= 12L * a.E) mx_stream_kernel<UP, 1, 512, 3><<<kStreamBlocks, 512, 0, s>>>(p);
   else mx_stream_kernel<UP, 2, 256, 4><<<kStreamBlocks, 512, 0, s>>>(p);
   if (splits > 1)
