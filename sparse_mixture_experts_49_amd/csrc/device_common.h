@@ -188,6 +188,13 @@ __device__ __forceinline__ float exp_f32(float x) {
 }
 __device__ __forceinline__ float sigmoid_f32(float x) { return __builtin_amdgcn_rcpf(1.f + exp_f32(-x)); }
 
+// sigmoid(x) and 1 - sigmoid(x), each to fp32: the difference itself would keep few bits of it.
+__device__ __forceinline__ void sigmoid_pair(float x, float& s, float& rest) {
+  const float t = exp_f32(-fabsf(x)), big = 1.f / (1.f + t), small = t * big;
+  s = x < 0.f ? small : big;
+  rest = x < 0.f ? big : small;
+}
+
 __device__ __forceinline__ int lane_id() { return __lane_id(); }
 
 }  // namespace moe

@@ -1,7 +1,7 @@
 // Gradients of the scored router on gfx950.
 //
 // For each token, with g = d topk_w, chosen scores r_j = s[idx_j], S = sum r + 1e-20:
-//   dr_j = scale g_j, or renormalised (scale g_j - sum_i g_i w_i) / S
+//   dr_j = scale g_j, or renormalised scale sum_i r_i (g_j - g_i) / S^2
 //   dq_e = d_aux E load_e / (T k) / T          (q = s / sum s; load is a constant)
 //   softmax: ds = dr + dq;                       dl = s (ds - sum ds s)
 //   sigmoid: ds = dr + (dq - sum dq q) / sum s;  dl = ds s (1 - s)
@@ -57,7 +57,7 @@ int score_grad_sum_blocks(int T) { return grad_blocks(T); }
 // dl of tiles of TT tokens, one at a time per wave, lane l the experts l, l + 64, ... and for
 // the chosen ones lane q < k the q-th.  Bound by instruction issue, so straight-line: experts
 // behind E and slots behind k carry zeros, what depends on an argument is computed with 0 where
-// it is absent.  16384 tokens, 256 experts, k = 8: 22 us for 34 MB.
+// it is absent.  16384 tokens, 256 experts, k = 8: 24 us for 34 MB.
 template <int PER, int TT, bool SIGMOID>
 __global__ __launch_bounds__(TT * 16) void score_dlogits_kernel(ScoreGradArgs a) {
   constexpr int WAVES = TT / 4, kThreads = TT * 16, kPitch = 64 * PER;
@@ -78,7 +78,7 @@ __global__ __launch_bounds__(TT * 16) void score_dlogits_kernel(ScoreGradArgs a)
   }
   for (int t0 = blockIdx.x * TT; t0 < T; t0 += gridDim.x * TT) {
     for (int t = t0 + wave; t < min(t0 + TT, T); t += WAVES) {
-      float l[PER], p[PER], s[PER];
+      float l[PER], p[PER], s[PER], rest[SIGMOID ? PER : 1];   // rest: 1 - s
 #pragma unroll
       for (int j = 0; j < PER; ++j) l[j] = a.logits[(size_t)t * E + min(j * 64 + lane, E - 1)];
       int idx = a.topk_idx[(size_t)t * k + min(lane, k - 1)];
@@ -106,7 +106,10 @@ __global__ __launch_bounds__(TT * 16) void score_dlogits_kernel(ScoreGradArgs a)
         for (int j = 0; j < PER; ++j) p[j] = 0.f;
       }
 #pragma unroll
-      for (int j = 0; j < PER; ++j) s[j] = SIGMOID ? sigmoid_f32(l[j]) : p[j];
+      for (int j = 0; j < PER; ++j) {
+        if constexpr (SIGMOID) sigmoid_pair(l[j], s[j], rest[j]);
+        else s[j] = p[j];
+      }
       // Chosen scores and the gradients of the raw weights, lane q those of choice q.
       float r = 0.f;
 #pragma unroll
@@ -116,8 +119,16 @@ __global__ __launch_bounds__(TT * 16) void score_dlogits_kernel(ScoreGradArgs a)
         r = idx >> 6 == j ? v : r;                     // idx -1: none
       }
       if (a.renorm) {
-        const float rS = 1.f / (wave_sum_f(r) + 1e-20f), gw = wave_sum_f(g * r);
-        g = a.scale * (g - gw * rS) * rS;
+        // g_j S - sum_i g_i r_i by differences: with one choice, or equal gradients, 0.
+        const float rS = 1.f / (wave_sum_f(r) + 1e-20f);
+        float v = 1e-20f * g;
+#pragma unroll
+        for (int q = 0; q < 8; ++q) {
+          const float rq = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(r), q));
+          const float gq = __uint_as_float((uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(g), q));
+          v = fmaf(rq, g - gq, v);
+        }
+        g = a.scale * (v * rS) * rS;
       } else {
         g *= a.scale;
       }
@@ -147,7 +158,7 @@ __global__ __launch_bounds__(TT * 16) void score_dlogits_kernel(ScoreGradArgs a)
           for (int j = 0; j < PER; ++j) ds[j] = fmaf(dq[j] - cq, rs, ds[j]);
         }
 #pragma unroll
-        for (int j = 0; j < PER; ++j) dl[j] = ds[j] * s[j] * (1.f - s[j]);
+        for (int j = 0; j < PER; ++j) dl[j] = ds[j] * s[j] * rest[j];
       } else {
         float cs = 0.f;
 #pragma unroll

@@ -379,3 +379,22 @@ def test_own_workspace_on_another_stream(monkeypatch):
         torch.cuda.synchronize()
         for name in ("topk_idx", "topk_w", "logits", "load", "prob_mean", "aux", "z_loss"):
             assert torch.equal(getattr(r, name), getattr(want, name)), name
+
+
+def test_backward_where_differences_cancel():
+    """One renormalised choice has weight `scale` whatever its score, so nothing flows through
+    it but the 1e-20 beside its score; and saturated sigmoid scores, whose 1 - s is a small
+    part of an ulp of s: every d_logits is good to the roundings of its own size (exp and its
+    argument, the division, eight products)."""
+    T, d, E = 33, 128, 16
+    for kind in ("softmax", "sigmoid"):
+        x, w, l, idx, load, dw = _grad_inputs(T, d, E, 1, "f32", 3)
+        got = _backward(_desc(T, d, E, 1, kind, scale=1.9, dtype="f32"), x, w, l, idx, load, dw, None, None)
+        assert torch.all(got.d_logits.abs() <= 1e-18) and torch.all(got.d_x.abs() <= 1e-15)
+    x, w, l, idx, load, dw = _grad_inputs(T, d, E, 3, "f32", 4)
+    l = 6 * l.abs() + 1                                     # up to about 20: 1 - s about 2e-9
+    idx = l.topk(3, 1).indices.to(torch.int32)
+    got = _backward(_desc(T, d, E, 3, "sigmoid", renorm=False, dtype="f32"), x, w, l, idx, load, dw, None, None)
+    s = torch.sigmoid(l.double())
+    want = torch.zeros_like(s).scatter_(1, idx.long(), dw.double()) * s * torch.exp(-l.double()) * s
+    assert torch.all((got.d_logits.cpu().double() - want).abs() <= 12 * U32 * want.abs())
