@@ -529,6 +529,9 @@ __global__ __launch_bounds__(1024) void score_reduce_kernel(ScoreArgs a, int blo
     }
   }
   if (!a.aux && !a.z_loss) return;
+  // The release below waits for its own wave's stores only, and a barrier for none: each wave
+  // has its share in L2 before it arrives there.
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");
   __syncthreads();
   if (threadIdx.x == 0)
     last = __hip_atomic_fetch_add(a.done, 1u, __ATOMIC_ACQ_REL, __HIP_MEMORY_SCOPE_AGENT) == gridDim.x - 1;

@@ -398,3 +398,25 @@ def test_backward_where_differences_cancel():
     s = torch.sigmoid(l.double())
     want = torch.zeros_like(s).scatter_(1, idx.long(), dw.double()) * s * torch.exp(-l.double()) * s
     assert torch.all((got.d_logits.cpu().double() - want).abs() <= 12 * U32 * want.abs())
+
+
+def test_losses_are_of_this_call():
+    """The losses are summed by whichever block of experts ends last, from what the others
+    left in the workspace.  Two batches that give very different shares take turns on one
+    workspace, many times: each aux is that of its own loads and mean probabilities (fp32
+    outputs: two roundings of each term, one of the result)."""
+    T, d, E, k = 64, 128, 256, 8
+    desc = _desc(T, d, E, k, "softmax")
+    x, w, _ = _grid_inputs(desc, 9)
+    b = torch.linspace(-4, 4, E)
+    ws, biases = _poison(desc), (b.to(DEV), b.flip(0).contiguous().to(DEV))
+    runs = [moe.ScoreRouting.allocate(desc, DEV, train=True) for _ in range(200)]
+    x, w = x.to(DEV), w.to(DEV)
+    torch.cuda.synchronize()
+    for i, r in enumerate(runs):
+        moe.moe_score_route(desc, x, w, r, b_router=biases[i % 2], workspace=ws)
+    torch.cuda.synchronize()
+    for i, r in enumerate(runs):
+        want = E * float((r.load.double() / (T * k) * r.prob_mean.double()).sum())
+        assert abs(float(r.aux) - want) <= 4 * U32 * want, i
+        assert torch.equal(r.aux, runs[i % 2].aux) and torch.equal(r.z_loss, runs[i % 2].z_loss), i
