@@ -6,6 +6,7 @@
 //   softmax: ds = dr + dq;                       dl = s (ds - sum ds s)
 //   sigmoid: ds = dr + (dq - sum dq q) / sum s;  dl = ds s (1 - s)
 //   dl += d_z (2 / T) lse softmax(l)
+// The differences with a sum over all experts are formed as of_leader says.
 // and d_b = sum_t dl, d_x = dl W_r, d_W = dl^T x.
 //
 // bf16 layers: x and W_r go to the bf16 MFMA as they are and dl as a sum of bf16 terms,
@@ -53,6 +54,26 @@ static int dl_pitch(int E) { return E <= 64 ? 64 : up_to(E, kGradRows); }
 
 size_t score_dl_bytes(const ScoreShape& s) { return (size_t)up_to(s.T, kGradK) * dl_pitch(s.E) * 4; }
 int score_grad_sum_blocks(int T) { return grad_blocks(T); }
+
+// The v of the expert with more than `half` (half of all) of a token's score, 0 if none has.
+// v_i - sum_j v_j s_j does not change when a constant is taken off every v.  With the leader's
+// own value taken off, its difference is the small sum of what the others get instead of two
+// nearly equal numbers, and no other's is less exact; without a leader nothing cancels.
+template <int PER>
+__device__ __forceinline__ float of_leader(const float (&s)[PER], float half, const float (&v)[PER]) {
+  float u = 0.f;
+  bool mine = false;
+#pragma unroll
+  for (int j = 0; j < PER; ++j) {
+    const bool it = s[j] > half;                         // one expert at most
+    u = it ? v[j] : u;
+    mine |= it;
+  }
+  const uint64_t at = __ballot(mine);
+  uint32_t c = (uint32_t)__builtin_amdgcn_readlane((int)__float_as_uint(u), (__ffsll((unsigned long long)at) - 1) & 63);
+  c = at ? c : 0u;
+  return __uint_as_float((c & 0x7f800000u) == 0x7f800000u ? 0u : c);   // infinite: off nothing
+}
 
 // dl of tiles of TT tokens, one at a time per wave, lane l the experts l, l + 64, ... and for
 // the chosen ones lane q < k the q-th.  Bound by instruction issue, so straight-line: experts
@@ -147,23 +168,25 @@ __global__ __launch_bounds__(TT * 16) void score_dlogits_kernel(ScoreGradArgs a)
         if (a.d_aux) {
           float cq = 0.f, ss = 0.f;
 #pragma unroll
-          for (int j = 0; j < PER; ++j) {
-            ss += s[j];
-            cq = fmaf(dq[j], s[j], cq);
-          }
+          for (int j = 0; j < PER; ++j) ss += s[j];
           ss = wave_sum_f(ss);
-          const float rs = 1.f / (ss < 1e-20f ? 1e-20f : ss);
+          const float rs = 1.f / (ss < 1e-20f ? 1e-20f : ss), c = of_leader(s, 0.5f * ss, dq);
+#pragma unroll
+          for (int j = 0; j < PER; ++j) cq = fmaf(dq[j] - c, s[j], cq);
           cq = wave_sum_f(cq) * rs;
 #pragma unroll
-          for (int j = 0; j < PER; ++j) ds[j] = fmaf(dq[j] - cq, rs, ds[j]);
+          for (int j = 0; j < PER; ++j) ds[j] = fmaf(dq[j] - c - cq, rs, ds[j]);
         }
 #pragma unroll
         for (int j = 0; j < PER; ++j) dl[j] = ds[j] * s[j] * rest[j];
       } else {
         float cs = 0.f;
 #pragma unroll
+        for (int j = 0; j < PER; ++j) ds[j] += dq[j];
+        const float c = of_leader(s, 0.5f, ds);
+#pragma unroll
         for (int j = 0; j < PER; ++j) {
-          ds[j] += dq[j];
+          ds[j] -= c;
           cs = fmaf(ds[j], s[j], cs);
         }
         cs = wave_sum_f(cs);

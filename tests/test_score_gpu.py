@@ -420,3 +420,75 @@ def test_losses_are_of_this_call():
         want = E * float((r.load.double() / (T * k) * r.prob_mean.double()).sum())
         assert abs(float(r.aux) - want) <= 4 * U32 * want, i
         assert torch.equal(r.aux, runs[i % 2].aux) and torch.equal(r.z_loss, runs[i % 2].z_loss), i
+
+
+def _saturated(l, E, g):
+    """Logits where one expert leads the others by 6 to 17; multiples of 2^-6 up to 32, so that
+    differences of logits are exact in fp32."""
+    T = l.shape[0]
+    l = (l * 64).round() / 64
+    lead = torch.randint(0, E, (T,), generator=g)
+    gap = 6 + 11 * torch.rand(T, generator=g)
+    top = ((l.amax(1) + gap) * 64).round() / 64
+    return l.scatter(1, lead[:, None], top[:, None])
+
+
+@pytest.mark.parametrize("renorm", [False, True], ids=["raw", "renorm"])
+@pytest.mark.parametrize("T,E,k,dtype", [(33, 16, 1, "f32"), (70, 60, 4, "f32"), (257, 256, 8, "bf16")])
+def test_backward_of_saturated_softmax(T, E, k, dtype, renorm):
+    """Where one score is nearly 1 its gradient is the small sum of what the others get, and
+    is good to the roundings of that: dl_i = s_i sum_j s_j (ds_i - ds_j), so an error of a few
+    roundings of s_i (|ds_i| (1 - s_i) + sum_{j != i} |ds_j| s_j).  Counted in halves of a step:
+    a score 18 (exp 4, a sum of 256 terms 10, division, product), a renormalised weight's
+    gradient 66 more (a score, and 22 for each of the two 1 / S), twice a score and a sum in
+    dl: under 128."""
+    d = 128
+    x, w, l, _, _, dw = _grad_inputs(T, d, E, k, dtype, 21)
+    g = torch.Generator().manual_seed(22)
+    l = _saturated(l, E, g)
+    idx = l.topk(k, 1).indices.to(torch.int32)
+    idx[::3, 0] = torch.randint(0, E, (len(idx[::3]),), generator=g).to(torch.int32)   # not always the leader
+    load = torch.bincount(idx.flatten().long(), minlength=E).to(torch.int32)
+    desc = _desc(T, d, E, k, "softmax", renorm=renorm, scale=1.5, dtype=dtype)
+    s = torch.softmax(l.double(), 1)
+    r = torch.take_along_dim(s, idx.long(), 1)
+    S = r.sum(1, keepdim=True) + 1e-20
+    diff = dw.double()[:, :, None] - dw.double()[:, None, :]
+    for da in (None, 0.7 * T):
+        if renorm:
+            dr = 1.5 * ((diff * r[:, None]).sum(2) + 1e-20 * dw) / S ** 2
+            dr_size = 1.5 * ((diff.abs() * r[:, None]).sum(2) + 1e-20 * dw.abs()) / S ** 2
+        else:
+            dr, dr_size = 1.5 * dw.double(), 1.5 * dw.double().abs()
+        dq = 0.0 if da is None else da * E * load.double() / (T * k) / T
+        ds = torch.zeros_like(s).scatter_add_(1, idx.long(), dr) + dq
+        size = torch.zeros_like(s).scatter_add_(1, idx.long(), dr_size) + dq
+        rest = torch.stack([s[:, torch.arange(E) != i].sum(1) for i in range(E)], 1)
+        want = torch.stack([s[:, i] * (s * (ds[:, i:i + 1] - ds)).sum(1) for i in range(E)], 1)
+        room = s * (size * rest + (size * s).sum(1, keepdim=True) - size * s)
+        got = _backward(desc, x, w, l, idx, load, dw, da, None)
+        err = (got.d_logits.cpu().double() - want).abs()
+        assert torch.all(err <= 128 * U32 * room), float((err / (U32 * room)).nan_to_num().max())
+        room = 128 * U32 * room.sum(0) + 2 * U32 * want.sum(0).abs()
+        assert torch.all((got.d_b_router.cpu().double() - want.sum(0)).abs() <= room)
+
+
+@pytest.mark.parametrize("T,E,dtype", [(33, 16, "f32"), (257, 256, "bf16")])
+def test_backward_of_the_balance_loss_where_one_sigmoid_leads(T, E, dtype):
+    """The same for q = s / sum s of sigmoid scores, one of them nearly all of the sum:
+    dl_i = s_i (1 - s_i) / S sum_j q_j (dq_i - dq_j)."""
+    d, k, da = 128, 2, 0.7 * T
+    x, w, l, _, _, dw = _grad_inputs(T, d, E, k, dtype, 23)
+    l = _saturated(l, E, torch.Generator().manual_seed(24))
+    l = l - l.amax(1, keepdim=True) + torch.arange(T)[:, None] % 5 - 2          # leaders at -2 to 2
+    idx = l.topk(k, 1).indices.to(torch.int32)
+    load = torch.bincount(idx.flatten().long(), minlength=E).to(torch.int32)
+    s = torch.sigmoid(l.double())
+    S = s.sum(1, keepdim=True)
+    q, dq = s / S, da * E * load.double() / (T * k) / T
+    want = torch.stack([(q * (dq[i] - dq)).sum(1) for i in range(E)], 1) / S * s * torch.sigmoid(-l.double())
+    rest = torch.stack([q[:, torch.arange(E) != i].sum(1) for i in range(E)], 1)
+    room = (dq * rest + (dq * q).sum(1, keepdim=True) - dq * q) / S * s * torch.sigmoid(-l.double())
+    got = _backward(_desc(T, d, E, k, "sigmoid", dtype=dtype), x, w, l, idx, load, torch.zeros(T, k), da, None)
+    err = (got.d_logits.cpu().double() - want).abs()
+    assert torch.all(err <= 128 * U32 * room), float((err / (U32 * room)).nan_to_num().max())
