@@ -492,3 +492,64 @@ def test_backward_of_the_balance_loss_where_one_sigmoid_leads(T, E, dtype):
     got = _backward(_desc(T, d, E, k, "sigmoid", dtype=dtype), x, w, l, idx, load, torch.zeros(T, k), da, None)
     err = (got.d_logits.cpu().double() - want).abs()
     assert torch.all(err <= 128 * U32 * room), float((err / (U32 * room)).nan_to_num().max())
+
+
+def _may_cross(v, err, n):
+    """Rows where, with every value off by up to its error, the n best may come out in another
+    order or with another member."""
+    v, at = v.sort(1, descending=True)
+    err = torch.take_along_dim(err, at, 1)
+    lowest = (v - err).cummin(1).values[:, :-1]                    # of those up to here
+    highest = (v + err).flip(1).cummax(1).values.flip(1)[:, 1:]    # of those after
+    return (lowest <= highest)[:, :n].any(1)
+
+
+def _close_choices(l, kind, bs, k, G, tg, gtop, off):
+    """Tokens whose choice hangs on logits that are off by `off`: a score is off by that times
+    its slope (at most 1/4; softmax: the score, once for its own logit and once for the sum)
+    and the roundings of scores and sums."""
+    s, b = R.scores(l, kind), bs.double()
+    T, E = l.shape
+    v = s + b
+    err = (off / 4 if kind == "sigmoid" else 2 * off * s) + 32 * U32 * s + U32 * v.abs()
+    close = torch.zeros(T, dtype=torch.bool)
+    if G > 1:
+        best, at = v.view(T, G, E // G).topk(gtop, 2)
+        value = best.sum(2)
+        # a group's best may be another of its experts, none of which is off by more
+        e = gtop * err.view(T, G, E // G).amax(2) + U32 * value.abs()
+        keep = torch.zeros(T, G).scatter_(1, value.topk(tg, 1).indices, 1.0) > 0
+        if tg < G:
+            inf = float("inf")
+            close |= (value - e).masked_fill(~keep, inf).amin(1) <= (value + e).masked_fill(keep, -inf).amax(1)
+        keep = keep.repeat_interleave(E // G, 1)
+        v, err = v[keep].view(T, -1), err[keep].view(T, -1)
+    return close | _may_cross(v, err, k)
+
+
+@pytest.mark.parametrize("T,d,E,k,kind,G,tg,gtop,dtype", [
+    (1, 4096, 256, 8, "sigmoid", 8, 4, 2, "bf16"), (40, 4096, 64, 6, "softmax", 1, 1, 1, "bf16"),
+    (300, 2048, 160, 6, "softmax", 8, 3, 1, "f32"), (1500, 1024, 256, 8, "sigmoid", 8, 4, 2, "bf16"),
+    (5000, 512, 128, 4, "softmax", 4, 2, 2, "bf16"), (900, 768, 60, 8, "sigmoid", 1, 1, 1, "f32"),
+])
+def test_every_clear_choice_is_made(T, d, E, k, kind, G, tg, gtop, dtype):
+    """Gaussian inputs with a selection bias, logits good to 2e-5 (see above): every token
+    whose choice does not hang on that is routed as in 64 bits, and those are nearly all."""
+    g = torch.Generator().manual_seed(E + T)
+    dt = torch.bfloat16 if dtype == "bf16" else torch.float32
+    x, w = torch.randn(T, d, generator=g).to(dt), (torch.randn(E, d, generator=g) * d ** -0.5).to(dt)
+    bs = torch.randn(E, generator=g) * (0.02 if kind == "sigmoid" else 0.1 / E)
+    desc = _desc(T, d, E, k, kind, G, tg, gtop, dtype=dtype)
+    l = x.double() @ w.double().T
+    ref = R.forward(l, kind, bs.double(), k, G, tg, gtop)
+    close = _close_choices(l, kind, bs, k, G, tg, gtop, 2e-5)
+    assert close.float().mean() <= 0.03
+    r = _run(desc, x, w, None, bs)
+    assert torch.all((r.logits.cpu().double() - l).abs() <= 2e-5)
+    same = (r.topk_idx.cpu().long() == ref["idx"]).all(1)
+    assert torch.all(same | close)
+    # dw / w: the logit's error twice (own and the renormalising sum's), and the roundings.
+    err = (r.topk_w.cpu().double() - ref["w"]).abs() / ref["w"]
+    assert torch.all(err[same] <= 2 * 2e-5 + 32 * U32)
+    load = torch.bincount(r.topk_idx.cpu().long().flatten(), minlength=E)
+    assert torch.equal(r.load.cpu().long(), load)
