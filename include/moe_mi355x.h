@@ -467,7 +467,8 @@ int moe_mx_dispatch(const moe_mx_desc* desc, moe_routing* r, void* workspace,
                     size_t workspace_bytes, void* stream);
 
 /* h[r] = GELU_erf(a[r] W1_e^T + b1_e), bf16 [T*k][F], for every row r of expert e's
- * segment; rows past the last segment are not written.  With src (the dispatch's
+ * segment; rows past the last segment are not written.  GELU of +inf is +inf, of -inf and
+ * NaN it is NaN (z Phi(z) in fp32).  With src (the dispatch's
  * [T*k]) a[r] is x[src[r] / k], x [T][d] bf16; src NULL: x is [T*k][d], a[r] = x[r]. */
 int moe_mx_ffn_up(const moe_mx_desc* desc, const void* x, const int32_t* src,
                   const int32_t* offsets, const moe_mx_weights* w, void* h, void* workspace,

@@ -118,9 +118,11 @@ __device__ __forceinline__ float gelu_erf(float z) {
 
 // The same for a result that is rounded to bf16 next: Phi(-|z|) = exp2(q(|z|)) with q of
 // degree 7 fitted to log2 Phi(-x) on [0, 7], so one transcendental instead of two.  Relative
-// error of that term under 1.3e-5, 1/300 of the rounding's; past 7 q falls on to -inf.
+// error of the term |z| Phi(-|z|) under 1.3e-5 there, 1/300 of the rounding's; past 7, where
+// the term itself is under 1e-11, q falls on to -inf.  Positive z is cut at 1e4 in the term
+// (0 from far below), so that +inf stays +inf; -inf and NaN give NaN, as z Phi(z) does.
 __device__ __forceinline__ float gelu_for_bf16(float z) {
-  const float x = fabsf(z);
+  const float x = fabsf(__builtin_elementwise_minimum(z, 1e4f));   // keeps NaN, as fminf would not
   float q = fmaf(-1.5882183106441516e-06f, x, 5.615340342046693e-05f);
   q = fmaf(q, x, -0.0008832158055156469f);
   q = fmaf(q, x, 0.008303220383822918f);

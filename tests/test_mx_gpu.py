@@ -419,3 +419,32 @@ def test_forward_on_the_tiled_path(act):
         graph.replay()
         torch.cuda.synchronize()
         assert torch.equal(y, want) and torch.equal(eager, want)
+
+
+@pytest.mark.parametrize("act", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("T,d,F", [(3, 4096, 256), (40, 128, 256), (300, 512, 256)], ids=["split", "streamed", "tiled"])
+def test_gelu_of_overflow_and_infinite_bias(T, d, F, act):
+    """z = +inf is +inf, z = -inf and z = NaN are NaN (-inf * 0 in z Phi(z)): from a bias, and
+    from a product past fp32's range; the largest finite z stays itself."""
+    desc = moe.MxDesc(T, d, F, 1, 1, act=act)
+    codes = torch.zeros(1, F, d // 2, dtype=torch.uint8)
+    scales = torch.full((1, F, d // 32), 127, dtype=torch.uint8)
+    codes[0, :, 0], scales[0, :, 0] = 0x02, 127 + 100        # column n: 2^100 times the token's first value
+    x = torch.zeros(T, d).bfloat16()
+    x[:, 0] = 2.0 ** -100
+    x[T // 2:, 0] = 2.0 ** 100                               # 2^200 in all columns
+    x[T // 2::2, 0] = -2.0 ** 100
+    bias = torch.zeros(1, F).bfloat16()
+    inf = float("inf")
+    bias[0, :5] = torch.tensor([inf, -inf, float("nan"), 3e38, -3e38]).bfloat16()
+    h = torch.full((T, F), -77.0, device=DEV).bfloat16()
+    moe.moe_mx_ffn_up(desc, x.to(DEV), torch.tensor([0, T], dtype=torch.int32, device=DEV),
+                      moe.MxWeights(w1=codes.to(DEV), s1=scales.to(DEV), b1=bias.to(DEV)), h, workspace=_poisoned(desc))
+    z = x[:, :1].double() * 2.0 ** 100
+    z = torch.where(z.abs() > 3.4e38, z * inf, z) + bias.double()
+    want = torch.where(z == inf, inf, torch.where((z == -inf) | z.isnan(), float("nan"), R.gelu(z)))
+    want = torch.where(z == bias[0, 3].double(), z, torch.where(z == bias[0, 4].double(), 0.0, want))
+    got = h.cpu().double()
+    assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got == inf, want == inf)
+    fine = want.isfinite()
+    assert torch.all((got - want)[fine].abs() <= 2 * U16 * want[fine].abs())
