@@ -448,3 +448,48 @@ def test_gelu_of_overflow_and_infinite_bias(T, d, F, act):
     assert torch.equal(got.isnan(), want.isnan()) and torch.equal(got == inf, want == inf)
     fine = want.isfinite()
     assert torch.all((got - want)[fine].abs() <= 2 * U16 * want[fine].abs())
+
+
+@pytest.mark.parametrize("act", ["bf16", "mxfp4"])
+@pytest.mark.parametrize("T,k,E,d,F", [(300, 2, 4, 512, 512), (450, 4, 16, 640, 384), (600, 8, 8, 1024, 1408)])
+def test_nan_scales_and_tokens_in_tiled_products(T, k, E, d, F, act):
+    """Experts that average 56 rows or more over k >= 512: a block of weights whose scale is NaN
+    makes its column of its expert NaN and nothing else, a NaN token its own rows, an infinite
+    activation no row but its own."""
+    L = _layer(T, k, E, d, F, False, 9)
+    e, n = 1, F - 100
+    s1 = L["w1"][1].view(E, F, d // 32)
+    old = int(s1[e, n, d // 32 - 1])
+    s1[e, n, d // 32 - 1] = 255
+    desc = moe.MxDesc(T, d, F, E, k, act=act, has_expert_bias=False)
+    off, src, rows = L["offsets"].to(DEV), L["src"].to(DEV), L["rows"]
+    h = torch.zeros(T * k, F, dtype=torch.bfloat16, device=DEV)
+    moe.moe_mx_ffn_up(desc, L["x"].to(DEV), off, _weights(L), h, src=src, workspace=_poisoned(desc))
+    want = torch.zeros(T * k, F, dtype=torch.bool)
+    want[int(L["offsets"][e]):int(L["offsets"][e + 1]), n] = True
+    assert torch.equal(h.cpu().isnan(), want) and not h.isinf().any()
+    s1[e, n, d // 32 - 1] = old
+    for bad in (float("nan"), float("inf")):
+        x = L["x"].clone()
+        x[2, d - 3], x[T - 1, 0] = bad, bad
+        moe.moe_mx_ffn_up(desc, x.to(DEV), off, _weights(L), h, src=src, workspace=_poisoned(desc))
+        mine = torch.zeros(T * k, dtype=torch.bool)
+        token = L["src"][:rows] // k
+        mine[:rows] = (token == 2) | (token == T - 1)
+        got = h.cpu()
+        assert got[~mine].isfinite().all()
+        if act == "mxfp4" or bad != bad:                       # the block's scale is NaN
+            assert got[mine].isnan().all()
+        else:
+            assert not got[mine].isfinite().any()
+    # The second product, h with a NaN and its weights with a NaN scale.
+    s2 = L["w2"][1].view(E, d, F // 32)
+    s2[E - 1, 5, 0] = 255
+    a = torch.nn.functional.gelu(torch.randn(T * k, F, generator=L["gen"])).bfloat16()
+    a[7, F - 1] = float("nan")
+    o = torch.zeros(T * k, d, device=DEV)
+    moe.moe_mx_ffn_down(desc, a.to(DEV), off, _weights(L), o, workspace=_poisoned(desc))
+    want = torch.zeros(T * k, d, dtype=torch.bool)
+    want[int(L["offsets"][E - 1]):int(L["offsets"][E]), 5] = True
+    want[7] = True
+    assert torch.equal(o.cpu().isnan(), want)
