@@ -275,7 +275,9 @@ int moe_shared_ffn(const moe_desc* desc, const void* x, const moe_weights* w, fl
  * in slot order (no atomics), plus o_shared[t] when o_shared is not NULL;
  * without a shared expert y[t] = 0 when every slot was dropped.
  *   o [T*k][d] fp32, dest [T][k], topk_w [T][k] fp32, o_shared [T][d] fp32 or
- *   NULL, y [T][d] fp32. */
+ *   NULL, y [T][d] fp32.
+ * Here desc->n_experts may be up to 256, for the layouts of moe_mx_dispatch; of the
+ * descriptor only tokens, d_model and top_k enter the result. */
 int moe_combine(const moe_desc* desc, const float* o, const int32_t* dest, const float* topk_w,
                 const float* o_shared, float* y, void* stream);
 
@@ -336,8 +338,8 @@ int moe_forward_noalloc(const moe_desc* desc, const void* x, const moe_weights* 
  *   prob_mean_e mean of q_e, q = s / sum(s) for sigmoid scores, s for softmax
  *   aux         E * sum_e load_e / (T k) * prob_mean_e
  *   z_loss      mean of (log sum_e exp l_e)^2
- * topk_idx and topk_w feed moe_permute, moe_combine (up to 64 experts),
- * moe_mx_dispatch and moe_mx_forward.  d_model is a multiple of 128.
+ * topk_idx and topk_w feed moe_permute (up to 64 experts), moe_mx_dispatch,
+ * moe_combine and moe_mx_forward.  d_model is a multiple of 128.
  * The calls use their workspace until they have run: calls, or replays of captured
  * ones, that may overlap need one each. */
 enum { MOE_SCORE_SOFTMAX = 0, MOE_SCORE_SIGMOID = 1 };

@@ -411,6 +411,8 @@ def moe_shared_ffn(desc, x, weights, o_shared, workspace=None, stream=None):
 
 
 def moe_combine(desc, o, dest, topk_w, y, o_shared=None, stream=None):
+    """Weighted sum of each token's expert rows; desc may have up to 256 experts here (the
+    layouts of moe_mx_dispatch), of it only tokens, d_model and top_k enter."""
     a = _Args(desc, o)
     _check(load_library().moe_combine(ctypes.byref(desc.to_c()), a.t(o, "o"), a.t(dest, "dest"),
                                       a.t(topk_w, "topk_w"), a.t(o_shared, "o_shared"), a.t(y, "y"),

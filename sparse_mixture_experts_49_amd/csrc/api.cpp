@@ -24,12 +24,12 @@ namespace {
 // switch-style layers) and h is kept as two bf16 terms.
 bool renormalised_or_multi(const moe_desc* d) { return d->top_k > 1 || d->renormalize != 0; }
 
-int validate_desc(const moe_desc* d) {
+int validate_desc(const moe_desc* d, int most_experts = 64) {
   if (!d) return fail(MOE_ERR_INVALID, "desc must not be NULL");
   if (d->tokens < 1) return fail(MOE_ERR_INVALID, "tokens must be >= 1 (got %d)", d->tokens);
   if (d->n_experts < 1) return fail(MOE_ERR_INVALID, "n_experts must be >= 1 (got %d)", d->n_experts);
-  if (d->n_experts > 64)
-    return fail(MOE_ERR_UNSUPPORTED, "n_experts must be <= 64 (got %d)", d->n_experts);
+  if (d->n_experts > most_experts)
+    return fail(MOE_ERR_UNSUPPORTED, "n_experts must be <= %d (got %d)", most_experts, d->n_experts);
   if (d->top_k < 1 || d->top_k > d->n_experts)
     return fail(MOE_ERR_INVALID, "top_k must be in [1, n_experts] (got %d)", d->top_k);
   if (d->top_k > 8) return fail(MOE_ERR_UNSUPPORTED, "top_k must be <= 8 (got %d)", d->top_k);
@@ -736,7 +736,8 @@ int moe_grouped_ffn(const moe_desc* desc, const void* x_perm, const int32_t* off
 
 int moe_combine(const moe_desc* desc, const float* o, const int32_t* dest, const float* topk_w,
                 const float* o_shared, float* y, void* stream) {
-  if (int st = validate_desc(desc)) return st;
+  // The sum runs over slots, whose rows dest names: as many experts as the dispatches have.
+  if (int st = validate_desc(desc, 256)) return st;
   MOE_REQUIRE_PTR(o, "o");
   MOE_REQUIRE_PTR(dest, "dest");
   MOE_REQUIRE_PTR(topk_w, "topk_w");

@@ -123,3 +123,23 @@ def test_more_values_than_a_launch_has_threads(rows, cols):
     for st in (lib.moe_mx_quantize(0x1000, 1, rows, cols, cols, 0x8000, 0x9000, None),
                lib.moe_mx_dequantize(0x8000, 0x9000, rows, cols, 1, 0x1000, cols, None)):
         assert st == B.MOE_ERR_UNSUPPORTED and "2^34" in lib.moe_last_error().decode()
+
+
+def test_only_the_combine_takes_more_than_64_experts():
+    """moe_combine takes the layers of moe_mx_dispatch, up to 256 experts; the others of its
+    family keep to 64."""
+    lib = moe.load_library()
+
+    def combine(E, o=0x100000):
+        d = moe.Desc(4, 128, 128, E, 2)
+        return _err(lib.moe_combine(ctypes.byref(d.to_c()), o, 0x200000, 0x300000, None, 0x100100, None))
+
+    for E in (64, 65, 256):
+        st, msg = combine(E)
+        assert st == B.MOE_ERR_INVALID and "y overlaps o" in msg, msg
+        assert "o must not be NULL" in combine(E, o=None)[1]
+    st, msg = combine(257)
+    assert st == B.MOE_ERR_UNSUPPORTED and "256" in msg
+    with pytest.raises(moe.MoeError) as ei:
+        moe.moe_workspace_size(moe.Desc(4, 128, 128, 65, 2))
+    assert ei.value.status == B.MOE_ERR_UNSUPPORTED

@@ -493,3 +493,33 @@ def test_nan_scales_and_tokens_in_tiled_products(T, k, E, d, F, act):
     want[int(L["offsets"][E - 1]):int(L["offsets"][E]), 5] = True
     want[7] = True
     assert torch.equal(o.cpu().isnan(), want)
+
+
+@pytest.mark.parametrize("T,k,E", [(1, 8, 256), (200, 8, 256), (33, 3, 65), (70, 2, 160)])
+def test_combine_of_up_to_256_experts(T, k, E):
+    """The layer step by step with public calls only: moe_combine takes the layer's own number
+    of experts, bit for bit what moe_mx_forward gives."""
+    d, F = 384, 256
+    L = _layer(T, k, E, d, F, True, T + 1)
+    g = torch.Generator().manual_seed(T)
+    wr = (torch.randn(E, d, generator=g) * d ** -0.5).bfloat16().to(DEV)
+    route, desc = moe.ScoreDesc(T, d, E, k, score="sigmoid", scale=2.5), moe.MxDesc(T, d, F, E, k)
+    w, x, y = _weights(L), L["x"].to(DEV), torch.empty(T, d, device=DEV)
+    moe.moe_mx_forward(route, desc, x, wr, w, y)
+    r = moe.ScoreRouting.allocate(route, DEV)
+    moe.moe_score_route(route, x, wr, r)
+    i32 = dict(dtype=torch.int32, device=DEV)
+    lay = moe.Routing(topk_idx=r.topk_idx, counts=torch.empty(E, **i32), offsets=torch.empty(E + 1, **i32),
+                      dest=torch.empty(T, k, **i32), src=torch.empty(T * k, **i32))
+    moe.moe_mx_dispatch(desc, lay)
+    h, o = torch.empty(T * k, F, dtype=torch.bfloat16, device=DEV), torch.empty(T * k, d, device=DEV)
+    moe.moe_mx_ffn_up(desc, x, lay.offsets, w, h, src=lay.src)
+    moe.moe_mx_ffn_down(desc, h, lay.offsets, w, o)
+    y2 = torch.empty_like(y)
+    moe.moe_combine(moe.Desc(T, d, F, E, k), o, lay.dest, r.topk_w, y2)
+    assert torch.equal(y, y2)
+    want = torch.zeros(T, d, dtype=torch.float64)
+    for s in range(k):
+        want += r.topk_w[:, s, None].double().cpu() * o.cpu().double()[lay.dest[:, s].long().cpu()]
+    size = sum(r.topk_w[:, s, None].abs().double().cpu() * o.cpu().double()[lay.dest[:, s].long().cpu()].abs() for s in range(k))
+    assert torch.all((y2.cpu().double() - want).abs() <= k * U32 * size)
