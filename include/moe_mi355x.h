@@ -458,7 +458,8 @@ int moe_mx_quantize(const void* x, int dtype, int64_t rows, int64_t cols, int64_
 int moe_mx_dequantize(const uint8_t* codes, const uint8_t* scales, int64_t rows, int64_t cols,
                       int dtype, void* out, int64_t row_stride, void* stream);
 
-/* Bytes of workspace any call below needs for this descriptor (host output);
+/* Bytes of workspace any call below needs for this descriptor (host output): one size for
+ * all of them, moe_mx_forward's h and o included (T*k * (2 d_ff + 4 d_model) bytes).
  * moe_mx_forward needs moe_score_workspace_size of its router on top. */
 int moe_mx_workspace_size(const moe_mx_desc* desc, size_t* bytes);
 

@@ -178,9 +178,9 @@ __device__ __forceinline__ float wave_sum_f(float v) {
   }));
 }
 
-// e^x within ~2 ulp for every x: 2^(x log2 e) with the rounding error of the product put
-// back to first order (not for |x| >= 88, where the result leaves fp32's normal range;
-// infinities and NaN come out as they should).
+// e^x within ~2 ulp for |x| < 88: 2^(x log2 e) with the rounding error of the product put
+// back to first order.  From 88 to 88.72, where it overflows, without that (3e-6 relative);
+// below -87.34 it is under fp32's normal range.  Infinities and NaN come out as they should.
 __device__ __forceinline__ float exp_f32(float x) {
   constexpr float kL = 1.44269504088896340736f, kLo = 1.92596299112661746887e-8f, kLn2 = 0.69314718055994530942f;
   const float t = x * kL;

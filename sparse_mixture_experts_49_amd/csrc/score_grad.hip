@@ -310,13 +310,13 @@ __global__ __launch_bounds__(512, 2) void score_dx_bf16_kernel(const float* __re
   }
 
   f32x4 next[kPer][2];
-  auto fetch = [&](int tile) {                         // dl has whole tiles of rows
+  auto fetch = [&](int tile) {                         // dl has whole tiles of rows, NE columns or more
     const float* row = dl + (size_t)min(tile, tiles - 1) * kDxRows * pitch;
 #pragma unroll
     for (int i = 0; i < kPer; ++i) {
       const int u = i * 512 + (int)threadIdx.x, r = u / kChunks, c = u % kChunks;
       next[i][0] = next[i][1] = f32x4{0.f, 0.f, 0.f, 0.f};
-      if (u < kUnits && c * 8 < pitch) {               // pitch: E up to 32, zeros behind E
+      if (u < kUnits) {
         next[i][0] = *reinterpret_cast<const f32x4*>(row + (size_t)r * pitch + c * 8);
         next[i][1] = *reinterpret_cast<const f32x4*>(row + (size_t)r * pitch + c * 8 + 4);
       }
