@@ -28,8 +28,10 @@ namespace moe {
 // at piece ^ (row % 16) (256 B rows) or piece ^ ((row >> 1) & 7) (128 B rows): 16 rows' reads
 // of one piece touch every bank once.
 // With `splits` > 1 a tile is one part of k, summed into `partial`.
-// 32 tokens x 2 of 8 experts, d = 4096, F = 14336, weights from memory: up 53 us, down 48: 4.7
-// and 5.2 TB/s of codes and scales, a copy's 4.8 read and written.  (Up's last round has half the blocks; giving those tiles to all blocks
+// 32 tokens x 2 of 8 experts, d = 4096, F = 14336, weights from memory: up 53 us, down 48 to 53
+// by the box, 4.7 to 5.2 TB/s of codes and scales, a copy's 4.8 read and written.  Down has 32
+// column tiles, 256 in all while no expert has more than 16 rows; one that has makes a second
+// round, 70 us.  (Up's last round has half the blocks; giving those tiles to all blocks
 // by halves measured the same: the bytes take their time either way.)
 // ---------------------------------------------------------------------------
 constexpr int kStreamWaves = 8, kStreamCols = kStreamWaves * 16, kStreamBlocks = 256;

@@ -22,12 +22,13 @@
 // finished and stored.  One barrier per step, before its last part: by then the next step
 // has landed, everyone has read the last of this one, and its stage is refilled.
 //
-// fp4: 32768 rows, K = 4096, N = 14336 1222 to 1278 us by the box, 3.1 PFLOP/s; random codes
+// fp4: 32768 rows, K = 4096, N = 14336 1197 to 1278 us by the box, 3.1 PFLOP/s; random codes
 // hold the chip at 1.8 GHz (the MFMA alone reaches 6.35 PFLOP/s on them, 8.9 on zeros).  About
 // a quarter of the time is the tiles' ends, GELU and 940 MB of stores, which nothing overlaps:
-// the accumulators fill the matrix cores' registers.  (Keeping packed results to store them
+// the accumulators fill the matrix cores' registers, and a tile's end waits for its own stores
+// (they and the bias loads of the next 32 columns, or the next step's loads, share a counter).  (Keeping packed results to store them
 // during the next tile: 1488 us; 128-row tiles with the end left out altogether: no faster
-// than this.)  bf16: 8192 rows, K = 1024, N = 4096 107 us, 0.64 PFLOP/s; K = 4096 1.3.
+// than this.)  bf16: 8192 rows, K = 1024, N = 4096 109 us, 0.63 PFLOP/s; K = 4096 1.3.
 //
 // LDS banks: 16-byte chunks of a row sit at chunk ^ f(row) such that 16 consecutive rows'
 // reads of one chunk touch every bank once (128 B rows: (row >> 1) & 7; 32 B rows:
