@@ -9,6 +9,10 @@ namespace moe {
 
 constexpr int kScoreMaxExperts = 256;
 
+// Sums of sigmoid scores under 2^-126, fp32's normal range, count as that: its reciprocal is
+// finite and a score over it at most about 1.
+constexpr float kLeastSum = 0x1p-126f;
+
 struct ScoreShape {
   bool bf16;
   int T, d, E, k;

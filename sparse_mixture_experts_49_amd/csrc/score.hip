@@ -165,7 +165,7 @@ struct Finisher {
 #pragma unroll
         for (int j = 0; j < PER; ++j) q += s[j];
         q = wave_sum_f(q);
-        r = 1.f / (q < 1e-20f ? 1e-20f : q);       // every score underflowed: q = 0
+        r = 1.f / (q < kLeastSum ? kLeastSum : q);   // every score underflowed: q = 0
       }
 #pragma unroll
       for (int j = 0; j < PER; ++j) pq[j] += (double)(s[j] * r);

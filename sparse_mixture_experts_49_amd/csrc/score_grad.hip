@@ -4,7 +4,7 @@
 //   dr_j = scale g_j, or renormalised scale sum_i r_i (g_j - g_i) / S^2
 //   dq_e = d_aux E load_e / (T k) / T          (q = s / sum s; load is a constant)
 //   softmax: ds = dr + dq;                       dl = s (ds - sum ds s)
-//   sigmoid: ds = dr + (dq - sum dq q) / sum s;  dl = ds s (1 - s)
+//   sigmoid: ds = dr + (dq - sum dq q) / sum s;  dl = ds s (1 - s) = (dr s + (dq - sum dq q) q) (1 - s)
 //   dl += d_z (2 / T) lse softmax(l)
 // The differences with a sum over all experts are formed as of_leader says.
 // and d_b = sum_t dl, d_x = dl W_r, d_W = dl^T x.
@@ -170,15 +170,22 @@ __global__ __launch_bounds__(TT * 16) void score_dlogits_kernel(ScoreGradArgs a)
 #pragma unroll
           for (int j = 0; j < PER; ++j) ss += s[j];
           ss = wave_sum_f(ss);
-          const float rs = 1.f / (ss < 1e-20f ? 1e-20f : ss), c = of_leader(s, 0.5f * ss, dq);
+          const float rs = 1.f / (ss < kLeastSum ? kLeastSum : ss), c = of_leader(s, 0.5f * ss, dq);
+          float q[PER];                                // s / sum s, where ds itself may overflow
 #pragma unroll
-          for (int j = 0; j < PER; ++j) cq = fmaf(dq[j] - c, s[j], cq);
-          cq = wave_sum_f(cq) * rs;
+          for (int j = 0; j < PER; ++j) {
+            q[j] = s[j] * rs;
+            cq = fmaf(dq[j] - c, q[j], cq);
+          }
+          cq = wave_sum_f(cq);
 #pragma unroll
-          for (int j = 0; j < PER; ++j) ds[j] = fmaf(dq[j] - c - cq, rs, ds[j]);
+          for (int j = 0; j < PER; ++j) dl[j] = (dq[j] - c - cq) * q[j];
+        } else {
+#pragma unroll
+          for (int j = 0; j < PER; ++j) dl[j] = 0.f;
         }
 #pragma unroll
-        for (int j = 0; j < PER; ++j) dl[j] = ds[j] * s[j] * rest[j];
+        for (int j = 0; j < PER; ++j) dl[j] = fmaf(ds[j], s[j], dl[j]) * rest[j];
       } else {
         float cs = 0.f;
 #pragma unroll

@@ -553,3 +553,30 @@ def test_every_clear_choice_is_made(T, d, E, k, kind, G, tg, gtop, dtype):
     assert torch.all(err[same] <= 2 * 2e-5 + 32 * U32)
     load = torch.bincount(r.topk_idx.cpu().long().flatten(), minlength=E)
     assert torch.equal(r.load.cpu().long(), load)
+
+
+@pytest.mark.parametrize("low", [40.0, 60.0, 80.0])
+@pytest.mark.parametrize("T,E,dtype", [(70, 60, "f32"), (1500, 256, "bf16")])
+def test_balance_loss_of_low_sigmoid_scores(T, E, dtype, low):
+    """q = s / sum s and the gradient of the loss over it do not depend on how low a token's
+    scores are as long as fp32 holds them: the bounds of the cases above at logits around
+    -40, -60 and -80."""
+    d, k, da = 128, 4, 0.7 * T
+    desc = _desc(T, d, E, k, "sigmoid", dtype=dtype)
+    x, w, b = _grid_inputs(desc, T)
+    b = b - low
+    l = x.double() @ w.double().T + b.double()
+    ref = R.forward(l, "sigmoid", None, k)
+    r = _run(desc, x, w, b)
+    assert torch.equal(r.logits.cpu().double(), l) and torch.equal(r.topk_idx.cpu().long(), ref["idx"])
+    assert torch.all((r.prob_mean.cpu().double() - ref["prob_mean"]).abs() <= 32 * U32 * ref["prob_mean"])
+    assert abs(float(r.aux) - float(ref["aux"])) <= 33 * U32 * float(ref["aux"])
+    s = torch.sigmoid(l)
+    S, sl = s.sum(1, keepdim=True), s * torch.sigmoid(-l)
+    q, dq = s / S, da * E * ref["load"].double() / (T * k) / T
+    mean = (q * dq).sum(1, keepdim=True)
+    want, room = (dq - mean) / S * sl, (dq * (1 - q) + mean - dq * q) / S * sl
+    got = _backward(desc, x, w, l.float(), ref["idx"].to(torch.int32), ref["load"].to(torch.int32),
+                    torch.zeros(T, k), da, None)
+    err = (got.d_logits.cpu().double() - want).abs()
+    assert torch.all(err <= 128 * U32 * room), float((err / (U32 * room)).max())
