@@ -335,7 +335,8 @@ int moe_forward_noalloc(const moe_desc* desc, const void* x, const moe_weights* 
  * indices are always k different experts in [0, E)).
  * Over the T tokens of a call:
  *   load_e      assignments of expert e (before any capacity)
- *   prob_mean_e mean of q_e, q = s / sum(s) for sigmoid scores, s for softmax
+ *   prob_mean_e mean of q_e, q = s / sum(s) for sigmoid scores (a sum under 2^-126 counts
+ *               as that), s for softmax
  *   aux         E * sum_e load_e / (T k) * prob_mean_e
  *   z_loss      mean of (log sum_e exp l_e)^2
  * topk_idx and topk_w feed moe_permute (up to 64 experts), moe_mx_dispatch,
@@ -397,7 +398,8 @@ int moe_score_route(const moe_score_desc* desc, const void* x, const void* w_rou
  * d_z_loss [1] fp32 device scalars or NULL (zero).  x is read for d_w_router only,
  * w_router for d_x only (either may be NULL otherwise).  Sums are fp32 or wider in
  * a fixed order; for bf16 layers the logit gradients enter the matrix products as
- * two (d_x) or three (d_w_router) bf16 terms. */
+ * two (d_x) or three (d_w_router) bf16 terms, so an infinite operand may give NaN
+ * where the product is infinite. */
 int moe_score_backward(const moe_score_desc* desc, const void* x, const void* w_router,
                        const moe_score_out* fwd, const float* d_topk_w, const float* d_aux,
                        const float* d_z_loss, moe_score_grads* grads, void* workspace,
@@ -415,8 +417,11 @@ int moe_score_backward(const moe_score_desc* desc, const void* x, const void* w_
  * bf16).  moe_mx_desc.act says what the activations are:
  *   MOE_MX_ACT_BF16   bf16; the weights are widened exactly to bf16 on the way into
  *                     the matrix instruction
- *   MOE_MX_ACT_MXFP4  quantised by the call as moe_mx_quantize does, both operands of
- *                     the matrix instruction in 4 bits
+ *   MOE_MX_ACT_MXFP4  quantised by the call as moe_mx_quantize does; the matrix
+ *                     instruction takes both operands in 4 bits, or, with few rows per
+ *                     expert, both widened to bf16
+ * Weights past bf16's range (scale bytes 253 and 254, which moe_mx_quantize never makes)
+ * may become infinite on the way.
  * Products accumulate in fp32.  Limits: 1 <= n_experts <= 256, 1 <= top_k <= min(8,
  * n_experts), d_model and d_ff multiples of 128, tokens * top_k * max(d_model, d_ff)
  * and one expert's d_model * d_ff under 2^31.  Rows of an expert are the segment
