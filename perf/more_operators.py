@@ -247,9 +247,8 @@ def _plain_balance(s):
     load.index_add_(0, (s["seq"][:, None] * E + s["idx"]).flatten(), live.repeat_interleave(k))
     load = load.view(S, E)
     valid = torch.zeros(S, dtype=torch.int32, device=q.device).index_add_(0, s["seq"], live)
-    run = torch.where(live[:, None] > 0, q, 0).cumsum(0, dtype=torch.float64)     # 64 bits: the differences keep fp32's
-    mean = torch.diff(run[s["offsets"][1:].long() - 1], dim=0, prepend=run.new_zeros(1, E))
-    mean = mean / valid.clamp(min=1)[:, None]
+    member = (s["seq"] == torch.arange(S, device=q.device)[:, None]).double()     # [S, T]: sums as one product
+    mean = member @ torch.where(live[:, None] > 0, q, 0).double() / valid.clamp(min=1)[:, None]
     loss = E * (load / (k * valid.clamp(min=1)[:, None].double()) * mean).sum(1)
     n_live = (valid > 0).sum()
     return {"load": load, "valid": torch.cat([valid, n_live[None].int()]), "prob_mean": mean.float(),
