@@ -243,11 +243,10 @@ def _plain_balance(s):
     T, E, k, S = c["T"], c["E"], c["k"], c["S"]
     q = _plain_scores(c, s["logits"])[1]
     live = s["mask"].int() if s["mask"] is not None else torch.ones(T, dtype=torch.int32, device=q.device)
-    load = torch.zeros(S * E, dtype=torch.int32, device=q.device)
-    load.index_add_(0, (s["seq"][:, None] * E + s["idx"]).flatten(), live.repeat_interleave(k))
-    load = load.view(S, E)
-    valid = torch.zeros(S, dtype=torch.int32, device=q.device).index_add_(0, s["seq"], live)
     member = (s["seq"] == torch.arange(S, device=q.device)[:, None]).double()     # [S, T]: sums as one product
+    chosen = torch.zeros_like(q).scatter_add_(1, s["idx"].long(), live[:, None].expand(-1, k).float())
+    load = (member @ chosen.double()).int()
+    valid = (member @ live.double()[:, None])[:, 0].int()
     mean = member @ torch.where(live[:, None] > 0, q, 0).double() / valid.clamp(min=1)[:, None]
     loss = E * (load / (k * valid.clamp(min=1)[:, None].double()) * mean).sum(1)
     n_live = (valid > 0).sum()
