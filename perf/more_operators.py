@@ -243,11 +243,13 @@ def _plain_balance(s):
     T, E, k, S = c["T"], c["E"], c["k"], c["S"]
     q = _plain_scores(c, s["logits"])[1]
     live = s["mask"].int() if s["mask"] is not None else torch.ones(T, dtype=torch.int32, device=q.device)
-    member = (s["seq"] == torch.arange(S, device=q.device)[:, None]).double()     # [S, T]: sums as one product
     chosen = torch.zeros_like(q).scatter_add_(1, s["idx"].long(), live[:, None].expand(-1, k).float())
-    load = (member @ chosen.double()).int()
-    valid = (member @ live.double()[:, None])[:, 0].int()
-    mean = member @ torch.where(live[:, None] > 0, q, 0).double() / valid.clamp(min=1)[:, None]
+    q = torch.where(live[:, None] > 0, q, 0)
+    # Running sums in 64 bits, and their differences at the sequences' ends.
+    run = torch.cat([chosen, q, live[:, None].float()], 1).T.contiguous().cumsum(1, dtype=torch.float64)
+    sums = torch.diff(run[:, s["offsets"][1:].long() - 1], dim=1, prepend=run.new_zeros(2 * E + 1, 1)).T
+    load, valid = sums[:, :E].int(), sums[:, -1].int()
+    mean = sums[:, E:-1] / valid.clamp(min=1)[:, None]
     loss = E * (load / (k * valid.clamp(min=1)[:, None].double()) * mean).sum(1)
     n_live = (valid > 0).sum()
     return {"load": load, "valid": torch.cat([valid, n_live[None].int()]), "prob_mean": mean.float(),
