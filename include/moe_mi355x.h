@@ -405,6 +405,113 @@ int moe_score_backward(const moe_score_desc* desc, const void* x, const void* w_
                        const float* d_z_loss, moe_score_grads* grads, void* workspace,
                        size_t workspace_bytes, void* stream);
 
+/* moe_score_backward with a gradient that reaches the logits from elsewhere, such as
+ * moe_balance_backward's: d_logits_in [T][E] fp32 (or NULL) is added to the gradient of the
+ * logits, and so enters every field of grads. */
+int moe_score_backward_add(const moe_score_desc* desc, const void* x, const void* w_router,
+                           const moe_score_out* fwd, const float* d_topk_w, const float* d_aux,
+                           const float* d_z_loss, const float* d_logits_in, moe_score_grads* grads,
+                           void* workspace, size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Balance loss by sequence.
+ *
+ * moe_score_route's aux is over all T tokens of a call.  Here the batch is packed: sequence b
+ * is the tokens [seq_offsets[b], seq_offsets[b+1]), of which those with token_mask 0 (padding)
+ * do not count.  With n_b the tokens of b that count and q the normalised scores as above:
+ *   load_be      choices of expert e by tokens of b that count (an index outside [0, E) is a
+ *                dropped slot; the same expert twice counts twice)
+ *   prob_mean_be mean of q_e over them
+ *   seq_loss_b   E * sum_e load_be / (k n_b) * prob_mean_be; 0 where n_b is 0
+ *   loss         mean of seq_loss over the sequences with a token that counts; 0 without any
+ * What is masked out is never part of a sum, NaN and infinities included.  Tokens before the
+ * first border and behind the last belong to no sequence.  seq_offsets [S+1] does not fall
+ * and stays in [0, T]; with others the results are unspecified, but nothing outside the
+ * arrays is touched.  A call uses its workspace until it has run. */
+typedef struct moe_balance_desc {
+  int32_t tokens;          /* T, 1 .. 2^22 */
+  int32_t n_experts;       /* E, 1 .. 256 */
+  int32_t top_k;           /* k, 1 .. min(8, E) */
+  int32_t n_seqs;          /* S, 1 .. 2^20; sequences may be empty */
+  int32_t score;           /* MOE_SCORE_* */
+} moe_balance_desc;
+
+/* Results (device pointers); the backward reads load and valid. */
+typedef struct moe_balance_out {
+  int32_t* load;           /* [S][E] */
+  int32_t* valid;          /* [S+1]: n_b of every sequence, then how many have n_b > 0 */
+  float* prob_mean;        /* [S][E] or NULL */
+  float* seq_loss;         /* [S] or NULL */
+  float* loss;             /* [1] or NULL */
+  int32_t* total_load;     /* [E] load summed over the sequences, or NULL */
+} moe_balance_out;
+
+/* Bytes of workspace moe_balance_loss needs (host output). */
+int moe_balance_workspace_size(const moe_balance_desc* desc, size_t* bytes);
+
+/* The loss and the counts.  logits [T][E] fp32 and topk_idx [T][k] as moe_score_route writes
+ * them; token_mask [T] bytes or NULL (every token counts). */
+int moe_balance_loss(const moe_balance_desc* desc, const float* logits, const int32_t* topk_idx,
+                     const int32_t* seq_offsets, const uint8_t* token_mask, moe_balance_out* out,
+                     void* workspace, size_t workspace_bytes, void* stream);
+
+/* Gradient of d_loss * loss + sum_b d_seq_loss_b seq_loss_b with respect to the logits; load is
+ * a constant.  d_loss [1] and d_seq_loss [S] fp32, either may be NULL (zero).  d_logits [T][E]
+ * is written whole: rows that do not count, or belong to no sequence, are 0.
+ * moe_score_backward_add takes it on to the router's weights and the tokens. */
+int moe_balance_backward(const moe_balance_desc* desc, const float* logits,
+                         const int32_t* seq_offsets, const uint8_t* token_mask,
+                         const moe_balance_out* fwd, const float* d_loss, const float* d_seq_loss,
+                         float* d_logits, void* stream);
+
+/* ---------------------------------------------------------------------------
+ * Layer norm, with the residual add before it.
+ *
+ * The step between one layer's output and the next layer's input:
+ *   x_out = x + add, rounded to dtype (x where add is NULL)
+ *   y     = (x_out - mean) * rstd * weight + bias, mean and rstd of the rounded row,
+ *   rstd  = 1 / sqrt(mean of (x_out - mean)^2 + eps)
+ * add is a layer's output (moe_forward's y is fp32, the stream may be bf16); y is what
+ * moe_route, moe_score_route and the expert products take.  Statistics and sums are fp32. */
+typedef struct moe_norm_desc {
+  int64_t rows;            /* >= 0; rows * d at most 2^40 */
+  int32_t d;               /* 1 .. 32768 */
+  int32_t dtype;           /* MOE_DTYPE_*: x, x_out, y and their gradients */
+  int32_t param_dtype;     /* MOE_DTYPE_*: weight and bias */
+  int32_t add_dtype;       /* MOE_DTYPE_*: add */
+  float eps;               /* finite, >= 0 */
+} moe_norm_desc;
+
+/* A matrix [rows][d] (host struct): its first row on the device and the elements from one row
+ * to the next, at least d.  Of one-row matrices the stride is not read.  Rows whose width and
+ * strides are multiples of eight go by 16-byte accesses.  Matrices of the same pitch in bytes
+ * may lie side by side in one buffer; otherwise their whole ranges must not overlap. */
+typedef struct moe_rows {
+  void* data;
+  int64_t stride;
+} moe_rows;
+
+/* Bytes of workspace moe_layer_norm_backward needs (host output). */
+int moe_norm_workspace_size(const moe_norm_desc* desc, size_t* bytes);
+
+/* add, weight (1), bias (0), x_out, mean and rstd may be NULL; a moe_rows with data NULL counts
+ * as NULL.  mean and rstd [rows] fp32, which the backward reads. */
+int moe_layer_norm(const moe_norm_desc* desc, const moe_rows* x, const moe_rows* add,
+                   const void* weight, const void* bias, const moe_rows* x_out, const moe_rows* y,
+                   float* mean, float* rstd, void* stream);
+
+/* Gradients.  dy is y's, d_x_out (or NULL) what reaches x_out by the residual path, x the row
+ * that was normalised (x_out, where there was an add):
+ *   d_x      = d_x_out + rstd (g - mean(g) - hat mean(g hat)),  g = dy weight, hat = (x - mean) rstd;
+ *              the gradient of both x and add
+ *   d_weight = sum over the rows of dy hat,  d_bias = sum of dy, fp32 [d], in a fixed order
+ * d_x, d_weight and d_bias may be NULL, not all; d_x_out needs d_x.  The workspace is needed for
+ * d_weight and d_bias.  rows = 0 makes them 0; matrices may then be NULL, here and above. */
+int moe_layer_norm_backward(const moe_norm_desc* desc, const moe_rows* dy, const moe_rows* x,
+                            const void* weight, const float* mean, const float* rstd,
+                            const moe_rows* d_x_out, const moe_rows* d_x, float* d_weight,
+                            float* d_bias, void* workspace, size_t workspace_bytes, void* stream);
+
 /* ---------------------------------------------------------------------------
  * Experts in microscaled 4-bit floating point (MXFP4).
  *

@@ -13,6 +13,9 @@ from .binding import (ENTRY_POINTS, MOE_CAPACITY_DROP, MOE_CAPACITY_REROUTE, MOE
                       moe_mx_ffn_down, moe_mx_ffn_up, moe_mx_forward, moe_mx_quantize, moe_mx_workspace_size, moe_permute, moe_query_plan,
                       moe_route, moe_score_backward, moe_score_route, moe_score_workspace_size,
                       moe_shared_ffn, moe_workspace_size)
+from .binding import (BalanceDesc, BalanceOut, NormDesc, alloc_balance_workspace, alloc_norm_workspace, moe_balance_backward,
+                      moe_balance_loss, moe_balance_workspace_size, moe_layer_norm, moe_layer_norm_backward,
+                      moe_norm_workspace_size, moe_score_backward_add)
 
 __all__ = ["ENTRY_POINTS", "MOE_CAPACITY_DROP", "MOE_CAPACITY_REROUTE", "MOE_FFN_AUTO", "MOE_FFN_STREAM", "MOE_FFN_TILED", "MOE_H_AUTO",
            "MOE_H_BF16", "MOE_H_SPLIT", "Desc", "MoeError", "MxDesc", "MxWeights", "Routing", "ScoreDesc", "ScoreGrads",
@@ -21,4 +24,7 @@ __all__ = ["ENTRY_POINTS", "MOE_CAPACITY_DROP", "MOE_CAPACITY_REROUTE", "MOE_FFN
            "moe_ffn_up", "moe_ffn_up_gather", "moe_forward", "moe_forward_noalloc", "moe_read_probe", "moe_grouped_ffn", "moe_mx_dequantize", "moe_mx_dispatch",
            "moe_mx_ffn_down", "moe_mx_ffn_up", "moe_mx_forward", "moe_mx_quantize", "moe_mx_workspace_size", "moe_permute", "moe_query_plan",
            "moe_route", "moe_score_backward", "moe_score_route", "moe_score_workspace_size",
-           "moe_shared_ffn", "moe_workspace_size"]
+           "moe_shared_ffn", "moe_workspace_size",
+           "BalanceDesc", "BalanceOut", "NormDesc", "alloc_balance_workspace", "alloc_norm_workspace", "moe_balance_backward",
+           "moe_balance_loss", "moe_balance_workspace_size", "moe_layer_norm", "moe_layer_norm_backward",
+           "moe_norm_workspace_size", "moe_score_backward_add"]

@@ -31,7 +31,10 @@ ENTRY_POINTS = ("moe_status_string", "moe_last_error", "moe_workspace_size", "mo
                 "moe_shared_ffn", "moe_combine", "moe_forward", "moe_forward_noalloc",
                 "moe_read_probe", "moe_score_workspace_size", "moe_score_route",
                 "moe_score_backward", "moe_mx_quantize", "moe_mx_dequantize", "moe_mx_workspace_size",
-                "moe_mx_dispatch", "moe_mx_ffn_up", "moe_mx_ffn_down", "moe_mx_forward")
+                "moe_mx_dispatch", "moe_mx_ffn_up", "moe_mx_ffn_down", "moe_mx_forward",
+                "moe_score_backward_add", "moe_balance_workspace_size", "moe_balance_loss",
+                "moe_balance_backward", "moe_norm_workspace_size", "moe_layer_norm",
+                "moe_layer_norm_backward")
 
 
 class MoeError(RuntimeError):
@@ -88,6 +91,24 @@ class CMxWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("w1", "s1", "b1", "w2", "s2", "b2")]
 
 
+class CBalanceDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in ("tokens", "n_experts", "top_k", "n_seqs", "score")]
+
+
+class CBalanceOut(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("load", "valid", "prob_mean", "seq_loss", "loss", "total_load")]
+
+
+class CNormDesc(ctypes.Structure):
+    _fields_ = [("rows", ctypes.c_int64), ("d", ctypes.c_int32), ("dtype", ctypes.c_int32),
+                ("param_dtype", ctypes.c_int32), ("add_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
+
+
+class CRows(ctypes.Structure):
+    _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64)]
+
+
 _lib: Optional[ctypes.CDLL] = None
 
 
@@ -121,6 +142,13 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_score_workspace_size": (I, [P, ctypes.POINTER(S)]),
         "moe_score_route": (I, [P, P, P, P, P, P, P, S, P]),
         "moe_score_backward": (I, [P, P, P, P, P, P, P, P, P, S, P]),
+        "moe_score_backward_add": (I, [P, P, P, P, P, P, P, P, P, P, S, P]),
+        "moe_balance_workspace_size": (I, [P, ctypes.POINTER(S)]),
+        "moe_balance_loss": (I, [P, P, P, P, P, P, P, S, P]),
+        "moe_balance_backward": (I, [P, P, P, P, P, P, P, P, P]),
+        "moe_norm_workspace_size": (I, [P, ctypes.POINTER(S)]),
+        "moe_layer_norm": (I, [P, P, P, P, P, P, P, P, P, P]),
+        "moe_layer_norm_backward": (I, [P, P, P, P, P, P, P, P, P, P, P, S, P]),
         "moe_mx_quantize": (I, [P, I, L, L, L, P, P, P]),
         "moe_mx_dequantize": (I, [P, P, L, L, I, P, L, P]),
         "moe_mx_workspace_size": (I, [P, ctypes.POINTER(S)]),
@@ -641,6 +669,13 @@ def moe_score_backward(desc: ScoreDesc, x, w_router, routing: ScoreRouting, d_to
                        d_aux=None, d_z_loss=None, workspace=None, stream=None):
     """Gradients of the scored router into the fields of `grads` that are not None; x may
     be None without d_w_router, w_router without d_x."""
+    moe_score_backward_add(desc, x, w_router, routing, d_topk_w, grads, None, d_aux, d_z_loss, workspace, stream)
+
+
+def moe_score_backward_add(desc: ScoreDesc, x, w_router, routing: ScoreRouting, d_topk_w, grads: ScoreGrads,
+                           d_logits_in, d_aux=None, d_z_loss=None, workspace=None, stream=None):
+    """The same with d_logits_in (fp32 [T, E] or None), which reaches the logits from elsewhere,
+    added to their gradient."""
     c = _Call(routing.logits, "routing.logits")
     T, d, E, k, dt = desc.tokens, desc.d_model, desc.n_experts, desc.top_k, desc.torch_dtype
     f32 = torch.float32
@@ -648,10 +683,168 @@ def moe_score_backward(desc: ScoreDesc, x, w_router, routing: ScoreRouting, d_to
     g = CScoreGrads(c.t(grads.d_x, "grads.d_x", dt, T * d), c.t(grads.d_w_router, "grads.d_w_router", f32, E * d),
                     c.t(grads.d_b_router, "grads.d_b_router", f32, E),
                     c.t(grads.d_logits, "grads.d_logits", f32, T * E))
-    c.run(load_library().moe_score_backward, desc.ref(), c.t(x, "x", dt, T * d),
+    c.run(load_library().moe_score_backward_add, desc.ref(), c.t(x, "x", dt, T * d),
           c.t(w_router, "w_router", dt, E * d), ctypes.byref(_score_out(c, desc, routing)),
           c.t(d_topk_w, "d_topk_w", f32, T * k), c.t(d_aux, "d_aux", f32, 1),
-          c.t(d_z_loss, "d_z_loss", f32, 1), ctypes.byref(g), ws, nb, stream=stream)
+          c.t(d_z_loss, "d_z_loss", f32, 1), c.t(d_logits_in, "d_logits_in", f32, T * E), ctypes.byref(g), ws, nb,
+          stream=stream)
+
+
+# ---- balance loss by sequence --------------------------------------------------------------
+
+@dataclasses.dataclass
+class BalanceDesc(_CDescOnce):
+    """Options of the balance loss by sequence (moe_balance_desc)."""
+    tokens: int
+    n_experts: int
+    top_k: int
+    n_seqs: int
+    score: str = "softmax"       # "softmax" or "sigmoid"
+
+    def to_c(self) -> CBalanceDesc:
+        return CBalanceDesc(self.tokens, self.n_experts, self.top_k, self.n_seqs, _SCORES.get(self.score, -1))
+
+
+@dataclasses.dataclass
+class BalanceOut:
+    """Results of moe_balance_loss; the backward reads load and valid."""
+    load: Optional[torch.Tensor] = None         # [S, E] int32
+    valid: Optional[torch.Tensor] = None        # [S + 1] int32: tokens that count, then live sequences
+    prob_mean: Optional[torch.Tensor] = None    # [S, E]
+    seq_loss: Optional[torch.Tensor] = None     # [S]
+    loss: Optional[torch.Tensor] = None         # scalar
+    total_load: Optional[torch.Tensor] = None   # [E] int32
+
+    @classmethod
+    def allocate(cls, desc: BalanceDesc, device) -> "BalanceOut":
+        S, E = desc.n_seqs, desc.n_experts
+        i32, f32 = dict(dtype=torch.int32, device=device), dict(dtype=torch.float32, device=device)
+        return cls(torch.empty(S, E, **i32), torch.empty(S + 1, **i32), torch.empty(S, E, **f32),
+                   torch.empty(S, **f32), torch.empty((), **f32), torch.empty(E, **i32))
+
+
+def moe_balance_workspace_size(desc: BalanceDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_balance_workspace_size(desc.ref(), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_balance_workspace(desc: BalanceDesc, device) -> torch.Tensor:
+    return torch.empty(moe_balance_workspace_size(desc), dtype=torch.uint8, device=device)
+
+
+def _token_mask(c: _Call, mask, T):
+    if isinstance(mask, torch.Tensor) and mask.dtype is torch.bool:
+        mask = mask.view(torch.uint8)
+    return c.t(mask, "token_mask", torch.uint8, T)
+
+
+def _balance_out(c: _Call, d: BalanceDesc, r: BalanceOut) -> CBalanceOut:
+    S, E, i32, f32 = d.n_seqs, d.n_experts, torch.int32, torch.float32
+    return CBalanceOut(c.t(r.load, "out.load", i32, S * E), c.t(r.valid, "out.valid", i32, S + 1),
+                       c.t(r.prob_mean, "out.prob_mean", f32, S * E), c.t(r.seq_loss, "out.seq_loss", f32, S),
+                       c.t(r.loss, "out.loss", f32, 1), c.t(r.total_load, "out.total_load", i32, E))
+
+
+def moe_balance_loss(desc: BalanceDesc, logits, topk_idx, seq_offsets, out: BalanceOut, token_mask=None,
+                     workspace=None, stream=None):
+    """Balance loss and expert counts of every sequence: writes every field of `out` that is not
+    None (load and valid have to be there).  token_mask: bool or uint8 [T], 0 = padding."""
+    c = _Call(logits, "logits")
+    T, E, i32 = desc.tokens, desc.n_experts, torch.int32
+    ws, nb = c.ws(workspace, lambda: moe_balance_workspace_size(desc), stream)
+    c.run(load_library().moe_balance_loss, desc.ref(), c.t(logits, "logits", torch.float32, T * E),
+          c.t(topk_idx, "topk_idx", i32, T * desc.top_k), c.t(seq_offsets, "seq_offsets", i32, desc.n_seqs + 1),
+          _token_mask(c, token_mask, T), ctypes.byref(_balance_out(c, desc, out)), ws, nb, stream=stream)
+
+
+def moe_balance_backward(desc: BalanceDesc, logits, seq_offsets, fwd: BalanceOut, d_logits, d_loss=None,
+                         d_seq_loss=None, token_mask=None, stream=None):
+    """Gradient of the logits into d_logits (fp32 [T, E], written whole)."""
+    c = _Call(logits, "logits")
+    T, E, S, f32 = desc.tokens, desc.n_experts, desc.n_seqs, torch.float32
+    c.run(load_library().moe_balance_backward, desc.ref(), c.t(logits, "logits", f32, T * E),
+          c.t(seq_offsets, "seq_offsets", torch.int32, S + 1), _token_mask(c, token_mask, T),
+          ctypes.byref(_balance_out(c, desc, fwd)), c.t(d_loss, "d_loss", f32, 1),
+          c.t(d_seq_loss, "d_seq_loss", f32, S), c.t(d_logits, "d_logits", f32, T * E), stream=stream)
+
+
+# ---- layer norm ------------------------------------------------------------------------------
+
+@dataclasses.dataclass
+class NormDesc(_CDescOnce):
+    """Options of the layer norm (moe_norm_desc)."""
+    rows: int
+    d: int
+    dtype: str = "bf16"          # x, x_out, y and their gradients: "bf16" or "f32"
+    param_dtype: str = "f32"     # weight and bias
+    add_dtype: str = "f32"       # add
+    eps: float = 1e-5
+
+    def to_c(self) -> CNormDesc:
+        return CNormDesc(self.rows, self.d, _DTYPES.get(self.dtype, -1), _DTYPES.get(self.param_dtype, -1),
+                         _DTYPES.get(self.add_dtype, -1), self.eps)
+
+
+def _torch_dtype(name):
+    return torch.bfloat16 if name == "bf16" else torch.float32
+
+
+def moe_norm_workspace_size(desc: NormDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_norm_workspace_size(desc.ref(), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_norm_workspace(desc: NormDesc, device) -> torch.Tensor:
+    return torch.empty(moe_norm_workspace_size(desc), dtype=torch.uint8, device=device)
+
+
+def _norm_rows(c: _Call, t, name, dtype, d: NormDesc):
+    """A [rows, d] tensor with contiguous rows (any row stride), by reference, or None."""
+    if t is None:
+        return None
+    if not isinstance(t, torch.Tensor):
+        raise MoeError(MOE_ERR_INVALID, f"{name} must be a torch tensor or None")
+    if not (t.is_cuda and t.get_device() == c.index and t.dtype is dtype):
+        check_tensor(t, name, dtype, 0, c.device)
+    if t.dim() < 1 or t.shape[-1] != d.d or t.numel() != d.rows * d.d:
+        raise MoeError(MOE_ERR_INVALID, f"{name} has shape {tuple(t.shape)}, expected [{d.rows}, {d.d}]")
+    if t.dim() != 2:
+        if not t.is_contiguous():
+            raise MoeError(MOE_ERR_INVALID, f"{name} must be contiguous, or a matrix with contiguous rows")
+        stride = d.d
+    else:
+        stride, inner = t.stride()
+        if d.d > 1 and inner != 1:
+            raise MoeError(MOE_ERR_INVALID, f"{name} must have contiguous rows")
+    return ctypes.byref(CRows(t.data_ptr(), stride))
+
+
+def moe_layer_norm(desc: NormDesc, x, y, weight=None, bias=None, add=None, x_out=None, mean=None, rstd=None,
+                   stream=None):
+    """x_out = x + add and its layer norm y; tensors are [rows, d] with any row stride."""
+    c = _Call(x, "x")
+    dt, pt, at, f32 = _torch_dtype(desc.dtype), _torch_dtype(desc.param_dtype), _torch_dtype(desc.add_dtype), torch.float32
+    c.run(load_library().moe_layer_norm, desc.ref(), _norm_rows(c, x, "x", dt, desc),
+          _norm_rows(c, add, "add", at, desc), c.t(weight, "weight", pt, desc.d), c.t(bias, "bias", pt, desc.d),
+          _norm_rows(c, x_out, "x_out", dt, desc), _norm_rows(c, y, "y", dt, desc),
+          c.t(mean, "mean", f32, desc.rows), c.t(rstd, "rstd", f32, desc.rows), stream=stream)
+
+
+def moe_layer_norm_backward(desc: NormDesc, dy, x, mean, rstd, weight=None, d_x_out=None, d_x=None, d_weight=None,
+                            d_bias=None, workspace=None, stream=None):
+    """Gradients into those of d_x, d_weight and d_bias that are not None; x is what was
+    normalised (x_out, where there was an add), d_x_out the residual path's gradient."""
+    c = _Call(x, "x")
+    dt, f32 = _torch_dtype(desc.dtype), torch.float32
+    ws, nb = (None, 0) if d_weight is None and d_bias is None else \
+        c.ws(workspace, lambda: moe_norm_workspace_size(desc), stream)
+    c.run(load_library().moe_layer_norm_backward, desc.ref(), _norm_rows(c, dy, "dy", dt, desc),
+          _norm_rows(c, x, "x", dt, desc), c.t(weight, "weight", _torch_dtype(desc.param_dtype), desc.d),
+          c.t(mean, "mean", f32, desc.rows), c.t(rstd, "rstd", f32, desc.rows),
+          _norm_rows(c, d_x_out, "d_x_out", dt, desc), _norm_rows(c, d_x, "d_x", dt, desc),
+          c.t(d_weight, "d_weight", f32, desc.d), c.t(d_bias, "d_bias", f32, desc.d), ws, nb, stream=stream)
 
 
 # ---- experts in microscaled 4-bit floating point ------------------------------------------

@@ -165,10 +165,10 @@ int moe_score_route(const moe_score_desc* desc, const void* x, const void* w_rou
   return hip_status(moe::launch_score(a, static_cast<hipStream_t>(stream)), "scored router launch");
 }
 
-int moe_score_backward(const moe_score_desc* desc, const void* x, const void* w_router,
-                       const moe_score_out* fwd, const float* d_topk_w, const float* d_aux,
-                       const float* d_z_loss, moe_score_grads* grads, void* ws, size_t ws_bytes,
-                       void* stream) {
+int moe_score_backward_add(const moe_score_desc* desc, const void* x, const void* w_router,
+                           const moe_score_out* fwd, const float* d_topk_w, const float* d_aux,
+                           const float* d_z_loss, const float* d_logits_in, moe_score_grads* grads,
+                           void* ws, size_t ws_bytes, void* stream) {
   if (int st = validate_score(desc)) return st;
   if (!fwd) return fail(MOE_ERR_INVALID, "fwd must not be NULL");
   if (!grads) return fail(MOE_ERR_INVALID, "grads must not be NULL");
@@ -178,6 +178,7 @@ int moe_score_backward(const moe_score_desc* desc, const void* x, const void* w_
   MOE_OPTIONAL_PTR(d_topk_w, "d_topk_w");
   MOE_OPTIONAL_PTR(d_aux, "d_aux");
   MOE_OPTIONAL_PTR(d_z_loss, "d_z_loss");
+  MOE_OPTIONAL_PTR(d_logits_in, "d_logits_in");
   if (!grads->d_x && !grads->d_w_router && !grads->d_b_router && !grads->d_logits)
     return fail(MOE_ERR_INVALID, "grads asks for nothing");
   MOE_OPTIONAL_PTR(grads->d_x, "grads->d_x");
@@ -204,6 +205,7 @@ int moe_score_backward(const moe_score_desc* desc, const void* x, const void* w_
     in.add(d_topk_w, T * k * 4, "d_topk_w");
     in.add(d_aux, 4, "d_aux");
     in.add(d_z_loss, 4, "d_z_loss");
+    in.add(d_logits_in, T * E * 4, "d_logits_in");
     if (int st = check_alias(o, in)) return st;
   }
   moe::ScoreGradArgs a{};
@@ -219,6 +221,7 @@ int moe_score_backward(const moe_score_desc* desc, const void* x, const void* w_
   a.d_topk_w = d_topk_w;
   a.d_aux = d_aux;
   a.d_z = d_z_loss;
+  a.d_logits_in = d_logits_in;
   a.d_x = grads->d_x;
   a.d_w = grads->d_w_router;
   a.d_b = grads->d_b_router;
@@ -228,6 +231,14 @@ int moe_score_backward(const moe_score_desc* desc, const void* x, const void* w_
   a.pw = at<float>(ws, L.pw);
   return hip_status(moe::launch_score_grad(a, static_cast<hipStream_t>(stream)),
                     "scored router backward launch");
+}
+
+int moe_score_backward(const moe_score_desc* desc, const void* x, const void* w_router,
+                       const moe_score_out* fwd, const float* d_topk_w, const float* d_aux,
+                       const float* d_z_loss, moe_score_grads* grads, void* ws, size_t ws_bytes,
+                       void* stream) {
+  return moe_score_backward_add(desc, x, w_router, fwd, d_topk_w, d_aux, d_z_loss, nullptr, grads, ws,
+                                ws_bytes, stream);
 }
 
 }  // extern "C"

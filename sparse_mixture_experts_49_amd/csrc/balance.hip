@@ -1,0 +1,348 @@
+// Balance loss of every sequence of a packed batch, the experts' counts, and the gradient of
+// the router's logits.
+//
+// For sequence b with the n tokens that count (inside its range, not masked out):
+//   q_t = softmax(l_t), or s / sum s with s = sigmoid(l_t)
+//   load_be = choices of expert e,  mean_be = sum_t q_te / n
+//   loss_b = sum_e f_be mean_be,  f_be = E load_be / (k n);  loss = mean over the b with n > 0
+// load is a constant in the gradient.  With c_e = d_loss_b E load_be / (k n^2):
+//   softmax d l_e = q_e (c_e - sum_j c_j q_j);  sigmoid the same times 1 - s_e
+// The difference is formed after the c of an expert with over half of the score is taken off
+// every c, so that its own keeps its digits.
+//
+// Bound by reading the logits (and writing their gradients).  A token is held by L lanes of
+// four experts each, L the least power of two with 4 L >= E, so its softmax is a few
+// exchanges between neighbouring lanes and a wave works on 64 / L tokens at once.
+//
+// Sums: a block sums a run of tokens, sequence by sequence.  The pieces (run c, sequence b)
+// that are not empty are met in an order in which c or b grows and neither falls, so c + b
+// numbers them without gaps in use and without a list.  A second kernel adds each sequence's
+// pieces in order, a third the sequences' losses.  fp32 within a piece, fp64 beyond.
+#include <algorithm>
+#include <type_traits>
+
+#include "balance.h"
+#include "device_common.h"
+#include "score.h"
+
+namespace moe {
+
+// Tokens a run has: short runs while there are fewer than 1024 of them, then longer ones.
+static int chunk_of(int T) { return T <= 16 * 1024 ? 16 : (T + 1023) / 1024; }
+int balance_chunks(const BalanceShape& s) { const int c = chunk_of(s.T); return (s.T + c - 1) / c; }
+int balance_blocks(int E) { return (E + 63) / 64; }
+
+// ---- sums over the L lanes of a token, in all of them --------------------------------------
+template <int CTRL>
+__device__ __forceinline__ float dpp(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
+}
+template <int L, typename F>
+__device__ __forceinline__ float across(float v, F f) {
+  if constexpr (L >= 2) v = f(v, dpp<0xB1>(v));      // quad [1,0,3,2]
+  if constexpr (L >= 4) v = f(v, dpp<0x4E>(v));      // quad [2,3,0,1]
+  if constexpr (L >= 8) v = f(v, dpp<0x141>(v));     // half-row mirror
+  if constexpr (L >= 16) v = f(v, dpp<0x140>(v));    // row mirror
+  if constexpr (L >= 32) v = f(v, __shfl_xor(v, 16));
+  if constexpr (L >= 64) v = f(v, __shfl_xor(v, 32));
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float sum_of(float v) {
+  return across<L>(v, [](float a, float b) { return a + b; });
+}
+template <int L>
+__device__ __forceinline__ float max_of(float v) {
+  return across<L>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
+// A lane's four logits of a row (experts e .. e + 3), -inf behind E.
+template <bool VEC>
+__device__ __forceinline__ f32x4 load_logits(const float* __restrict__ row, int e, int E) {
+  if constexpr (VEC) {
+    return e < E ? *reinterpret_cast<const f32x4*>(row + e)
+                 : (f32x4){-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+  } else {
+    f32x4 v;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) v[j] = e + j < E ? row[e + j] : -INFINITY;
+    return v;
+  }
+}
+
+// Shares q of a token from its logits, and for sigmoid scores 1 - s.
+template <int L, bool SIGMOID>
+__device__ __forceinline__ void shares(const f32x4& l, f32x4& q, f32x4& rest) {
+  if constexpr (SIGMOID) {
+#pragma unroll
+    for (int j = 0; j < 4; ++j) {
+      float s, r;
+      sigmoid_pair(l[j], s, r);
+      q[j] = s;
+      rest[j] = r;
+    }
+    const float sum = sum_of<L>((q[0] + q[1]) + (q[2] + q[3]));
+    const float inv = 1.f / (sum < kLeastSum ? kLeastSum : sum);
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[j] *= inv;
+  } else {
+    float m = max_of<L>(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])));
+    m = m == -INFINITY ? 0.f : m;                    // every expert masked: no shares
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[j] = exp_f32(l[j] - m);
+    const float sum = sum_of<L>((q[0] + q[1]) + (q[2] + q[3]));
+    const float inv = sum > 0.f ? 1.f / sum : sum != sum ? sum : 0.f;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) q[j] *= inv;
+  }
+}
+
+// The borders of the sequences, brought into [0, T] and order, so that no content of
+// `offsets` leads out of the arrays.
+__device__ __forceinline__ int border(const int32_t* __restrict__ offsets, int b, int T) {
+  return min(max(offsets[b], 0), T);
+}
+
+// The first sequence that ends behind token t (S if none does), 64 of them probed at a time:
+// every lane takes part.
+__device__ __forceinline__ int sequence_of(const int32_t* __restrict__ offsets, int S, int T, int t) {
+  int lo = 0, hi = S;
+  while (lo < hi) {
+    const int step = (hi - lo + 63) / 64, p = lo + (int)(threadIdx.x & 63) * step + step - 1;
+    const uint64_t behind = __ballot(p >= hi || border(offsets, min(p, hi - 1) + 1, T) > t);
+    if (!behind) return hi;
+    lo += (__ffsll((unsigned long long)behind) - 1) * step;
+    hi = min(hi, lo + step - 1);
+  }
+  return lo;
+}
+
+template <int L, bool SIGMOID, bool VEC>
+__global__ __launch_bounds__(256) void balance_part_kernel(BalanceArgs a, int chunk) {
+  constexpr int kTok = 64 / L;                       // tokens of a wave at once
+  __shared__ float sum_q[4][4 * L];
+  __shared__ int hist[kBalanceMaxExperts];
+  __shared__ int count;
+  const int T = a.sh.T, E = a.sh.E, S = a.sh.S, k = a.sh.k;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int e = (lane % L) * 4, slot = wave * kTok + lane / L;
+  const int t0 = blockIdx.x * chunk, t1 = min(t0 + chunk, T);
+  if (a.total_load && blockIdx.x == 0)
+    for (int i = threadIdx.x; i < E; i += 256) a.total_load[i] = 0;
+  for (int i = threadIdx.x; i < E; i += 256) hist[i] = 0;
+  if (threadIdx.x == 0) count = 0;
+  __syncthreads();
+  for (int b = sequence_of(a.offsets, S, T, t0); b < S; ++b) {
+    const int lo = max(border(a.offsets, b, T), t0), hi = min(border(a.offsets, b + 1, T), t1);
+    if (lo >= t1) break;
+    if (hi <= lo) continue;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    for (int t = lo + slot; t < hi + slot; t += 4 * kTok) {      // the same trips for all lanes of a wave
+      const bool in = t < hi && (!a.mask || a.mask[t]);
+      const f32x4 l = load_logits<VEC>(a.logits + (size_t)min(t, hi - 1) * E, e, E);
+      f32x4 q, rest;
+      shares<L, SIGMOID>(l, q, rest);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] += in ? q[j] : 0.f;
+    }
+    int n = 0;
+    for (int i = threadIdx.x; i < (hi - lo) * k; i += 256) {
+      const int t = lo + i / k, id = a.topk_idx[(size_t)lo * k + i];
+      const bool in = !a.mask || a.mask[t];
+      if (in && (uint32_t)id < (uint32_t)E) atomicAdd(&hist[id], 1);   // counts: order-independent
+      n += in && i % k == 0;
+    }
+    if (n) atomicAdd(&count, n);
+#pragma unroll
+    for (int o = L; o < 64; o <<= 1)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] += __shfl_xor(acc[j], o);
+    if (lane < L)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) sum_q[wave][e + j] = acc[j];
+    __syncthreads();
+    const size_t at = (size_t)blockIdx.x + b;
+    for (int i = threadIdx.x; i < E; i += 256) {
+      a.pq[at * E + i] = (sum_q[0][i] + sum_q[1][i]) + (sum_q[2][i] + sum_q[3][i]);
+      a.pload[at * E + i] = hist[i];
+      hist[i] = 0;
+    }
+    if (threadIdx.x == 0) {
+      a.pvalid[at] = count;
+      count = 0;
+    }
+    __syncthreads();
+  }
+}
+
+// A sequence's pieces added up for 64 experts: 16 waves a sixteenth of them each.
+__global__ __launch_bounds__(1024) void balance_seq_kernel(BalanceArgs a, int chunk) {
+  __shared__ double sq[16][64];
+  __shared__ int sl[16][64], sn[16];
+  const int T = a.sh.T, E = a.sh.E, b = blockIdx.x;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6, e = blockIdx.y * 64 + lane;
+  const int lo = border(a.offsets, b, T), hi = border(a.offsets, b + 1, T);
+  const int c0 = lo / chunk, c1 = hi > lo ? (hi - 1) / chunk + 1 : c0;
+  double q = 0.0;
+  int load = 0, n = 0;
+#pragma unroll 4
+  for (int c = c0 + wave; c < c1; c += 16) {
+    const size_t at = (size_t)c + b;
+    if (e < E) {
+      q += (double)a.pq[at * E + e];
+      load += a.pload[at * E + e];
+    }
+  }
+  for (int c = c0 + (int)threadIdx.x; c < c1; c += 1024) n += a.pvalid[(size_t)c + b];
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) n += __shfl_xor(n, o);
+  sq[wave][lane] = q;
+  sl[wave][lane] = load;
+  if (lane == 0) sn[wave] = n;
+  __syncthreads();
+  if (wave) return;
+  n = sn[0];
+#pragma unroll
+  for (int w = 1; w < 16; ++w) q += sq[w][lane], load += sl[w][lane], n += sn[w];
+  const double mean = n ? q / n : 0.0;
+  double part = n && e < E ? (double)E * load / ((double)a.sh.k * n) * mean : 0.0;
+  if (e < E) {
+    a.load[(size_t)b * E + e] = load;
+    if (a.prob_mean) a.prob_mean[(size_t)b * E + e] = (float)mean;
+    if (a.total_load && load) atomicAdd(&a.total_load[e], load);
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) part += __shfl_xor(part, o);
+  if (lane == 0) {
+    a.part[(size_t)b * gridDim.y + blockIdx.y] = part;
+    if (blockIdx.y == 0) a.valid[b] = n;
+  }
+}
+
+__global__ __launch_bounds__(1024) void balance_total_kernel(BalanceArgs a, int parts) {
+  __shared__ double sl[16];
+  __shared__ int sn[16];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  double loss = 0.0;
+  int live = 0;
+  for (int b = threadIdx.x; b < a.sh.S; b += 1024) {
+    double l = 0.0;
+    for (int p = 0; p < parts; ++p) l += a.part[(size_t)b * parts + p];
+    if (a.seq_loss) a.seq_loss[b] = (float)l;
+    loss += l;
+    live += a.valid[b] > 0;
+  }
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) loss += __shfl_xor(loss, o), live += __shfl_xor(live, o);
+  if (lane == 0) sl[wave] = loss, sn[wave] = live;
+  __syncthreads();
+  if (threadIdx.x) return;
+#pragma unroll
+  for (int w = 1; w < 16; ++w) loss += sl[w], live += sn[w];
+  a.valid[a.sh.S] = live;
+  if (a.loss) *a.loss = live ? (float)(loss / live) : 0.f;
+}
+
+// A wave's tokens are neighbours, so the coefficients change only where a sequence does.
+template <int L, bool SIGMOID, bool VEC>
+__global__ __launch_bounds__(256) void balance_grad_kernel(BalanceGradArgs a, int per) {
+  constexpr int kTok = 64 / L;
+  const int T = a.sh.T, E = a.sh.E, S = a.sh.S;
+  const int lane = threadIdx.x & 63;
+  const int e = (lane % L) * 4, slot = lane / L;
+  const int w0 = __builtin_amdgcn_readfirstlane((blockIdx.x * 4 + (threadIdx.x >> 6)) * per);
+  if (w0 >= T) return;
+  const int w1 = min(w0 + per, T);
+  const float up = a.d_loss ? *a.d_loss : 0.f;
+  const int live_seqs = a.valid[S];
+  auto write = [&](int t, const f32x4& d) {
+    float* row = a.d_logits + (size_t)t * E;
+    if constexpr (VEC) {
+      if (e < E) *reinterpret_cast<f32x4*>(row + e) = d;
+    } else {
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (e + j < E) row[e + j] = d[j];
+    }
+  };
+  int at = w0;                                       // tokens below are done
+  for (int b = sequence_of(a.offsets, S, T, w0); at < w1; ++b) {
+    const int lo = b < S ? min(max(border(a.offsets, b, T), at), w1) : w1;
+    for (int t = at + slot; t < lo; t += kTok) write(t, f32x4{0.f, 0.f, 0.f, 0.f});   // of no sequence
+    if (b >= S) break;
+    const int hi = min(max(border(a.offsets, b + 1, T), lo), w1);
+    at = hi;
+    if (hi <= lo) continue;
+    f32x4 c;
+    const int n = a.valid[b];
+    const double by = n > 0 && live_seqs > 0
+                          ? ((double)up / live_seqs + (a.d_seq_loss ? (double)a.d_seq_loss[b] : 0.0)) * E /
+                                ((double)a.sh.k * n * n)
+                          : 0.0;
+#pragma unroll
+    for (int j = 0; j < 4; ++j) c[j] = e + j < E ? (float)(by * a.load[(size_t)b * E + e + j]) : 0.f;
+    for (int t = lo + slot; t < hi + slot; t += kTok) {
+      const int row = min(t, hi - 1);
+      const bool in = !a.mask || a.mask[row];
+      const f32x4 l = load_logits<VEC>(a.logits + (size_t)row * E, e, E);
+      f32x4 q, rest, d;
+      shares<L, SIGMOID>(l, q, rest);
+      float lead = 0.f, dot = 0.f;
+#pragma unroll
+      for (int j = 0; j < 4; ++j) lead += q[j] > 0.5f ? c[j] : 0.f;
+      lead = sum_of<L>(lead);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) dot = fmaf(c[j] - lead, q[j], dot);
+      dot = sum_of<L>(dot);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        d[j] = q[j] * (c[j] - lead - dot);
+        if (SIGMOID) d[j] *= rest[j];
+        d[j] = in ? d[j] : 0.f;
+      }
+      if (t < hi) write(t, d);
+    }
+  }
+}
+
+// ---- launches ------------------------------------------------------------------------------
+template <typename F>
+static void for_experts(int E, F f) {
+  if (E <= 16) f(std::integral_constant<int, 4>());
+  else if (E <= 32) f(std::integral_constant<int, 8>());
+  else if (E <= 64) f(std::integral_constant<int, 16>());
+  else if (E <= 128) f(std::integral_constant<int, 32>());
+  else f(std::integral_constant<int, 64>());
+}
+
+template <typename F>
+static void for_kind(bool sigmoid, int E, F f) {
+  for_experts(E, [&](auto l) {
+    auto with = [&](auto s) { E % 4 ? f(l, s, std::false_type()) : f(l, s, std::true_type()); };
+    sigmoid ? with(std::true_type()) : with(std::false_type());
+  });
+}
+
+hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
+  const int chunk = chunk_of(a.sh.T), parts = balance_blocks(a.sh.E);
+  for_kind(a.sh.sigmoid, a.sh.E, [&](auto l, auto sig, auto vec) {
+    balance_part_kernel<decltype(l)::value, decltype(sig)::value, decltype(vec)::value>
+        <<<balance_chunks(a.sh), 256, 0, s>>>(a, chunk);
+  });
+  balance_seq_kernel<<<dim3(a.sh.S, parts), 1024, 0, s>>>(a, chunk);
+  balance_total_kernel<<<1, 1024, 0, s>>>(a, parts);
+  return hipGetLastError();
+}
+
+hipError_t launch_balance_grad(const BalanceGradArgs& a, hipStream_t s) {
+  for_kind(a.sh.sigmoid, a.sh.E, [&](auto l, auto sig, auto vec) {
+    constexpr int kTok = 64 / decltype(l)::value;
+    // 8 steps of a wave each while that gives 8192 waves, more beyond.
+    const int per = kTok * std::max(8, (a.sh.T / kTok + 8191) / 8192);
+    const int blocks = (a.sh.T + 4 * per - 1) / (4 * per);
+    balance_grad_kernel<decltype(l)::value, decltype(sig)::value, decltype(vec)::value><<<blocks, 256, 0, s>>>(a, per);
+  });
+  return hipGetLastError();
+}
+
+}  // namespace moe

@@ -1,0 +1,346 @@
+// Layer norm over rows of d values, with the residual add before it, and its gradients.
+//
+//   h = x + add (rounded to x's type, the residual stream)
+//   mean = sum h / d,  rstd = 1 / sqrt(sum (h - mean)^2 / d + eps)
+//   y = (h - mean) rstd w + b
+// Backward, with hat = (h - mean) rstd and g = dy w:
+//   d_x = rstd (g - mean(g) - hat mean(g hat)) + d_x_out
+//   d_w = sum over rows of dy hat,  d_b = sum over rows of dy
+//
+// Memory bounds both.  A group of G threads has a row in registers (8 NV values a thread), so
+// it is read once and the squares are those of the differences from the mean; the groups take
+// rows in turn, and their threads keep the same columns, so weight and bias stay in
+// registers, and so do the column sums of the backward pass.  Those are written once
+// per group and added up, in order, by a second kernel.  Everything is summed in fp32.
+#include <algorithm>
+
+#include "device_common.h"
+#include "norm.h"
+
+namespace moe {
+
+// ---- eight values at a time --------------------------------------------------------------
+__device__ __forceinline__ void load8(const uint16_t* p, float (&v)[8]) {
+  const u32x4 u = ld16(p);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    v[2 * i] = __uint_as_float(u[i] << 16);
+    v[2 * i + 1] = __uint_as_float(u[i] & 0xffff0000u);
+  }
+}
+__device__ __forceinline__ void load8(const float* p, float (&v)[8]) {
+  const f32x4 a = *reinterpret_cast<const f32x4*>(p), b = *reinterpret_cast<const f32x4*>(p + 4);
+#pragma unroll
+  for (int i = 0; i < 4; ++i) v[i] = a[i], v[4 + i] = b[i];
+}
+__device__ __forceinline__ void store8(uint16_t* p, const float (&v)[8]) {
+  u32x4 u;
+#pragma unroll
+  for (int i = 0; i < 4; ++i) u[i] = pack_bf16x2(v[2 * i], v[2 * i + 1]);
+  st16(p, u);
+}
+__device__ __forceinline__ void store8(float* p, const float (&v)[8]) {
+  *reinterpret_cast<f32x4*>(p) = (f32x4){v[0], v[1], v[2], v[3]};
+  *reinterpret_cast<f32x4*>(p + 4) = (f32x4){v[4], v[5], v[6], v[7]};
+}
+__device__ __forceinline__ float load1(const uint16_t* p) { return bf16_to_f32(*p); }
+__device__ __forceinline__ float load1(const float* p) { return *p; }
+__device__ __forceinline__ void store1(uint16_t* p, float v) { *p = (uint16_t)pack_bf16x2(v, 0.f); }
+__device__ __forceinline__ void store1(float* p, float v) { *p = v; }
+// The value that is stored.
+__device__ __forceinline__ float stored(float v, uint16_t) { return __uint_as_float(pack_bf16x2(v, 0.f) << 16); }
+__device__ __forceinline__ float stored(float v, float) { return v; }
+
+// Which columns thread t of a group of G holds: VEC, eight neighbours per 8 G columns (rows
+// of whole 16-byte pieces); else every G-th, so that odd widths and strides still read whole
+// lines.  Columns at and past d hold 0.
+template <int G, int NV, bool VEC>
+struct Columns {
+  static __device__ __forceinline__ int at(int t, int v, int j) {
+    return VEC ? (v * G + t) * 8 + j : (v * 8 + j) * G + t;
+  }
+  template <typename T>
+  static __device__ __forceinline__ void load(const T* row, int t, int d, float (&x)[NV][8]) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if constexpr (VEC) {
+        if (at(t, v, 0) < d) {
+          load8(row + at(t, v, 0), x[v]);
+        } else {
+#pragma unroll
+          for (int j = 0; j < 8; ++j) x[v][j] = 0.f;
+        }
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[v][j] = at(t, v, j) < d ? load1(row + at(t, v, j)) : 0.f;
+      }
+    }
+  }
+  template <typename T>
+  static __device__ __forceinline__ void store(T* row, int t, int d, const float (&x)[NV][8]) {
+#pragma unroll
+    for (int v = 0; v < NV; ++v) {
+      if constexpr (VEC) {
+        if (at(t, v, 0) < d) store8(row + at(t, v, 0), x[v]);
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (at(t, v, j) < d) store1(row + at(t, v, j), x[v][j]);
+      }
+    }
+  }
+  // weight or bias, of either type, or `none` where there is none
+  static __device__ __forceinline__ void load_param(const void* p, bool bf16, float none, int t, int d,
+                                                    float (&x)[NV][8]) {
+    if (!p) {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[v][j] = none;
+    } else if (bf16) {
+      load(static_cast<const uint16_t*>(p), t, d, x);
+    } else {
+      load(static_cast<const float*>(p), t, d, x);
+    }
+  }
+};
+
+// Sums of N values over a group, returned to all its threads.  Groups wider than a wave
+// exchange through `red`; calls alternate its halves, so one barrier each is enough.
+template <int G, int N>
+struct GroupSum {
+  static constexpr int kW = G / 64;
+  float (*red)[N][kW];
+  int half = 0;
+  __device__ __forceinline__ void operator()(float (&v)[N]) {
+#pragma unroll
+    for (int n = 0; n < N; ++n) v[n] = wave_sum_f(v[n]);
+    if constexpr (kW > 1) {
+      if ((threadIdx.x & 63) == 0)
+#pragma unroll
+        for (int n = 0; n < N; ++n) red[half][n][threadIdx.x >> 6] = v[n];
+      __syncthreads();
+#pragma unroll
+      for (int n = 0; n < N; ++n) {
+        float s = red[half][n][0];
+#pragma unroll
+        for (int w = 1; w < kW; ++w) s += red[half][n][w];
+        v[n] = s;
+      }
+      half ^= 1;
+    }
+  }
+};
+
+constexpr int block_of(int G) { return G < 256 ? 256 : G; }
+
+template <typename T, int G, int NV, bool VEC>
+__global__ __launch_bounds__(block_of(G)) void norm_kernel(NormArgs a) {
+  using C = Columns<G, NV, VEC>;
+  constexpr int kGroups = block_of(G) / G;
+  __shared__ float red[2][1][G / 64];
+  GroupSum<G, 1> sum{red};
+  const int t = threadIdx.x % G, d = a.sh.d;
+  const float inv = 1.f / d;
+  float w[NV][8], b[NV][8];
+  C::load_param(a.weight, a.sh.w_bf16, 1.f, t, d, w);
+  C::load_param(a.bias, a.sh.w_bf16, 0.f, t, d, b);
+  for (int64_t row = (int64_t)blockIdx.x * kGroups + threadIdx.x / G; row < a.sh.rows;
+       row += (int64_t)gridDim.x * kGroups) {
+    float x[NV][8];
+    C::load(static_cast<const T*>(a.x.p) + row * a.x.stride, t, d, x);
+    if (a.add.p) {
+      float r[NV][8];
+      if (a.sh.add_bf16) C::load(static_cast<const uint16_t*>(a.add.p) + row * a.add.stride, t, d, r);
+      else C::load(static_cast<const float*>(a.add.p) + row * a.add.stride, t, d, r);
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[v][j] = stored(x[v][j] + r[v][j], T());
+    }
+    if (a.x_out.p) C::store(static_cast<T*>(a.x_out.p) + row * a.x_out.stride, t, d, x);
+    float s[1] = {0.f};
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) s[0] += x[v][j];
+    sum(s);
+    const float mean = s[0] * inv;
+    s[0] = 0.f;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        x[v][j] -= mean;
+        if (C::at(t, v, VEC ? 0 : j) < d) s[0] = fmaf(x[v][j], x[v][j], s[0]);
+      }
+    sum(s);
+    const float rstd = 1.f / sqrtf(fmaf(s[0], inv, a.sh.eps));
+    if (t == 0) {
+      if (a.mean) a.mean[row] = mean;
+      if (a.rstd) a.rstd[row] = rstd;
+    }
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[v][j] = fmaf(x[v][j] * rstd, w[v][j], b[v][j]);
+    C::store(static_cast<T*>(a.y.p) + row * a.y.stride, t, d, x);
+  }
+}
+
+template <typename T, int G, int NV, bool VEC>
+__global__ __launch_bounds__(block_of(G)) void norm_grad_kernel(NormGradArgs a) {
+  using C = Columns<G, NV, VEC>;
+  constexpr int kGroups = block_of(G) / G;
+  __shared__ float red[2][2][G / 64];
+  GroupSum<G, 2> sum{red};
+  const int t = threadIdx.x % G, d = a.sh.d;
+  const int64_t group = (int64_t)blockIdx.x * kGroups + threadIdx.x / G;
+  const float inv = 1.f / d;
+  float w[NV][8], dw[NV][8] = {}, db[NV][8] = {};
+  C::load_param(a.weight, a.sh.w_bf16, 1.f, t, d, w);
+  for (int64_t row = group; row < a.sh.rows; row += (int64_t)gridDim.x * kGroups) {
+    float x[NV][8], g[NV][8];
+    C::load(static_cast<const T*>(a.dy.p) + row * a.dy.stride, t, d, g);
+    C::load(static_cast<const T*>(a.x.p) + row * a.x.stride, t, d, x);
+    const float mean = a.mean[row], rstd = a.rstd[row];
+    float s[2] = {0.f, 0.f};
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        // past d: (0 - mean) rstd may be anything, its dy is 0
+        x[v][j] = C::at(t, v, VEC ? 0 : j) < d ? (x[v][j] - mean) * rstd : 0.f;
+        dw[v][j] = fmaf(g[v][j], x[v][j], dw[v][j]);
+        db[v][j] += g[v][j];
+        g[v][j] *= w[v][j];
+        s[0] += g[v][j];
+        s[1] = fmaf(g[v][j], x[v][j], s[1]);
+      }
+    if (a.d_x.p) {
+      float r[NV][8];
+      if (a.d_x_out.p) {
+        C::load(static_cast<const T*>(a.d_x_out.p) + row * a.d_x_out.stride, t, d, r);
+      } else {
+#pragma unroll
+        for (int v = 0; v < NV; ++v)
+#pragma unroll
+          for (int j = 0; j < 8; ++j) r[v][j] = 0.f;
+      }
+      sum(s);
+      s[0] *= inv;
+      s[1] *= inv;
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[v][j] = fmaf(rstd, g[v][j] - fmaf(x[v][j], s[1], s[0]), r[v][j]);
+      C::store(static_cast<T*>(a.d_x.p) + row * a.d_x.stride, t, d, r);
+    }
+  }
+  float* part = a.part + group * 2 * d;
+  if (a.d_weight) C::store(part, t, d, dw);
+  if (a.d_bias) C::store(part + d, t, d, db);
+}
+
+// Column sums of the groups' partial rows [groups][2 d]: 64 columns a block, 16 waves a
+// sixteenth of the groups each.
+__global__ __launch_bounds__(1024) void norm_sum_kernel(const float* __restrict__ part, int groups, int d,
+                                                        float* __restrict__ d_weight, float* __restrict__ d_bias) {
+  __shared__ float acc[16][64];
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int c = blockIdx.x * 64 + lane;
+  float* out = c < d ? d_weight : d_bias;
+  const bool live = c < 2 * d && out;
+  float s = 0.f;
+  if (live)
+#pragma unroll 8
+    for (int g = wave; g < groups; g += 16) s += part[(size_t)g * 2 * d + c];
+  acc[wave][lane] = s;
+  __syncthreads();
+  if (wave == 0 && live) {
+#pragma unroll
+    for (int w = 1; w < 16; ++w) s += acc[w][lane];
+    out[c < d ? c : c - d] = s;
+  }
+}
+
+// ---- launches ----------------------------------------------------------------------------
+static int group_of(int d) { return d <= 1024 ? 64 : d <= 4096 ? 256 : d <= 8192 ? 512 : 1024; }
+static int groups_per_block(int d) { return block_of(group_of(d)) / group_of(d); }
+
+static int blocks_for(const NormShape& s, int most) {
+  const int per = groups_per_block(s.d);
+  return (int)std::min<int64_t>((s.rows + per - 1) / per, most);
+}
+static int grad_blocks(const NormShape& s) { return blocks_for(s, 512); }
+
+size_t norm_grad_part_bytes(const NormShape& s) {
+  return (size_t)grad_blocks(s) * groups_per_block(s.d) * 2 * s.d * 4;
+}
+
+// Rows of whole 16-byte pieces of eight values.
+template <typename P>
+static bool whole(const Rows<P>& r, int64_t rows, bool bf16) {
+  return !r.p || rows <= 1 || r.stride % (bf16 ? 8 : 4) == 0;
+}
+
+template <typename T, typename F>
+static void for_width(int d, bool vec, F f) {
+  auto with = [&](auto g, auto nv) {
+    if (vec) f(g, nv, std::true_type());
+    else f(g, nv, std::false_type());
+  };
+  using std::integral_constant;
+  if (d <= 512) with(integral_constant<int, 64>(), integral_constant<int, 1>());
+  else if (d <= 1024) with(integral_constant<int, 64>(), integral_constant<int, 2>());
+  else if (d <= 2048) with(integral_constant<int, 256>(), integral_constant<int, 1>());
+  else if (d <= 4096) with(integral_constant<int, 256>(), integral_constant<int, 2>());
+  else if (d <= 8192) with(integral_constant<int, 512>(), integral_constant<int, 2>());
+  else if (d <= 16384) with(integral_constant<int, 1024>(), integral_constant<int, 2>());
+  else with(integral_constant<int, 1024>(), integral_constant<int, 4>());
+}
+
+template <typename T>
+static void run_norm(const NormArgs& a, hipStream_t s) {
+  const NormShape& n = a.sh;
+  const bool vec = n.d % 8 == 0 && whole(a.x, n.rows, n.bf16) && whole(a.add, n.rows, n.add_bf16) &&
+                   whole(a.x_out, n.rows, n.bf16) && whole(a.y, n.rows, n.bf16);
+  const int blocks = blocks_for(n, 2048);
+  for_width<T>(n.d, vec, [&](auto g, auto nv, auto v) {
+    constexpr int G = decltype(g)::value;
+    norm_kernel<T, G, decltype(nv)::value, decltype(v)::value><<<blocks, block_of(G), 0, s>>>(a);
+  });
+}
+
+hipError_t launch_norm(const NormArgs& a, hipStream_t s) {
+  if (a.sh.rows == 0) return hipSuccess;
+  if (a.sh.bf16) run_norm<uint16_t>(a, s);
+  else run_norm<float>(a, s);
+  return hipGetLastError();
+}
+
+template <typename T>
+static void run_grad(const NormGradArgs& a, int blocks, hipStream_t s) {
+  const NormShape& n = a.sh;
+  const bool vec = n.d % 8 == 0 && whole(a.x, n.rows, n.bf16) && whole(a.dy, n.rows, n.bf16) &&
+                   whole(a.d_x_out, n.rows, n.bf16) && whole(a.d_x, n.rows, n.bf16);
+  for_width<T>(n.d, vec, [&](auto g, auto nv, auto v) {
+    constexpr int G = decltype(g)::value;
+    norm_grad_kernel<T, G, decltype(nv)::value, decltype(v)::value><<<blocks, block_of(G), 0, s>>>(a);
+  });
+}
+
+hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s) {
+  const int blocks = grad_blocks(a.sh);
+  if (blocks > 0) {
+    if (a.sh.bf16) run_grad<uint16_t>(a, blocks, s);
+    else run_grad<float>(a, blocks, s);
+    if (hipError_t e = hipGetLastError()) return e;
+  }
+  if (a.d_weight || a.d_bias)                        // no rows: zeros
+    norm_sum_kernel<<<(2 * a.sh.d + 63) / 64, 1024, 0, s>>>(a.part, blocks * groups_per_block(a.sh.d), a.sh.d,
+                                                             a.d_weight, a.d_bias);
+  return hipGetLastError();
+}
+
+}  // namespace moe

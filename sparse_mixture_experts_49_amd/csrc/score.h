@@ -62,9 +62,10 @@ struct ScoreGradArgs {
   const int32_t* topk_idx;
   const float* logits;
   const int32_t* load;     // with d_aux
-  const float* d_topk_w;   // or null, as the next two
+  const float* d_topk_w;   // or null, as the next three
   const float* d_aux;
   const float* d_z;
+  const float* d_logits_in;
   void* d_x;               // or null, as the next three
   float* d_w;
   float* d_b;

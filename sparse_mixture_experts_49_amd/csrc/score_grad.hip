@@ -5,7 +5,7 @@
 //   dq_e = d_aux E load_e / (T k) / T          (q = s / sum s; load is a constant)
 //   softmax: ds = dr + dq;                       dl = s (ds - sum ds s)
 //   sigmoid: ds = dr + (dq - sum dq q) / sum s;  dl = ds s (1 - s) = (dr s + (dq - sum dq q) q) (1 - s)
-//   dl += d_z (2 / T) lse softmax(l)
+//   dl += d_z (2 / T) lse softmax(l) + what reaches the logits from elsewhere
 // The differences with a sum over all experts are formed as of_leader says.
 // and d_b = sum_t dl, d_x = dl W_r, d_W = dl^T x.
 //
@@ -203,6 +203,7 @@ __global__ __launch_bounds__(TT * 16) void score_dlogits_kernel(ScoreGradArgs a)
 #pragma unroll
       for (int j = 0; j < PER; ++j) {
         dl[j] = live[j] ? fmaf(zl, p[j], dl[j]) : 0.f;
+        if (a.d_logits_in && live[j]) dl[j] += a.d_logits_in[(size_t)t * E + j * 64 + lane];
         pb[j] += (double)dl[j];
         a.dl[(size_t)t * kPitch + j * 64 + lane] = dl[j];
       }
