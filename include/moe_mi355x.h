@@ -513,6 +513,56 @@ int moe_layer_norm_backward(const moe_norm_desc* desc, const moe_rows* dy, const
                             float* d_bias, void* workspace, size_t workspace_bytes, void* stream);
 
 /* ---------------------------------------------------------------------------
+ * A shared projection with low-rank adapters of many requests beside it.
+ *
+ * A batch holds tokens of many requests, and each request may have an adapter of its own for a
+ * projection that all of them share (the shared expert's, which runs on every token):
+ *   y_t = act(W x_t + bias + scale_a B_a (A_a x_t)),  a = adapter[t]
+ * An adapter id outside [0, n_adapters) is none: y_t = act(W x_t + bias).  Tokens may be in any
+ * order; runs of tokens of one adapter are fastest.  x, W, A, B and bias are bf16; products
+ * accumulate in fp32 and A x keeps at least 16 bits on its way into B.  What the adapters
+ * of other tokens hold, infinities and NaN included, does not reach a token.  Serving only:
+ * no backward.  Calls, or replays of captured ones, that may overlap need a workspace each. */
+enum { MOE_LORA_ACT_NONE = 0, MOE_LORA_ACT_GELU = 1 };   /* GELU in its erf form */
+
+typedef struct moe_lora_desc {
+  int32_t tokens;          /* T */
+  int32_t d_in;            /* d, a multiple of 128 */
+  int32_t d_out;           /* n, a multiple of 128; T * max(d, n) and d * n under 2^31 */
+  int32_t rank;            /* r, a multiple of 8, at most 128; adapters of less are padded with zeros */
+  int32_t n_adapters;      /* N, 1 .. 4096 */
+  int32_t act;             /* MOE_LORA_ACT_* */
+  int32_t out_dtype;       /* MOE_DTYPE_*: y */
+  int32_t has_bias;        /* 1: bias is given; 0: absent */
+} moe_lora_desc;
+
+typedef struct moe_lora_weights {
+  const void* w;           /* [n][d] bf16 */
+  const void* a;           /* [N][r][d] bf16 */
+  const void* b;           /* [N][n][r] bf16 */
+  const float* scale;      /* [N] fp32, or NULL (1) */
+  const void* bias;        /* [n] bf16, NULL iff !has_bias */
+} moe_lora_weights;
+
+/* Bytes of workspace moe_lora_linear needs (host output). */
+int moe_lora_workspace_size(const moe_lora_desc* desc, size_t* bytes);
+
+/* The projection: x [T][d] bf16, adapter [T] int32, y [T][n]. */
+int moe_lora_linear(const moe_lora_desc* desc, const void* x, const int32_t* adapter,
+                    const moe_lora_weights* w, void* y, void* workspace, size_t workspace_bytes,
+                    void* stream);
+
+/* The shared expert with adapters on both of its products, bit for bit as two calls of
+ * moe_lora_linear: h = GELU(up), bf16, in the workspace; o_shared = down(h) [T][d_model] fp32, as
+ * moe_combine takes it.  up: d_model -> d_ff_shared, MOE_LORA_ACT_GELU, bf16; down: back,
+ * MOE_LORA_ACT_NONE, fp32; ranks, biases and the number of adapters may differ. */
+int moe_lora_shared_workspace_size(const moe_lora_desc* up, const moe_lora_desc* down, size_t* bytes);
+int moe_lora_shared_ffn(const moe_lora_desc* up, const moe_lora_desc* down, const void* x,
+                        const int32_t* adapter, const moe_lora_weights* w_up,
+                        const moe_lora_weights* w_down, float* o_shared, void* workspace,
+                        size_t workspace_bytes, void* stream);
+
+/* ---------------------------------------------------------------------------
  * Experts in microscaled 4-bit floating point (MXFP4).
  *
  * A row of K values is K / 32 blocks of 32.  Block b has one scale byte s (e8m0:

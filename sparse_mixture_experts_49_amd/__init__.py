@@ -16,6 +16,8 @@ from .binding import (ENTRY_POINTS, MOE_CAPACITY_DROP, MOE_CAPACITY_REROUTE, MOE
 from .binding import (BalanceDesc, BalanceOut, NormDesc, alloc_balance_workspace, alloc_norm_workspace, moe_balance_backward,
                       moe_balance_loss, moe_balance_workspace_size, moe_layer_norm, moe_layer_norm_backward,
                       moe_norm_workspace_size, moe_score_backward_add)
+from .binding import (LoraDesc, LoraWeights, alloc_lora_shared_workspace, alloc_lora_workspace, moe_lora_linear,
+                      moe_lora_shared_ffn, moe_lora_shared_workspace_size, moe_lora_workspace_size)
 
 __all__ = ["ENTRY_POINTS", "MOE_CAPACITY_DROP", "MOE_CAPACITY_REROUTE", "MOE_FFN_AUTO", "MOE_FFN_STREAM", "MOE_FFN_TILED", "MOE_H_AUTO",
            "MOE_H_BF16", "MOE_H_SPLIT", "Desc", "MoeError", "MxDesc", "MxWeights", "Routing", "ScoreDesc", "ScoreGrads",
@@ -27,4 +29,6 @@ __all__ = ["ENTRY_POINTS", "MOE_CAPACITY_DROP", "MOE_CAPACITY_REROUTE", "MOE_FFN
            "moe_shared_ffn", "moe_workspace_size",
            "BalanceDesc", "BalanceOut", "NormDesc", "alloc_balance_workspace", "alloc_norm_workspace", "moe_balance_backward",
            "moe_balance_loss", "moe_balance_workspace_size", "moe_layer_norm", "moe_layer_norm_backward",
-           "moe_norm_workspace_size", "moe_score_backward_add"]
+           "moe_norm_workspace_size", "moe_score_backward_add",
+           "LoraDesc", "LoraWeights", "alloc_lora_shared_workspace", "alloc_lora_workspace", "moe_lora_linear",
+           "moe_lora_shared_ffn", "moe_lora_shared_workspace_size", "moe_lora_workspace_size"]

@@ -23,6 +23,8 @@ MOE_SCORE_SOFTMAX, MOE_SCORE_SIGMOID = 0, 1
 _SCORES = {"softmax": MOE_SCORE_SOFTMAX, "sigmoid": MOE_SCORE_SIGMOID}
 MOE_MX_ACT_BF16, MOE_MX_ACT_MXFP4 = 0, 1
 _MX_ACTS = {"bf16": MOE_MX_ACT_BF16, "mxfp4": MOE_MX_ACT_MXFP4}
+MOE_LORA_ACT_NONE, MOE_LORA_ACT_GELU = 0, 1
+_LORA_ACTS = {"none": MOE_LORA_ACT_NONE, "gelu": MOE_LORA_ACT_GELU}
 _DTYPES = {"bf16": MOE_DTYPE_BF16, "f32": MOE_DTYPE_F32}
 _POLICIES = {"drop": MOE_CAPACITY_DROP, "reroute": MOE_CAPACITY_REROUTE}
 
@@ -34,7 +36,8 @@ ENTRY_POINTS = ("moe_status_string", "moe_last_error", "moe_workspace_size", "mo
                 "moe_mx_dispatch", "moe_mx_ffn_up", "moe_mx_ffn_down", "moe_mx_forward",
                 "moe_score_backward_add", "moe_balance_workspace_size", "moe_balance_loss",
                 "moe_balance_backward", "moe_norm_workspace_size", "moe_layer_norm",
-                "moe_layer_norm_backward")
+                "moe_layer_norm_backward", "moe_lora_workspace_size", "moe_lora_linear",
+                "moe_lora_shared_workspace_size", "moe_lora_shared_ffn")
 
 
 class MoeError(RuntimeError):
@@ -105,6 +108,15 @@ class CNormDesc(ctypes.Structure):
                 ("param_dtype", ctypes.c_int32), ("add_dtype", ctypes.c_int32), ("eps", ctypes.c_float)]
 
 
+class CLoraDesc(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int32) for n in
+                ("tokens", "d_in", "d_out", "rank", "n_adapters", "act", "out_dtype", "has_bias")]
+
+
+class CLoraWeights(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in ("w", "a", "b", "scale", "bias")]
+
+
 class CRows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64)]
 
@@ -149,6 +161,10 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_norm_workspace_size": (I, [P, ctypes.POINTER(S)]),
         "moe_layer_norm": (I, [P, P, P, P, P, P, P, P, P, P]),
         "moe_layer_norm_backward": (I, [P, P, P, P, P, P, P, P, P, P, P, S, P]),
+        "moe_lora_workspace_size": (I, [P, ctypes.POINTER(S)]),
+        "moe_lora_linear": (I, [P, P, P, P, P, P, S, P]),
+        "moe_lora_shared_workspace_size": (I, [P, P, ctypes.POINTER(S)]),
+        "moe_lora_shared_ffn": (I, [P, P, P, P, P, P, P, P, S, P]),
         "moe_mx_quantize": (I, [P, I, L, L, L, P, P, P]),
         "moe_mx_dequantize": (I, [P, P, L, L, I, P, L, P]),
         "moe_mx_workspace_size": (I, [P, ctypes.POINTER(S)]),
@@ -845,6 +861,86 @@ def moe_layer_norm_backward(desc: NormDesc, dy, x, mean, rstd, weight=None, d_x_
           c.t(mean, "mean", f32, desc.rows), c.t(rstd, "rstd", f32, desc.rows),
           _norm_rows(c, d_x_out, "d_x_out", dt, desc), _norm_rows(c, d_x, "d_x", dt, desc),
           c.t(d_weight, "d_weight", f32, desc.d), c.t(d_bias, "d_bias", f32, desc.d), ws, nb, stream=stream)
+
+
+# ---- a shared projection with low-rank adapters ----------------------------------------------
+
+@dataclasses.dataclass
+class LoraDesc(_CDescOnce):
+    """Options of a projection with low-rank adapters (moe_lora_desc)."""
+    tokens: int
+    d_in: int
+    d_out: int
+    rank: int
+    n_adapters: int
+    act: str = "none"            # "none" or "gelu"
+    out_dtype: str = "bf16"      # "bf16" or "f32"
+    has_bias: bool = False
+
+    def to_c(self) -> CLoraDesc:
+        return CLoraDesc(self.tokens, self.d_in, self.d_out, self.rank, self.n_adapters,
+                         _LORA_ACTS.get(self.act, -1), _DTYPES.get(self.out_dtype, -1), int(bool(self.has_bias)))
+
+
+@dataclasses.dataclass
+class LoraWeights:
+    """The shared matrix w [d_out, d_in] and the adapters a [N, rank, d_in], b [N, d_out, rank]
+    (bf16), their scales [N] (fp32, or None: 1) and the bias [d_out] (bf16)."""
+    w: torch.Tensor
+    a: torch.Tensor
+    b: torch.Tensor
+    scale: Optional[torch.Tensor] = None
+    bias: Optional[torch.Tensor] = None
+
+
+def moe_lora_workspace_size(desc: LoraDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_lora_workspace_size(desc.ref(), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_lora_workspace(desc: LoraDesc, device) -> torch.Tensor:
+    return torch.empty(moe_lora_workspace_size(desc), dtype=torch.uint8, device=device)
+
+
+def _lora_weights(c: _Call, d: LoraDesc, w: LoraWeights) -> CLoraWeights:
+    N, r, bf = d.n_adapters, d.rank, torch.bfloat16
+    return CLoraWeights(c.t(w.w, "weights.w", bf, d.d_out * d.d_in), c.t(w.a, "weights.a", bf, N * r * d.d_in),
+                        c.t(w.b, "weights.b", bf, N * d.d_out * r), c.t(w.scale, "weights.scale", torch.float32, N),
+                        c.t(w.bias, "weights.bias", bf, d.d_out))
+
+
+def moe_lora_linear(desc: LoraDesc, x, adapter, weights: LoraWeights, y, workspace=None, stream=None):
+    """y = act(W x + bias + scale B A x) with each token's own A, B and scale (adapter: int32 [T],
+    -1 for none)."""
+    c = _Call(x, "x")
+    T = desc.tokens
+    ws, nb = c.ws(workspace, lambda: moe_lora_workspace_size(desc), stream)
+    c.run(load_library().moe_lora_linear, desc.ref(), c.t(x, "x", torch.bfloat16, T * desc.d_in),
+          c.t(adapter, "adapter", torch.int32, T), ctypes.byref(_lora_weights(c, desc, weights)),
+          c.t(y, "y", _torch_dtype(desc.out_dtype), T * desc.d_out), ws, nb, stream=stream)
+
+
+def moe_lora_shared_workspace_size(up: LoraDesc, down: LoraDesc) -> int:
+    n = ctypes.c_size_t(0)
+    _check(load_library().moe_lora_shared_workspace_size(up.ref(), down.ref(), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_lora_shared_workspace(up: LoraDesc, down: LoraDesc, device) -> torch.Tensor:
+    return torch.empty(moe_lora_shared_workspace_size(up, down), dtype=torch.uint8, device=device)
+
+
+def moe_lora_shared_ffn(up: LoraDesc, down: LoraDesc, x, adapter, w_up: LoraWeights, w_down: LoraWeights, o_shared,
+                        workspace=None, stream=None):
+    """The shared expert with adapters on both products; o_shared fp32, as moe_combine takes it."""
+    c = _Call(x, "x")
+    T = up.tokens
+    ws, nb = c.ws(workspace, lambda: moe_lora_shared_workspace_size(up, down), stream)
+    c.run(load_library().moe_lora_shared_ffn, up.ref(), down.ref(), c.t(x, "x", torch.bfloat16, T * up.d_in),
+          c.t(adapter, "adapter", torch.int32, T), ctypes.byref(_lora_weights(c, up, w_up)),
+          ctypes.byref(_lora_weights(c, down, w_down)), c.t(o_shared, "o_shared", torch.float32, T * down.d_out), ws, nb,
+          stream=stream)
 
 
 # ---- experts in microscaled 4-bit floating point ------------------------------------------

@@ -16,7 +16,8 @@ BUILD = os.path.join(PKG, "_build")
 LIB = os.path.join(PKG, "libmoe_mi355x.so")
 SOURCES = ["api.cpp", "api_score.cpp", "score.hip", "score_grad.hip", "api_mx.cpp", "mx_quant.hip",
            "mx_dispatch.hip", "mx_ffn.hip", "mx_tile.hip", "router.hip", "reroute.hip", "permute.hip", "ffn.hip", "combine.hip",
-           "probe.hip", "api_norm.cpp", "norm.hip", "api_balance.cpp", "balance.hip"]
+           "probe.hip", "api_norm.cpp", "norm.hip", "api_balance.cpp", "balance.hip",
+           "api_lora.cpp", "lora.hip", "lora_tile.hip"]
 ARCH = "gfx950"
 
 # -packed-fp32-ops: keep the compiler from emitting packed fp32 VALU ops.

@@ -1,0 +1,41 @@
+// Launchers of the shared projection with low-rank adapters (lora.hip, lora_tile.hip).
+#pragma once
+
+#include <hip/hip_runtime.h>
+#include <stddef.h>
+#include <stdint.h>
+
+namespace moe {
+
+constexpr int kLoraMaxRank = 128, kLoraMaxAdapters = 4096;
+
+struct LoraShape {
+  int T, d, n, rank, N;
+  bool gelu, f32_out;
+};
+
+// Bytes of the adapters' first products u in the workspace.
+size_t lora_u_bytes(const LoraShape& s);
+
+struct LoraArgs {
+  LoraShape sh;
+  const uint16_t* x;          // [T][d]
+  const int32_t* adapter;     // [T]
+  const uint16_t* w;          // [n][d]
+  const uint16_t* bias;       // [n] or null
+  const uint16_t* a;          // [N][rank][d]
+  const uint16_t* b;          // [N][n][rank]
+  const float* scale;         // [N] or null
+  void* y;                    // [T][n] bf16 or fp32
+  void* u;                    // workspace of lora_u_bytes
+};
+hipError_t launch_lora(const LoraArgs& a, hipStream_t s);
+
+// Whether the tiled product runs (lora_tile.hip), and how u is laid out for it: `lora_terms`
+// bf16 matrices [T][lora_pitch] that add up to u.  Else u is fp32 [T][lora_pitch].
+bool lora_tiled(const LoraShape& s);
+inline int lora_pitch(int rank) { return (rank + 15) / 16 * 16; }
+inline int lora_terms(const LoraShape& s) { return s.f32_out ? 3 : 2; }
+hipError_t launch_lora_tile(const LoraArgs& a, hipStream_t s);
+
+}  // namespace moe

@@ -1,0 +1,347 @@
+// The shared projection with low-rank adapters, many tokens: LDS-tiled.
+//
+// Block tile BM tokens x BN columns, 4 waves as 2 x 2, each with BM/2 x BN/2 outputs as 32x32
+// MFMA tiles in fp32 accumulators; the MFMA takes W rows as its first operand, so a lane holds
+// four consecutive columns of a token.  Steps of 64 k go straight from memory into LDS in whole
+// 128-byte lines: two stages of x, three of W, one barrier per step.  A wave that waits to issue
+// a load cannot issue MFMAs, so each half step interleaves MFMAs, the LDS reads of the next
+// half's fragments and its share of the loads in a fixed order.  Persistent blocks: the loads
+// go on into the block's next tile.
+//
+// At a tile's end the adapters join as further steps of k: for each 32 tokens of a wave and each
+// different adapter a among them, B_a (its rows as they lie in memory: 16 bytes are 8 ranks of a
+// column) times u, which the first kernel left as bf16 terms (two under a bf16 result, 17 bits;
+// three under fp32, all of its 24).  Where the 32 tokens have one adapter the products
+// go straight into the accumulators; else each adapter's are taken over by its own tokens only,
+// so what another token or adapter holds, infinities included, never meets them.
+//
+// LDS: rows of 128 B, the eight 16-byte chunks of row r at chunk ^ ((r >> 1) & 7): a fragment
+// read (16 rows, one chunk) touches every bank once.
+#include <algorithm>
+#include <cmath>
+#include <type_traits>
+
+#include "device_common.h"
+#include "lora.h"
+
+namespace moe {
+
+constexpr int kLoraXcds = 8, kLoraBand = 4, kLoraCus = 256;
+
+// Tile of index i: XCD i % 8 owns 4 m-tiles of every group of 32 and walks them n-tile by
+// n-tile, so the blocks it runs together share their tokens in its L2 and all XCDs sweep the
+// same columns of W; leftover m-tiles are dealt round-robin.
+__device__ __forceinline__ bool lora_tile_of(int total, int ntn, int b, int& mt, int& nt) {
+  constexpr int kGroup = kLoraXcds * kLoraBand;
+  const int x = b % kLoraXcds, i = b / kLoraXcds;
+  const int G = total / kGroup, full = G * kLoraBand * ntn, lm = total - G * kGroup;
+  if (i < full) {
+    const int g = i / (kLoraBand * ntn), rem = i - g * kLoraBand * ntn;
+    nt = rem / kLoraBand;
+    mt = g * kGroup + x * kLoraBand + rem % kLoraBand;
+    return true;
+  }
+  const int u = (i - full) * kLoraXcds + x;
+  if (u >= lm * ntn) return false;
+  nt = u / lm;
+  mt = G * kGroup + u % lm;
+  return true;
+}
+
+static long lora_tile_blocks(long total, long ntn) {
+  const long G = total / (kLoraXcds * kLoraBand), lm = total % (kLoraXcds * kLoraBand);
+  return kLoraXcds * (G * kLoraBand * ntn + (lm * ntn + kLoraXcds - 1) / kLoraXcds);
+}
+
+template <int BM, int BN, int TERMS, int OCC>
+__global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraArgs p) {
+  constexpr int kA = BM * 128, kW = BN * 128, kWS = 3;             // bytes a stage; stages of W
+  constexpr int oW = 2 * kA;
+  constexpr int kMT = BM / 64, kNT = BN / 64;                      // 32x32 tiles per wave
+  constexpr int kAI = BM / 32, kWI = BN / 32;                      // 1 KB loads per wave
+  constexpr bool F32 = TERMS == 3;
+  static_assert(2 * kA + kWS * kW <= 160 * 1024, "LDS plan");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kA + kWS * kW];
+
+  const int T = p.sh.T, N = p.sh.n, K = p.sh.d, nk = K / 64;
+  const int ntn = (N + BN - 1) / BN, total = (T + BM - 1) / BM;
+  const int tid = threadIdx.x, lane = tid & 63;
+  const int wave = __builtin_amdgcn_readfirstlane(tid >> 6);
+  const int wm = wave >> 1, wn = wave & 1, fr = lane & 31, fc = lane >> 5;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+
+  struct Where {
+    int r0, n0;
+  };
+  int b = blockIdx.x;
+  auto locate = [&](Where& w) {
+    int mt, nt;
+    if (!lora_tile_of(total, ntn, b, mt, nt)) return false;
+    w = Where{mt * BM, nt * BN};
+    return true;
+  };
+  // Loads: instruction i of a wave fills rows (4 i + wave) 8 + lane / 8.  32-bit lane offsets
+  // (x and W are under 4 GiB) from uniform bases; rows past the end read the last.
+  uint32_t a_off[kAI], w_off[kWI];
+  auto row_of = [&](int i) { return (i * 4 + wave) * 8 + (lane >> 3); };
+  auto chunk_of = [&](int row) { return (uint32_t)(((lane & 7) ^ ((row >> 1) & 7)) << 4); };
+  auto aim_a = [&](const Where& w) {
+#pragma unroll
+    for (int i = 0; i < kAI; ++i) a_off[i] = (uint32_t)min(w.r0 + row_of(i), T - 1) * (uint32_t)K * 2u + chunk_of(row_of(i));
+  };
+  auto aim_w = [&](const Where& w) {
+#pragma unroll
+    for (int i = 0; i < kWI; ++i) w_off[i] = (uint32_t)min(w.n0 + row_of(i), N - 1) * (uint32_t)K * 2u + chunk_of(row_of(i));
+  };
+  const uint8_t *xb = reinterpret_cast<const uint8_t*>(p.x), *wb = reinterpret_cast<const uint8_t*>(p.w);
+  auto load_a = [&](int i, int stage, int step) {
+    dma16(xb + (size_t)step * 128, a_off[i], lds0 + stage * kA + (i * 4 + wave) * 1024);
+  };
+  auto load_w = [&](int i, int stage, int step) {
+    dma16(wb + (size_t)step * 128, w_off[i], lds0 + oW + stage * kW + (i * 4 + wave) * 1024);
+  };
+
+  Where cur, next;
+  if (!locate(cur)) return;
+  next = cur;
+  bool more = true;
+  aim_a(cur);
+  aim_w(cur);
+  int as = 0, ws = 0;                                  // the steps to load next
+  // After a step's loads of W: on to the next step, or tile.  The loads of x follow half a step
+  // later, with the tile found here.  Past the last tile the last step is loaded again, unread.
+  bool a_moves = false;
+  auto advance_w = [&]() {
+    if (++ws < nk) return;
+    if (more) {
+      b += gridDim.x;
+      Where w;
+      more = locate(w);
+      if (more) {
+        next = w;
+        aim_w(w);
+        ws = 0;
+        a_moves = true;
+        return;
+      }
+    }
+    ws = nk - 1;
+  };
+  auto advance_a = [&]() {
+    if (++as < nk) return;
+    if (a_moves) {
+      aim_a(next);
+      as = 0;
+      a_moves = false;
+      return;
+    }
+    as = nk - 1;
+  };
+
+  f32x16 acc[kNT][kMT];
+  constexpr int kReads = 2 * (kMT + kNT), kMfmas = 2 * kMT * kNT;  // per half step
+  constexpr int kPer = 2;                              // reads behind one MFMA, until all are done
+  static_assert(kPer * kMfmas >= kReads, "reads");
+  u32x4 xa[2][kMT], xw[2][kNT], ya[2][kMT], yw[2][kNT];
+  // Fragment addresses: rows 32 apart share their swizzle.
+  const uint32_t swz = (fr >> 1) & 7;
+  const uint32_t a_lane = (uint32_t)(wm * (BM / 2) + fr) * 128, w_lane = oW + (uint32_t)(wn * (BN / 2) + fr) * 128;
+  auto read_at = [&](u32x4 (&fa)[2][kMT], u32x4 (&fw)[2][kNT], int sa, int sw, int half, int r) {
+    const int sl = r / (kMT + kNT), q = r % (kMT + kNT);
+    const uint32_t c = (((half * 2 + sl) * 2 + fc) ^ swz) << 4;
+    if (q < kMT) fa[sl][q] = ld16(lds + (sa * kA + a_lane + c) + q * 4096);
+    else fw[sl][q - kMT] = ld16(lds + (sw * kW + w_lane + c) + (q - kMT) * 4096);
+  };
+  auto half_step = [&](const u32x4 (&fa)[2][kMT], const u32x4 (&fw)[2][kNT], u32x4 (&na)[2][kMT],
+                       u32x4 (&nw)[2][kNT], int sa, int sw, int half, auto load_fn, auto loads) {
+    constexpr int L = decltype(loads)::value;
+#pragma unroll
+    for (int m = 0; m < kMfmas; ++m) {
+      const int sl = m / (kMT * kNT), j = m / kMT % kNT, i = m % kMT;
+      acc[j][i] = mfma32_bf16(fw[sl][j], fa[sl][i], acc[j][i]);
+#pragma unroll
+      for (int r = m * kPer; r < (m + 1) * kPer; ++r)
+        if (r < kReads) read_at(na, nw, sa, sw, half, r);
+#pragma unroll
+      for (int q = m * L / kMfmas; q < (m + 1) * L / kMfmas; ++q) load_fn(q);
+      __builtin_amdgcn_sched_barrier(0);
+    }
+  };
+
+  // The adapters of the tile's tokens, lane l that of row 32 m + l % 32 of the wave (-1: none;
+  // rows past the end take their neighbours').
+  int ids[kMT];
+  auto load_ids = [&](const Where& w) {
+#pragma unroll
+    for (int m = 0; m < kMT; ++m) {
+      const int id = p.adapter[min(w.r0 + wm * (BM / 2) + m * 32 + fr, T - 1)];
+      ids[m] = (uint32_t)id < (uint32_t)p.sh.N ? id : -1;
+    }
+  };
+  const int rank = p.sh.rank, pitch = (rank + 15) / 16 * 16;
+  auto expand = [&](const Where& w) {
+    const uint16_t* u = static_cast<const uint16_t*>(p.u);
+#pragma unroll
+    for (int m = 0; m < kMT; ++m) {
+      const uint16_t* um = u + (size_t)min(w.r0 + wm * (BM / 2) + m * 32 + fr, T - 1) * pitch + fc * 8;
+      uint64_t left = __ballot(ids[m] >= 0);
+      while (left) {
+        const int id = __builtin_amdgcn_readlane(ids[m], __ffsll((unsigned long long)left) - 1);
+        const uint64_t same = __ballot(ids[m] == id);
+        left &= ~same;
+        const bool mine = ids[m] == id, all = same == ~0ull;
+        for (int k = 0; k < pitch; k += 16) {
+          u32x4 bf[kNT], uf[TERMS];
+#pragma unroll
+          for (int j = 0; j < kNT; ++j) {
+            const int col = min(w.n0 + wn * (BN / 2) + j * 32 + fr, N - 1);
+            const bool in = k + fc * 8 < rank;             // rank 8 more than a multiple of 16
+            bf[j] = in ? ld16(p.b + ((size_t)id * N + col) * rank + k + fc * 8) : u32x4{0, 0, 0, 0};
+          }
+#pragma unroll
+          for (int q = 0; q < TERMS; ++q) uf[q] = ld16(um + (size_t)q * T * pitch + k);
+#pragma unroll
+          for (int j = 0; j < kNT; ++j) {
+            if constexpr (BM * BN >= 256 * 256) asm volatile("" : "+a"(acc[j][m]));
+            if (all) {
+#pragma unroll
+              for (int q = 0; q < TERMS; ++q) acc[j][m] = mfma32_bf16(bf[j], uf[q], acc[j][m]);
+            } else {
+              f32x16 t = {};
+#pragma unroll
+              for (int q = 0; q < TERMS; ++q) t = mfma32_bf16(bf[j], uf[q], t);
+#pragma unroll
+              for (int q = 0; q < 16; ++q) acc[j][m][q] = mine ? acc[j][m][q] + t[q] : acc[j][m][q];
+            }
+          }
+        }
+      }
+    }
+  };
+
+  // Bias, GELU, stores straight from the accumulators.  A lane has columns 8 g + 4 fc .. + 3 of
+  // its token; bf16 first swaps between the lane halves, so that one has all 8 columns of g and
+  // the other those of g + 1.
+  auto finish = [&](const Where& w) {
+#pragma unroll
+    for (int j = 0; j < kNT; ++j) {
+      const int col0 = w.n0 + wn * (BN / 2) + j * 32;
+      uint2 braw[4];
+#pragma unroll
+      for (int g = 0; g < 4; ++g)
+        braw[g] = (p.bias && col0 < N) ? *reinterpret_cast<const uint2*>(p.bias + col0 + 8 * g + 4 * fc) : make_uint2(0u, 0u);
+#pragma unroll
+      for (int m = 0; m < kMT; ++m) {
+        const int r = w.r0 + wm * (BM / 2) + m * 32 + fr;
+        const bool in = r < T && col0 < N;
+        // Out of the matrix cores' registers one tile at a time: all at once would spill.
+        if constexpr (BM * BN >= 256 * 256) asm volatile("" : "+a"(acc[j][m]));
+        f32x4 v[4];
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[g][q] = acc[j][m][4 * g + q];
+          v[g][0] += __uint_as_float(braw[g].x << 16);
+          v[g][1] += __uint_as_float(braw[g].x & 0xffff0000u);
+          v[g][2] += __uint_as_float(braw[g].y << 16);
+          v[g][3] += __uint_as_float(braw[g].y & 0xffff0000u);
+        }
+        if (p.sh.gelu) {
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[g][q] = F32 ? gelu_erf(v[g][q]) : gelu_for_bf16(v[g][q]);
+        }
+        if constexpr (F32) {
+          float* o = static_cast<float*>(p.y) + (size_t)r * N + col0 + 4 * fc;
+#pragma unroll
+          for (int g = 0; g < 4; ++g)
+            if (in) *reinterpret_cast<f32x4*>(o + 8 * g) = v[g];
+        } else {
+          uint16_t* o = static_cast<uint16_t*>(p.y) + (size_t)r * N + col0 + 8 * fc;
+#pragma unroll
+          for (int g = 0; g < 4; g += 2) {
+            uint32_t h[2][2];
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+              h[i][0] = pack_bf16x2(v[g + i][0], v[g + i][1]);
+              h[i][1] = pack_bf16x2(v[g + i][2], v[g + i][3]);
+            }
+            const auto s0 = __builtin_amdgcn_permlane32_swap(h[0][0], h[1][0], false, false);
+            const auto s1 = __builtin_amdgcn_permlane32_swap(h[0][1], h[1][1], false, false);
+            if (in) st16(o + 8 * g, u32x4{s0[0], s1[0], s0[1], s1[1]});
+          }
+        }
+      }
+    }
+  };
+
+  // Step t: its x in stage t % 2, its W in t % 3.  First half: MFMAs of the fragments at hand,
+  // reads of the step's second half, loads of W two steps on (into the stage of step t - 1, which
+  // nobody reads any more).  Then all but those have landed; barrier.  Second half: reads of
+  // the next step's first half, loads of x two steps on (every wave is done with this stage).
+#pragma unroll
+  for (int s = 0; s < 2; ++s) {
+#pragma unroll
+    for (int i = 0; i < kWI; ++i) load_w(i, s, ws);
+    advance_w();
+#pragma unroll
+    for (int i = 0; i < kAI; ++i) load_a(i, s, as);
+    advance_a();
+  }
+  __builtin_amdgcn_s_waitcnt(wait_vm(0));
+  __syncthreads();
+#pragma unroll
+  for (int r = 0; r < kReads; ++r) read_at(xa, xw, 0, 0, 0, r);
+  int sa = 0, sw = 0;
+  using LoadsA = std::integral_constant<int, kAI>;
+  using LoadsW = std::integral_constant<int, kWI>;
+  for (;;) {
+#pragma unroll
+    for (int j = 0; j < kNT; ++j)
+#pragma unroll
+      for (int m = 0; m < kMT; ++m)
+#pragma unroll
+        for (int q = 0; q < 16; ++q) acc[j][m][q] = 0.f;
+    const Where done = cur;
+    bool go_on = false;
+    for (int t = 0; t < nk; ++t) {
+      const int sw1 = sw == 2 ? 0 : sw + 1, sw2 = sw == 0 ? 2 : sw - 1;
+      half_step(xa, xw, ya, yw, sa, sw, 1, [&](int i) { load_w(i, sw2, ws); }, LoadsW{});
+      advance_w();
+      __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(kWI));
+      __syncthreads();
+      half_step(ya, yw, xa, xw, sa ^ 1, sw1, 0, [&](int i) { load_a(i, sa, as); }, LoadsA{});
+      advance_a();
+      sa ^= 1;
+      sw = sw1;
+    }
+    go_on = next.r0 != cur.r0 || next.n0 != cur.n0;
+    load_ids(done);
+    expand(done);
+    finish(done);
+    if (!go_on) break;
+    cur = next;
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // no load outlives its LDS
+}
+
+template <int BM, int BN, int OCC>
+static void run_tile(const LoraArgs& a, hipStream_t s) {
+  const long blocks = lora_tile_blocks((a.sh.T + BM - 1) / BM, (a.sh.n + BN - 1) / BN);
+  const unsigned grid = (unsigned)std::min(blocks, (long)kLoraCus * OCC);
+  if (a.sh.f32_out) lora_tile_kernel<BM, BN, 3, OCC><<<grid, 256, 0, s>>>(a);
+  else lora_tile_kernel<BM, BN, 2, OCC><<<grid, 256, 0, s>>>(a);
+}
+
+// At least four steps: the loads run two ahead of the products, into the next tile only.
+bool lora_tiled(const LoraShape& s) { return s.T > 512 && s.d >= 256; }
+
+hipError_t launch_lora_tile(const LoraArgs& a, hipStream_t s) {
+  const long big = (long)((a.sh.T + 255) / 256) * ((a.sh.n + 255) / 256);
+  if (big >= 192) run_tile<256, 256, 1>(a, s);
+  else run_tile<128, 128, 2>(a, s);
+  return hipGetLastError();
+}
+
+}  // namespace moe
