@@ -11,9 +11,9 @@
 // At a tile's end the adapters join as further steps of k: for each 32 tokens of a wave and each
 // different adapter a among them, B_a (its rows as they lie in memory: 16 bytes are 8 ranks of a
 // column) times u, which the first kernel left as bf16 terms (two under a bf16 result, 17 bits;
-// three under fp32, all of its 24).  Where the 32 tokens have one adapter the products
-// go straight into the accumulators; else each adapter's are taken over by its own tokens only,
-// so what another token or adapter holds, infinities included, never meets them.
+// three under fp32, all of its 24).  Where the 32 tokens have several adapters u is 0 for all
+// but a's own; what of B_a is infinite or NaN, so that even 0 times it would spread, is then
+// taken out and the results that it is meant for are made infinite by a product of their own.
 //
 // LDS: rows of 128 B, the eight 16-byte chunks of row r at chunk ^ ((r >> 1) & 7): a fragment
 // read (16 rows, one chunk) touches every bank once.
@@ -52,6 +52,10 @@ static long lora_tile_blocks(long total, long ntn) {
   const long G = total / (kLoraXcds * kLoraBand), lm = total % (kLoraXcds * kLoraBand);
   return kLoraXcds * (G * kLoraBand * ntn + (lm * ntn + kLoraXcds - 1) / kLoraXcds);
 }
+
+// Whether the lower or upper bf16 of a word is infinite or NaN.
+__device__ __forceinline__ bool infinite_lo(uint32_t w) { return (w & 0x7f80u) == 0x7f80u; }
+__device__ __forceinline__ bool infinite_hi(uint32_t w) { return (w & 0x7f800000u) == 0x7f800000u; }
 
 template <int BM, int BN, int TERMS, int OCC>
 __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraArgs p) {
@@ -139,6 +143,17 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraArgs p) {
   };
 
   f32x16 acc[kNT][kMT];
+  // The large tile's accumulators fill the matrix cores' registers: held there, or the compiler
+  // moves some in and out in every step, and all of them at once, by spilling, at the end.
+  auto pin_one = [&](int j, int m) {
+    if constexpr (BM * BN >= 256 * 256) asm volatile("" : "+a"(acc[j][m]));
+  };
+  auto pin = [&]() {
+#pragma unroll
+    for (int j = 0; j < kNT; ++j)
+#pragma unroll
+      for (int m = 0; m < kMT; ++m) pin_one(j, m);
+  };
   constexpr int kReads = 2 * (kMT + kNT), kMfmas = 2 * kMT * kNT;  // per half step
   constexpr int kPer = 2;                              // reads behind one MFMA, until all are done
   static_assert(kPer * kMfmas >= kReads, "reads");
@@ -199,20 +214,33 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraArgs p) {
             bf[j] = in ? ld16(p.b + ((size_t)id * N + col) * rank + k + fc * 8) : u32x4{0, 0, 0, 0};
           }
 #pragma unroll
-          for (int q = 0; q < TERMS; ++q) uf[q] = ld16(um + (size_t)q * T * pitch + k);
+          for (int q = 0; q < TERMS; ++q) {
+            uf[q] = ld16(um + (size_t)q * T * pitch + k);
+            uf[q] = mine ? uf[q] : u32x4{0, 0, 0, 0};
+          }
 #pragma unroll
           for (int j = 0; j < kNT; ++j) {
-            if constexpr (BM * BN >= 256 * 256) asm volatile("" : "+a"(acc[j][m]));
-            if (all) {
+            if (!all) {
+              bool bad = false;
 #pragma unroll
-              for (int q = 0; q < TERMS; ++q) acc[j][m] = mfma32_bf16(bf[j], uf[q], acc[j][m]);
-            } else {
-              f32x16 t = {};
+              for (int i = 0; i < 4; ++i) bad |= infinite_lo(bf[j][i]) | infinite_hi(bf[j][i]);
+              if (__ballot(bad)) {
+                // Infinity for the columns where B is infinite or NaN and the tokens that it is
+                // meant for: products of finite values that overflow; 0 for all others.
+                u32x4 c = {0, 0, 0, 0}, v = {0, 0, 0, 0};
+                const bool column = bad || __shfl_xor((int)bad, 32);
+                if (fc == 0 && column) c[0] = 0x7f7f7f7fu;
+                if (fc == 0 && mine) v[0] = 0x7f7f7f7fu;
+                acc[j][m] = mfma32_bf16(c, v, acc[j][m]);
 #pragma unroll
-              for (int q = 0; q < TERMS; ++q) t = mfma32_bf16(bf[j], uf[q], t);
-#pragma unroll
-              for (int q = 0; q < 16; ++q) acc[j][m][q] = mine ? acc[j][m][q] + t[q] : acc[j][m][q];
+                for (int i = 0; i < 4; ++i) {
+                  if (infinite_lo(bf[j][i])) bf[j][i] &= 0xffff0000u;
+                  if (infinite_hi(bf[j][i])) bf[j][i] &= 0xffffu;
+                }
+              }
             }
+#pragma unroll
+            for (int q = 0; q < TERMS; ++q) acc[j][m] = mfma32_bf16(bf[j], uf[q], acc[j][m]);
           }
         }
       }
@@ -234,8 +262,7 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraArgs p) {
       for (int m = 0; m < kMT; ++m) {
         const int r = w.r0 + wm * (BM / 2) + m * 32 + fr;
         const bool in = r < T && col0 < N;
-        // Out of the matrix cores' registers one tile at a time: all at once would spill.
-        if constexpr (BM * BN >= 256 * 256) asm volatile("" : "+a"(acc[j][m]));
+        pin_one(j, m);
         f32x4 v[4];
 #pragma unroll
         for (int g = 0; g < 4; ++g) {
@@ -306,6 +333,7 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraArgs p) {
     const Where done = cur;
     bool go_on = false;
     for (int t = 0; t < nk; ++t) {
+      pin();
       const int sw1 = sw == 2 ? 0 : sw + 1, sw2 = sw == 0 ? 2 : sw - 1;
       half_step(xa, xw, ya, yw, sa, sw, 1, [&](int i) { load_w(i, sw2, ws); }, LoadsW{});
       advance_w();
