@@ -14,7 +14,7 @@ struct LoraShape {
   bool gelu, f32_out;
 };
 
-// Bytes of the adapters' first products u in the workspace.
+// Bytes of workspace: the adapters' first products u, and parts of sums.
 size_t lora_u_bytes(const LoraShape& s);
 
 struct LoraArgs {
@@ -31,9 +31,8 @@ struct LoraArgs {
 };
 hipError_t launch_lora(const LoraArgs& a, hipStream_t s);
 
-// Whether the tiled product runs (lora_tile.hip), and how u is laid out for it: `lora_terms`
-// bf16 matrices [T][lora_pitch] that add up to u.  Else u is fp32 [T][lora_pitch].
-bool lora_tiled(const LoraShape& s);
+// The tiled product (lora_tile.hip).  u is `lora_terms` bf16 matrices [T][lora_pitch] that add up
+// to scale A x.
 inline int lora_pitch(int rank) { return (rank + 15) / 16 * 16; }
 inline int lora_terms(const LoraShape& s) { return s.f32_out ? 3 : 2; }
 hipError_t launch_lora_tile(const LoraArgs& a, hipStream_t s);

@@ -1,10 +1,10 @@
 // A projection shared by all tokens, with a low-rank adapter of each token's own beside it:
 //   y_t = act(W x_t + bias + scale_a B_a (A_a x_t)),  a = adapter[t]; outside [0, N): no adapter
 //
-// Two kernels: u_t = scale_a A_a x_t, then the projection, which adds B_a u_t at its end.
-// The tokens stay in their order.  A tile of tokens runs once through the list of the
-// different adapters that its tokens have: one for a long request, as many as tokens in a
-// decode batch.
+// The tokens stay in their order.  A tile of tokens runs once through the list of the different
+// adapters that its tokens have: one for a long request, as many as tokens in a decode batch.
+// Three ways: one token (lora_token_kernel), up to some hundred (lora_part_kernel and
+// lora_finish_kernel), more (lora_shrink_kernel, then the tiles of lora_tile.hip).
 #include <algorithm>
 #include <type_traits>
 
@@ -49,23 +49,16 @@ __device__ __forceinline__ void dot_rows(const uint16_t* (&pa)[NA], const uint16
 }
 
 // ---------------------------------------------------------------------------
-// u: a block has 16 MT tokens and first lists the different adapters among them.  An adapter is
-// pitch / 16 groups of 16 ranks; a pass over k takes NS groups, of one adapter or of several, so
-// that x is read once for a few adapters; block y takes every gridDim.y-th pass.  The
-// waves share out k, so the sums meet in LDS.  Bound by reading x, with few tokens by
-// the latency of reading A.
+// u = scale A x before the tiled product, as bf16 terms: a block has 16 MT tokens and first lists
+// the different adapters among them.  An adapter is pitch / 16 groups of 16 ranks; a pass over
+// k takes NS groups, of one adapter or of several, so that x is read once for a few
+// adapters.  The waves share out k, so the sums meet in LDS.  Bound by reading x.
 // ---------------------------------------------------------------------------
-struct ShrinkArgs {
-  LoraArgs a;
-  bool terms;                          // bf16 terms, else fp32
-};
-
 template <int MT, int NS, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(ShrinkArgs p) {
+__global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(LoraArgs a) {
   constexpr int kRows = 16 * MT, kRanks = 16 * NS;
   __shared__ __attribute__((aligned(16))) float part[WAVES][kRows][kRanks];
   __shared__ int list[kRows];
-  const LoraArgs& a = p.a;
   const int T = a.sh.T, d = a.sh.d, rank = a.sh.rank, pitch = (rank + 15) / 16 * 16, per = pitch / 16;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, fc = lane >> 4, t0 = blockIdx.x * kRows;
@@ -81,7 +74,7 @@ __global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(ShrinkArgs p) {
 #pragma unroll
   for (int m = 0; m < MT; ++m) px[m] = a.x + (size_t)min(t0 + m * 16 + fr, T - 1) * d + fc * 8;
   const int groups = count * per;
-  for (int g0 = blockIdx.y * NS; g0 < groups; g0 += gridDim.y * NS) {
+  for (int g0 = 0; g0 < groups; g0 += NS) {
     const uint16_t* pa[NS];
 #pragma unroll
     for (int j = 0; j < NS; ++j) {
@@ -109,18 +102,14 @@ __global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(ShrinkArgs p) {
 #pragma unroll
       for (int q = 0; q < 2; ++q) v[q] = at_rank + q < rank ? v[q] * scale : 0.f;
       const size_t at = (size_t)t * pitch + at_rank;
-      if (!p.terms) {
-        *reinterpret_cast<float2*>(static_cast<float*>(a.u) + at) = make_float2(v[0], v[1]);
-      } else {
-        uint16_t* u = static_cast<uint16_t*>(a.u);
-        const int terms = a.sh.f32_out ? 3 : 2;
-        for (int q = 0; q < terms; ++q) {
-          const uint32_t h = pack_bf16x2(v[0], v[1]);
-          *reinterpret_cast<uint32_t*>(u + (size_t)q * T * pitch + at) = h;
-          // what the term left over; nothing of an infinity
-          v[0] = (h & 0x7f80u) == 0x7f80u ? 0.f : v[0] - __uint_as_float(h << 16);
-          v[1] = (h & 0x7f800000u) == 0x7f800000u ? 0.f : v[1] - __uint_as_float(h & 0xffff0000u);
-        }
+      uint16_t* u = static_cast<uint16_t*>(a.u);
+      const int terms = a.sh.f32_out ? 3 : 2;
+      for (int q = 0; q < terms; ++q) {
+        const uint32_t h = pack_bf16x2(v[0], v[1]);
+        *reinterpret_cast<uint32_t*>(u + (size_t)q * T * pitch + at) = h;
+        // what the term left over; nothing of an infinity
+        v[0] = (h & 0x7f80u) == 0x7f80u ? 0.f : v[0] - __uint_as_float(h << 16);
+        v[1] = (h & 0x7f800000u) == 0x7f800000u ? 0.f : v[1] - __uint_as_float(h & 0xffff0000u);
       }
     }
     __syncthreads();
@@ -128,11 +117,10 @@ __global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(ShrinkArgs p) {
 }
 
 // ---------------------------------------------------------------------------
-// The projection with few tokens, bound by the bytes of W: a block has 16 NMT tokens and 16 NNT
-// columns, its eight waves share out k, fragments go straight from memory to registers.  The
-// sums meet in LDS, where a thread finishes an output: bias, B_a u, activation.
-// FUSED > 0, one token: its adapter's 16 FUSED ranks are further rows beside the block's columns of
-// W, so every block has u itself and there is one launch; its reads of A come from L2.
+// One token: bound by the bytes of W.  A block has 16 NNT columns; its adapter's 16 RANKS ranks are
+// further rows beside them, so every block has u itself and one launch does all; A is read from
+// memory once and then from L2.  Eight waves share out k, fragments go straight from memory to
+// registers, the sums meet in LDS, where a thread finishes a column.
 // ---------------------------------------------------------------------------
 constexpr int kWaves = 8;
 
@@ -146,156 +134,341 @@ __device__ __forceinline__ float dot8(const u32x4& q, const float* u, float s) {
   return s;
 }
 
-template <int NMT, int NNT, int FUSED>
-__global__ __launch_bounds__(kWaves * 64) void lora_stream_kernel(LoraArgs a) {
-  static_assert(!FUSED || NMT == 1, "one token");
-  constexpr int kRows = 16 * NMT, kCols = 16 * NNT, kAll = kCols + 16 * FUSED, NA = NNT + FUSED;
-  constexpr int kThreads = kWaves * 64, kOut = (kRows * kCols + kThreads - 1) / kThreads;
-  constexpr bool kEarly = kOut <= 2;                 // the first 16 ranks of B and u: loaded before the sums meet
-  __shared__ __attribute__((aligned(16))) float part[kWaves][kRows][kAll];
-  __shared__ __attribute__((aligned(16))) float su[FUSED ? 16 * FUSED : 4];
-  __shared__ int ids[kRows];
-  const int T = a.sh.T, d = a.sh.d, n = a.sh.n, rank = a.sh.rank, pitch = (rank + 15) / 16 * 16;
+template <int NNT, int RANKS>
+__global__ __launch_bounds__(kWaves * 64) void lora_token_kernel(LoraArgs a) {
+  constexpr int kCols = 16 * NNT, NA = NNT + RANKS;
+  __shared__ __attribute__((aligned(16))) float part[kWaves][16 * NA];
+  __shared__ __attribute__((aligned(16))) float su[16 * RANKS];
+  const int d = a.sh.d, n = a.sh.n, rank = a.sh.rank;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int fr = lane & 15, fc = lane >> 4, t0 = blockIdx.y * kRows, n0 = blockIdx.x * kCols;
-  if (threadIdx.x < kRows) {
-    const int id = t0 + (int)threadIdx.x < T ? a.adapter[t0 + threadIdx.x] : -1;
-    ids[threadIdx.x] = (uint32_t)id < (uint32_t)a.sh.N ? id : -1;
-  }
-  const uint16_t *px[NMT], *pw[NA];
-#pragma unroll
-  for (int m = 0; m < NMT; ++m) px[m] = a.x + (size_t)min(t0 + m * 16 + fr, T - 1) * d + fc * 8;
+  const int fr = lane & 15, fc = lane >> 4, n0 = blockIdx.x * kCols;
+  const int given = a.adapter[0], id = (uint32_t)given < (uint32_t)a.sh.N ? given : -1;
+  const int any = max(id, 0);                          // without an adapter A and B are read, not used
+  const uint16_t *px[1] = {a.x + fc * 8}, *pw[NA];
 #pragma unroll
   for (int j = 0; j < NNT; ++j) pw[j] = a.w + (size_t)min(n0 + j * 16 + fr, n - 1) * d + fc * 8;
-  __syncthreads();
 #pragma unroll
-  for (int j = 0; j < FUSED; ++j)                    // no adapter: any will do, it is not used
-    pw[NNT + j] = a.a + ((size_t)max(ids[0], 0) * rank + min(j * 16 + fr, rank - 1)) * d + fc * 8;
-  f32x4 acc[NA][NMT] = {};
-  dot_rows<NA, NMT, (NMT + NA >= 7 ? 2 : NMT + NA >= 4 ? 4 : 8), kWaves>(pw, px, d / 32, wave, acc);
-
-  // Output i of a thread, columns fastest.
-  auto where = [&](int i, int& t, int& c, int& id) {
-    const int o = i * kThreads + threadIdx.x;
-    t = t0 + o / kCols;
-    c = n0 + o % kCols;
-    const bool in = o < kRows * kCols && t < T && c < n;
-    id = in ? ids[o / kCols] : -1;
-    return in;
-  };
-  u32x4 qb[kEarly ? kOut : 1][2];
-  f32x4 qu[kEarly && !FUSED ? kOut : 1][4];
-  if constexpr (kEarly) {
-#pragma unroll
-    for (int i = 0; i < kOut; ++i) {
-      int t, c, id;
-      where(i, t, c, id);
-      if (id < 0) continue;
-      const uint16_t* b = a.b + ((size_t)id * n + c) * rank;
-      qb[i][0] = ld16(b);
-      qb[i][1] = rank > 8 ? ld16(b + 8) : u32x4{0, 0, 0, 0};
-      if constexpr (!FUSED) {
-        const float* u = static_cast<const float*>(a.u) + (size_t)t * pitch;
-#pragma unroll
-        for (int q = 0; q < 4; ++q) qu[i][q] = *reinterpret_cast<const f32x4*>(u + 4 * q);
-      }
-    }
+  for (int j = 0; j < RANKS; ++j) pw[NNT + j] = a.a + ((size_t)any * rank + min(j * 16 + fr, rank - 1)) * d + fc * 8;
+  // The thread's column (its first 16 ranks of B), scale and bias, under way with the rest.
+  const int c = min(n0 + (int)threadIdx.x, n - 1);
+  u32x4 qb[2] = {};
+  float bias = 0.f, scale = 1.f;
+  if (threadIdx.x < kCols) {
+    const uint16_t* b = a.b + ((size_t)any * n + c) * rank;
+    qb[0] = ld16(b);
+    if (rank > 8) qb[1] = ld16(b + 8);
+    if (a.bias) bias = bf16_to_f32(a.bias[c]);
   }
+  if (a.scale) scale = a.scale[any];
+  f32x4 acc[NA][1] = {};
+  dot_rows<NA, 1, (NA >= 5 ? 4 : NA >= 3 ? 8 : 12), kWaves>(pw, px, d / 32, wave, acc);
+  // Every token of the tile is the same one: lane fr = 0 has columns 4 fc .. + 3.
+  if (fr == 0)
 #pragma unroll
-  for (int j = 0; j < NA; ++j)
-#pragma unroll
-    for (int m = 0; m < NMT; ++m)
-      *reinterpret_cast<f32x4*>(&part[wave][m * 16 + fr][j * 16 + fc * 4]) = acc[j][m];
+    for (int j = 0; j < NA; ++j) *reinterpret_cast<f32x4*>(&part[wave][j * 16 + fc * 4]) = acc[j][0];
   __syncthreads();
-  if constexpr (FUSED > 0) {
-    if (threadIdx.x < 16 * FUSED) {
-      float v = 0.f;
-#pragma unroll
-      for (int w = 0; w < kWaves; ++w) v += part[w][0][kCols + threadIdx.x];
-      su[threadIdx.x] = (int)threadIdx.x < rank ? v * (a.scale && ids[0] >= 0 ? a.scale[ids[0]] : 1.f) : 0.f;
-    }
-    __syncthreads();
-  }
-#pragma unroll
-  for (int i = 0; i < kOut; ++i) {
-    int t, c, id;
-    if (!where(i, t, c, id)) continue;
+  auto sum = [&](int i) {
     float v = 0.f;
 #pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += part[w][t - t0][c - n0];
-    if (a.bias) v += bf16_to_f32(a.bias[c]);
-    if (id >= 0) {
-      const uint16_t* b = a.b + ((size_t)id * n + c) * rank;
-      const float* u = FUSED ? su : static_cast<const float*>(a.u) + (size_t)t * pitch;
-      float s = 0.f;
-      int r = 0;
-      if constexpr (kEarly) {
-        const float* u0 = FUSED ? su : reinterpret_cast<const float*>(qu[FUSED ? 0 : i]);
-        s = dot8(qb[i][0], u0, s);
-        if (rank > 8) s = dot8(qb[i][1], u0 + 8, s);
-        r = 16;
-      }
-      for (; r < rank; r += 8) {
-        f32x4 v4[2] = {*reinterpret_cast<const f32x4*>(u + r), *reinterpret_cast<const f32x4*>(u + r + 4)};
-        s = dot8(ld16(b + r), reinterpret_cast<const float*>(v4), s);
-      }
-      v += s;
+    for (int w = 0; w < kWaves; ++w) v += part[w][i];
+    return v;
+  };
+  // The last wave sums u, the first columns' threads what they wait for anyway.
+  if ((int)threadIdx.x >= kWaves * 64 - 16 * RANKS) {
+    const int r = threadIdx.x - (kWaves * 64 - 16 * RANKS);
+    su[r] = r < rank ? sum(kCols + r) * scale : 0.f;
+  }
+  float v = threadIdx.x < kCols ? sum(threadIdx.x) + bias : 0.f;
+  __syncthreads();
+  if (threadIdx.x >= kCols || n0 + (int)threadIdx.x >= n) return;
+  if (id >= 0) {
+    float s = dot8(qb[0], su, 0.f);
+    if (rank > 8) s = dot8(qb[1], su + 8, s);
+    for (int r = 16; r < rank; r += 8) s = dot8(ld16(a.b + ((size_t)id * n + c) * rank + r), su + r, s);
+    v += s;
+  }
+  if (a.sh.f32_out) static_cast<float*>(a.y)[c] = a.sh.gelu ? gelu_erf(v) : v;
+  else static_cast<uint16_t*>(a.y)[c] = (uint16_t)pack_bf16x2(a.sh.gelu ? gelu_for_bf16(v) : v, 0.f);
+}
+
+// ---------------------------------------------------------------------------
+// Up to some hundred tokens: the bytes of W bound it, and the latency of what has to wait for
+// what.  So W x and A x go in one kernel, as columns of one product: a block has BM tokens
+// and 64 columns, of W or of the adapters that its tokens have (16 ranks of one after the other's),
+// and one part of k.  It stores fp32 sums, of A x a token's own adapter's only.  A second kernel
+// adds up the parts, B u, the bias and the activation.
+//
+// Both operands go from memory into LDS in runs of RB bytes of every row, ST stages, the
+// 16-byte pieces of row r at piece ^ swizzle(r) so that 16 rows' reads of one piece touch every
+// bank once.  Four waves as WM x 4 / WM.  Two blocks fit a CU, so one's start and end go under
+// the other's loads.
+// ---------------------------------------------------------------------------
+struct PartArgs {
+  LoraArgs a;
+  int splits, a_tiles;                 // parts of k; column tiles that A can have per BM tokens
+  float* part;                         // [splits][T][n]
+  float* u;                            // [splits][T][pitch]
+};
+
+constexpr int kPartCols = 64;
+
+template <int BM, int RB, int ST, int WM>
+__global__ __launch_bounds__(256, 2) void lora_part_kernel(PartArgs p) {
+  constexpr int kPieces = RB / 16, kPer = 1024 / RB;             // of a row; rows per load
+  constexpr int kA = BM * RB, kStage = (BM + kPartCols) * RB;
+  constexpr int kAI = kA / 4096, kWI = kPartCols * RB / 4096, L = kAI + kWI;   // loads per wave
+  constexpr int kM = BM / WM / 16, kN = kPartCols * WM / 64;     // 16x16 tiles per wave
+  static_assert(kA % 4096 == 0 && 2 * (ST * kStage + BM * 8 + 64) <= 160 * 1024, "LDS plan");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[ST * kStage];
+  __shared__ int ids[BM], list[BM];
+  const LoraArgs& a = p.a;
+  const int T = a.sh.T, d = a.sh.d, n = a.sh.n, rank = a.sh.rank, pitch = (rank + 15) / 16 * 16, per = pitch / 16;
+  const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
+  const int fr = lane & 15, fc = lane >> 4, wm = wave % WM, wn = wave / WM;
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
+
+  // Block b: the row tiles of one (column tile, part of k) follow one another on one XCD.
+  const int mts = (T + BM - 1) / BM, cols = n / kPartCols + p.a_tiles;
+  const int q = blockIdx.x / 8, cs = q / mts * 8 + blockIdx.x % 8;
+  if (cs >= cols * p.splits) return;
+  const int t0 = q % mts * BM, col = cs % cols, split = cs / cols;
+  const bool of_a = col >= n / kPartCols;
+  const int g0 = (col - n / kPartCols) * 4;            // of A: its first group of 16 ranks
+  int groups = 0;
+  if (of_a) {
+    int own[(BM + 63) / 64];
+    uint64_t left[(BM + 63) / 64];
+#pragma unroll
+    for (int i = 0; i < (BM + 63) / 64; ++i) {
+      const int r = i * 64 + lane;
+      own[i] = r < BM && t0 + r < T ? a.adapter[t0 + r] : -1;
+      if ((uint32_t)own[i] >= (uint32_t)a.sh.N) own[i] = -1;
+      left[i] = __ballot(own[i] >= 0);
+      if (r < BM) ids[r] = own[i];                     // every wave the same values
     }
-    if (a.sh.f32_out) {
-      static_cast<float*>(a.y)[(size_t)t * n + c] = a.sh.gelu ? gelu_erf(v) : v;
+    int count = 0;
+#pragma unroll
+    for (int i = 0; i < (BM + 63) / 64; ++i)
+      for (; left[i]; ++count) {
+        const int one = __builtin_amdgcn_readlane(own[i], __ffsll((unsigned long long)left[i]) - 1);
+#pragma unroll
+        for (int j = 0; j < (BM + 63) / 64; ++j) left[j] &= ~__ballot(own[j] == one);
+        list[count] = one;
+      }
+    groups = count * per;
+    if (g0 >= groups) return;
+    __syncthreads();
+  }
+
+  // Loads: instruction i of a wave fills rows (4 i + wave) kPer + lane / kPieces, of one group of
+  // 16 ranks where they are A's.
+  const uint32_t row_bytes = (uint32_t)d * 2u;
+  auto row_of = [&](int i) { return (i * 4 + wave) * kPer + lane / kPieces; };
+  auto piece_of = [&](int row) { return (uint32_t)((lane % kPieces) ^ (RB == 256 ? row & 15 : (row >> 1) & 7)) << 4; };
+  uint32_t x_off[kAI], w_off[kWI];
+  const uint8_t* w_base[kWI];
+#pragma unroll
+  for (int i = 0; i < kAI; ++i) x_off[i] = (uint32_t)min(t0 + row_of(i), T - 1) * row_bytes + piece_of(row_of(i));
+#pragma unroll
+  for (int i = 0; i < kWI; ++i) {
+    const int row = row_of(i);
+    if (of_a) {
+      const int g = min(g0 + (i * 4 + wave) * kPer / 16, groups - 1);
+      const int id = __builtin_amdgcn_readfirstlane(list[g / per]);
+      w_base[i] = reinterpret_cast<const uint8_t*>(a.a) + (size_t)id * rank * row_bytes;
+      w_off[i] = (uint32_t)min(g % per * 16 + row % 16, rank - 1) * row_bytes + piece_of(row);
     } else {
-      static_cast<uint16_t*>(a.y)[(size_t)t * n + c] = (uint16_t)pack_bf16x2(a.sh.gelu ? gelu_for_bf16(v) : v, 0.f);
+      w_base[i] = reinterpret_cast<const uint8_t*>(a.w) + (size_t)col * kPartCols * row_bytes;
+      w_off[i] = (uint32_t)row * row_bytes + piece_of(row);
     }
+  }
+  const int nk = d / (RB / 2), k0 = (int)((long)split * nk / p.splits), k1 = (int)((long)(split + 1) * nk / p.splits);
+  auto load = [&](int step, int stage) {               // past the part's end: its last step, never read
+    const size_t k = (size_t)min(step, k1 - 1) * RB;
+    const uint32_t to = lds0 + stage * kStage;
+#pragma unroll
+    for (int i = 0; i < kWI; ++i) dma16(w_base[i] + k, w_off[i], to + kA + (i * 4 + wave) * 1024);
+#pragma unroll
+    for (int i = 0; i < kAI; ++i)
+      dma16(reinterpret_cast<const uint8_t*>(a.x) + k, x_off[i], to + (i * 4 + wave) * 1024);
+  };
+#pragma unroll
+  for (int s = 0; s < ST - 1; ++s) load(k0 + s, s);
+  f32x4 acc[kN][kM] = {};
+  const uint32_t swz = RB == 256 ? fr : (fr >> 1) & 7;
+  int stage = 0;
+  for (int step = k0; step < k1; ++step) {
+    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0((ST - 2) * L));
+    __syncthreads();                                   // the step has landed, the one before is read
+    load(step + ST - 1, stage == 0 ? ST - 1 : stage - 1);
+    const uint8_t* at = lds + stage * kStage;
+#pragma unroll
+    for (int s = 0; s < RB / 64; ++s) {
+      u32x4 xf[kM], wf[kN];
+      const uint32_t piece = ((4 * s + fc) ^ swz) << 4;
+#pragma unroll
+      for (int m = 0; m < kM; ++m) xf[m] = ld16(at + (wm * (BM / WM) + m * 16 + fr) * RB + piece);
+#pragma unroll
+      for (int j = 0; j < kN; ++j) wf[j] = ld16(at + kA + (wn * kN * 16 + j * 16 + fr) * RB + piece);
+#pragma unroll
+      for (int j = 0; j < kN; ++j)
+#pragma unroll
+        for (int m = 0; m < kM; ++m) acc[j][m] = mfma_bf16(wf[j], xf[m], acc[j][m]);
+    }
+    stage = stage == ST - 1 ? 0 : stage + 1;
+  }
+  asm volatile("s_waitcnt vmcnt(0)" ::: "memory");     // no load outlives its LDS
+  // A lane has columns 4 fc .. + 3 of token fr.
+#pragma unroll
+  for (int j = 0; j < kN; ++j)
+#pragma unroll
+    for (int m = 0; m < kM; ++m) {
+      const int row = wm * (BM / WM) + m * 16 + fr, t = t0 + row, c = (wn * kN + j) * 16 + fc * 4;
+      if (t >= T) continue;
+      f32x4 v = acc[j][m];
+      if (!of_a) {
+        *reinterpret_cast<f32x4*>(p.part + ((size_t)split * T + t) * n + col * kPartCols + c) = v;
+      } else {
+        const int g = g0 + c / 16;
+        if (g >= groups || ids[row] != list[g / per]) continue;
+        const int r = g % per * 16 + c % 16;
+#pragma unroll
+        for (int i = 0; i < 4; ++i) v[i] = r + i < rank ? v[i] : 0.f;
+        *reinterpret_cast<f32x4*>(p.u + ((size_t)split * T + t) * pitch + r) = v;
+      }
+    }
+}
+
+// Parts of k added up in order, then bias, B u, activation: a block one token's 1024 columns, four
+// a thread.
+__global__ __launch_bounds__(256) void lora_finish_kernel(PartArgs p) {
+  __shared__ __attribute__((aligned(16))) float su[kLoraMaxRank];
+  const LoraArgs& a = p.a;
+  const int T = a.sh.T, n = a.sh.n, rank = a.sh.rank, pitch = (rank + 15) / 16 * 16;
+  const int t = blockIdx.x, c = (blockIdx.y * 256 + threadIdx.x) * 4;
+  const int given = a.adapter[t], id = (uint32_t)given < (uint32_t)a.sh.N ? given : -1;
+  const bool in = c < n;
+  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  u32x4 q[4][2] = {};
+  const uint16_t* b = a.b + ((size_t)max(id, 0) * n + min(c, n - 4)) * rank;
+  if (in && id >= 0) {                                 // the first 16 ranks, under way with the sums
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      q[i][0] = ld16(b + i * rank);
+      if (rank > 8) q[i][1] = ld16(b + i * rank + 8);
+    }
+  }
+  if (in) {
+#pragma unroll 4
+    for (int s = 0; s < p.splits; ++s) v += *reinterpret_cast<const f32x4*>(p.part + ((size_t)s * T + t) * n + c);
+    if (a.bias) {
+      const uint2 w = *reinterpret_cast<const uint2*>(a.bias + c);
+      v[0] += __uint_as_float(w.x << 16);
+      v[1] += __uint_as_float(w.x & 0xffff0000u);
+      v[2] += __uint_as_float(w.y << 16);
+      v[3] += __uint_as_float(w.y & 0xffff0000u);
+    }
+  }
+  if (id >= 0) {
+    if ((int)threadIdx.x < pitch) {
+      float u = 0.f;
+#pragma unroll 4
+      for (int s = 0; s < p.splits; ++s) u += p.u[((size_t)s * T + t) * pitch + threadIdx.x];
+      su[threadIdx.x] = u * (a.scale ? a.scale[id] : 1.f);
+    }
+    __syncthreads();
+    if (in)
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        float s = dot8(q[i][0], su, 0.f);
+        if (rank > 8) s = dot8(q[i][1], su + 8, s);
+        for (int r = 16; r < rank; r += 8) s = dot8(ld16(b + i * rank + r), su + r, s);
+        v[i] += s;
+      }
+  }
+  if (!in) return;
+  if (a.sh.f32_out) {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = a.sh.gelu ? gelu_erf(v[i]) : v[i];
+    *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + (size_t)t * n + c) = v;
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) v[i] = a.sh.gelu ? gelu_for_bf16(v[i]) : v[i];
+    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + (size_t)t * n + c) =
+        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
   }
 }
 
 // ---- launches ------------------------------------------------------------------------------
+enum LoraPath { kToken, kPart, kTile };
+
+static LoraPath path_of(const LoraShape& s) {
+  if (s.T == 1 && s.rank <= 32) return kToken;
+  // Tiles need four steps of 64 k: their loads run two ahead, into the next tile only.
+  return s.T > 512 && s.d >= 256 ? kTile : kPart;
+}
+
+// Tokens of a block, and the parts that k is cut into so that every CU has a block.
+static int part_rows(const LoraShape& s) { return s.T <= 32 ? 32 : s.T <= 64 ? 64 : 128; }
+static int part_splits(const LoraShape& s) {
+  const int bm = part_rows(s), steps = s.d / (bm == 32 ? 128 : 64);
+  const long tiles = (long)((s.T + bm - 1) / bm) * (s.n / kPartCols);
+  return (int)std::max(1L, std::min({(256 + tiles / 2) / tiles, (long)steps / 2, 16L}));
+}
+
 size_t lora_u_bytes(const LoraShape& s) {
-  return (size_t)s.T * lora_pitch(s.rank) * (lora_tiled(s) ? 2 * lora_terms(s) : 4);
+  const size_t T = s.T, pitch = lora_pitch(s.rank);
+  switch (path_of(s)) {
+    case kToken: return 256;
+    case kTile: return T * pitch * 2 * lora_terms(s);
+    default: return part_splits(s) * T * (s.n + pitch) * 4;
+  }
 }
 
-template <int MT, int NS, int WAVES>
-static void run_shrink(const ShrinkArgs& p, int passes, hipStream_t s) {
-  const dim3 grid((p.a.sh.T + 16 * MT - 1) / (16 * MT), passes);
-  lora_shrink_kernel<MT, NS, WAVES><<<grid, WAVES * 64, 0, s>>>(p);
+template <int MT>
+static void run_shrink(const LoraArgs& a, hipStream_t s) {
+  lora_shrink_kernel<MT, 4, kWaves><<<(a.sh.T + 16 * MT - 1) / (16 * MT), kWaves * 64, 0, s>>>(a);
 }
 
-static void launch_shrink(const ShrinkArgs& p, hipStream_t s) {
-  const LoraShape& h = p.a.sh;
-  const int per = lora_pitch(h.rank) / 16;
-  const int tiles = (h.T + 15) / 16, most = std::min(h.N, 16) * per;   // groups that a tile of 16 can have
-  if (tiles <= 64) run_shrink<1, 1, 16>(p, std::min(most, 1024 / tiles), s);
-  else if (tiles <= 256) run_shrink<1, 4, 8>(p, std::max(1, std::min((most + 3) / 4, 512 / tiles)), s);
-  else if (tiles <= 1024) run_shrink<2, 4, 8>(p, 1, s);
-  else run_shrink<4, 4, 8>(p, 1, s);
+static hipError_t launch_part(const LoraArgs& a, hipStream_t s) {
+  const LoraShape& h = a.sh;
+  PartArgs p{a, part_splits(h), 0, static_cast<float*>(a.u), nullptr};
+  p.u = p.part + (size_t)p.splits * h.T * h.n;
+  const int bm = part_rows(h), mts = (h.T + bm - 1) / bm;
+  p.a_tiles = (std::min(h.N, std::min(h.T, bm)) * (lora_pitch(h.rank) / 16) + 3) / 4;
+  const int cs = (h.n / kPartCols + p.a_tiles) * p.splits;
+  const unsigned grid = (unsigned)((cs + 7) / 8 * mts * 8);
+  if (bm == 32) lora_part_kernel<32, 256, 3, 1><<<grid, 256, 0, s>>>(p);
+  else if (bm == 64) lora_part_kernel<64, 128, 4, 2><<<grid, 256, 0, s>>>(p);
+  else lora_part_kernel<128, 128, 3, 2><<<grid, 256, 0, s>>>(p);
+  if (hipError_t e = hipGetLastError()) return e;
+  lora_finish_kernel<<<dim3(h.T, (h.n + 1023) / 1024), 256, 0, s>>>(p);
+  return hipGetLastError();
+}
+
+template <int RANKS>
+static void launch_token(const LoraArgs& a, hipStream_t s) {
+  const int n = a.sh.n;
+  if (n >= 12288) lora_token_kernel<4, RANKS><<<(n + 63) / 64, kWaves * 64, 0, s>>>(a);
+  else if (n >= 8192) lora_token_kernel<2, RANKS><<<(n + 31) / 32, kWaves * 64, 0, s>>>(a);
+  else lora_token_kernel<1, RANKS><<<(n + 15) / 16, kWaves * 64, 0, s>>>(a);
 }
 
 hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
-  using std::integral_constant;
-  const integral_constant<int, 0> none;
-  const integral_constant<int, 1> one;
-  const integral_constant<int, 2> two;
-  const integral_constant<int, 4> four;
-  auto stream = [&](auto mt, auto nt, auto fused) {
-    constexpr int M = decltype(mt)::value, C = decltype(nt)::value;
-    const dim3 grid((a.sh.n + 16 * C - 1) / (16 * C), (a.sh.T + 16 * M - 1) / (16 * M));
-    lora_stream_kernel<M, C, decltype(fused)::value><<<grid, kWaves * 64, 0, s>>>(a);
-    return hipGetLastError();
-  };
-  if (a.sh.T == 1 && a.sh.rank <= 32) {
-    auto wide = [&](auto fused) {
-      return a.sh.n >= 12288 ? stream(one, four, fused) : a.sh.n >= 8192 ? stream(one, two, fused) : stream(one, one, fused);
-    };
-    return a.sh.rank <= 16 ? wide(one) : wide(two);
+  switch (path_of(a.sh)) {
+    case kToken:
+      if (a.sh.rank <= 16) launch_token<1>(a, s);
+      else launch_token<2>(a, s);
+      return hipGetLastError();
+    case kTile:
+      if (a.sh.T > 16384) run_shrink<4>(a, s);
+      else if (a.sh.T > 4096) run_shrink<2>(a, s);
+      else run_shrink<1>(a, s);
+      if (hipError_t e = hipGetLastError()) return e;
+      return launch_lora_tile(a, s);
+    default:
+      return launch_part(a, s);
   }
-  const bool tiled = lora_tiled(a.sh);
-  launch_shrink(ShrinkArgs{a, tiled}, s);
-  if (hipError_t e = hipGetLastError()) return e;
-  if (tiled) return launch_lora_tile(a, s);
-  if (a.sh.T <= 16) return a.sh.n >= 8192 ? stream(one, two, none) : stream(one, one, none);
-  if (a.sh.T <= 32) return a.sh.n >= 8192 ? stream(two, two, none) : stream(two, one, none);
-  if ((long)((a.sh.T + 63) / 64) * a.sh.n >= 64 * 256) return stream(four, four, none);
-  return stream(four, one, none);
 }
 
 }  // namespace moe

@@ -362,9 +362,6 @@ static void run_tile(const LoraArgs& a, hipStream_t s) {
   else lora_tile_kernel<BM, BN, 2, OCC><<<grid, 256, 0, s>>>(a);
 }
 
-// At least four steps: the loads run two ahead of the products, into the next tile only.
-bool lora_tiled(const LoraShape& s) { return s.T > 512 && s.d >= 256; }
-
 hipError_t launch_lora_tile(const LoraArgs& a, hipStream_t s) {
   const long big = (long)((a.sh.T + 255) / 256) * ((a.sh.n + 255) / 256);
   if (big >= 192) run_tile<256, 256, 1>(a, s);
