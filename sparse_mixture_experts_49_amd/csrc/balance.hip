@@ -119,7 +119,7 @@ __device__ __forceinline__ int sequence_of(const int32_t* __restrict__ offsets, 
 
 template <int L, bool SIGMOID, bool VEC>
 __global__ __launch_bounds__(256) void balance_part_kernel(BalanceArgs a, int chunk) {
-  constexpr int kTok = 64 / L;                       // tokens of a wave at once
+  constexpr int kTok = 64 / L, kAhead = 4;           // tokens of a wave at once; such steps under way
   __shared__ float sum_q[4][4 * L];
   __shared__ int hist[kBalanceMaxExperts];
   __shared__ int count;
@@ -137,13 +137,22 @@ __global__ __launch_bounds__(256) void balance_part_kernel(BalanceArgs a, int ch
     if (lo >= t1) break;
     if (hi <= lo) continue;
     f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    for (int t = lo + slot; t < hi + slot; t += 4 * kTok) {      // the same trips for all lanes of a wave
-      const bool in = t < hi && (!a.mask || a.mask[t]);
-      const f32x4 l = load_logits<VEC>(a.logits + (size_t)min(t, hi - 1) * E, e, E);
-      f32x4 q, rest;
-      shares<L, SIGMOID>(l, q, rest);
+    for (int t = lo + slot; t < hi + slot; t += kAhead * 4 * kTok) {      // the same trips for all lanes of a wave
+      f32x4 l[kAhead];
+      bool in[kAhead];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] += in ? q[j] : 0.f;
+      for (int i = 0; i < kAhead; ++i) {
+        const int at = t + i * 4 * kTok;
+        l[i] = load_logits<VEC>(a.logits + (size_t)min(at, hi - 1) * E, e, E);
+        in[i] = at < hi && (!a.mask || a.mask[at]);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        f32x4 q, rest;
+        shares<L, SIGMOID>(l[i], q, rest);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] += in[i] ? q[j] : 0.f;
+      }
     }
     int n = 0;
     for (int i = threadIdx.x; i < (hi - lo) * k; i += 256) {

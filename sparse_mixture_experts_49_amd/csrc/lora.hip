@@ -13,91 +13,102 @@
 
 namespace moe {
 
-// Fragments of `NA` and `NB` 16-row groups, 32 values of k each, through U register stages; the
-// WAVES waves of a block take every WAVES-th step of k.  acc[j][m] += A_j B_m^T.
-template <int NA, int NB, int U, int WAVES>
-__device__ __forceinline__ void dot_rows(const uint16_t* (&pa)[NA], const uint16_t* (&pb)[NB], int steps, int wave,
-                                         f32x4 (&acc)[NA][NB]) {
-  u32x4 fa[U][NA], fb[U][NB];
-  const int mine = (steps - wave + WAVES - 1) / WAVES, last = steps - 1;
-  auto load = [&](int slot, int i) {                 // past the end: the last step again, not used
-    const int k = min(wave + i * WAVES, last) * 32;
-#pragma unroll
-    for (int j = 0; j < NA; ++j) fa[slot][j] = ld16(pa[j] + k);
-#pragma unroll
-    for (int m = 0; m < NB; ++m) fb[slot][m] = ld16(pb[m] + k);
-  };
-  auto multiply = [&](int slot) {
-#pragma unroll
-    for (int j = 0; j < NA; ++j)
-#pragma unroll
-      for (int m = 0; m < NB; ++m) acc[j][m] = mfma_bf16(fa[slot][j], fb[slot][m], acc[j][m]);
-  };
-#pragma unroll
-  for (int q = 0; q < U; ++q) load(q, q);
-  int i = 0;
-  for (; i + U <= mine; i += U) {
-#pragma unroll
-    for (int q = 0; q < U; ++q) {
-      multiply(q);
-      load(q, i + U + q);
-    }
-  }
-#pragma unroll
-  for (int q = 0; q < U; ++q)
-    if (i + q < mine) multiply(q);
-}
-
 // ---------------------------------------------------------------------------
-// u = scale A x before the tiled product, as bf16 terms: a block has 16 MT tokens and first lists
-// the different adapters among them.  An adapter is pitch / 16 groups of 16 ranks; a pass over
-// k takes NS groups, of one adapter or of several, so that x is read once for a few
-// adapters.  The waves share out k, so the sums meet in LDS.  Bound by reading x.
+// u = scale A x before the tiled product, as bf16 terms.  A block has 32 tokens and first lists the
+// different adapters among them.  An adapter is pitch / 16 groups of 16 ranks; a pass over k takes
+// G groups, of one adapter or of several, so that x is read once for a few adapters.  x and
+// A go into LDS in runs of 256 bytes of every row, ST stages, pieces at piece ^ (row % 16); of a
+// stage's 128 k each of the four waves multiplies 32, and their sums meet in LDS.
+// Bound by reading x.
 // ---------------------------------------------------------------------------
-template <int MT, int NS, int WAVES>
-__global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(LoraArgs a) {
-  constexpr int kRows = 16 * MT, kRanks = 16 * NS;
-  __shared__ __attribute__((aligned(16))) float part[WAVES][kRows][kRanks];
-  __shared__ int list[kRows];
+template <int G, int ST>
+__global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs a) {
+  constexpr int kRows = 32, kRanks = 16 * G, kStage = (kRows + kRanks) * 256;
+  constexpr int kA = kRows * 256, L = kStage / 4096;             // 1 KB loads per wave
+  static_assert(kRanks % 16 == 0 && kStage % 4096 == 0 && 4 * kRows * kRanks * 4 <= ST * kStage, "LDS plan");
+  static_assert(ST * kStage <= 159 * 1024 && (ST - 2) * L < 64, "stages");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[ST * kStage];
+  __shared__ int list[kRows], ids[kRows];
   const int T = a.sh.T, d = a.sh.d, rank = a.sh.rank, pitch = (rank + 15) / 16 * 16, per = pitch / 16;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, fc = lane >> 4, t0 = blockIdx.x * kRows;
-  const int own = t0 + lane < T && lane < kRows ? a.adapter[t0 + lane] : -1;   // lane l: token t0 + l
+  const uint32_t lds0 = (uint32_t)(uintptr_t)lds, row_bytes = (uint32_t)d * 2u;
+  int own = t0 + lane < T && lane < kRows ? a.adapter[t0 + lane] : -1;   // lane l: token t0 + l
+  if ((uint32_t)own >= (uint32_t)a.sh.N) own = -1;
+  if (threadIdx.x < kRows) ids[lane] = own;
   int count = 0;
-  for (uint64_t left = __ballot((uint32_t)own < (uint32_t)a.sh.N); left; ++count) {
+  for (uint64_t left = __ballot(own >= 0); left; ++count) {
     const int id = __builtin_amdgcn_readlane(own, __ffsll((unsigned long long)left) - 1);
     left &= ~__ballot(own == id);
-    if (threadIdx.x == 0) list[count] = id;
+    list[count] = id;                                  // every wave the same
   }
   __syncthreads();
-  const uint16_t* px[MT];
+  const int groups = count * per, nk = d / 128;
+  // Load i of a wave: four rows, of x first, then of A.
+  auto row_of = [&](int i) { return (i * 4 + wave) * 4 + (lane >> 4); };
+  for (int g0 = 0; g0 < groups; g0 += G) {
+    const uint8_t* base[L];
+    uint32_t off[L];
 #pragma unroll
-  for (int m = 0; m < MT; ++m) px[m] = a.x + (size_t)min(t0 + m * 16 + fr, T - 1) * d + fc * 8;
-  const int groups = count * per;
-  for (int g0 = 0; g0 < groups; g0 += NS) {
-    const uint16_t* pa[NS];
-#pragma unroll
-    for (int j = 0; j < NS; ++j) {
-      const int g = min(g0 + j, groups - 1);
-      pa[j] = a.a + ((size_t)list[g / per] * rank + min(g % per * 16 + fr, rank - 1)) * d + fc * 8;
+    for (int i = 0; i < L; ++i) {
+      const int row = row_of(i), r = row - kRows;
+      const uint32_t piece = (uint32_t)((lane & 15) ^ (row & 15)) << 4;
+      if (i * 16 < kRows) {                            // 16 rows a load of all waves: of x or of A
+        base[i] = reinterpret_cast<const uint8_t*>(a.x);
+        off[i] = (uint32_t)min(t0 + row, T - 1) * row_bytes + piece;
+      } else {
+        const int g = min(g0 + (i * 16 - kRows) / 16, groups - 1);
+        const int id = __builtin_amdgcn_readfirstlane(list[g / per]);
+        base[i] = reinterpret_cast<const uint8_t*>(a.a) + (size_t)id * rank * row_bytes;
+        off[i] = (uint32_t)min(g % per * 16 + r % 16, rank - 1) * row_bytes + piece;
+      }
     }
-    f32x4 acc[NS][MT] = {};
-    dot_rows<NS, MT, (NS + MT >= 8 ? 2 : NS + MT >= 4 ? 4 : 8), WAVES>(pa, px, d / 32, wave, acc);
-    // A lane has ranks 4 fc .. + 3 of token fr.
+    auto load = [&](int step, int stage) {             // past the end: the last step, never read
+      const size_t k = (size_t)min(step, nk - 1) * 256;
 #pragma unroll
-    for (int j = 0; j < NS; ++j)
+      for (int i = 0; i < L; ++i) dma16(base[i] + k, off[i], lds0 + stage * kStage + (i * 4 + wave) * 1024);
+    };
 #pragma unroll
-      for (int m = 0; m < MT; ++m)
-        *reinterpret_cast<f32x4*>(&part[wave][m * 16 + fr][j * 16 + fc * 4]) = acc[j][m];
+    for (int s = 0; s < ST - 1; ++s) load(s, s);
+    f32x4 acc[G][2] = {};
+    int stage = 0;
+    for (int step = 0; step < nk; ++step) {
+      __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0((ST - 2) * L));
+      __syncthreads();                                 // the step has landed, the one before is read
+      load(step + ST - 1, stage == 0 ? ST - 1 : stage - 1);
+      const uint8_t* at = lds + stage * kStage + (((4 * wave + fc) ^ fr) << 4);
+      u32x4 xf[2], af[G];
+#pragma unroll
+      for (int m = 0; m < 2; ++m) xf[m] = ld16(at + (m * 16 + fr) * 256);
+#pragma unroll
+      for (int j = 0; j < G; ++j) af[j] = ld16(at + kA + (j * 16 + fr) * 256);
+#pragma unroll
+      for (int j = 0; j < G; ++j)
+#pragma unroll
+        for (int m = 0; m < 2; ++m) acc[j][m] = mfma_bf16(af[j], xf[m], acc[j][m]);
+      stage = stage == ST - 1 ? 0 : stage + 1;
+    }
+    __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(0));      // no load lands any more
     __syncthreads();
-    for (int o = threadIdx.x; o < kRows * kRanks / 2; o += WAVES * 64) {   // two ranks a thread
+    // The waves' sums by LDS: [wave][token][rank].  A lane has ranks 4 fc .. + 3 of token fr.
+    float* part = reinterpret_cast<float*>(lds);
+#pragma unroll
+    for (int j = 0; j < G; ++j)
+#pragma unroll
+      for (int m = 0; m < 2; ++m)
+        *reinterpret_cast<f32x4*>(part + ((wave * kRows + m * 16 + fr) * kRanks + j * 16 + fc * 4)) = acc[j][m];
+    __syncthreads();
+    for (int o = threadIdx.x; o < kRows * kRanks / 2; o += 256) {        // two ranks a thread
       const int row = o / (kRanks / 2), r = o % (kRanks / 2) * 2, g = g0 + r / 16, t = t0 + row;
       if (t >= T || g >= groups) continue;
       const int id = list[g / per], at_rank = g % per * 16 + r % 16;
-      if (a.adapter[t] != id) continue;
+      if (ids[row] != id) continue;
       float v[2] = {0.f, 0.f};
 #pragma unroll
-      for (int w = 0; w < WAVES; ++w) v[0] += part[w][row][r], v[1] += part[w][row][r + 1];
+      for (int w = 0; w < 4; ++w) {
+        v[0] += part[(w * kRows + row) * kRanks + r];
+        v[1] += part[(w * kRows + row) * kRanks + r + 1];
+      }
       const float scale = a.scale ? a.scale[id] : 1.f;
 #pragma unroll
       for (int q = 0; q < 2; ++q) v[q] = at_rank + q < rank ? v[q] * scale : 0.f;
@@ -116,15 +127,7 @@ __global__ __launch_bounds__(WAVES * 64) void lora_shrink_kernel(LoraArgs a) {
   }
 }
 
-// ---------------------------------------------------------------------------
-// One token: bound by the bytes of W.  A block has 16 NNT columns; its adapter's 16 RANKS ranks are
-// further rows beside them, so every block has u itself and one launch does all; A is read from
-// memory once and then from L2.  Eight waves share out k, fragments go straight from memory to
-// registers, the sums meet in LDS, where a thread finishes a column.
-// ---------------------------------------------------------------------------
-constexpr int kWaves = 8;
-
-// Eight ranks of B times eight values of u.
+// Eight values of a row times eight of another, added to s.
 __device__ __forceinline__ float dot8(const u32x4& q, const float* u, float s) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -133,62 +136,94 @@ __device__ __forceinline__ float dot8(const u32x4& q, const float* u, float s) {
   }
   return s;
 }
+__device__ __forceinline__ float dot8(const u32x4& q, const u32x4& x, float s) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) {
+    s = fmaf(__uint_as_float(q[i] << 16), __uint_as_float(x[i] << 16), s);
+    s = fmaf(__uint_as_float(q[i] & 0xffff0000u), __uint_as_float(x[i] & 0xffff0000u), s);
+  }
+  return s;
+}
 
-template <int NNT, int RANKS>
-__global__ __launch_bounds__(kWaves * 64) void lora_token_kernel(LoraArgs a) {
-  constexpr int kCols = 16 * NNT, NA = NNT + RANKS;
-  __shared__ __attribute__((aligned(16))) float part[kWaves][16 * NA];
-  __shared__ __attribute__((aligned(16))) float su[16 * RANKS];
+// ---------------------------------------------------------------------------
+// One token, bound by the bytes of W and by latency: every wave takes whole rows of W, in runs of
+// 1 KB, P runs at a time, one set ahead; x lies in LDS.  Every block works out u itself (an eighth of
+// the ranks a wave; A is read from memory once and then from L2), so one launch does all.
+// Lane l brings in rank l's share of B u before the lanes' sums meet.
+// ---------------------------------------------------------------------------
+constexpr int kTokenWaves = 8, kTokenMaxWidth = 32768;
+
+template <int P>
+__global__ __launch_bounds__(kTokenWaves * 64, 2) void lora_token_kernel(LoraArgs a) {
+  __shared__ __attribute__((aligned(16))) uint16_t sx[kTokenMaxWidth];
+  __shared__ float su[kLoraMaxRank];
   const int d = a.sh.d, n = a.sh.n, rank = a.sh.rank;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
-  const int fr = lane & 15, fc = lane >> 4, n0 = blockIdx.x * kCols;
-  const int given = a.adapter[0], id = (uint32_t)given < (uint32_t)a.sh.N ? given : -1;
-  const int any = max(id, 0);                          // without an adapter A and B are read, not used
-  const uint16_t *px[1] = {a.x + fc * 8}, *pw[NA];
+  const int first = blockIdx.x * kTokenWaves + wave, stride = gridDim.x * kTokenWaves;   // rows of W
+  const int segs = (d + P * 512 - 1) / (P * 512);
+  // Set s of a row: lane l has values 512 q + 8 l .. + 7 of its runs q; 0 past the row's end.
+  auto load = [&](const uint16_t* row, int s, u32x4 (&v)[P]) {
 #pragma unroll
-  for (int j = 0; j < NNT; ++j) pw[j] = a.w + (size_t)min(n0 + j * 16 + fr, n - 1) * d + fc * 8;
-#pragma unroll
-  for (int j = 0; j < RANKS; ++j) pw[NNT + j] = a.a + ((size_t)any * rank + min(j * 16 + fr, rank - 1)) * d + fc * 8;
-  // The thread's column (its first 16 ranks of B), scale and bias, under way with the rest.
-  const int c = min(n0 + (int)threadIdx.x, n - 1);
-  u32x4 qb[2] = {};
-  float bias = 0.f, scale = 1.f;
-  if (threadIdx.x < kCols) {
-    const uint16_t* b = a.b + ((size_t)any * n + c) * rank;
-    qb[0] = ld16(b);
-    if (rank > 8) qb[1] = ld16(b + 8);
-    if (a.bias) bias = bf16_to_f32(a.bias[c]);
-  }
-  if (a.scale) scale = a.scale[any];
-  f32x4 acc[NA][1] = {};
-  dot_rows<NA, 1, (NA >= 5 ? 4 : NA >= 3 ? 8 : 12), kWaves>(pw, px, d / 32, wave, acc);
-  // Every token of the tile is the same one: lane fr = 0 has columns 4 fc .. + 3.
-  if (fr == 0)
-#pragma unroll
-    for (int j = 0; j < NA; ++j) *reinterpret_cast<f32x4*>(&part[wave][j * 16 + fc * 4]) = acc[j][0];
-  __syncthreads();
-  auto sum = [&](int i) {
-    float v = 0.f;
-#pragma unroll
-    for (int w = 0; w < kWaves; ++w) v += part[w][i];
-    return v;
+    for (int q = 0; q < P; ++q) {
+      const int k = (s * P + q) * 512 + lane * 8;
+      v[q] = ld16(row + min(k, d - 8));
+      v[q] = k < d ? v[q] : u32x4{0, 0, 0, 0};
+    }
   };
-  // The last wave sums u, the first columns' threads what they wait for anyway.
-  if ((int)threadIdx.x >= kWaves * 64 - 16 * RANKS) {
-    const int r = threadIdx.x - (kWaves * 64 - 16 * RANKS);
-    su[r] = r < rank ? sum(kCols + r) * scale : 0.f;
-  }
-  float v = threadIdx.x < kCols ? sum(threadIdx.x) + bias : 0.f;
+  auto dot = [&](const u32x4 (&v)[P], int s, float sum) {
+#pragma unroll
+    for (int q = 0; q < P; ++q) sum = dot8(v[q], ld16(sx + min((s * P + q) * 512 + lane * 8, d - 8)), sum);
+    return sum;
+  };
+  u32x4 cur[P];
+  load(a.w + (size_t)min(first, n - 1) * d, 0, cur);
+  for (int i = threadIdx.x * 8; i < d; i += kTokenWaves * 64 * 8) st16(sx + i, ld16(a.x + i));
+  const int given = a.adapter[0], id = (uint32_t)given < (uint32_t)a.sh.N ? given : -1;
+  const float scale = a.scale && id >= 0 ? a.scale[id] : 1.f;
   __syncthreads();
-  if (threadIdx.x >= kCols || n0 + (int)threadIdx.x >= n) return;
   if (id >= 0) {
-    float s = dot8(qb[0], su, 0.f);
-    if (rank > 8) s = dot8(qb[1], su + 8, s);
-    for (int r = 16; r < rank; r += 8) s = dot8(ld16(a.b + ((size_t)id * n + c) * rank + r), su + r, s);
-    v += s;
+    const uint16_t* rows = a.a + (size_t)id * rank * d;
+    for (int r = wave; r < rank; r += 2 * kTokenWaves) {
+      const int r2 = min(r + kTokenWaves, rank - 1);
+      float s0 = 0.f, s1 = 0.f;
+      for (int s = 0; s < segs; ++s) {
+        u32x4 v0[P], v1[P];
+        load(rows + (size_t)r * d, s, v0);
+        load(rows + (size_t)r2 * d, s, v1);
+        s0 = dot(v0, s, s0);
+        s1 = dot(v1, s, s1);
+      }
+      s0 = wave_sum_f(s0) * scale;
+      s1 = wave_sum_f(s1) * scale;
+      if (lane == 0) {
+        su[r] = s0;
+        if (r + kTokenWaves < rank) su[r2] = s1;
+      }
+    }
   }
-  if (a.sh.f32_out) static_cast<float*>(a.y)[c] = a.sh.gelu ? gelu_erf(v) : v;
-  else static_cast<uint16_t*>(a.y)[c] = (uint16_t)pack_bf16x2(a.sh.gelu ? gelu_for_bf16(v) : v, 0.f);
+  __syncthreads();
+  for (int row = first; row < n; row += stride) {
+    float sum = 0.f;
+    const uint16_t* b = a.b + ((size_t)max(id, 0) * n + row) * rank;
+    const bool mine = id >= 0 && lane < rank, more = id >= 0 && lane + 64 < rank;
+    const float b0 = mine ? bf16_to_f32(b[lane]) : 0.f, b1 = more ? bf16_to_f32(b[lane + 64]) : 0.f;
+    const float bias = a.bias ? bf16_to_f32(a.bias[row]) : 0.f;
+    for (int s = 0; s < segs; ++s) {
+      u32x4 next[P];
+      const bool last = s + 1 == segs;
+      load(a.w + (size_t)min(last ? row + stride : row, n - 1) * d, last ? 0 : s + 1, next);
+      sum = dot(cur, s, sum);
+#pragma unroll
+      for (int q = 0; q < P; ++q) cur[q] = next[q];
+    }
+    if (mine) sum = fmaf(b0, su[lane], sum);
+    if (more) sum = fmaf(b1, su[lane + 64], sum);
+    sum = wave_sum_f(sum) + bias;
+    if (lane == 0) {
+      if (a.sh.f32_out) static_cast<float*>(a.y)[row] = a.sh.gelu ? gelu_erf(sum) : sum;
+      else static_cast<uint16_t*>(a.y)[row] = (uint16_t)pack_bf16x2(a.sh.gelu ? gelu_for_bf16(sum) : sum, 0.f);
+    }
+  }
 }
 
 // ---------------------------------------------------------------------------
@@ -403,7 +438,7 @@ __global__ __launch_bounds__(256) void lora_finish_kernel(PartArgs p) {
 enum LoraPath { kToken, kPart, kTile };
 
 static LoraPath path_of(const LoraShape& s) {
-  if (s.T == 1 && s.rank <= 32) return kToken;
+  if (s.T == 1 && s.rank <= 32 && s.d <= kTokenMaxWidth) return kToken;
   // Tiles need four steps of 64 k: their loads run two ahead, into the next tile only.
   return s.T > 512 && s.d >= 256 ? kTile : kPart;
 }
@@ -425,9 +460,16 @@ size_t lora_u_bytes(const LoraShape& s) {
   }
 }
 
-template <int MT>
-static void run_shrink(const LoraArgs& a, hipStream_t s) {
-  lora_shrink_kernel<MT, 4, kWaves><<<(a.sh.T + 16 * MT - 1) / (16 * MT), kWaves * 64, 0, s>>>(a);
+// Deep stages while a CU has one block at most, two blocks a CU beyond.
+static void launch_shrink(const LoraArgs& a, hipStream_t s) {
+  const int tiles = (a.sh.T + 31) / 32;
+  if (a.sh.rank <= 32) {
+    if (tiles <= 256) lora_shrink_kernel<2, 9><<<tiles, 256, 0, s>>>(a);
+    else lora_shrink_kernel<2, 4><<<tiles, 256, 0, s>>>(a);
+  } else {
+    if (tiles <= 256) lora_shrink_kernel<4, 6><<<tiles, 256, 0, s>>>(a);
+    else lora_shrink_kernel<4, 3><<<tiles, 256, 0, s>>>(a);
+  }
 }
 
 static hipError_t launch_part(const LoraArgs& a, hipStream_t s) {
@@ -446,24 +488,20 @@ static hipError_t launch_part(const LoraArgs& a, hipStream_t s) {
   return hipGetLastError();
 }
 
-template <int RANKS>
 static void launch_token(const LoraArgs& a, hipStream_t s) {
-  const int n = a.sh.n;
-  if (n >= 12288) lora_token_kernel<4, RANKS><<<(n + 63) / 64, kWaves * 64, 0, s>>>(a);
-  else if (n >= 8192) lora_token_kernel<2, RANKS><<<(n + 31) / 32, kWaves * 64, 0, s>>>(a);
-  else lora_token_kernel<1, RANKS><<<(n + 15) / 16, kWaves * 64, 0, s>>>(a);
+  const int blocks = std::min(256, (a.sh.n + kTokenWaves - 1) / kTokenWaves);
+  if (a.sh.d <= 1024) lora_token_kernel<2><<<blocks, kTokenWaves * 64, 0, s>>>(a);
+  else if (a.sh.d <= 2048) lora_token_kernel<4><<<blocks, kTokenWaves * 64, 0, s>>>(a);
+  else lora_token_kernel<8><<<blocks, kTokenWaves * 64, 0, s>>>(a);
 }
 
 hipError_t launch_lora(const LoraArgs& a, hipStream_t s) {
   switch (path_of(a.sh)) {
     case kToken:
-      if (a.sh.rank <= 16) launch_token<1>(a, s);
-      else launch_token<2>(a, s);
+      launch_token(a, s);
       return hipGetLastError();
     case kTile:
-      if (a.sh.T > 16384) run_shrink<4>(a, s);
-      else if (a.sh.T > 4096) run_shrink<2>(a, s);
-      else run_shrink<1>(a, s);
+      launch_shrink(a, s);
       if (hipError_t e = hipGetLastError()) return e;
       return launch_lora_tile(a, s);
     default:

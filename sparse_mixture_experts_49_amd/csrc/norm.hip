@@ -188,6 +188,41 @@ __global__ __launch_bounds__(block_of(G)) void norm_kernel(NormArgs a) {
   }
 }
 
+// A row's values as they lie in memory, so that the next row can be under way in few registers.
+template <typename T, int G, int NV, bool VEC>
+struct RawRow {
+  using C = Columns<G, NV, VEC>;
+  static constexpr int kWords = VEC ? sizeof(T) / 2 : 1;
+  u32x4 v[NV][kWords];                               // VEC: 8 values
+  float s[VEC ? 1 : NV][8];
+  __device__ __forceinline__ void load(const T* row, int t, int d) {
+#pragma unroll
+    for (int i = 0; i < NV; ++i) {
+      if constexpr (VEC) {
+#pragma unroll
+        for (int w = 0; w < kWords; ++w)
+          v[i][w] = ld16(row + min(C::at(t, i, 0), d - 8) + w * (16 / sizeof(T)));
+      } else {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) s[i][j] = load1(row + min(C::at(t, i, j), d - 1));
+      }
+    }
+  }
+  // Columns at and past d are 0.
+  __device__ __forceinline__ void get(int t, int d, float (&x)[NV][8]) const {
+#pragma unroll
+    for (int i = 0; i < NV; ++i)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+        float f;
+        if constexpr (!VEC) f = s[i][j];
+        else if constexpr (sizeof(T) == 4) f = __uint_as_float(v[i][j / 4][j % 4]);
+        else f = __uint_as_float(j % 2 ? v[i][0][j / 2] & 0xffff0000u : v[i][0][j / 2] << 16);
+        x[i][j] = C::at(t, i, VEC ? 0 : j) < d ? f : 0.f;
+      }
+  }
+};
+
 template <typename T, int G, int NV, bool VEC>
 __global__ __launch_bounds__(block_of(G)) void norm_grad_kernel(NormGradArgs a) {
   using C = Columns<G, NV, VEC>;
@@ -195,15 +230,38 @@ __global__ __launch_bounds__(block_of(G)) void norm_grad_kernel(NormGradArgs a) 
   __shared__ float red[2][2][G / 64];
   GroupSum<G, 2> sum{red};
   const int t = threadIdx.x % G, d = a.sh.d;
-  const int64_t group = (int64_t)blockIdx.x * kGroups + threadIdx.x / G;
+  const int64_t group = (int64_t)blockIdx.x * kGroups + threadIdx.x / G, step = (int64_t)gridDim.x * kGroups;
   const float inv = 1.f / d;
   float w[NV][8], dw[NV][8] = {}, db[NV][8] = {};
   C::load_param(a.weight, a.sh.w_bf16, 1.f, t, d, w);
-  for (int64_t row = group; row < a.sh.rows; row += (int64_t)gridDim.x * kGroups) {
-    float x[NV][8], g[NV][8];
-    C::load(static_cast<const T*>(a.dy.p) + row * a.dy.stride, t, d, g);
-    C::load(static_cast<const T*>(a.x.p) + row * a.x.stride, t, d, x);
-    const float mean = a.mean[row], rstd = a.rstd[row];
+  RawRow<T, G, NV, VEC> nx, ng, nr;
+  float next_mean, next_rstd;
+  const bool through = a.d_x_out.p;
+  auto fetch = [&](int64_t row) {                    // past the end: the last row again, not used
+    row = row < a.sh.rows ? row : a.sh.rows - 1;
+    ng.load(static_cast<const T*>(a.dy.p) + row * a.dy.stride, t, d);
+    nx.load(static_cast<const T*>(a.x.p) + row * a.x.stride, t, d);
+    if (through) nr.load(static_cast<const T*>(a.d_x_out.p) + row * a.d_x_out.stride, t, d);
+    next_mean = a.mean[row];
+    next_rstd = a.rstd[row];
+  };
+  constexpr bool kAhead = VEC && G <= 512;           // else the next row's registers would spill
+  if (kAhead) fetch(group);
+  for (int64_t row = group; row < a.sh.rows; row += step) {
+    if (!kAhead) fetch(row);
+    float x[NV][8], g[NV][8], r[NV][8];
+    ng.get(t, d, g);
+    nx.get(t, d, x);
+    if (through) {
+      nr.get(t, d, r);
+    } else {
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) r[v][j] = 0.f;
+    }
+    const float mean = next_mean, rstd = next_rstd;
+    if (kAhead) fetch(row + step);
     float s[2] = {0.f, 0.f};
 #pragma unroll
     for (int v = 0; v < NV; ++v)
@@ -218,15 +276,6 @@ __global__ __launch_bounds__(block_of(G)) void norm_grad_kernel(NormGradArgs a) 
         s[1] = fmaf(g[v][j], x[v][j], s[1]);
       }
     if (a.d_x.p) {
-      float r[NV][8];
-      if (a.d_x_out.p) {
-        C::load(static_cast<const T*>(a.d_x_out.p) + row * a.d_x_out.stride, t, d, r);
-      } else {
-#pragma unroll
-        for (int v = 0; v < NV; ++v)
-#pragma unroll
-          for (int j = 0; j < 8; ++j) r[v][j] = 0.f;
-      }
       sum(s);
       s[0] *= inv;
       s[1] *= inv;
