@@ -70,31 +70,35 @@ __device__ __forceinline__ f32x4 load_logits(const float* __restrict__ row, int 
   }
 }
 
-// Shares q of a token from its logits, and for sigmoid scores 1 - s.
-template <int L, bool SIGMOID>
-__device__ __forceinline__ void shares(const f32x4& l, f32x4& q, f32x4& rest) {
+// e^x as a power of two: the product's rounding costs |x| half steps, of which scores that weigh
+// anything have few.  (exp_f32 puts them back; the kernels here are near the instruction rate's bound.)
+__device__ __forceinline__ float exp_near(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
+__device__ __forceinline__ float inverse(float x) { return __builtin_amdgcn_rcpf(x); }   // 1 ulp
+
+// Scores e of a token from its logits and the inverse of their sum, of which q = e inv are the
+// shares; REST: for sigmoid scores also 1 - s.
+template <int L, bool SIGMOID, bool REST>
+__device__ __forceinline__ float scores(const f32x4& l, f32x4& e, f32x4& rest) {
   if constexpr (SIGMOID) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      float s, r;
-      sigmoid_pair(l[j], s, r);
-      q[j] = s;
-      rest[j] = r;
+      if constexpr (REST) {
+        const float t = exp_near(-fabsf(l[j])), big = inverse(1.f + t), small = t * big;
+        e[j] = l[j] < 0.f ? small : big;
+        rest[j] = l[j] < 0.f ? big : small;
+      } else {
+        e[j] = inverse(1.f + exp_near(-l[j]));
+      }
     }
-    const float sum = sum_of<L>((q[0] + q[1]) + (q[2] + q[3]));
-    const float inv = 1.f / (sum < kLeastSum ? kLeastSum : sum);
-#pragma unroll
-    for (int j = 0; j < 4; ++j) q[j] *= inv;
   } else {
     float m = max_of<L>(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])));
     m = m == -INFINITY ? 0.f : m;                    // every expert masked: no shares
 #pragma unroll
-    for (int j = 0; j < 4; ++j) q[j] = exp_f32(l[j] - m);
-    const float sum = sum_of<L>((q[0] + q[1]) + (q[2] + q[3]));
-    const float inv = sum > 0.f ? 1.f / sum : sum != sum ? sum : 0.f;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) q[j] *= inv;
+    for (int j = 0; j < 4; ++j) e[j] = exp_near(l[j] - m);
   }
+  const float sum = sum_of<L>((e[0] + e[1]) + (e[2] + e[3]));
+  if constexpr (SIGMOID) return inverse(sum < kLeastSum ? kLeastSum : sum);
+  return sum > 0.f ? inverse(sum) : sum != sum ? sum : 0.f;
 }
 
 // The borders of the sequences, brought into [0, T] and order, so that no content of
@@ -117,70 +121,128 @@ __device__ __forceinline__ int sequence_of(const int32_t* __restrict__ offsets, 
   return lo;
 }
 
+// What a block of four waves holds of a piece: the waves' sums of shares, choices, tokens.
+template <int L>
+struct PieceSums {
+  float q[4][4 * L];
+  int hist[kBalanceMaxExperts];
+  int count;
+  __device__ __forceinline__ void clear(int E) {
+    for (int i = threadIdx.x; i < E; i += 256) hist[i] = 0;
+    if (threadIdx.x == 0) count = 0;
+  }
+  __device__ __forceinline__ float share(int e) const { return (q[0][e] + q[1][e]) + (q[2][e] + q[3][e]); }
+};
+
+// The sums of tokens [lo, hi) into s, cleared before; complete after a barrier.
 template <int L, bool SIGMOID, bool VEC>
-__global__ __launch_bounds__(256) void balance_part_kernel(BalanceArgs a, int chunk) {
+__device__ __forceinline__ void sum_piece(const BalanceArgs& a, int lo, int hi, PieceSums<L>& s) {
   constexpr int kTok = 64 / L, kAhead = 4;           // tokens of a wave at once; such steps under way
-  __shared__ float sum_q[4][4 * L];
-  __shared__ int hist[kBalanceMaxExperts];
-  __shared__ int count;
-  const int T = a.sh.T, E = a.sh.E, S = a.sh.S, k = a.sh.k;
+  const int E = a.sh.E, k = a.sh.k;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int e = (lane % L) * 4, slot = wave * kTok + lane / L;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  for (int t = lo + slot; t < hi + slot; t += kAhead * 4 * kTok) {      // the same trips for all lanes of a wave
+    f32x4 l[kAhead];
+    bool in[kAhead];
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      const int at = t + i * 4 * kTok;
+      l[i] = load_logits<VEC>(a.logits + (size_t)min(at, hi - 1) * E, e, E);
+      in[i] = at < hi && (!a.mask || a.mask[at]);
+    }
+#pragma unroll
+    for (int i = 0; i < kAhead; ++i) {
+      if (!__ballot(in[i])) continue;
+      f32x4 q, rest;
+      const float inv = scores<L, SIGMOID, false>(l[i], q, rest);
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] += in[i] ? q[j] * inv : 0.f;
+    }
+  }
+  int n = 0;
+  for (int i = threadIdx.x; i < (hi - lo) * k; i += 256) {
+    const int t = lo + i / k, id = a.topk_idx[(size_t)lo * k + i];
+    const bool in = !a.mask || a.mask[t];
+    if (in && (uint32_t)id < (uint32_t)E) atomicAdd(&s.hist[id], 1);   // counts: order-independent
+    n += in && i % k == 0;
+  }
+  if (n) atomicAdd(&s.count, n);
+#pragma unroll
+  for (int o = L; o < 64; o <<= 1)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) acc[j] += __shfl_xor(acc[j], o);
+  if (lane < L)
+#pragma unroll
+    for (int j = 0; j < 4; ++j) s.q[wave][e + j] = acc[j];
+}
+
+template <int L, bool SIGMOID, bool VEC>
+__global__ __launch_bounds__(256) void balance_part_kernel(BalanceArgs a, int chunk) {
+  __shared__ PieceSums<L> s;
+  const int T = a.sh.T, E = a.sh.E, S = a.sh.S;
   const int t0 = blockIdx.x * chunk, t1 = min(t0 + chunk, T);
   if (a.total_load && blockIdx.x == 0)
     for (int i = threadIdx.x; i < E; i += 256) a.total_load[i] = 0;
-  for (int i = threadIdx.x; i < E; i += 256) hist[i] = 0;
-  if (threadIdx.x == 0) count = 0;
+  s.clear(E);
   __syncthreads();
   for (int b = sequence_of(a.offsets, S, T, t0); b < S; ++b) {
     const int lo = max(border(a.offsets, b, T), t0), hi = min(border(a.offsets, b + 1, T), t1);
     if (lo >= t1) break;
     if (hi <= lo) continue;
-    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
-    for (int t = lo + slot; t < hi + slot; t += kAhead * 4 * kTok) {      // the same trips for all lanes of a wave
-      f32x4 l[kAhead];
-      bool in[kAhead];
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        const int at = t + i * 4 * kTok;
-        l[i] = load_logits<VEC>(a.logits + (size_t)min(at, hi - 1) * E, e, E);
-        in[i] = at < hi && (!a.mask || a.mask[at]);
-      }
-#pragma unroll
-      for (int i = 0; i < kAhead; ++i) {
-        f32x4 q, rest;
-        shares<L, SIGMOID>(l[i], q, rest);
-#pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] += in[i] ? q[j] : 0.f;
-      }
-    }
-    int n = 0;
-    for (int i = threadIdx.x; i < (hi - lo) * k; i += 256) {
-      const int t = lo + i / k, id = a.topk_idx[(size_t)lo * k + i];
-      const bool in = !a.mask || a.mask[t];
-      if (in && (uint32_t)id < (uint32_t)E) atomicAdd(&hist[id], 1);   // counts: order-independent
-      n += in && i % k == 0;
-    }
-    if (n) atomicAdd(&count, n);
-#pragma unroll
-    for (int o = L; o < 64; o <<= 1)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) acc[j] += __shfl_xor(acc[j], o);
-    if (lane < L)
-#pragma unroll
-      for (int j = 0; j < 4; ++j) sum_q[wave][e + j] = acc[j];
+    sum_piece<L, SIGMOID, VEC>(a, lo, hi, s);
     __syncthreads();
     const size_t at = (size_t)blockIdx.x + b;
     for (int i = threadIdx.x; i < E; i += 256) {
-      a.pq[at * E + i] = (sum_q[0][i] + sum_q[1][i]) + (sum_q[2][i] + sum_q[3][i]);
-      a.pload[at * E + i] = hist[i];
-      hist[i] = 0;
+      a.pq[at * E + i] = s.share(i);
+      a.pload[at * E + i] = s.hist[i];
     }
-    if (threadIdx.x == 0) {
-      a.pvalid[at] = count;
-      count = 0;
-    }
+    if (threadIdx.x == 0) a.pvalid[at] = s.count;
     __syncthreads();
+    s.clear(E);
+    __syncthreads();
+  }
+}
+
+// A small batch in one launch: one block takes the sequences in turn, thread e expert e.
+template <int L, bool SIGMOID, bool VEC>
+__global__ __launch_bounds__(256) void balance_single_kernel(BalanceArgs a) {
+  __shared__ PieceSums<L> s;
+  __shared__ double part[4];
+  const int T = a.sh.T, E = a.sh.E, S = a.sh.S, e = threadIdx.x;
+  const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  double total = 0.0;
+  int live = 0, all = 0;
+  for (int b = 0; b < S; ++b) {
+    const int lo = border(a.offsets, b, T), hi = border(a.offsets, b + 1, T);
+    s.clear(E);
+    __syncthreads();
+    if (hi > lo) sum_piece<L, SIGMOID, VEC>(a, lo, hi, s);
+    __syncthreads();
+    const int n = s.count, load = e < E ? s.hist[e] : 0;
+    const double mean = n && e < E ? (double)s.share(e) / n : 0.0;
+    double loss = n ? (double)E * load / ((double)a.sh.k * n) * mean : 0.0;
+    if (e < E) {
+      a.load[(size_t)b * E + e] = load;
+      if (a.prob_mean) a.prob_mean[(size_t)b * E + e] = (float)mean;
+    }
+#pragma unroll
+    for (int o = 32; o > 0; o >>= 1) loss += __shfl_xor(loss, o);
+    if (lane == 0) part[wave] = loss;
+    __syncthreads();
+    loss = (part[0] + part[1]) + (part[2] + part[3]);
+    if (e == 0) {
+      a.valid[b] = n;
+      if (a.seq_loss) a.seq_loss[b] = (float)loss;
+    }
+    total += loss;
+    live += n > 0;
+    all += load;
+  }
+  if (a.total_load && e < E) a.total_load[e] = all;
+  if (e == 0) {
+    a.valid[S] = live;
+    if (a.loss) *a.loss = live ? (float)(total / live) : 0.f;
   }
 }
 
@@ -295,17 +357,28 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(BalanceGradArgs a, in
       const bool in = !a.mask || a.mask[row];
       const f32x4 l = load_logits<VEC>(a.logits + (size_t)row * E, e, E);
       f32x4 q, rest, d;
-      shares<L, SIGMOID>(l, q, rest);
+      const float inv = scores<L, SIGMOID, SIGMOID>(l, q, rest);
       float lead = 0.f, dot = 0.f;
+      bool leads = false;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) lead += q[j] > 0.5f ? c[j] : 0.f;
-      lead = sum_of<L>(lead);
+      for (int j = 0; j < 4; ++j) {
+        q[j] *= inv;
+        leads |= q[j] > 0.5f;
+      }
+      if (__ballot(leads)) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j) dot = fmaf(c[j] - lead, q[j], dot);
+        for (int j = 0; j < 4; ++j) lead += q[j] > 0.5f ? c[j] : 0.f;
+        lead = sum_of<L>(lead);
+      }
+#pragma unroll
+      for (int j = 0; j < 4; ++j) {
+        d[j] = c[j] - lead;
+        dot = fmaf(d[j], q[j], dot);
+      }
       dot = sum_of<L>(dot);
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        d[j] = q[j] * (c[j] - lead - dot);
+        d[j] = q[j] * (d[j] - dot);
         if (SIGMOID) d[j] *= rest[j];
         d[j] = in ? d[j] : 0.f;
       }
@@ -332,7 +405,16 @@ static void for_kind(bool sigmoid, int E, F f) {
   });
 }
 
+// Few values and few sequences (each costs its barriers): one block and one launch.
+static bool single(const BalanceShape& s) { return s.S <= 8 && (long)s.T * s.E <= 32 * 1024; }
+
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
+  if (single(a.sh)) {
+    for_kind(a.sh.sigmoid, a.sh.E, [&](auto l, auto sig, auto vec) {
+      balance_single_kernel<decltype(l)::value, decltype(sig)::value, decltype(vec)::value><<<1, 256, 0, s>>>(a);
+    });
+    return hipGetLastError();
+  }
   const int chunk = chunk_of(a.sh.T), parts = balance_blocks(a.sh.E);
   for_kind(a.sh.sigmoid, a.sh.E, [&](auto l, auto sig, auto vec) {
     balance_part_kernel<decltype(l)::value, decltype(sig)::value, decltype(vec)::value>

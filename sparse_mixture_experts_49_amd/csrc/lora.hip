@@ -146,84 +146,84 @@ __device__ __forceinline__ float dot8(const u32x4& q, const u32x4& x, float s) {
 }
 
 // ---------------------------------------------------------------------------
-// One token, bound by the bytes of W and by latency: every wave takes whole rows of W, in runs of
-// 1 KB, P runs at a time, one set ahead; x lies in LDS.  Every block works out u itself (an eighth of
-// the ranks a wave; A is read from memory once and then from L2), so one launch does all.
+// One token, bound by the bytes of W and by latency.  Every block works out u itself (A is read from
+// memory once and then from L2), so one launch does all.  A wave takes whole rows, first its
+// eighth of A's, then of W, in runs of 1 KB, P runs a set, three sets under way; x lies in LDS.
 // Lane l brings in rank l's share of B u before the lanes' sums meet.
 // ---------------------------------------------------------------------------
-constexpr int kTokenWaves = 8, kTokenMaxWidth = 32768;
+constexpr int kTokenWaves = 8, kTokenMaxWidth = 32768, kTokenMaxRank = 64;
 
 template <int P>
 __global__ __launch_bounds__(kTokenWaves * 64, 2) void lora_token_kernel(LoraArgs a) {
+  constexpr int kSets = 3;
   __shared__ __attribute__((aligned(16))) uint16_t sx[kTokenMaxWidth];
-  __shared__ float su[kLoraMaxRank];
+  __shared__ float su[kTokenMaxRank];
   const int d = a.sh.d, n = a.sh.n, rank = a.sh.rank;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int first = blockIdx.x * kTokenWaves + wave, stride = gridDim.x * kTokenWaves;   // rows of W
   const int segs = (d + P * 512 - 1) / (P * 512);
-  // Set s of a row: lane l has values 512 q + 8 l .. + 7 of its runs q; 0 past the row's end.
-  auto load = [&](const uint16_t* row, int s, u32x4 (&v)[P]) {
+  const int given = a.adapter[0], id = (uint32_t)given < (uint32_t)a.sh.N ? given : -1;
+  const int of_a = id >= 0 ? rank / kTokenWaves * segs : 0;             // sets of A's rows (rank is a multiple of 8)
+  const int total = of_a + (first < n ? ((n - 1 - first) / stride + 1) * segs : 0);
+  const uint16_t* rows_a = a.a + (size_t)max(id, 0) * rank * d + (size_t)wave * d;
+  const float scale = a.scale && id >= 0 ? a.scale[id] : 1.f;
+  const int lane_rank = min(lane, rank - 1);
+  u32x4 v[kSets][P];
+  uint16_t vb[kSets], vbias[kSets];                    // the row's B of the lane's rank, its bias
+  // Set i: lane l has values 512 q + 8 l .. + 7 of its runs q; 0 past the row's end.  Past the last
+  // set that one again, not used.
+  auto load = [&](int slot, int i) {
+    i = max(min(i, total - 1), 0);
+    const bool w = i >= of_a;
+    const int j = w ? i - of_a : i, s = j % segs, row = min(first + j / segs * stride, n - 1);
+    const uint16_t* p = w ? a.w + (size_t)row * d : rows_a + (size_t)(j / segs) * kTokenWaves * d;
 #pragma unroll
     for (int q = 0; q < P; ++q) {
       const int k = (s * P + q) * 512 + lane * 8;
-      v[q] = ld16(row + min(k, d - 8));
-      v[q] = k < d ? v[q] : u32x4{0, 0, 0, 0};
+      v[slot][q] = ld16(p + min(k, d - 8));
     }
+    const size_t at = (size_t)max(id, 0) * n + (w ? row : 0);
+    vb[slot] = a.b[at * rank + lane_rank];
+    vbias[slot] = a.bias ? a.bias[w ? row : 0] : (uint16_t)0;
   };
-  auto dot = [&](const u32x4 (&v)[P], int s, float sum) {
 #pragma unroll
-    for (int q = 0; q < P; ++q) sum = dot8(v[q], ld16(sx + min((s * P + q) * 512 + lane * 8, d - 8)), sum);
-    return sum;
-  };
-  u32x4 cur[P];
-  load(a.w + (size_t)min(first, n - 1) * d, 0, cur);
+  for (int q = 0; q < kSets; ++q) load(q, q);
   for (int i = threadIdx.x * 8; i < d; i += kTokenWaves * 64 * 8) st16(sx + i, ld16(a.x + i));
-  const int given = a.adapter[0], id = (uint32_t)given < (uint32_t)a.sh.N ? given : -1;
-  const float scale = a.scale && id >= 0 ? a.scale[id] : 1.f;
   __syncthreads();
-  if (id >= 0) {
-    const uint16_t* rows = a.a + (size_t)id * rank * d;
-    for (int r = wave; r < rank; r += 2 * kTokenWaves) {
-      const int r2 = min(r + kTokenWaves, rank - 1);
-      float s0 = 0.f, s1 = 0.f;
-      for (int s = 0; s < segs; ++s) {
-        u32x4 v0[P], v1[P];
-        load(rows + (size_t)r * d, s, v0);
-        load(rows + (size_t)r2 * d, s, v1);
-        s0 = dot(v0, s, s0);
-        s1 = dot(v1, s, s1);
-      }
-      s0 = wave_sum_f(s0) * scale;
-      s1 = wave_sum_f(s1) * scale;
-      if (lane == 0) {
-        su[r] = s0;
-        if (r + kTokenWaves < rank) su[r2] = s1;
-      }
-    }
-  }
-  __syncthreads();
-  for (int row = first; row < n; row += stride) {
-    float sum = 0.f;
-    const uint16_t* b = a.b + ((size_t)max(id, 0) * n + row) * rank;
-    const bool mine = id >= 0 && lane < rank, more = id >= 0 && lane + 64 < rank;
-    const float b0 = mine ? bf16_to_f32(b[lane]) : 0.f, b1 = more ? bf16_to_f32(b[lane + 64]) : 0.f;
-    const float bias = a.bias ? bf16_to_f32(a.bias[row]) : 0.f;
-    for (int s = 0; s < segs; ++s) {
-      u32x4 next[P];
-      const bool last = s + 1 == segs;
-      load(a.w + (size_t)min(last ? row + stride : row, n - 1) * d, last ? 0 : s + 1, next);
-      sum = dot(cur, s, sum);
+  float sum = 0.f;
+  auto use = [&](int slot, int i) {
+    if (i == of_a) __syncthreads();                    // every wave's u is there
+    const bool w = i >= of_a;
+    const int j = w ? i - of_a : i, s = j % segs;
 #pragma unroll
-      for (int q = 0; q < P; ++q) cur[q] = next[q];
+    for (int q = 0; q < P; ++q) {
+      const int k = (s * P + q) * 512 + lane * 8;
+      const u32x4 x = v[slot][q];
+      if (k < d) sum = dot8(x, ld16(sx + k), sum);
     }
-    if (mine) sum = fmaf(b0, su[lane], sum);
-    if (more) sum = fmaf(b1, su[lane + 64], sum);
-    sum = wave_sum_f(sum) + bias;
-    if (lane == 0) {
-      if (a.sh.f32_out) static_cast<float*>(a.y)[row] = a.sh.gelu ? gelu_erf(sum) : sum;
-      else static_cast<uint16_t*>(a.y)[row] = (uint16_t)pack_bf16x2(a.sh.gelu ? gelu_for_bf16(sum) : sum, 0.f);
+    if (s + 1 < segs) return;
+    if (!w) {
+      sum = wave_sum_f(sum) * scale;
+      if (lane == 0) su[j / segs * kTokenWaves + wave] = sum;
+    } else {
+      if (id >= 0 && lane < rank) sum = fmaf(bf16_to_f32(vb[slot]), su[lane], sum);
+      sum = wave_sum_f(sum) + bf16_to_f32(vbias[slot]);
+      const int row = first + j / segs * stride;
+      if (lane == 0) {
+        if (a.sh.f32_out) static_cast<float*>(a.y)[row] = a.sh.gelu ? gelu_erf(sum) : sum;
+        else static_cast<uint16_t*>(a.y)[row] = (uint16_t)pack_bf16x2(a.sh.gelu ? gelu_for_bf16(sum) : sum, 0.f);
+      }
+    }
+    sum = 0.f;
+  };
+  for (int i = 0; i < total; i += kSets) {
+#pragma unroll
+    for (int q = 0; q < kSets; ++q) {
+      if (i + q < total) use(q, i + q);
+      load(q, i + q + kSets);
     }
   }
+  if (total == of_a) __syncthreads();                  // no row of W: the barrier all the same
 }
 
 // ---------------------------------------------------------------------------
@@ -438,7 +438,7 @@ __global__ __launch_bounds__(256) void lora_finish_kernel(PartArgs p) {
 enum LoraPath { kToken, kPart, kTile };
 
 static LoraPath path_of(const LoraShape& s) {
-  if (s.T == 1 && s.rank <= 32 && s.d <= kTokenMaxWidth) return kToken;
+  if (s.T == 1 && s.rank <= kTokenMaxRank && s.d <= kTokenMaxWidth) return kToken;
   // Tiles need four steps of 64 k: their loads run two ahead, into the next tile only.
   return s.T > 512 && s.d >= 256 ? kTile : kPart;
 }
