@@ -43,8 +43,14 @@ __device__ __forceinline__ float across(float v, F f) {
   if constexpr (L >= 4) v = f(v, dpp<0x4E>(v));      // quad [2,3,0,1]
   if constexpr (L >= 8) v = f(v, dpp<0x141>(v));     // half-row mirror
   if constexpr (L >= 16) v = f(v, dpp<0x140>(v));    // row mirror
-  if constexpr (L >= 32) v = f(v, __shfl_xor(v, 16));
-  if constexpr (L >= 64) v = f(v, __shfl_xor(v, 32));
+  if constexpr (L >= 32) {                           // neighbouring rows of 16, then halves
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  if constexpr (L >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
   return v;
 }
 template <int L>
@@ -56,19 +62,33 @@ __device__ __forceinline__ float max_of(float v) {
   return across<L>(v, [](float a, float b) { return fmaxf(a, b); });
 }
 
-// A lane's four logits of a row (experts e .. e + 3), -inf behind E.
+// A lane's four logits of a row (experts e .. e + 3), -inf behind E.  No branches: loads of several
+// tokens are to be under way at once.
 template <bool VEC>
 __device__ __forceinline__ f32x4 load_logits(const float* __restrict__ row, int e, int E) {
+  f32x4 v;
   if constexpr (VEC) {
-    return e < E ? *reinterpret_cast<const f32x4*>(row + e)
-                 : (f32x4){-INFINITY, -INFINITY, -INFINITY, -INFINITY};
+    v = *reinterpret_cast<const f32x4*>(row + min(e, E - 4));
   } else {
-    f32x4 v;
 #pragma unroll
-    for (int j = 0; j < 4; ++j) v[j] = e + j < E ? row[e + j] : -INFINITY;
-    return v;
+    for (int j = 0; j < 4; ++j) v[j] = row[min(e + j, E - 1)];
   }
+#pragma unroll
+  for (int j = 0; j < 4; ++j) v[j] = e + (VEC ? 0 : j) < E ? v[j] : -INFINITY;
+  return v;
 }
+
+// Whether a token counts, likewise: without a mask any byte is read in its place.
+struct TokenMask {
+  const uint8_t* p;
+  bool none;
+  __device__ TokenMask(const uint8_t* mask, const float* logits)
+      : p(mask ? mask : reinterpret_cast<const uint8_t*>(logits)), none(!mask) {}
+  __device__ __forceinline__ bool operator[](int t) const {
+    const uint8_t v = p[t];
+    return none | (v != 0);
+  }
+};
 
 // e^x as a power of two: the product's rounding costs |x| half steps, of which scores that weigh
 // anything have few.  (exp_f32 puts them back; the kernels here are near the instruction rate's bound.)
@@ -141,15 +161,16 @@ __device__ __forceinline__ void sum_piece(const BalanceArgs& a, int lo, int hi, 
   const int E = a.sh.E, k = a.sh.k;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
   const int e = (lane % L) * 4, slot = wave * kTok + lane / L;
+  const TokenMask mask(a.mask, a.logits);
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   for (int t = lo + slot; t < hi + slot; t += kAhead * 4 * kTok) {      // the same trips for all lanes of a wave
     f32x4 l[kAhead];
     bool in[kAhead];
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
-      const int at = t + i * 4 * kTok;
-      l[i] = load_logits<VEC>(a.logits + (size_t)min(at, hi - 1) * E, e, E);
-      in[i] = at < hi && (!a.mask || a.mask[at]);
+      const int at = min(t + i * 4 * kTok, hi - 1);
+      l[i] = load_logits<VEC>(a.logits + (size_t)at * E, e, E);
+      in[i] = mask[at] & (t + i * 4 * kTok < hi);
     }
 #pragma unroll
     for (int i = 0; i < kAhead; ++i) {
@@ -163,7 +184,7 @@ __device__ __forceinline__ void sum_piece(const BalanceArgs& a, int lo, int hi, 
   int n = 0;
   for (int i = threadIdx.x; i < (hi - lo) * k; i += 256) {
     const int t = lo + i / k, id = a.topk_idx[(size_t)lo * k + i];
-    const bool in = !a.mask || a.mask[t];
+    const bool in = mask[t];
     if (in && (uint32_t)id < (uint32_t)E) atomicAdd(&s.hist[id], 1);   // counts: order-independent
     n += in && i % k == 0;
   }
@@ -317,10 +338,11 @@ __global__ __launch_bounds__(1024) void balance_total_kernel(BalanceArgs a, int 
 // A wave's tokens are neighbours, so the coefficients change only where a sequence does.
 template <int L, bool SIGMOID, bool VEC>
 __global__ __launch_bounds__(256) void balance_grad_kernel(BalanceGradArgs a, int per) {
-  constexpr int kTok = 64 / L;
+  constexpr int kTok = 64 / L, kAhead = 4;
   const int T = a.sh.T, E = a.sh.E, S = a.sh.S;
   const int lane = threadIdx.x & 63;
   const int e = (lane % L) * 4, slot = lane / L;
+  const TokenMask mask(a.mask, a.logits);
   const int w0 = __builtin_amdgcn_readfirstlane((blockIdx.x * 4 + (threadIdx.x >> 6)) * per);
   if (w0 >= T) return;
   const int w1 = min(w0 + per, T);
@@ -352,37 +374,47 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(BalanceGradArgs a, in
                           : 0.0;
 #pragma unroll
     for (int j = 0; j < 4; ++j) c[j] = e + j < E ? (float)(by * a.load[(size_t)b * E + e + j]) : 0.f;
-    for (int t = lo + slot; t < hi + slot; t += kTok) {
-      const int row = min(t, hi - 1);
-      const bool in = !a.mask || a.mask[row];
-      const f32x4 l = load_logits<VEC>(a.logits + (size_t)row * E, e, E);
-      f32x4 q, rest, d;
-      const float inv = scores<L, SIGMOID, SIGMOID>(l, q, rest);
-      float lead = 0.f, dot = 0.f;
-      bool leads = false;
+    for (int t0 = lo + slot; t0 < hi + slot; t0 += kAhead * kTok) {
+      f32x4 l[kAhead];
+      bool counts[kAhead];
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        q[j] *= inv;
-        leads |= q[j] > 0.5f;
-      }
-      if (__ballot(leads)) {
-#pragma unroll
-        for (int j = 0; j < 4; ++j) lead += q[j] > 0.5f ? c[j] : 0.f;
-        lead = sum_of<L>(lead);
+      for (int i = 0; i < kAhead; ++i) {
+        const int row = min(t0 + i * kTok, hi - 1);
+        l[i] = load_logits<VEC>(a.logits + (size_t)row * E, e, E);
+        counts[i] = mask[row];
       }
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        d[j] = c[j] - lead;
-        dot = fmaf(d[j], q[j], dot);
-      }
-      dot = sum_of<L>(dot);
+      for (int i = 0; i < kAhead; ++i) {
+        const int t = t0 + i * kTok;
+        const bool in = counts[i];
+        f32x4 q, rest, d;
+        const float inv = scores<L, SIGMOID, SIGMOID>(l[i], q, rest);
+        float lead = 0.f, dot = 0.f;
+        bool leads = false;
 #pragma unroll
-      for (int j = 0; j < 4; ++j) {
-        d[j] = q[j] * (d[j] - dot);
-        if (SIGMOID) d[j] *= rest[j];
-        d[j] = in ? d[j] : 0.f;
+        for (int j = 0; j < 4; ++j) {
+          q[j] *= inv;
+          leads |= q[j] > 0.5f;
+        }
+        if (__ballot(leads)) {
+#pragma unroll
+          for (int j = 0; j < 4; ++j) lead += q[j] > 0.5f ? c[j] : 0.f;
+          lead = sum_of<L>(lead);
+        }
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          d[j] = c[j] - lead;
+          dot = fmaf(d[j], q[j], dot);
+        }
+        dot = sum_of<L>(dot);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+          d[j] = q[j] * (d[j] - dot);
+          if (SIGMOID) d[j] *= rest[j];
+          d[j] = in ? d[j] : 0.f;
+        }
+        if (t < hi) write(t, d);
       }
-      if (t < hi) write(t, d);
     }
   }
 }

@@ -127,7 +127,7 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs a) {
   }
 }
 
-// Eight values of a row times eight of another, added to s.
+// Eight values of B times eight of u, added to s.
 __device__ __forceinline__ float dot8(const u32x4& q, const float* u, float s) {
 #pragma unroll
   for (int i = 0; i < 4; ++i) {
@@ -136,26 +136,29 @@ __device__ __forceinline__ float dot8(const u32x4& q, const float* u, float s) {
   }
   return s;
 }
-__device__ __forceinline__ float dot8(const u32x4& q, const u32x4& x, float s) {
-#pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    s = fmaf(__uint_as_float(q[i] << 16), __uint_as_float(x[i] << 16), s);
-    s = fmaf(__uint_as_float(q[i] & 0xffff0000u), __uint_as_float(x[i] & 0xffff0000u), s);
-  }
-  return s;
-}
-
 // ---------------------------------------------------------------------------
 // One token, bound by the bytes of W and by latency.  Every block works out u itself (A is read from
 // memory once and then from L2), so one launch does all.  A wave takes whole rows, first its
-// eighth of A's, then of W, in runs of 1 KB, P runs a set, three sets under way; x lies in LDS.
-// Lane l brings in rank l's share of B u before the lanes' sums meet.
+// eighth of A's, then of W, in runs of 1 KB, P runs a set, four sets under way; x lies in LDS.
+// Lane l brings in rank l's share of B u before the lanes' sums meet.  Products by the 4x4x4 MFMA: it
+// multiplies four values of every lane of four with four of each of them, and the lane's own
+// with its own is the one that is kept (16 cycles for 8 values; converting and
+// multiplying them takes 96).
 // ---------------------------------------------------------------------------
+typedef short i16x4 __attribute__((ext_vector_type(4)));
+// Lane l's four values (two words) of each operand: column l % 4 of the result's 4x4 block l / 4,
+// of which row l % 4 is the lane's own times its own.
+__device__ __forceinline__ f32x4 mfma_4x4(uint32_t a0, uint32_t a1, uint32_t b0, uint32_t b1, f32x4 c) {
+  typedef uint32_t u32x2 __attribute__((ext_vector_type(2)));
+  return __builtin_amdgcn_mfma_f32_4x4x4bf16_1k(__builtin_bit_cast(i16x4, (u32x2){a0, a1}),
+                                                __builtin_bit_cast(i16x4, (u32x2){b0, b1}), c, 0, 0, 0);
+}
+
 constexpr int kTokenWaves = 8, kTokenMaxWidth = 32768, kTokenMaxRank = 64;
 
 template <int P>
 __global__ __launch_bounds__(kTokenWaves * 64, 2) void lora_token_kernel(LoraArgs a) {
-  constexpr int kSets = 3;
+  constexpr int kSets = 4;
   __shared__ __attribute__((aligned(16))) uint16_t sx[kTokenMaxWidth];
   __shared__ float su[kTokenMaxRank];
   const int d = a.sh.d, n = a.sh.n, rank = a.sh.rank;
@@ -190,7 +193,7 @@ __global__ __launch_bounds__(kTokenWaves * 64, 2) void lora_token_kernel(LoraArg
   for (int q = 0; q < kSets; ++q) load(q, q);
   for (int i = threadIdx.x * 8; i < d; i += kTokenWaves * 64 * 8) st16(sx + i, ld16(a.x + i));
   __syncthreads();
-  float sum = 0.f;
+  f32x4 acc = {0.f, 0.f, 0.f, 0.f};
   auto use = [&](int slot, int i) {
     if (i == of_a) __syncthreads();                    // every wave's u is there
     const bool w = i >= of_a;
@@ -198,10 +201,13 @@ __global__ __launch_bounds__(kTokenWaves * 64, 2) void lora_token_kernel(LoraArg
 #pragma unroll
     for (int q = 0; q < P; ++q) {
       const int k = (s * P + q) * 512 + lane * 8;
-      const u32x4 x = v[slot][q];
-      if (k < d) sum = dot8(x, ld16(sx + k), sum);
+      const u32x4 zero = {0, 0, 0, 0}, x = k < d ? ld16(sx + min(k, d - 8)) : zero, y = k < d ? v[slot][q] : zero;
+      acc = mfma_4x4(y[0], y[1], x[0], x[1], acc);
+      acc = mfma_4x4(y[2], y[3], x[2], x[3], acc);
     }
     if (s + 1 < segs) return;
+    const int own = lane & 3;
+    float sum = own == 0 ? acc[0] : own == 1 ? acc[1] : own == 2 ? acc[2] : acc[3];
     if (!w) {
       sum = wave_sum_f(sum) * scale;
       if (lane == 0) su[j / segs * kTokenWaves + wave] = sum;
@@ -214,7 +220,7 @@ __global__ __launch_bounds__(kTokenWaves * 64, 2) void lora_token_kernel(LoraArg
         else static_cast<uint16_t*>(a.y)[row] = (uint16_t)pack_bf16x2(a.sh.gelu ? gelu_for_bf16(sum) : sum, 0.f);
       }
     }
-    sum = 0.f;
+    acc = f32x4{0.f, 0.f, 0.f, 0.f};
   };
   for (int i = 0; i < total; i += kSets) {
 #pragma unroll
