@@ -225,46 +225,83 @@ __global__ __launch_bounds__(256) void balance_part_kernel(BalanceArgs a, int ch
   }
 }
 
-// A small batch in one launch: one block takes the sequences in turn, thread e expert e.
+// A small batch in one launch: a wave has every 16th sequence to itself, no barrier before the end.
 template <int L, bool SIGMOID, bool VEC>
-__global__ __launch_bounds__(256) void balance_single_kernel(BalanceArgs a) {
-  __shared__ PieceSums<L> s;
-  __shared__ double part[4];
-  const int T = a.sh.T, E = a.sh.E, S = a.sh.S, e = threadIdx.x;
+__global__ __launch_bounds__(1024) void balance_single_kernel(BalanceArgs a) {
+  constexpr int kTok = 64 / L, kAhead = 4, kWaves = 16;
+  __shared__ int hist[kWaves][4 * L], all[4 * L], lives[kWaves];
+  __shared__ double losses[kWaves];
+  const int T = a.sh.T, E = a.sh.E, S = a.sh.S, k = a.sh.k;
   const int lane = threadIdx.x & 63, wave = threadIdx.x >> 6;
+  const int e = (lane % L) * 4, slot = lane / L;
+  const TokenMask mask(a.mask, a.logits);
+  int* mine = hist[wave];
+  if (threadIdx.x < 4 * L) all[threadIdx.x] = 0;
+  __syncthreads();
   double total = 0.0;
-  int live = 0, all = 0;
-  for (int b = 0; b < S; ++b) {
+  int live = 0;
+  for (int b = wave; b < S; b += kWaves) {
     const int lo = border(a.offsets, b, T), hi = border(a.offsets, b + 1, T);
-    s.clear(E);
-    __syncthreads();
-    if (hi > lo) sum_piece<L, SIGMOID, VEC>(a, lo, hi, s);
-    __syncthreads();
-    const int n = s.count, load = e < E ? s.hist[e] : 0;
-    const double mean = n && e < E ? (double)s.share(e) / n : 0.0;
-    double loss = n ? (double)E * load / ((double)a.sh.k * n) * mean : 0.0;
-    if (e < E) {
-      a.load[(size_t)b * E + e] = load;
-      if (a.prob_mean) a.prob_mean[(size_t)b * E + e] = (float)mean;
+    for (int i = lane; i < 4 * L; i += 64) mine[i] = 0;
+    f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+    int n = 0;
+    for (int t = lo + slot; t < hi + slot; t += kAhead * kTok) {
+      f32x4 l[kAhead];
+      bool in[kAhead];
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        const int at = min(t + i * kTok, hi - 1);
+        l[i] = load_logits<VEC>(a.logits + (size_t)at * E, e, E);
+        in[i] = mask[at] & (t + i * kTok < hi);
+      }
+#pragma unroll
+      for (int i = 0; i < kAhead; ++i) {
+        f32x4 q, rest;
+        const float inv = scores<L, SIGMOID, false>(l[i], q, rest);
+#pragma unroll
+        for (int j = 0; j < 4; ++j) acc[j] += in[i] ? q[j] * inv : 0.f;
+        n += __popcll(__ballot(in[i] && lane % L == 0));
+      }
     }
+    for (int i = lane; i < (hi - lo) * k; i += 64) {
+      const int id = a.topk_idx[(size_t)lo * k + i];
+      if (mask[lo + i / k] && (uint32_t)id < (uint32_t)E) atomicAdd(&mine[id], 1);
+    }
+    __builtin_amdgcn_fence(__ATOMIC_ACQ_REL, "wavefront");
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int o = L; o < 64; o <<= 1)
+#pragma unroll
+      for (int j = 0; j < 4; ++j) acc[j] += __shfl_xor(acc[j], o);
+    double loss = 0.0;
+    if (lane < L)
+#pragma unroll
+      for (int j = 0; j < 4; ++j)
+        if (e + j < E) {
+          const int load = mine[e + j];
+          const double mean = n ? (double)acc[j] / n : 0.0;
+          loss += n ? (double)E * load / ((double)k * n) * mean : 0.0;
+          a.load[(size_t)b * E + e + j] = load;
+          if (a.prob_mean) a.prob_mean[(size_t)b * E + e + j] = (float)mean;
+          if (load) atomicAdd(&all[e + j], load);
+        }
 #pragma unroll
     for (int o = 32; o > 0; o >>= 1) loss += __shfl_xor(loss, o);
-    if (lane == 0) part[wave] = loss;
-    __syncthreads();
-    loss = (part[0] + part[1]) + (part[2] + part[3]);
-    if (e == 0) {
+    if (lane == 0) {
       a.valid[b] = n;
       if (a.seq_loss) a.seq_loss[b] = (float)loss;
     }
     total += loss;
     live += n > 0;
-    all += load;
   }
-  if (a.total_load && e < E) a.total_load[e] = all;
-  if (e == 0) {
-    a.valid[S] = live;
-    if (a.loss) *a.loss = live ? (float)(total / live) : 0.f;
-  }
+  if (lane == 0) losses[wave] = total, lives[wave] = live;
+  __syncthreads();
+  if (a.total_load && (int)threadIdx.x < E) a.total_load[threadIdx.x] = all[threadIdx.x];
+  if (threadIdx.x) return;
+#pragma unroll
+  for (int w = 1; w < kWaves; ++w) total += losses[w], live += lives[w];
+  a.valid[S] = live;
+  if (a.loss) *a.loss = live ? (float)(total / live) : 0.f;
 }
 
 // A sequence's pieces added up for 64 experts: 16 waves a sixteenth of them each.
@@ -437,13 +474,13 @@ static void for_kind(bool sigmoid, int E, F f) {
   });
 }
 
-// Few values and few sequences (each costs its barriers): one block and one launch.
-static bool single(const BalanceShape& s) { return s.S <= 8 && (long)s.T * s.E <= 32 * 1024; }
+// One launch where a wave can take a whole sequence: at most 32 of its steps, and 64 sequences.
+static bool single(const BalanceShape& s) { return s.S <= 64 && (long)s.T * s.E <= 8 * 1024; }
 
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
   if (single(a.sh)) {
     for_kind(a.sh.sigmoid, a.sh.E, [&](auto l, auto sig, auto vec) {
-      balance_single_kernel<decltype(l)::value, decltype(sig)::value, decltype(vec)::value><<<1, 256, 0, s>>>(a);
+      balance_single_kernel<decltype(l)::value, decltype(sig)::value, decltype(vec)::value><<<1, 1024, 0, s>>>(a);
     });
     return hipGetLastError();
   }

@@ -31,9 +31,18 @@ struct LoraArgs {
 };
 hipError_t launch_lora(const LoraArgs& a, hipStream_t s);
 
+// Parts of the k range: fp32 sums for lora_finish_kernel.
+struct LoraPartArgs {
+  LoraArgs a;
+  int splits, a_tiles;                 // parts of k; column tiles that A can have per row tile
+  float* part;                         // [splits][T][n]
+  float* u;                            // [splits][T][lora_pitch], not scaled
+};
+void launch_lora_part_tile(const LoraPartArgs& p, unsigned grid, hipStream_t s);   // 128 x 128 tiles
+
 // The tiled product (lora_tile.hip).  u is `lora_terms` bf16 matrices [T][lora_pitch] that add up
 // to scale A x.
-inline int lora_pitch(int rank) { return (rank + 15) / 16 * 16; }
+__host__ __device__ inline int lora_pitch(int rank) { return (rank + 15) / 16 * 16; }
 inline int lora_terms(const LoraShape& s) { return s.f32_out ? 3 : 2; }
 hipError_t launch_lora_tile(const LoraArgs& a, hipStream_t s);
 

@@ -10,6 +10,7 @@
 
 #include "device_common.h"
 #include "lora.h"
+#include "lora_parts.h"
 
 namespace moe {
 
@@ -139,7 +140,7 @@ __device__ __forceinline__ float dot8(const u32x4& q, const float* u, float s) {
 // ---------------------------------------------------------------------------
 // One token, bound by the bytes of W and by latency.  Every block works out u itself (A is read from
 // memory once and then from L2), so one launch does all.  A wave takes whole rows, first its
-// eighth of A's, then of W, in runs of 1 KB, P runs a set, four sets under way; x lies in LDS.
+// eighth of A's, then of W, in runs of 1 KB, P runs a set, three sets under way; x lies in LDS.
 // Lane l brings in rank l's share of B u before the lanes' sums meet.  Products by the 4x4x4 MFMA: it
 // multiplies four values of every lane of four with four of each of them, and the lane's own
 // with its own is the one that is kept (16 cycles for 8 values; converting and
@@ -158,39 +159,51 @@ constexpr int kTokenWaves = 8, kTokenMaxWidth = 32768, kTokenMaxRank = 64;
 
 template <int P>
 __global__ __launch_bounds__(kTokenWaves * 64, 2) void lora_token_kernel(LoraArgs a) {
-  constexpr int kSets = 4;
+  constexpr int kSets = 3;
   __shared__ __attribute__((aligned(16))) uint16_t sx[kTokenMaxWidth];
   __shared__ float su[kTokenMaxRank];
   const int d = a.sh.d, n = a.sh.n, rank = a.sh.rank;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int first = blockIdx.x * kTokenWaves + wave, stride = gridDim.x * kTokenWaves;   // rows of W
   const int segs = (d + P * 512 - 1) / (P * 512);
-  const int given = a.adapter[0], id = (uint32_t)given < (uint32_t)a.sh.N ? given : -1;
-  const int of_a = id >= 0 ? rank / kTokenWaves * segs : 0;             // sets of A's rows (rank is a multiple of 8)
+  const int of_a = rank / kTokenWaves * segs;          // sets of A's rows (rank is a multiple of 8)
   const int total = of_a + (first < n ? ((n - 1 - first) / stride + 1) * segs : 0);
-  const uint16_t* rows_a = a.a + (size_t)max(id, 0) * rank * d + (size_t)wave * d;
-  const float scale = a.scale && id >= 0 ? a.scale[id] : 1.f;
   const int lane_rank = min(lane, rank - 1);
+  const int turn = (wave + blockIdx.x / 8) % kTokenWaves;   // blocks of an XCD read different rows of A at a time
   u32x4 v[kSets][P];
   uint16_t vb[kSets], vbias[kSets];                    // the row's B of the lane's rank, its bias
-  // Set i: lane l has values 512 q + 8 l .. + 7 of its runs q; 0 past the row's end.  Past the last
-  // set that one again, not used.
+  // Set i: lane l has values 512 q + 8 l .. + 7 of its runs q; past the row's end any of its values.
+  // Past the last set that one again, not used.
+  auto load_row = [&](int slot, const uint16_t* p, int s) {
+#pragma unroll
+    for (int q = 0; q < P; ++q) v[slot][q] = ld16(p + min((s * P + q) * 512 + lane * 8, d - 8));
+  };
+  auto row_of = [&](int i) { return min(first + (i - of_a) / segs * stride, n - 1); };
+  // W's first rows, before anything that has to wait for the adapter's number.
+#pragma unroll
+  for (int q = 0; q < kSets; ++q)
+    if (q >= of_a) load_row(q, a.w + (size_t)row_of(q) * d, (q - of_a) % segs);
+  const int given = a.adapter[0], id = (uint32_t)given < (uint32_t)a.sh.N ? given : -1;
+  const int any = max(id, 0);                          // without an adapter A and B are read, not used
+  const uint16_t* rows_a = a.a + ((size_t)any * rank + turn) * d;
+  const float scale = a.scale ? a.scale[any] : 1.f;
+  auto load_ends = [&](int slot, int i) {
+    const int row = i >= of_a ? row_of(i) : 0;
+    vb[slot] = a.b[((size_t)any * n + row) * rank + lane_rank];
+    vbias[slot] = a.bias ? a.bias[row] : (uint16_t)0;
+  };
   auto load = [&](int slot, int i) {
     i = max(min(i, total - 1), 0);
     const bool w = i >= of_a;
-    const int j = w ? i - of_a : i, s = j % segs, row = min(first + j / segs * stride, n - 1);
-    const uint16_t* p = w ? a.w + (size_t)row * d : rows_a + (size_t)(j / segs) * kTokenWaves * d;
-#pragma unroll
-    for (int q = 0; q < P; ++q) {
-      const int k = (s * P + q) * 512 + lane * 8;
-      v[slot][q] = ld16(p + min(k, d - 8));
-    }
-    const size_t at = (size_t)max(id, 0) * n + (w ? row : 0);
-    vb[slot] = a.b[at * rank + lane_rank];
-    vbias[slot] = a.bias ? a.bias[w ? row : 0] : (uint16_t)0;
+    const int j = w ? i - of_a : i;
+    load_row(slot, w ? a.w + (size_t)row_of(i) * d : rows_a + (size_t)(j / segs) * kTokenWaves * d, j % segs);
+    load_ends(slot, i);
   };
 #pragma unroll
-  for (int q = 0; q < kSets; ++q) load(q, q);
+  for (int q = 0; q < kSets; ++q) {
+    if (q < of_a) load(q, q);
+    else load_ends(q, q);
+  }
   for (int i = threadIdx.x * 8; i < d; i += kTokenWaves * 64 * 8) st16(sx + i, ld16(a.x + i));
   __syncthreads();
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
@@ -210,7 +223,7 @@ __global__ __launch_bounds__(kTokenWaves * 64, 2) void lora_token_kernel(LoraArg
     float sum = own == 0 ? acc[0] : own == 1 ? acc[1] : own == 2 ? acc[2] : acc[3];
     if (!w) {
       sum = wave_sum_f(sum) * scale;
-      if (lane == 0) su[j / segs * kTokenWaves + wave] = sum;
+      if (lane == 0) su[j / segs * kTokenWaves + turn] = sum;
     } else {
       if (id >= 0 && lane < rank) sum = fmaf(bf16_to_f32(vb[slot]), su[lane], sum);
       sum = wave_sum_f(sum) + bf16_to_f32(vbias[slot]);
@@ -244,60 +257,28 @@ __global__ __launch_bounds__(kTokenWaves * 64, 2) void lora_token_kernel(LoraArg
 // bank once.  Four waves as WM x 4 / WM.  Two blocks fit a CU, so one's start and end go under
 // the other's loads.
 // ---------------------------------------------------------------------------
-struct PartArgs {
-  LoraArgs a;
-  int splits, a_tiles;                 // parts of k; column tiles that A can have per BM tokens
-  float* part;                         // [splits][T][n]
-  float* u;                            // [splits][T][pitch]
-};
-
 constexpr int kPartCols = 64;
 
-template <int BM, int RB, int ST, int WM>
-__global__ __launch_bounds__(256, 2) void lora_part_kernel(PartArgs p) {
+template <int BM, int RB, int ST, int WM, int OCC>
+__global__ __launch_bounds__(256, OCC) void lora_part_kernel(LoraPartArgs p) {
   constexpr int kPieces = RB / 16, kPer = 1024 / RB;             // of a row; rows per load
   constexpr int kA = BM * RB, kStage = (BM + kPartCols) * RB;
   constexpr int kAI = kA / 4096, kWI = kPartCols * RB / 4096, L = kAI + kWI;   // loads per wave
   constexpr int kM = BM / WM / 16, kN = kPartCols * WM / 64;     // 16x16 tiles per wave
-  static_assert(kA % 4096 == 0 && 2 * (ST * kStage + BM * 8 + 64) <= 160 * 1024, "LDS plan");
+  static_assert(kA % 4096 == 0 && OCC * (ST * kStage + BM * 4) <= 160 * 1024 && (ST - 2) * L < 64, "LDS plan");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[ST * kStage];
-  __shared__ int ids[BM], list[BM];
+  __shared__ int list[BM];
   const LoraArgs& a = p.a;
-  const int T = a.sh.T, d = a.sh.d, n = a.sh.n, rank = a.sh.rank, pitch = (rank + 15) / 16 * 16, per = pitch / 16;
+  const int T = a.sh.T, d = a.sh.d, n = a.sh.n, rank = a.sh.rank, pitch = lora_pitch(rank), per = pitch / 16;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, fc = lane >> 4, wm = wave % WM, wn = wave / WM;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds;
-
-  // Block b: the row tiles of one (column tile, part of k) follow one another on one XCD.
-  const int mts = (T + BM - 1) / BM, cols = n / kPartCols + p.a_tiles;
-  const int q = blockIdx.x / 8, cs = q / mts * 8 + blockIdx.x % 8;
-  if (cs >= cols * p.splits) return;
-  const int t0 = q % mts * BM, col = cs % cols, split = cs / cols;
-  const bool of_a = col >= n / kPartCols;
-  const int g0 = (col - n / kPartCols) * 4;            // of A: its first group of 16 ranks
+  LoraUnit w;
+  if (!lora_unit<BM, kPartCols>(p, w)) return;
   int groups = 0;
-  if (of_a) {
-    int own[(BM + 63) / 64];
-    uint64_t left[(BM + 63) / 64];
-#pragma unroll
-    for (int i = 0; i < (BM + 63) / 64; ++i) {
-      const int r = i * 64 + lane;
-      own[i] = r < BM && t0 + r < T ? a.adapter[t0 + r] : -1;
-      if ((uint32_t)own[i] >= (uint32_t)a.sh.N) own[i] = -1;
-      left[i] = __ballot(own[i] >= 0);
-      if (r < BM) ids[r] = own[i];                     // every wave the same values
-    }
-    int count = 0;
-#pragma unroll
-    for (int i = 0; i < (BM + 63) / 64; ++i)
-      for (; left[i]; ++count) {
-        const int one = __builtin_amdgcn_readlane(own[i], __ffsll((unsigned long long)left[i]) - 1);
-#pragma unroll
-        for (int j = 0; j < (BM + 63) / 64; ++j) left[j] &= ~__ballot(own[j] == one);
-        list[count] = one;
-      }
-    groups = count * per;
-    if (g0 >= groups) return;
+  if (w.of_a) {
+    groups = lora_list<BM>(a, w.t0, list) * per;
+    if (w.g0 >= groups) return;
     __syncthreads();
   }
 
@@ -309,21 +290,22 @@ __global__ __launch_bounds__(256, 2) void lora_part_kernel(PartArgs p) {
   uint32_t x_off[kAI], w_off[kWI];
   const uint8_t* w_base[kWI];
 #pragma unroll
-  for (int i = 0; i < kAI; ++i) x_off[i] = (uint32_t)min(t0 + row_of(i), T - 1) * row_bytes + piece_of(row_of(i));
+  for (int i = 0; i < kAI; ++i) x_off[i] = (uint32_t)min(w.t0 + row_of(i), T - 1) * row_bytes + piece_of(row_of(i));
 #pragma unroll
   for (int i = 0; i < kWI; ++i) {
     const int row = row_of(i);
-    if (of_a) {
-      const int g = min(g0 + (i * 4 + wave) * kPer / 16, groups - 1);
+    if (w.of_a) {
+      const int g = min(w.g0 + (i * 4 + wave) * kPer / 16, groups - 1);
       const int id = __builtin_amdgcn_readfirstlane(list[g / per]);
       w_base[i] = reinterpret_cast<const uint8_t*>(a.a) + (size_t)id * rank * row_bytes;
       w_off[i] = (uint32_t)min(g % per * 16 + row % 16, rank - 1) * row_bytes + piece_of(row);
     } else {
-      w_base[i] = reinterpret_cast<const uint8_t*>(a.w) + (size_t)col * kPartCols * row_bytes;
+      w_base[i] = reinterpret_cast<const uint8_t*>(a.w) + (size_t)w.n0 * row_bytes;
       w_off[i] = (uint32_t)row * row_bytes + piece_of(row);
     }
   }
-  const int nk = d / (RB / 2), k0 = (int)((long)split * nk / p.splits), k1 = (int)((long)(split + 1) * nk / p.splits);
+  // In steps of RB bytes; runs of 256 bytes start at whole ones, so the parts' borders are even.
+  const int k0 = w.k0 * 128 / RB, k1 = w.split + 1 < p.splits ? w.k1 * 128 / RB : d * 2 / RB;
   auto load = [&](int step, int stage) {               // past the part's end: its last step, never read
     const size_t k = (size_t)min(step, k1 - 1) * RB;
     const uint32_t to = lds0 + stage * kStage;
@@ -361,35 +343,38 @@ __global__ __launch_bounds__(256, 2) void lora_part_kernel(PartArgs p) {
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");     // no load outlives its LDS
   // A lane has columns 4 fc .. + 3 of token fr.
 #pragma unroll
-  for (int j = 0; j < kN; ++j)
+  for (int m = 0; m < kM; ++m) {
+    const int t = w.t0 + wm * (BM / WM) + m * 16 + fr;
+    if (t >= T) continue;
+    const int id = w.of_a ? a.adapter[t] : -1;
 #pragma unroll
-    for (int m = 0; m < kM; ++m) {
-      const int row = wm * (BM / WM) + m * 16 + fr, t = t0 + row, c = (wn * kN + j) * 16 + fc * 4;
-      if (t >= T) continue;
+    for (int j = 0; j < kN; ++j) {
+      const int c = (wn * kN + j) * 16 + fc * 4;
       f32x4 v = acc[j][m];
-      if (!of_a) {
-        *reinterpret_cast<f32x4*>(p.part + ((size_t)split * T + t) * n + col * kPartCols + c) = v;
+      if (!w.of_a) {
+        *reinterpret_cast<f32x4*>(p.part + ((size_t)w.split * T + t) * n + w.n0 + c) = v;
       } else {
-        const int g = g0 + c / 16;
-        if (g >= groups || ids[row] != list[g / per]) continue;
+        const int g = w.g0 + c / 16;
+        if (g >= groups || id != list[g / per]) continue;
         const int r = g % per * 16 + c % 16;
 #pragma unroll
         for (int i = 0; i < 4; ++i) v[i] = r + i < rank ? v[i] : 0.f;
-        *reinterpret_cast<f32x4*>(p.u + ((size_t)split * T + t) * pitch + r) = v;
+        *reinterpret_cast<f32x4*>(p.u + ((size_t)w.split * T + t) * pitch + r) = v;
       }
     }
+  }
 }
 
 // Parts of k added up in order, then bias, B u, activation: a block one token's 1024 columns, four
 // a thread.
-__global__ __launch_bounds__(256) void lora_finish_kernel(PartArgs p) {
+__global__ __launch_bounds__(256) void lora_finish_kernel(LoraPartArgs p) {
   __shared__ __attribute__((aligned(16))) float su[kLoraMaxRank];
   const LoraArgs& a = p.a;
   const int T = a.sh.T, n = a.sh.n, rank = a.sh.rank, pitch = (rank + 15) / 16 * 16;
   const int t = blockIdx.x, c = (blockIdx.y * 256 + threadIdx.x) * 4;
   const int given = a.adapter[t], id = (uint32_t)given < (uint32_t)a.sh.N ? given : -1;
   const bool in = c < n;
-  f32x4 v = {0.f, 0.f, 0.f, 0.f};
+  f32x4 v = in ? *reinterpret_cast<const f32x4*>(p.part + (size_t)t * n + c) : f32x4{0.f, 0.f, 0.f, 0.f};
   u32x4 q[4][2] = {};
   const uint16_t* b = a.b + ((size_t)max(id, 0) * n + min(c, n - 4)) * rank;
   if (in && id >= 0) {                                 // the first 16 ranks, under way with the sums
@@ -401,7 +386,7 @@ __global__ __launch_bounds__(256) void lora_finish_kernel(PartArgs p) {
   }
   if (in) {
 #pragma unroll 4
-    for (int s = 0; s < p.splits; ++s) v += *reinterpret_cast<const f32x4*>(p.part + ((size_t)s * T + t) * n + c);
+    for (int s = 1; s < p.splits; ++s) v += *reinterpret_cast<const f32x4*>(p.part + ((size_t)s * T + t) * n + c);
     if (a.bias) {
       const uint2 w = *reinterpret_cast<const uint2*>(a.bias + c);
       v[0] += __uint_as_float(w.x << 16);
@@ -443,18 +428,23 @@ __global__ __launch_bounds__(256) void lora_finish_kernel(PartArgs p) {
 // ---- launches ------------------------------------------------------------------------------
 enum LoraPath { kToken, kPart, kTile };
 
-static LoraPath path_of(const LoraShape& s) {
-  if (s.T == 1 && s.rank <= kTokenMaxRank && s.d <= kTokenMaxWidth) return kToken;
-  // Tiles need four steps of 64 k: their loads run two ahead, into the next tile only.
-  return s.T > 512 && s.d >= 256 ? kTile : kPart;
+// Tokens of a part's block, and the parts that k is cut into, so that every CU has a block (the
+// tiles of 128 x 128: two).
+static int part_rows(const LoraShape& s) { return s.T <= 32 ? 32 : s.T <= 64 ? 64 : 128; }
+static long part_tiles(const LoraShape& s) {
+  const int bm = part_rows(s), bn = bm == 128 ? 128 : kPartCols;
+  return (long)((s.T + bm - 1) / bm) * ((s.n + bn - 1) / bn);
+}
+static int part_splits(const LoraShape& s) {
+  const long tiles = part_tiles(s), want = part_rows(s) == 128 ? 448 : 256;
+  // at least 128 k each, and whole runs of 256 bytes
+  return (int)std::max(1L, std::min({(want + tiles / 2) / tiles, (long)s.d / 128, 16L}));
 }
 
-// Tokens of a block, and the parts that k is cut into so that every CU has a block.
-static int part_rows(const LoraShape& s) { return s.T <= 32 ? 32 : s.T <= 64 ? 64 : 128; }
-static int part_splits(const LoraShape& s) {
-  const int bm = part_rows(s), steps = s.d / (bm == 32 ? 128 : 64);
-  const long tiles = (long)((s.T + bm - 1) / bm) * (s.n / kPartCols);
-  return (int)std::max(1L, std::min({(256 + tiles / 2) / tiles, (long)steps / 2, 16L}));
+static LoraPath path_of(const LoraShape& s) {
+  if (s.T == 1 && s.rank <= kTokenMaxRank && (long)s.rank * s.d <= 128 * 1024 && s.d <= kTokenMaxWidth) return kToken;
+  // Tiles need four steps of 64 k: their loads run two ahead, into the next tile only.
+  return s.T > 128 && s.d >= 256 && part_splits(s) == 1 ? kTile : kPart;
 }
 
 size_t lora_u_bytes(const LoraShape& s) {
@@ -480,15 +470,15 @@ static void launch_shrink(const LoraArgs& a, hipStream_t s) {
 
 static hipError_t launch_part(const LoraArgs& a, hipStream_t s) {
   const LoraShape& h = a.sh;
-  PartArgs p{a, part_splits(h), 0, static_cast<float*>(a.u), nullptr};
+  LoraPartArgs p{a, part_splits(h), 0, static_cast<float*>(a.u), nullptr};
   p.u = p.part + (size_t)p.splits * h.T * h.n;
-  const int bm = part_rows(h), mts = (h.T + bm - 1) / bm;
-  p.a_tiles = (std::min(h.N, std::min(h.T, bm)) * (lora_pitch(h.rank) / 16) + 3) / 4;
-  const int cs = (h.n / kPartCols + p.a_tiles) * p.splits;
+  const int bm = part_rows(h), bn = bm == 128 ? 128 : kPartCols, mts = (h.T + bm - 1) / bm;
+  p.a_tiles = (std::min(h.N, std::min(h.T, bm)) * (lora_pitch(h.rank) / 16) * 16 + bn - 1) / bn;
+  const int cs = ((h.n + bn - 1) / bn + p.a_tiles) * p.splits;
   const unsigned grid = (unsigned)((cs + 7) / 8 * mts * 8);
-  if (bm == 32) lora_part_kernel<32, 256, 3, 1><<<grid, 256, 0, s>>>(p);
-  else if (bm == 64) lora_part_kernel<64, 128, 4, 2><<<grid, 256, 0, s>>>(p);
-  else lora_part_kernel<128, 128, 3, 2><<<grid, 256, 0, s>>>(p);
+  if (bm == 32) lora_part_kernel<32, 256, 3, 1, 2><<<grid, 256, 0, s>>>(p);
+  else if (bm == 64) lora_part_kernel<64, 128, 4, 2, 2><<<grid, 256, 0, s>>>(p);
+  else launch_lora_part_tile(p, grid, s);
   if (hipError_t e = hipGetLastError()) return e;
   lora_finish_kernel<<<dim3(h.T, (h.n + 1023) / 1024), 256, 0, s>>>(p);
   return hipGetLastError();

@@ -23,6 +23,7 @@
 
 #include "device_common.h"
 #include "lora.h"
+#include "lora_parts.h"
 
 namespace moe {
 
@@ -57,13 +58,16 @@ static long lora_tile_blocks(long total, long ntn) {
 __device__ __forceinline__ bool infinite_lo(uint32_t w) { return (w & 0x7f80u) == 0x7f80u; }
 __device__ __forceinline__ bool infinite_hi(uint32_t w) { return (w & 0x7f800000u) == 0x7f800000u; }
 
+// TERMS: the bf16 terms of u, 2 for a bf16 result, 3 for fp32; 0: a part of the k range of W x, or
+// of A x as further columns, stored in fp32 for a finish of its own (one tile a block).
 template <int BM, int BN, int TERMS, int OCC>
-__global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraArgs p) {
+__global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraPartArgs all) {
+  const LoraArgs& p = all.a;
   constexpr int kA = BM * 128, kW = BN * 128, kWS = 3;             // bytes a stage; stages of W
   constexpr int oW = 2 * kA;
   constexpr int kMT = BM / 64, kNT = BN / 64;                      // 32x32 tiles per wave
   constexpr int kAI = BM / 32, kWI = BN / 32;                      // 1 KB loads per wave
-  constexpr bool F32 = TERMS == 3;
+  constexpr bool F32 = TERMS == 3, PART = TERMS == 0;
   static_assert(2 * kA + kWS * kW <= 160 * 1024, "LDS plan");
   __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kA + kWS * kW];
 
@@ -77,6 +81,23 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraArgs p) {
   struct Where {
     int r0, n0;
   };
+  // A part: which of the k range, and of which columns.
+  LoraUnit unit;
+  int groups = 0, wide[kWI];                           // groups of 16 ranks; the ids that the wave loads
+  if constexpr (PART) {
+    if (!lora_unit<BM, BN>(all, unit)) return;
+    if (unit.of_a) {
+      int* list = reinterpret_cast<int*>(lds);
+      groups = lora_list<BM>(p, unit.t0, list) * (lora_pitch(p.sh.rank) / 16);
+      if (unit.g0 >= groups) return;
+      __syncthreads();
+#pragma unroll
+      for (int i = 0; i < kWI; ++i)
+        wide[i] = __builtin_amdgcn_readfirstlane(list[min(unit.g0 + (i * 4 + wave) / 2, groups - 1) / (lora_pitch(p.sh.rank) / 16)]);
+      __syncthreads();
+    }
+  }
+  const int k0 = PART ? unit.k0 : 0, k1 = PART ? unit.k1 : nk;
   int b = blockIdx.x;
   auto locate = [&](Where& w) {
     int mt, nt;
@@ -93,30 +114,42 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraArgs p) {
 #pragma unroll
     for (int i = 0; i < kAI; ++i) a_off[i] = (uint32_t)min(w.r0 + row_of(i), T - 1) * (uint32_t)K * 2u + chunk_of(row_of(i));
   };
+  const uint8_t *xb = reinterpret_cast<const uint8_t*>(p.x), *wb[PART ? kWI : 1];
+  wb[0] = reinterpret_cast<const uint8_t*>(p.w);
   auto aim_w = [&](const Where& w) {
 #pragma unroll
-    for (int i = 0; i < kWI; ++i) w_off[i] = (uint32_t)min(w.n0 + row_of(i), N - 1) * (uint32_t)K * 2u + chunk_of(row_of(i));
+    for (int i = 0; i < kWI; ++i) {
+      if (PART && unit.of_a) {                         // rows of one adapter in every load
+        const int rank = p.sh.rank, g = min(unit.g0 + (i * 4 + wave) / 2, groups - 1);
+        const int row = min(g % (lora_pitch(rank) / 16) * 16 + row_of(i) % 16, rank - 1);
+        wb[PART ? i : 0] = reinterpret_cast<const uint8_t*>(p.a) + (size_t)wide[i] * rank * K * 2;
+        w_off[i] = (uint32_t)row * (uint32_t)K * 2u + chunk_of(row_of(i));
+      } else {
+        if (PART) wb[PART ? i : 0] = reinterpret_cast<const uint8_t*>(p.w);
+        w_off[i] = (uint32_t)min(w.n0 + row_of(i), N - 1) * (uint32_t)K * 2u + chunk_of(row_of(i));
+      }
+    }
   };
-  const uint8_t *xb = reinterpret_cast<const uint8_t*>(p.x), *wb = reinterpret_cast<const uint8_t*>(p.w);
   auto load_a = [&](int i, int stage, int step) {
     dma16(xb + (size_t)step * 128, a_off[i], lds0 + stage * kA + (i * 4 + wave) * 1024);
   };
   auto load_w = [&](int i, int stage, int step) {
-    dma16(wb + (size_t)step * 128, w_off[i], lds0 + oW + stage * kW + (i * 4 + wave) * 1024);
+    dma16(wb[PART ? i : 0] + (size_t)step * 128, w_off[i], lds0 + oW + stage * kW + (i * 4 + wave) * 1024);
   };
 
   Where cur, next;
-  if (!locate(cur)) return;
+  if (PART) cur = Where{unit.t0, unit.n0};
+  else if (!locate(cur)) return;
   next = cur;
-  bool more = true;
+  bool more = !PART;
   aim_a(cur);
   aim_w(cur);
-  int as = 0, ws = 0;                                  // the steps to load next
+  int as = k0, ws = k0;                                // the steps to load next
   // After a step's loads of W: on to the next step, or tile.  The loads of x follow half a step
   // later, with the tile found here.  Past the last tile the last step is loaded again, unread.
   bool a_moves = false;
   auto advance_w = [&]() {
-    if (++ws < nk) return;
+    if (++ws < k1) return;
     if (more) {
       b += gridDim.x;
       Where w;
@@ -129,17 +162,17 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraArgs p) {
         return;
       }
     }
-    ws = nk - 1;
+    ws = k1 - 1;
   };
   auto advance_a = [&]() {
-    if (++as < nk) return;
+    if (++as < k1) return;
     if (a_moves) {
       aim_a(next);
       as = 0;
       a_moves = false;
       return;
     }
-    as = nk - 1;
+    as = k1 - 1;
   };
 
   f32x16 acc[kNT][kMT];
@@ -195,6 +228,7 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraArgs p) {
   };
   const int rank = p.sh.rank, pitch = (rank + 15) / 16 * 16;
   auto expand = [&](const Where& w) {
+    constexpr int kTerms = PART ? 1 : TERMS;
     const uint16_t* u = static_cast<const uint16_t*>(p.u);
 #pragma unroll
     for (int m = 0; m < kMT; ++m) {
@@ -206,7 +240,7 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraArgs p) {
         left &= ~same;
         const bool mine = ids[m] == id, all = same == ~0ull;
         for (int k = 0; k < pitch; k += 16) {
-          u32x4 bf[kNT], uf[TERMS];
+          u32x4 bf[kNT], uf[kTerms];
 #pragma unroll
           for (int j = 0; j < kNT; ++j) {
             const int col = min(w.n0 + wn * (BN / 2) + j * 32 + fr, N - 1);
@@ -214,7 +248,7 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraArgs p) {
             bf[j] = in ? ld16(p.b + ((size_t)id * N + col) * rank + k + fc * 8) : u32x4{0, 0, 0, 0};
           }
 #pragma unroll
-          for (int q = 0; q < TERMS; ++q) {
+          for (int q = 0; q < kTerms; ++q) {
             uf[q] = ld16(um + (size_t)q * T * pitch + k);
             uf[q] = mine ? uf[q] : u32x4{0, 0, 0, 0};
           }
@@ -240,7 +274,7 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraArgs p) {
               }
             }
 #pragma unroll
-            for (int q = 0; q < TERMS; ++q) acc[j][m] = mfma32_bf16(bf[j], uf[q], acc[j][m]);
+            for (int q = 0; q < kTerms; ++q) acc[j][m] = mfma32_bf16(bf[j], uf[q], acc[j][m]);
           }
         }
       }
@@ -332,7 +366,7 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraArgs p) {
         for (int q = 0; q < 16; ++q) acc[j][m][q] = 0.f;
     const Where done = cur;
     bool go_on = false;
-    for (int t = 0; t < nk; ++t) {
+    for (int t = k0; t < k1; ++t) {
       pin();
       const int sw1 = sw == 2 ? 0 : sw + 1, sw2 = sw == 0 ? 2 : sw - 1;
       half_step(xa, xw, ya, yw, sa, sw, 1, [&](int i) { load_w(i, sw2, ws); }, LoadsW{});
@@ -344,6 +378,7 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraArgs p) {
       sa ^= 1;
       sw = sw1;
     }
+    if constexpr (PART) break;
     go_on = next.r0 != cur.r0 || next.n0 != cur.n0;
     load_ids(done);
     expand(done);
@@ -352,14 +387,53 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraArgs p) {
     cur = next;
   }
   asm volatile("s_waitcnt vmcnt(0)" ::: "memory");       // no load outlives its LDS
+  if constexpr (PART) {
+    // A lane has columns 8 g + 4 fc .. + 3 of token fr: of W, or of its own adapter's ranks.
+    const int per = pitch / 16;
+    int* list = reinterpret_cast<int*>(lds);
+    if (unit.of_a) {
+      __syncthreads();
+      lora_list<BM>(p, unit.t0, list);
+      __syncthreads();
+    }
+#pragma unroll
+    for (int m = 0; m < kMT; ++m) {
+      const int t = unit.t0 + wm * (BM / 2) + m * 32 + fr;
+      const int id = unit.of_a && t < T ? p.adapter[t] : -1;
+#pragma unroll
+      for (int j = 0; j < kNT; ++j)
+#pragma unroll
+        for (int g = 0; g < 4; ++g) {
+          const int c = wn * (BN / 2) + j * 32 + 8 * g + 4 * fc;
+          f32x4 v;
+#pragma unroll
+          for (int q = 0; q < 4; ++q) v[q] = acc[j][m][4 * g + q];
+          if (!unit.of_a) {
+            if (t < T && unit.n0 + c < N)
+              *reinterpret_cast<f32x4*>(all.part + ((size_t)unit.split * T + t) * N + unit.n0 + c) = v;
+          } else {
+            const int group = unit.g0 + c / 16, r = group % per * 16 + c % 16;
+            if (t >= T || group >= groups || id != list[group / per]) continue;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) v[q] = r + q < rank ? v[q] : 0.f;
+            *reinterpret_cast<f32x4*>(all.u + ((size_t)unit.split * T + t) * pitch + r) = v;
+          }
+        }
+    }
+  }
+}
+
+void launch_lora_part_tile(const LoraPartArgs& p, unsigned grid, hipStream_t s) {
+  lora_tile_kernel<128, 128, 0, 2><<<grid, 256, 0, s>>>(p);
 }
 
 template <int BM, int BN, int OCC>
 static void run_tile(const LoraArgs& a, hipStream_t s) {
   const long blocks = lora_tile_blocks((a.sh.T + BM - 1) / BM, (a.sh.n + BN - 1) / BN);
   const unsigned grid = (unsigned)std::min(blocks, (long)kLoraCus * OCC);
-  if (a.sh.f32_out) lora_tile_kernel<BM, BN, 3, OCC><<<grid, 256, 0, s>>>(a);
-  else lora_tile_kernel<BM, BN, 2, OCC><<<grid, 256, 0, s>>>(a);
+  const LoraPartArgs p{a, 1, 0, nullptr, nullptr};
+  if (a.sh.f32_out) lora_tile_kernel<BM, BN, 3, OCC><<<grid, 256, 0, s>>>(p);
+  else lora_tile_kernel<BM, BN, 2, OCC><<<grid, 256, 0, s>>>(p);
 }
 
 hipError_t launch_lora_tile(const LoraArgs& a, hipStream_t s) {
