@@ -17,37 +17,31 @@ namespace moe {
 // ---------------------------------------------------------------------------
 // u = scale A x before the tiled product, as bf16 terms.  A block has 32 tokens and first lists the
 // different adapters among them.  An adapter is pitch / 16 groups of 16 ranks; a pass over k takes
-// G groups, of one adapter or of several, so that x is read once for a few adapters.  x and
-// A go into LDS in runs of 256 bytes of every row, ST stages, pieces at piece ^ (row % 16); of a
-// stage's 128 k each of the four waves multiplies 32, and their sums meet in LDS.
-// Bound by reading x.
+// one, two or four groups, of one adapter or of several, so that x is read once for a few
+// adapters.  x and A go into LDS in runs of 256 bytes of every row, as many stages as fit, pieces at
+// piece ^ (row % 16); of a stage's 128 k each of the four waves multiplies 32, and their sums
+// meet in LDS.  Bound by reading x.
 // ---------------------------------------------------------------------------
-template <int G, int ST>
-__global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs a) {
-  constexpr int kRows = 32, kRanks = 16 * G, kStage = (kRows + kRanks) * 256;
-  constexpr int kA = kRows * 256, L = kStage / 4096;             // 1 KB loads per wave
-  static_assert(kRanks % 16 == 0 && kStage % 4096 == 0 && 4 * kRows * kRanks * 4 <= ST * kStage, "LDS plan");
-  static_assert(ST * kStage <= 159 * 1024 && (ST - 2) * L < 64, "stages");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[ST * kStage];
+template <int LDS, int OCC>
+__global__ __launch_bounds__(256, OCC) void lora_shrink_kernel(LoraArgs a) {
+  constexpr int kRows = 32, kA = kRows * 256;
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS];
   __shared__ int list[kRows], ids[kRows];
-  const int T = a.sh.T, d = a.sh.d, rank = a.sh.rank, pitch = (rank + 15) / 16 * 16, per = pitch / 16;
+  const int T = a.sh.T, d = a.sh.d, rank = a.sh.rank, pitch = lora_pitch(rank), per = pitch / 16;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int fr = lane & 15, fc = lane >> 4, t0 = blockIdx.x * kRows;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds, row_bytes = (uint32_t)d * 2u;
-  int own = t0 + lane < T && lane < kRows ? a.adapter[t0 + lane] : -1;   // lane l: token t0 + l
-  if ((uint32_t)own >= (uint32_t)a.sh.N) own = -1;
-  if (threadIdx.x < kRows) ids[lane] = own;
-  int count = 0;
-  for (uint64_t left = __ballot(own >= 0); left; ++count) {
-    const int id = __builtin_amdgcn_readlane(own, __ffsll((unsigned long long)left) - 1);
-    left &= ~__ballot(own == id);
-    list[count] = id;                                  // every wave the same
-  }
+  if (threadIdx.x < kRows) ids[lane] = t0 + lane < T ? a.adapter[t0 + lane] : -1;
+  const int groups = lora_list<kRows>(a, t0, list) * per, nk = d / 128;
   __syncthreads();
-  const int groups = count * per, nk = d / 128;
   // Load i of a wave: four rows, of x first, then of A.
   auto row_of = [&](int i) { return (i * 4 + wave) * 4 + (lane >> 4); };
-  for (int g0 = 0; g0 < groups; g0 += G) {
+
+  // Groups g0 .. g0 + G - 1.
+  auto pass = [&](auto g_tag, int g0) {
+    constexpr int G = decltype(g_tag)::value, kRanks = 16 * G, kStage = (kRows + kRanks) * 256;
+    constexpr int L = kStage / 4096, ST = LDS / kStage;          // 1 KB loads per wave and stage; stages
+    static_assert(ST >= 3 && 4 * kRows * kRanks * 4 <= LDS && (ST - 2) * L < 64, "stages");
     const uint8_t* base[L];
     uint32_t off[L];
 #pragma unroll
@@ -125,6 +119,18 @@ __global__ __launch_bounds__(256) void lora_shrink_kernel(LoraArgs a) {
       }
     }
     __syncthreads();
+  };
+  for (int g0 = 0; g0 < groups;) {
+    if (groups - g0 == 1) {
+      pass(std::integral_constant<int, 1>(), g0);
+      ++g0;
+    } else if (groups - g0 == 2) {
+      pass(std::integral_constant<int, 2>(), g0);
+      g0 += 2;
+    } else {
+      pass(std::integral_constant<int, 4>(), g0);
+      g0 += 4;
+    }
   }
 }
 
@@ -365,36 +371,35 @@ __global__ __launch_bounds__(256, OCC) void lora_part_kernel(LoraPartArgs p) {
   }
 }
 
-// Parts of k added up in order, then bias, B u, activation: a block one token's 1024 columns, four
-// a thread.
+// Parts of k added up in order, then bias, B u, activation.  A block has 1024 columns of one token, a
+// thread every 256th of them: B's columns lie side by side, so lanes that take neighbours read
+// whole lines (four neighbours a thread read 64 lines of 128 bytes with every load: 16 us for 512 x 4096).
 __global__ __launch_bounds__(256) void lora_finish_kernel(LoraPartArgs p) {
+  constexpr int kCols = 4;
   __shared__ __attribute__((aligned(16))) float su[kLoraMaxRank];
   const LoraArgs& a = p.a;
-  const int T = a.sh.T, n = a.sh.n, rank = a.sh.rank, pitch = (rank + 15) / 16 * 16;
-  const int t = blockIdx.x, c = (blockIdx.y * 256 + threadIdx.x) * 4;
-  const int given = a.adapter[t], id = (uint32_t)given < (uint32_t)a.sh.N ? given : -1;
-  const bool in = c < n;
-  f32x4 v = in ? *reinterpret_cast<const f32x4*>(p.part + (size_t)t * n + c) : f32x4{0.f, 0.f, 0.f, 0.f};
-  u32x4 q[4][2] = {};
-  const uint16_t* b = a.b + ((size_t)max(id, 0) * n + min(c, n - 4)) * rank;
-  if (in && id >= 0) {                                 // the first 16 ranks, under way with the sums
+  const int T = a.sh.T, n = a.sh.n, rank = a.sh.rank, pitch = lora_pitch(rank);
+  const int t = blockIdx.x, c0 = blockIdx.y * 256 * kCols + threadIdx.x;
+  float v[kCols];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      q[i][0] = ld16(b + i * rank);
-      if (rank > 8) q[i][1] = ld16(b + i * rank + 8);
+  for (int i = 0; i < kCols; ++i) v[i] = p.part[(size_t)t * n + min(c0 + i * 256, n - 1)];
+  const int given = a.adapter[t], id = (uint32_t)given < (uint32_t)a.sh.N ? given : -1;
+  const uint16_t* b = a.b + (size_t)max(id, 0) * n * rank;
+  u32x4 q[kCols][2] = {};
+  if (id >= 0) {                                       // the first 16 ranks, under way with the sums
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) {
+      const uint16_t* row = b + (size_t)min(c0 + i * 256, n - 1) * rank;
+      q[i][0] = ld16(row);
+      if (rank > 8) q[i][1] = ld16(row + 8);
     }
   }
-  if (in) {
-#pragma unroll 4
-    for (int s = 1; s < p.splits; ++s) v += *reinterpret_cast<const f32x4*>(p.part + ((size_t)s * T + t) * n + c);
-    if (a.bias) {
-      const uint2 w = *reinterpret_cast<const uint2*>(a.bias + c);
-      v[0] += __uint_as_float(w.x << 16);
-      v[1] += __uint_as_float(w.x & 0xffff0000u);
-      v[2] += __uint_as_float(w.y << 16);
-      v[3] += __uint_as_float(w.y & 0xffff0000u);
-    }
-  }
+  for (int s = 1; s < p.splits; ++s)
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) v[i] += p.part[((size_t)s * T + t) * n + min(c0 + i * 256, n - 1)];
+  if (a.bias)
+#pragma unroll
+    for (int i = 0; i < kCols; ++i) v[i] += bf16_to_f32(a.bias[min(c0 + i * 256, n - 1)]);
   if (id >= 0) {
     if ((int)threadIdx.x < pitch) {
       float u = 0.f;
@@ -403,40 +408,37 @@ __global__ __launch_bounds__(256) void lora_finish_kernel(LoraPartArgs p) {
       su[threadIdx.x] = u * (a.scale ? a.scale[id] : 1.f);
     }
     __syncthreads();
-    if (in)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        float s = dot8(q[i][0], su, 0.f);
-        if (rank > 8) s = dot8(q[i][1], su + 8, s);
-        for (int r = 16; r < rank; r += 8) s = dot8(ld16(b + i * rank + r), su + r, s);
-        v[i] += s;
-      }
+    for (int i = 0; i < kCols; ++i) {
+      const uint16_t* row = b + (size_t)min(c0 + i * 256, n - 1) * rank;
+      float s = dot8(q[i][0], su, 0.f);
+      if (rank > 8) s = dot8(q[i][1], su + 8, s);
+      for (int r = 16; r < rank; r += 8) s = dot8(ld16(row + r), su + r, s);
+      v[i] += s;
+    }
   }
-  if (!in) return;
-  if (a.sh.f32_out) {
 #pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = a.sh.gelu ? gelu_erf(v[i]) : v[i];
-    *reinterpret_cast<f32x4*>(static_cast<float*>(a.y) + (size_t)t * n + c) = v;
-  } else {
-#pragma unroll
-    for (int i = 0; i < 4; ++i) v[i] = a.sh.gelu ? gelu_for_bf16(v[i]) : v[i];
-    *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.y) + (size_t)t * n + c) =
-        make_uint2(pack_bf16x2(v[0], v[1]), pack_bf16x2(v[2], v[3]));
+  for (int i = 0; i < kCols; ++i) {
+    const int c = c0 + i * 256;
+    if (c >= n) continue;
+    if (a.sh.f32_out) static_cast<float*>(a.y)[(size_t)t * n + c] = a.sh.gelu ? gelu_erf(v[i]) : v[i];
+    else static_cast<uint16_t*>(a.y)[(size_t)t * n + c] = (uint16_t)pack_bf16x2(a.sh.gelu ? gelu_for_bf16(v[i]) : v[i], 0.f);
   }
 }
 
 // ---- launches ------------------------------------------------------------------------------
 enum LoraPath { kToken, kPart, kTile };
 
-// Tokens of a part's block, and the parts that k is cut into, so that every CU has a block (the
-// tiles of 128 x 128: two).
+// Tokens of a part's block, and the parts that k is cut into, so that every CU has a block, or
+// nearly two where k is long.  96 to 512 tokens, n = 4096: d = 4096 in 256 blocks 25 to 50 us, in 448 26
+// to 52; d = 14336 50 to 125 and 43 to 116.
 static int part_rows(const LoraShape& s) { return s.T <= 32 ? 32 : s.T <= 64 ? 64 : 128; }
 static long part_tiles(const LoraShape& s) {
   const int bm = part_rows(s), bn = bm == 128 ? 128 : kPartCols;
   return (long)((s.T + bm - 1) / bm) * ((s.n + bn - 1) / bn);
 }
 static int part_splits(const LoraShape& s) {
-  const long tiles = part_tiles(s), want = part_rows(s) == 128 ? 448 : 256;
+  const long tiles = part_tiles(s), want = tiles <= 128 && s.d >= 8192 ? 448 : 256;
   // at least 128 k each, and whole runs of 256 bytes
   return (int)std::max(1L, std::min({(want + tiles / 2) / tiles, (long)s.d / 128, 16L}));
 }
@@ -456,16 +458,11 @@ size_t lora_u_bytes(const LoraShape& s) {
   }
 }
 
-// Deep stages while a CU has one block at most, two blocks a CU beyond.
+// All of a CU's LDS while it has one block at most, half of it beyond.
 static void launch_shrink(const LoraArgs& a, hipStream_t s) {
   const int tiles = (a.sh.T + 31) / 32;
-  if (a.sh.rank <= 32) {
-    if (tiles <= 256) lora_shrink_kernel<2, 9><<<tiles, 256, 0, s>>>(a);
-    else lora_shrink_kernel<2, 4><<<tiles, 256, 0, s>>>(a);
-  } else {
-    if (tiles <= 256) lora_shrink_kernel<4, 6><<<tiles, 256, 0, s>>>(a);
-    else lora_shrink_kernel<4, 3><<<tiles, 256, 0, s>>>(a);
-  }
+  if (tiles <= 256) lora_shrink_kernel<144 * 1024, 1><<<tiles, 256, 0, s>>>(a);
+  else lora_shrink_kernel<72 * 1024, 2><<<tiles, 256, 0, s>>>(a);
 }
 
 static hipError_t launch_part(const LoraArgs& a, hipStream_t s) {

@@ -29,11 +29,13 @@ namespace moe {
 
 constexpr int kLoraXcds = 8, kLoraBand = 4, kLoraCus = 256;
 
-// Tile of index i: XCD i % 8 owns 4 m-tiles of every group of 32 and walks them n-tile by
+// Tile of block b.  Whole groups of 32 m-tiles: XCD b % 8 owns 4 of them and walks them n-tile by
 // n-tile, so the blocks it runs together share their tokens in its L2 and all XCDs sweep the
-// same columns of W; leftover m-tiles are dealt round-robin.
+// same columns of W.  The m-tiles left over go in bands of 8, each n-tile by n-tile, and every XCD
+// takes one run of that order: with few tokens each W tile is read into one L2 (dealt round-robin,
+// 512 tokens, 4096 -> 14336: 124 us instead of 88).
 __device__ __forceinline__ bool lora_tile_of(int total, int ntn, int b, int& mt, int& nt) {
-  constexpr int kGroup = kLoraXcds * kLoraBand;
+  constexpr int kGroup = kLoraXcds * kLoraBand, kRest = 8;
   const int x = b % kLoraXcds, i = b / kLoraXcds;
   const int G = total / kGroup, full = G * kLoraBand * ntn, lm = total - G * kGroup;
   if (i < full) {
@@ -42,10 +44,11 @@ __device__ __forceinline__ bool lora_tile_of(int total, int ntn, int b, int& mt,
     mt = g * kGroup + x * kLoraBand + rem % kLoraBand;
     return true;
   }
-  const int u = (i - full) * kLoraXcds + x;
-  if (u >= lm * ntn) return false;
-  nt = u / lm;
-  mt = G * kGroup + u % lm;
+  const int run = (lm * ntn + kLoraXcds - 1) / kLoraXcds, j = i - full, v = x * run + j;
+  if (j >= run || v >= lm * ntn) return false;
+  const int band = v / (kRest * ntn), rem = v - band * kRest * ntn, wide = min(kRest, lm - band * kRest);
+  nt = rem / wide;
+  mt = G * kGroup + band * kRest + rem % wide;
   return true;
 }
 
@@ -60,16 +63,19 @@ __device__ __forceinline__ bool infinite_hi(uint32_t w) { return (w & 0x7f800000
 
 // TERMS: the bf16 terms of u, 2 for a bf16 result, 3 for fp32; 0: a part of the k range of W x, or
 // of A x as further columns, stored in fp32 for a finish of its own (one tile a block).
-template <int BM, int BN, int TERMS, int OCC>
+// AS: stages of x; W has one more.
+template <int BM, int BN, int TERMS, int AS, int OCC>
 __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraPartArgs all) {
   const LoraArgs& p = all.a;
-  constexpr int kA = BM * 128, kW = BN * 128, kWS = 3;             // bytes a stage; stages of W
-  constexpr int oW = 2 * kA;
+  constexpr int kA = BM * 128, kW = BN * 128, kWS = AS + 1;        // bytes a stage; stages of W
+  constexpr int oW = AS * kA;
   constexpr int kMT = BM / 64, kNT = BN / 64;                      // 32x32 tiles per wave
   constexpr int kAI = BM / 32, kWI = BN / 32;                      // 1 KB loads per wave
   constexpr bool F32 = TERMS == 3, PART = TERMS == 0;
-  static_assert(2 * kA + kWS * kW <= 160 * 1024, "LDS plan");
-  __shared__ __attribute__((aligned(1024))) uint8_t lds[2 * kA + kWS * kW];
+  // Loads that may be under way when the next step's have to be there (see the loop).
+  constexpr int kUnderWay = (AS - 1) * kWI + (AS - 2) * kAI;
+  static_assert(OCC * (AS * kA + kWS * kW) <= 160 * 1024 && (AS - 1) * (kWI + kAI) < 64, "LDS plan");
+  __shared__ __attribute__((aligned(1024))) uint8_t lds[AS * kA + kWS * kW];
 
   const int T = p.sh.T, N = p.sh.n, K = p.sh.d, nk = K / 64;
   const int ntn = (N + BN - 1) / BN, total = (T + BM - 1) / BM;
@@ -337,12 +343,13 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraPartArgs all) {
     }
   };
 
-  // Step t: its x in stage t % 2, its W in t % 3.  First half: MFMAs of the fragments at hand,
-  // reads of the step's second half, loads of W two steps on (into the stage of step t - 1, which
-  // nobody reads any more).  Then all but those have landed; barrier.  Second half: reads of
-  // the next step's first half, loads of x two steps on (every wave is done with this stage).
+  // Step t: its x in stage t % AS, its W in t % (AS + 1).  First half: MFMAs of the fragments at
+  // hand, reads of the step's second half, loads of W AS steps on (into the stage of step t - 1,
+  // which nobody reads any more).  Then the next step's x and W have landed, all but the AS - 1
+  // loads of W and AS - 2 of x after them; barrier.  Second half: reads of the next step's
+  // first half, loads of x AS steps on (every wave is done with this stage).
 #pragma unroll
-  for (int s = 0; s < 2; ++s) {
+  for (int s = 0; s < AS; ++s) {
 #pragma unroll
     for (int i = 0; i < kWI; ++i) load_w(i, s, ws);
     advance_w();
@@ -350,7 +357,7 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraPartArgs all) {
     for (int i = 0; i < kAI; ++i) load_a(i, s, as);
     advance_a();
   }
-  __builtin_amdgcn_s_waitcnt(wait_vm(0));
+  __builtin_amdgcn_s_waitcnt(wait_vm((AS - 1) * (kWI + kAI)));
   __syncthreads();
 #pragma unroll
   for (int r = 0; r < kReads; ++r) read_at(xa, xw, 0, 0, 0, r);
@@ -368,14 +375,14 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraPartArgs all) {
     bool go_on = false;
     for (int t = k0; t < k1; ++t) {
       pin();
-      const int sw1 = sw == 2 ? 0 : sw + 1, sw2 = sw == 0 ? 2 : sw - 1;
+      const int sw1 = sw == AS ? 0 : sw + 1, sw2 = sw == 0 ? AS : sw - 1, sa1 = sa == AS - 1 ? 0 : sa + 1;
       half_step(xa, xw, ya, yw, sa, sw, 1, [&](int i) { load_w(i, sw2, ws); }, LoadsW{});
       advance_w();
-      __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(kWI));
+      __builtin_amdgcn_s_waitcnt(wait_vm_lgkm0(kUnderWay));
       __syncthreads();
-      half_step(ya, yw, xa, xw, sa ^ 1, sw1, 0, [&](int i) { load_a(i, sa, as); }, LoadsA{});
+      half_step(ya, yw, xa, xw, sa1, sw1, 0, [&](int i) { load_a(i, sa, as); }, LoadsA{});
       advance_a();
-      sa ^= 1;
+      sa = sa1;
       sw = sw1;
     }
     if constexpr (PART) break;
@@ -424,7 +431,7 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraPartArgs all) {
 }
 
 void launch_lora_part_tile(const LoraPartArgs& p, unsigned grid, hipStream_t s) {
-  lora_tile_kernel<128, 128, 0, 2><<<grid, 256, 0, s>>>(p);
+  lora_tile_kernel<128, 128, 0, 2, 2><<<grid, 256, 0, s>>>(p);
 }
 
 template <int BM, int BN, int OCC>
@@ -432,8 +439,8 @@ static void run_tile(const LoraArgs& a, hipStream_t s) {
   const long blocks = lora_tile_blocks((a.sh.T + BM - 1) / BM, (a.sh.n + BN - 1) / BN);
   const unsigned grid = (unsigned)std::min(blocks, (long)kLoraCus * OCC);
   const LoraPartArgs p{a, 1, 0, nullptr, nullptr};
-  if (a.sh.f32_out) lora_tile_kernel<BM, BN, 3, OCC><<<grid, 256, 0, s>>>(p);
-  else lora_tile_kernel<BM, BN, 2, OCC><<<grid, 256, 0, s>>>(p);
+  if (a.sh.f32_out) lora_tile_kernel<BM, BN, 3, 2, OCC><<<grid, 256, 0, s>>>(p);
+  else lora_tile_kernel<BM, BN, 2, 2, OCC><<<grid, 256, 0, s>>>(p);
 }
 
 hipError_t launch_lora_tile(const LoraArgs& a, hipStream_t s) {
