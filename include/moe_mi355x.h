@@ -654,6 +654,37 @@ int moe_mx_forward(const moe_score_desc* route, const moe_mx_desc* desc, const v
                    const moe_mx_weights* w, float* y, moe_score_out* out, void* workspace,
                    size_t workspace_bytes, void* stream);
 
+/* One pre-norm sublayer: the residual add and layer norm, the shared expert with its requests'
+ * adapters (or none), and the layer of moe_mx_forward on the normed tokens, bit for bit as
+ * moe_layer_norm, moe_lora_shared_ffn and the steps of moe_mx_forward with the shared
+ * expert's output in moe_combine.
+ *   x_out = x + add,  xn = norm(x_out),  y = sum of the chosen experts' outputs + shared(xn)
+ * y [T][d] fp32 is the next sublayer's add.  x, add, x_out, norm as in moe_layer_norm (add and
+ * x_out may be NULL; x_out must not overlap x); norm->rows, norm->d, the router's and the
+ * experts' tokens and widths agree, and everything is bf16.  `out` may be NULL or any of
+ * its fields. */
+typedef struct moe_mx_block {
+  const moe_norm_desc* norm;          /* host */
+  const void* weight;                 /* [d] or NULL */
+  const void* bias;                   /* [d] or NULL */
+  const moe_score_desc* route;        /* host */
+  const void* w_router;               /* [E][d] bf16 */
+  const float* b_router;              /* [E] or NULL */
+  const float* b_select;              /* [E] or NULL */
+  const moe_mx_desc* experts;         /* host */
+  const moe_mx_weights* w;            /* host struct */
+  const moe_lora_desc* up;            /* host; the shared expert, NULL: none */
+  const moe_lora_desc* down;          /* host; NULL iff up is */
+  const moe_lora_weights* w_up;       /* host structs, read where up is given */
+  const moe_lora_weights* w_down;
+  const int32_t* adapter;             /* [T], read where up is given */
+} moe_mx_block;
+
+int moe_mx_block_workspace_size(const moe_mx_block* block, size_t* bytes);
+int moe_mx_block_forward(const moe_mx_block* block, const moe_rows* x, const moe_rows* add,
+                         const moe_rows* x_out, float* y, moe_score_out* out, void* workspace,
+                         size_t workspace_bytes, void* stream);
+
 #ifdef __cplusplus
 }
 #endif

@@ -16,6 +16,7 @@ from .binding import (ENTRY_POINTS, MOE_CAPACITY_DROP, MOE_CAPACITY_REROUTE, MOE
 from .binding import (BalanceDesc, BalanceOut, NormDesc, alloc_balance_workspace, alloc_norm_workspace, moe_balance_backward,
                       moe_balance_loss, moe_balance_workspace_size, moe_layer_norm, moe_layer_norm_backward,
                       moe_norm_workspace_size, moe_score_backward_add)
+from .binding import (MxBlock, alloc_mx_block_workspace, moe_mx_block_forward, moe_mx_block_workspace_size)
 from .binding import (LoraDesc, LoraWeights, alloc_lora_shared_workspace, alloc_lora_workspace, moe_lora_linear,
                       moe_lora_shared_ffn, moe_lora_shared_workspace_size, moe_lora_workspace_size)
 
@@ -30,5 +31,6 @@ __all__ = ["ENTRY_POINTS", "MOE_CAPACITY_DROP", "MOE_CAPACITY_REROUTE", "MOE_FFN
            "BalanceDesc", "BalanceOut", "NormDesc", "alloc_balance_workspace", "alloc_norm_workspace", "moe_balance_backward",
            "moe_balance_loss", "moe_balance_workspace_size", "moe_layer_norm", "moe_layer_norm_backward",
            "moe_norm_workspace_size", "moe_score_backward_add",
+           "MxBlock", "alloc_mx_block_workspace", "moe_mx_block_forward", "moe_mx_block_workspace_size",
            "LoraDesc", "LoraWeights", "alloc_lora_shared_workspace", "alloc_lora_workspace", "moe_lora_linear",
            "moe_lora_shared_ffn", "moe_lora_shared_workspace_size", "moe_lora_workspace_size"]

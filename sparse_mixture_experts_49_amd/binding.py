@@ -37,7 +37,8 @@ ENTRY_POINTS = ("moe_status_string", "moe_last_error", "moe_workspace_size", "mo
                 "moe_score_backward_add", "moe_balance_workspace_size", "moe_balance_loss",
                 "moe_balance_backward", "moe_norm_workspace_size", "moe_layer_norm",
                 "moe_layer_norm_backward", "moe_lora_workspace_size", "moe_lora_linear",
-                "moe_lora_shared_workspace_size", "moe_lora_shared_ffn")
+                "moe_lora_shared_workspace_size", "moe_lora_shared_ffn", "moe_mx_block_workspace_size",
+                "moe_mx_block_forward")
 
 
 class MoeError(RuntimeError):
@@ -117,6 +118,12 @@ class CLoraWeights(ctypes.Structure):
     _fields_ = [(n, ctypes.c_void_p) for n in ("w", "a", "b", "scale", "bias")]
 
 
+class CMxBlock(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_void_p) for n in
+                ("norm", "weight", "bias", "route", "w_router", "b_router", "b_select", "experts", "w", "up", "down",
+                 "w_up", "w_down", "adapter")]
+
+
 class CRows(ctypes.Structure):
     _fields_ = [("data", ctypes.c_void_p), ("stride", ctypes.c_int64)]
 
@@ -165,6 +172,8 @@ def load_library(path: str = LIB_PATH) -> ctypes.CDLL:
         "moe_lora_linear": (I, [P, P, P, P, P, P, S, P]),
         "moe_lora_shared_workspace_size": (I, [P, P, ctypes.POINTER(S)]),
         "moe_lora_shared_ffn": (I, [P, P, P, P, P, P, P, P, S, P]),
+        "moe_mx_block_workspace_size": (I, [P, ctypes.POINTER(S)]),
+        "moe_mx_block_forward": (I, [P, P, P, P, P, P, P, S, P]),
         "moe_mx_quantize": (I, [P, I, L, L, L, P, P, P]),
         "moe_mx_dequantize": (I, [P, P, L, L, I, P, L, P]),
         "moe_mx_workspace_size": (I, [P, ctypes.POINTER(S)]),
@@ -1088,3 +1097,73 @@ def moe_mx_forward(route: ScoreDesc, desc: MxDesc, x, w_router, weights: MxWeigh
           c.t(x, "x", bf, T * D), c.t(w_router, "w_router", bf, E * D), c.t(b_router, "b_router", f32, E),
           c.t(b_select, "b_select", f32, E), ctypes.byref(_mx_weights(c, desc, weights, True, True)),
           c.t(y, "y", f32, T * D), out, ws, nb, stream=stream)
+
+
+@dataclasses.dataclass
+class MxBlock:
+    """One pre-norm sublayer (moe_mx_block): norm, router, MXFP4 experts, and the shared expert
+    with its requests' adapters (up, down, w_up, w_down, adapter) or none."""
+    norm: NormDesc
+    route: ScoreDesc
+    experts: MxDesc
+    w_router: torch.Tensor
+    weights: MxWeights
+    weight: Optional[torch.Tensor] = None
+    bias: Optional[torch.Tensor] = None
+    b_router: Optional[torch.Tensor] = None
+    b_select: Optional[torch.Tensor] = None
+    up: Optional[LoraDesc] = None
+    down: Optional[LoraDesc] = None
+    w_up: Optional[LoraWeights] = None
+    w_down: Optional[LoraWeights] = None
+
+
+def _mx_block(block: MxBlock, c: Optional[_Call], adapter):
+    """The C struct and what it points to; without a call only the descriptors."""
+    def at(s):
+        return None if s is None else ctypes.cast(ctypes.pointer(s), ctypes.c_void_p)
+
+    b, f32, bf = block, torch.float32, torch.bfloat16
+    up, down = (None if d is None else d.to_c() for d in (b.up, b.down))
+    keep = [b.norm.to_c(), b.route.to_c(), b.experts.to_c(), up, down]
+    s = CMxBlock(norm=at(keep[0]), route=at(keep[1]), experts=at(keep[2]), up=at(up), down=at(down))
+    if c is not None:
+        d, E, pt = b.norm.d, b.route.n_experts, _torch_dtype(b.norm.param_dtype)
+        s.weight, s.bias = c.t(b.weight, "weight", pt, d), c.t(b.bias, "bias", pt, d)
+        s.w_router = c.t(b.w_router, "w_router", bf, E * d)
+        s.b_router, s.b_select = c.t(b.b_router, "b_router", f32, E), c.t(b.b_select, "b_select", f32, E)
+        keep.append(_mx_weights(c, b.experts, b.weights, True, True))
+        s.w = at(keep[-1])
+        if b.up is not None and b.down is not None:
+            if b.w_up is None or b.w_down is None:
+                raise MoeError(MOE_ERR_INVALID, "w_up and w_down must not be None")
+            keep += [_lora_weights(c, b.up, b.w_up), _lora_weights(c, b.down, b.w_down)]
+            s.w_up, s.w_down = at(keep[-2]), at(keep[-1])
+            s.adapter = c.t(adapter, "adapter", torch.int32, b.up.tokens)
+    return s, keep
+
+
+def moe_mx_block_workspace_size(block: MxBlock) -> int:
+    n = ctypes.c_size_t(0)
+    s, _keep = _mx_block(block, None, None)
+    _check(load_library().moe_mx_block_workspace_size(ctypes.byref(s), ctypes.byref(n)))
+    return n.value
+
+
+def alloc_mx_block_workspace(block: MxBlock, device) -> torch.Tensor:
+    return torch.empty(moe_mx_block_workspace_size(block), dtype=torch.uint8, device=device)
+
+
+def moe_mx_block_forward(block: MxBlock, x, y, add=None, x_out=None, adapter=None, routing=None, workspace=None,
+                         stream=None):
+    """x_out = x + add, its norm, and y = the experts' and the shared expert's output on it (fp32
+    [T, d], the next block's add)."""
+    c = _Call(x, "x")
+    n = block.norm
+    ws, nb = c.ws(workspace, lambda: moe_mx_block_workspace_size(block), stream)
+    s, _keep = _mx_block(block, c, adapter)
+    out = ctypes.byref(_score_out(c, block.route, routing)) if routing is not None else None
+    dt = _torch_dtype(n.dtype)
+    c.run(load_library().moe_mx_block_forward, ctypes.byref(s), _norm_rows(c, x, "x", dt, n),
+          _norm_rows(c, add, "add", _torch_dtype(n.add_dtype), n), _norm_rows(c, x_out, "x_out", dt, n),
+          c.t(y, "y", torch.float32, n.rows * n.d), out, ws, nb, stream=stream)

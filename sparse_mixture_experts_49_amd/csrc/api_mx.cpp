@@ -164,6 +164,80 @@ size_t rows_bytes(int dtype, int64_t rows, int64_t cols, int64_t stride) {
   return rows ? ((size_t)(rows - 1) * stride + cols) * (dtype == MOE_DTYPE_BF16 ? 2 : 4) : 0;
 }
 
+// The layer on tokens x, its workspace carved as L with the router's behind it; shared [T][d] fp32
+// or null is added to y.
+int run_layer(const moe_score_desc* route, const moe_mx_desc* desc, const void* x, const void* w_router,
+              const float* b_router, const float* b_select, const moe_mx_weights* w, const float* shared, float* y,
+              moe_score_out r, void* ws, const MxLayout& L, size_t route_bytes, void* stream) {
+  if (!r.topk_idx) r.topk_idx = at<int32_t>(ws, L.topk_idx);
+  if (!r.topk_w) r.topk_w = at<float>(ws, L.topk_w);
+  hipStream_t s = static_cast<hipStream_t>(stream);
+  int32_t *counts = at<int32_t>(ws, L.counts), *offsets = at<int32_t>(ws, L.offsets),
+          *dest = at<int32_t>(ws, L.dest), *src = at<int32_t>(ws, L.src);
+  void* h = at<void>(ws, L.h);
+  float* o = at<float>(ws, L.o);
+  if (int st = moe_score_route(route, x, w_router, b_router, b_select, &r, at<void>(ws, L.total),
+                               route_bytes, stream))
+    return st;
+  if (int st = launch_dispatch(desc, r.topk_idx, counts, offsets, dest, src, ws, L, s)) return st;
+  if (int st = launch_product(desc, true, x, src, offsets, w, h, ws, L, s)) return st;
+  if (int st = launch_product(desc, false, h, nullptr, offsets, w, o, ws, L, s)) return st;
+  moe::CombineArgs c{};
+  c.o = o;
+  c.dest = dest;
+  c.topk_w = r.topk_w;
+  c.shared = shared;
+  c.y = y;
+  c.T = desc->tokens;
+  c.d = desc->d_model;
+  c.k = desc->top_k;
+  return hip_status(moe::launch_combine(c, s), "combine launch");
+}
+
+// Routing, experts and shared expert of a block agree in tokens and width; where its workspace's
+// parts begin.
+struct BlockLayout {
+  size_t xn, shared, lora, layer, total;
+  size_t route_bytes, lora_bytes;
+};
+
+int validate_pairing(const moe_score_desc* route, const moe_mx_desc* desc) {
+  if (route->tokens != desc->tokens || route->d_model != desc->d_model || route->n_experts != desc->n_experts ||
+      route->top_k != desc->top_k)
+    return fail(MOE_ERR_INVALID, "route and desc differ in tokens, d_model, n_experts or top_k");
+  if (route->dtype != MOE_DTYPE_BF16)
+    return fail(MOE_ERR_UNSUPPORTED, "moe_mx_forward takes bf16 tokens (route->dtype)");
+  return MOE_OK;
+}
+
+int validate_block(const moe_mx_block* b, BlockLayout& B) {
+  B = BlockLayout{};
+  if (!b) return fail(MOE_ERR_INVALID, "block must not be NULL");
+  size_t bytes = 0;
+  if (int st = moe_norm_workspace_size(b->norm, &bytes)) return st;
+  if (int st = moe_score_workspace_size(b->route, &B.route_bytes)) return st;
+  if (int st = validate_mx(b->experts)) return st;
+  if (int st = validate_pairing(b->route, b->experts)) return st;
+  if (b->norm->rows != b->experts->tokens || b->norm->d != b->experts->d_model)
+    return fail(MOE_ERR_INVALID, "norm and experts differ in tokens or d_model");
+  if (b->norm->dtype != MOE_DTYPE_BF16) return fail(MOE_ERR_UNSUPPORTED, "norm->dtype must be MOE_DTYPE_BF16");
+  if (!b->up != !b->down) return fail(MOE_ERR_INVALID, "up and down must both be given, or neither");
+  const size_t T = b->experts->tokens, D = b->experts->d_model;
+  size_t p = 0;
+  auto take = [&](size_t n) { size_t at = p; p += up256(n); return at; };
+  B.xn = take(T * D * 2);
+  if (b->up) {
+    if (int st = moe_lora_shared_workspace_size(b->up, b->down, &B.lora_bytes)) return st;
+    if (b->up->tokens != b->experts->tokens || b->up->d_in != b->experts->d_model)
+      return fail(MOE_ERR_INVALID, "up and experts differ in tokens or d_model");
+    B.shared = take(T * D * 4);
+    B.lora = take(B.lora_bytes);
+  }
+  B.layer = take(layout_of(b->experts).total + B.route_bytes);
+  B.total = p;
+  return MOE_OK;
+}
+
 }  // namespace
 
 extern "C" {
@@ -291,11 +365,7 @@ int moe_mx_forward(const moe_score_desc* route, const moe_mx_desc* desc, const v
   size_t route_bytes = 0;
   if (int st = moe_score_workspace_size(route, &route_bytes)) return st;
   if (int st = validate_mx(desc)) return st;
-  if (route->tokens != desc->tokens || route->d_model != desc->d_model ||
-      route->n_experts != desc->n_experts || route->top_k != desc->top_k)
-    return fail(MOE_ERR_INVALID, "route and desc differ in tokens, d_model, n_experts or top_k");
-  if (route->dtype != MOE_DTYPE_BF16)
-    return fail(MOE_ERR_UNSUPPORTED, "moe_mx_forward takes bf16 tokens (route->dtype)");
+  if (int st = validate_pairing(route, desc)) return st;
   MOE_REQUIRE_PTR(x, "x");
   MOE_REQUIRE_PTR(y, "y");
   if (int st = validate_weights(desc, w, true, true)) return st;
@@ -324,28 +394,121 @@ int moe_mx_forward(const moe_score_desc* route, const moe_mx_desc* desc, const v
     add_weights(in, desc, w, true, true);
     if (int st = check_alias(o, in)) return st;
   }
-  if (!r.topk_idx) r.topk_idx = at<int32_t>(ws, L.topk_idx);
-  if (!r.topk_w) r.topk_w = at<float>(ws, L.topk_w);
-  hipStream_t s = static_cast<hipStream_t>(stream);
-  int32_t *counts = at<int32_t>(ws, L.counts), *offsets = at<int32_t>(ws, L.offsets),
-          *dest = at<int32_t>(ws, L.dest), *src = at<int32_t>(ws, L.src);
-  void* h = at<void>(ws, L.h);
-  float* o = at<float>(ws, L.o);
-  if (int st = moe_score_route(route, x, w_router, b_router, b_select, &r, at<void>(ws, L.total),
-                               route_bytes, stream))
-    return st;
-  if (int st = launch_dispatch(desc, r.topk_idx, counts, offsets, dest, src, ws, L, s)) return st;
-  if (int st = launch_product(desc, true, x, src, offsets, w, h, ws, L, s)) return st;
-  if (int st = launch_product(desc, false, h, nullptr, offsets, w, o, ws, L, s)) return st;
-  moe::CombineArgs c{};
-  c.o = o;
-  c.dest = dest;
-  c.topk_w = r.topk_w;
-  c.y = y;
-  c.T = desc->tokens;
-  c.d = desc->d_model;
-  c.k = desc->top_k;
-  return hip_status(moe::launch_combine(c, s), "combine launch");
+  return run_layer(route, desc, x, w_router, b_router, b_select, w, nullptr, y, r, ws, L, route_bytes, stream);
+}
+
+int moe_mx_block_workspace_size(const moe_mx_block* block, size_t* bytes) {
+  BlockLayout B;
+  if (int st = validate_block(block, B)) return st;
+  if (!bytes) return fail(MOE_ERR_INVALID, "bytes must not be NULL");
+  *bytes = B.total;
+  return ok();
+}
+
+int moe_mx_block_forward(const moe_mx_block* block, const moe_rows* x, const moe_rows* add, const moe_rows* x_out,
+                         float* y, moe_score_out* out, void* ws, size_t ws_bytes, void* stream) {
+  BlockLayout B;
+  if (int st = validate_block(block, B)) return st;
+  const moe_mx_block& b = *block;
+  const moe_mx_desc* desc = b.experts;
+  const size_t T = desc->tokens, D = desc->d_model, E = desc->n_experts;
+  // Everything is checked before the first launch: no call below then finds a fault.
+  auto rows = [&](const moe_rows* r, const char* name, bool needed) -> int {
+    if (!r || !r->data) return needed ? fail(MOE_ERR_INVALID, "%s must not be NULL", name) : MOE_OK;
+    if (!aligned16(r->data)) return fail(MOE_ERR_INVALID, "%s must be 16-byte aligned", name);
+    if (T > 1 && r->stride < (int64_t)D) return fail(MOE_ERR_INVALID, "%s: stride must be >= d", name);
+    if (T > 1 && r->stride > (int64_t(1) << 40) / (int64_t)T)
+      return fail(MOE_ERR_UNSUPPORTED, "%s: rows * stride must be <= 2^40", name);
+    return MOE_OK;
+  };
+  if (int st = rows(x, "x", true)) return st;
+  if (int st = rows(add, "add", false)) return st;
+  if (int st = rows(x_out, "x_out", false)) return st;
+  MOE_OPTIONAL_PTR(b.weight, "weight");
+  MOE_OPTIONAL_PTR(b.bias, "bias");
+  MOE_REQUIRE_PTR(b.w_router, "w_router");
+  MOE_OPTIONAL_PTR(b.b_router, "b_router");
+  MOE_OPTIONAL_PTR(b.b_select, "b_select");
+  if (int st = validate_weights(desc, b.w, true, true)) return st;
+  MOE_REQUIRE_PTR(y, "y");
+  moe_score_out r{};
+  if (out) r = *out;
+  MOE_OPTIONAL_PTR(r.topk_idx, "out->topk_idx");
+  MOE_OPTIONAL_PTR(r.topk_w, "out->topk_w");
+  MOE_OPTIONAL_PTR(r.logits, "out->logits");
+  MOE_OPTIONAL_PTR(r.load, "out->load");
+  MOE_OPTIONAL_PTR(r.prob_mean, "out->prob_mean");
+  MOE_OPTIONAL_PTR(r.aux, "out->aux");
+  MOE_OPTIONAL_PTR(r.z_loss, "out->z_loss");
+  if (b.up) {
+    MOE_REQUIRE_PTR(b.adapter, "adapter");
+    const moe_lora_weights* both[2] = {b.w_up, b.w_down};
+    const moe_lora_desc* of[2] = {b.up, b.down};
+    for (int i = 0; i < 2; ++i) {
+      const moe_lora_weights* w = both[i];
+      if (!w) return fail(MOE_ERR_INVALID, "w_up and w_down must not be NULL");
+      MOE_REQUIRE_PTR(w->w, "w");
+      MOE_REQUIRE_PTR(w->a, "a");
+      MOE_REQUIRE_PTR(w->b, "b");
+      MOE_OPTIONAL_PTR(w->scale, "scale");
+      if (of[i]->has_bias) MOE_REQUIRE_PTR(w->bias, "bias");
+      if (!of[i]->has_bias && w->bias) return fail(MOE_ERR_INVALID, "bias given but has_bias == 0");
+    }
+  }
+  if (!ws) return fail(MOE_ERR_WORKSPACE, "workspace must not be NULL");
+  if ((reinterpret_cast<uintptr_t>(ws) & 255u) != 0)
+    return fail(MOE_ERR_WORKSPACE, "workspace must be 256-byte aligned");
+  if (ws_bytes < B.total) return fail(MOE_ERR_WORKSPACE, "workspace has %zu bytes, needs %zu", ws_bytes, B.total);
+  {
+    auto reach = [&](const moe_rows* m, size_t e) { return m && m->data ? (T - 1) * (size_t)m->stride * e + D * e : 0; };
+    auto data = [](const moe_rows* m) -> const void* { return m ? m->data : nullptr; };
+    const size_t pe = b.norm->param_dtype == MOE_DTYPE_BF16 ? 2 : 4, ae = b.norm->add_dtype == MOE_DTYPE_BF16 ? 2 : 4;
+    Spans o, in;
+    o.add(y, T * D * 4, "y");
+    o.add(data(x_out), T > 1 ? reach(x_out, 2) : D * 2, "x_out");
+    o.add(r.topk_idx, T * desc->top_k * 4, "topk_idx");
+    o.add(r.topk_w, T * desc->top_k * 4, "topk_w");
+    o.add(r.logits, T * E * 4, "logits");
+    o.add(r.load, E * 4, "load");
+    o.add(r.prob_mean, E * 4, "prob_mean");
+    o.add(r.aux, 4, "aux");
+    o.add(r.z_loss, 4, "z_loss");
+    o.add(ws, ws_bytes, "workspace");
+    in.add(data(x), T > 1 ? reach(x, 2) : D * 2, "x");
+    in.add(data(add), T > 1 ? reach(add, ae) : D * ae, "add");
+    in.add(b.weight, D * pe, "weight");
+    in.add(b.bias, D * pe, "bias");
+    in.add(b.w_router, E * D * 2, "w_router");
+    in.add(b.b_router, E * 4, "b_router");
+    in.add(b.b_select, E * 4, "b_select");
+    add_weights(in, desc, b.w, true, true);
+    if (b.up) {
+      in.add(b.adapter, T * 4, "adapter");
+      const moe_lora_weights* both[2] = {b.w_up, b.w_down};
+      const moe_lora_desc* of[2] = {b.up, b.down};
+      for (int i = 0; i < 2; ++i) {
+        const size_t N = of[i]->n_adapters, rank = of[i]->rank, n = of[i]->d_out, k = of[i]->d_in;
+        in.add(both[i]->w, n * k * 2, "w");
+        in.add(both[i]->bias, n * 2, "bias");
+        in.add(both[i]->a, N * rank * k * 2, "a");
+        in.add(both[i]->b, N * rank * n * 2, "b");
+        in.add(both[i]->scale, N * 4, "scale");
+      }
+    }
+    if (int st = check_alias(o, in)) return st;
+  }
+  void* xn = at<void>(ws, B.xn);
+  const moe_rows normed{xn, (int64_t)D};
+  if (int st = moe_layer_norm(b.norm, x, add, b.weight, b.bias, x_out, &normed, nullptr, nullptr, stream)) return st;
+  float* shared = nullptr;
+  if (b.up) {
+    shared = at<float>(ws, B.shared);
+    if (int st = moe_lora_shared_ffn(b.up, b.down, xn, b.adapter, b.w_up, b.w_down, shared, at<void>(ws, B.lora),
+                                     B.lora_bytes, stream))
+      return st;
+  }
+  return run_layer(b.route, desc, xn, b.w_router, b.b_router, b.b_select, b.w, shared, y, r, at<void>(ws, B.layer),
+                   layout_of(desc), B.route_bytes, stream);
 }
 
 }  // extern "C"
