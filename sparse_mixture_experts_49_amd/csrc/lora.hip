@@ -145,12 +145,12 @@ __device__ __forceinline__ float dot8(const u32x4& q, const float* u, float s) {
 }
 // ---------------------------------------------------------------------------
 // One token, bound by the bytes of W and by latency.  Every block works out u itself (A is read from
-// memory once and then from L2), so one launch does all.  A wave takes whole rows, first its
-// eighth of A's, then of W, in runs of 1 KB, P runs a set, three sets under way; x lies in LDS.
-// Lane l brings in rank l's share of B u before the lanes' sums meet.  Products by the 4x4x4 MFMA: it
+// memory once and then from L2), so one launch does all.  A wave takes whole rows, first of W, then
+// its eighth of A's, in runs of 1 KB, P runs a set, three sets under way; x lies in LDS.  Lane j keeps
+// the sum of the wave's j-th row of W and finishes it once u is there.  Products by the 4x4x4 MFMA: it
 // multiplies four values of every lane of four with four of each of them, and the lane's own
-// with its own is the one that is kept (16 cycles for 8 values; converting and
-// multiplying them takes 96).
+// with its own is the one that is kept (16 cycles for 8 values; converting and multiplying
+// them takes 96).
 // ---------------------------------------------------------------------------
 typedef short i16x4 __attribute__((ext_vector_type(4)));
 // Lane l's four values (two words) of each operand: column l % 4 of the result's 4x4 block l / 4,
@@ -167,56 +167,42 @@ template <int P>
 __global__ __launch_bounds__(kTokenWaves * 64, 2) void lora_token_kernel(LoraArgs a) {
   constexpr int kSets = 3;
   __shared__ __attribute__((aligned(16))) uint16_t sx[kTokenMaxWidth];
-  __shared__ float su[kTokenMaxRank];
+  __shared__ __attribute__((aligned(16))) float su[kTokenMaxRank];
   const int d = a.sh.d, n = a.sh.n, rank = a.sh.rank;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int first = blockIdx.x * kTokenWaves + wave, stride = gridDim.x * kTokenWaves;   // rows of W
   const int segs = (d + P * 512 - 1) / (P * 512);
-  const int of_a = rank / kTokenWaves * segs;          // sets of A's rows (rank is a multiple of 8)
-  const int total = of_a + (first < n ? ((n - 1 - first) / stride + 1) * segs : 0);
-  const int lane_rank = min(lane, rank - 1);
+  const int of_w = first < n ? ((n - 1 - first) / stride + 1) * segs : 0;   // sets of W's rows
+  const int total = of_w + rank / kTokenWaves * segs;  // and of A's (rank is a multiple of 8)
   const int turn = (wave + blockIdx.x / 8) % kTokenWaves;   // blocks of an XCD read different rows of A at a time
-  u32x4 v[kSets][P];
-  uint16_t vb[kSets], vbias[kSets];                    // the row's B of the lane's rank, its bias
-  // Set i: lane l has values 512 q + 8 l .. + 7 of its runs q; past the row's end any of its values.
-  // Past the last set that one again, not used.
-  auto load_row = [&](int slot, const uint16_t* p, int s) {
-#pragma unroll
-    for (int q = 0; q < P; ++q) v[slot][q] = ld16(p + min((s * P + q) * 512 + lane * 8, d - 8));
-  };
-  auto row_of = [&](int i) { return min(first + (i - of_a) / segs * stride, n - 1); };
-  // W's first rows, before anything that has to wait for the adapter's number.
-#pragma unroll
-  for (int q = 0; q < kSets; ++q)
-    if (q >= of_a) load_row(q, a.w + (size_t)row_of(q) * d, (q - of_a) % segs);
   const int given = a.adapter[0], id = (uint32_t)given < (uint32_t)a.sh.N ? given : -1;
   const int any = max(id, 0);                          // without an adapter A and B are read, not used
   const uint16_t* rows_a = a.a + ((size_t)any * rank + turn) * d;
-  const float scale = a.scale ? a.scale[any] : 1.f;
-  auto load_ends = [&](int slot, int i) {
-    const int row = i >= of_a ? row_of(i) : 0;
-    vb[slot] = a.b[((size_t)any * n + row) * rank + lane_rank];
-    vbias[slot] = a.bias ? a.bias[row] : (uint16_t)0;
-  };
+  u32x4 v[kSets][P];
+  // Set i: lane l has values 512 q + 8 l .. + 7 of its runs q; past the row's end any of its values.
+  // Past the last set that one again, not used.
   auto load = [&](int slot, int i) {
-    i = max(min(i, total - 1), 0);
-    const bool w = i >= of_a;
-    const int j = w ? i - of_a : i;
-    load_row(slot, w ? a.w + (size_t)row_of(i) * d : rows_a + (size_t)(j / segs) * kTokenWaves * d, j % segs);
-    load_ends(slot, i);
+    i = min(i, total - 1);
+    const bool w = i < of_w;
+    const int j = w ? i : i - of_w, s = j % segs;
+    const uint16_t* p = w ? a.w + (size_t)(first + j / segs * stride) * d : rows_a + (size_t)(j / segs) * kTokenWaves * d;
+#pragma unroll
+    for (int q = 0; q < P; ++q) v[slot][q] = ld16(p + min((s * P + q) * 512 + lane * 8, d - 8));
   };
 #pragma unroll
-  for (int q = 0; q < kSets; ++q) {
-    if (q < of_a) load(q, q);
-    else load_ends(q, q);
-  }
+  for (int q = 0; q < kSets; ++q) load(q, q);
   for (int i = threadIdx.x * 8; i < d; i += kTokenWaves * 64 * 8) st16(sx + i, ld16(a.x + i));
+  // The lane's own row: 16 ranks of its B, its bias; and the scale.
+  const int row = min(first + lane * stride, n - 1);
+  const uint16_t* b = a.b + ((size_t)any * n + row) * rank;
+  const u32x4 b0 = ld16(b), b1 = rank > 8 ? ld16(b + 8) : u32x4{0, 0, 0, 0};
+  const float bias = a.bias ? bf16_to_f32(a.bias[row]) : 0.f, scale = a.scale ? a.scale[any] : 1.f;
   __syncthreads();
   f32x4 acc = {0.f, 0.f, 0.f, 0.f};
+  float mine = 0.f;
   auto use = [&](int slot, int i) {
-    if (i == of_a) __syncthreads();                    // every wave's u is there
-    const bool w = i >= of_a;
-    const int j = w ? i - of_a : i, s = j % segs;
+    const bool w = i < of_w;
+    const int j = w ? i : i - of_w, s = j % segs;
 #pragma unroll
     for (int q = 0; q < P; ++q) {
       const int k = (s * P + q) * 512 + lane * 8;
@@ -226,19 +212,9 @@ __global__ __launch_bounds__(kTokenWaves * 64, 2) void lora_token_kernel(LoraArg
     }
     if (s + 1 < segs) return;
     const int own = lane & 3;
-    float sum = own == 0 ? acc[0] : own == 1 ? acc[1] : own == 2 ? acc[2] : acc[3];
-    if (!w) {
-      sum = wave_sum_f(sum) * scale;
-      if (lane == 0) su[j / segs * kTokenWaves + turn] = sum;
-    } else {
-      if (id >= 0 && lane < rank) sum = fmaf(bf16_to_f32(vb[slot]), su[lane], sum);
-      sum = wave_sum_f(sum) + bf16_to_f32(vbias[slot]);
-      const int row = first + j / segs * stride;
-      if (lane == 0) {
-        if (a.sh.f32_out) static_cast<float*>(a.y)[row] = a.sh.gelu ? gelu_erf(sum) : sum;
-        else static_cast<uint16_t*>(a.y)[row] = (uint16_t)pack_bf16x2(a.sh.gelu ? gelu_for_bf16(sum) : sum, 0.f);
-      }
-    }
+    const float sum = wave_sum_f(own == 0 ? acc[0] : own == 1 ? acc[1] : own == 2 ? acc[2] : acc[3]);
+    if (w) mine = lane == j / segs ? sum : mine;
+    else if (lane == 0) su[j / segs * kTokenWaves + turn] = sum * scale;
     acc = f32x4{0.f, 0.f, 0.f, 0.f};
   };
   for (int i = 0; i < total; i += kSets) {
@@ -248,7 +224,17 @@ __global__ __launch_bounds__(kTokenWaves * 64, 2) void lora_token_kernel(LoraArg
       load(q, i + q + kSets);
     }
   }
-  if (total == of_a) __syncthreads();                  // no row of W: the barrier all the same
+  __syncthreads();
+  if (first + lane * stride >= n) return;
+  float sum = mine + bias;
+  if (id >= 0) {
+    float s = dot8(b0, su, 0.f);
+    if (rank > 8) s = dot8(b1, su + 8, s);
+    for (int r = 16; r < rank; r += 8) s = dot8(ld16(b + r), su + r, s);
+    sum += s;
+  }
+  if (a.sh.f32_out) static_cast<float*>(a.y)[row] = a.sh.gelu ? gelu_erf(sum) : sum;
+  else static_cast<uint16_t*>(a.y)[row] = (uint16_t)pack_bf16x2(a.sh.gelu ? gelu_for_bf16(sum) : sum, 0.f);
 }
 
 // ---------------------------------------------------------------------------
@@ -444,7 +430,9 @@ static int part_splits(const LoraShape& s) {
 }
 
 static LoraPath path_of(const LoraShape& s) {
-  if (s.T == 1 && s.rank <= kTokenMaxRank && (long)s.rank * s.d <= 128 * 1024 && s.d <= kTokenMaxWidth) return kToken;
+  if (s.T == 1 && s.rank <= kTokenMaxRank && (long)s.rank * s.d <= 128 * 1024 && s.d <= kTokenMaxWidth &&
+      s.n <= 64 * 256 * kTokenWaves)                   // a lane for every row of a wave
+    return kToken;
   // Tiles need four steps of 64 k: their loads run two ahead, into the next tile only.
   return s.T > 128 && s.d >= 256 && part_splits(s) == 1 ? kTile : kPart;
 }
