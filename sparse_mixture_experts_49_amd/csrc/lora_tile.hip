@@ -373,6 +373,7 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraPartArgs all) {
         for (int q = 0; q < 16; ++q) acc[j][m][q] = 0.f;
     const Where done = cur;
     bool go_on = false;
+    if constexpr (!PART) load_ids(cur);
     for (int t = k0; t < k1; ++t) {
       pin();
       const int sw1 = sw == AS ? 0 : sw + 1, sw2 = sw == 0 ? AS : sw - 1, sa1 = sa == AS - 1 ? 0 : sa + 1;
@@ -387,7 +388,6 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraPartArgs all) {
     }
     if constexpr (PART) break;
     go_on = next.r0 != cur.r0 || next.n0 != cur.n0;
-    load_ids(done);
     expand(done);
     finish(done);
     if (!go_on) break;
