@@ -622,8 +622,7 @@ class _Call:
             return None
         if not isinstance(t, torch.Tensor):
             raise MoeError(MOE_ERR_INVALID, f"{name} must be a torch tensor or None")
-        if not (t.is_cuda and t.get_device() == self.index and t.dtype is dtype and t.numel() >= numel
-                and t.is_contiguous()):
+        if not (t.get_device() == self.index and t.dtype is dtype and t.numel() >= numel and t.is_contiguous()):
             check_tensor(t, name, dtype, numel, self.device)
         return t.data_ptr()
 
@@ -831,19 +830,16 @@ def _norm_rows(c: _Call, t, name, dtype, d: NormDesc):
         return None
     if not isinstance(t, torch.Tensor):
         raise MoeError(MOE_ERR_INVALID, f"{name} must be a torch tensor or None")
-    if not (t.is_cuda and t.get_device() == c.index and t.dtype is dtype):
+    if not (t.get_device() == c.index and t.dtype is dtype):
         check_tensor(t, name, dtype, 0, c.device)
+    shape, strides = t.shape, t.stride()
+    if len(shape) == 2 and shape[0] == d.rows and shape[1] == d.d and (strides[1] == 1 or d.d == 1):
+        return ctypes.byref(CRows(t.data_ptr(), strides[0]))
     if t.dim() < 1 or t.shape[-1] != d.d or t.numel() != d.rows * d.d:
         raise MoeError(MOE_ERR_INVALID, f"{name} has shape {tuple(t.shape)}, expected [{d.rows}, {d.d}]")
-    if t.dim() != 2:
-        if not t.is_contiguous():
-            raise MoeError(MOE_ERR_INVALID, f"{name} must be contiguous, or a matrix with contiguous rows")
-        stride = d.d
-    else:
-        stride, inner = t.stride()
-        if d.d > 1 and inner != 1:
-            raise MoeError(MOE_ERR_INVALID, f"{name} must have contiguous rows")
-    return ctypes.byref(CRows(t.data_ptr(), stride))
+    if not t.is_contiguous():
+        raise MoeError(MOE_ERR_INVALID, f"{name} must be contiguous, or a matrix with contiguous rows")
+    return ctypes.byref(CRows(t.data_ptr(), d.d))
 
 
 def moe_layer_norm(desc: NormDesc, x, y, weight=None, bias=None, add=None, x_out=None, mean=None, rstd=None,
