@@ -27,40 +27,11 @@
 
 namespace moe {
 
-// Tokens a run has: short runs while there are fewer than 1024 of them, then longer ones.
-static int chunk_of(int T) { return T <= 16 * 1024 ? 16 : (T + 1023) / 1024; }
+// Tokens a run has: short runs while there are fewer than 1024 of them, then longer ones, of 512 at
+// most, so that a lane's fp32 sum stays short.
+static int chunk_of(int T) { return T <= 16 * 1024 ? 16 : std::min(512, (T + 1023) / 1024); }
 int balance_chunks(const BalanceShape& s) { const int c = chunk_of(s.T); return (s.T + c - 1) / c; }
 int balance_blocks(int E) { return (E + 63) / 64; }
-
-// ---- sums over the L lanes of a token, in all of them --------------------------------------
-template <int CTRL>
-__device__ __forceinline__ float dpp(float v) {
-  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
-}
-template <int L, typename F>
-__device__ __forceinline__ float across(float v, F f) {
-  if constexpr (L >= 2) v = f(v, dpp<0xB1>(v));      // quad [1,0,3,2]
-  if constexpr (L >= 4) v = f(v, dpp<0x4E>(v));      // quad [2,3,0,1]
-  if constexpr (L >= 8) v = f(v, dpp<0x141>(v));     // half-row mirror
-  if constexpr (L >= 16) v = f(v, dpp<0x140>(v));    // row mirror
-  if constexpr (L >= 32) {                           // neighbouring rows of 16, then halves
-    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
-  }
-  if constexpr (L >= 64) {
-    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
-    v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
-  }
-  return v;
-}
-template <int L>
-__device__ __forceinline__ float sum_of(float v) {
-  return across<L>(v, [](float a, float b) { return a + b; });
-}
-template <int L>
-__device__ __forceinline__ float max_of(float v) {
-  return across<L>(v, [](float a, float b) { return fmaxf(a, b); });
-}
 
 // A lane's four logits of a row (experts e .. e + 3), -inf behind E.  No branches: loads of several
 // tokens are to be under way at once.
@@ -111,12 +82,12 @@ __device__ __forceinline__ float scores(const f32x4& l, f32x4& e, f32x4& rest) {
       }
     }
   } else {
-    float m = max_of<L>(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])));
+    float m = lanes_max<L>(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])));
     m = m == -INFINITY ? 0.f : m;                    // every expert masked: no shares
 #pragma unroll
     for (int j = 0; j < 4; ++j) e[j] = exp_near(l[j] - m);
   }
-  const float sum = sum_of<L>((e[0] + e[1]) + (e[2] + e[3]));
+  const float sum = lanes_sum<L>((e[0] + e[1]) + (e[2] + e[3]));
   if constexpr (SIGMOID) return inverse(sum < kLeastSum ? kLeastSum : sum);
   return sum > 0.f ? inverse(sum) : sum != sum ? sum : 0.f;
 }
@@ -436,14 +407,14 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(BalanceGradArgs a, in
         if (__ballot(leads)) {
 #pragma unroll
           for (int j = 0; j < 4; ++j) lead += q[j] > 0.5f ? c[j] : 0.f;
-          lead = sum_of<L>(lead);
+          lead = lanes_sum<L>(lead);
         }
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           d[j] = c[j] - lead;
           dot = fmaf(d[j], q[j], dot);
         }
-        dot = sum_of<L>(dot);
+        dot = lanes_sum<L>(dot);
 #pragma unroll
         for (int j = 0; j < 4; ++j) {
           d[j] = q[j] * (d[j] - dot);

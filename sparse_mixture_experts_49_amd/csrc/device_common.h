@@ -178,6 +178,36 @@ __device__ __forceinline__ float wave_sum_f(float v) {
   }));
 }
 
+// The same over every L neighbouring lanes (a power of two), in all of them.
+template <int CTRL>
+__device__ __forceinline__ float dpp_of(float v) {
+  return __uint_as_float((uint32_t)__builtin_amdgcn_update_dpp(0, (int)__float_as_uint(v), CTRL, 0xF, 0xF, false));
+}
+template <int L, typename F>
+__device__ __forceinline__ float lanes_reduce(float v, F f) {
+  if constexpr (L >= 2) v = f(v, dpp_of<0xB1>(v));   // quad [1,0,3,2]
+  if constexpr (L >= 4) v = f(v, dpp_of<0x4E>(v));   // quad [2,3,0,1]
+  if constexpr (L >= 8) v = f(v, dpp_of<0x141>(v));  // half-row mirror
+  if constexpr (L >= 16) v = f(v, dpp_of<0x140>(v)); // row mirror
+  if constexpr (L >= 32) {                           // neighbouring rows of 16, then halves
+    const auto r = __builtin_amdgcn_permlane16_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  if constexpr (L >= 64) {
+    const auto r = __builtin_amdgcn_permlane32_swap(__float_as_uint(v), __float_as_uint(v), false, false);
+    v = f(__uint_as_float(r[0]), __uint_as_float(r[1]));
+  }
+  return v;
+}
+template <int L>
+__device__ __forceinline__ float lanes_sum(float v) {
+  return lanes_reduce<L>(v, [](float a, float b) { return a + b; });
+}
+template <int L>
+__device__ __forceinline__ float lanes_max(float v) {
+  return lanes_reduce<L>(v, [](float a, float b) { return fmaxf(a, b); });
+}
+
 // e^x within ~2 ulp for |x| < 88: 2^(x log2 e) with the rounding error of the product put
 // back to first order.  From 88 to 88.72, where it overflows, without that (3e-6 relative);
 // below -87.34 it is under fp32's normal range.  Infinities and NaN come out as they should.

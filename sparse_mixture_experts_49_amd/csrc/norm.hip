@@ -10,8 +10,8 @@
 // Memory bounds both.  A group of G threads has a row in registers (8 NV values a thread), so
 // it is read once and the squares are those of the differences from the mean; the groups take
 // rows in turn, and their threads keep the same columns, so weight and bias stay in
-// registers, and so do the column sums of the backward pass.  Those are written once
-// per group and added up, in order, by a second kernel.  Everything is summed in fp32.
+// registers, and so do the column sums of the backward pass.  Those are written once a block
+// and added up, in order, by a second kernel.  Everything is summed in fp32.
 #include <algorithm>
 
 #include "device_common.h"
@@ -107,14 +107,16 @@ struct Columns {
 
 // Sums of N values over a group, returned to all its threads.  Groups wider than a wave
 // exchange through `red`; calls alternate its halves, so one barrier each is enough.
+constexpr int waves_of(int G) { return G < 64 ? 1 : G / 64; }
+
 template <int G, int N>
 struct GroupSum {
-  static constexpr int kW = G / 64;
+  static constexpr int kW = waves_of(G);
   float (*red)[N][kW];
   int half = 0;
   __device__ __forceinline__ void operator()(float (&v)[N]) {
 #pragma unroll
-    for (int n = 0; n < N; ++n) v[n] = wave_sum_f(v[n]);
+    for (int n = 0; n < N; ++n) v[n] = G < 64 ? lanes_sum<(G < 64 ? G : 64)>(v[n]) : wave_sum_f(v[n]);
     if constexpr (kW > 1) {
       if ((threadIdx.x & 63) == 0)
 #pragma unroll
@@ -138,7 +140,7 @@ template <typename T, int G, int NV, bool VEC>
 __global__ __launch_bounds__(block_of(G)) void norm_kernel(NormArgs a) {
   using C = Columns<G, NV, VEC>;
   constexpr int kGroups = block_of(G) / G;
-  __shared__ float red[2][1][G / 64];
+  __shared__ float red[2][1][waves_of(G)];
   GroupSum<G, 1> sum{red};
   const int t = threadIdx.x % G, d = a.sh.d;
   const float inv = 1.f / d;
@@ -227,7 +229,7 @@ template <typename T, int G, int NV, bool VEC>
 __global__ __launch_bounds__(block_of(G)) void norm_grad_kernel(NormGradArgs a) {
   using C = Columns<G, NV, VEC>;
   constexpr int kGroups = block_of(G) / G;
-  __shared__ float red[2][2][G / 64];
+  __shared__ float red[2][2][waves_of(G)];
   GroupSum<G, 2> sum{red};
   const int t = threadIdx.x % G, d = a.sh.d;
   const int64_t group = (int64_t)blockIdx.x * kGroups + threadIdx.x / G, step = (int64_t)gridDim.x * kGroups;
@@ -286,13 +288,39 @@ __global__ __launch_bounds__(block_of(G)) void norm_grad_kernel(NormGradArgs a) 
       C::store(static_cast<T*>(a.d_x.p) + row * a.d_x.stride, t, d, r);
     }
   }
-  float* part = a.part + group * 2 * d;
-  if (a.d_weight) C::store(part, t, d, dw);
-  if (a.d_bias) C::store(part + d, t, d, db);
+  // One row of partial sums a block: its groups' added up, by lanes, then by waves.
+  float* part = a.part + (size_t)blockIdx.x * 2 * d;
+  if constexpr (kGroups > 1) {
+    __shared__ float all[4][2][8 * G * NV];
+    if (!a.d_weight && !a.d_bias) return;
+    const int wave = threadIdx.x >> 6;
+#pragma unroll
+    for (int v = 0; v < NV; ++v)
+#pragma unroll
+      for (int j = 0; j < 8; ++j) {
+#pragma unroll
+        for (int o = G; o < 64; o <<= 1) {
+          dw[v][j] += __shfl_xor(dw[v][j], o);
+          db[v][j] += __shfl_xor(db[v][j], o);
+        }
+        if ((threadIdx.x & 63) < G) {
+          all[wave][0][C::at(t, v, j)] = dw[v][j];
+          all[wave][1][C::at(t, v, j)] = db[v][j];
+        }
+      }
+    __syncthreads();
+    for (int i = threadIdx.x; i < 2 * d; i += 256) {
+      const int b = i >= d, c = b ? i - d : i;
+      part[i] = (all[0][b][c] + all[1][b][c]) + (all[2][b][c] + all[3][b][c]);
+    }
+  } else {
+    if (a.d_weight) C::store(part, t, d, dw);
+    if (a.d_bias) C::store(part + d, t, d, db);
+  }
 }
 
-// Column sums of the groups' partial rows [groups][2 d]: 64 columns a block, 16 waves a
-// sixteenth of the groups each.
+// Column sums of the blocks' partial rows [groups][2 d]: 64 columns a block here, 16 waves a
+// sixteenth of the rows each.
 __global__ __launch_bounds__(1024) void norm_sum_kernel(const float* __restrict__ part, int groups, int d,
                                                         float* __restrict__ d_weight, float* __restrict__ d_bias) {
   __shared__ float acc[16][64];
@@ -314,18 +342,25 @@ __global__ __launch_bounds__(1024) void norm_sum_kernel(const float* __restrict_
 }
 
 // ---- launches ----------------------------------------------------------------------------
-static int group_of(int d) { return d <= 1024 ? 64 : d <= 4096 ? 256 : d <= 8192 ? 512 : 1024; }
+// Threads of a row: as few as hold it with 8 values each up to a wave (64 values in 64 lanes took
+// twice as long), then 16.
+static int group_of(int d) {
+  return d <= 64 ? 8 : d <= 128 ? 16 : d <= 256 ? 32 : d <= 1024 ? 64 : d <= 4096 ? 256 : d <= 8192 ? 512 : 1024;
+}
 static int groups_per_block(int d) { return block_of(group_of(d)) / group_of(d); }
 
 static int blocks_for(const NormShape& s, int most) {
   const int per = groups_per_block(s.d);
   return (int)std::min<int64_t>((s.rows + per - 1) / per, most);
 }
-static int grad_blocks(const NormShape& s) { return blocks_for(s, 512); }
-
-size_t norm_grad_part_bytes(const NormShape& s) {
-  return (size_t)grad_blocks(s) * groups_per_block(s.d) * 2 * s.d * 4;
+// Four rows a group at least, or the sums of their sums take longer than they; at most 512 blocks
+// (256: 16384 x 2048 85 us against 63), past 4096 columns 256 (2048 x 8192 34 us against 41).
+static int grad_blocks(const NormShape& s) {
+  const int64_t rows = 4 * groups_per_block(s.d);
+  return (int)std::min<int64_t>((s.rows + rows - 1) / rows, s.d > 4096 ? 256 : 512);
 }
+
+size_t norm_grad_part_bytes(const NormShape& s) { return (size_t)grad_blocks(s) * 2 * s.d * 4; }
 
 // Rows of whole 16-byte pieces of eight values.
 template <typename P>
@@ -340,7 +375,10 @@ static void for_width(int d, bool vec, F f) {
     else f(g, nv, std::false_type());
   };
   using std::integral_constant;
-  if (d <= 512) with(integral_constant<int, 64>(), integral_constant<int, 1>());
+  if (d <= 64) with(integral_constant<int, 8>(), integral_constant<int, 1>());
+  else if (d <= 128) with(integral_constant<int, 16>(), integral_constant<int, 1>());
+  else if (d <= 256) with(integral_constant<int, 32>(), integral_constant<int, 1>());
+  else if (d <= 512) with(integral_constant<int, 64>(), integral_constant<int, 1>());
   else if (d <= 1024) with(integral_constant<int, 64>(), integral_constant<int, 2>());
   else if (d <= 2048) with(integral_constant<int, 256>(), integral_constant<int, 1>());
   else if (d <= 4096) with(integral_constant<int, 256>(), integral_constant<int, 2>());
@@ -387,7 +425,7 @@ hipError_t launch_norm_grad(const NormGradArgs& a, hipStream_t s) {
     if (hipError_t e = hipGetLastError()) return e;
   }
   if (a.d_weight || a.d_bias)                        // no rows: zeros
-    norm_sum_kernel<<<(2 * a.sh.d + 63) / 64, 1024, 0, s>>>(a.part, blocks * groups_per_block(a.sh.d), a.sh.d,
+    norm_sum_kernel<<<(2 * a.sh.d + 63) / 64, 1024, 0, s>>>(a.part, blocks, a.sh.d,
                                                              a.d_weight, a.d_bias);
   return hipGetLastError();
 }

@@ -40,7 +40,9 @@ def _params(d, name, g):
 
 # rows, d, dtype, params, add (dtype or None), extra elements between rows
 SHAPES = [
-    (1, 1, "f32", "f32", None, 0), (1, 4096, "bf16", "bf16", "f32", 0), (5, 7, "bf16", "f32", "bf16", 0),
+    (1, 1, "f32", "f32", None, 0), (3000, 64, "bf16", "f32", "f32", 0), (2500, 65, "f32", "bf16", None, 0),
+    (999, 128, "f32", "f32", "f32", 8), (4100, 100, "bf16", "bf16", "bf16", 4), (700, 250, "bf16", "f32", None, 0),
+    (257, 256, "f32", "f32", "bf16", 0), (1, 4096, "bf16", "bf16", "f32", 0), (5, 7, "bf16", "f32", "bf16", 0),
     (3, 63, "f32", "f32", "f32", 1), (70, 512, "bf16", "f32", "f32", 8), (9, 513, "bf16", "bf16", "f32", 0),
     (130, 1000, "f32", "f32", None, 0), (33, 1024, "bf16", "f32", "bf16", 3), (17, 1032, "f32", "bf16", "bf16", 4),
     (300, 2048, "bf16", "f32", "f32", 0), (2100, 2056, "bf16", "bf16", None, 0), (40, 4095, "bf16", "f32", "f32", 0),
@@ -110,7 +112,8 @@ def test_backward(shape):
     tol = U32 * (rstd.double()[:, None] * inner + 2 * ref.abs() + (res.double().abs() if res is not None else 0.0))
     tol = tol + (ref.abs() + tol) * _half(dtype)
     assert torch.all((dx[:, :d].double() - ref).abs() <= tol)
-    # Column sums: at most 5 rows in a group here, 128 groups in a wave, 16 waves; 3 a term.
+    # Column sums, on any way to a value: at most 8 rows of a group, 8 adds between a block's groups,
+    # 32 blocks in a wave, 16 waves; 3 a term.
     assert torch.all((dw[:d].double() - (dy.double() * hat).sum(0)).abs() <= 170 * U32 * (dy.double() * hat).abs().sum(0) + 1e-30)
     assert torch.all((db[:d].double() - dy.double().sum(0)).abs() <= 170 * U32 * dy.double().abs().sum(0) + 1e-30)
     # Each output alone is the same, bit for bit.
