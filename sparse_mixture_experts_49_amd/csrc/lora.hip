@@ -161,13 +161,14 @@ __device__ __forceinline__ f32x4 mfma_4x4(uint32_t a0, uint32_t a1, uint32_t b0,
                                                 __builtin_bit_cast(i16x4, (u32x2){b0, b1}), c, 0, 0, 0);
 }
 
-constexpr int kTokenWaves = 8, kTokenMaxWidth = 32768, kTokenMaxRank = 64;
+// A block reads all of the adapter's A, so that is bounded (see path_of), and with it the width.
+constexpr int kTokenWaves = 8, kTokenMostA = 128 * 1024, kTokenMaxWidth = kTokenMostA / 8;
 
 template <int P>
 __global__ __launch_bounds__(kTokenWaves * 64, 2) void lora_token_kernel(LoraArgs a) {
   constexpr int kSets = 3;
   __shared__ __attribute__((aligned(16))) uint16_t sx[kTokenMaxWidth];
-  __shared__ __attribute__((aligned(16))) float su[kTokenMaxRank];
+  __shared__ __attribute__((aligned(16))) float su[kLoraMaxRank];
   const int d = a.sh.d, n = a.sh.n, rank = a.sh.rank;
   const int lane = threadIdx.x & 63, wave = __builtin_amdgcn_readfirstlane(threadIdx.x >> 6);
   const int first = blockIdx.x * kTokenWaves + wave, stride = gridDim.x * kTokenWaves;   // rows of W
@@ -233,7 +234,7 @@ __global__ __launch_bounds__(kTokenWaves * 64, 2) void lora_token_kernel(LoraArg
     for (int r = 16; r < rank; r += 8) s = dot8(ld16(b + r), su + r, s);
     sum += s;
   }
-  if (a.sh.f32_out) static_cast<float*>(a.y)[row] = a.sh.gelu ? gelu_erf(sum) : sum;
+  if (a.sh.f32_out) static_cast<float*>(a.y)[row] = a.sh.gelu ? gelu_f32(sum) : sum;
   else static_cast<uint16_t*>(a.y)[row] = (uint16_t)pack_bf16x2(a.sh.gelu ? gelu_for_bf16(sum) : sum, 0.f);
 }
 
@@ -407,7 +408,7 @@ __global__ __launch_bounds__(256) void lora_finish_kernel(LoraPartArgs p) {
   for (int i = 0; i < kCols; ++i) {
     const int c = c0 + i * 256;
     if (c >= n) continue;
-    if (a.sh.f32_out) static_cast<float*>(a.y)[(size_t)t * n + c] = a.sh.gelu ? gelu_erf(v[i]) : v[i];
+    if (a.sh.f32_out) static_cast<float*>(a.y)[(size_t)t * n + c] = a.sh.gelu ? gelu_f32(v[i]) : v[i];
     else static_cast<uint16_t*>(a.y)[(size_t)t * n + c] = (uint16_t)pack_bf16x2(a.sh.gelu ? gelu_for_bf16(v[i]) : v[i], 0.f);
   }
 }
@@ -430,8 +431,9 @@ static int part_splits(const LoraShape& s) {
 }
 
 static LoraPath path_of(const LoraShape& s) {
-  if (s.T == 1 && s.rank <= kTokenMaxRank && (long)s.rank * s.d <= 128 * 1024 && s.d <= kTokenMaxWidth &&
-      s.n <= 64 * 256 * kTokenWaves)                   // a lane for every row of a wave
+  // One token, us by this way (A's values) and in parts: n = d = 4096, 64 K 14 and 16, 256 K 20 and 20;
+  // 14336 x 4096, 224 K 33 and 34, 448 K 39 and 36; 2048 x 2816, 64 K 9 and 12.
+  if (s.T == 1 && (long)s.rank * s.d <= kTokenMostA && s.n <= 64 * 256 * kTokenWaves)   // a lane for a wave's every row
     return kToken;
   // Tiles need four steps of 64 k: their loads run two ahead, into the next tile only.
   return s.T > 128 && s.d >= 256 && part_splits(s) == 1 ? kTile : kPart;

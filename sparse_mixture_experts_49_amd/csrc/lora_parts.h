@@ -7,6 +7,9 @@
 
 namespace moe {
 
+// GELU for an fp32 result: +inf stays +inf, as it does for bf16.
+__device__ __forceinline__ float gelu_f32(float z) { return z > 1e4f ? z : gelu_erf(z); }
+
 // A block's part: BM tokens, BN columns of W or of the adapters that the tokens have (16 ranks of one
 // after the other's), steps [k0, k1) of 64 k.
 struct LoraUnit {

@@ -317,7 +317,7 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraPartArgs all) {
 #pragma unroll
           for (int g = 0; g < 4; ++g)
 #pragma unroll
-            for (int q = 0; q < 4; ++q) v[g][q] = F32 ? gelu_erf(v[g][q]) : gelu_for_bf16(v[g][q]);
+            for (int q = 0; q < 4; ++q) v[g][q] = F32 ? gelu_f32(v[g][q]) : gelu_for_bf16(v[g][q]);
         }
         if constexpr (F32) {
           float* o = static_cast<float*>(p.y) + (size_t)r * N + col0 + 4 * fc;

@@ -74,6 +74,17 @@ def test_block_is_its_steps(T, shared):
     assert torch.equal(routing.topk_idx, r.topk_idx) and torch.equal(routing.logits, r.logits)
 
 
+def test_block_with_strided_rows_and_no_add():
+    T = 33
+    b, x, add, ids = _made(T, 256, 384, 16, 4, 512, True, 8)
+    wide = torch.zeros(T, 300, dtype=torch.bfloat16, device=DEV)
+    wide[:, :256] = x
+    y, z = torch.empty(T, 256, device=DEV), torch.empty(T, 256, device=DEV)
+    moe.moe_mx_block_forward(b, x, y, adapter=ids)
+    moe.moe_mx_block_forward(b, wide[:, :256], z, add=torch.zeros_like(add), adapter=ids)
+    assert torch.equal(y, z)
+
+
 def test_two_blocks_captured():
     """A stack of two: the first one's output is the second one's add; replayed three times."""
     T = 50

@@ -74,6 +74,9 @@ def _run(desc, x, ids, w, a, b, scale, bias, guard=64):
 # T, d, n, rank, N, ids, bias, scale
 SHAPES = [
     (1, 128, 128, 8, 1, "one", False, True), (1, 4096, 4096, 16, 8, "one", False, True),
+    (1, 640, 256, 24, 3, "one", True, True), (1, 1152, 384, 32, 2, "one", True, False),
+    (1, 8192, 2176, 16, 2, "one", False, True), (1, 5120, 384, 8, 2, "none", True, True),
+    (1, 1024, 128, 128, 2, "one", False, True), (1, 2048, 256, 128, 2, "one", True, True),
     (2, 256, 384, 16, 3, "random", True, False), (16, 640, 128, 24, 40, "random", False, True),
     (17, 128, 256, 128, 5, "random", True, True), (32, 384, 8192, 16, 32, "random", True, True),
     (33, 512, 512, 40, 2, "runs", False, False), (64, 2048, 256, 72, 70, "random", True, True),
@@ -112,7 +115,8 @@ def _gaussians(T, d, n, r, N, bias, g):
     return x, w, a, b, 0.5 + torch.rand(N, generator=g), torch.randn(n, generator=g).bfloat16() if bias else None
 
 
-@pytest.mark.parametrize("shape", [SHAPES[i] for i in (1, 4, 7, 8, 12, 15, 17)], ids=[IDS[i] for i in (1, 4, 7, 8, 12, 15, 17)])
+@pytest.mark.parametrize("shape", [SHAPES[i] for i in (1, 3, 10, 13, 14, 18, 21, 23)],
+                         ids=[IDS[i] for i in (1, 3, 10, 13, 14, 18, 21, 23)])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("act", ["none", "gelu"])
 def test_gaussian_values(shape, out, act):
@@ -170,6 +174,21 @@ def test_a_large_first_product():
     assert torch.all(_run(desc, x, ids, w, a, b, None, None) == 2.0 ** 27)
     got = _run(desc, x, ids, w, a, b, torch.tensor([4.0]), None)
     assert not torch.any(torch.isfinite(got))
+
+
+@pytest.mark.parametrize("T", [1, 20, 100, 600])
+def test_gelu_of_large_values(T):
+    """GELU of what is past any doubt: +inf stays, large values stay, -large is 0."""
+    d, n = 256, 128
+    x, w = torch.zeros(T, d).bfloat16(), torch.zeros(n, d).bfloat16()
+    x[:, 0], w[:, 0] = 1.0, torch.tensor([float("inf"), 3e38, 1e5, 20.0, -20.0, -1e5, 0.0, 1.0] * 16).bfloat16()
+    a, b = torch.zeros(1, 8, d).bfloat16(), torch.zeros(1, n, 8).bfloat16()
+    ids = torch.full((T,), -1, dtype=torch.int32)
+    ref = w[:, 0].double()
+    ref = torch.where(ref > 1e4, ref, torch.special.ndtr(ref) * ref)
+    for out, half in (("f32", U32), ("bf16", U16)):
+        got = _run(moe.LoraDesc(T, d, n, 8, 1, act="gelu", out_dtype=out), x, ids, w, a, b, None, None).double()
+        assert torch.all((got == ref) | ((got - ref).abs() <= half * ref.abs() + 2e-7 * 20))
 
 
 @pytest.mark.parametrize("T", [3, 100, 700])
