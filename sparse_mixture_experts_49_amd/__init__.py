@@ -1,5 +1,5 @@
 """MI355X-native (gfx950) sparsely-gated Mixture-of-Experts layer, with a scored router, its
-gradients and MXFP4 experts beside it.
+gradients and MXFP4 experts beside it, layer norm, balance loss by sequence and low-rank adapters.
 
 The layer runs in hand-written HIP kernels behind the C ABI of
 libmoe_mi355x.so (header: include/moe_mi355x.h); this package is its ctypes

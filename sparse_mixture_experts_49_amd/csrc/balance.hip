@@ -18,6 +18,9 @@
 // that are not empty are met in an order in which c or b grows and neither falls, so c + b
 // numbers them without gaps in use and without a list.  A second kernel adds each sequence's
 // pieces in order, a third the sequences' losses.  fp32 within a piece, fp64 beyond.
+//
+// 131072 tokens, 256 experts, sigmoid, 64 sequences: 40 us, 3.5 TB/s; runs 32 (33 M sigmoids: near the
+// instruction rate), the two others 5 and 4.  Its gradient 57 us, 4.7 TB/s.  A small batch: 4.5 and 8 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -450,7 +453,8 @@ static void for_kind(bool sigmoid, int E, F f) {
   });
 }
 
-// One launch where a wave can take a whole sequence: at most 32 of its steps, and 64 sequences.
+// One launch where a wave can take a whole sequence: at most 32 of its steps, and 64 sequences (4.5 us;
+// three kernels take 16).
 static bool single(const BalanceShape& s) { return s.S <= 64 && (long)s.T * s.E <= 8 * 1024; }
 
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
@@ -465,6 +469,7 @@ hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
     balance_part_kernel<decltype(l)::value, decltype(sig)::value, decltype(vec)::value>
         <<<balance_chunks(a.sh), 256, 0, s>>>(a, chunk);
   });
+  // A sequence's pieces by 16 waves or by one: 131072 x 256 in 512 sequences 47 and 42 us, in 4096 105 and 52.
   if (balance_chunks(a.sh) >= 8 * a.sh.S) balance_seq_kernel<16><<<dim3(a.sh.S, parts), 1024, 0, s>>>(a, chunk);
   else balance_seq_kernel<1><<<dim3((a.sh.S + 15) / 16, parts), 1024, 0, s>>>(a, chunk);
   balance_total_kernel<<<1, 1024, 0, s>>>(a, parts);
