@@ -33,7 +33,11 @@ __global__ __launch_bounds__(256, OCC) void lora_shrink_kernel(LoraArgs a) {
   const int fr = lane & 15, fc = lane >> 4, t0 = blockIdx.x * kRows;
   const uint32_t lds0 = (uint32_t)(uintptr_t)lds, row_bytes = (uint32_t)d * 2u;
   if (threadIdx.x < kRows) ids[lane] = t0 + lane < T ? a.adapter[t0 + lane] : -1;
-  const int groups = lora_list<kRows>(a, t0, list) * per, nk = d / 128;
+  const int all = lora_list<kRows>(a, t0, list) * per, nk = d / 128;
+  // The block's share of the groups, in pairs.
+  const int share = ((all + 1) / 2 + gridDim.y - 1) / gridDim.y * 2, from = blockIdx.y * share;
+  const int groups = min(from + share, all);
+  if (from >= all) return;
   __syncthreads();
   // Load i of a wave: four rows, of x first, then of A.
   auto row_of = [&](int i) { return (i * 4 + wave) * 4 + (lane >> 4); };
@@ -121,7 +125,7 @@ __global__ __launch_bounds__(256, OCC) void lora_shrink_kernel(LoraArgs a) {
     }
     __syncthreads();
   };
-  for (int g0 = 0; g0 < groups;) {
+  for (int g0 = from; g0 < groups;) {
     if (groups - g0 == 1) {
       pass(std::integral_constant<int, 1>(), g0);
       ++g0;
@@ -144,6 +148,7 @@ __device__ __forceinline__ float dot8(const u32x4& q, const float* u, float s) {
   }
   return s;
 }
+
 // ---------------------------------------------------------------------------
 // One token, bound by the bytes of W and by latency.  Every block works out u itself (A is read from
 // memory once and then from L2), so one launch does all.  A wave takes whole rows, first of W, then
@@ -454,8 +459,7 @@ size_t lora_u_bytes(const LoraShape& s) {
 // All of a CU's LDS while it has one block at most, half of it beyond.
 static void launch_shrink(const LoraArgs& a, hipStream_t s) {
   const int tiles = (a.sh.T + 31) / 32;
-  if (tiles <= 256) lora_shrink_kernel<144 * 1024, 1><<<tiles, 256, 0, s>>>(a);
-  else lora_shrink_kernel<72 * 1024, 2><<<tiles, 256, 0, s>>>(a);
+  lora_shrink_kernel<72 * 1024, 2><<<dim3(tiles, std::max(2, std::min(8, 512 / tiles))), 256, 0, s>>>(a);
 }
 
 static hipError_t launch_part(const LoraArgs& a, hipStream_t s) {
