@@ -16,16 +16,15 @@ namespace moe {
 
 // ---------------------------------------------------------------------------
 // u = scale A x before the tiled product, as bf16 terms.  A block has 32 tokens and first lists the
-// different adapters among them.  An adapter is pitch / 16 groups of 16 ranks; a pass over k takes
+// different adapters among them; a few blocks share one tile's.  An adapter is pitch / 16 groups of 16 ranks; a pass over k takes
 // one, two or four groups, of one adapter or of several, so that x is read once for a few
 // adapters.  x and A go into LDS in runs of 256 bytes of every row, as many stages as fit, pieces at
 // piece ^ (row % 16); of a stage's 128 k each of the four waves multiplies 32, and their sums
 // meet in LDS.  Bound by reading x: 16384 x 4096, 16 adapters of 16 ranks, 40 us, 3.4 TB/s; 8192 x 2816 of
-// 32 ranks 13 to 24 us, one block a CU, whose A takes as many bytes as its x.
+// 32 ranks 13 us with one adapter, 19 with 64 requests of eight.
 // ---------------------------------------------------------------------------
-template <int LDS, int OCC>
-__global__ __launch_bounds__(256, OCC) void lora_shrink_kernel(LoraArgs a) {
-  constexpr int kRows = 32, kA = kRows * 256;
+__global__ __launch_bounds__(256, 2) void lora_shrink_kernel(LoraArgs a) {
+  constexpr int kRows = 32, kA = kRows * 256, LDS = 72 * 1024;   // two blocks a CU
   __shared__ __attribute__((aligned(1024))) uint8_t lds[LDS];
   __shared__ int list[kRows], ids[kRows];
   const int T = a.sh.T, d = a.sh.d, rank = a.sh.rank, pitch = lora_pitch(rank), per = pitch / 16;
@@ -456,10 +455,11 @@ size_t lora_u_bytes(const LoraShape& s) {
   }
 }
 
-// All of a CU's LDS while it has one block at most, half of it beyond.
+// Blocks that share a tile's groups: those without any end at once.  8192 x 2816, 64 requests of 8 adapters of
+// 32 ranks: two a tile 22 us, four 19; scattered adapters gain by eight where tiles are few.
 static void launch_shrink(const LoraArgs& a, hipStream_t s) {
   const int tiles = (a.sh.T + 31) / 32;
-  lora_shrink_kernel<72 * 1024, 2><<<dim3(tiles, std::max(2, std::min(8, 512 / tiles))), 256, 0, s>>>(a);
+  lora_shrink_kernel<<<dim3(tiles, tiles <= 128 ? 8 : 4), 256, 0, s>>>(a);
 }
 
 static hipError_t launch_part(const LoraArgs& a, hipStream_t s) {
