@@ -16,11 +16,11 @@ namespace moe {
 
 // ---------------------------------------------------------------------------
 // u = scale A x before the tiled product, as bf16 terms.  A block has 32 tokens and first lists the
-// different adapters among them; a few blocks share one tile's.  An adapter is pitch / 16 groups of 16 ranks; a pass over k takes
-// one, two or four groups, of one adapter or of several, so that x is read once for a few
-// adapters.  x and A go into LDS in runs of 256 bytes of every row, as many stages as fit, pieces at
-// piece ^ (row % 16); of a stage's 128 k each of the four waves multiplies 32, and their sums
-// meet in LDS.  Bound by reading x: 16384 x 4096, 16 adapters of 16 ranks, 40 us, 3.4 TB/s; 8192 x 2816 of
+// different adapters among them; a few blocks share one tile's.  An adapter is pitch / 16 groups of 16
+// ranks; a pass over k takes one, two or four groups, of one adapter or of several, so that x is
+// read once for a few adapters.  x and A go into LDS in runs of 256 bytes of every row, as many
+// stages as fit, pieces at piece ^ (row % 16); of a stage's 128 k each of the four waves multiplies
+// 32, and their sums meet in LDS.  Bound by reading x: 16384 x 4096, 16 adapters of 16 ranks, 40 us, 3.4 TB/s; 8192 x 2816 of
 // 32 ranks 13 us with one adapter, 19 with 64 requests of eight.
 // ---------------------------------------------------------------------------
 __global__ __launch_bounds__(256, 2) void lora_shrink_kernel(LoraArgs a) {
