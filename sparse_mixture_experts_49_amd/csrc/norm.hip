@@ -59,6 +59,9 @@ __device__ __forceinline__ float stored(float v, float) { return v; }
 // lines.  Columns at and past d hold 0.
 template <int G, int NV, bool VEC>
 struct Columns {
+  // Odd widths: every load under way before the first is used, while registers last (3000 x 4095 bf16 35 us
+  // against 52 behind branches; 3000 x 14999 in 1024 threads 397 against 175).
+  static constexpr bool kWhole = G <= 512;
   static __device__ __forceinline__ int at(int t, int v, int j) {
     return VEC ? (v * G + t) * 8 + j : (v * 8 + j) * G + t;
   }
@@ -75,9 +78,17 @@ struct Columns {
         }
       } else {
 #pragma unroll
-        for (int j = 0; j < 8; ++j) x[v][j] = at(t, v, j) < d ? load1(row + at(t, v, j)) : 0.f;
+        for (int j = 0; j < 8; ++j) {
+          if constexpr (kWhole) x[v][j] = load1(row + min(at(t, v, j), d - 1));
+          else x[v][j] = at(t, v, j) < d ? load1(row + at(t, v, j)) : 0.f;
+        }
       }
     }
+    if constexpr (!VEC && kWhole)
+#pragma unroll
+      for (int v = 0; v < NV; ++v)
+#pragma unroll
+        for (int j = 0; j < 8; ++j) x[v][j] = at(t, v, j) < d ? x[v][j] : 0.f;
   }
   template <typename T>
   static __device__ __forceinline__ void store(T* row, int t, int d, const float (&x)[NV][8]) {
@@ -357,9 +368,10 @@ static int blocks_for(const NormShape& s, int most) {
   return (int)std::min<int64_t>((s.rows + per - 1) / per, most);
 }
 // Four rows a group at least, or the sums of their sums take longer than they; at most 512 blocks
-// (256: 16384 x 2048 85 us against 63), past 4096 columns 256 (2048 x 8192 34 us against 41).
+// (256: 16384 x 2048 85 us against 63).  Past 4096 columns two rows (200 x 16384 fp32 35 us, with four 48)
+// and 256 blocks (2048 x 8192 34 us against 41).
 static int grad_blocks(const NormShape& s) {
-  const int64_t rows = 4 * groups_per_block(s.d);
+  const int64_t rows = (s.d > 4096 ? 2 : 4) * groups_per_block(s.d);
   return (int)std::min<int64_t>((s.rows + rows - 1) / rows, s.d > 4096 ? 256 : 512);
 }
 
