@@ -51,7 +51,8 @@ SHAPES = [
     (100, 24, 8, "softmax", True, 9), (300, 60, 4, "sigmoid", True, 20), (33, 64, 6, "softmax", False, [0, 33]),
     (515, 96, 8, "sigmoid", False, 40), (1000, 128, 8, "softmax", True, 3), (130, 255, 7, "softmax", True, 130),
     (2100, 256, 8, "sigmoid", True, 70), (20000, 160, 6, "softmax", True, 5), (40, 256, 8, "softmax", False, 300),
-    (16500, 33, 3, "sigmoid", False, [0, 16500]),
+    (16500, 33, 3, "sigmoid", False, [0, 16500]), (40000, 72, 2, "softmax", True, 3001),
+    (530000, 8, 2, "sigmoid", True, 7),
 ]
 IDS = ["T%d_E%d_k%d_%s_%s_%s" % (s[:5] + ((s[5] if isinstance(s[5], int) else len(s[5]) - 1),)) for s in SHAPES]
 

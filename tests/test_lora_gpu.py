@@ -86,6 +86,8 @@ SHAPES = [
     (777, 384, 128, 48, 2, "one", True, False), (1100, 512, 1152, 128, 6, "runs", False, True),
     (1024, 256, 256, 16, 5, "none", True, True), (8200, 256, 2176, 24, 30, "runs", True, True),
     (12300, 384, 1280, 16, 200, "random", False, True), (16400, 256, 1024, 72, 3, "runs", True, True),
+    (2000, 256, 1536, 40, 60, "random", True, True), (1500, 384, 2176, 128, 5, "random", False, True),
+    (1400, 256, 2176, 16, 300, "random", True, False),
 ]
 IDS = ["T%d_%dx%d_r%d_N%d_%s" % s[:6] for s in SHAPES]
 
@@ -115,8 +117,8 @@ def _gaussians(T, d, n, r, N, bias, g):
     return x, w, a, b, 0.5 + torch.rand(N, generator=g), torch.randn(n, generator=g).bfloat16() if bias else None
 
 
-@pytest.mark.parametrize("shape", [SHAPES[i] for i in (1, 3, 10, 13, 14, 18, 21, 23)],
-                         ids=[IDS[i] for i in (1, 3, 10, 13, 14, 18, 21, 23)])
+@pytest.mark.parametrize("shape", [SHAPES[i] for i in (1, 3, 10, 13, 14, 18, 21, 23, 27)],
+                         ids=[IDS[i] for i in (1, 3, 10, 13, 14, 18, 21, 23, 27)])
 @pytest.mark.parametrize("out", ["f32", "bf16"])
 @pytest.mark.parametrize("act", ["none", "gelu"])
 def test_gaussian_values(shape, out, act):
