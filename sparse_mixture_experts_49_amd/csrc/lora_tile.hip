@@ -12,8 +12,10 @@
 // different adapter a among them, B_a (its rows as they lie in memory: 16 bytes are 8 ranks of a
 // column) times u, which the first kernel left as bf16 terms (two under a bf16 result, 17 bits;
 // three under fp32, all of its 24).  Where the 32 tokens have several adapters u is 0 for all
-// but a's own; what of B_a is infinite or NaN, so that even 0 times it would spread, is then
-// taken out and the results that it is meant for are made infinite by a product of their own.
+// but a's own.  What of B_a is infinite or NaN goes by a product of its own, with u's sign
+// (1, -1 or 0) in one term: 0 times it would spread to the others, and u's later terms, 0 or of
+// either sign, would make NaN of an infinity.  In the main product +-1 stands in its place, so that an
+// infinite u does not meet a 0.
 //
 // 16384 x 4096 -> 14336, rank 16, GELU: 1520 to 1580 us, 1.25 PFLOP/s (1.50 in a library product of
 // 16384 x 16384 x 8192): steps 1335, GELU 130, stores 60, adapters 40.  8192 x 2816 -> 2048, rank 32,
@@ -64,6 +66,19 @@ static long lora_tile_blocks(long total, long ntn) {
 // Whether the lower or upper bf16 of a word is infinite or NaN.
 __device__ __forceinline__ bool infinite_lo(uint32_t w) { return (w & 0x7f80u) == 0x7f80u; }
 __device__ __forceinline__ bool infinite_hi(uint32_t w) { return (w & 0x7f800000u) == 0x7f800000u; }
+
+// Of two bf16 the signs: 1, -1 or 0.
+constexpr uint32_t kSigns = 0x80008000u, kOnes = 0x3f803f80u;
+__device__ __forceinline__ uint32_t signs_of(uint32_t w) {
+  const uint32_t some = ((w & 0x7fffu) ? 0xffffu : 0u) | ((w & 0x7fff0000u) ? 0xffff0000u : 0u);
+  return (w & kSigns) | (kOnes & some);
+}
+
+// Of two pairs of 16 bits the larger of each half.
+__device__ __forceinline__ uint32_t max_pair(uint32_t a, uint32_t b) {
+  typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+  return __builtin_bit_cast(uint32_t, __builtin_elementwise_max(__builtin_bit_cast(u16x2, a), __builtin_bit_cast(u16x2, b)));
+}
 
 // TERMS: the bf16 terms of u, 2 for a bf16 result, 3 for fp32; 0: a part of the k range of W x, or
 // of A x as further columns, stored in fp32 for a finish of its own (one tile a block).
@@ -248,7 +263,7 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraPartArgs all) {
         const int id = __builtin_amdgcn_readlane(ids[m], __ffsll((unsigned long long)left) - 1);
         const uint64_t same = __ballot(ids[m] == id);
         left &= ~same;
-        const bool mine = ids[m] == id, all = same == ~0ull;
+        const bool mine = ids[m] == id;
         for (int k = 0; k < pitch; k += 16) {
           u32x4 bf[kNT], uf[kTerms];
 #pragma unroll
@@ -262,30 +277,35 @@ __global__ __launch_bounds__(256, OCC) void lora_tile_kernel(LoraPartArgs all) {
             uf[q] = ld16(um + (size_t)q * T * pitch + k);
             uf[q] = mine ? uf[q] : u32x4{0, 0, 0, 0};
           }
+          uint32_t most = 0;
 #pragma unroll
-          for (int j = 0; j < kNT; ++j) {
-            if (!all) {
-              bool bad = false;
+          for (int j = 0; j < kNT; ++j)
 #pragma unroll
-              for (int i = 0; i < 4; ++i) bad |= infinite_lo(bf[j][i]) | infinite_hi(bf[j][i]);
-              if (__ballot(bad)) {
-                // Infinity for the columns where B is infinite or NaN and the tokens that it is
-                // meant for: products of finite values that overflow; 0 for all others.
-                u32x4 c = {0, 0, 0, 0}, v = {0, 0, 0, 0};
-                const bool column = bad || __shfl_xor((int)bad, 32);
-                if (fc == 0 && column) c[0] = 0x7f7f7f7fu;
-                if (fc == 0 && mine) v[0] = 0x7f7f7f7fu;
-                acc[j][m] = mfma32_bf16(c, v, acc[j][m]);
+            for (int i = 0; i < 4; ++i) most = max_pair(most, bf[j][i] & ~kSigns);
+          if (__ballot(infinite_lo(most) | infinite_hi(most))) {   // a few registers of the 256 x 256 tile spill for it, outside the steps
+            u32x4 sign;
 #pragma unroll
-                for (int i = 0; i < 4; ++i) {
-                  if (infinite_lo(bf[j][i])) bf[j][i] &= 0xffff0000u;
-                  if (infinite_hi(bf[j][i])) bf[j][i] &= 0xffffu;
-                }
+            for (int i = 0; i < 4; ++i) sign[i] = signs_of(uf[0][i]);
+#pragma unroll
+            for (int j = 0; j < kNT; ++j) {
+              u32x4 far;
+#pragma unroll
+              for (int i = 0; i < 4; ++i) {
+                const uint32_t v = bf[j][i], bad = (infinite_lo(v) ? 0xffffu : 0u) | (infinite_hi(v) ? 0xffff0000u : 0u);
+                far[i] = v & bad;
+                bf[j][i] = (v & (~bad | kSigns)) | (kOnes & bad);
               }
+              f32x16 v = {};
+              v = mfma32_bf16(far, sign, v);
+#pragma unroll
+              for (int i = 0; i < 16; ++i) acc[j][m][i] += mine ? v[i] : 0.f;
+              pin_one(j, m);
             }
+          }
+#pragma unroll
+          for (int j = 0; j < kNT; ++j)
 #pragma unroll
             for (int q = 0; q < kTerms; ++q) acc[j][m] = mfma32_bf16(bf[j], uf[q], acc[j][m]);
-          }
         }
       }
     }

@@ -239,3 +239,29 @@ def test_capture_streams_and_repetition(T):
         got = y.clone()
         moe.moe_lora_linear(desc, x, ids, weights, y, workspace=ws)
         assert torch.equal(y, got)
+
+
+# Under the tiled kernels: 128 x 128 tiles, and 256 x 256.
+TILED = [(1400, 256, 2176), (8200, 256, 2176)]
+
+
+@pytest.mark.parametrize("T,d,n", [(1, 256, 384), (20, 256, 384), (100, 256, 384), (600, 256, 384)] + TILED)
+@pytest.mark.parametrize("kind", ["one", "runs", "random"])
+def test_infinite_and_nan_factors_of_its_own(T, d, n, kind):
+    """What a token's own adapter holds of infinities and NaN comes out as in 64 bits, sign and
+    all, whatever tokens are beside it; other tokens keep their bits.  Exact values, as above."""
+    r, N = 24, 4
+    g = torch.Generator().manual_seed(T + d)
+    x, w, a, b, scale, _ = _small_integers(T, d, n, r, N, False, g)
+    ids = _ids(T, N, kind, g)
+    inf, nan = float("inf"), float("nan")
+    for i, c, q, v in ((0, 3, 2, inf), (1, 9, 5, -inf), (3, 70, 7, nan), (3, 100, 9, inf), (2, 33, 15, -inf), (1, 131, 12, nan),
+                       (3, 200, 19, inf), (0, 255, 23, -inf), (2, 300, 16, nan), (3, 301, 0, -inf), (3, 301, 11, inf)):
+        b[i, c, q] = v
+    a[3, 6, 17], b[3, 310, 6], b[3, 311, 6] = inf, inf, -inf       # an infinite u, which meets them too
+    ref, _ = _reference(x, w, a, b, scale, None, ids)
+    for out in ("f32", "bf16"):
+        got = _run(moe.LoraDesc(T, d, n, r, N, out_dtype=out), x, ids, w, a, b, scale, None)
+        want = ref.float() if out == "f32" else ref.float().bfloat16()
+        same = (got == want) | (torch.isnan(got) & torch.isnan(want))
+        assert torch.all(same), (out, (~same).nonzero()[:8].tolist())
