@@ -148,3 +148,24 @@ def test_gradients_through_norm_router_and_losses():
     # fp32 in every step: a few hundred roundings of values of the size of the largest
     for got, ref in ((dx, want[0]), (dx, want[1]), (gr.d_w_router, want[2]), (dwt, want[3]), (dbi, want[4])):
         assert (got.cpu().double() - ref).abs().max() <= 512 * 2.0 ** -24 * max(1.0, float(ref.abs().max()))
+
+
+def test_block_with_a_tiled_shared_expert():
+    """Rows and columns enough for the shared expert's tiled products, as above; and replayed."""
+    T, d = 1400, 2176
+    b, x, add, ids = _made(T, d, 384, 16, 4, 2304, True, 5)
+    ws = moe.alloc_mx_block_workspace(b, DEV).fill_(0xFF)
+    x_out, y = torch.empty_like(x), torch.empty(T, d, device=DEV)
+    moe.moe_mx_block_forward(b, x, y, add=add, x_out=x_out, adapter=ids, workspace=ws)
+    want_x, want_y, _ = _steps(b, x, add, ids)
+    assert torch.equal(x_out, want_x) and torch.equal(y, want_y)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_mx_block_forward(b, x, y, add=add, x_out=x_out, adapter=ids, workspace=ws)
+    for k in range(3):
+        x.copy_(torch.randn(T, d, generator=torch.Generator().manual_seed(k)).bfloat16())
+        graph.replay()
+        torch.cuda.synchronize()
+        got = [x_out.clone(), y.clone()]
+        moe.moe_mx_block_forward(b, x, y, add=add, x_out=x_out, adapter=ids, workspace=ws)
+        assert torch.equal(x_out, got[0]) and torch.equal(y, got[1])

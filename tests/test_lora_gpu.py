@@ -265,3 +265,118 @@ def test_infinite_and_nan_factors_of_its_own(T, d, n, kind):
         want = ref.float() if out == "f32" else ref.float().bfloat16()
         same = (got == want) | (torch.isnan(got) & torch.isnan(want))
         assert torch.all(same), (out, (~same).nonzero()[:8].tolist())
+
+
+# The cases above whose rows and columns are few run in parts of k; the same under the tiles.
+
+@pytest.mark.parametrize("T,d,n", TILED)
+@pytest.mark.parametrize("kind", ["random", "runs"])
+def test_what_others_hold_stays_out_of_tiles(T, d, n, kind):
+    r, N = 16, 4
+    g = torch.Generator().manual_seed(T)
+    x, w, a, b, scale, _ = _gaussians(T, d, n, r, N, False, g)
+    ids = _ids(T, N, kind, g)
+    ids[0], ids[1], ids[2] = 2, 1, -1
+    for out in ("f32", "bf16"):
+        desc = moe.LoraDesc(T, d, n, r, N, out_dtype=out)
+        want = _run(desc, x, ids, w, a, b, scale, None)
+        a2, b2, x2, s2 = a.clone(), b.clone(), x.clone(), scale.clone()
+        a2[2, 0, 5] = float("nan")
+        b2[2, 7, 3], b2[2, 9, 12] = float("inf"), float("nan")
+        s2[3] = float("inf")
+        x2[1, 9] = float("inf")
+        got = _run(desc, x2, ids, w, a2, b2, s2, None)
+        clean = (ids != 2) & (ids != 3)
+        clean[1] = False
+        assert torch.equal(got[clean], want[clean])
+        assert torch.all(torch.isnan(got[0])) and not torch.any(torch.isfinite(got[1]))
+        assert not torch.any(torch.isfinite(got[ids == 3]))
+
+
+@pytest.mark.parametrize("T,d,n", TILED)
+def test_a_large_first_product_in_tiles(T, d, n):
+    r = 8
+    x, a = torch.zeros(T, d).bfloat16(), torch.zeros(1, r, d).bfloat16()
+    x[:, 0], a[0, 0, 0] = 2.0 ** 100, 2.0 ** 27
+    w, b = torch.zeros(n, d).bfloat16(), torch.full((1, n, r), 2.0 ** -100).bfloat16()
+    ids = torch.zeros(T, dtype=torch.int32)
+    desc = moe.LoraDesc(T, d, n, r, 1, out_dtype="f32")
+    assert torch.all(_run(desc, x, ids, w, a, b, None, None) == 2.0 ** 27)
+    assert torch.all(_run(desc, x, ids, w, a, b, torch.tensor([4.0]), None) == float("inf"))
+
+
+@pytest.mark.parametrize("T,n", [(1400, 2176), (8200, 2176)])
+def test_a_first_product_of_24_bits_in_tiles(T, n):
+    """A x of up to 24 bits, exact in fp32 in whatever order, and every bit of it in an fp32 result."""
+    d, r, N = 1024, 24, 3
+    g = torch.Generator().manual_seed(T)
+    x = torch.randint(120, 128, (T, d), generator=g).bfloat16()
+    a = torch.randint(100, 128, (N, r, d), generator=g).bfloat16()
+    b = torch.zeros(N, n, r).bfloat16()
+    b[:, torch.arange(n), torch.arange(n) % r] = 1.0
+    ids = torch.randint(0, N, (T,), generator=g).to(torch.int32)
+    u = torch.stack([x.double() @ a[i].double().T for i in range(N)])[ids.long(), torch.arange(T)]
+    assert 2 ** 23 < u.min() and u.max() < 2 ** 24 and (u % 2 == 1).any()
+    got = _run(moe.LoraDesc(T, d, n, r, N, out_dtype="f32"), x, ids, torch.zeros(n, d).bfloat16(), a, b, None, None)
+    assert torch.equal(got.double(), u[:, torch.arange(n) % r])
+
+
+@pytest.mark.parametrize("T,d,n", TILED)
+def test_gelu_of_large_values_in_tiles(T, d, n):
+    x, w = torch.zeros(T, d).bfloat16(), torch.zeros(n, d).bfloat16()
+    x[:, 0], w[:, 0] = 1.0, torch.tensor([float("inf"), 3e38, 1e5, 20.0, -20.0, -1e5, 0.0, 1.0] * (n // 8)).bfloat16()
+    a, b = torch.zeros(1, 8, d).bfloat16(), torch.zeros(1, n, 8).bfloat16()
+    ids = torch.full((T,), -1, dtype=torch.int32)
+    ref = w[:, 0].double()
+    ref = torch.where(ref > 1e4, ref, torch.special.ndtr(ref) * ref)
+    for out, half in (("f32", U32), ("bf16", U16)):
+        got = _run(moe.LoraDesc(T, d, n, 8, 1, act="gelu", out_dtype=out), x, ids, w, a, b, None, None).double()
+        assert torch.all((got == ref) | ((got - ref).abs() <= half * ref.abs() + 2e-7 * 20))
+
+
+@pytest.mark.parametrize("T", [1400, 8200])
+def test_shared_expert_in_tiles_is_its_two_products(T):
+    d, F, g = 2176, 2304, torch.Generator().manual_seed(T)
+    up, down = moe.LoraDesc(T, d, F, 16, 3, act="gelu", has_bias=True), moe.LoraDesc(T, F, d, 8, 2, out_dtype="f32")
+    x, w, a, b, s, bi = _gaussians(T, d, F, 16, 3, True, g)
+    _, w2, a2, b2, s2, _ = _gaussians(1, F, d, 8, 2, False, g)
+    ids = _ids(T, 3, "runs", g).to(DEV)
+    wu = moe.LoraWeights(w.to(DEV), a.to(DEV), b.to(DEV), s.to(DEV), bi.to(DEV))
+    wd = moe.LoraWeights(w2.to(DEV), a2.to(DEV), b2.to(DEV), s2.to(DEV))
+    x = x.to(DEV)
+    h, o, q = torch.empty(T, F, dtype=torch.bfloat16, device=DEV), torch.empty(T, d, device=DEV), torch.empty(T, d, device=DEV)
+    moe.moe_lora_linear(up, x, ids, wu, h)
+    moe.moe_lora_linear(down, h, ids, wd, o)
+    moe.moe_lora_shared_ffn(up, down, x, ids, wu, wd, q, workspace=moe.alloc_lora_shared_workspace(up, down, DEV).fill_(0xFF))
+    assert torch.equal(o, q)
+
+
+@pytest.mark.parametrize("T,d,n", TILED)
+def test_capture_streams_and_repetition_in_tiles(T, d, n):
+    r, N = 16, 5
+    g = torch.Generator().manual_seed(T)
+    x, w, a, b, s, _ = _gaussians(T, d, n, r, N, False, g)
+    weights = moe.LoraWeights(w.to(DEV), a.to(DEV), b.to(DEV), s.to(DEV))
+    x, ids = x.to(DEV), _ids(T, N, "random", g).to(DEV)
+    desc = moe.LoraDesc(T, d, n, r, N)
+    y, ws = torch.empty(T, n, dtype=torch.bfloat16, device=DEV), moe.alloc_lora_workspace(desc, DEV)
+    moe.moe_lora_linear(desc, x, ids, weights, y, workspace=ws)
+    want = y.clone()
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        y.zero_()
+        moe.moe_lora_linear(desc, x, ids, weights, y)
+    torch.cuda.synchronize()
+    assert torch.equal(y, want)
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        moe.moe_lora_linear(desc, x, ids, weights, y, workspace=ws)
+    for k in range(3):
+        ids.copy_(_ids(T, N, "random", torch.Generator().manual_seed(k)))
+        y.zero_()
+        graph.replay()
+        torch.cuda.synchronize()
+        got = y.clone()
+        moe.moe_lora_linear(desc, x, ids, weights, y, workspace=ws)
+        assert torch.equal(y, got)
