@@ -19,8 +19,9 @@
 // numbers them without gaps in use and without a list.  A second kernel adds each sequence's
 // pieces in order, a third the sequences' losses.  fp32 within a piece, fp64 beyond.
 //
-// 131072 tokens, 256 experts, sigmoid, 64 sequences: 40 us, 3.5 TB/s; runs 32 (33 M sigmoids: near the
-// instruction rate), the two others 5 and 4.  Its gradient 57 us, 4.7 TB/s.  A small batch: 4.5 and 8 us.
+// 131072 tokens, 256 experts, sigmoid, 64 sequences: 43 us, 3.3 TB/s; runs 34 (28 by bytes, and partly
+// instructions: 24 more a token and wave took 2.3), the two others 5 and 4.  Its gradient 57 us, 4.7 TB/s.  A small
+// batch: 4.7 and 8 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -64,10 +65,18 @@ struct TokenMask {
   }
 };
 
-// e^x as a power of two: the product's rounding costs |x| half steps, of which scores that weigh
-// anything have few.  (exp_f32 puts them back; the kernels here are near the instruction rate's bound.)
-__device__ __forceinline__ float exp_near(float x) { return __builtin_amdgcn_exp2f(x * 1.44269504088896340736f); }
-__device__ __forceinline__ float inverse(float x) { return __builtin_amdgcn_rcpf(x); }   // 1 ulp
+// e^x as exp_f32 gives it (2 ulp for |x| < 88; from there without the correction), with two instructions
+// less: 2^t of t = x log2 e rounded, times 1 + what x has beyond t ln 2.  Without that the error grows with |x|
+// (82 half steps in a share of scores of e^-80).
+__device__ __forceinline__ float exp_score(float x) {
+  constexpr float kLn2 = 0.69314718055994530942f, kLn2Lo = -1.90465429995776804525e-9f;
+  const float t = x * 1.44269504088896340736f, r = __builtin_amdgcn_exp2f(t);
+  const float c = fmaf(-t, kLn2Lo, fmaf(-t, kLn2, x));
+  return fabsf(x) < 88.f ? fmaf(r, c, r) : r;
+}
+// 1 / x within 1 ulp, which is 2 of a share's 25 half steps.  (The exact quotient is ten instructions: with it and
+// exp_f32 the runs of 131072 x 256 took 36.5 us instead of 34.2, their gradient 60 instead of 57.)
+__device__ __forceinline__ float inverse(float x) { return __builtin_amdgcn_rcpf(x); }
 
 // Scores e of a token from its logits and the inverse of their sum, of which q = e inv are the
 // shares; REST: for sigmoid scores also 1 - s.
@@ -77,18 +86,18 @@ __device__ __forceinline__ float scores(const f32x4& l, f32x4& e, f32x4& rest) {
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
       if constexpr (REST) {
-        const float t = exp_near(-fabsf(l[j])), big = inverse(1.f + t), small = t * big;
+        const float t = exp_score(-fabsf(l[j])), big = inverse(1.f + t), small = t * big;
         e[j] = l[j] < 0.f ? small : big;
         rest[j] = l[j] < 0.f ? big : small;
       } else {
-        e[j] = inverse(1.f + exp_near(-l[j]));
+        e[j] = inverse(1.f + exp_score(-l[j]));
       }
     }
   } else {
     float m = lanes_max<L>(fmaxf(fmaxf(l[0], l[1]), fmaxf(l[2], l[3])));
     m = m == -INFINITY ? 0.f : m;                    // every expert masked: no shares
 #pragma unroll
-    for (int j = 0; j < 4; ++j) e[j] = exp_near(l[j] - m);
+    for (int j = 0; j < 4; ++j) e[j] = exp_score(l[j] - m);
   }
   const float sum = lanes_sum<L>((e[0] + e[1]) + (e[2] + e[3]));
   if constexpr (SIGMOID) return inverse(sum < kLeastSum ? kLeastSum : sum);

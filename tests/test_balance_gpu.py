@@ -222,3 +222,45 @@ def test_gradient_on_through_the_router(T, E, dtype):
     ref_x, half = dl @ w.double(), 2.0 ** -8 if dtype == "bf16" else U32
     tol = (E * U32 + (2.0 ** -16 if dtype == "bf16" else 0)) * (dl.abs() @ w.double().abs())
     assert torch.all((more.d_x.double() - ref_x).abs() <= tol + half * (ref_x.abs() + tol))
+
+
+@pytest.mark.parametrize("T,E,S", [(64, 16, 64), (2000, 24, 1500), (3000, 256, 3)])
+@pytest.mark.parametrize("kind,low", [("sigmoid", -20.0), ("sigmoid", -40.0), ("sigmoid", -80.0), ("softmax", -80.0)])
+def test_low_scores_keep_their_digits(T, E, S, kind, low):
+    """Shares of scores far below 1: of sigmoid scores that are all low, and of a softmax's least.  Logits
+    are multiples of 2^-10, so that their differences are exact."""
+    k, g = 4, torch.Generator().manual_seed(E)
+    l = (torch.randn(T, E, generator=g) * 1024).clamp(-5000, 5000).round() / 1024
+    l = l + (low if kind == "sigmoid" else torch.arange(E) % 3 * (low / 2))
+    idx = torch.randint(0, E, (T, k), generator=g).to(torch.int32)
+    off = list(range(S)) + [T]
+    desc = moe.BalanceDesc(T, E, k, S, score=kind)
+    ref = R.forward(l.double(), kind, idx.long(), off, None, k)
+    o = torch.tensor(off, dtype=torch.int32)
+    out = _run(desc, l, idx, o, None)
+    # In half steps.  A score: 4 for the exponential, 1 + 2 for the sum with 1 and its inverse.  Their sum: 7 and 8
+    # levels; its inverse, the product: 7 + 15 + 3 = 25.  A mean: 40 terms and levels as in test_loss, 2 more.
+    # A softmax's least score is e^-90 (differences of up to 80 + 10) and under 2^-126 = e^-87.3, below which fp32
+    # keeps no full digits or none: the score, and with a sum of 1 or more the share, is off by at most that;
+    # so is a result of that size, and a loss takes E load / (k n) <= E times the mean's.
+    share, terms, least = 25, 4 if S == T else 42, 2.0 ** -126
+    assert torch.all((out.prob_mean.cpu().double() - ref["prob_mean"]).abs() <= (share + terms) * U32 * ref["prob_mean"] + 2 * least)
+    assert torch.all((out.seq_loss.cpu().double() - ref["seq_loss"]).abs() <=
+                     (share + terms + 2) * U32 * ref["seq_loss"] + (E + 1) * least)
+    d_seq = torch.randn(S, generator=g)
+    grad = R.gradient(l.double(), kind, idx.long(), off, None, k, 0.0, d_seq.double())
+    d = torch.empty(T, E, device=DEV)
+    moe.moe_balance_backward(desc, l.to(DEV), o.to(DEV), out, d, d_seq_loss=d_seq.to(DEV))
+    q = R.shares(l.double(), kind)
+    n = torch.tensor(off[1:]) - torch.tensor(off[:-1])
+    c = ((d_seq.double() * E / (k * n.double() ** 2))[:, None] * ref["load"].double()).repeat_interleave(n, 0)
+    leads = q > 0.5
+    lead = (leads * c).sum(1, keepdim=True)
+    # d = q (c - lead - dot) (1 - s): q to 25, the rest 5; dot's terms q to 25, the products and 10 levels 12.
+    # c and lead themselves are good to 2, which the leader's own difference does not see.
+    away, size = (c - lead).abs(), (c.abs() + lead.abs()) * ~leads
+    tol = U32 * q * (30 * away + 67 * (away * q).sum(1, keepdim=True) + 4 * (size + (size * q).sum(1, keepdim=True)))
+    # a share's 2^-126 times its difference, and the result's own (its factors are sums of the differences' size)
+    tol = tol + least * (1 + away + (away * q).sum(1, keepdim=True) + away.sum(1, keepdim=True) * q)
+    bad = ((d.cpu().double() - grad).abs() > tol).nonzero()
+    assert not len(bad), [(d[i, j].item(), grad[i, j].item(), tol[i, j].item(), l[i, j].item()) for i, j in bad[:5].tolist()]
