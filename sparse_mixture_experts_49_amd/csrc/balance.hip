@@ -462,9 +462,18 @@ static void for_kind(bool sigmoid, int E, F f) {
   });
 }
 
-// One launch where a wave can take a whole sequence: at most 32 of its steps, and 64 sequences (4.5 us;
-// three kernels take 16).
-static bool single(const BalanceShape& s) { return s.S <= 64 && (long)s.T * s.E <= 8 * 1024; }
+// Lanes that hold a token.
+static int lanes_of(int E) {
+  int l = 0;
+  for_experts(E, [&](auto n) { l = decltype(n)::value; });
+  return l;
+}
+
+// One launch where a wave can take a whole sequence: at most 32 of its steps in all, so 512 tokens, and 64
+// sequences.  One launch and three, us, 8 experts: 4 sequences of 8 steps 6.6 and 9.4, of 32 steps 15.7 and 9.9;
+// 64 of half a step 19.8 and 11.2, with 256 experts 23.6 and 32.5.  A single sequence of 8 steps 6.2 and 9.2, of 16
+// 9.1 and 9.3, of 32 15 and 9.5, of 128 50 and 11.6; how long the longest is the host does not know.
+static bool single(const BalanceShape& s) { return s.S <= 64 && (long)s.T * lanes_of(s.E) <= 32 * 64; }
 
 hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
   if (single(a.sh)) {

@@ -264,3 +264,20 @@ def test_low_scores_keep_their_digits(T, E, S, kind, low):
     tol = tol + least * (1 + away + (away * q).sum(1, keepdim=True) + away.sum(1, keepdim=True) * q)
     bad = ((d.cpu().double() - grad).abs() > tol).nonzero()
     assert not len(bad), [(d[i, j].item(), grad[i, j].item(), tol[i, j].item(), l[i, j].item()) for i, j in bad[:5].tolist()]
+
+
+@pytest.mark.parametrize("T,E", [(512, 1), (513, 1), (2000, 1), (8192, 1), (512, 4), (2000, 4), (128, 33), (129, 33), (248, 33)])
+@pytest.mark.parametrize("S", [1, 5, 64])
+def test_few_experts_and_long_sequences(T, E, S):
+    """Around the most that one launch takes, where the experts do not fill a token's lanes."""
+    k = min(E, 3)
+    off = _borders(T, S, T + S)
+    off[0], off[-1] = 0, T
+    desc = moe.BalanceDesc(T, E, k, S, score="softmax")
+    l, idx, o, _ = _inputs(T, E, k, off, False, T + E)
+    ref = R.forward(l.double(), "softmax", idx.long(), off, None, k)
+    out = _run(desc, l, idx, o, None)
+    for n in ("load", "valid", "total_load"):
+        assert torch.equal(getattr(out, n).cpu().long(), ref[n]), n
+    assert torch.all((out.prob_mean.cpu().double() - ref["prob_mean"]).abs() <= 110 * U32 * ref["prob_mean"])
+    assert abs(float(out.loss) - float(ref["loss"])) <= 113 * U32 * float(ref["loss"])
