@@ -190,10 +190,15 @@ __global__ __launch_bounds__(256) void balance_part_kernel(BalanceArgs a, int ch
     for (int i = threadIdx.x; i < E; i += 256) a.total_load[i] = 0;
   s.clear(E);
   __syncthreads();
+  int empty = 0;                                     // in a row: from two on the next full one is searched for
   for (int b = sequence_of(a.offsets, S, T, t0); b < S; ++b) {
     const int lo = max(border(a.offsets, b, T), t0), hi = min(border(a.offsets, b + 1, T), t1);
     if (lo >= t1) break;
-    if (hi <= lo) continue;
+    if (hi <= lo) {
+      if (++empty > 1) b = max(b, sequence_of(a.offsets, S, T, lo) - 1);
+      continue;
+    }
+    empty = 0;
     sum_piece<L, SIGMOID, VEC>(a, lo, hi, s);
     __syncthreads();
     const size_t at = (size_t)blockIdx.x + b;
@@ -383,14 +388,18 @@ __global__ __launch_bounds__(256) void balance_grad_kernel(BalanceGradArgs a, in
         if (e + j < E) row[e + j] = d[j];
     }
   };
-  int at = w0;                                       // tokens below are done
+  int at = w0, empty = 0;                            // tokens below are done; empty sequences in a row
   for (int b = sequence_of(a.offsets, S, T, w0); at < w1; ++b) {
     const int lo = b < S ? min(max(border(a.offsets, b, T), at), w1) : w1;
     for (int t = at + slot; t < lo; t += kTok) write(t, f32x4{0.f, 0.f, 0.f, 0.f});   // of no sequence
     if (b >= S) break;
     const int hi = min(max(border(a.offsets, b + 1, T), lo), w1);
     at = hi;
-    if (hi <= lo) continue;
+    if (hi <= lo) {
+      if (++empty > 1 && at < w1) b = max(b, sequence_of(a.offsets, S, T, at) - 1);
+      continue;
+    }
+    empty = 0;
     f32x4 c;
     const int n = a.valid[b];
     const double by = n > 0 && live_seqs > 0

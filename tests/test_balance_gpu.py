@@ -281,3 +281,44 @@ def test_few_experts_and_long_sequences(T, E, S):
         assert torch.equal(getattr(out, n).cpu().long(), ref[n]), n
     assert torch.all((out.prob_mean.cpu().double() - ref["prob_mean"]).abs() <= 110 * U32 * ref["prob_mean"])
     assert abs(float(out.loss) - float(ref["loss"])) <= 113 * U32 * float(ref["loss"])
+
+
+@pytest.mark.parametrize("T,S,E,masked", [(40, 1 << 14, 24, True), (40, 1 << 20, 8, False), (3000, 1 << 20, 33, True),
+                                          (20000, 1 << 18, 8, False)])
+@pytest.mark.parametrize("where", ["spread", "one place"])
+def test_many_more_empty_sequences_than_tokens(T, S, E, masked, where):
+    k, g = 2, torch.Generator().manual_seed(T)
+    if where == "spread":
+        off = torch.randint(0, T + 1, (S + 1,), generator=g).sort().values
+    else:                                            # all but a few empty, between two tokens
+        off = torch.full((S + 1,), T // 2)
+        off[:3], off[-3:] = torch.tensor([1, 5, 9]), torch.tensor([T // 2 + 1, T - 3, T])
+    desc = moe.BalanceDesc(T, E, k, S)
+    l, idx, o, mask = _inputs(T, E, k, off.tolist(), masked, T)
+    out = _run(desc, l, idx, o, mask)
+    # the sequences that are not empty, which are one after the other
+    full = (off[1:] > off[:-1]).nonzero()[:, 0]
+    ref = R.forward(l.double(), "softmax", idx.long(), torch.cat([off[full], off[full[-1:] + 1]]).tolist(), mask, k)
+    assert int(out.valid[S]) == int(ref["valid"][-1]) and torch.equal(out.total_load.cpu().long(), ref["total_load"])
+    for n, want in (("load", ref["load"]), ("valid", ref["valid"][:-1])):
+        got = getattr(out, n).cpu().long()[:S]
+        assert torch.equal(got[full], want)
+        assert int(got.abs().sum()) == int(want.sum())
+    for n in ("prob_mean", "seq_loss"):
+        got = getattr(out, n).cpu().double()
+        assert torch.all((got[full] - ref[n]).abs() <= 112 * U32 * ref[n])
+        got[full] = 0
+        assert torch.all(got == 0)
+    assert abs(float(out.loss) - float(ref["loss"])) <= 113 * U32 * float(ref["loss"])
+    d = torch.full((T * E + 1,), 7.0, device=DEV)
+    moe.moe_balance_backward(desc, l.to(DEV), o.to(DEV), out, d, d_loss=torch.ones(1, device=DEV),
+                             token_mask=None if mask is None else mask.to(DEV))
+    assert d[T * E] == 7
+    # the same gradient with the empty sequences left out, bit for bit
+    few = moe.BalanceDesc(T, E, k, len(full))
+    kept = torch.cat([off[full], off[full[-1:] + 1]]).to(torch.int32)
+    fwd = _run(few, l, idx, kept, mask)
+    e = torch.empty(T, E, device=DEV)
+    moe.moe_balance_backward(few, l.to(DEV), kept.to(DEV), fwd, e, d_loss=torch.ones(1, device=DEV),
+                             token_mask=None if mask is None else mask.to(DEV))
+    assert torch.equal(d[:T * E].view(T, E), e)
