@@ -322,3 +322,36 @@ def test_many_more_empty_sequences_than_tokens(T, S, E, masked, where):
     moe.moe_balance_backward(few, l.to(DEV), kept.to(DEV), fwd, e, d_loss=torch.ones(1, device=DEV),
                              token_mask=None if mask is None else mask.to(DEV))
     assert torch.equal(d[:T * E].view(T, E), e)
+
+
+@pytest.mark.parametrize("T,E,S", [(50, 24, 5), (2000, 24, 5), (2000, 24, 80), (20000, 33, 300), (3000, 256, 64)])
+@pytest.mark.parametrize("borders", ["falling", "anything", "one far"])
+def test_borders_that_are_none_stay_inside_every_array(T, E, S, borders):
+    """As above, by one launch and by three: guards behind every output and the workspace."""
+    k, g = 3, torch.Generator().manual_seed(T + S)
+    l, idx, _, _ = _inputs(T, E, k, [0, T], False, 2)
+    if borders == "falling":
+        o = torch.linspace(T + 7, -7, S + 1).to(torch.int32)
+    elif borders == "anything":
+        o = torch.randint(-2 * T, 3 * T, (S + 1,), generator=g).to(torch.int32)
+        o[1::5], o[2::7] = (1 << 31) - 1, -(1 << 31)
+    else:                                            # sequences that meet the same pieces
+        o = torch.linspace(0, T, S + 1).to(torch.int32)
+        o[S // 2] = 0
+        o[S // 3] = T
+    desc, G = moe.BalanceDesc(T, E, k, S), 512
+    i32, f32 = dict(dtype=torch.int32, device=DEV), dict(dtype=torch.float32, device=DEV)
+    full = {n: torch.full((size + G,), 77, **kw) for n, size, kw in (
+        ("load", S * E, i32), ("valid", S + 1, i32), ("prob_mean", S * E, f32), ("seq_loss", S, f32), ("loss", 1, f32),
+        ("total_load", E, i32))}
+    sizes = dict(load=S * E, valid=S + 1, prob_mean=S * E, seq_loss=S, loss=1, total_load=E)
+    need = moe.moe_balance_workspace_size(desc)
+    ws = torch.full((need + 4096,), 0x5A, dtype=torch.uint8, device=DEV)
+    out = moe.BalanceOut(**{n: t[:sizes[n]] for n, t in full.items()})
+    moe.moe_balance_loss(desc, l.to(DEV), idx.to(DEV), o.to(DEV), out, workspace=ws[:need])
+    d = torch.full((T * E + G,), 7.0, device=DEV)
+    moe.moe_balance_backward(desc, l.to(DEV), o.to(DEV), out, d, d_loss=torch.ones(1, device=DEV))
+    torch.cuda.synchronize()
+    for n, t in full.items():
+        assert torch.all(t[sizes[n]:] == 77), n
+    assert torch.all(ws[need:] == 0x5A) and torch.all(d[T * E:] == 7)
