@@ -463,9 +463,9 @@ int moe_mx_block_forward(const moe_mx_block* block, const moe_rows* x, const moe
     auto reach = [&](const moe_rows* m, size_t e) { return m && m->data ? (T - 1) * (size_t)m->stride * e + D * e : 0; };
     auto data = [](const moe_rows* m) -> const void* { return m ? m->data : nullptr; };
     const size_t pe = b.norm->param_dtype == MOE_DTYPE_BF16 ? 2 : 4, ae = b.norm->add_dtype == MOE_DTYPE_BF16 ? 2 : 4;
-    Spans o, in;
+    Spans o, in, xo;
     o.add(y, T * D * 4, "y");
-    o.add(data(x_out), T > 1 ? reach(x_out, 2) : D * 2, "x_out");
+    xo.add(data(x_out), T > 1 ? reach(x_out, 2) : D * 2, "x_out");
     o.add(r.topk_idx, T * desc->top_k * 4, "topk_idx");
     o.add(r.topk_w, T * desc->top_k * 4, "topk_w");
     o.add(r.logits, T * E * 4, "logits");
@@ -474,8 +474,6 @@ int moe_mx_block_forward(const moe_mx_block* block, const moe_rows* x, const moe
     o.add(r.aux, 4, "aux");
     o.add(r.z_loss, 4, "z_loss");
     o.add(ws, ws_bytes, "workspace");
-    in.add(data(x), T > 1 ? reach(x, 2) : D * 2, "x");
-    in.add(data(add), T > 1 ? reach(add, ae) : D * ae, "add");
     in.add(b.weight, D * pe, "weight");
     in.add(b.bias, D * pe, "bias");
     in.add(b.w_router, E * D * 2, "w_router");
@@ -495,6 +493,11 @@ int moe_mx_block_forward(const moe_mx_block* block, const moe_rows* x, const moe
         in.add(both[i]->scale, N * 4, "scale");
       }
     }
+    // x_out may lie beside x and add in one buffer's rows: moe_layer_norm, the first launch, tells them apart.
+    if (int st = check_alias(xo, in)) return st;
+    in.add(data(x), T > 1 ? reach(x, 2) : D * 2, "x");
+    in.add(data(add), T > 1 ? reach(add, ae) : D * ae, "add");
+    in.add(data(x_out), T > 1 ? reach(x_out, 2) : D * 2, "x_out");
     if (int st = check_alias(o, in)) return st;
   }
   void* xn = at<void>(ws, B.xn);

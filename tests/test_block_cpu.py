@@ -85,3 +85,22 @@ def test_refusals():
         assert _forward(**kw)[0] == B.MOE_ERR_INVALID, kw
     for kw in (dict(ws=None), dict(ws=P["ws"] + 16), dict(n=-1)):
         assert _forward(**kw)[0] == B.MOE_ERR_WORKSPACE, kw
+
+
+def test_outputs_over_strided_rows_are_refused():
+    """What lies between two rows counts as theirs, but for x, add and x_out among themselves."""
+    lib = moe.load_library()
+    wide = 1024
+    assert _forward(y=P["x_out"])[0] == B.MOE_ERR_INVALID and _forward(x_out=P["w_router"])[0] == B.MOE_ERR_INVALID
+    assert _forward(x_out=P["ws"])[0] == B.MOE_ERR_INVALID and _forward(x_out=P["add"] + 16)[0] == B.MOE_ERR_INVALID
+    s, keep = B._mx_block(_block(shared=False), None, None)
+    mx = B.CMxWeights(*(P["mx"] + 0x1000000 * i for i in range(6)))
+    s.w_router, s.w = P["w_router"], ctypes.cast(ctypes.pointer(mx), ctypes.c_void_p)
+    size = ctypes.c_size_t(0)
+    assert lib.moe_mx_block_workspace_size(ctypes.byref(s), ctypes.byref(size)) == 0
+    rows = lambda q: ctypes.byref(B.CRows(q, wide))  # noqa: E731
+    for x_out, y in ((P["x"], P["y"]), (P["x"] + 2 * D - 16, P["y"]), (P["x"] + 2 * D, P["x"] + 4 * D),
+                     (P["x_out"], P["x_out"] + 2 * D)):
+        st = lib.moe_mx_block_forward(ctypes.byref(s), rows(P["x"]), None, rows(x_out), y, None, P["ws"], size, None)
+        assert st == B.MOE_ERR_INVALID, (hex(x_out), hex(y))
+    del keep

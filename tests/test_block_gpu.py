@@ -169,3 +169,19 @@ def test_block_with_a_tiled_shared_expert():
         got = [x_out.clone(), y.clone()]
         moe.moe_mx_block_forward(b, x, y, add=add, x_out=x_out, adapter=ids, workspace=ws)
         assert torch.equal(x_out, got[0]) and torch.equal(y, got[1])
+
+
+def test_block_with_columns_of_one_buffer():
+    """x and x_out beside each other in the rows of one buffer, as the layer norm takes them."""
+    T, d = 37, 256
+    b, x, add, ids = _made(T, d, 384, 16, 4, 512, True, 6)
+    x_out, y, z = torch.empty_like(x), torch.empty(T, d, device=DEV), torch.empty(T, d, device=DEV)
+    moe.moe_mx_block_forward(b, x, y, add=add, x_out=x_out, adapter=ids)
+    buf = torch.full((T, 2 * d + 8), 7.0, dtype=torch.bfloat16, device=DEV)
+    buf[:, d + 8:] = x
+    moe.moe_mx_block_forward(b, buf[:, d + 8:], z, add=add, x_out=buf[:, :d], adapter=ids)
+    assert torch.equal(y, z) and torch.equal(buf[:, :d], x_out) and torch.equal(buf[:, d + 8:], x)
+    assert torch.all(buf[:, d:d + 8] == 7)
+    for c in (16, d, d + 8):                         # columns that x has too
+        with pytest.raises(moe.MoeError, match="x_out overlaps x"):
+            moe.moe_mx_block_forward(b, buf[:, d + 8:], z, add=add, x_out=buf[:, c:c + d], adapter=ids)
