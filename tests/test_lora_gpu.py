@@ -380,3 +380,21 @@ def test_capture_streams_and_repetition_in_tiles(T, d, n):
         got = y.clone()
         moe.moe_lora_linear(desc, x, ids, weights, y, workspace=ws)
         assert torch.equal(y, got)
+
+
+def test_the_most_tokens_with_the_most_columns_of_a():
+    """As many tokens as int32 allows, of 128 adapters of rank 128: 17.8 million blocks, offsets past 32 bits.  Exact
+    values; the first rows, the last and some between are compared."""
+    T, d, n, r, N = (1 << 24) - 1, 128, 128, 128, 128
+    if torch.cuda.mem_get_info()[0] < 40 << 30:
+        pytest.skip("40 GB needed")
+    g = torch.Generator().manual_seed(1)
+    few, w, a, b, scale, _ = _small_integers(4096, d, n, r, N, False, g)
+    x = few.to(DEV).repeat(4096, 1)[:T]
+    ids = (torch.arange(T, device=DEV, dtype=torch.int32) // 517) % (N + 1) - 1
+    y = torch.full((T, n), 7.0, dtype=torch.bfloat16, device=DEV)
+    desc = moe.LoraDesc(T, d, n, r, N)
+    moe.moe_lora_linear(desc, x, ids, moe.LoraWeights(w.to(DEV), a.to(DEV), b.to(DEV), scale.to(DEV)), y)
+    at = torch.cat([torch.arange(3000), torch.randint(0, T, (20000,), generator=g), torch.arange(T - 3000, T)])
+    ref, _ = _reference(few[at % 4096], w, a, b, scale, None, ids[at.to(DEV)].cpu())
+    assert torch.equal(y[at.to(DEV)].cpu(), ref.float().bfloat16())
