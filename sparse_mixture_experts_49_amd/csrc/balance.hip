@@ -19,9 +19,9 @@
 // numbers them without gaps in use and without a list.  A second kernel adds each sequence's
 // pieces in order, a third the sequences' losses.  fp32 within a piece, fp64 beyond.
 //
-// 131072 tokens, 256 experts, sigmoid, 64 sequences: 43 us, 3.3 TB/s; runs 34 (28 by bytes, and partly
-// instructions: 24 more a token and wave took 2.3), the two others 5 and 4.  Its gradient 57 us, 4.7 TB/s.  A small
-// batch: 4.7 and 8 us.
+// 131072 tokens, 256 experts, sigmoid, 64 sequences: 41 us, 3.4 TB/s; runs 34 (28 by bytes at a copy's rate;
+// instructions count too: 24 more a token and wave took 2), the two others 5 and 4.  Its gradient 57 us, 4.7 TB/s.
+// A small batch: 4.6 and 8 us.
 #include <algorithm>
 #include <type_traits>
 
@@ -496,7 +496,9 @@ hipError_t launch_balance(const BalanceArgs& a, hipStream_t s) {
     balance_part_kernel<decltype(l)::value, decltype(sig)::value, decltype(vec)::value>
         <<<balance_chunks(a.sh), 256, 0, s>>>(a, chunk);
   });
-  // A sequence's pieces by 16 waves or by one: 131072 x 256 in 512 sequences 47 and 42 us, in 4096 105 and 52.
+  // A sequence's pieces by 16 waves or by one, 131072 x 256, the whole call without total_load: 64 sequences 38
+  // and 43 us, 128 37 and 39, 512 42 and 37, 4096 104 and 47.  total_load's atomics meet at E counts: 512
+  // sequences 8 us more, 4096 110; 131072 x 64 in 65536 sequences 1390 us with and 197 without it.
   if (balance_chunks(a.sh) >= 8 * a.sh.S) balance_seq_kernel<16><<<dim3(a.sh.S, parts), 1024, 0, s>>>(a, chunk);
   else balance_seq_kernel<1><<<dim3((a.sh.S + 15) / 16, parts), 1024, 0, s>>>(a, chunk);
   balance_total_kernel<<<1, 1024, 0, s>>>(a, parts);

@@ -19,7 +19,7 @@
 //
 // 16384 x 4096 -> 14336, rank 16, GELU: 1520 to 1580 us, 1.25 PFLOP/s (1.50 in a library product of
 // 16384 x 16384 x 8192): steps 1335, GELU 130, stores 60, adapters 40.  8192 x 2816 -> 2048, rank 32,
-// fp32: 88 us, one tile a CU.
+// fp32: 88 to 92 us, one tile a CU.
 //
 // LDS: rows of 128 B, the eight 16-byte chunks of row r at chunk ^ ((r >> 1) & 7): a fragment
 // read (16 rows, one chunk) touches every bank once.
